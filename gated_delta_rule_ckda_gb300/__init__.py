@@ -8,6 +8,10 @@ fallback: if the library is missing or fails to load, every call raises.
     o, hT = fwd(q, k, v, alpha, beta, h0=None, cu_seqlens=None, scale=1.0)
     o = decode_step(q, k, v, alpha, beta, state)      # state updated in place
 
+Next to the recurrence are linear attention with a scalar decay per head
+(linear_fwd, linear_bwd, linear_decode_step) and layer norm (layernorm_fwd,
+layernorm_bwd).
+
 Shapes follow the C ABI: q, k, alpha [B, H, T, dk]; v [B, H, T, dv];
 beta [B, H, T]; h0 / hT fp32 [N, H, dk, dv] with N = B, or the number of
 packed sequences when cu_seqlens (int32 [N + 1], B == 1) is given.
@@ -23,7 +27,9 @@ import torch
 __all__ = ["fwd", "fwd_host", "fwd_split", "decode_step", "decode_step_raw", "prep", "bwd",
            "bwd_workspace_bytes", "fwd_status", "workspace_bytes", "split_segments",
            "split_workspace_bytes", "host_scratch_bytes", "selftest_timeout", "lib",
-           "library_path", "CkdaError", "STATUS", "recurrence", "prepare"]
+           "library_path", "CkdaError", "STATUS", "recurrence", "prepare", "linear_fwd",
+           "linear_bwd", "linear_decode_step", "linear_attention", "layernorm_fwd",
+           "layernorm_bwd", "layer_norm"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libckda.so")
@@ -106,6 +112,24 @@ def lib():
             L.ckda_fwd_split.restype = i32
             L.ckda_fwd_split.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32,
                                          i32, f32, i32, vp, sz, vp]
+            lin = [vp, vp, vp, vp, i32, vp]
+            L.ckda_linear_fwd_workspace_bytes.restype = sz
+            L.ckda_linear_fwd_workspace_bytes.argtypes = [i32] * 7
+            L.ckda_linear_fwd.restype = i32
+            L.ckda_linear_fwd.argtypes = lin + [vp] * 3 + [i32] * 8 + [f32, vp, sz, vp]
+            L.ckda_linear_bwd_workspace_bytes.restype = sz
+            L.ckda_linear_bwd_workspace_bytes.argtypes = [i32] * 7
+            L.ckda_linear_bwd.restype = i32
+            L.ckda_linear_bwd.argtypes = lin + [vp] * 8 + [i32] * 8 + [f32, vp, sz, vp]
+            L.ckda_linear_decode_step.restype = i32
+            L.ckda_linear_decode_step.argtypes = [vp] * 4 + [i32, vp, vp] + [i32] * 6 + [f32, vp]
+            L.ckda_layernorm_fwd.restype = i32
+            L.ckda_layernorm_fwd.argtypes = [vp] * 6 + [ctypes.c_longlong, i32, i32, i32, f32, vp]
+            L.ckda_layernorm_bwd_workspace_bytes.restype = sz
+            L.ckda_layernorm_bwd_workspace_bytes.argtypes = [ctypes.c_longlong, i32]
+            L.ckda_layernorm_bwd.restype = i32
+            L.ckda_layernorm_bwd.argtypes = [vp] * 8 + [ctypes.c_longlong, i32, i32, i32, vp, sz,
+                                                        vp]
             _lib = L
     return _lib
 
@@ -578,6 +602,225 @@ def decode_step_raw(q_raw, k_raw, v, a_raw, b_raw, state, scale=1.0, normalize_q
     return o
 
 
+# ------------------------------------ linear attention with a decay per head
+def _check_linear(q, k, v, g, cu_seqlens, states, more=()):
+    """Checks the arguments that linear_fwd and linear_bwd share; returns
+    (B, H, Hk, T, dk, dv, N, g per head, io dtype)."""
+    device, dt = q.device, q.dtype
+    io = _io_dtype(q)
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q [B, Hk, T, dk] and v [B, H, T, dv] have four axes")
+    B, Hk, T, dk = q.shape
+    H, dv = v.shape[1], v.shape[3]
+    if Hk < 1 or H % Hk:
+        raise ValueError(f"{H} heads cannot share {Hk} key heads evenly")
+    _check(q, "q", dt, (B, Hk, T, dk), device)
+    _check(k, "k", dt, (B, Hk, T, dk), device)
+    _check(v, "v", dt, (B, H, T, dv), device)
+    for name, t in more:
+        _check(t, name, dt, (B, H, T, dv), device)
+    per_head = g.dim() == 1
+    _check(g, "g", torch.float32, (H,) if per_head else (B, H, T), device)
+    N = B
+    if cu_seqlens is not None:
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2 or B != 1:
+            raise ValueError("packed input has B = 1 and cu_seqlens [num_seqs + 1]")
+        N = cu_seqlens.numel() - 1
+        _check(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,), device)
+    for name, t in states:
+        if t is not None:
+            _check(t, name, torch.float32, (N, H, dk, dv), device)
+    return B, H, Hk, T, dk, dv, N, per_head, io
+
+
+def linear_fwd_workspace_bytes(B, H, T, dk, dv, dtype=torch.bfloat16, num_seqs=0) -> int:
+    io = _BF16 if dtype == torch.bfloat16 else _F32
+    return int(lib().ckda_linear_fwd_workspace_bytes(num_seqs, B, H, T, dk, dv, io))
+
+
+def linear_bwd_workspace_bytes(B, H, T, dk, dv, dtype=torch.bfloat16, num_seqs=0) -> int:
+    io = _BF16 if dtype == torch.bfloat16 else _F32
+    return int(lib().ckda_linear_bwd_workspace_bytes(num_seqs, B, H, T, dk, dv, io))
+
+
+def linear_fwd(q, k, v, g, h0=None, cu_seqlens=None, scale=1.0, store_final_state=True, o=None,
+               hT=None, workspace=None, stream=None):
+    """Linear attention with a scalar decay per head (ckda_linear_fwd):
+    H_t = exp(g_t) H_{t-1} + k_t v_t^T, o_t = H_t^T (scale q_t).
+
+    q, k [B, Hk, T, dk] with Hk dividing H (heads share keys in order),
+    v [B, H, T, dv], g fp32 [B, H, T] or [H] (one decay for all of a head's
+    tokens); h0, hT fp32 [N, H, dk, dv].  Returns (o, hT or None)."""
+    L = lib()
+    device = q.device
+    B, H, Hk, T, dk, dv, N, per_head, io = _check_linear(q, k, v, g, cu_seqlens,
+                                                         (("h0", h0), ("hT", hT)))
+    if o is None:
+        o = torch.empty((B, H, T, dv), dtype=q.dtype, device=device)
+    else:
+        _check(o, "o", q.dtype, (B, H, T, dv), device)
+    if store_final_state and hT is None:
+        hT = torch.empty((N, H, dk, dv), dtype=torch.float32, device=device)
+    nseq = N if cu_seqlens is not None else 0
+    if workspace is None:
+        workspace = torch.empty(L.ckda_linear_fwd_workspace_bytes(nseq, B, H, T, dk, dv, io),
+                                dtype=torch.uint8, device=device)
+    with torch.cuda.device(device):
+        rc = L.ckda_linear_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), int(per_head), _ptr(h0),
+                               _ptr(o), _ptr(hT), _ptr(cu_seqlens), nseq, B, H, Hk, T, dk, dv, io,
+                               float(scale), _ptr(workspace), workspace.numel(),
+                               _stream_handle(stream, device))
+    if rc != 0:
+        raise CkdaError(rc, "ckda_linear_fwd")
+    linear_fwd.last_workspace = workspace
+    return o, hT
+
+
+def linear_bwd(q, k, v, g, do, h0=None, dhT=None, cu_seqlens=None, scale=1.0, store_dh0=True,
+               workspace=None, stream=None):
+    """Backward of linear_fwd (ckda_linear_bwd): gradients of
+    sum <o, do> + <hT, dhT>.  Returns (dq, dk, dv, dg, dh0 or None); dg (of g's
+    shape) and dh0 are fp32."""
+    L = lib()
+    device = q.device
+    B, H, Hk, T, dk, dv, N, per_head, io = _check_linear(q, k, v, g, cu_seqlens,
+                                                         (("h0", h0), ("dhT", dhT)), (("do", do),))
+    nseq = N if cu_seqlens is not None else 0
+    if workspace is None:
+        workspace = torch.empty(L.ckda_linear_bwd_workspace_bytes(nseq, B, H, T, dk, dv, io),
+                                dtype=torch.uint8, device=device)
+    dq, dkk, dvv, dg = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v),
+                        torch.empty_like(g))
+    dh0 = torch.empty((N, H, dk, dv), dtype=torch.float32, device=device) if store_dh0 else None
+    with torch.cuda.device(device):
+        rc = L.ckda_linear_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), int(per_head), _ptr(h0),
+                               _ptr(do), _ptr(dhT), _ptr(dq), _ptr(dkk), _ptr(dvv), _ptr(dg),
+                               _ptr(dh0), _ptr(cu_seqlens), nseq, B, H, Hk, T, dk, dv, io,
+                               float(scale), _ptr(workspace), workspace.numel(),
+                               _stream_handle(stream, device))
+    if rc != 0:
+        raise CkdaError(rc, "ckda_linear_bwd")
+    linear_bwd.last_workspace = workspace
+    return dq, dkk, dvv, dg, dh0
+
+
+def linear_decode_step(q, k, v, g, state, scale=1.0, o=None, stream=None):
+    """One token of linear attention (ckda_linear_decode_step) on a resident
+    state [B, H, dk, dv] fp32, updated in place.  q, k [B, Hk, dk],
+    v [B, H, dv], g fp32 [B, H] or [H].  Returns o [B, H, dv]."""
+    L = lib()
+    device, dt = q.device, q.dtype
+    io = _io_dtype(q)
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q [B, Hk, dk] and v [B, H, dv] have three axes")
+    B, Hk, dk = q.shape
+    H, dv = v.shape[1], v.shape[2]
+    if Hk < 1 or H % Hk:
+        raise ValueError(f"{H} heads cannot share {Hk} key heads evenly")
+    _check(q, "q", dt, (B, Hk, dk), device)
+    _check(k, "k", dt, (B, Hk, dk), device)
+    _check(v, "v", dt, (B, H, dv), device)
+    per_head = g.dim() == 1
+    _check(g, "g", torch.float32, (H,) if per_head else (B, H), device)
+    _check(state, "state", torch.float32, (B, H, dk, dv), device)
+    if o is None:
+        o = torch.empty((B, H, dv), dtype=dt, device=device)
+    else:
+        _check(o, "o", dt, (B, H, dv), device)
+    with torch.cuda.device(device):
+        rc = L.ckda_linear_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), int(per_head),
+                                       _ptr(state), _ptr(o), B, H, Hk, dk, dv, io, float(scale),
+                                       _stream_handle(stream, device))
+    if rc != 0:
+        raise CkdaError(rc, "ckda_linear_decode_step")
+    return o
+
+
+# ----------------------------------------------------------------- layer norm
+def _check_weight(weight, bias, width, device):
+    """The weights' dtype code (fp32 when there are none)."""
+    wt = weight if weight is not None else bias
+    if wt is None:
+        return _F32
+    code = _io_dtype(wt)
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None:
+            _check(t, name, wt.dtype, (width,), device)
+    return code
+
+
+def layernorm_fwd(x, weight=None, bias=None, eps=1e-5, y=None, mean=None, rstd=None, stream=None):
+    """Layer norm over the last axis (ckda_layernorm_fwd).  Returns (y, mean,
+    rstd); mean and rstd are fp32 of x's leading shape.  weight and bias are
+    bf16 or fp32 [width], whatever x's type.  y may be x (in place)."""
+    L = lib()
+    device = x.device
+    io = _io_dtype(x)
+    if x.dim() < 1:
+        raise ValueError("x has no last axis")
+    lead, width = x.shape[:-1], x.shape[-1]
+    _check(x, "x", x.dtype, x.shape, device)
+    wcode = _check_weight(weight, bias, width, device)
+    if y is None:
+        y = torch.empty_like(x)
+    else:
+        _check(y, "y", x.dtype, x.shape, device)
+    if mean is None:
+        mean = torch.empty(lead, dtype=torch.float32, device=device)
+    else:
+        _check(mean, "mean", torch.float32, lead, device)
+    if rstd is None:
+        rstd = torch.empty(lead, dtype=torch.float32, device=device)
+    else:
+        _check(rstd, "rstd", torch.float32, lead, device)
+    with torch.cuda.device(device):
+        rc = L.ckda_layernorm_fwd(_ptr(x), _ptr(weight), _ptr(bias), _ptr(y), _ptr(mean),
+                                  _ptr(rstd), mean.numel(), width, io, wcode, float(eps),
+                                  _stream_handle(stream, device))
+    if rc != 0:
+        raise CkdaError(rc, "ckda_layernorm_fwd")
+    return y, mean, rstd
+
+
+def layernorm_bwd(dy, x, mean, rstd, weight=None, weight_grad=True, dx=None, workspace=None,
+                  stream=None):
+    """Backward of layernorm_fwd (ckda_layernorm_bwd).  Returns (dx, dweight,
+    dbias); the last two have weight's type (fp32 without one) and are None
+    when weight_grad is false.  dx may be dy or x (in place)."""
+    L = lib()
+    device = x.device
+    io = _io_dtype(x)
+    if x.dim() < 1:
+        raise ValueError("x has no last axis")
+    lead, width = x.shape[:-1], x.shape[-1]
+    _check(x, "x", x.dtype, x.shape, device)
+    _check(dy, "dy", x.dtype, x.shape, device)
+    _check(mean, "mean", torch.float32, lead, device)
+    _check(rstd, "rstd", torch.float32, lead, device)
+    wcode = _check_weight(weight, None, width, device)
+    if dx is None:
+        dx = torch.empty_like(x)
+    else:
+        _check(dx, "dx", x.dtype, x.shape, device)
+    rows = mean.numel()
+    dw = db = None
+    if weight_grad:
+        wdt = torch.float32 if weight is None else weight.dtype
+        dw = torch.empty(width, dtype=wdt, device=device)
+        db = torch.empty(width, dtype=wdt, device=device)
+        if workspace is None:
+            workspace = torch.empty(L.ckda_layernorm_bwd_workspace_bytes(rows, width),
+                                    dtype=torch.uint8, device=device)
+    with torch.cuda.device(device):
+        rc = L.ckda_layernorm_bwd(_ptr(dy), _ptr(x), _ptr(mean), _ptr(rstd), _ptr(weight),
+                                  _ptr(dx), _ptr(dw), _ptr(db), rows, width, io, wcode,
+                                  _ptr(workspace), 0 if workspace is None else workspace.numel(),
+                                  _stream_handle(stream, device))
+    if rc != 0:
+        raise CkdaError(rc, "ckda_layernorm_bwd")
+    return dx, dw, db
+
+
 # ------------------------------------------------------------------- autograd
 # Training use: the forward (fwd) with its backward (bwd), and the input
 # preparation (prep) with its backward (prep_bwd), as torch.autograd
@@ -630,3 +873,53 @@ def prepare(q_raw, k_raw, a_raw, b_raw, normalize_q=True, norm_eps=1e-6):
     """(q, k, alpha, beta) = prep(...) with q_raw given, differentiable in the
     raw inputs (the gradients come from prep_bwd)."""
     return _Prepare.apply(q_raw, k_raw, a_raw, b_raw, bool(normalize_q), float(norm_eps))
+
+
+class _LinearAttention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, g, h0, cu_seqlens, scale):
+        o, hT = linear_fwd(q, k, v, g, h0, cu_seqlens, scale=scale)
+        ctx.save_for_backward(q, k, v, g, h0, cu_seqlens)
+        ctx.scale = scale
+        ctx.set_materialize_grads(False)
+        return o, hT
+
+    @staticmethod
+    def backward(ctx, do, dhT):
+        q, k, v, g, h0, cu = ctx.saved_tensors
+        do = torch.zeros_like(v) if do is None else do.contiguous()
+        dhT = None if dhT is None else dhT.contiguous()
+        dq, dk, dv, dg, dh0 = linear_bwd(q, k, v, g, do, h0=h0, dhT=dhT, cu_seqlens=cu,
+                                         scale=ctx.scale, store_dh0=h0 is not None)
+        return dq, dk, dv, dg, dh0, None, None
+
+
+def linear_attention(q, k, v, g, h0=None, cu_seqlens=None, scale=1.0):
+    """(o, hT) = linear_fwd(...), differentiable in q, k, v, g and h0 (the
+    gradients come from linear_bwd)."""
+    return _LinearAttention.apply(q, k, v, g, h0, cu_seqlens, float(scale))
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps):
+        y, mean, rstd = layernorm_fwd(x, weight, bias, eps=eps)
+        ctx.save_for_backward(x, mean, rstd, weight)
+        ctx.has_bias = bias is not None
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, mean, rstd, weight = ctx.saved_tensors
+        need = (weight is not None and ctx.needs_input_grad[1]) or \
+            (ctx.has_bias and ctx.needs_input_grad[2])
+        dx, dw, db = layernorm_bwd(dy.contiguous(), x, mean, rstd, weight, weight_grad=need)
+        return dx, dw if weight is not None else None, db if ctx.has_bias else None, None
+
+
+def layer_norm(x, weight=None, bias=None, eps=1e-5):
+    """y = layernorm_fwd(...)[0], differentiable in x, weight and bias (the
+    gradients come from layernorm_bwd).  A bias without a weight is fp32."""
+    if weight is None and bias is not None and bias.dtype != torch.float32:
+        raise TypeError(f"bias: dtype {bias.dtype}, expected {torch.float32} without a weight")
+    return _LayerNorm.apply(x, weight, bias, float(eps))

@@ -1,0 +1,109 @@
+// ckda_linear.cu -- C ABI of linear attention with a scalar decay per head:
+// argument checks, the choice of path and the workspace's layout.
+#include "ckda_linear.cuh"
+
+namespace ckda {
+namespace {
+
+ckda_status check(int N, int B, int H, int Hk, int T, int dk, int dv, ckda_dtype io, float scale,
+                  const int32_t* cu, int num_seqs) {
+  (void)N;
+  if (io != CKDA_F32 && io != CKDA_BF16) return CKDA_ERR_INVALID_ARG;
+  if (B < 1 || H < 1 || Hk < 1 || H % Hk != 0 || T < 0 || dk < 1 || dv < 1)
+    return CKDA_ERR_INVALID_ARG;
+  if (!(scale == scale)) return CKDA_ERR_INVALID_ARG;
+  if (cu) {
+    if (B != 1 || num_seqs < 1) return CKDA_ERR_INVALID_ARG;
+  } else if (num_seqs != 0 && num_seqs != B) {
+    return CKDA_ERR_INVALID_ARG;
+  }
+  if (dk > 128 || dv > 128) return CKDA_ERR_UNSUPPORTED;
+  if ((long long)B * H * T > 0x7fffffffLL) return CKDA_ERR_UNSUPPORTED;
+  if ((long long)(cu ? num_seqs : B) * H > 0x7fffffffLL) return CKDA_ERR_UNSUPPORTED;
+  return CKDA_OK;
+}
+
+size_t head_bytes(int num_seqs) {  // status word, order of packed sequences
+  const size_t n = num_seqs > 0 ? (size_t)num_seqs : 0;
+  return kWsStatusBytes + (n * sizeof(int32_t) + 255) / 256 * 256;
+}
+
+}  // namespace
+}  // namespace ckda
+
+using namespace ckda;
+
+extern "C" {
+
+size_t ckda_linear_fwd_workspace_bytes(int num_seqs, int B, int H, int T, int dk, int dv,
+                                       ckda_dtype io_dtype) {
+  (void)B; (void)H; (void)T; (void)dk; (void)dv; (void)io_dtype;
+  return head_bytes(num_seqs);
+}
+
+ckda_status ckda_linear_fwd(const void* q, const void* k, const void* v, const float* g,
+                            int g_per_head, const float* h0, void* o, float* hT,
+                            const int32_t* cu_seqlens, int num_seqs, int B, int H, int Hk, int T,
+                            int dk, int dv, ckda_dtype io_dtype, float scale, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  const int N = cu_seqlens ? num_seqs : B;
+  const ckda_status st = check(N, B, H, Hk, T, dk, dv, io_dtype, scale, cu_seqlens, num_seqs);
+  if (st != CKDA_OK) return st;
+  if (T > 0 && (!q || !k || !v || !g || !o)) return CKDA_ERR_INVALID_ARG;
+  if (!workspace ||
+      workspace_bytes < ckda_linear_fwd_workspace_bytes(cu_seqlens ? num_seqs : 0, B, H, T, dk, dv,
+                                                        io_dtype) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255) != 0)
+    return CKDA_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  LinearArgs a{};
+  a.q = q; a.k = k; a.v = v; a.g = g; a.h0 = h0; a.o = o; a.hT = hT;
+  a.cu_seqlens = cu_seqlens;
+  a.status = static_cast<int*>(workspace);
+  a.N = N; a.B = B; a.H = H; a.Hk = Hk; a.T = T; a.dk = dk; a.dv = dv;
+  a.g_head = g_per_head ? 1 : 0;
+  a.scale = scale; a.io = io_dtype;
+  if (cudaMemsetAsync(workspace, 0, sizeof(int), s) != cudaSuccess) return CKDA_ERR_CUDA;
+  return linear_serial_fwd(a, s) == cudaSuccess ? CKDA_OK : CKDA_ERR_CUDA;
+}
+
+size_t ckda_linear_bwd_workspace_bytes(int num_seqs, int B, int H, int T, int dk, int dv,
+                                       ckda_dtype io_dtype) {
+  (void)io_dtype;
+  if (num_seqs < 0 || B < 1 || H < 1 || T < 0 || dk < 1 || dv < 1) return 0;
+  return head_bytes(num_seqs) +
+         linear_serial_bwd_bytes(num_seqs > 0 ? num_seqs : B, B, H, T, dk, dv, num_seqs > 0);
+}
+
+ckda_status ckda_linear_bwd(const void* q, const void* k, const void* v, const float* g,
+                            int g_per_head, const float* h0, const void* dout, const float* dhT,
+                            void* dq, void* dkey, void* dval, float* dg, float* dh0,
+                            const int32_t* cu_seqlens, int num_seqs, int B, int H, int Hk, int T,
+                            int dk, int dv, ckda_dtype io_dtype, float scale, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  const int N = cu_seqlens ? num_seqs : B;
+  const ckda_status st = check(N, B, H, Hk, T, dk, dv, io_dtype, scale, cu_seqlens, num_seqs);
+  if (st != CKDA_OK) return st;
+  if (T > 0 && (!q || !k || !v || !g || !dout || !dq || !dkey || !dval)) return CKDA_ERR_INVALID_ARG;
+  if ((T > 0 || g_per_head) && !dg) return CKDA_ERR_INVALID_ARG;
+  if (!workspace ||
+      workspace_bytes < ckda_linear_bwd_workspace_bytes(cu_seqlens ? num_seqs : 0, B, H, T, dk, dv,
+                                                        io_dtype) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255) != 0)
+    return CKDA_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  LinearArgs a{};
+  a.q = q; a.k = k; a.v = v; a.g = g; a.h0 = h0;
+  a.dout = dout; a.dhT = dhT;
+  a.dq = dq; a.dkey = dkey; a.dval = dval; a.dg = dg; a.dh0 = dh0;
+  a.cu_seqlens = cu_seqlens;
+  a.status = static_cast<int*>(workspace);
+  a.N = N; a.B = B; a.H = H; a.Hk = Hk; a.T = T; a.dk = dk; a.dv = dv;
+  a.g_head = g_per_head ? 1 : 0;
+  a.scale = scale; a.io = io_dtype;
+  if (cudaMemsetAsync(workspace, 0, sizeof(int), s) != cudaSuccess) return CKDA_ERR_CUDA;
+  char* scratch = static_cast<char*>(workspace) + head_bytes(cu_seqlens ? num_seqs : 0);
+  return linear_serial_bwd(a, scratch, s) == cudaSuccess ? CKDA_OK : CKDA_ERR_CUDA;
+}
+
+}  // extern "C"

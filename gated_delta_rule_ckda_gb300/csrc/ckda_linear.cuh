@@ -1,0 +1,71 @@
+// ckda_linear.cuh -- declarations shared by the translation units of linear
+// attention with a scalar decay per head:
+//     H_t = exp(g_t) H_{t-1} + k_t v_t^T,    o_t = H_t^T (scale q_t)
+#pragma once
+#include "ckda_internal.cuh"
+
+namespace ckda {
+
+constexpr int kLinSms = 152;       // SMs of a GB300
+constexpr float kLog2e = 1.4426950408889634f;
+// A decay of exp2(-160) is zero in fp32 whatever it multiplies; log decays are
+// clamped there so that g = -inf (a reset) leaves sums and differences finite.
+constexpr float kMinLog2Decay = -160.f;
+constexpr int kCkptTokens = 64;    // token-serial backward: tokens between stored states
+
+struct LinearArgs {
+  const void* q;      // io   [B, Hk, T, dk]
+  const void* k;      // io   [B, Hk, T, dk]
+  const void* v;      // io   [B, H, T, dv]
+  const float* g;     // fp32 [B, H, T], or [H] when g_head
+  const float* h0;    // fp32 [N, H, dk, dv] or null
+  void* o;            // io   [B, H, T, dv]
+  float* hT;          // fp32 [N, H, dk, dv] or null
+  const int32_t* cu_seqlens;
+  const int32_t* order;
+  int* status;
+  int N;              // sequences: B, or the packed ones
+  int B, H, Hk, T, dk, dv;
+  int g_head;
+  float scale;
+  ckda_dtype io;
+  // backward
+  const void* dout;   // io   [B, H, T, dv]
+  const float* dhT;   // fp32 [N, H, dk, dv] or null
+  void* dq;           // io   [B, Hk, T, dk]
+  void* dkey;         // io   [B, Hk, T, dk]
+  void* dval;         // io   [B, H, T, dv]
+  float* dg;          // fp32 [B, H, T], or [H] when g_head
+  float* dh0;         // fp32 [N, H, dk, dv] or null
+};
+
+// Tokens [t0, t0 + len) of sequence n on the T axis.  Offsets outside [0, T]
+// are clamped, so that a bad cu_seqlens reads and writes nothing outside.
+__device__ __forceinline__ void seq_range(const LinearArgs& a, int n, int& t0, int& len) {
+  t0 = 0;
+  len = a.T;
+  if (a.cu_seqlens) {
+    t0 = min(max(a.cu_seqlens[n], 0), a.T);
+    len = max(min(a.cu_seqlens[n + 1], a.T) - t0, 0);
+  }
+}
+__device__ __forceinline__ float log2_decay(float g) {
+  // (a NaN stays one)
+  const float x = g * kLog2e;
+  return x < kMinLog2Decay ? kMinLog2Decay : x;
+}
+
+// Token-serial kernels on CUDA cores: every type and width up to 128.
+cudaError_t linear_serial_fwd(const LinearArgs& a, cudaStream_t s);
+size_t linear_serial_bwd_bytes(int N, int B, int H, int T, int dk, int dv, bool packed);
+cudaError_t linear_serial_bwd(const LinearArgs& a, char* ws, cudaStream_t s);
+
+// dq and dk of the key heads: the sum over the H / Hk heads that share one, of
+// fp32 [B, H, T, dk] partial gradients.  own (or null): fp32 [B, H, T], scale
+// v_t.do_t, where the partial gradients lack own_t k_t and own_t q_t.
+cudaError_t linear_sum_heads(const LinearArgs& a, const float* dq_part, const float* dk_part,
+                             const float* own, cudaStream_t s);
+// dg of a decay per head: the sum of fp32 [B, H, T] over B and T.
+cudaError_t linear_sum_decay(const LinearArgs& a, const float* dg_full, cudaStream_t s);
+
+}  // namespace ckda

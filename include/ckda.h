@@ -29,7 +29,8 @@
  *   - k is NOT normalised by the library: ||k_t|| = 1 is the caller's
  *     precondition, as on the pages.  The library accepts any finite k.
  *   - The compute calls (ckda_fwd, ckda_fwd_raw, the split forwards,
- *     ckda_decode_step(_raw), ckda_prep(_bwd), ckda_bwd) enqueue only kernels
+ *     ckda_decode_step(_raw), ckda_prep(_bwd), ckda_bwd, the ckda_linear_ and
+ *     ckda_layernorm_ calls) enqueue only kernels
  *     and asynchronous memsets on `stream`, so they may be captured into a
  *     CUDA graph and replayed; the tensor maps and launch arguments are fixed
  *     at capture.  ckda_fwd_status and ckda_fwd_host synchronise and may not
@@ -465,6 +466,105 @@ ckda_status ckda_prep_bwd(const void *q_raw, const void *k_raw, const void *a_ra
                           const void *d_alpha, const void *d_beta, void *d_q_raw,
                           void *d_k_raw, void *d_a_raw, void *d_b_raw, long long rows, int dk,
                           ckda_dtype io_dtype, int normalize_q, float norm_eps, void *stream);
+
+/*
+ * Linear attention with a scalar decay per head: the recurrence without the
+ * correction by what the state already holds (no beta, no unit keys), one
+ * decay per token and head in place of one per channel:
+ *
+ *     H_t = exp(g_t) H_{t-1} + k_t v_t^T,    o_t = H_t^T (scale q_t)
+ *
+ *   q, k : io   [B, Hk, T, dk]    H / Hk heads share a query/key head: head h
+ *                                 reads key head h / (H / Hk); Hk divides H
+ *   v, o : io   [B, H, T, dv]
+ *   g    : fp32 [B, H, T], or [H] when g_per_head != 0 (one decay for all of a
+ *          head's tokens).  The log decay, g <= 0 (not checked; a positive g
+ *          grows the state as the formula says).  g = -infinity resets the
+ *          state before that token's write.
+ *   h0, hT, cu_seqlens, num_seqs, scale: as ckda_fwd.  An empty sequence hands
+ *          its h0 on as hT.  hT may alias h0, o no input.
+ *
+ * dk, dv <= 128.  bf16 I/O with dk and dv multiples of 8 and 16-byte aligned
+ * q, k, v runs chunks of 128 tokens on the tensor cores; everything else runs
+ * token by token on CUDA cores.  The state is fp32 on both.
+ *
+ * workspace: ckda_linear_fwd_workspace_bytes(cu_seqlens ? num_seqs : 0, ...)
+ * bytes, 256-byte aligned, scratch with the status word ckda_fwd_status() reads
+ * (CKDA_ERR_TIMEOUT only).
+ */
+size_t ckda_linear_fwd_workspace_bytes(int num_seqs, int B, int H, int T, int dk, int dv,
+                                       ckda_dtype io_dtype);
+ckda_status ckda_linear_fwd(const void *q, const void *k, const void *v, const float *g,
+                            int g_per_head, const float *h0, void *o, float *hT,
+                            const int32_t *cu_seqlens, int num_seqs, int B, int H, int Hk,
+                            int T, int dk, int dv, ckda_dtype io_dtype, float scale,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Backward of ckda_linear_fwd: the gradients of sum <o, dout> + <hT, dhT>.
+ *
+ *   dout        : io   [B, H, T, dv]
+ *   dhT         : fp32 [N, H, dk, dv] or NULL (zero)
+ *   dq, dkey    : io   [B, Hk, T, dk], summed over the heads that share them
+ *   dval        : io   [B, H, T, dv]
+ *   dg          : fp32, of g's shape ([H] is summed over B and T)
+ *   dh0         : fp32 [N, H, dk, dv] or NULL (not stored)
+ *
+ * The forward's states are recomputed.  No atomics: the same inputs give the
+ * same bits.  workspace as above, of ckda_linear_bwd_workspace_bytes bytes.
+ */
+size_t ckda_linear_bwd_workspace_bytes(int num_seqs, int B, int H, int T, int dk, int dv,
+                                       ckda_dtype io_dtype);
+ckda_status ckda_linear_bwd(const void *q, const void *k, const void *v, const float *g,
+                            int g_per_head, const float *h0, const void *dout,
+                            const float *dhT, void *dq, void *dkey, void *dval, float *dg,
+                            float *dh0, const int32_t *cu_seqlens, int num_seqs, int B, int H,
+                            int Hk, int T, int dk, int dv, ckda_dtype io_dtype, float scale,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * One token of the same recurrence on a resident state, updated in place.
+ *   q, k : io [B, Hk, dk];  v, o : io [B, H, dv];  g : fp32 [B, H], or [H]
+ *   state: fp32 [B, H, dk, dv]
+ * dk, dv <= 128.
+ */
+ckda_status ckda_linear_decode_step(const void *q, const void *k, const void *v,
+                                    const float *g, int g_per_head, float *state, void *o,
+                                    int B, int H, int Hk, int dk, int dv, ckda_dtype io_dtype,
+                                    float scale, void *stream);
+
+/*
+ * Layer norm over the last axis (before a layer, or over each head's output):
+ *     y = (x - mean) rstd weight + bias,   rstd = 1 / sqrt(var + eps),
+ * var the mean of (x - mean)^2.
+ *   x, y         : io [rows, width]; y may alias x
+ *   weight, bias : weight_dtype [width], each may be NULL (one, zero)
+ *   mean, rstd   : fp32 [rows], for the backward pass
+ * Arithmetic in fp32 with one rounding to io_dtype.  Rows of any width; 16-byte
+ * aligned rows (width a multiple of 8 in bf16, 4 in fp32, and aligned bases) are
+ * moved in 16-byte vectors.  rows = 0 launches nothing.
+ */
+ckda_status ckda_layernorm_fwd(const void *x, const void *weight, const void *bias, void *y,
+                               float *mean, float *rstd, long long rows, int width,
+                               ckda_dtype io_dtype, ckda_dtype weight_dtype, float eps,
+                               void *stream);
+
+/*
+ * Its backward: with t = dy weight and xh = (x - mean) rstd, per row
+ *     dx = rstd (t - mean(t) - xh mean(t xh)),
+ * and dweight = sum over rows of dy xh, dbias = sum over rows of dy, in
+ * weight_dtype from fp32 sums in a fixed order.
+ *   dx may alias dy or x; dweight and dbias are both set or both NULL (not
+ *   wanted; the workspace may then be NULL).  rows = 0 writes zero weight
+ *   gradients.  workspace: ckda_layernorm_bwd_workspace_bytes(rows, width)
+ *   bytes, 16-byte aligned.
+ */
+size_t ckda_layernorm_bwd_workspace_bytes(long long rows, int width);
+ckda_status ckda_layernorm_bwd(const void *dy, const void *x, const float *mean,
+                               const float *rstd, const void *weight, void *dx, void *dweight,
+                               void *dbias, long long rows, int width, ckda_dtype io_dtype,
+                               ckda_dtype weight_dtype, void *workspace,
+                               size_t workspace_bytes, void *stream);
 
 /*
  * Self-test of the bounded-wait path: launches one block that waits on a
