@@ -64,7 +64,19 @@ ckda_status ckda_linear_fwd(const void* q, const void* k, const void* v, const f
   a.g_head = g_per_head ? 1 : 0;
   a.scale = scale; a.io = io_dtype;
   if (cudaMemsetAsync(workspace, 0, sizeof(int), s) != cudaSuccess) return CKDA_ERR_CUDA;
-  return linear_serial_fwd(a, s) == cudaSuccess ? CKDA_OK : CKDA_ERR_CUDA;
+  cudaError_t e = cudaSuccess;
+  if (linear_chunk_path(io_dtype, dk, dv) && aligned16(q) && aligned16(k) && aligned16(v) &&
+      aligned16(o)) {
+    if (cu_seqlens) {
+      int32_t* order = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + kWsStatusBytes);
+      e = launch_seq_order(cu_seqlens, num_seqs, order, s);
+      a.order = order;
+    }
+    if (e == cudaSuccess) e = linear_chunk_fwd(a, s);
+  } else {
+    e = linear_serial_fwd(a, s);
+  }
+  return e == cudaSuccess ? CKDA_OK : CKDA_ERR_CUDA;
 }
 
 size_t ckda_linear_bwd_workspace_bytes(int num_seqs, int B, int H, int T, int dk, int dv,

@@ -60,6 +60,15 @@ cudaError_t linear_serial_fwd(const LinearArgs& a, cudaStream_t s);
 size_t linear_serial_bwd_bytes(int N, int B, int H, int T, int dk, int dv, bool packed);
 cudaError_t linear_serial_bwd(const LinearArgs& a, char* ws, cudaStream_t s);
 
+// Shapes and pointers the chunked tensor-core kernels take: TMA wants 16-byte
+// aligned rows and bases.
+inline bool linear_chunk_path(ckda_dtype io, int dk, int dv) {
+  return io == CKDA_BF16 && dk % 8 == 0 && dv % 8 == 0;
+}
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+// Chunks of 128 tokens on the tensor cores.
+cudaError_t linear_chunk_fwd(const LinearArgs& a, cudaStream_t s);
+
 // dq and dk of the key heads: the sum over the H / Hk heads that share one, of
 // fp32 [B, H, T, dk] partial gradients.  own (or null): fp32 [B, H, T], scale
 // v_t.do_t, where the partial gradients lack own_t k_t and own_t q_t.

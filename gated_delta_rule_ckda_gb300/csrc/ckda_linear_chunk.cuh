@@ -1,0 +1,198 @@
+// ckda_linear_chunk.cuh -- what the chunked tensor-core kernels of linear
+// attention share: tiles of 128 tokens by 128 channels, their loads, the decay
+// factors of a chunk, and bounded waits.
+#pragma once
+#include "ckda_linear.cuh"
+#include "sm103.cuh"
+
+namespace ckda {
+namespace chunk {
+
+constexpr int C = 128;                 // tokens of a chunk
+constexpr uint32_t kTile = 32768;      // bytes of a 128 x 128 bf16 tile, two 64-column panels
+constexpr uint32_t kPanel = 16384;
+
+// A unit of work: one (sequence, head), or one segment of it.
+struct Unit {
+  int n, h, hk, b;     // sequence, head, key head, batch row
+  int t0, len;         // tokens on the T axis
+  int seg;             // segment of the sequence (0 when not split)
+  size_t krow, vrow;   // row of token t0 among [B * Hk * T] and [B * H * T]
+};
+
+// ------------------------------------------------------------------- TMA
+// Box of 64 channels x 128 tokens of one head; coordinates (channel, token,
+// head).  Channels past the width and tokens past T are filled with zeros.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint64_t* bar,
+                                            int32_t x, int32_t y, int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+// Both panels of a tile; completion counts kTile bytes on `bar`.
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, uint64_t* bar,
+                                          int32_t token, int32_t head) {
+  mbar_arrive_expect_tx(bar, kTile);
+  tma_load_3d(dst, map, bar, 0, token, head);
+  tma_load_3d(dst + kPanel, map, bar, 64, token, head);
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]: row i of A in lane i, two bf16 a column.
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                        uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// 128 x 128 products over K = 128, bf16 operands.  `mn`: the operand is stored
+// with its K index along the rows.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, bool a_mn, uint32_t b, bool b_mn,
+                                       bool accumulate) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    umma_ss(d, a_mn ? mnmajor_desc(a, 128, k) : kmajor_desc(a, 128, k),
+            b_mn ? mnmajor_desc(b, 128, k) : kmajor_desc(b, 128, k),
+            idesc_f16(128, 128, 1, a_mn, b_mn), (accumulate || k > 0) ? 1u : 0u);
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b, bool b_mn,
+                                       bool accumulate) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    umma_ts(d, a_tmem + 8 * k, b_mn ? mnmajor_desc(b, 128, k) : kmajor_desc(b, 128, k),
+            idesc_f16(128, 128, 1, 0, b_mn), (accumulate || k > 0) ? 1u : 0u);
+}
+
+// ----------------------------------------------------------------- waiting
+// Bounded (about a second), and over at once when another warp has given up.
+// Called by whole warps; the answer is the same in every lane.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  bool ok = mbar_try_wait(bar, parity, 1000000u);
+  if (!ok) {
+    const uint64_t start = globaltimer_ns();
+    for (uint32_t i = 0; i < (1u << 24) && !ok; ++i) {
+      ok = mbar_try_wait(bar, parity, 1000000u);
+      if (!ok && (*abort || globaltimer_ns() - start > kWaitLimitNs)) break;
+    }
+  }
+  ok = __all_sync(0xffffffffu, ok);
+  if (!ok) *abort = 1;
+  return ok;
+}
+// Orders this warp's shared-memory writes and TMEM accesses before the tensor
+// cores' next use, and arrives once for the warp.
+__device__ __forceinline__ void warp_publish(uint64_t* bar) {
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  tc_fence_before();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+// ------------------------------------------------------------------ decays
+// Factors of a chunk of 128 tokens in four blocks of 32, from log2 decays x_t
+// (zero past the end).  Sums run inside a block and over whole blocks, each
+// from the side it is read from, so that no factor is the exponential of a
+// difference of large sums:
+//   pre_t  sum of x over the block's tokens up to t
+//   es_t   exp2 of the sum over the block's tokens after t
+//   eL_t   exp2 of the sum from the chunk's start to t
+//   w_t    exp2 of the sum after t to the chunk's end
+//   tot_b  sum over block b;   all = exp2 of the sum over the chunk
+struct Gates {
+  float pre[C], es[C], eL[C], w[C];
+  float tot[4];
+  float all;
+  float pad[3];
+};
+// One warp: lane l brings tokens 4l .. 4l+3.
+__device__ __forceinline__ void make_gates(Gates* g, float4 x, int lane) {
+  const float p0 = x.x, p1 = p0 + x.y, p2 = p1 + x.z, sum = p2 + x.w;
+  const float s2 = x.w, s1 = x.z + s2, s0 = x.y + s1;
+  float up = sum, down = sum;  // inclusive scans over the block's eight lanes
+#pragma unroll
+  for (int m = 1; m < 8; m <<= 1) {
+    const float a = __shfl_up_sync(0xffffffffu, up, m, 8);
+    const float b = __shfl_down_sync(0xffffffffu, down, m, 8);
+    if ((lane & 7) >= m) up += a;
+    if ((lane & 7) + m < 8) down += b;
+  }
+  // exclusive: shifted, not subtracted
+  float before = __shfl_up_sync(0xffffffffu, up, 1, 8);
+  float after = __shfl_down_sync(0xffffffffu, down, 1, 8);
+  if ((lane & 7) == 0) before = 0.f;
+  if ((lane & 7) == 7) after = 0.f;
+  const float tot = __shfl_sync(0xffffffffu, up, 7, 8);
+  const float t0 = __shfl_sync(0xffffffffu, tot, 0), t1 = __shfl_sync(0xffffffffu, tot, 8);
+  const float t2 = __shfl_sync(0xffffffffu, tot, 16), t3 = __shfl_sync(0xffffffffu, tot, 24);
+  const int b = lane >> 3;
+  const float earlier = b == 0 ? 0.f : b == 1 ? t0 : b == 2 ? t0 + t1 : t0 + t1 + t2;
+  const float later = b == 3 ? 0.f : b == 2 ? t3 : b == 1 ? t3 + t2 : t3 + t2 + t1;
+  const float4 pre = make_float4(before + p0, before + p1, before + p2, before + sum);
+  const float4 suf = make_float4(after + s0, after + s1, after + s2, after);
+  reinterpret_cast<float4*>(g->pre)[lane] = pre;
+  reinterpret_cast<float4*>(g->es)[lane] =
+      make_float4(exp2f(suf.x), exp2f(suf.y), exp2f(suf.z), exp2f(suf.w));
+  reinterpret_cast<float4*>(g->eL)[lane] =
+      make_float4(exp2f(earlier + pre.x), exp2f(earlier + pre.y), exp2f(earlier + pre.z),
+                  exp2f(earlier + pre.w));
+  reinterpret_cast<float4*>(g->w)[lane] =
+      make_float4(exp2f(later + suf.x), exp2f(later + suf.y), exp2f(later + suf.z),
+                  exp2f(later + suf.w));
+  if ((lane & 7) == 0) g->tot[b] = tot;
+  if (lane == 0) g->all = exp2f(t0 + t1 + t2 + t3);
+}
+// log2 decays of tokens 4l .. 4l+3 of a chunk, `valid` of its tokens in the sequence.
+__device__ __forceinline__ float4 load_decays(const float* g, int stride, int valid, int lane) {
+  float x[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    x[e] = 4 * lane + e < valid ? log2_decay(g[(size_t)(4 * lane + e) * stride]) : 0.f;
+  return make_float4(x[0], x[1], x[2], x[3]);
+}
+
+// Rows [valid, 128) of a tile, row by row, set to zero (by 128 threads): tokens
+// of the next packed sequence, whose values must not reach a product even with
+// a factor of zero.
+__device__ __forceinline__ void zero_row(char* tile, int row) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    *reinterpret_cast<uint4*>(tile + sw128_chunk(128, row, j)) = make_uint4(0, 0, 0, 0);
+}
+
+// A token row of 64 channels times w, in two bf16 parts: hi in place, lo at the
+// same place of another tile.  hi + lo is w k to 2^-16, which fp32 results need.
+__device__ __forceinline__ void scale_row(char* tile, char* lo, int row, int panel, float w,
+                                          bool keep) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t off = sw128_chunk(128, row, 8 * panel + j);
+    const uint4 v = *reinterpret_cast<const uint4*>(tile + off);
+    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+    uint32_t hi[4], rest[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float a = keep ? __uint_as_float(in[e] << 16) * w : 0.f;
+      const float b = keep ? __uint_as_float(in[e] & 0xffff0000u) * w : 0.f;
+      hi[e] = pack_bf162(a, b);
+      rest[e] = pack_bf162(a - __uint_as_float(hi[e] << 16),
+                           b - __uint_as_float(hi[e] & 0xffff0000u));
+    }
+    *reinterpret_cast<uint4*>(tile + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(lo + off) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
+  }
+}
+
+}  // namespace chunk
+
+// Tensor map of a [heads, T, width] bf16 tensor for load_tile.
+bool linear_map(CUtensorMap* m, const void* base, uint64_t heads, uint64_t T, uint64_t width);
+
+}  // namespace ckda

@@ -1,0 +1,351 @@
+// ckda_linear_fwd.cu -- chunked forward of linear attention with a scalar decay
+// per head on the tensor cores (bf16 I/O, widths up to 128).
+//
+// A chunk of 128 tokens, with L_i the cumulative log decay inside it and H the
+// state entering it:
+//     S = Q K^T,   P_ij = S_ij e^{L_i - L_j} (j <= i),
+//     O = P V + e^{L_i} (Q H),
+//     H <- e^{L_C} H + sum_j e^{L_C - L_j} k_j v_j^T.
+// Every exponent is a sum of log decays, so with g <= 0 no factor exceeds one.
+//
+// One CTA of 512 threads walks the chunks of one (sequence, head); the state
+// never leaves the SM.  It is bound by HBM: 1 KiB a token at 128 x 128 against
+// five 128 x 128 x 128 products a chunk.
+//   warp 0       loads tiles with TMA into a ring of five 32 KB slots, in the
+//                order k, q, v of chunk after chunk
+//   warp 1       issues the products (tcgen05, one thread)
+//   warp 2       the decay factors of a chunk
+//   warps 4-7    one row of S a thread: P as bf16 into TMEM, where the product
+//                P V reads it; later the row of o
+//   warps 8-15   the state: thread (r, s) holds H[64 s .. 64 s + 63][r] in
+//                fp32 registers, rounded to nearest at every step (tensor-core
+//                accumulators truncate, which over thousands of chunks would
+//                bias a slowly decaying state).  A chunk's own contribution is
+//                a product of its own into fresh TMEM columns, so it does not
+//                wait for the state; per chunk the state warps
+//                  - write H as bf16 to shared memory for Q H,
+//                  - scale the keys by e^{L_C - L_j} in two bf16 parts (hi over
+//                    the key tile, lo beside it): the state is an fp32 output,
+//                    and one rounding of the keys would leave it with 2^-9,
+//                  - read the product and update H.
+// Rounded to bf16 are P, and H where it is read by the queries: o is bf16.
+#include "ckda_linear_chunk.cuh"
+
+namespace ckda {
+namespace {
+using namespace chunk;
+
+constexpr int kThreads = 512;
+constexpr int kSlots = 5;
+constexpr uint32_t kLo = kSlots * kTile;        // lo part of the scaled keys
+constexpr uint32_t kH = kLo + kTile;            // bf16 state, [dv][dk]
+constexpr uint32_t kGates = kH + kTile;
+constexpr uint32_t kBars = kGates + sizeof(Gates);
+constexpr uint32_t kSmem = kBars + 512;
+static_assert(kSmem <= 232448, "shared memory of a CTA");
+
+enum {
+  B_FULL = 0, B_EMPTY = kSlots, B_S = 2 * kSlots, B_P, B_O, B_OFREE, B_HREADY, B_OI, B_KT, B_DF,
+  B_G, B_GFREE, B_END, B_COUNT
+};
+// TMEM columns
+constexpr uint32_t T_S = 0, T_P = 0, T_DF = 128, T_OI = 256, T_O = 384;
+
+__global__ void __launch_bounds__(kThreads, 1)
+linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ CUtensorMap mq,
+                  const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+  extern __shared__ __align__(1024) char sm[];
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kBars);
+  Gates* gates = reinterpret_cast<Gates*>(sm + kGates);
+  volatile int* abort = reinterpret_cast<volatile int*>(sm + kBars + 400);
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(sm + kBars + 404);
+  const uint32_t sb = smem_u32(sm);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (sb & 1023u) {  // swizzled tiles need it; no room to align by hand
+    if (tid == 0) set_status(a.status, CKDA_ERR_CUDA);
+    return;
+  }
+
+  const int order = blockIdx.x / a.H, h = blockIdx.x % a.H;
+  const int n = a.order ? a.order[order] : order;
+  const int b = a.cu_seqlens ? 0 : n, hk = h / (a.H / a.Hk);
+  int t0, len;
+  seq_range(a, n, t0, len);
+  const int chunks = (len + C - 1) / C;
+  const int qz = b * a.Hk + hk, vz = b * a.H + h;
+  const size_t vrow = (size_t)vz * a.T + t0;
+  const size_t st = ((size_t)n * a.H + h) * (size_t)a.dk * a.dv;
+
+  if (tid == 0) {
+    for (int i = 0; i < B_COUNT; ++i) {
+      const uint32_t count = i == B_P || i == B_OFREE ? 4
+                             : i == B_HREADY || i == B_KT ? 8
+                             : i == B_GFREE ? 12
+                                            : 1;
+      mbar_init(bars + i, count);
+    }
+    *abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 3) {
+    tmem_alloc(tmem_at, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_at;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------- loads
+    if (lane == 0) {
+      for (int i = 0; i < 3 * chunks; ++i) {
+        const int slot = i % kSlots, use = i / kSlots, c = i / 3;
+        if (use > 0 && !mbar_wait(bars + B_EMPTY + slot, (use - 1) & 1)) { *abort = 1; break; }
+        if (*abort) break;
+        const CUtensorMap* m = i % 3 == 0 ? &mk : i % 3 == 1 ? &mq : &mv;
+        load_tile(sb + slot * kTile, m, bars + B_FULL + slot, t0 + c * C, i % 3 == 2 ? vz : qz);
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- products
+    for (int c = 0; c < chunks; ++c) {
+      const uint32_t par = c & 1;
+      const int ik = 3 * c, iq = ik + 1, iv = ik + 2;
+      const uint32_t K = sb + (ik % kSlots) * kTile, Q = sb + (iq % kSlots) * kTile,
+                     V = sb + (iv % kSlots) * kTile;
+      if (!warp_wait(bars + B_FULL + ik % kSlots, (ik / kSlots) & 1, abort)) break;
+      if (!warp_wait(bars + B_FULL + iq % kSlots, (iq / kSlots) & 1, abort)) break;
+      // P shares the columns of S: the previous chunk's P V must be done
+      if (c > 0 && !warp_wait(bars + B_O, (c - 1) & 1, abort)) break;
+      tc_fence_after();
+      if (lane == 0) {
+        mma_ss(tmem + T_S, Q, false, K, false, false);
+        umma_commit(bars + B_S);
+      }
+      if (!warp_wait(bars + B_HREADY, par, abort)) break;
+      if (c > 0 && !warp_wait(bars + B_OFREE, (c - 1) & 1, abort)) break;
+      tc_fence_after();
+      if (lane == 0) {
+        mma_ss(tmem + T_OI, Q, false, sb + kH, false, false);
+        umma_commit(bars + B_OI);
+        umma_commit(bars + B_EMPTY + iq % kSlots);
+      }
+      if (!warp_wait(bars + B_FULL + iv % kSlots, (iv / kSlots) & 1, abort)) break;
+      if (!warp_wait(bars + B_P, par, abort)) break;
+      tc_fence_after();
+      if (lane == 0) {
+        mma_ts(tmem + T_O, tmem + T_P, V, true, false);
+        umma_commit(bars + B_O);
+      }
+      if (!warp_wait(bars + B_KT, par, abort)) break;
+      tc_fence_after();
+      if (lane == 0) {
+        mma_ss(tmem + T_DF, V, true, K, true, false);
+        mma_ss(tmem + T_DF, V, true, sb + kLo, true, true);
+        umma_commit(bars + B_DF);
+        umma_commit(bars + B_EMPTY + ik % kSlots);
+        umma_commit(bars + B_EMPTY + iv % kSlots);
+      }
+    }
+    if (lane == 0) umma_commit(bars + B_END);
+  } else if (warp == 2) {
+    // ------------------------------------------------------------- decays
+    const float* g = a.g_head ? a.g + h : a.g + vrow;
+    const int gs = a.g_head ? 0 : 1;
+    float4 x = load_decays(g, gs, min(len, C), lane);
+    for (int c = 0; c < chunks; ++c) {
+      if (c > 0 && !warp_wait(bars + B_GFREE, (c - 1) & 1, abort)) break;
+      make_gates(gates, x, lane);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + B_G);
+      if (c + 1 < chunks)
+        x = load_decays(g + (size_t)(c + 1) * C * gs, gs, min(len - (c + 1) * C, C), lane);
+    }
+  } else if (warp >= 4 && warp < 8) {
+    // ------------------------------------------------------------- P and o
+    const int w = warp - 4, i = tid - 128;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16);
+    for (int c = 0; c < chunks; ++c) {
+      const uint32_t par = c & 1;
+      const int valid = min(len - c * C, C), iv = 3 * c + 2;
+      if (a.cu_seqlens && valid < C) {  // tokens of the next sequence behind this one
+        if (!warp_wait(bars + B_FULL + iv % kSlots, (iv / kSlots) & 1, abort)) break;
+        if (i >= valid) zero_row(sm + (iv % kSlots) * kTile, i);
+      }
+      if (!warp_wait(bars + B_G, par, abort)) break;
+      const float pre = gates->pre[i], into = gates->eL[i];
+      if (!warp_wait(bars + B_S, par, abort)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        uint32_t out[16];
+        if (p > w) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) out[e] = 0;
+        } else {
+          uint32_t s[32];
+          tmem_ld32<32>(lanes + T_S + 32 * p, s);
+          if (p == w) {
+            tmem_ld_wait();
+            // j <= i inside a block of 32: from the difference of short sums
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float2 q = reinterpret_cast<const float2*>(gates->pre + 32 * p)[e];
+              const float u = 2 * e <= lane ? __uint_as_float(s[2 * e]) * exp2f(pre - q.x) : 0.f;
+              const float v =
+                  2 * e + 1 <= lane ? __uint_as_float(s[2 * e + 1]) * exp2f(pre - q.y) : 0.f;
+              out[e] = pack_bf162(u, v);
+            }
+          } else {
+            // an earlier block: from j to its block's end, over the blocks
+            // between, and from this block's start to i
+            float x = pre;
+#pragma unroll
+            for (int m = 1; m < 3; ++m)
+              if (m > p && m < w) x += gates->tot[m];
+            const float r = exp2f(x);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float2 q = reinterpret_cast<const float2*>(gates->es + 32 * p)[e];
+              out[e] = pack_bf162(__uint_as_float(s[2 * e]) * (r * q.x),
+                                  __uint_as_float(s[2 * e + 1]) * (r * q.y));
+            }
+          }
+        }
+        tmem_st32<16>(lanes + T_P + 16 * p, out);
+      }
+      tmem_st_wait();
+      warp_publish(bars + B_P);
+      if (lane == 0) mbar_arrive(bars + B_GFREE);
+
+      if (!warp_wait(bars + B_O, par, abort)) break;
+      tc_fence_after();
+      __nv_bfloat16* row = static_cast<__nv_bfloat16*>(a.o) + (vrow + (size_t)c * C + i) * a.dv;
+      const float fo = a.scale, fi = a.scale * into;
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        if (32 * p >= a.dv) break;
+        uint32_t x[32], y[32];
+        tmem_ld32<32>(lanes + T_O + 32 * p, x);
+        tmem_ld32<32>(lanes + T_OI + 32 * p, y);
+        tmem_ld_wait();
+        if (i < valid) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (32 * p + 8 * j >= a.dv) break;
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int k = 8 * j + 2 * e;
+              o[e] = pack_bf162(
+                  fmaf(fo, __uint_as_float(x[k]), fi * __uint_as_float(y[k])),
+                  fmaf(fo, __uint_as_float(x[k + 1]), fi * __uint_as_float(y[k + 1])));
+            }
+            *reinterpret_cast<uint4*>(row + 32 * p + 8 * j) = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+        }
+      }
+      warp_arrive(bars + B_OFREE);
+    }
+  } else if (warp >= 8) {
+    // --------------------------------------------------------------- state
+    const int s = (warp - 8) >> 2, r = (tid - 256) & 127;   // panel of dk, value column
+    const uint32_t lanes = tmem + ((uint32_t)(r & 96) << 16);
+    float H[64];
+#pragma unroll
+    for (int i = 0; i < 64; ++i) {
+      const int d = 64 * s + i;
+      H[i] = a.h0 && r < a.dv && d < a.dk ? a.h0[st + (size_t)d * a.dv + r] : 0.f;
+    }
+    bool ok = true;
+    for (int c = 0; c < chunks; ++c) {
+      const uint32_t par = c & 1;
+      const int ik = 3 * c, valid = min(len - c * C, C);
+      // the state entering the chunk, once the last chunk's queries have read theirs
+      if (c > 0 && !(ok = warp_wait(bars + B_OI, (c - 1) & 1, abort))) break;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        *reinterpret_cast<uint4*>(sm + kH + sw128_chunk(128, r, 8 * s + j)) =
+            make_uint4(pack_bf162(H[8 * j], H[8 * j + 1]), pack_bf162(H[8 * j + 2], H[8 * j + 3]),
+                       pack_bf162(H[8 * j + 4], H[8 * j + 5]),
+                       pack_bf162(H[8 * j + 6], H[8 * j + 7]));
+      warp_publish(bars + B_HREADY);
+      // the keys, scaled, once S has read them
+      if (!(ok = warp_wait(bars + B_G, par, abort))) break;
+      const float wt = gates->w[r], all = gates->all;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + B_GFREE);
+      if (!(ok = warp_wait(bars + B_FULL + ik % kSlots, (ik / kSlots) & 1, abort))) break;
+      if (!(ok = warp_wait(bars + B_S, par, abort))) break;
+      scale_row(sm + (ik % kSlots) * kTile, sm + kLo, r, s, wt, r < valid);
+      warp_publish(bars + B_KT);
+      // the chunk's contribution
+      if (!(ok = warp_wait(bars + B_DF, par, abort))) break;
+      tc_fence_after();
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        uint32_t x[32];
+        tmem_ld32<32>(lanes + T_DF + 64 * s + 32 * p, x);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          H[32 * p + i] = fmaf(all, H[32 * p + i], __uint_as_float(x[i]));
+      }
+      tc_fence_before();
+    }
+    if (ok && a.hT && r < a.dv) {
+#pragma unroll
+      for (int i = 0; i < 64; ++i) {
+        const int d = 64 * s + i;
+        if (d < a.dk) a.hT[st + (size_t)d * a.dv + r] = H[i];
+      }
+    }
+  }
+
+  // ------------------------------------------------------------- teardown
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0) {
+    // every commit has arrived before the memory is given back
+    if (!mbar_wait(bars + B_END, 0)) *abort = 1;
+    if (*abort) {
+      set_status(a.status, CKDA_ERR_TIMEOUT);
+      for (int i = 0; i < kSlots; ++i) mbar_wait(bars + B_FULL + i, 0, 1u << 12, 1000u);
+    }
+  }
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 3) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace
+
+bool linear_map(CUtensorMap* m, const void* base, uint64_t heads, uint64_t T, uint64_t width) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t dim[3] = {width, T, heads};
+  cuuint64_t stride[2] = {width * 2, width * T * 2};
+  cuuint32_t box[3] = {64, 128, 1};
+  cuuint32_t step[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dim, stride, box,
+             step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t linear_chunk_fwd(const LinearArgs& a, cudaStream_t s) {
+  CUtensorMap mq{}, mk{}, mv{};
+  if (a.T > 0 && (!linear_map(&mq, a.q, (uint64_t)a.B * a.Hk, a.T, a.dk) ||
+                  !linear_map(&mk, a.k, (uint64_t)a.B * a.Hk, a.T, a.dk) ||
+                  !linear_map(&mv, a.v, (uint64_t)a.B * a.H, a.T, a.dv)))
+    return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(linear_fwd_kernel,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  if (e != cudaSuccess) return e;
+  linear_fwd_kernel<<<(unsigned)a.N * a.H, kThreads, kSmem, s>>>(a, mq, mk, mv);
+  return cudaGetLastError();
+}
+
+}  // namespace ckda
