@@ -118,7 +118,7 @@ def lib():
             L.ckda_linear_fwd.restype = i32
             L.ckda_linear_fwd.argtypes = lin + [vp] * 3 + [i32] * 8 + [f32, vp, sz, vp]
             L.ckda_linear_bwd_workspace_bytes.restype = sz
-            L.ckda_linear_bwd_workspace_bytes.argtypes = [i32] * 7
+            L.ckda_linear_bwd_workspace_bytes.argtypes = [i32] * 8
             L.ckda_linear_bwd.restype = i32
             L.ckda_linear_bwd.argtypes = lin + [vp] * 8 + [i32] * 8 + [f32, vp, sz, vp]
             L.ckda_linear_decode_step.restype = i32
@@ -638,9 +638,9 @@ def linear_fwd_workspace_bytes(B, H, T, dk, dv, dtype=torch.bfloat16, num_seqs=0
     return int(lib().ckda_linear_fwd_workspace_bytes(num_seqs, B, H, T, dk, dv, io))
 
 
-def linear_bwd_workspace_bytes(B, H, T, dk, dv, dtype=torch.bfloat16, num_seqs=0) -> int:
+def linear_bwd_workspace_bytes(B, H, Hk, T, dk, dv, dtype=torch.bfloat16, num_seqs=0) -> int:
     io = _BF16 if dtype == torch.bfloat16 else _F32
-    return int(lib().ckda_linear_bwd_workspace_bytes(num_seqs, B, H, T, dk, dv, io))
+    return int(lib().ckda_linear_bwd_workspace_bytes(num_seqs, B, H, Hk, T, dk, dv, io))
 
 
 def linear_fwd(q, k, v, g, h0=None, cu_seqlens=None, scale=1.0, store_final_state=True, o=None,
@@ -687,7 +687,7 @@ def linear_bwd(q, k, v, g, do, h0=None, dhT=None, cu_seqlens=None, scale=1.0, st
                                                          (("h0", h0), ("dhT", dhT)), (("do", do),))
     nseq = N if cu_seqlens is not None else 0
     if workspace is None:
-        workspace = torch.empty(L.ckda_linear_bwd_workspace_bytes(nseq, B, H, T, dk, dv, io),
+        workspace = torch.empty(L.ckda_linear_bwd_workspace_bytes(nseq, B, H, Hk, T, dk, dv, io),
                                 dtype=torch.uint8, device=device)
     dq, dkk, dvv, dg = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v),
                         torch.empty_like(g))

@@ -79,12 +79,17 @@ ckda_status ckda_linear_fwd(const void* q, const void* k, const void* v, const f
   return e == cudaSuccess ? CKDA_OK : CKDA_ERR_CUDA;
 }
 
-size_t ckda_linear_bwd_workspace_bytes(int num_seqs, int B, int H, int T, int dk, int dv,
+size_t ckda_linear_bwd_workspace_bytes(int num_seqs, int B, int H, int Hk, int T, int dk, int dv,
                                        ckda_dtype io_dtype) {
-  (void)io_dtype;
-  if (num_seqs < 0 || B < 1 || H < 1 || T < 0 || dk < 1 || dv < 1) return 0;
-  return head_bytes(num_seqs) +
-         linear_serial_bwd_bytes(num_seqs > 0 ? num_seqs : B, B, H, T, dk, dv, num_seqs > 0);
+  if (num_seqs < 0 || B < 1 || H < 1 || Hk < 1 || T < 0 || dk < 1 || dv < 1) return 0;
+  const int N = num_seqs > 0 ? num_seqs : B;
+  // what either path takes: which one runs depends on the pointers' alignment too
+  size_t bytes = linear_serial_bwd_bytes(N, B, H, T, dk, dv, num_seqs > 0);
+  if (linear_chunk_path(io_dtype, dk, dv)) {
+    const size_t chunk = linear_chunk_bwd_bytes(N, B, H, Hk, T, dk, num_seqs > 0);
+    if (chunk > bytes) bytes = chunk;
+  }
+  return head_bytes(num_seqs) + bytes;
 }
 
 ckda_status ckda_linear_bwd(const void* q, const void* k, const void* v, const float* g,
@@ -99,7 +104,7 @@ ckda_status ckda_linear_bwd(const void* q, const void* k, const void* v, const f
   if (T > 0 && (!q || !k || !v || !g || !dout || !dq || !dkey || !dval)) return CKDA_ERR_INVALID_ARG;
   if ((T > 0 || g_per_head) && !dg) return CKDA_ERR_INVALID_ARG;
   if (!workspace ||
-      workspace_bytes < ckda_linear_bwd_workspace_bytes(cu_seqlens ? num_seqs : 0, B, H, T, dk, dv,
+      workspace_bytes < ckda_linear_bwd_workspace_bytes(cu_seqlens ? num_seqs : 0, B, H, Hk, T, dk, dv,
                                                         io_dtype) ||
       (reinterpret_cast<uintptr_t>(workspace) & 255) != 0)
     return CKDA_ERR_WORKSPACE;
@@ -115,7 +120,19 @@ ckda_status ckda_linear_bwd(const void* q, const void* k, const void* v, const f
   a.scale = scale; a.io = io_dtype;
   if (cudaMemsetAsync(workspace, 0, sizeof(int), s) != cudaSuccess) return CKDA_ERR_CUDA;
   char* scratch = static_cast<char*>(workspace) + head_bytes(cu_seqlens ? num_seqs : 0);
-  return linear_serial_bwd(a, scratch, s) == cudaSuccess ? CKDA_OK : CKDA_ERR_CUDA;
+  cudaError_t e = cudaSuccess;
+  if (linear_chunk_path(io_dtype, dk, dv) && aligned16(q) && aligned16(k) && aligned16(v) &&
+      aligned16(dout) && aligned16(dq) && aligned16(dkey) && aligned16(dval)) {
+    if (cu_seqlens) {
+      int32_t* order = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + kWsStatusBytes);
+      e = launch_seq_order(cu_seqlens, num_seqs, order, s);
+      a.order = order;
+    }
+    if (e == cudaSuccess) e = linear_chunk_bwd(a, scratch, s);
+  } else {
+    e = linear_serial_bwd(a, scratch, s);
+  }
+  return e == cudaSuccess ? CKDA_OK : CKDA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -68,6 +68,8 @@ inline bool linear_chunk_path(ckda_dtype io, int dk, int dv) {
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 // Chunks of 128 tokens on the tensor cores.
 cudaError_t linear_chunk_fwd(const LinearArgs& a, cudaStream_t s);
+size_t linear_chunk_bwd_bytes(int N, int B, int H, int Hk, int T, int dk, bool packed);
+cudaError_t linear_chunk_bwd(const LinearArgs& a, char* ws, cudaStream_t s);
 
 // dq and dk of the key heads: the sum over the H / Hk heads that share one, of
 // fp32 [B, H, T, dk] partial gradients.  own (or null): fp32 [B, H, T], scale

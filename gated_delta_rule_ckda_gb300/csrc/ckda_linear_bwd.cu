@@ -1,0 +1,783 @@
+// ckda_linear_bwd.cu -- chunked backward of linear attention with a scalar decay
+// per head on the tensor cores (bf16 I/O, widths up to 128).
+//
+// With the forward's notation (chunks of 128 tokens, H the state entering a
+// chunk, L the cumulative log decay inside it) and G = dL/dH at the chunk's end:
+//     dQ = s e^{L_i} (dO H^T) + dS K,       dS_ij = s e^{L_i - L_j} (do_i.v_j)
+//     dK = e^{L_C - L_j} (V G^T) + dS^T Q
+//     dV = e^{L_C - L_j} (K G) + P^T dO,    P_ij  = s e^{L_i - L_j} (q_i.k_j)
+//     G <- e^{L_C} G + sum_i s e^{L_i} q_i do_i^T      (to the chunk before)
+//     dg_t = e^{L_C} <H, G> + sum_{j<t} e^{L_C-L_j} k_j.(G v_j)
+//            + sum_{i>=t} [ s e^{L_i} q_i.(H do_i) + sum_{j<i} W_ij - sum_{l>i} W_li ],
+//     W_ij = s e^{L_i - L_j} (q_i.k_j)(do_i.v_j)
+// (s the query scale).  dg has no term that is larger than what it counts: a
+// token's own product W_ii, which no decay touches, is not in it, and pairs on
+// the same side of t cancel inside one chunk only.
+//
+// Three launches:
+//   1. linear_state_kernel, forward in time: H entering every chunk;
+//   2. the same kernel, backward in time over (q, do): G at every chunk's end;
+//   3. linear_grad_kernel: a chunk to a CTA, all gradients.
+// The states pass through HBM in two bf16 parts (hi + lo, 64 KiB a chunk and
+// direction): dg and dh0 are fp32 and need more than one bf16 rounding.
+#include "ckda_linear_chunk.cuh"
+
+namespace ckda {
+namespace {
+using namespace chunk;
+
+constexpr uint32_t kImage = 2 * kTile;  // a state: hi tile, lo tile, [dv][dk], swizzled
+
+struct BwdWs {
+  char* himg;           // [slots * H] images of H
+  char* gimg;           // of G
+  float* dg;            // [B, H, T] (a decay per head only)
+  float* dq;            // [B, H, T, dk] (shared key heads only)
+  float* dk;
+  int32_t* first;       // [N + 1] first chunk of each sequence (packed only)
+  int chunks;           // slots of a head: chunks, or a bound on them
+};
+
+// Chunks of the packed sequences before each.
+__global__ void __launch_bounds__(1024) chunk_plan_kernel(LinearArgs a, int32_t* first) {
+  __shared__ int32_t sum[1024];
+  const int per = (a.N + 1023) / 1024, i0 = threadIdx.x * per, i1 = min(i0 + per, a.N);
+  int32_t s = 0;
+  for (int i = i0; i < i1; ++i) {
+    int t0, len;
+    seq_range(a, i, t0, len);
+    s += (len + C - 1) / C;
+  }
+  sum[threadIdx.x] = s;
+  __syncthreads();
+  int32_t before = 0;
+  for (int j = 0; j < (int)threadIdx.x; ++j) before += sum[j];
+  for (int i = i0; i < i1; ++i) {
+    first[i] = before;
+    int t0, len;
+    seq_range(a, i, t0, len);
+    before += (len + C - 1) / C;
+  }
+  if (threadIdx.x == 1023) first[a.N] = before;
+}
+
+// ----------------------------------------------------------- states of chunks
+// One CTA of 512 threads walks the chunks of one (sequence, head), forward over
+// (k, v) from h0 or backward over (q, do) from dhT, writes the state met at
+// each chunk and, backward, dh0.  Bound by HBM: two tiles in and an image out,
+// 128 KiB a chunk.
+//   warp 0 loads, warp 1 issues the products, warp 2 makes the decays,
+//   warps 4-7 scale a chunk's keys (queries) in two bf16 parts,
+//   warps 8-15 hold the state: thread (r, s) has its channels 64 s .. + 63 of
+//   value column r in fp32 registers.
+namespace st {
+constexpr int kThreads = 512;
+constexpr int kSlots = 4;                       // x and y tiles of two chunks
+constexpr uint32_t kLo = kSlots * kTile;        // two lo tiles
+constexpr uint32_t kGates = kLo + 2 * kTile;    // two
+constexpr uint32_t kBars = kGates + 2 * sizeof(Gates);
+constexpr uint32_t kSmem = kBars + 512;
+enum { B_FULL = 0, B_EMPTY = 4, B_KT = 8, B_DF = 10, B_DFREE = 12, B_G = 14, B_GFREE = 16,
+       B_END = 18, B_COUNT };
+}  // namespace st
+
+template <bool BACK>
+__global__ void __launch_bounds__(st::kThreads, 1)
+linear_state_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ BwdWs w,
+                    const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap my) {
+  using namespace st;
+  extern __shared__ __align__(1024) char sm[];
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kBars);
+  Gates* gates = reinterpret_cast<Gates*>(sm + kGates);
+  volatile int* abort = reinterpret_cast<volatile int*>(sm + kBars + 400);
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(sm + kBars + 404);
+  const uint32_t sb = smem_u32(sm);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (sb & 1023u) {
+    if (tid == 0) set_status(a.status, CKDA_ERR_CUDA);
+    return;
+  }
+  const int order = blockIdx.x / a.H, h = blockIdx.x % a.H;
+  const int n = a.order ? a.order[order] : order;
+  const int b = a.cu_seqlens ? 0 : n, hk = h / (a.H / a.Hk);
+  int t0, len;
+  seq_range(a, n, t0, len);
+  const int chunks = (len + C - 1) / C;
+  const int xz = b * a.Hk + hk, yz = b * a.H + h;
+  const size_t vrow = (size_t)yz * a.T + t0;
+  const size_t state = ((size_t)n * a.H + h) * (size_t)a.dk * a.dv;
+  const size_t first = w.first ? (size_t)w.first[n] : (size_t)n * chunks;
+  auto at = [&](int i) { return BACK ? chunks - 1 - i : i; };  // chunk of step i
+  // forward, no chunk is entered by what the last one leaves
+  const int steps = BACK ? chunks : chunks - 1;
+
+  if (tid == 0) {
+    for (int i = 0; i < B_COUNT; ++i)
+      mbar_init(bars + i, i >= B_KT && i < B_KT + 2         ? 4
+                          : i >= B_DFREE && i < B_DFREE + 2 ? 8
+                          : i >= B_GFREE && i < B_GFREE + 2 ? 12
+                                                            : 1);
+    *abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 3) {
+    tmem_alloc(tmem_at, 256);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_at;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      for (int i = 0; i < 2 * steps; ++i) {
+        const int slot = i % kSlots, use = i / kSlots;
+        if (use > 0 && !mbar_wait(bars + B_EMPTY + slot, (use - 1) & 1)) { *abort = 1; break; }
+        if (*abort) break;
+        load_tile(sb + slot * kTile, i & 1 ? &my : &mx, bars + B_FULL + slot, t0 + at(i / 2) * C,
+                  i & 1 ? yz : xz);
+      }
+    }
+  } else if (warp == 1) {
+    for (int i = 0; i < steps; ++i) {
+      const int ix = (2 * i) % kSlots, iy = ix + 1, p = i & 1;
+      if (!warp_wait(bars + B_FULL + iy, (i / 2) & 1, abort)) break;
+      if (!warp_wait(bars + B_KT + p, (i / 2) & 1, abort)) break;
+      if (i >= 2 && !warp_wait(bars + B_DFREE + p, (i / 2 - 1) & 1, abort)) break;
+      tc_fence_after();
+      if (lane == 0) {
+        mma_ss(tmem + 128 * p, sb + iy * kTile, true, sb + ix * kTile, true, false);
+        mma_ss(tmem + 128 * p, sb + iy * kTile, true, sb + kLo + p * kTile, true, true);
+        umma_commit(bars + B_DF + p);
+        umma_commit(bars + B_EMPTY + ix);
+        umma_commit(bars + B_EMPTY + iy);
+      }
+    }
+    if (lane == 0) umma_commit(bars + B_END);
+  } else if (warp == 2) {
+    const float* g = a.g_head ? a.g + h : a.g + vrow;
+    const int gs = a.g_head ? 0 : 1;
+    for (int i = 0; i < steps; ++i) {
+      const int p = i & 1, c = at(i);
+      const float4 x = load_decays(g + (size_t)c * C * gs, gs, min(len - c * C, C), lane);
+      if (i >= 2 && !warp_wait(bars + B_GFREE + p, (i / 2 - 1) & 1, abort)) break;
+      make_gates(gates + p, x, lane);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + B_G + p);
+    }
+  } else if (warp >= 4 && warp < 8) {
+    const int t = tid - 128;
+    for (int i = 0; i < steps; ++i) {
+      const int ix = (2 * i) % kSlots, p = i & 1, valid = min(len - at(i) * C, C);
+      const uint32_t par = (i / 2) & 1;
+      if (!warp_wait(bars + B_G + p, par, abort)) break;
+      const float wt = BACK ? a.scale * gates[p].eL[t] : gates[p].w[t];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + B_GFREE + p);
+      if (i >= 2 && !warp_wait(bars + B_DF + p, (i / 2 - 1) & 1, abort)) break;  // lo is free
+      if (!warp_wait(bars + B_FULL + ix, par, abort)) break;
+      scale_row(sm + ix * kTile, sm + kLo + p * kTile, t, 0, wt, t < valid);
+      scale_row(sm + ix * kTile, sm + kLo + p * kTile, t, 1, wt, t < valid);
+      if (a.cu_seqlens && valid < C) {  // tokens of the next sequence behind this one
+        if (!warp_wait(bars + B_FULL + ix + 1, par, abort)) break;
+        if (t >= valid) zero_row(sm + (ix + 1) * kTile, t);
+      }
+      warp_publish(bars + B_KT + p);
+    }
+  } else if (warp >= 8) {
+    const int s = (warp - 8) >> 2, r = (tid - 256) & 127;
+    const uint32_t lanes = tmem + ((uint32_t)(r & 96) << 16);
+    const float* init = BACK ? a.dhT : a.h0;
+    char* img = BACK ? w.gimg : w.himg;
+    float S[64];
+#pragma unroll
+    for (int i = 0; i < 64; ++i) {
+      const int d = 64 * s + i;
+      S[i] = init && r < a.dv && d < a.dk ? init[state + (size_t)d * a.dv + r] : 0.f;
+    }
+    bool ok = true;
+    for (int i = 0; i < chunks; ++i) {
+      const int p = i & 1, c = at(i);
+      const uint32_t par = (i / 2) & 1;
+      // (offsets that are no packing would run past the workspace)
+      const size_t slot = min(first + c, (size_t)w.chunks - 1) * a.H + h;
+      char* out = img + slot * kImage;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x = S[8 * j + 2 * e], y = S[8 * j + 2 * e + 1];
+          hi[e] = pack_bf162(x, y);
+          lo[e] = pack_bf162(x - __uint_as_float(hi[e] << 16),
+                             y - __uint_as_float(hi[e] & 0xffff0000u));
+        }
+        const uint32_t off = sw128_chunk(128, r, 8 * s + j);
+        *reinterpret_cast<uint4*>(out + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(out + kTile + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+      if (i >= steps) break;
+      if (!(ok = warp_wait(bars + B_G + p, par, abort))) break;
+      const float all = gates[p].all;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + B_GFREE + p);
+      if (!(ok = warp_wait(bars + B_DF + p, par, abort))) break;
+      tc_fence_after();
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t x[32];
+        tmem_ld32<32>(lanes + 128 * p + 64 * s + 32 * q, x);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          S[32 * q + e] = fmaf(all, S[32 * q + e], __uint_as_float(x[e]));
+      }
+      warp_arrive(bars + B_DFREE + p);
+    }
+    if (BACK && ok && a.dh0 && r < a.dv) {
+#pragma unroll
+      for (int i = 0; i < 64; ++i) {
+        const int d = 64 * s + i;
+        if (d < a.dk) a.dh0[state + (size_t)d * a.dv + r] = S[i];
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0) {
+    if (!mbar_wait(bars + B_END, 0)) *abort = 1;
+    if (*abort) {
+      set_status(a.status, CKDA_ERR_TIMEOUT);
+      for (int i = 0; i < kSlots; ++i) mbar_wait(bars + B_FULL + i, 0, 1u << 12, 1000u);
+    }
+  }
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 3) tmem_dealloc(tmem, 256);
+}
+
+// ------------------------------------------------------ gradients of a chunk
+// A CTA of 512 threads takes one chunk of one (sequence, head).  Products, each
+// 128 x 128 x 128: S, dP and their transposes (so that both dS and dS^T, P^T
+// are rows of a thread and go back to TMEM as operands), dO H^T, V G^T and K G
+// in two parts each, dS K, dS^T Q, P^T dO.
+//   warp 0 loads, warp 1 issues the products, warp 2 makes the decays
+//   warps 4-7   A: thread = query row.  dS and the row sums of W; dQ; then dV
+//   warps 8-11  B: thread = key row.  P^T, dS^T and the column sums of W; dK
+//   warps 12-15 C: <H, G>, from the images in L2
+// An accumulator takes the state's part first; its thread scales that row in
+// place and the product inside the chunk is added to it.  A token's own product
+// (W_ii's factors, the largest under strong decay) stays out of the bf16 operands
+// and is added there in fp32.
+namespace gr {
+constexpr int kThreads = 512;
+constexpr uint32_t kQ = 0, kK = kTile, kV = 2 * kTile, kDo = 3 * kTile;
+constexpr uint32_t kS0 = 4 * kTile, kS1 = 5 * kTile, kS2 = 6 * kTile;  // Hhi then Glo, Hlo, Ghi
+constexpr uint32_t kGates = 7 * kTile;
+constexpr uint32_t kBars = kGates + sizeof(Gates);
+constexpr uint32_t kSmem = kBars + 512;
+static_assert(kSmem <= 232448, "shared memory of a CTA");
+enum { B_QK, B_VD, B_H, B_GH, B_GL, B_G, B_TAIL, B_A, B_B, B_DSA, B_DSB, B_X1, B_X2, B_X1S, B_X2S,
+       B_DQ, B_DK, B_DQR, B_X3, B_X3S, B_DV, B_COUNT };
+// TMEM columns: S, dP, S^T, dP^T; then dS over S, dS^T behind it, X1 over dP,
+// P^T over S^T, X2 over dP^T
+constexpr uint32_t T_S = 0, T_DP = 128, T_ST = 256, T_DPT = 384;
+constexpr uint32_t T_DS = 0, T_DST = 64, T_X1 = 128, T_PT = 256, T_X2 = 384;
+}  // namespace gr
+
+__device__ __forceinline__ void load_image(uint32_t dst, const char* src, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(src), "r"(kTile), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Scales an accumulator's row in place, adds a multiple of the same row of a
+// bf16 tile, and (DOT) returns the scaled row's dot product with that of another.
+template <bool DOT>
+__device__ __forceinline__ float scale_acc(uint32_t acc, float f, float m, const char* add,
+                                           const char* tile, int row) {
+  float dot = 0.f;
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    uint32_t x[32];
+    tmem_ld32<32>(acc + 32 * p, x);
+    tmem_ld_wait();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t off = sw128_chunk(128, row, 4 * p + j);
+      const uint4 u = *reinterpret_cast<const uint4*>(add + off);
+      const uint32_t t[4] = {u.x, u.y, u.z, u.w};
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (DOT) v = *reinterpret_cast<const uint4*>(tile + off);
+      const uint32_t y[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float a = f * __uint_as_float(x[8 * j + 2 * e]);
+        const float b = f * __uint_as_float(x[8 * j + 2 * e + 1]);
+        if (DOT) {
+          dot = fmaf(a, __uint_as_float(y[e] << 16), dot);
+          dot = fmaf(b, __uint_as_float(y[e] & 0xffff0000u), dot);
+        }
+        x[8 * j + 2 * e] = __float_as_uint(fmaf(m, __uint_as_float(t[e] << 16), a));
+        x[8 * j + 2 * e + 1] = __float_as_uint(fmaf(m, __uint_as_float(t[e] & 0xffff0000u), b));
+      }
+    }
+    tmem_st32<32>(acc + 32 * p, x);
+  }
+  tmem_st_wait();
+  return dot;
+}
+
+// A row of an accumulator to memory: bf16, or fp32 partial gradients.
+__device__ __forceinline__ void store_acc(uint32_t acc, __nv_bfloat16* row, float* part, int width,
+                                          bool keep) {
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    if (32 * p >= width) break;
+    uint32_t x[32];
+    tmem_ld32<32>(acc + 32 * p, x);
+    tmem_ld_wait();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (!keep || 32 * p + 8 * j >= width) break;
+      if (part) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          *reinterpret_cast<uint4*>(part + 32 * p + 8 * j + 4 * e) =
+              make_uint4(x[8 * j + 4 * e], x[8 * j + 4 * e + 1], x[8 * j + 4 * e + 2],
+                         x[8 * j + 4 * e + 3]);
+      } else {
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          o[e] = pack_bf162(__uint_as_float(x[8 * j + 2 * e]),
+                            __uint_as_float(x[8 * j + 2 * e + 1]));
+        *reinterpret_cast<uint4*>(row + 32 * p + 8 * j) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(gr::kThreads, 1)
+linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ BwdWs w,
+                   const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                   const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo) {
+  using namespace gr;
+  extern __shared__ __align__(1024) char sm[];
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kBars);
+  Gates* gates = reinterpret_cast<Gates*>(sm + kGates);
+  volatile int* abort = reinterpret_cast<volatile int*>(sm + kBars + 400);
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(sm + kBars + 404);
+  float* hg = reinterpret_cast<float*>(sm + kBars + 408);  // <H, G> by warp of C
+  const uint32_t sb = smem_u32(sm);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (sb & 1023u) {
+    if (tid == 0) set_status(a.status, CKDA_ERR_CUDA);
+    return;
+  }
+  const int ci = blockIdx.x / a.H, h = blockIdx.x % a.H;
+  int n, c;
+  if (w.first) {
+    if (ci >= w.first[a.N]) return;  // the grid is a bound
+    int lo = 0, hi = a.N;            // first[lo] <= ci < first[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (w.first[mid] <= ci) lo = mid; else hi = mid;
+    }
+    n = lo;
+    c = ci - w.first[n];
+  } else {
+    const int per = (a.T + C - 1) / C;
+    n = ci / per;
+    c = ci % per;
+  }
+  const int b = a.cu_seqlens ? 0 : n, hk = h / (a.H / a.Hk);
+  int t0, len;
+  seq_range(a, n, t0, len);
+  const int valid = min(len - c * C, C);
+  if (valid <= 0) return;
+  const int y = t0 + c * C, qz = b * a.Hk + hk, vz = b * a.H + h;
+  const size_t vrow = (size_t)vz * a.T + y;
+  const size_t krow = (size_t)qz * a.T + y;
+  const char* himg = w.himg + ((size_t)ci * a.H + h) * kImage;
+  const char* gimg = w.gimg + ((size_t)ci * a.H + h) * kImage;
+  const bool tail = a.cu_seqlens && valid < C;
+
+  if (tid == 0) {
+    for (int i = 0; i < B_COUNT; ++i)
+      mbar_init(bars + i, i == B_TAIL ? 12
+                          : i == B_DSA || i == B_DSB || i == B_X1S || i == B_X2S || i == B_DQR ||
+                                  i == B_X3S
+                              ? 4
+                              : 1);
+    *abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 3) {
+    tmem_alloc(tmem_at, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_at;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(bars + B_QK, 2 * kTile);
+      for (int p = 0; p < 2; ++p) {
+        tma_load_3d(sb + kQ + p * kPanel, &mq, bars + B_QK, 64 * p, y, qz);
+        tma_load_3d(sb + kK + p * kPanel, &mk, bars + B_QK, 64 * p, y, qz);
+      }
+      mbar_arrive_expect_tx(bars + B_VD, 2 * kTile);
+      for (int p = 0; p < 2; ++p) {
+        tma_load_3d(sb + kV + p * kPanel, &mv, bars + B_VD, 64 * p, y, vz);
+        tma_load_3d(sb + kDo + p * kPanel, &mo, bars + B_VD, 64 * p, y, vz);
+      }
+      mbar_arrive_expect_tx(bars + B_H, 2 * kTile);
+      load_image(sb + kS0, himg, bars + B_H);
+      load_image(sb + kS1, himg + kTile, bars + B_H);
+      mbar_arrive_expect_tx(bars + B_GH, kTile);
+      load_image(sb + kS2, gimg, bars + B_GH);
+      if (mbar_wait(bars + B_X1, 0)) {  // dO H^T is done with Hhi
+        mbar_arrive_expect_tx(bars + B_GL, kTile);
+        load_image(sb + kS0, gimg + kTile, bars + B_GL);
+      } else {
+        *abort = 1;
+      }
+    }
+  } else if (warp == 1) {
+    do {
+      if (!warp_wait(bars + B_QK, 0, abort)) break;
+      if (!warp_wait(bars + B_VD, 0, abort)) break;
+      if (tail && !warp_wait(bars + B_TAIL, 0, abort)) break;
+      tc_fence_after();
+      if (lane == 0) {
+        mma_ss(tmem + T_S, sb + kQ, false, sb + kK, false, false);
+        mma_ss(tmem + T_DP, sb + kDo, false, sb + kV, false, false);
+        umma_commit(bars + B_A);
+        mma_ss(tmem + T_ST, sb + kK, false, sb + kQ, false, false);
+        mma_ss(tmem + T_DPT, sb + kV, false, sb + kDo, false, false);
+        umma_commit(bars + B_B);
+      }
+      if (!warp_wait(bars + B_H, 0, abort)) break;
+      if (!warp_wait(bars + B_DSA, 0, abort)) break;
+      tc_fence_after();
+      if (lane == 0) {
+        mma_ss(tmem + T_X1, sb + kDo, false, sb + kS0, true, false);
+        mma_ss(tmem + T_X1, sb + kDo, false, sb + kS1, true, true);
+        umma_commit(bars + B_X1);
+      }
+      if (!warp_wait(bars + B_GH, 0, abort)) break;
+      if (!warp_wait(bars + B_DSB, 0, abort)) break;
+      tc_fence_after();
+      if (lane == 0) mma_ss(tmem + T_X2, sb + kV, false, sb + kS2, true, false);
+      if (!warp_wait(bars + B_GL, 0, abort)) break;
+      if (lane == 0) {
+        mma_ss(tmem + T_X2, sb + kV, false, sb + kS0, true, true);
+        umma_commit(bars + B_X2);
+      }
+      if (!warp_wait(bars + B_X1S, 0, abort)) break;
+      tc_fence_after();
+      if (lane == 0) {
+        mma_ts(tmem + T_X1, tmem + T_DS, sb + kK, true, true);
+        umma_commit(bars + B_DQ);
+      }
+      if (!warp_wait(bars + B_X2S, 0, abort)) break;
+      tc_fence_after();
+      if (lane == 0) {
+        mma_ts(tmem + T_X2, tmem + T_DST, sb + kQ, true, true);
+        umma_commit(bars + B_DK);
+      }
+      if (!warp_wait(bars + B_DQR, 0, abort)) break;
+      tc_fence_after();
+      if (lane == 0) {
+        mma_ss(tmem + T_X1, sb + kK, false, sb + kS2, false, false);
+        mma_ss(tmem + T_X1, sb + kK, false, sb + kS0, false, true);
+        umma_commit(bars + B_X3);
+      }
+      if (!warp_wait(bars + B_X3S, 0, abort)) break;
+      tc_fence_after();
+      if (lane == 0) {
+        mma_ts(tmem + T_X1, tmem + T_PT, sb + kDo, true, true);
+        umma_commit(bars + B_DV);
+      }
+    } while (false);
+  } else if (warp == 2) {
+    const float* g = a.g_head ? a.g + h : a.g + vrow;
+    make_gates(gates, load_decays(g, a.g_head ? 0 : 1, valid, lane), lane);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars + B_G);
+  } else if (warp >= 4) {
+    const int wg = (warp - 4) >> 2, wq = warp & 3, row = tid & 127;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * wq) << 16);
+    const bool in = row < valid;
+    do {
+      if (tail) {  // tokens of the next sequence behind this one: out of every sum over tokens
+        if (!warp_wait(bars + (wg == 2 ? B_VD : B_QK), 0, abort)) break;
+        if (!in) zero_row(sm + (wg == 0 ? kQ : wg == 1 ? kK : kDo), row);
+        warp_publish(bars + B_TAIL);
+      }
+      if (wg == 2) {
+        // <H, G> from both parts of both images
+        float s = 0.f;
+        for (int i = row; i < (int)kTile / 16; i += 128) {
+          const uint4 v[4] = {reinterpret_cast<const uint4*>(himg)[i],
+                              reinterpret_cast<const uint4*>(himg + kTile)[i],
+                              reinterpret_cast<const uint4*>(gimg)[i],
+                              reinterpret_cast<const uint4*>(gimg + kTile)[i]};
+          const uint32_t* t = reinterpret_cast<const uint32_t*>(v);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float x0 = __uint_as_float(t[e] << 16) + __uint_as_float(t[4 + e] << 16);
+            const float y0 = __uint_as_float(t[8 + e] << 16) + __uint_as_float(t[12 + e] << 16);
+            const float x1 = __uint_as_float(t[e] & 0xffff0000u) +
+                             __uint_as_float(t[4 + e] & 0xffff0000u);
+            const float y1 = __uint_as_float(t[8 + e] & 0xffff0000u) +
+                             __uint_as_float(t[12 + e] & 0xffff0000u);
+            s = fmaf(x0, y0, s);
+            s = fmaf(x1, y1, s);
+          }
+        }
+#pragma unroll
+        for (int m = 16; m >= 1; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+        if (lane == 0) hg[wq] = s;
+        break;
+      }
+      if (!warp_wait(bars + B_G, 0, abort)) break;
+      const float pre = gates->pre[row], es = gates->es[row];
+      const float into = a.scale * gates->eL[row], out = gates->w[row], s = a.scale;
+      float wsum = 0.f, dot = 0.f, own = 0.f, own_p = 0.f;  // s do_i.v_i, s q_i.k_i
+      if (wg == 0) {
+        // row i: j over blocks up to its own
+        if (!warp_wait(bars + B_A, 0, abort)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          uint32_t o[16];
+          if (p > wq) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = 0;
+          } else {
+            uint32_t x[32], d[32];
+            tmem_ld32<32>(lanes + T_S + 32 * p, x);
+            tmem_ld32<32>(lanes + T_DP + 32 * p, d);
+            float f = pre;
+#pragma unroll
+            for (int m = 1; m < 3; ++m)
+              if (m > p && m < wq) f += gates->tot[m];
+            f = s * exp2f(f);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float v[2];
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                const int j = 2 * e + z;
+                const float dp = __uint_as_float(d[j]);
+                if (p == wq) {
+                  v[z] = j < lane ? dp * (s * exp2f(pre - gates->pre[32 * p + j])) : 0.f;
+                  if (j < lane) wsum = fmaf(v[z], __uint_as_float(x[j]), wsum);
+                  if (j == lane) {
+                    own = s * dp;
+                    own_p = s * __uint_as_float(x[j]);
+                  }
+                } else {
+                  v[z] = dp * (f * gates->es[32 * p + j]);
+                  wsum = fmaf(v[z], __uint_as_float(x[j]), wsum);
+                }
+              }
+              o[e] = pack_bf162(v[0], v[1]);
+            }
+          }
+          tmem_st32<16>(lanes + T_DS + 16 * p, o);
+        }
+        tmem_st_wait();
+        warp_arrive(bars + B_DSA);
+        if (!warp_wait(bars + B_X1, 0, abort)) break;
+        tc_fence_after();
+        dot = scale_acc<true>(lanes + T_X1, into, own, sm + kK, sm + kQ, row);
+        warp_arrive(bars + B_X1S);
+        if (!warp_wait(bars + B_DQ, 0, abort)) break;
+        tc_fence_after();
+        store_acc(lanes + T_X1, static_cast<__nv_bfloat16*>(a.dq) + (krow + row) * a.dk,
+                  w.dq ? w.dq + (vrow + row) * a.dk : nullptr, a.dk, in);
+        warp_arrive(bars + B_DQR);
+        if (!warp_wait(bars + B_X3, 0, abort)) break;
+        tc_fence_after();
+        scale_acc<false>(lanes + T_X1, out, own_p, sm + kDo, nullptr, row);
+        warp_arrive(bars + B_X3S);
+        if (!warp_wait(bars + B_DV, 0, abort)) break;
+        tc_fence_after();
+        store_acc(lanes + T_X1, static_cast<__nv_bfloat16*>(a.dval) + (vrow + row) * a.dv, nullptr,
+                  a.dv, in);
+      } else {
+        // row j: i over blocks from its own on
+        if (!warp_wait(bars + B_B, 0, abort)) break;
+        if (!warp_wait(bars + B_DSA, 0, abort)) break;  // dS^T goes behind dS
+        tc_fence_after();
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          uint32_t o[16], q[16];
+          if (p < wq) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = q[e] = 0;
+          } else {
+            uint32_t x[32], d[32];
+            tmem_ld32<32>(lanes + T_ST + 32 * p, x);
+            tmem_ld32<32>(lanes + T_DPT + 32 * p, d);
+            float f = 0.f;
+#pragma unroll
+            for (int m = 1; m < 3; ++m)
+              if (m > wq && m < p) f += gates->tot[m];
+            f = s * es * exp2f(f);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float u[2], v[2];
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                const int i = 2 * e + z;
+                const float pi = gates->pre[32 * p + i];
+                const bool on = p != wq || i > lane;
+                const float k = p == wq ? (on ? s * exp2f(pi - pre) : 0.f) : f * exp2f(pi);
+                u[z] = on ? __uint_as_float(x[i]) * k : 0.f;
+                v[z] = on ? __uint_as_float(d[i]) * k : 0.f;
+                if (on) wsum = fmaf(v[z], __uint_as_float(x[i]), wsum);
+                if (p == wq && i == lane) own = s * __uint_as_float(d[i]);
+              }
+              o[e] = pack_bf162(u[0], u[1]);
+              q[e] = pack_bf162(v[0], v[1]);
+            }
+          }
+          tmem_st32<16>(lanes + T_PT + 16 * p, o);
+          tmem_st32<16>(lanes + T_DST + 16 * p, q);
+        }
+        tmem_st_wait();
+        warp_arrive(bars + B_DSB);
+        if (!warp_wait(bars + B_X2, 0, abort)) break;
+        tc_fence_after();
+        dot = scale_acc<true>(lanes + T_X2, out, own, sm + kQ, sm + kK, row);
+        warp_arrive(bars + B_X2S);
+        if (!warp_wait(bars + B_DK, 0, abort)) break;
+        tc_fence_after();
+        store_acc(lanes + T_X2, static_cast<__nv_bfloat16*>(a.dkey) + (krow + row) * a.dk,
+                  w.dk ? w.dk + (vrow + row) * a.dk : nullptr, a.dk, in);
+      }
+      // dg's sums: by token in shared memory, over the tile of Hlo
+      float* part = reinterpret_cast<float*>(sm + kS1) + 256 * wg;
+      part[row] = in ? wsum : 0.f;
+      part[128 + row] = in ? dot : 0.f;
+    } while (false);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp >= 4 && warp < 8 && !*abort) {
+    // dg_t = e^{L_C} <H, G> + sum_{j<t} kd_j + sum_{i>=t} (qd_i + row_i - col_i)
+    const float* part = reinterpret_cast<const float*>(sm + kS1);
+    float* run = reinterpret_cast<float*>(sm + kS1) + 512;
+    const int t = tid & 127, wq = warp & 3;
+    float fwd = part[384 + t], back = part[128 + t] + part[t] - part[256 + t];
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const float x = __shfl_up_sync(0xffffffffu, fwd, m), z = __shfl_down_sync(0xffffffffu, back, m);
+      if (lane >= m) fwd += x;
+      if (lane + m < 32) back += z;
+    }
+    float excl = __shfl_up_sync(0xffffffffu, fwd, 1);
+    if (lane == 0) excl = 0.f;
+    if (lane == 31) run[wq] = fwd;
+    if (lane == 0) run[4 + wq] = back;
+    named_sync(1, 128);
+    float r = gates->all * (hg[0] + hg[1] + hg[2] + hg[3]) + excl + back;
+    for (int i = 0; i < wq; ++i) r += run[i];
+    for (int i = wq + 1; i < 4; ++i) r += run[4 + i];
+    if (t < valid) (w.dg ? w.dg : a.dg)[vrow + t] = r;
+  }
+  if (tid == 0 && *abort) {
+    // let copies and products in flight land before the memory is given back
+    set_status(a.status, CKDA_ERR_TIMEOUT);
+    const int land[] = {B_QK, B_VD, B_H, B_GH, B_GL, B_B, B_X1, B_X2, B_DQ, B_DK, B_X3, B_DV};
+    for (int i : land) mbar_wait(bars + i, 0, 1u << 12, 1000u);
+  }
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 3) tmem_dealloc(tmem, 512);
+}
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+struct ChunkPlan {
+  size_t chunks, himg, gimg, dg, dq, dk, first, total;
+};
+ChunkPlan chunk_plan(int N, int B, int H, int Hk, int T, int dk, bool packed) {
+  ChunkPlan p;
+  // packed: ceil(len / 128) over sequences that add up to T
+  p.chunks = packed ? (size_t)T / C + N : (size_t)N * ((T + C - 1) / C);
+  const size_t rows = (size_t)B * H * T;
+  size_t at = 0;
+  p.himg = at; at += p.chunks * H * kImage;
+  p.gimg = at; at += p.chunks * H * kImage;
+  p.dg = at; at += up256(rows * 4);
+  p.dq = at; at += Hk == H ? 0 : up256(rows * dk * 4);
+  p.dk = at; at += Hk == H ? 0 : up256(rows * dk * 4);
+  p.first = at; at += up256(((size_t)N + 1) * 4);
+  p.total = at;
+  return p;
+}
+
+}  // namespace
+
+size_t linear_chunk_bwd_bytes(int N, int B, int H, int Hk, int T, int dk, bool packed) {
+  return chunk_plan(N, B, H, Hk, T, dk, packed).total;
+}
+
+cudaError_t linear_chunk_bwd(const LinearArgs& a, char* ws, cudaStream_t s) {
+  const ChunkPlan p = chunk_plan(a.N, a.B, a.H, a.Hk, a.T, a.dk, a.cu_seqlens != nullptr);
+  BwdWs w{};
+  w.himg = ws + p.himg;
+  w.gimg = ws + p.gimg;
+  w.dg = a.g_head ? reinterpret_cast<float*>(ws + p.dg) : nullptr;
+  w.dq = a.Hk == a.H ? nullptr : reinterpret_cast<float*>(ws + p.dq);
+  w.dk = a.Hk == a.H ? nullptr : reinterpret_cast<float*>(ws + p.dk);
+  w.chunks = (int)p.chunks;
+  cudaError_t e = cudaSuccess;
+  CUtensorMap mq{}, mk{}, mv{}, mo{};
+  if (a.T > 0 && (!linear_map(&mq, a.q, (uint64_t)a.B * a.Hk, a.T, a.dk) ||
+                  !linear_map(&mk, a.k, (uint64_t)a.B * a.Hk, a.T, a.dk) ||
+                  !linear_map(&mv, a.v, (uint64_t)a.B * a.H, a.T, a.dv) ||
+                  !linear_map(&mo, a.dout, (uint64_t)a.B * a.H, a.T, a.dv)))
+    return cudaErrorInvalidValue;
+  if (a.cu_seqlens) {
+    w.first = reinterpret_cast<int32_t*>(ws + p.first);
+    chunk_plan_kernel<<<1, 1024, 0, s>>>(a, w.first);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  const struct { const void* f; uint32_t bytes; } kernels[] = {
+      {(const void*)linear_state_kernel<false>, st::kSmem},
+      {(const void*)linear_state_kernel<true>, st::kSmem},
+      {(const void*)linear_grad_kernel, gr::kSmem}};
+  for (const auto& k : kernels)
+    if ((e = cudaFuncSetAttribute(k.f, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  (int)k.bytes)) != cudaSuccess)
+      return e;
+  const unsigned units = (unsigned)a.N * a.H;
+  linear_state_kernel<false><<<units, st::kThreads, st::kSmem, s>>>(a, w, mk, mv);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  linear_state_kernel<true><<<units, st::kThreads, st::kSmem, s>>>(a, w, mq, mo);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (a.T > 0) {
+    linear_grad_kernel<<<(unsigned)(p.chunks * a.H), gr::kThreads, gr::kSmem, s>>>(a, w, mq, mk, mv,
+                                                                                 mo);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (w.dq && (e = linear_sum_heads(a, w.dq, w.dk, nullptr, s)) != cudaSuccess) return e;
+  }
+  return a.g_head ? linear_sum_decay(a, w.dg, s) : e;
+}
+
+}  // namespace ckda

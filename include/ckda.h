@@ -513,8 +513,8 @@ ckda_status ckda_linear_fwd(const void *q, const void *k, const void *v, const f
  * The forward's states are recomputed.  No atomics: the same inputs give the
  * same bits.  workspace as above, of ckda_linear_bwd_workspace_bytes bytes.
  */
-size_t ckda_linear_bwd_workspace_bytes(int num_seqs, int B, int H, int T, int dk, int dv,
-                                       ckda_dtype io_dtype);
+size_t ckda_linear_bwd_workspace_bytes(int num_seqs, int B, int H, int Hk, int T, int dk,
+                                       int dv, ckda_dtype io_dtype);
 ckda_status ckda_linear_bwd(const void *q, const void *k, const void *v, const float *g,
                             int g_per_head, const float *h0, const void *dout,
                             const float *dhT, void *dq, void *dkey, void *dval, float *dg,
