@@ -296,12 +296,11 @@ __device__ __forceinline__ void load_image(uint32_t dst, const char* src, uint64
 }
 
 // Scales an accumulator's row in place, adds a multiple of the same row of a
-// bf16 tile, and (DOT) returns the scaled row's dot product with that of another.
-template <bool DOT>
-__device__ __forceinline__ float scale_acc(uint32_t acc, float f, float m, const char* add,
-                                           const char* tile, int row) {
+// bf16 tile, and returns the scaled row's dot product with that of another.
+static __device__ __noinline__ float scale_acc(uint32_t acc, float f, float m, const char* add,
+                                               const char* tile, int row) {
   float dot = 0.f;
-#pragma unroll
+#pragma unroll 1
   for (int p = 0; p < 4; ++p) {
     uint32_t x[32];
     tmem_ld32<32>(acc + 32 * p, x);
@@ -310,18 +309,14 @@ __device__ __forceinline__ float scale_acc(uint32_t acc, float f, float m, const
     for (int j = 0; j < 4; ++j) {
       const uint32_t off = sw128_chunk(128, row, 4 * p + j);
       const uint4 u = *reinterpret_cast<const uint4*>(add + off);
-      const uint32_t t[4] = {u.x, u.y, u.z, u.w};
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (DOT) v = *reinterpret_cast<const uint4*>(tile + off);
-      const uint32_t y[4] = {v.x, v.y, v.z, v.w};
+      const uint4 v = *reinterpret_cast<const uint4*>(tile + off);
+      const uint32_t t[4] = {u.x, u.y, u.z, u.w}, y[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float a = f * __uint_as_float(x[8 * j + 2 * e]);
         const float b = f * __uint_as_float(x[8 * j + 2 * e + 1]);
-        if (DOT) {
-          dot = fmaf(a, __uint_as_float(y[e] << 16), dot);
-          dot = fmaf(b, __uint_as_float(y[e] & 0xffff0000u), dot);
-        }
+        dot = fmaf(a, __uint_as_float(y[e] << 16), dot);
+        dot = fmaf(b, __uint_as_float(y[e] & 0xffff0000u), dot);
         x[8 * j + 2 * e] = __float_as_uint(fmaf(m, __uint_as_float(t[e] << 16), a));
         x[8 * j + 2 * e + 1] = __float_as_uint(fmaf(m, __uint_as_float(t[e] & 0xffff0000u), b));
       }
@@ -333,9 +328,9 @@ __device__ __forceinline__ float scale_acc(uint32_t acc, float f, float m, const
 }
 
 // A row of an accumulator to memory: bf16, or fp32 partial gradients.
-__device__ __forceinline__ void store_acc(uint32_t acc, __nv_bfloat16* row, float* part, int width,
-                                          bool keep) {
-#pragma unroll
+static __device__ __noinline__ void store_acc(uint32_t acc, __nv_bfloat16* row, float* part,
+                                              int width, bool keep) {
+#pragma unroll 1
   for (int p = 0; p < 4; ++p) {
     if (32 * p >= width) break;
     uint32_t x[32];
@@ -359,6 +354,7 @@ __device__ __forceinline__ void store_acc(uint32_t acc, __nv_bfloat16* row, floa
         *reinterpret_cast<uint4*>(row + 32 * p + 8 * j) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
+    __syncwarp();
   }
 }
 
@@ -525,6 +521,7 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
       if (wg == 2) {
         // <H, G> from both parts of both images
         float s = 0.f;
+#pragma unroll 2
         for (int i = row; i < (int)kTile / 16; i += 128) {
           const uint4 v[4] = {reinterpret_cast<const uint4*>(himg)[i],
                               reinterpret_cast<const uint4*>(himg + kTile)[i],
@@ -556,51 +553,66 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
         // row i: j over blocks up to its own
         if (!warp_wait(bars + B_A, 0, abort)) break;
         tc_fence_after();
+#pragma unroll 1
+        for (int p = 0; p < wq; ++p) {
+          uint32_t x[32], d[32], o[16];
+          tmem_ld32<32>(lanes + T_S + 32 * p, x);
+          tmem_ld32<32>(lanes + T_DP + 32 * p, d);
+          float f = pre;
+          if (p < 1 && wq > 1) f += gates->tot[1];
+          if (p < 2 && wq > 2) f += gates->tot[2];
+          f = s * ex2(f);
+          tmem_ld_wait();
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          uint32_t o[16];
-          if (p > wq) {
+          for (int e = 0; e < 8; ++e) {
+            const float4 g = reinterpret_cast<const float4*>(gates->es + 32 * p)[e];
+            const float gg[4] = {g.x, g.y, g.z, g.w};
+            float v[4];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = 0;
-          } else {
-            uint32_t x[32], d[32];
-            tmem_ld32<32>(lanes + T_S + 32 * p, x);
-            tmem_ld32<32>(lanes + T_DP + 32 * p, d);
-            float f = pre;
-#pragma unroll
-            for (int m = 1; m < 3; ++m)
-              if (m > p && m < wq) f += gates->tot[m];
-            f = s * exp2f(f);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float v[2];
-#pragma unroll
-              for (int z = 0; z < 2; ++z) {
-                const int j = 2 * e + z;
-                const float dp = __uint_as_float(d[j]);
-                if (p == wq) {
-                  v[z] = j < lane ? dp * (s * exp2f(pre - gates->pre[32 * p + j])) : 0.f;
-                  if (j < lane) wsum = fmaf(v[z], __uint_as_float(x[j]), wsum);
-                  if (j == lane) {
-                    own = s * dp;
-                    own_p = s * __uint_as_float(x[j]);
-                  }
-                } else {
-                  v[z] = dp * (f * gates->es[32 * p + j]);
-                  wsum = fmaf(v[z], __uint_as_float(x[j]), wsum);
-                }
-              }
-              o[e] = pack_bf162(v[0], v[1]);
+            for (int z = 0; z < 4; ++z) {
+              v[z] = __uint_as_float(d[4 * e + z]) * (f * gg[z]);
+              wsum = fmaf(v[z], __uint_as_float(x[4 * e + z]), wsum);
             }
+            o[2 * e] = pack_bf162(v[0], v[1]);
+            o[2 * e + 1] = pack_bf162(v[2], v[3]);
           }
           tmem_st32<16>(lanes + T_DS + 16 * p, o);
+        }
+        {
+          uint32_t x[32], d[32], o[16];
+          tmem_ld32<32>(lanes + T_S + 32 * wq, x);
+          tmem_ld32<32>(lanes + T_DP + 32 * wq, d);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float4 g = reinterpret_cast<const float4*>(gates->pre + 32 * wq)[e];
+            const float gg[4] = {g.x, g.y, g.z, g.w};
+            float v[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              const int j = 4 * e + z;
+              const float dp = s * __uint_as_float(d[j]), sc = __uint_as_float(x[j]);
+              v[z] = j < lane ? dp * ex2(pre - gg[z]) : 0.f;
+              if (j < lane) wsum = fmaf(v[z], sc, wsum);
+              if (j == lane) {
+                own = dp;
+                own_p = s * sc;
+              }
+            }
+            o[2 * e] = pack_bf162(v[0], v[1]);
+            o[2 * e + 1] = pack_bf162(v[2], v[3]);
+          }
+          tmem_st32<16>(lanes + T_DS + 16 * wq, o);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = 0;
+#pragma unroll 1
+          for (int p = wq + 1; p < 4; ++p) tmem_st32<16>(lanes + T_DS + 16 * p, o);
         }
         tmem_st_wait();
         warp_arrive(bars + B_DSA);
         if (!warp_wait(bars + B_X1, 0, abort)) break;
         tc_fence_after();
-        dot = scale_acc<true>(lanes + T_X1, into, own, sm + kK, sm + kQ, row);
+        dot = scale_acc(lanes + T_X1, into, own, sm + kK, sm + kQ, row);
         warp_arrive(bars + B_X1S);
         if (!warp_wait(bars + B_DQ, 0, abort)) break;
         tc_fence_after();
@@ -609,7 +621,7 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
         warp_arrive(bars + B_DQR);
         if (!warp_wait(bars + B_X3, 0, abort)) break;
         tc_fence_after();
-        scale_acc<false>(lanes + T_X1, out, own_p, sm + kDo, nullptr, row);
+        scale_acc(lanes + T_X1, out, own_p, sm + kDo, sm + kDo, row);
         warp_arrive(bars + B_X3S);
         if (!warp_wait(bars + B_DV, 0, abort)) break;
         tc_fence_after();
@@ -620,39 +632,68 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
         if (!warp_wait(bars + B_B, 0, abort)) break;
         if (!warp_wait(bars + B_DSA, 0, abort)) break;  // dS^T goes behind dS
         tc_fence_after();
+        uint32_t o[16], q[16];
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          uint32_t o[16], q[16];
-          if (p < wq) {
+        for (int e = 0; e < 16; ++e) o[e] = q[e] = 0;
+#pragma unroll 1
+        for (int p = 0; p < wq; ++p) {
+          tmem_st32<16>(lanes + T_PT + 16 * p, o);
+          tmem_st32<16>(lanes + T_DST + 16 * p, q);
+        }
+        {
+          uint32_t x[32], d[32];
+          tmem_ld32<32>(lanes + T_ST + 32 * wq, x);
+          tmem_ld32<32>(lanes + T_DPT + 32 * wq, d);
+          tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = q[e] = 0;
-          } else {
-            uint32_t x[32], d[32];
-            tmem_ld32<32>(lanes + T_ST + 32 * p, x);
-            tmem_ld32<32>(lanes + T_DPT + 32 * p, d);
-            float f = 0.f;
+          for (int e = 0; e < 8; ++e) {
+            const float4 g = reinterpret_cast<const float4*>(gates->pre + 32 * wq)[e];
+            const float gg[4] = {g.x, g.y, g.z, g.w};
+            float u[4], v[4];
 #pragma unroll
-            for (int m = 1; m < 3; ++m)
-              if (m > wq && m < p) f += gates->tot[m];
-            f = s * es * exp2f(f);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float u[2], v[2];
-#pragma unroll
-              for (int z = 0; z < 2; ++z) {
-                const int i = 2 * e + z;
-                const float pi = gates->pre[32 * p + i];
-                const bool on = p != wq || i > lane;
-                const float k = p == wq ? (on ? s * exp2f(pi - pre) : 0.f) : f * exp2f(pi);
-                u[z] = on ? __uint_as_float(x[i]) * k : 0.f;
-                v[z] = on ? __uint_as_float(d[i]) * k : 0.f;
-                if (on) wsum = fmaf(v[z], __uint_as_float(x[i]), wsum);
-                if (p == wq && i == lane) own = s * __uint_as_float(d[i]);
-              }
-              o[e] = pack_bf162(u[0], u[1]);
-              q[e] = pack_bf162(v[0], v[1]);
+            for (int z = 0; z < 4; ++z) {
+              const int i = 4 * e + z;
+              const float k = s * ex2(gg[z] - pre);
+              u[z] = i > lane ? __uint_as_float(x[i]) * k : 0.f;
+              v[z] = i > lane ? __uint_as_float(d[i]) * k : 0.f;
+              if (i > lane) wsum = fmaf(v[z], __uint_as_float(x[i]), wsum);
+              if (i == lane) own = s * __uint_as_float(d[i]);
             }
+            o[2 * e] = pack_bf162(u[0], u[1]);
+            o[2 * e + 1] = pack_bf162(u[2], u[3]);
+            q[2 * e] = pack_bf162(v[0], v[1]);
+            q[2 * e + 1] = pack_bf162(v[2], v[3]);
+          }
+          tmem_st32<16>(lanes + T_PT + 16 * wq, o);
+          tmem_st32<16>(lanes + T_DST + 16 * wq, q);
+        }
+#pragma unroll 1
+        for (int p = wq + 1; p < 4; ++p) {
+          uint32_t x[32], d[32];
+          tmem_ld32<32>(lanes + T_ST + 32 * p, x);
+          tmem_ld32<32>(lanes + T_DPT + 32 * p, d);
+          float f = 0.f;
+          if (wq < 1 && p > 1) f += gates->tot[1];
+          if (wq < 2 && p > 2) f += gates->tot[2];
+          f = s * es * ex2(f);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float4 g = reinterpret_cast<const float4*>(gates->pre + 32 * p)[e];
+            const float gg[4] = {g.x, g.y, g.z, g.w};
+            float u[4], v[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              const int i = 4 * e + z;
+              const float k = f * ex2(gg[z]);
+              u[z] = __uint_as_float(x[i]) * k;
+              v[z] = __uint_as_float(d[i]) * k;
+              wsum = fmaf(v[z], __uint_as_float(x[i]), wsum);
+            }
+            o[2 * e] = pack_bf162(u[0], u[1]);
+            o[2 * e + 1] = pack_bf162(u[2], u[3]);
+            q[2 * e] = pack_bf162(v[0], v[1]);
+            q[2 * e + 1] = pack_bf162(v[2], v[3]);
           }
           tmem_st32<16>(lanes + T_PT + 16 * p, o);
           tmem_st32<16>(lanes + T_DST + 16 * p, q);
@@ -661,7 +702,7 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
         warp_arrive(bars + B_DSB);
         if (!warp_wait(bars + B_X2, 0, abort)) break;
         tc_fence_after();
-        dot = scale_acc<true>(lanes + T_X2, out, own, sm + kQ, sm + kK, row);
+        dot = scale_acc(lanes + T_X2, out, own, sm + kQ, sm + kK, row);
         warp_arrive(bars + B_X2S);
         if (!warp_wait(bars + B_DK, 0, abort)) break;
         tc_fence_after();

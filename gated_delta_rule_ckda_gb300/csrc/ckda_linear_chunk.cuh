@@ -39,6 +39,38 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, 
   tma_load_3d(dst + kPanel, map, bar, 64, token, head);
 }
 
+// The same tile into L2 only.
+__device__ __forceinline__ void prefetch_tile(const CUtensorMap* map, int32_t token, int32_t head,
+                                              bool second) {
+  for (int p = 0; p < (second ? 2 : 1); ++p)
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(64 * p), "r"(token), "r"(head)
+                 : "memory");
+}
+// Both panels of a tile to memory; rows past T and channels past the width are
+// not written.
+__device__ __forceinline__ void store_tile(const CUtensorMap* map, uint32_t src, int32_t token,
+                                           int32_t head, bool second) {
+  for (int p = 0; p < (second ? 2 : 1); ++p)
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(src + p * kPanel), "r"(64 * p), "r"(token), "r"(head)
+                 : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// This thread's stores have read their shared memory.
+__device__ __forceinline__ void store_read_wait() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+
+// 2^x, zero below 2^-126.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // D[tmem] (+)= A[tmem] * B[smem]: row i of A in lane i, two bf16 a column.
 __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
                                         uint32_t idesc, uint32_t accumulate) {
@@ -49,38 +81,50 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64
       : "memory");
 }
 // 128 x 128 products over K = 128, bf16 operands.  `mn`: the operand is stored
-// with its K index along the rows.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, bool a_mn, uint32_t b, bool b_mn,
-                                       bool accumulate) {
-#pragma unroll
-  for (int k = 0; k < 8; ++k)
-    umma_ss(d, a_mn ? mnmajor_desc(a, 128, k) : kmajor_desc(a, 128, k),
-            b_mn ? mnmajor_desc(b, 128, k) : kmajor_desc(b, 128, k),
-            idesc_f16(128, 128, 1, a_mn, b_mn), (accumulate || k > 0) ? 1u : 0u);
+// with its K index along the rows.  Kept out of line, so that one copy of the
+// issue code serves every product (see the note on short loops below).
+__device__ __forceinline__ uint64_t tile_desc(uint32_t tile, bool mn) {
+  return mn ? mnmajor_desc(tile, 128, 0) : kmajor_desc(tile, 128, 0);
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b, bool b_mn,
-                                       bool accumulate) {
+// Step k of 16 along K starts 2 (k % 4) + 1024 (k / 4) units of 16 bytes
+// further in a K-major tile and 128 k in an MN-major one.
+__device__ __forceinline__ uint64_t desc_step(bool mn, int k) {
+  return mn ? 128u * k : 1024u * (k >> 2) + 2u * (k & 3);
+}
+static __device__ __noinline__ void mma_ss(uint32_t d, uint32_t a, bool a_mn, uint32_t b, bool b_mn,
+                                           bool accumulate) {
+  const uint64_t da = tile_desc(a, a_mn), db = tile_desc(b, b_mn);
+  const uint32_t id = idesc_f16(128, 128, 1, 0, 0) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
 #pragma unroll
   for (int k = 0; k < 8; ++k)
-    umma_ts(d, a_tmem + 8 * k, b_mn ? mnmajor_desc(b, 128, k) : kmajor_desc(b, 128, k),
-            idesc_f16(128, 128, 1, 0, b_mn), (accumulate || k > 0) ? 1u : 0u);
+    umma_ss(d, da + desc_step(a_mn, k), db + desc_step(b_mn, k), id,
+            (accumulate || k > 0) ? 1u : 0u);
+}
+static __device__ __noinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b, bool b_mn,
+                                           bool accumulate) {
+  const uint64_t db = tile_desc(b, b_mn);
+  const uint32_t id = idesc_f16(128, 128, 1, 0, 0) | (b_mn ? 1u << 16 : 0u);
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    umma_ts(d, a_tmem + 8 * k, db + desc_step(b_mn, k), id, (accumulate || k > 0) ? 1u : 0u);
 }
 
 // ----------------------------------------------------------------- waiting
 // Bounded (about a second), and over at once when another warp has given up.
 // Called by whole warps; the answer is the same in every lane.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  bool ok = mbar_try_wait(bar, parity, 1000000u);
-  if (!ok) {
-    const uint64_t start = globaltimer_ns();
-    for (uint32_t i = 0; i < (1u << 24) && !ok; ++i) {
-      ok = mbar_try_wait(bar, parity, 1000000u);
-      if (!ok && (*abort || globaltimer_ns() - start > kWaitLimitNs)) break;
-    }
+static __device__ __noinline__ bool warp_wait_on(uint64_t* bar, uint32_t parity,
+                                                 volatile int* abort) {
+  const uint64_t start = globaltimer_ns();
+  for (uint32_t i = 0; i < (1u << 24); ++i) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity, 1000000u))) return true;
+    if (__any_sync(0xffffffffu, *abort || globaltimer_ns() - start > kWaitLimitNs)) break;
   }
-  ok = __all_sync(0xffffffffu, ok);
-  if (!ok) *abort = 1;
-  return ok;
+  *abort = 1;
+  return false;
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity, 1000000u))) return true;
+  return warp_wait_on(bar, parity, abort);
 }
 // Orders this warp's shared-memory writes and TMEM accesses before the tensor
 // cores' next use, and arrives once for the warp.
@@ -139,15 +183,15 @@ __device__ __forceinline__ void make_gates(Gates* g, float4 x, int lane) {
   const float4 suf = make_float4(after + s0, after + s1, after + s2, after);
   reinterpret_cast<float4*>(g->pre)[lane] = pre;
   reinterpret_cast<float4*>(g->es)[lane] =
-      make_float4(exp2f(suf.x), exp2f(suf.y), exp2f(suf.z), exp2f(suf.w));
+      make_float4(ex2(suf.x), ex2(suf.y), ex2(suf.z), ex2(suf.w));
   reinterpret_cast<float4*>(g->eL)[lane] =
-      make_float4(exp2f(earlier + pre.x), exp2f(earlier + pre.y), exp2f(earlier + pre.z),
-                  exp2f(earlier + pre.w));
+      make_float4(ex2(earlier + pre.x), ex2(earlier + pre.y), ex2(earlier + pre.z),
+                  ex2(earlier + pre.w));
   reinterpret_cast<float4*>(g->w)[lane] =
-      make_float4(exp2f(later + suf.x), exp2f(later + suf.y), exp2f(later + suf.z),
-                  exp2f(later + suf.w));
+      make_float4(ex2(later + suf.x), ex2(later + suf.y), ex2(later + suf.z),
+                  ex2(later + suf.w));
   if ((lane & 7) == 0) g->tot[b] = tot;
-  if (lane == 0) g->all = exp2f(t0 + t1 + t2 + t3);
+  if (lane == 0) g->all = ex2(t0 + t1 + t2 + t3);
 }
 // log2 decays of tokens 4l .. 4l+3 of a chunk, `valid` of its tokens in the sequence.
 __device__ __forceinline__ float4 load_decays(const float* g, int stride, int valid, int lane) {
@@ -167,11 +211,21 @@ __device__ __forceinline__ void zero_row(char* tile, int row) {
     *reinterpret_cast<uint4*>(tile + sw128_chunk(128, row, j)) = make_uint4(0, 0, 0, 0);
 }
 
+// (The loops over a row's pieces here and in the kernels are kept short on
+// purpose: with a dozen warps in different code, instructions that run once a
+// chunk come from beyond the instruction cache, and unrolled rows took three
+// times as long.)
+//
 // A token row of 64 channels times w, in two bf16 parts: hi in place, lo at the
-// same place of another tile.  hi + lo is w k to 2^-16, which fp32 results need.
+// same place of another tile.  With w = wh + wl in bf16, hi = round(k wh), what
+// that rounding left is exact in bf16 (k wh has 16 bits), and k wl joins it:
+// hi + lo is w k to 2^-16, which fp32 results need, in three packed operations.
 __device__ __forceinline__ void scale_row(char* tile, char* lo, int row, int panel, float w,
                                           bool keep) {
-#pragma unroll
+  const __nv_bfloat16 h = __float2bfloat16_rn(w);
+  const __nv_bfloat162 wh = __bfloat162bfloat162(h);
+  const __nv_bfloat162 wl = __float2bfloat162_rn(w - __bfloat162float(h));
+#pragma unroll 2
   for (int j = 0; j < 8; ++j) {
     const uint32_t off = sw128_chunk(128, row, 8 * panel + j);
     const uint4 v = *reinterpret_cast<const uint4*>(tile + off);
@@ -179,11 +233,11 @@ __device__ __forceinline__ void scale_row(char* tile, char* lo, int row, int pan
     uint32_t hi[4], rest[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float a = keep ? __uint_as_float(in[e] << 16) * w : 0.f;
-      const float b = keep ? __uint_as_float(in[e] & 0xffff0000u) * w : 0.f;
-      hi[e] = pack_bf162(a, b);
-      rest[e] = pack_bf162(a - __uint_as_float(hi[e] << 16),
-                           b - __uint_as_float(hi[e] & 0xffff0000u));
+      const __nv_bfloat162 k = *reinterpret_cast<const __nv_bfloat162*>(&in[e]);
+      const __nv_bfloat162 a = __hmul2_rn(k, wh);
+      const __nv_bfloat162 b = __hfma2(k, wl, __hfma2(k, wh, __hneg2(a)));
+      hi[e] = keep ? *reinterpret_cast<const uint32_t*>(&a) : 0u;
+      rest[e] = keep ? *reinterpret_cast<const uint32_t*>(&b) : 0u;
     }
     *reinterpret_cast<uint4*>(tile + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     *reinterpret_cast<uint4*>(lo + off) = make_uint4(rest[0], rest[1], rest[2], rest[3]);

@@ -16,7 +16,9 @@
 //   warp 1       issues the products (tcgen05, one thread)
 //   warp 2       the decay factors of a chunk
 //   warps 4-7    one row of S a thread: P as bf16 into TMEM, where the product
-//                P V reads it; later the row of o
+//                P V reads it; later the row of o, staged in the query tile's
+//                slot and stored with TMA (a thread's own 256-byte rows cost
+//                four times the L1 passes)
 //   warps 8-15   the state: thread (r, s) holds H[64 s .. 64 s + 63][r] in
 //                fp32 registers, rounded to nearest at every step (tensor-core
 //                accumulators truncate, which over thousands of chunks would
@@ -37,6 +39,7 @@ using namespace chunk;
 
 constexpr int kThreads = 512;
 constexpr int kSlots = 5;
+constexpr int kAhead = 2;                       // chunks prefetched into L2
 constexpr uint32_t kLo = kSlots * kTile;        // lo part of the scaled keys
 constexpr uint32_t kH = kLo + kTile;            // bf16 state, [dv][dk]
 constexpr uint32_t kGates = kH + kTile;
@@ -53,7 +56,8 @@ constexpr uint32_t T_S = 0, T_P = 0, T_DF = 128, T_OI = 256, T_O = 384;
 
 __global__ void __launch_bounds__(kThreads, 1)
 linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ CUtensorMap mq,
-                  const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+                  const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                  const __grid_constant__ CUtensorMap mo) {
   extern __shared__ __align__(1024) char sm[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kBars);
   Gates* gates = reinterpret_cast<Gates*>(sm + kGates);
@@ -104,19 +108,24 @@ linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ 
         if (use > 0 && !mbar_wait(bars + B_EMPTY + slot, (use - 1) & 1)) { *abort = 1; break; }
         if (*abort) break;
         const CUtensorMap* m = i % 3 == 0 ? &mk : i % 3 == 1 ? &mq : &mv;
+        // the ring holds less than two chunks: a slot comes free late, and its
+        // load must not wait for DRAM
+        if (c + kAhead < chunks)
+          prefetch_tile(m, t0 + (c + kAhead) * C, i % 3 == 2 ? vz : qz,
+                        (i % 3 == 2 ? a.dv : a.dk) > 64);
         load_tile(sb + slot * kTile, m, bars + B_FULL + slot, t0 + c * C, i % 3 == 2 ? vz : qz);
       }
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------- products
+    auto slot = [&](int i) { return i % kSlots; };
+    auto tile = [&](int i) { return sb + (i % kSlots) * kTile; };
+    auto full = [&](int i) { return warp_wait(bars + B_FULL + i % kSlots, (i / kSlots) & 1, abort); };
     for (int c = 0; c < chunks; ++c) {
       const uint32_t par = c & 1;
-      const int ik = 3 * c, iq = ik + 1, iv = ik + 2;
-      const uint32_t K = sb + (ik % kSlots) * kTile, Q = sb + (iq % kSlots) * kTile,
-                     V = sb + (iv % kSlots) * kTile;
-      if (!warp_wait(bars + B_FULL + ik % kSlots, (ik / kSlots) & 1, abort)) break;
-      if (!warp_wait(bars + B_FULL + iq % kSlots, (iq / kSlots) & 1, abort)) break;
-      // P shares the columns of S: the previous chunk's P V must be done
+      const uint32_t K = tile(3 * c), Q = tile(3 * c + 1), V = tile(3 * c + 2);
+      if (!full(3 * c) || !full(3 * c + 1)) break;
+      // P shares the columns of S
       if (c > 0 && !warp_wait(bars + B_O, (c - 1) & 1, abort)) break;
       tc_fence_after();
       if (lane == 0) {
@@ -129,23 +138,22 @@ linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ 
       if (lane == 0) {
         mma_ss(tmem + T_OI, Q, false, sb + kH, false, false);
         umma_commit(bars + B_OI);
-        umma_commit(bars + B_EMPTY + iq % kSlots);
       }
-      if (!warp_wait(bars + B_FULL + iv % kSlots, (iv / kSlots) & 1, abort)) break;
-      if (!warp_wait(bars + B_P, par, abort)) break;
-      tc_fence_after();
-      if (lane == 0) {
-        mma_ts(tmem + T_O, tmem + T_P, V, true, false);
-        umma_commit(bars + B_O);
-      }
+      if (!full(3 * c + 2)) break;
       if (!warp_wait(bars + B_KT, par, abort)) break;
       tc_fence_after();
       if (lane == 0) {
         mma_ss(tmem + T_DF, V, true, K, true, false);
         mma_ss(tmem + T_DF, V, true, sb + kLo, true, true);
         umma_commit(bars + B_DF);
-        umma_commit(bars + B_EMPTY + ik % kSlots);
-        umma_commit(bars + B_EMPTY + iv % kSlots);
+        umma_commit(bars + B_EMPTY + slot(3 * c));
+      }
+      if (!warp_wait(bars + B_P, par, abort)) break;
+      tc_fence_after();
+      if (lane == 0) {
+        mma_ts(tmem + T_O, tmem + T_P, V, true, false);
+        umma_commit(bars + B_O);
+        umma_commit(bars + B_EMPTY + slot(3 * c + 2));
       }
     }
     if (lane == 0) umma_commit(bars + B_END);
@@ -168,53 +176,54 @@ linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ 
     const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16);
     for (int c = 0; c < chunks; ++c) {
       const uint32_t par = c & 1;
-      const int valid = min(len - c * C, C), iv = 3 * c + 2;
-      if (a.cu_seqlens && valid < C) {  // tokens of the next sequence behind this one
-        if (!warp_wait(bars + B_FULL + iv % kSlots, (iv / kSlots) & 1, abort)) break;
-        if (i >= valid) zero_row(sm + (iv % kSlots) * kTile, i);
-      }
+      const int valid = min(len - c * C, C), sq = (3 * c + 1) % kSlots;
       if (!warp_wait(bars + B_G, par, abort)) break;
       const float pre = gates->pre[i], into = gates->eL[i];
       if (!warp_wait(bars + B_S, par, abort)) break;
       tc_fence_after();
-#pragma unroll
-      for (int p = 0; p < 4; ++p) {
+      // earlier blocks: from j to its block's end, over the blocks between, and
+      // from this block's start to i
+#pragma unroll 1
+      for (int p = 0; p < w; ++p) {
+        uint32_t s[32];
+        tmem_ld32<32>(lanes + T_S + 32 * p, s);
+        float x = pre;
+        if (p < 1 && w > 1) x += gates->tot[1];
+        if (p < 2 && w > 2) x += gates->tot[2];
+        const float r = ex2(x);
         uint32_t out[16];
-        if (p > w) {
+        tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) out[e] = 0;
-        } else {
-          uint32_t s[32];
-          tmem_ld32<32>(lanes + T_S + 32 * p, s);
-          if (p == w) {
-            tmem_ld_wait();
-            // j <= i inside a block of 32: from the difference of short sums
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float2 q = reinterpret_cast<const float2*>(gates->pre + 32 * p)[e];
-              const float u = 2 * e <= lane ? __uint_as_float(s[2 * e]) * exp2f(pre - q.x) : 0.f;
-              const float v =
-                  2 * e + 1 <= lane ? __uint_as_float(s[2 * e + 1]) * exp2f(pre - q.y) : 0.f;
-              out[e] = pack_bf162(u, v);
-            }
-          } else {
-            // an earlier block: from j to its block's end, over the blocks
-            // between, and from this block's start to i
-            float x = pre;
-#pragma unroll
-            for (int m = 1; m < 3; ++m)
-              if (m > p && m < w) x += gates->tot[m];
-            const float r = exp2f(x);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float2 q = reinterpret_cast<const float2*>(gates->es + 32 * p)[e];
-              out[e] = pack_bf162(__uint_as_float(s[2 * e]) * (r * q.x),
-                                  __uint_as_float(s[2 * e + 1]) * (r * q.y));
-            }
-          }
+        for (int e = 0; e < 8; ++e) {
+          const float4 q = reinterpret_cast<const float4*>(gates->es + 32 * p)[e];
+          out[2 * e] = pack_bf162(__uint_as_float(s[4 * e]) * (r * q.x),
+                                  __uint_as_float(s[4 * e + 1]) * (r * q.y));
+          out[2 * e + 1] = pack_bf162(__uint_as_float(s[4 * e + 2]) * (r * q.z),
+                                      __uint_as_float(s[4 * e + 3]) * (r * q.w));
         }
         tmem_st32<16>(lanes + T_P + 16 * p, out);
+      }
+      {
+        // its own block, j <= i: from the difference of short sums
+        uint32_t s[32], out[16];
+        tmem_ld32<32>(lanes + T_S + 32 * w, s);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float4 q = reinterpret_cast<const float4*>(gates->pre + 32 * w)[e];
+          const float qq[4] = {q.x, q.y, q.z, q.w};
+          float v[4];
+#pragma unroll
+          for (int z = 0; z < 4; ++z)
+            v[z] = 4 * e + z <= lane ? __uint_as_float(s[4 * e + z]) * ex2(pre - qq[z]) : 0.f;
+          out[2 * e] = pack_bf162(v[0], v[1]);
+          out[2 * e + 1] = pack_bf162(v[2], v[3]);
+        }
+        tmem_st32<16>(lanes + T_P + 16 * w, out);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) out[e] = 0;
+#pragma unroll 1
+        for (int p = w + 1; p < 4; ++p) tmem_st32<16>(lanes + T_P + 16 * p, out);
       }
       tmem_st_wait();
       warp_publish(bars + B_P);
@@ -222,32 +231,46 @@ linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ 
 
       if (!warp_wait(bars + B_O, par, abort)) break;
       tc_fence_after();
-      __nv_bfloat16* row = static_cast<__nv_bfloat16*>(a.o) + (vrow + (size_t)c * C + i) * a.dv;
+      // o by way of the query tile's slot, which nothing reads any more
+      char* stage = sm + sq * kTile;
       const float fo = a.scale, fi = a.scale * into;
-#pragma unroll
+#pragma unroll 1
       for (int p = 0; p < 4; ++p) {
-        if (32 * p >= a.dv) break;
         uint32_t x[32], y[32];
         tmem_ld32<32>(lanes + T_O + 32 * p, x);
         tmem_ld32<32>(lanes + T_OI + 32 * p, y);
         tmem_ld_wait();
-        if (i < valid) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (32 * p + 8 * j >= a.dv) break;
-            uint32_t o[4];
+        for (int j = 0; j < 4; ++j) {
+          uint32_t o[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int k = 8 * j + 2 * e;
-              o[e] = pack_bf162(
-                  fmaf(fo, __uint_as_float(x[k]), fi * __uint_as_float(y[k])),
-                  fmaf(fo, __uint_as_float(x[k + 1]), fi * __uint_as_float(y[k + 1])));
-            }
-            *reinterpret_cast<uint4*>(row + 32 * p + 8 * j) = make_uint4(o[0], o[1], o[2], o[3]);
+          for (int e = 0; e < 4; ++e) {
+            const int k = 8 * j + 2 * e;
+            o[e] = pack_bf162(fmaf(fo, __uint_as_float(x[k]), fi * __uint_as_float(y[k])),
+                              fmaf(fo, __uint_as_float(x[k + 1]), fi * __uint_as_float(y[k + 1])));
           }
+          *reinterpret_cast<uint4*>(stage + sw128_chunk(128, i, 4 * p + j)) =
+              make_uint4(o[0], o[1], o[2], o[3]);
         }
       }
       warp_arrive(bars + B_OFREE);
+      fence_proxy_async_smem();
+      named_sync(1, 128);
+      if (a.cu_seqlens && valid < C) {
+        // the rows behind belong to the next sequence: 16 lanes to a row of this one
+        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + (vrow + (size_t)c * C) * a.dv;
+        for (int e = i; e < 16 * valid; e += 128) {
+          const int row = e >> 4, j = e & 15;
+          if (8 * j < a.dv)
+            *reinterpret_cast<uint4*>(o + (size_t)row * a.dv + 8 * j) =
+                *reinterpret_cast<const uint4*>(stage + sw128_chunk(128, row, j));
+        }
+        named_sync(1, 128);  // (the last chunk of the sequence: nothing reuses the slot)
+      } else if (i == 0) {
+        store_tile(&mo, sb + sq * kTile, t0 + c * C, vz, a.dv > 64);
+        store_read_wait();  // (this warp has the shortest rows of P)
+        mbar_arrive(bars + B_EMPTY + sq);
+      }
     }
   } else if (warp >= 8) {
     // --------------------------------------------------------------- state
@@ -279,6 +302,11 @@ linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ 
       if (lane == 0) mbar_arrive(bars + B_GFREE);
       if (!(ok = warp_wait(bars + B_FULL + ik % kSlots, (ik / kSlots) & 1, abort))) break;
       if (!(ok = warp_wait(bars + B_S, par, abort))) break;
+      if (a.cu_seqlens && valid < C) {  // tokens of the next sequence behind this one
+        const int iv = ik + 2;
+        if (!(ok = warp_wait(bars + B_FULL + iv % kSlots, (iv / kSlots) & 1, abort))) break;
+        if (s == 0 && r >= valid) zero_row(sm + (iv % kSlots) * kTile, r);
+      }
       scale_row(sm + (ik % kSlots) * kTile, sm + kLo, r, s, wt, r < valid);
       warp_publish(bars + B_KT);
       // the chunk's contribution
@@ -336,15 +364,16 @@ bool linear_map(CUtensorMap* m, const void* base, uint64_t heads, uint64_t T, ui
 }
 
 cudaError_t linear_chunk_fwd(const LinearArgs& a, cudaStream_t s) {
-  CUtensorMap mq{}, mk{}, mv{};
+  CUtensorMap mq{}, mk{}, mv{}, mo{};
   if (a.T > 0 && (!linear_map(&mq, a.q, (uint64_t)a.B * a.Hk, a.T, a.dk) ||
                   !linear_map(&mk, a.k, (uint64_t)a.B * a.Hk, a.T, a.dk) ||
-                  !linear_map(&mv, a.v, (uint64_t)a.B * a.H, a.T, a.dv)))
+                  !linear_map(&mv, a.v, (uint64_t)a.B * a.H, a.T, a.dv) ||
+                  !linear_map(&mo, a.o, (uint64_t)a.B * a.H, a.T, a.dv)))
     return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(linear_fwd_kernel,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return e;
-  linear_fwd_kernel<<<(unsigned)a.N * a.H, kThreads, kSmem, s>>>(a, mq, mk, mv);
+  linear_fwd_kernel<<<(unsigned)a.N * a.H, kThreads, kSmem, s>>>(a, mq, mk, mv, mo);
   return cudaGetLastError();
 }
 
