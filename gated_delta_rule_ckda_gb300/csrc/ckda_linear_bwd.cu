@@ -147,8 +147,8 @@ linear_state_kernel(const __grid_constant__ LinearArgs a, const __grid_constant_
       if (i >= 2 && !warp_wait(bars + B_DFREE + p, (i / 2 - 1) & 1, abort)) break;
       tc_fence_after();
       if (lane == 0) {
-        mma_ss(tmem + 128 * p, sb + iy * kTile, true, sb + ix * kTile, true, false);
-        mma_ss(tmem + 128 * p, sb + iy * kTile, true, sb + kLo + p * kTile, true, true);
+        mma_ss<true, true>(tmem + 128 * p, sb + iy * kTile, sb + ix * kTile, 0);
+        mma_ss<true, true>(tmem + 128 * p, sb + iy * kTile, sb + kLo + p * kTile, 1);
         umma_commit(bars + B_DF + p);
         umma_commit(bars + B_EMPTY + ix);
         umma_commit(bars + B_EMPTY + iy);
@@ -453,53 +453,53 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
       if (tail && !warp_wait(bars + B_TAIL, 0, abort)) break;
       tc_fence_after();
       if (lane == 0) {
-        mma_ss(tmem + T_S, sb + kQ, false, sb + kK, false, false);
-        mma_ss(tmem + T_DP, sb + kDo, false, sb + kV, false, false);
+        mma_ss<false, false>(tmem + T_S, sb + kQ, sb + kK, 0);
+        mma_ss<false, false>(tmem + T_DP, sb + kDo, sb + kV, 0);
         umma_commit(bars + B_A);
-        mma_ss(tmem + T_ST, sb + kK, false, sb + kQ, false, false);
-        mma_ss(tmem + T_DPT, sb + kV, false, sb + kDo, false, false);
+        mma_ss<false, false>(tmem + T_ST, sb + kK, sb + kQ, 0);
+        mma_ss<false, false>(tmem + T_DPT, sb + kV, sb + kDo, 0);
         umma_commit(bars + B_B);
       }
       if (!warp_wait(bars + B_H, 0, abort)) break;
       if (!warp_wait(bars + B_DSA, 0, abort)) break;
       tc_fence_after();
       if (lane == 0) {
-        mma_ss(tmem + T_X1, sb + kDo, false, sb + kS0, true, false);
-        mma_ss(tmem + T_X1, sb + kDo, false, sb + kS1, true, true);
+        mma_ss<false, true>(tmem + T_X1, sb + kDo, sb + kS0, 0);
+        mma_ss<false, true>(tmem + T_X1, sb + kDo, sb + kS1, 1);
         umma_commit(bars + B_X1);
       }
       if (!warp_wait(bars + B_GH, 0, abort)) break;
       if (!warp_wait(bars + B_DSB, 0, abort)) break;
       tc_fence_after();
-      if (lane == 0) mma_ss(tmem + T_X2, sb + kV, false, sb + kS2, true, false);
+      if (lane == 0) mma_ss<false, true>(tmem + T_X2, sb + kV, sb + kS2, 0);
       if (!warp_wait(bars + B_GL, 0, abort)) break;
       if (lane == 0) {
-        mma_ss(tmem + T_X2, sb + kV, false, sb + kS0, true, true);
+        mma_ss<false, true>(tmem + T_X2, sb + kV, sb + kS0, 1);
         umma_commit(bars + B_X2);
       }
       if (!warp_wait(bars + B_X1S, 0, abort)) break;
       tc_fence_after();
       if (lane == 0) {
-        mma_ts(tmem + T_X1, tmem + T_DS, sb + kK, true, true);
+        mma_ts<true>(tmem + T_X1, tmem + T_DS, sb + kK, 1);
         umma_commit(bars + B_DQ);
       }
       if (!warp_wait(bars + B_X2S, 0, abort)) break;
       tc_fence_after();
       if (lane == 0) {
-        mma_ts(tmem + T_X2, tmem + T_DST, sb + kQ, true, true);
+        mma_ts<true>(tmem + T_X2, tmem + T_DST, sb + kQ, 1);
         umma_commit(bars + B_DK);
       }
       if (!warp_wait(bars + B_DQR, 0, abort)) break;
       tc_fence_after();
       if (lane == 0) {
-        mma_ss(tmem + T_X1, sb + kK, false, sb + kS2, false, false);
-        mma_ss(tmem + T_X1, sb + kK, false, sb + kS0, false, true);
+        mma_ss<false, false>(tmem + T_X1, sb + kK, sb + kS2, 0);
+        mma_ss<false, false>(tmem + T_X1, sb + kK, sb + kS0, 1);
         umma_commit(bars + B_X3);
       }
       if (!warp_wait(bars + B_X3S, 0, abort)) break;
       tc_fence_after();
       if (lane == 0) {
-        mma_ts(tmem + T_X1, tmem + T_PT, sb + kDo, true, true);
+        mma_ts<true>(tmem + T_X1, tmem + T_PT, sb + kDo, 1);
         umma_commit(bars + B_DV);
       }
     } while (false);

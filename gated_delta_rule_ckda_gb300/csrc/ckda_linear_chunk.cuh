@@ -39,15 +39,6 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, 
   tma_load_3d(dst + kPanel, map, bar, 64, token, head);
 }
 
-// The same tile into L2 only.
-__device__ __forceinline__ void prefetch_tile(const CUtensorMap* map, int32_t token, int32_t head,
-                                              bool second) {
-  for (int p = 0; p < (second ? 2 : 1); ++p)
-    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(64 * p), "r"(token), "r"(head)
-                 : "memory");
-}
 // Both panels of a tile to memory; rows past T and channels past the width are
 // not written.
 __device__ __forceinline__ void store_tile(const CUtensorMap* map, uint32_t src, int32_t token,
@@ -80,33 +71,37 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// 128 x 128 products over K = 128, bf16 operands.  `mn`: the operand is stored
-// with its K index along the rows.  Kept out of line, so that one copy of the
-// issue code serves every product (see the note on short loops below).
-__device__ __forceinline__ uint64_t tile_desc(uint32_t tile, bool mn) {
-  return mn ? mnmajor_desc(tile, 128, 0) : kmajor_desc(tile, 128, 0);
+// 128 x 128 products over K = 128, bf16 operands, issued by one thread.  AMN,
+// BMN: the operand is stored with its K index along the rows.  One copy of the
+// issue code for each pair of layouts, out of line (see the note on short loops
+// below), with the descriptors' steps as constants: one that is looked up costs
+// the issuing thread as long as two products take.
+template <bool MN>
+__device__ __forceinline__ uint64_t tile_desc(uint32_t tile) {
+  return MN ? mnmajor_desc(tile, 128, 0) : kmajor_desc(tile, 128, 0);
 }
 // Step k of 16 along K starts 2 (k % 4) + 1024 (k / 4) units of 16 bytes
 // further in a K-major tile and 128 k in an MN-major one.
-__device__ __forceinline__ uint64_t desc_step(bool mn, int k) {
-  return mn ? 128u * k : 1024u * (k >> 2) + 2u * (k & 3);
+template <bool MN>
+__device__ __forceinline__ uint64_t desc_step(int k) {
+  return MN ? 128u * k : 1024u * (k >> 2) + 2u * (k & 3);
 }
-static __device__ __noinline__ void mma_ss(uint32_t d, uint32_t a, bool a_mn, uint32_t b, bool b_mn,
-                                           bool accumulate) {
-  const uint64_t da = tile_desc(a, a_mn), db = tile_desc(b, b_mn);
-  const uint32_t id = idesc_f16(128, 128, 1, 0, 0) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
+template <bool AMN, bool BMN>
+static __device__ __noinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t accumulate) {
+  const uint64_t da = tile_desc<AMN>(a), db = tile_desc<BMN>(b);
+  umma_ss(d, da, db, idesc_f16(128, 128, 1, AMN, BMN), accumulate);
 #pragma unroll
-  for (int k = 0; k < 8; ++k)
-    umma_ss(d, da + desc_step(a_mn, k), db + desc_step(b_mn, k), id,
-            (accumulate || k > 0) ? 1u : 0u);
+  for (int k = 1; k < 8; ++k)
+    umma_ss(d, da + desc_step<AMN>(k), db + desc_step<BMN>(k), idesc_f16(128, 128, 1, AMN, BMN), 1);
 }
-static __device__ __noinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b, bool b_mn,
-                                           bool accumulate) {
-  const uint64_t db = tile_desc(b, b_mn);
-  const uint32_t id = idesc_f16(128, 128, 1, 0, 0) | (b_mn ? 1u << 16 : 0u);
+template <bool BMN>
+static __device__ __noinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b,
+                                           uint32_t accumulate) {
+  const uint64_t db = tile_desc<BMN>(b);
+  umma_ts(d, a_tmem, db, idesc_f16(128, 128, 1, 0, BMN), accumulate);
 #pragma unroll
-  for (int k = 0; k < 8; ++k)
-    umma_ts(d, a_tmem + 8 * k, db + desc_step(b_mn, k), id, (accumulate || k > 0) ? 1u : 0u);
+  for (int k = 1; k < 8; ++k)
+    umma_ts(d, a_tmem + 8 * k, db + desc_step<BMN>(k), idesc_f16(128, 128, 1, 0, BMN), 1);
 }
 
 // ----------------------------------------------------------------- waiting

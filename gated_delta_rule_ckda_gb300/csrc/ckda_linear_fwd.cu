@@ -12,12 +12,12 @@
 // never leaves the SM.  It is bound by HBM: 1 KiB a token at 128 x 128 against
 // five 128 x 128 x 128 products a chunk.
 //   warp 0       loads tiles with TMA into a ring of five 32 KB slots, in the
-//                order k, q, v of chunk after chunk
+//                order q, k, v of chunk after chunk
 //   warp 1       issues the products (tcgen05, one thread)
 //   warp 2       the decay factors of a chunk
 //   warps 4-7    one row of S a thread: P as bf16 into TMEM, where the product
-//                P V reads it; later the row of o, staged in the query tile's
-//                slot and stored with TMA (a thread's own 256-byte rows cost
+//                P V reads it; later the row of o, staged in the state's
+//                tile (between its readers and the next state) and stored with TMA (a thread's own 256-byte rows cost
 //                four times the L1 passes)
 //   warps 8-15   the state: thread (r, s) holds H[64 s .. 64 s + 63][r] in
 //                fp32 registers, rounded to nearest at every step (tensor-core
@@ -39,7 +39,6 @@ using namespace chunk;
 
 constexpr int kThreads = 512;
 constexpr int kSlots = 5;
-constexpr int kAhead = 2;                       // chunks prefetched into L2
 constexpr uint32_t kLo = kSlots * kTile;        // lo part of the scaled keys
 constexpr uint32_t kH = kLo + kTile;            // bf16 state, [dv][dk]
 constexpr uint32_t kGates = kH + kTile;
@@ -48,8 +47,9 @@ constexpr uint32_t kSmem = kBars + 512;
 static_assert(kSmem <= 232448, "shared memory of a CTA");
 
 enum {
-  B_FULL = 0, B_EMPTY = kSlots, B_S = 2 * kSlots, B_P, B_O, B_OFREE, B_HREADY, B_OI, B_KT, B_DF,
-  B_G, B_GFREE, B_END, B_COUNT
+  // B_O and B_DF by chunk parity: the loads wait on them too, and may lag a chunk
+  B_FULL = 0, B_S = kSlots, B_P, B_PV, B_O, B_HREADY = B_O + 2, B_HFREE, B_KT, B_DF, B_G = B_DF + 2,
+  B_GFREE, B_END, B_COUNT
 };
 // TMEM columns
 constexpr uint32_t T_S = 0, T_P = 0, T_DF = 128, T_OI = 256, T_O = 384;
@@ -82,7 +82,7 @@ linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ 
 
   if (tid == 0) {
     for (int i = 0; i < B_COUNT; ++i) {
-      const uint32_t count = i == B_P || i == B_OFREE ? 4
+      const uint32_t count = i == B_P ? 4
                              : i == B_HREADY || i == B_KT ? 8
                              : i == B_GFREE ? 12
                                             : 1;
@@ -105,58 +105,71 @@ linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ 
     if (lane == 0) {
       for (int i = 0; i < 3 * chunks; ++i) {
         const int slot = i % kSlots, use = i / kSlots, c = i / 3;
-        if (use > 0 && !mbar_wait(bars + B_EMPTY + slot, (use - 1) & 1)) { *abort = 1; break; }
+        if (use > 0) {  // the slot's last tile has been read: q by Q H, k and v by the state's product
+          const int j = i - kSlots, cj = j / 3;
+          if (!mbar_wait(bars + (j % 3 == 0 ? B_O : B_DF) + (cj & 1), (cj >> 1) & 1)) *abort = 1;
+        }
         if (*abort) break;
-        const CUtensorMap* m = i % 3 == 0 ? &mk : i % 3 == 1 ? &mq : &mv;
-        // the ring holds less than two chunks: a slot comes free late, and its
-        // load must not wait for DRAM
-        if (c + kAhead < chunks)
-          prefetch_tile(m, t0 + (c + kAhead) * C, i % 3 == 2 ? vz : qz,
-                        (i % 3 == 2 ? a.dv : a.dk) > 64);
+        const CUtensorMap* m = i % 3 == 0 ? &mq : i % 3 == 1 ? &mk : &mv;
         load_tile(sb + slot * kTile, m, bars + B_FULL + slot, t0 + c * C, i % 3 == 2 ? vz : qz);
       }
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------- products
-    auto slot = [&](int i) { return i % kSlots; };
-    auto tile = [&](int i) { return sb + (i % kSlots) * kTile; };
-    auto full = [&](int i) { return warp_wait(bars + B_FULL + i % kSlots, (i / kSlots) & 1, abort); };
-    for (int c = 0; c < chunks; ++c) {
-      const uint32_t par = c & 1;
-      const uint32_t K = tile(3 * c), Q = tile(3 * c + 1), V = tile(3 * c + 2);
-      if (!full(3 * c) || !full(3 * c + 1)) break;
-      // P shares the columns of S
-      if (c > 0 && !warp_wait(bars + B_O, (c - 1) & 1, abort)) break;
-      tc_fence_after();
-      if (lane == 0) {
-        mma_ss(tmem + T_S, Q, false, K, false, false);
-        umma_commit(bars + B_S);
+    // One thread, so that nothing but a barrier stands between two products.
+    // S of the next chunk goes ahead of this chunk's contribution to the state:
+    // the warps of P wait for it, while the state has slack.
+    if (lane == 0) {
+      bool ok = true;
+      auto wait = [&](int bar, uint32_t parity) {
+        ok = ok && mbar_wait(bars + bar, parity);
+        return ok;
+      };
+      int sq = 0;          // slot of Q, and how often the ring has come round
+      uint32_t round = 0;
+      for (int c = -1; c < chunks; ++c) {
+        int sk = sq + 1, sv = sq + 2;
+        uint32_t rk = round, rv = round;
+        if (sk >= kSlots) { sk -= kSlots; ++rk; }
+        if (sv >= kSlots) { sv -= kSlots; ++rv; }
+        const uint32_t par = c & 1;
+        if (c >= 0) {
+          wait(B_FULL + sv, rv & 1);
+          if (!wait(B_P, par)) break;  // and o of the last chunk has been read
+          tc_fence_after();
+          mma_ts<true>(tmem + T_O, tmem + T_P, sb + sv * kTile, 0);
+          umma_commit(bars + B_PV);
+          if (!wait(B_HREADY, par)) break;
+          tc_fence_after();
+          mma_ss<false, false>(tmem + T_OI, sb + sq * kTile, sb + kH, 0);
+          umma_commit(bars + B_O + par);
+        }
+        if (c + 1 < chunks) {
+          int nq = c < 0 ? 0 : sv + 1, nk;
+          uint32_t rq = c < 0 ? 0 : rv;
+          if (nq >= kSlots) { nq -= kSlots; ++rq; }
+          nk = nq + 1;
+          wait(B_FULL + nq, rq & 1);
+          wait(B_FULL + (nk < kSlots ? nk : 0), (rq + (nk >= kSlots)) & 1);
+          if (c >= 0) wait(B_PV, par);  // P shares the columns of S
+          if (!ok) break;
+          tc_fence_after();
+          mma_ss<false, false>(tmem + T_S, sb + nq * kTile, sb + (nk < kSlots ? nk : 0) * kTile, 0);
+          umma_commit(bars + B_S);
+        }
+        if (c < 0) continue;
+        if (!wait(B_KT, par)) break;
+        tc_fence_after();
+        mma_ss<true, true>(tmem + T_DF, sb + sv * kTile, sb + sk * kTile, 0);
+        mma_ss<true, true>(tmem + T_DF, sb + sv * kTile, sb + kLo, 1);
+        umma_commit(bars + B_DF + par);
+        sq = sv + 1;
+        round = rv;
+        if (sq >= kSlots) { sq -= kSlots; ++round; }
       }
-      if (!warp_wait(bars + B_HREADY, par, abort)) break;
-      if (c > 0 && !warp_wait(bars + B_OFREE, (c - 1) & 1, abort)) break;
-      tc_fence_after();
-      if (lane == 0) {
-        mma_ss(tmem + T_OI, Q, false, sb + kH, false, false);
-        umma_commit(bars + B_OI);
-      }
-      if (!full(3 * c + 2)) break;
-      if (!warp_wait(bars + B_KT, par, abort)) break;
-      tc_fence_after();
-      if (lane == 0) {
-        mma_ss(tmem + T_DF, V, true, K, true, false);
-        mma_ss(tmem + T_DF, V, true, sb + kLo, true, true);
-        umma_commit(bars + B_DF);
-        umma_commit(bars + B_EMPTY + slot(3 * c));
-      }
-      if (!warp_wait(bars + B_P, par, abort)) break;
-      tc_fence_after();
-      if (lane == 0) {
-        mma_ts(tmem + T_O, tmem + T_P, V, true, false);
-        umma_commit(bars + B_O);
-        umma_commit(bars + B_EMPTY + slot(3 * c + 2));
-      }
+      if (!ok) *abort = 1;
+      umma_commit(bars + B_END);
     }
-    if (lane == 0) umma_commit(bars + B_END);
   } else if (warp == 2) {
     // ------------------------------------------------------------- decays
     const float* g = a.g_head ? a.g + h : a.g + vrow;
@@ -176,7 +189,12 @@ linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ 
     const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16);
     for (int c = 0; c < chunks; ++c) {
       const uint32_t par = c & 1;
-      const int valid = min(len - c * C, C), sq = (3 * c + 1) % kSlots;
+      const int valid = min(len - c * C, C);
+      if (a.cu_seqlens && valid < C) {  // tokens of the next sequence behind this one
+        const int iv = 3 * c + 2;
+        if (!warp_wait(bars + B_FULL + iv % kSlots, (iv / kSlots) & 1, abort)) break;
+        if (i >= valid) zero_row(sm + (iv % kSlots) * kTile, i);
+      }
       if (!warp_wait(bars + B_G, par, abort)) break;
       const float pre = gates->pre[i], into = gates->eL[i];
       if (!warp_wait(bars + B_S, par, abort)) break;
@@ -229,10 +247,10 @@ linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ 
       warp_publish(bars + B_P);
       if (lane == 0) mbar_arrive(bars + B_GFREE);
 
-      if (!warp_wait(bars + B_O, par, abort)) break;
+      if (!warp_wait(bars + B_O + par, (c >> 1) & 1, abort)) break;
       tc_fence_after();
-      // o by way of the query tile's slot, which nothing reads any more
-      char* stage = sm + sq * kTile;
+      // o by way of the state's tile, which nothing reads any more
+      char* stage = sm + kH;
       const float fo = a.scale, fi = a.scale * into;
 #pragma unroll 1
       for (int p = 0; p < 4; ++p) {
@@ -253,7 +271,7 @@ linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ 
               make_uint4(o[0], o[1], o[2], o[3]);
         }
       }
-      warp_arrive(bars + B_OFREE);
+      tc_fence_before();
       fence_proxy_async_smem();
       named_sync(1, 128);
       if (a.cu_seqlens && valid < C) {
@@ -265,11 +283,11 @@ linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ 
             *reinterpret_cast<uint4*>(o + (size_t)row * a.dv + 8 * j) =
                 *reinterpret_cast<const uint4*>(stage + sw128_chunk(128, row, j));
         }
-        named_sync(1, 128);  // (the last chunk of the sequence: nothing reuses the slot)
+        // (the last chunk of the sequence: nothing reuses the tile)
       } else if (i == 0) {
-        store_tile(&mo, sb + sq * kTile, t0 + c * C, vz, a.dv > 64);
+        store_tile(&mo, sb + kH, t0 + c * C, vz, a.dv > 64);
         store_read_wait();  // (this warp has the shortest rows of P)
-        mbar_arrive(bars + B_EMPTY + sq);
+        mbar_arrive(bars + B_HFREE);
       }
     }
   } else if (warp >= 8) {
@@ -285,9 +303,10 @@ linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ 
     bool ok = true;
     for (int c = 0; c < chunks; ++c) {
       const uint32_t par = c & 1;
-      const int ik = 3 * c, valid = min(len - c * C, C);
-      // the state entering the chunk, once the last chunk's queries have read theirs
-      if (c > 0 && !(ok = warp_wait(bars + B_OI, (c - 1) & 1, abort))) break;
+      const int ik = 3 * c + 1, valid = min(len - c * C, C);
+      // the state entering the chunk, once the last chunk's queries have read
+      // theirs and o has left the tile again
+      if (c > 0 && !(ok = warp_wait(bars + B_HFREE, (c - 1) & 1, abort))) break;
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         *reinterpret_cast<uint4*>(sm + kH + sw128_chunk(128, r, 8 * s + j)) =
@@ -302,15 +321,10 @@ linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ 
       if (lane == 0) mbar_arrive(bars + B_GFREE);
       if (!(ok = warp_wait(bars + B_FULL + ik % kSlots, (ik / kSlots) & 1, abort))) break;
       if (!(ok = warp_wait(bars + B_S, par, abort))) break;
-      if (a.cu_seqlens && valid < C) {  // tokens of the next sequence behind this one
-        const int iv = ik + 2;
-        if (!(ok = warp_wait(bars + B_FULL + iv % kSlots, (iv / kSlots) & 1, abort))) break;
-        if (s == 0 && r >= valid) zero_row(sm + (iv % kSlots) * kTile, r);
-      }
       scale_row(sm + (ik % kSlots) * kTile, sm + kLo, r, s, wt, r < valid);
       warp_publish(bars + B_KT);
       // the chunk's contribution
-      if (!(ok = warp_wait(bars + B_DF, par, abort))) break;
+      if (!(ok = warp_wait(bars + B_DF + par, (c >> 1) & 1, abort))) break;
       tc_fence_after();
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
