@@ -69,16 +69,20 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(LinearArgs a, int32_t*
 //   warp 0 loads, warp 1 issues the products, warp 2 makes the decays,
 //   warps 4-7 scale a chunk's keys (queries) in two bf16 parts,
 //   warps 8-15 hold the state: thread (r, s) has its channels 64 s .. + 63 of
-//   value column r in fp32 registers.
+//   value column r in fp32 registers.  They stage the image in shared memory
+//   and one bulk copy writes it (rows written by their own threads would take
+//   an L1 pass for every 16 bytes).
 namespace st {
 constexpr int kThreads = 512;
 constexpr int kSlots = 4;                       // x and y tiles of two chunks
-constexpr uint32_t kLo = kSlots * kTile;        // two lo tiles
-constexpr uint32_t kGates = kLo + 2 * kTile;    // two
-constexpr uint32_t kBars = kGates + 2 * sizeof(Gates);
+constexpr uint32_t kLo = kSlots * kTile;        // lo part of the scaled tile
+constexpr uint32_t kStage = kLo + kTile;        // the image on its way out
+constexpr uint32_t kGates = kStage + kImage;
+constexpr uint32_t kBars = kGates + sizeof(Gates);
 constexpr uint32_t kSmem = kBars + 512;
-enum { B_FULL = 0, B_EMPTY = 4, B_KT = 8, B_DF = 10, B_DFREE = 12, B_G = 14, B_GFREE = 16,
-       B_END = 18, B_COUNT };
+static_assert(kSmem <= 232448, "shared memory of a CTA");
+enum { B_FULL = 0, B_EMPTY = 4, B_KT = 8, B_DF, B_DFREE = B_DF + 2, B_G = B_DFREE + 2, B_GFREE,
+       B_END, B_COUNT };
 }  // namespace st
 
 template <bool BACK>
@@ -113,9 +117,9 @@ linear_state_kernel(const __grid_constant__ LinearArgs a, const __grid_constant_
 
   if (tid == 0) {
     for (int i = 0; i < B_COUNT; ++i)
-      mbar_init(bars + i, i >= B_KT && i < B_KT + 2         ? 4
+      mbar_init(bars + i, i == B_KT                         ? 4
                           : i >= B_DFREE && i < B_DFREE + 2 ? 8
-                          : i >= B_GFREE && i < B_GFREE + 2 ? 12
+                          : i == B_GFREE                    ? 12
                                                             : 1);
     *abort = 0;
     fence_mbar_init();
@@ -140,50 +144,51 @@ linear_state_kernel(const __grid_constant__ LinearArgs a, const __grid_constant_
       }
     }
   } else if (warp == 1) {
-    for (int i = 0; i < steps; ++i) {
-      const int ix = (2 * i) % kSlots, iy = ix + 1, p = i & 1;
-      if (!warp_wait(bars + B_FULL + iy, (i / 2) & 1, abort)) break;
-      if (!warp_wait(bars + B_KT + p, (i / 2) & 1, abort)) break;
-      if (i >= 2 && !warp_wait(bars + B_DFREE + p, (i / 2 - 1) & 1, abort)) break;
-      tc_fence_after();
-      if (lane == 0) {
+    if (lane == 0) {
+      for (int i = 0; i < steps; ++i) {
+        const int ix = (2 * i) % kSlots, iy = ix + 1, p = i & 1;
+        bool ok = mbar_wait(bars + B_FULL + iy, (i / 2) & 1);
+        if (ok && i >= 2) ok = mbar_wait(bars + B_DFREE + p, (i / 2 - 1) & 1);
+        if (!ok || !mbar_wait(bars + B_KT, p)) { *abort = 1; break; }
+        tc_fence_after();
         mma_ss<true, true>(tmem + 128 * p, sb + iy * kTile, sb + ix * kTile, 0);
-        mma_ss<true, true>(tmem + 128 * p, sb + iy * kTile, sb + kLo + p * kTile, 1);
+        mma_ss<true, true>(tmem + 128 * p, sb + iy * kTile, sb + kLo, 1);
         umma_commit(bars + B_DF + p);
         umma_commit(bars + B_EMPTY + ix);
         umma_commit(bars + B_EMPTY + iy);
       }
+      umma_commit(bars + B_END);
     }
-    if (lane == 0) umma_commit(bars + B_END);
   } else if (warp == 2) {
     const float* g = a.g_head ? a.g + h : a.g + vrow;
     const int gs = a.g_head ? 0 : 1;
     for (int i = 0; i < steps; ++i) {
-      const int p = i & 1, c = at(i);
+      const int c = at(i);
       const float4 x = load_decays(g + (size_t)c * C * gs, gs, min(len - c * C, C), lane);
-      if (i >= 2 && !warp_wait(bars + B_GFREE + p, (i / 2 - 1) & 1, abort)) break;
-      make_gates(gates + p, x, lane);
+      if (i >= 1 && !warp_wait(bars + B_GFREE, (i - 1) & 1, abort)) break;
+      make_gates(gates, x, lane);
       __syncwarp();
-      if (lane == 0) mbar_arrive(bars + B_G + p);
+      if (lane == 0) mbar_arrive(bars + B_G);
     }
   } else if (warp >= 4 && warp < 8) {
     const int t = tid - 128;
     for (int i = 0; i < steps; ++i) {
-      const int ix = (2 * i) % kSlots, p = i & 1, valid = min(len - at(i) * C, C);
+      const int ix = (2 * i) % kSlots, valid = min(len - at(i) * C, C);
       const uint32_t par = (i / 2) & 1;
-      if (!warp_wait(bars + B_G + p, par, abort)) break;
-      const float wt = BACK ? a.scale * gates[p].eL[t] : gates[p].w[t];
+      if (!warp_wait(bars + B_G, i & 1, abort)) break;
+      const float wt = BACK ? a.scale * gates->eL[t] : gates->w[t];
       __syncwarp();
-      if (lane == 0) mbar_arrive(bars + B_GFREE + p);
-      if (i >= 2 && !warp_wait(bars + B_DF + p, (i / 2 - 1) & 1, abort)) break;  // lo is free
+      if (lane == 0) mbar_arrive(bars + B_GFREE);
       if (!warp_wait(bars + B_FULL + ix, par, abort)) break;
-      scale_row(sm + ix * kTile, sm + kLo + p * kTile, t, 0, wt, t < valid);
-      scale_row(sm + ix * kTile, sm + kLo + p * kTile, t, 1, wt, t < valid);
       if (a.cu_seqlens && valid < C) {  // tokens of the next sequence behind this one
         if (!warp_wait(bars + B_FULL + ix + 1, par, abort)) break;
         if (t >= valid) zero_row(sm + (ix + 1) * kTile, t);
       }
-      warp_publish(bars + B_KT + p);
+      if (i >= 1 && !warp_wait(bars + B_DF + ((i - 1) & 1), ((i - 1) / 2) & 1, abort)) break;
+#pragma unroll 1
+      for (int p = 0; p < 2; ++p)
+        scale_row(sm + ix * kTile, sm + kLo, t, p, wt, t < valid);
+      warp_publish(bars + B_KT);
     }
   } else if (warp >= 8) {
     const int s = (warp - 8) >> 2, r = (tid - 256) & 127;
@@ -199,10 +204,12 @@ linear_state_kernel(const __grid_constant__ LinearArgs a, const __grid_constant_
     bool ok = true;
     for (int i = 0; i < chunks; ++i) {
       const int p = i & 1, c = at(i);
-      const uint32_t par = (i / 2) & 1;
       // (offsets that are no packing would run past the workspace)
       const size_t slot = min(first + c, (size_t)w.chunks - 1) * a.H + h;
-      char* out = img + slot * kImage;
+      if (i > 0) {  // the last image has left the stage
+        if (tid == 256) store_read_wait();
+        named_sync(1, 256);
+      }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         uint32_t hi[4], lo[4];
@@ -213,16 +220,19 @@ linear_state_kernel(const __grid_constant__ LinearArgs a, const __grid_constant_
           lo[e] = pack_bf162(x - __uint_as_float(hi[e] << 16),
                              y - __uint_as_float(hi[e] & 0xffff0000u));
         }
-        const uint32_t off = sw128_chunk(128, r, 8 * s + j);
-        *reinterpret_cast<uint4*>(out + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(out + kTile + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        char* out = sm + kStage + sw128_chunk(128, r, 8 * s + j);
+        *reinterpret_cast<uint4*>(out) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(out + kTile) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
+      fence_proxy_async_smem();
+      named_sync(1, 256);
+      if (tid == 256) store_bytes(img + slot * kImage, sb + kStage, kImage);
       if (i >= steps) break;
-      if (!(ok = warp_wait(bars + B_G + p, par, abort))) break;
-      const float all = gates[p].all;
+      if (!(ok = warp_wait(bars + B_G, p, abort))) break;
+      const float all = gates->all;
       __syncwarp();
-      if (lane == 0) mbar_arrive(bars + B_GFREE + p);
-      if (!(ok = warp_wait(bars + B_DF + p, par, abort))) break;
+      if (lane == 0) mbar_arrive(bars + B_GFREE);
+      if (!(ok = warp_wait(bars + B_DF + p, (i / 2) & 1, abort))) break;
       tc_fence_after();
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
@@ -235,6 +245,7 @@ linear_state_kernel(const __grid_constant__ LinearArgs a, const __grid_constant_
       }
       warp_arrive(bars + B_DFREE + p);
     }
+    if (tid == 256) store_read_wait();
     if (BACK && ok && a.dh0 && r < a.dv) {
 #pragma unroll
       for (int i = 0; i < 64; ++i) {
@@ -263,14 +274,17 @@ linear_state_kernel(const __grid_constant__ LinearArgs a, const __grid_constant_
 // 128 x 128 x 128: S, dP and their transposes (so that both dS and dS^T, P^T
 // are rows of a thread and go back to TMEM as operands), dO H^T, V G^T and K G
 // in two parts each, dS K, dS^T Q, P^T dO.
-//   warp 0 loads, warp 1 issues the products, warp 2 makes the decays
-//   warps 4-7   A: thread = query row.  dS and the row sums of W; dQ; then dV
-//   warps 8-11  B: thread = key row.  P^T, dS^T and the column sums of W; dK
-//   warps 12-15 C: <H, G>, from the images in L2
+//   warp 0 loads; warp 1 issues the products, each as soon as its operands are
+//   there; warp 2 makes the decays
+//   warps 4-7   A: thread = query row.  dS and the row sums of W; dQ
+//   warps 8-11  B: thread = key row.    dS^T and the column sums of W; dK
+//   warps 12-15 C: thread = key row.    <H, G> from the images; P^T; dV, in two
+//               halves of 64 columns for want of TMEM
 // An accumulator takes the state's part first; its thread scales that row in
 // place and the product inside the chunk is added to it.  A token's own product
 // (W_ii's factors, the largest under strong decay) stays out of the bf16 operands
-// and is added there in fp32.
+// and is added there in fp32.  Results are staged in tiles that are no longer
+// read and stored with TMA.
 namespace gr {
 constexpr int kThreads = 512;
 constexpr uint32_t kQ = 0, kK = kTile, kV = 2 * kTile, kDo = 3 * kTile;
@@ -279,12 +293,12 @@ constexpr uint32_t kGates = 7 * kTile;
 constexpr uint32_t kBars = kGates + sizeof(Gates);
 constexpr uint32_t kSmem = kBars + 512;
 static_assert(kSmem <= 232448, "shared memory of a CTA");
-enum { B_QK, B_VD, B_H, B_GH, B_GL, B_G, B_TAIL, B_A, B_B, B_DSA, B_DSB, B_X1, B_X2, B_X1S, B_X2S,
-       B_DQ, B_DK, B_DQR, B_X3, B_X3S, B_DV, B_COUNT };
-// TMEM columns: S, dP, S^T, dP^T; then dS over S, dS^T behind it, X1 over dP,
-// P^T over S^T, X2 over dP^T
+enum { B_QK, B_VD, B_H, B_GH, B_GL, B_G, B_TAIL, B_A, B_B, B_DSA, B_DSB, B_DSC, B_X1, B_X2, B_X3,
+       B_X1S = B_X3 + 2, B_X2S, B_X3S, B_DQ = B_X3S + 2, B_DK, B_DV, B_HALF = B_DV + 2, B_COUNT };
+// TMEM columns: S, dP, S^T, dP^T; then dS over S and P^T behind it, X1 over dP,
+// X2 over S^T, dS^T over dP^T and X3 (64 columns) behind it
 constexpr uint32_t T_S = 0, T_DP = 128, T_ST = 256, T_DPT = 384;
-constexpr uint32_t T_DS = 0, T_DST = 64, T_X1 = 128, T_PT = 256, T_X2 = 384;
+constexpr uint32_t T_DS = 0, T_PT = 64, T_X1 = 128, T_X2 = 256, T_DST = 384, T_X3 = 448;
 }  // namespace gr
 
 __device__ __forceinline__ void load_image(uint32_t dst, const char* src, uint64_t* bar) {
@@ -295,15 +309,16 @@ __device__ __forceinline__ void load_image(uint32_t dst, const char* src, uint64
       : "memory");
 }
 
-// Scales an accumulator's row in place, adds a multiple of the same row of a
-// bf16 tile, and returns the scaled row's dot product with that of another.
+// Scales columns [32 p0, 32 p1) of an accumulator's row in place, adds a multiple
+// of the same row of a bf16 tile, and returns the scaled row's dot product with
+// that of another.  acc: the TMEM address of column 32 p0.
 static __device__ __noinline__ float scale_acc(uint32_t acc, float f, float m, const char* add,
-                                               const char* tile, int row) {
+                                               const char* tile, int row, int p0, int p1) {
   float dot = 0.f;
 #pragma unroll 1
-  for (int p = 0; p < 4; ++p) {
+  for (int p = p0; p < p1; ++p) {
     uint32_t x[32];
-    tmem_ld32<32>(acc + 32 * p, x);
+    tmem_ld32<32>(acc + 32 * (p - p0), x);
     tmem_ld_wait();
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -321,54 +336,58 @@ static __device__ __noinline__ float scale_acc(uint32_t acc, float f, float m, c
         x[8 * j + 2 * e + 1] = __float_as_uint(fmaf(m, __uint_as_float(t[e] & 0xffff0000u), b));
       }
     }
-    tmem_st32<32>(acc + 32 * p, x);
+    tmem_st32<32>(acc + 32 * (p - p0), x);
   }
   tmem_st_wait();
   return dot;
 }
 
-// A row of an accumulator to memory: bf16, or fp32 partial gradients.
-static __device__ __noinline__ void store_acc(uint32_t acc, __nv_bfloat16* row, float* part,
-                                              int width, bool keep) {
+// The same columns as bf16 into a tile, or (part) as fp32 partial gradients to
+// memory.
+static __device__ __noinline__ void stage_acc(uint32_t acc, char* tile, float* part, int width,
+                                              bool keep, int row, int p0, int p1) {
 #pragma unroll 1
-  for (int p = 0; p < 4; ++p) {
-    if (32 * p >= width) break;
+  for (int p = p0; p < p1; ++p) {
     uint32_t x[32];
-    tmem_ld32<32>(acc + 32 * p, x);
+    tmem_ld32<32>(acc + 32 * (p - p0), x);
     tmem_ld_wait();
+    if (part) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (!keep || 32 * p + 8 * j >= width) break;
-      if (part) {
+      for (int j = 0; j < 8; ++j)
+        if (keep && 32 * p + 4 * j < width)
+          *reinterpret_cast<uint4*>(part + 32 * p + 4 * j) =
+              make_uint4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+      __syncwarp();
+    } else {
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          *reinterpret_cast<uint4*>(part + 32 * p + 8 * j + 4 * e) =
-              make_uint4(x[8 * j + 4 * e], x[8 * j + 4 * e + 1], x[8 * j + 4 * e + 2],
-                         x[8 * j + 4 * e + 3]);
-      } else {
+      for (int j = 0; j < 4; ++j) {
         uint32_t o[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           o[e] = pack_bf162(__uint_as_float(x[8 * j + 2 * e]),
                             __uint_as_float(x[8 * j + 2 * e + 1]));
-        *reinterpret_cast<uint4*>(row + 32 * p + 8 * j) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(tile + sw128_chunk(128, row, 4 * p + j)) =
+            make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
-    __syncwarp();
   }
 }
 
 __global__ void __launch_bounds__(gr::kThreads, 1)
 linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ BwdWs w,
                    const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                   const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo) {
+                   const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo,
+                   const __grid_constant__ CUtensorMap mdq,
+                   const __grid_constant__ CUtensorMap mdk,
+                   const __grid_constant__ CUtensorMap mdv) {
   using namespace gr;
   extern __shared__ __align__(1024) char sm[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kBars);
   Gates* gates = reinterpret_cast<Gates*>(sm + kGates);
   volatile int* abort = reinterpret_cast<volatile int*>(sm + kBars + 400);
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(sm + kBars + 404);
-  float* hg = reinterpret_cast<float*>(sm + kBars + 408);  // <H, G> by warp of C
+  float* hg = reinterpret_cast<float*>(sm + kBars + 408);   // <H, G> by warp of C
+  float* run = reinterpret_cast<float*>(sm + kBars + 424);  // sums by warp of A
   const uint32_t sb = smem_u32(sm);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (sb & 1023u) {
@@ -404,12 +423,10 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
   const bool tail = a.cu_seqlens && valid < C;
 
   if (tid == 0) {
-    for (int i = 0; i < B_COUNT; ++i)
-      mbar_init(bars + i, i == B_TAIL ? 12
-                          : i == B_DSA || i == B_DSB || i == B_X1S || i == B_X2S || i == B_DQR ||
-                                  i == B_X3S
-                              ? 4
-                              : 1);
+    for (int i = 0; i < B_COUNT; ++i) {
+      const bool by_warps = (i >= B_DSA && i <= B_DSC) || (i >= B_X1S && i < B_DQ) || i == B_HALF;
+      mbar_init(bars + i, i == B_TAIL ? 12 : by_warps ? 4 : 1);
+    }
     *abort = 0;
     fence_mbar_init();
   }
@@ -447,62 +464,73 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
       }
     }
   } else if (warp == 1) {
-    do {
-      if (!warp_wait(bars + B_QK, 0, abort)) break;
-      if (!warp_wait(bars + B_VD, 0, abort)) break;
-      if (tail && !warp_wait(bars + B_TAIL, 0, abort)) break;
+    if (lane == 0 && mbar_wait(bars + B_QK, 0) && (!tail || mbar_wait(bars + B_TAIL, 0)) &&
+        mbar_wait(bars + B_VD, 0)) {
       tc_fence_after();
-      if (lane == 0) {
-        mma_ss<false, false>(tmem + T_S, sb + kQ, sb + kK, 0);
-        mma_ss<false, false>(tmem + T_DP, sb + kDo, sb + kV, 0);
-        umma_commit(bars + B_A);
-        mma_ss<false, false>(tmem + T_ST, sb + kK, sb + kQ, 0);
-        mma_ss<false, false>(tmem + T_DPT, sb + kV, sb + kDo, 0);
-        umma_commit(bars + B_B);
+      mma_ss<false, false>(tmem + T_S, sb + kQ, sb + kK, 0);
+      mma_ss<false, false>(tmem + T_DP, sb + kDo, sb + kV, 0);
+      umma_commit(bars + B_A);
+      mma_ss<false, false>(tmem + T_ST, sb + kK, sb + kQ, 0);
+      mma_ss<false, false>(tmem + T_DPT, sb + kV, sb + kDo, 0);
+      umma_commit(bars + B_B);
+      // what is left, by readiness; `done` keeps the order that TMEM asks for
+      enum { X1 = 1, X2H = 2, X2L = 4, X3A = 8, X3B = 16, DQ = 32, DK = 64, DVA = 128, DVB = 256 };
+      uint32_t done = 0;
+      const uint64_t start = globaltimer_ns();
+      auto ready = [&](uint32_t what, uint32_t after, int bar) {
+        if ((done & (what | after)) != after || !mbar_test(bars + bar, 0)) return false;
+        tc_fence_after();
+        done |= what;
+        return true;
+      };
+      bool dsa = false, dsb = false, dsc = false;
+      while (done != 511 && !*abort) {
+        if (!dsa) dsa = mbar_test(bars + B_DSA, 0);
+        if (!dsb) dsb = mbar_test(bars + B_DSB, 0);
+        if (!dsc) dsc = mbar_test(bars + B_DSC, 0);
+        if (dsa && ready(X1, 0, B_H)) {
+          mma_ss<false, true>(tmem + T_X1, sb + kDo, sb + kS0, 0);
+          mma_ss<false, true>(tmem + T_X1, sb + kDo, sb + kS1, 1);
+          umma_commit(bars + B_X1);
+        }
+        if (dsb && dsc && ready(X2H, 0, B_GH))
+          mma_ss<false, true>(tmem + T_X2, sb + kV, sb + kS2, 0);
+        if (ready(X2L, X2H, B_GL)) {
+          mma_ss<false, true>(tmem + T_X2, sb + kV, sb + kS0, 1);
+          umma_commit(bars + B_X2);
+        }
+        if (ready(DQ, X1, B_X1S)) {
+          mma_ts<true>(tmem + T_X1, tmem + T_DS, sb + kK, 1);
+          umma_commit(bars + B_DQ);
+        }
+        if (dsb && ready(X3A, X2L, B_GL)) {
+          mma_ss<false, false, 64>(tmem + T_X3, sb + kK, sb + kS2, 0);
+          mma_ss<false, false, 64>(tmem + T_X3, sb + kK, sb + kS0, 1);
+          umma_commit(bars + B_X3);
+        }
+        if (ready(DK, X2L, B_X2S)) {
+          mma_ts<true>(tmem + T_X2, tmem + T_DST, sb + kQ, 1);
+          umma_commit(bars + B_DK);
+        }
+        if (ready(DVA, X3A, B_X3S)) {
+          mma_ts<true, 64>(tmem + T_X3, tmem + T_PT, sb + kDo, 1);
+          umma_commit(bars + B_DV);
+        }
+        if (ready(X3B, DVA, B_HALF)) {
+          mma_ss<false, false, 64>(tmem + T_X3, sb + kK, sb + kS2 + kPanel / 2, 0);
+          mma_ss<false, false, 64>(tmem + T_X3, sb + kK, sb + kS0 + kPanel / 2, 1);
+          umma_commit(bars + B_X3 + 1);
+        }
+        if (ready(DVB, X3B, B_X3S + 1)) {
+          mma_ts<true, 64>(tmem + T_X3, tmem + T_PT, sb + kDo + kPanel, 1);
+          umma_commit(bars + B_DV + 1);
+        }
+        if (globaltimer_ns() - start > kWaitLimitNs) break;
       }
-      if (!warp_wait(bars + B_H, 0, abort)) break;
-      if (!warp_wait(bars + B_DSA, 0, abort)) break;
-      tc_fence_after();
-      if (lane == 0) {
-        mma_ss<false, true>(tmem + T_X1, sb + kDo, sb + kS0, 0);
-        mma_ss<false, true>(tmem + T_X1, sb + kDo, sb + kS1, 1);
-        umma_commit(bars + B_X1);
-      }
-      if (!warp_wait(bars + B_GH, 0, abort)) break;
-      if (!warp_wait(bars + B_DSB, 0, abort)) break;
-      tc_fence_after();
-      if (lane == 0) mma_ss<false, true>(tmem + T_X2, sb + kV, sb + kS2, 0);
-      if (!warp_wait(bars + B_GL, 0, abort)) break;
-      if (lane == 0) {
-        mma_ss<false, true>(tmem + T_X2, sb + kV, sb + kS0, 1);
-        umma_commit(bars + B_X2);
-      }
-      if (!warp_wait(bars + B_X1S, 0, abort)) break;
-      tc_fence_after();
-      if (lane == 0) {
-        mma_ts<true>(tmem + T_X1, tmem + T_DS, sb + kK, 1);
-        umma_commit(bars + B_DQ);
-      }
-      if (!warp_wait(bars + B_X2S, 0, abort)) break;
-      tc_fence_after();
-      if (lane == 0) {
-        mma_ts<true>(tmem + T_X2, tmem + T_DST, sb + kQ, 1);
-        umma_commit(bars + B_DK);
-      }
-      if (!warp_wait(bars + B_DQR, 0, abort)) break;
-      tc_fence_after();
-      if (lane == 0) {
-        mma_ss<false, false>(tmem + T_X1, sb + kK, sb + kS2, 0);
-        mma_ss<false, false>(tmem + T_X1, sb + kK, sb + kS0, 1);
-        umma_commit(bars + B_X3);
-      }
-      if (!warp_wait(bars + B_X3S, 0, abort)) break;
-      tc_fence_after();
-      if (lane == 0) {
-        mma_ts<true>(tmem + T_X1, tmem + T_PT, sb + kDo, 1);
-        umma_commit(bars + B_DV);
-      }
-    } while (false);
+      if (done != 511) *abort = 1;
+    } else if (lane == 0) {
+      *abort = 1;
+    }
   } else if (warp == 2) {
     const float* g = a.g_head ? a.g + h : a.g + vrow;
     make_gates(gates, load_decays(g, a.g_head ? 0 : 1, valid, lane), lane);
@@ -511,7 +539,18 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
   } else if (warp >= 4) {
     const int wg = (warp - 4) >> 2, wq = warp & 3, row = tid & 127;
     const uint32_t lanes = tmem + ((uint32_t)(32 * wq) << 16);
-    const bool in = row < valid;
+    const bool in = row < valid, lead = row == 0;
+    // a staged result to memory, by its 128 threads
+    auto put = [&](const CUtensorMap* m, void* dst, size_t at, int width, uint32_t tile, int head,
+                   int p0, int p1) {
+      fence_proxy_async_smem();
+      named_sync(1 + wg, 128);
+      if (tail)
+        store_rows(static_cast<__nv_bfloat16*>(dst) + at * width, sm + tile, valid, width, p0, p1,
+                   row);
+      else if (lead && 64 * p0 < width)
+        store_tile(m, sb + tile, y, head, p0, min(p1, (width + 63) / 64));
+    };
     do {
       if (tail) {  // tokens of the next sequence behind this one: out of every sum over tokens
         if (!warp_wait(bars + (wg == 2 ? B_VD : B_QK), 0, abort)) break;
@@ -543,12 +582,11 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
 #pragma unroll
         for (int m = 16; m >= 1; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
         if (lane == 0) hg[wq] = s;
-        break;
       }
       if (!warp_wait(bars + B_G, 0, abort)) break;
       const float pre = gates->pre[row], es = gates->es[row];
       const float into = a.scale * gates->eL[row], out = gates->w[row], s = a.scale;
-      float wsum = 0.f, dot = 0.f, own = 0.f, own_p = 0.f;  // s do_i.v_i, s q_i.k_i
+      float wsum = 0.f, dot = 0.f, own = 0.f;  // own: s do_i.v_i (A, B), s q_i.k_i (C)
       if (wg == 0) {
         // row i: j over blocks up to its own
         if (!warp_wait(bars + B_A, 0, abort)) break;
@@ -591,13 +629,10 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
 #pragma unroll
             for (int z = 0; z < 4; ++z) {
               const int j = 4 * e + z;
-              const float dp = s * __uint_as_float(d[j]), sc = __uint_as_float(x[j]);
+              const float dp = s * __uint_as_float(d[j]);
               v[z] = j < lane ? dp * ex2(pre - gg[z]) : 0.f;
-              if (j < lane) wsum = fmaf(v[z], sc, wsum);
-              if (j == lane) {
-                own = dp;
-                own_p = s * sc;
-              }
+              if (j < lane) wsum = fmaf(v[z], __uint_as_float(x[j]), wsum);
+              if (j == lane) own = dp;
             }
             o[2 * e] = pack_bf162(v[0], v[1]);
             o[2 * e + 1] = pack_bf162(v[2], v[3]);
@@ -612,107 +647,130 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
         warp_arrive(bars + B_DSA);
         if (!warp_wait(bars + B_X1, 0, abort)) break;
         tc_fence_after();
-        dot = scale_acc(lanes + T_X1, into, own, sm + kK, sm + kQ, row);
+        dot = scale_acc(lanes + T_X1, into, own, sm + kK, sm + kQ, row, 0, 4);
         warp_arrive(bars + B_X1S);
         if (!warp_wait(bars + B_DQ, 0, abort)) break;
         tc_fence_after();
-        store_acc(lanes + T_X1, static_cast<__nv_bfloat16*>(a.dq) + (krow + row) * a.dk,
-                  w.dq ? w.dq + (vrow + row) * a.dk : nullptr, a.dk, in);
-        warp_arrive(bars + B_DQR);
-        if (!warp_wait(bars + B_X3, 0, abort)) break;
-        tc_fence_after();
-        scale_acc(lanes + T_X1, out, own_p, sm + kDo, sm + kDo, row);
-        warp_arrive(bars + B_X3S);
-        if (!warp_wait(bars + B_DV, 0, abort)) break;
-        tc_fence_after();
-        store_acc(lanes + T_X1, static_cast<__nv_bfloat16*>(a.dval) + (vrow + row) * a.dv, nullptr,
-                  a.dv, in);
+        // over Hlo's tile
+        stage_acc(lanes + T_X1, sm + kS1, w.dq ? w.dq + (vrow + row) * a.dk : nullptr, a.dk, in,
+                  row, 0, 4);
+        if (!w.dq) put(&mdq, a.dq, krow, a.dk, kS1, qz, 0, 2);
       } else {
-        // row j: i over blocks from its own on
+        // row j: i over blocks from its own on.  B forms dS^T (over dP^T) and the
+        // sums of W, C forms P^T (behind dS, so after A).
+        const bool isb = wg == 1;
+        const uint32_t to = lanes + (isb ? T_DST : T_PT);
         if (!warp_wait(bars + B_B, 0, abort)) break;
-        if (!warp_wait(bars + B_DSA, 0, abort)) break;  // dS^T goes behind dS
+        if (!isb && !warp_wait(bars + B_DSA, 0, abort)) break;
         tc_fence_after();
-        uint32_t o[16], q[16];
+        uint32_t o[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) o[e] = q[e] = 0;
+        for (int e = 0; e < 16; ++e) o[e] = 0;
 #pragma unroll 1
-        for (int p = 0; p < wq; ++p) {
-          tmem_st32<16>(lanes + T_PT + 16 * p, o);
-          tmem_st32<16>(lanes + T_DST + 16 * p, q);
-        }
+        for (int p = 0; p < wq; ++p) tmem_st32<16>(to + 16 * p, o);
         {
           uint32_t x[32], d[32];
           tmem_ld32<32>(lanes + T_ST + 32 * wq, x);
-          tmem_ld32<32>(lanes + T_DPT + 32 * wq, d);
-          tmem_ld_wait();
+          if (isb) {
+            tmem_ld32<32>(lanes + T_DPT + 32 * wq, d);
+            tmem_ld_wait();
+          } else {
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) d[e] = x[e];
+          }
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float4 g = reinterpret_cast<const float4*>(gates->pre + 32 * wq)[e];
             const float gg[4] = {g.x, g.y, g.z, g.w};
-            float u[4], v[4];
+            float v[4];
 #pragma unroll
             for (int z = 0; z < 4; ++z) {
               const int i = 4 * e + z;
-              const float k = s * ex2(gg[z] - pre);
-              u[z] = i > lane ? __uint_as_float(x[i]) * k : 0.f;
-              v[z] = i > lane ? __uint_as_float(d[i]) * k : 0.f;
+              const float dp = s * __uint_as_float(d[i]);
+              v[z] = i > lane ? dp * ex2(gg[z] - pre) : 0.f;
               if (i > lane) wsum = fmaf(v[z], __uint_as_float(x[i]), wsum);
-              if (i == lane) own = s * __uint_as_float(d[i]);
+              if (i == lane) own = dp;
             }
-            o[2 * e] = pack_bf162(u[0], u[1]);
-            o[2 * e + 1] = pack_bf162(u[2], u[3]);
-            q[2 * e] = pack_bf162(v[0], v[1]);
-            q[2 * e + 1] = pack_bf162(v[2], v[3]);
+            o[2 * e] = pack_bf162(v[0], v[1]);
+            o[2 * e + 1] = pack_bf162(v[2], v[3]);
           }
-          tmem_st32<16>(lanes + T_PT + 16 * wq, o);
-          tmem_st32<16>(lanes + T_DST + 16 * wq, q);
+          tmem_st32<16>(to + 16 * wq, o);
         }
 #pragma unroll 1
         for (int p = wq + 1; p < 4; ++p) {
           uint32_t x[32], d[32];
           tmem_ld32<32>(lanes + T_ST + 32 * p, x);
-          tmem_ld32<32>(lanes + T_DPT + 32 * p, d);
           float f = 0.f;
           if (wq < 1 && p > 1) f += gates->tot[1];
           if (wq < 2 && p > 2) f += gates->tot[2];
           f = s * es * ex2(f);
-          tmem_ld_wait();
+          if (isb) {
+            tmem_ld32<32>(lanes + T_DPT + 32 * p, d);
+            tmem_ld_wait();
+          } else {
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) d[e] = x[e];
+          }
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float4 g = reinterpret_cast<const float4*>(gates->pre + 32 * p)[e];
             const float gg[4] = {g.x, g.y, g.z, g.w};
-            float u[4], v[4];
+            float v[4];
 #pragma unroll
             for (int z = 0; z < 4; ++z) {
               const int i = 4 * e + z;
-              const float k = f * ex2(gg[z]);
-              u[z] = __uint_as_float(x[i]) * k;
-              v[z] = __uint_as_float(d[i]) * k;
+              v[z] = __uint_as_float(d[i]) * (f * ex2(gg[z]));
               wsum = fmaf(v[z], __uint_as_float(x[i]), wsum);
             }
-            o[2 * e] = pack_bf162(u[0], u[1]);
-            o[2 * e + 1] = pack_bf162(u[2], u[3]);
-            q[2 * e] = pack_bf162(v[0], v[1]);
-            q[2 * e + 1] = pack_bf162(v[2], v[3]);
+            o[2 * e] = pack_bf162(v[0], v[1]);
+            o[2 * e + 1] = pack_bf162(v[2], v[3]);
           }
-          tmem_st32<16>(lanes + T_PT + 16 * p, o);
-          tmem_st32<16>(lanes + T_DST + 16 * p, q);
+          tmem_st32<16>(to + 16 * p, o);
         }
         tmem_st_wait();
-        warp_arrive(bars + B_DSB);
-        if (!warp_wait(bars + B_X2, 0, abort)) break;
-        tc_fence_after();
-        dot = scale_acc(lanes + T_X2, out, own, sm + kQ, sm + kK, row);
-        warp_arrive(bars + B_X2S);
-        if (!warp_wait(bars + B_DK, 0, abort)) break;
-        tc_fence_after();
-        store_acc(lanes + T_X2, static_cast<__nv_bfloat16*>(a.dkey) + (krow + row) * a.dk,
-                  w.dk ? w.dk + (vrow + row) * a.dk : nullptr, a.dk, in);
+        warp_arrive(bars + (isb ? B_DSB : B_DSC));
+        if (isb) {
+          if (!warp_wait(bars + B_X2, 0, abort)) break;
+          tc_fence_after();
+          dot = scale_acc(lanes + T_X2, out, own, sm + kQ, sm + kK, row, 0, 4);
+          warp_arrive(bars + B_X2S);
+          if (!warp_wait(bars + B_DK, 0, abort)) break;
+          tc_fence_after();
+          // over V's tile: X2 was its last reader
+          stage_acc(lanes + T_X2, sm + kV, w.dk ? w.dk + (vrow + row) * a.dk : nullptr, a.dk, in,
+                    row, 0, 4);
+          if (!w.dk) put(&mdk, a.dkey, krow, a.dk, kV, qz, 0, 2);
+        } else {
+          bool ok = true;
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            if (!(ok = warp_wait(bars + B_X3 + half, 0, abort))) break;
+            tc_fence_after();
+            scale_acc(lanes + T_X3, out, own, sm + kDo, sm + kDo, row, 2 * half, 2 * half + 2);
+            warp_arrive(bars + B_X3S + half);
+            if (!(ok = warp_wait(bars + B_DV + half, 0, abort))) break;
+            tc_fence_after();
+            // over this panel of dO, which this half's product was the last to read,
+            // but for dO H^T
+            if (!(ok = warp_wait(bars + B_X1, 0, abort))) break;
+            stage_acc(lanes + T_X3, sm + kDo, nullptr, a.dv, in, row, 2 * half, 2 * half + 2);
+            if (half == 0) warp_arrive(bars + B_HALF);
+            put(&mdv, a.dval, vrow, a.dv, kDo, vz, half, half + 1);
+          }
+          if (!ok) break;
+        }
       }
-      // dg's sums: by token in shared memory, over the tile of Hlo
-      float* part = reinterpret_cast<float*>(sm + kS1) + 256 * wg;
-      part[row] = in ? wsum : 0.f;
-      part[128 + row] = in ? dot : 0.f;
+      if (lead) store_read_wait();
+      // dg's sums by token, over the decays once all three are done with them
+      if (wg != 2) {
+        if (!warp_wait(bars + B_DSA, 0, abort) || !warp_wait(bars + B_DSB, 0, abort) ||
+            !warp_wait(bars + B_DSC, 0, abort))
+          break;
+        (wg == 0 ? gates->pre : gates->eL)[row] = in ? wsum : 0.f;
+        (wg == 0 ? gates->es : gates->w)[row] = in ? dot : 0.f;
+      }
     } while (false);
   }
 
@@ -720,10 +778,8 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
   __syncthreads();
   if (warp >= 4 && warp < 8 && !*abort) {
     // dg_t = e^{L_C} <H, G> + sum_{j<t} kd_j + sum_{i>=t} (qd_i + row_i - col_i)
-    const float* part = reinterpret_cast<const float*>(sm + kS1);
-    float* run = reinterpret_cast<float*>(sm + kS1) + 512;
     const int t = tid & 127, wq = warp & 3;
-    float fwd = part[384 + t], back = part[128 + t] + part[t] - part[256 + t];
+    float fwd = gates->w[t], back = gates->es[t] + gates->pre[t] - gates->eL[t];
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
       const float x = __shfl_up_sync(0xffffffffu, fwd, m), z = __shfl_down_sync(0xffffffffu, back, m);
@@ -743,7 +799,7 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
   if (tid == 0 && *abort) {
     // let copies and products in flight land before the memory is given back
     set_status(a.status, CKDA_ERR_TIMEOUT);
-    const int land[] = {B_QK, B_VD, B_H, B_GH, B_GL, B_B, B_X1, B_X2, B_DQ, B_DK, B_X3, B_DV};
+    const int land[] = {B_QK, B_VD, B_H, B_GH, B_GL, B_B, B_X1, B_X2, B_DQ, B_DK, B_DV, B_DV + 1};
     for (int i : land) mbar_wait(bars + i, 0, 1u << 12, 1000u);
   }
   __syncthreads();
@@ -788,11 +844,14 @@ cudaError_t linear_chunk_bwd(const LinearArgs& a, char* ws, cudaStream_t s) {
   w.dk = a.Hk == a.H ? nullptr : reinterpret_cast<float*>(ws + p.dk);
   w.chunks = (int)p.chunks;
   cudaError_t e = cudaSuccess;
-  CUtensorMap mq{}, mk{}, mv{}, mo{};
+  CUtensorMap mq{}, mk{}, mv{}, mo{}, mdq{}, mdk{}, mdv{};
   if (a.T > 0 && (!linear_map(&mq, a.q, (uint64_t)a.B * a.Hk, a.T, a.dk) ||
                   !linear_map(&mk, a.k, (uint64_t)a.B * a.Hk, a.T, a.dk) ||
                   !linear_map(&mv, a.v, (uint64_t)a.B * a.H, a.T, a.dv) ||
-                  !linear_map(&mo, a.dout, (uint64_t)a.B * a.H, a.T, a.dv)))
+                  !linear_map(&mo, a.dout, (uint64_t)a.B * a.H, a.T, a.dv) ||
+                  !linear_map(&mdq, a.dq, (uint64_t)a.B * a.Hk, a.T, a.dk) ||
+                  !linear_map(&mdk, a.dkey, (uint64_t)a.B * a.Hk, a.T, a.dk) ||
+                  !linear_map(&mdv, a.dval, (uint64_t)a.B * a.H, a.T, a.dv)))
     return cudaErrorInvalidValue;
   if (a.cu_seqlens) {
     w.first = reinterpret_cast<int32_t*>(ws + p.first);
@@ -813,8 +872,8 @@ cudaError_t linear_chunk_bwd(const LinearArgs& a, char* ws, cudaStream_t s) {
   linear_state_kernel<true><<<units, st::kThreads, st::kSmem, s>>>(a, w, mq, mo);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (a.T > 0) {
-    linear_grad_kernel<<<(unsigned)(p.chunks * a.H), gr::kThreads, gr::kSmem, s>>>(a, w, mq, mk, mv,
-                                                                                 mo);
+    linear_grad_kernel<<<(unsigned)(p.chunks * a.H), gr::kThreads, gr::kSmem, s>>>(
+        a, w, mq, mk, mv, mo, mdq, mdk, mdv);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (w.dq && (e = linear_sum_heads(a, w.dq, w.dk, nullptr, s)) != cudaSuccess) return e;
   }

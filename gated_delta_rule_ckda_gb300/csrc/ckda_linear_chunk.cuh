@@ -39,16 +39,35 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, 
   tma_load_3d(dst + kPanel, map, bar, 64, token, head);
 }
 
-// Both panels of a tile to memory; rows past T and channels past the width are
-// not written.
+// Panels [p0, p1) of a tile to memory; rows past T and channels past the width
+// are not written.
 __device__ __forceinline__ void store_tile(const CUtensorMap* map, uint32_t src, int32_t token,
-                                           int32_t head, bool second) {
-  for (int p = 0; p < (second ? 2 : 1); ++p)
+                                           int32_t head, int p0, int p1) {
+  for (int p = p0; p < p1; ++p)
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
                      reinterpret_cast<uint64_t>(map)),
                  "r"(src + p * kPanel), "r"(64 * p), "r"(token), "r"(head)
                  : "memory");
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// `bytes` of shared memory to memory, both 16-byte aligned.
+__device__ __forceinline__ void store_bytes(char* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src),
+               "r"(bytes)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// The first `valid` rows of panels [p0, p1) of a staged tile to memory by 128
+// threads (t), 16 bytes a lane: where the rows behind belong to another sequence.
+__device__ __forceinline__ void store_rows(__nv_bfloat16* dst, const char* tile, int valid,
+                                           int width, int p0, int p1, int t) {
+  const int per = 8 * (p1 - p0);
+  for (int e = t; e < per * valid; e += 128) {
+    const int row = e / per, j = 8 * p0 + e % per;
+    if (8 * j < width)
+      *reinterpret_cast<uint4*>(dst + (size_t)row * width + 8 * j) =
+          *reinterpret_cast<const uint4*>(tile + sw128_chunk(128, row, j));
+  }
 }
 // This thread's stores have read their shared memory.
 __device__ __forceinline__ void store_read_wait() {
@@ -71,7 +90,7 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// 128 x 128 products over K = 128, bf16 operands, issued by one thread.  AMN,
+// 128 x N products over K = 128, bf16 operands, issued by one thread.  AMN,
 // BMN: the operand is stored with its K index along the rows.  One copy of the
 // issue code for each pair of layouts, out of line (see the note on short loops
 // below), with the descriptors' steps as constants: one that is looked up costs
@@ -86,22 +105,22 @@ template <bool MN>
 __device__ __forceinline__ uint64_t desc_step(int k) {
   return MN ? 128u * k : 1024u * (k >> 2) + 2u * (k & 3);
 }
-template <bool AMN, bool BMN>
+template <bool AMN, bool BMN, int N = 128>
 static __device__ __noinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t accumulate) {
   const uint64_t da = tile_desc<AMN>(a), db = tile_desc<BMN>(b);
-  umma_ss(d, da, db, idesc_f16(128, 128, 1, AMN, BMN), accumulate);
+  umma_ss(d, da, db, idesc_f16(128, N, 1, AMN, BMN), accumulate);
 #pragma unroll
   for (int k = 1; k < 8; ++k)
-    umma_ss(d, da + desc_step<AMN>(k), db + desc_step<BMN>(k), idesc_f16(128, 128, 1, AMN, BMN), 1);
+    umma_ss(d, da + desc_step<AMN>(k), db + desc_step<BMN>(k), idesc_f16(128, N, 1, AMN, BMN), 1);
 }
-template <bool BMN>
+template <bool BMN, int N = 128>
 static __device__ __noinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b,
                                            uint32_t accumulate) {
   const uint64_t db = tile_desc<BMN>(b);
-  umma_ts(d, a_tmem, db, idesc_f16(128, 128, 1, 0, BMN), accumulate);
+  umma_ts(d, a_tmem, db, idesc_f16(128, N, 1, 0, BMN), accumulate);
 #pragma unroll
   for (int k = 1; k < 8; ++k)
-    umma_ts(d, a_tmem + 8 * k, db + desc_step<BMN>(k), idesc_f16(128, 128, 1, 0, BMN), 1);
+    umma_ts(d, a_tmem + 8 * k, db + desc_step<BMN>(k), idesc_f16(128, N, 1, 0, BMN), 1);
 }
 
 // ----------------------------------------------------------------- waiting
@@ -116,6 +135,17 @@ static __device__ __noinline__ bool warp_wait_on(uint64_t* bar, uint32_t parity,
   }
   *abort = 1;
   return false;
+}
+// One thread's look at a barrier, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity, 1000000u))) return true;

@@ -275,17 +275,11 @@ linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ 
       fence_proxy_async_smem();
       named_sync(1, 128);
       if (a.cu_seqlens && valid < C) {
-        // the rows behind belong to the next sequence: 16 lanes to a row of this one
-        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + (vrow + (size_t)c * C) * a.dv;
-        for (int e = i; e < 16 * valid; e += 128) {
-          const int row = e >> 4, j = e & 15;
-          if (8 * j < a.dv)
-            *reinterpret_cast<uint4*>(o + (size_t)row * a.dv + 8 * j) =
-                *reinterpret_cast<const uint4*>(stage + sw128_chunk(128, row, j));
-        }
+        store_rows(static_cast<__nv_bfloat16*>(a.o) + (vrow + (size_t)c * C) * a.dv, stage, valid,
+                   a.dv, 0, 2, i);
         // (the last chunk of the sequence: nothing reuses the tile)
       } else if (i == 0) {
-        store_tile(&mo, sb + kH, t0 + c * C, vz, a.dv > 64);
+        store_tile(&mo, sb + kH, t0 + c * C, vz, 0, a.dv > 64 ? 2 : 1);
         store_read_wait();  // (this warp has the shortest rows of P)
         mbar_arrive(bars + B_HFREE);
       }
