@@ -276,10 +276,10 @@ linear_state_kernel(const __grid_constant__ LinearArgs a, const __grid_constant_
 // in two parts each, dS K, dS^T Q, P^T dO.
 //   warp 0 loads; warp 1 issues the products, each as soon as its operands are
 //   there; warp 2 makes the decays
-//   warps 4-7   A: thread = query row.  dS and the row sums of W; dQ
+//   warps 4-7   A: thread = query row.  dS and the row sums of W; dQ; then the
+//               second 64 columns of dV, where dQ was
 //   warps 8-11  B: thread = key row.    dS^T and the column sums of W; dK
-//   warps 12-15 C: thread = key row.    <H, G> from the images; P^T; dV, in two
-//               halves of 64 columns for want of TMEM
+//   warps 12-15 C: thread = key row.    <H, G>; P^T; the first 64 columns of dV
 // An accumulator takes the state's part first; its thread scales that row in
 // place and the product inside the chunk is added to it.  A token's own product
 // (W_ii's factors, the largest under strong decay) stays out of the bf16 operands
@@ -288,18 +288,53 @@ linear_state_kernel(const __grid_constant__ LinearArgs a, const __grid_constant_
 namespace gr {
 constexpr int kThreads = 512;
 constexpr uint32_t kQ = 0, kK = kTile, kV = 2 * kTile, kDo = 3 * kTile;
-constexpr uint32_t kS0 = 4 * kTile, kS1 = 5 * kTile, kS2 = 6 * kTile;  // Hhi then Glo, Hlo, Ghi
+constexpr uint32_t kS0 = 4 * kTile, kS1 = 5 * kTile, kS2 = 6 * kTile;  // Hhi; Hlo, then Glo; Ghi
 constexpr uint32_t kGates = 7 * kTile;
 constexpr uint32_t kBars = kGates + sizeof(Gates);
 constexpr uint32_t kSmem = kBars + 512;
 static_assert(kSmem <= 232448, "shared memory of a CTA");
 enum { B_QK, B_VD, B_H, B_GH, B_GL, B_G, B_TAIL, B_A, B_B, B_DSA, B_DSB, B_DSC, B_X1, B_X2, B_X3,
-       B_X1S = B_X3 + 2, B_X2S, B_X3S, B_DQ = B_X3S + 2, B_DK, B_DV, B_HALF = B_DV + 2, B_COUNT };
+       B_X1S = B_X3 + 2, B_X2S, B_X3S, B_DQ = B_X3S + 2, B_DK, B_DV, B_DQR = B_DV + 2, B_HG, B_COUNT = B_HG + 2 };
 // TMEM columns: S, dP, S^T, dP^T; then dS over S and P^T behind it, X1 over dP,
 // X2 over S^T, dS^T over dP^T and X3 (64 columns) behind it
 constexpr uint32_t T_S = 0, T_DP = 128, T_ST = 256, T_DPT = 384;
 constexpr uint32_t T_DS = 0, T_PT = 64, T_X1 = 128, T_X2 = 256, T_DST = 384, T_X3 = 448;
 }  // namespace gr
+
+// Chunk and head of a block.
+struct Chunk {
+  int h, valid;     // head; tokens (none: no such chunk)
+  int y, qz, vz;    // first token, rows of the key and value heads
+};
+__device__ __forceinline__ Chunk chunk_of(const LinearArgs& a, const BwdWs& w, unsigned block) {
+  Chunk u;
+  const int ci = block / a.H;
+  u.h = block % a.H;
+  u.valid = 0;
+  int n, c;
+  if (w.first) {
+    if (ci >= w.first[a.N]) return u;
+    int lo = 0, hi = a.N;  // first[lo] <= ci < first[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (w.first[mid] <= ci) lo = mid; else hi = mid;
+    }
+    n = lo;
+    c = ci - w.first[n];
+  } else {
+    const int per = (a.T + C - 1) / C;
+    n = ci / per;
+    c = ci % per;
+  }
+  int t0, len;
+  seq_range(a, n, t0, len);
+  const int b = a.cu_seqlens ? 0 : n;
+  u.valid = min(len - c * C, C);
+  u.y = t0 + c * C;
+  u.qz = b * a.Hk + u.h / (a.H / a.Hk);
+  u.vz = b * a.H + u.h;
+  return u;
+}
 
 __device__ __forceinline__ void load_image(uint32_t dst, const char* src, uint64_t* bar) {
   asm volatile(
@@ -307,6 +342,22 @@ __device__ __forceinline__ void load_image(uint32_t dst, const char* src, uint64
           dst),
       "l"(src), "r"(kTile), "r"(smem_u32(bar))
       : "memory");
+}
+
+// A 128th of the elementwise product of two tiles, summed.
+static __device__ __noinline__ float tile_dot(const char* a, const char* b, int t) {
+  float s0 = 0.f, s1 = 0.f;
+#pragma unroll 4
+  for (int i = t; i < (int)kTile / 16; i += 128) {
+    const uint4 u = reinterpret_cast<const uint4*>(a)[i], v = reinterpret_cast<const uint4*>(b)[i];
+    const uint32_t x[4] = {u.x, u.y, u.z, u.w}, y[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      s0 = fmaf(__uint_as_float(x[e] << 16), __uint_as_float(y[e] << 16), s0);
+      s1 = fmaf(__uint_as_float(x[e] & 0xffff0000u), __uint_as_float(y[e] & 0xffff0000u), s1);
+    }
+  }
+  return s0 + s1;
 }
 
 // Scales columns [32 p0, 32 p1) of an accumulator's row in place, adds a multiple
@@ -394,37 +445,18 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
     if (tid == 0) set_status(a.status, CKDA_ERR_CUDA);
     return;
   }
-  const int ci = blockIdx.x / a.H, h = blockIdx.x % a.H;
-  int n, c;
-  if (w.first) {
-    if (ci >= w.first[a.N]) return;  // the grid is a bound
-    int lo = 0, hi = a.N;            // first[lo] <= ci < first[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (w.first[mid] <= ci) lo = mid; else hi = mid;
-    }
-    n = lo;
-    c = ci - w.first[n];
-  } else {
-    const int per = (a.T + C - 1) / C;
-    n = ci / per;
-    c = ci % per;
-  }
-  const int b = a.cu_seqlens ? 0 : n, hk = h / (a.H / a.Hk);
-  int t0, len;
-  seq_range(a, n, t0, len);
-  const int valid = min(len - c * C, C);
-  if (valid <= 0) return;
-  const int y = t0 + c * C, qz = b * a.Hk + hk, vz = b * a.H + h;
+  const Chunk u = chunk_of(a, w, blockIdx.x);
+  if (u.valid <= 0) return;  // the grid is a bound
+  const int h = u.h, valid = u.valid, y = u.y, qz = u.qz, vz = u.vz;
   const size_t vrow = (size_t)vz * a.T + y;
   const size_t krow = (size_t)qz * a.T + y;
-  const char* himg = w.himg + ((size_t)ci * a.H + h) * kImage;
-  const char* gimg = w.gimg + ((size_t)ci * a.H + h) * kImage;
+  const char* himg = w.himg + (size_t)blockIdx.x * kImage;
+  const char* gimg = w.gimg + (size_t)blockIdx.x * kImage;
   const bool tail = a.cu_seqlens && valid < C;
 
   if (tid == 0) {
     for (int i = 0; i < B_COUNT; ++i) {
-      const bool by_warps = (i >= B_DSA && i <= B_DSC) || (i >= B_X1S && i < B_DQ) || i == B_HALF;
+      const bool by_warps = (i >= B_DSA && i <= B_DSC) || (i >= B_X1S && i < B_DQ) || i >= B_DQR;
       mbar_init(bars + i, i == B_TAIL ? 12 : by_warps ? 4 : 1);
     }
     *abort = 0;
@@ -456,9 +488,23 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
       load_image(sb + kS1, himg + kTile, bars + B_H);
       mbar_arrive_expect_tx(bars + B_GH, kTile);
       load_image(sb + kS2, gimg, bars + B_GH);
-      if (mbar_wait(bars + B_X1, 0)) {  // dO H^T is done with Hhi
+      // What the next block on this SM will read, into L2 while this one works:
+      // the SMs run in step, and without it HBM idles while they compute.
+      const unsigned next = blockIdx.x + kLinSms;
+      if (next < gridDim.x) {
+        const Chunk v = chunk_of(a, w, next);
+        if (v.valid > 0) {
+          prefetch_tile(&mq, v.y, v.qz, a.dk);
+          prefetch_tile(&mk, v.y, v.qz, a.dk);
+          prefetch_tile(&mv, v.y, v.vz, a.dv);
+          prefetch_tile(&mo, v.y, v.vz, a.dv);
+          prefetch_bytes(w.himg + (size_t)next * kImage, kImage);
+          prefetch_bytes(w.gimg + (size_t)next * kImage, kImage);
+        }
+      }
+      if (mbar_wait(bars + B_X1, 0) && mbar_wait(bars + B_HG, 0)) {  // Hlo has been read
         mbar_arrive_expect_tx(bars + B_GL, kTile);
-        load_image(sb + kS0, gimg + kTile, bars + B_GL);
+        load_image(sb + kS1, gimg + kTile, bars + B_GL);
       } else {
         *abort = 1;
       }
@@ -496,7 +542,7 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
         if (dsb && dsc && ready(X2H, 0, B_GH))
           mma_ss<false, true>(tmem + T_X2, sb + kV, sb + kS2, 0);
         if (ready(X2L, X2H, B_GL)) {
-          mma_ss<false, true>(tmem + T_X2, sb + kV, sb + kS0, 1);
+          mma_ss<false, true>(tmem + T_X2, sb + kV, sb + kS1, 1);
           umma_commit(bars + B_X2);
         }
         if (ready(DQ, X1, B_X1S)) {
@@ -505,7 +551,7 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
         }
         if (dsb && ready(X3A, X2L, B_GL)) {
           mma_ss<false, false, 64>(tmem + T_X3, sb + kK, sb + kS2, 0);
-          mma_ss<false, false, 64>(tmem + T_X3, sb + kK, sb + kS0, 1);
+          mma_ss<false, false, 64>(tmem + T_X3, sb + kK, sb + kS1, 1);
           umma_commit(bars + B_X3);
         }
         if (ready(DK, X2L, B_X2S)) {
@@ -516,13 +562,13 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
           mma_ts<true, 64>(tmem + T_X3, tmem + T_PT, sb + kDo, 1);
           umma_commit(bars + B_DV);
         }
-        if (ready(X3B, DVA, B_HALF)) {
-          mma_ss<false, false, 64>(tmem + T_X3, sb + kK, sb + kS2 + kPanel / 2, 0);
-          mma_ss<false, false, 64>(tmem + T_X3, sb + kK, sb + kS0 + kPanel / 2, 1);
+        if (ready(X3B, X2L, B_DQR)) {  // dQ has left its columns
+          mma_ss<false, false, 64>(tmem + T_X1, sb + kK, sb + kS2 + kPanel / 2, 0);
+          mma_ss<false, false, 64>(tmem + T_X1, sb + kK, sb + kS1 + kPanel / 2, 1);
           umma_commit(bars + B_X3 + 1);
         }
-        if (ready(DVB, X3B, B_X3S + 1)) {
-          mma_ts<true, 64>(tmem + T_X3, tmem + T_PT, sb + kDo + kPanel, 1);
+        if (dsc && ready(DVB, X3B, B_X3S + 1)) {
+          mma_ts<true, 64>(tmem + T_X1, tmem + T_PT, sb + kDo + kPanel, 1);
           umma_commit(bars + B_DV + 1);
         }
         if (globaltimer_ns() - start > kWaitLimitNs) break;
@@ -557,36 +603,20 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
         if (!in) zero_row(sm + (wg == 0 ? kQ : wg == 1 ? kK : kDo), row);
         warp_publish(bars + B_TAIL);
       }
+      float hgsum = 0.f;
       if (wg == 2) {
-        // <H, G> from both parts of both images
-        float s = 0.f;
-#pragma unroll 2
-        for (int i = row; i < (int)kTile / 16; i += 128) {
-          const uint4 v[4] = {reinterpret_cast<const uint4*>(himg)[i],
-                              reinterpret_cast<const uint4*>(himg + kTile)[i],
-                              reinterpret_cast<const uint4*>(gimg)[i],
-                              reinterpret_cast<const uint4*>(gimg + kTile)[i]};
-          const uint32_t* t = reinterpret_cast<const uint32_t*>(v);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float x0 = __uint_as_float(t[e] << 16) + __uint_as_float(t[4 + e] << 16);
-            const float y0 = __uint_as_float(t[8 + e] << 16) + __uint_as_float(t[12 + e] << 16);
-            const float x1 = __uint_as_float(t[e] & 0xffff0000u) +
-                             __uint_as_float(t[4 + e] & 0xffff0000u);
-            const float y1 = __uint_as_float(t[8 + e] & 0xffff0000u) +
-                             __uint_as_float(t[12 + e] & 0xffff0000u);
-            s = fmaf(x0, y0, s);
-            s = fmaf(x1, y1, s);
-          }
-        }
-#pragma unroll
-        for (int m = 16; m >= 1; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-        if (lane == 0) hg[wq] = s;
+        // <H, G>, first (Hhi + Hlo, Ghi); (Hhi, Glo) follows when Glo has come
+        // (plain loads of it from memory arrived thousands of cycles later than
+        // the tiles).  (Hlo, Glo) is 2^-18 of the rest and left out.
+        if (!warp_wait(bars + B_H, 0, abort) || !warp_wait(bars + B_GH, 0, abort)) break;
+        hgsum = tile_dot(sm + kS0, sm + kS2, row) + tile_dot(sm + kS1, sm + kS2, row);
+        warp_arrive(bars + B_HG);
       }
       if (!warp_wait(bars + B_G, 0, abort)) break;
       const float pre = gates->pre[row], es = gates->es[row];
       const float into = a.scale * gates->eL[row], out = gates->w[row], s = a.scale;
-      float wsum = 0.f, dot = 0.f, own = 0.f;  // own: s do_i.v_i (A, B), s q_i.k_i (C)
+      // own, own_p: s do_i.v_i (A, B) and s q_i.k_i (A; C has it in own)
+      float wsum = 0.f, dot = 0.f, own = 0.f, own_p = 0.f;
       if (wg == 0) {
         // row i: j over blocks up to its own
         if (!warp_wait(bars + B_A, 0, abort)) break;
@@ -632,7 +662,10 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
               const float dp = s * __uint_as_float(d[j]);
               v[z] = j < lane ? dp * ex2(pre - gg[z]) : 0.f;
               if (j < lane) wsum = fmaf(v[z], __uint_as_float(x[j]), wsum);
-              if (j == lane) own = dp;
+              if (j == lane) {
+                own = dp;
+                own_p = s * __uint_as_float(x[j]);
+              }
             }
             o[2 * e] = pack_bf162(v[0], v[1]);
             o[2 * e + 1] = pack_bf162(v[2], v[3]);
@@ -651,10 +684,11 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
         warp_arrive(bars + B_X1S);
         if (!warp_wait(bars + B_DQ, 0, abort)) break;
         tc_fence_after();
-        // over Hlo's tile
-        stage_acc(lanes + T_X1, sm + kS1, w.dq ? w.dq + (vrow + row) * a.dk : nullptr, a.dk, in,
+        // over Hhi's tile
+        if (!warp_wait(bars + B_HG + 1, 0, abort)) break;
+        stage_acc(lanes + T_X1, sm + kS0, w.dq ? w.dq + (vrow + row) * a.dk : nullptr, a.dk, in,
                   row, 0, 4);
-        if (!w.dq) put(&mdq, a.dq, krow, a.dk, kS1, qz, 0, 2);
+        if (!w.dq) put(&mdq, a.dq, krow, a.dk, kS0, qz, 0, 2);
       } else {
         // row j: i over blocks from its own on.  B forms dS^T (over dP^T) and the
         // sums of W, C forms P^T (behind dS, so after A).
@@ -743,24 +777,30 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
                     row, 0, 4);
           if (!w.dk) put(&mdk, a.dkey, krow, a.dk, kV, qz, 0, 2);
         } else {
-          bool ok = true;
-#pragma unroll 1
-          for (int half = 0; half < 2; ++half) {
-            if (!(ok = warp_wait(bars + B_X3 + half, 0, abort))) break;
-            tc_fence_after();
-            scale_acc(lanes + T_X3, out, own, sm + kDo, sm + kDo, row, 2 * half, 2 * half + 2);
-            warp_arrive(bars + B_X3S + half);
-            if (!(ok = warp_wait(bars + B_DV + half, 0, abort))) break;
-            tc_fence_after();
-            // over this panel of dO, which this half's product was the last to read,
-            // but for dO H^T
-            if (!(ok = warp_wait(bars + B_X1, 0, abort))) break;
-            stage_acc(lanes + T_X3, sm + kDo, nullptr, a.dv, in, row, 2 * half, 2 * half + 2);
-            if (half == 0) warp_arrive(bars + B_HALF);
-            put(&mdv, a.dval, vrow, a.dv, kDo, vz, half, half + 1);
-          }
-          if (!ok) break;
+          own_p = own;
+          if (!warp_wait(bars + B_GL, 0, abort)) break;
+          hgsum += tile_dot(sm + kS0, sm + kS1, row);
+          warp_arrive(bars + B_HG + 1);
+#pragma unroll
+          for (int m = 16; m >= 1; m >>= 1) hgsum += __shfl_xor_sync(0xffffffffu, hgsum, m);
+          if (lane == 0) hg[wq] = hgsum;
         }
+      }
+      if (wg != 1) {
+        // dV: C the first panel, A the second
+        const int half = wg == 0 ? 1 : 0;
+        const uint32_t acc = lanes + (half ? T_X1 : T_X3);
+        if (half) warp_arrive(bars + B_DQR);
+        if (!warp_wait(bars + B_X3 + half, 0, abort)) break;
+        tc_fence_after();
+        scale_acc(acc, out, own_p, sm + kDo, sm + kDo, row, 2 * half, 2 * half + 2);
+        warp_arrive(bars + B_X3S + half);
+        if (!warp_wait(bars + B_DV + half, 0, abort)) break;
+        tc_fence_after();
+        // over this panel of dO: its readers were this product and dO H^T
+        if (!warp_wait(bars + B_X1, 0, abort)) break;
+        stage_acc(acc, sm + kDo, nullptr, a.dv, in, row, 2 * half, 2 * half + 2);
+        put(&mdv, a.dval, vrow, a.dv, kDo, vz, half, half + 1);
       }
       if (lead) store_read_wait();
       // dg's sums by token, over the decays once all three are done with them

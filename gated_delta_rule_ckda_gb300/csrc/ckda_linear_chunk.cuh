@@ -39,6 +39,18 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, 
   tma_load_3d(dst + kPanel, map, bar, 64, token, head);
 }
 
+// The same tile, and `bytes` of memory, into L2 only.
+__device__ __forceinline__ void prefetch_tile(const CUtensorMap* map, int32_t token, int32_t head,
+                                              int width) {
+  for (int x = 0; x < width; x += 64)
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(token), "r"(head)
+                 : "memory");
+}
+__device__ __forceinline__ void prefetch_bytes(const char* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
 // Panels [p0, p1) of a tile to memory; rows past T and channels past the width
 // are not written.
 __device__ __forceinline__ void store_tile(const CUtensorMap* map, uint32_t src, int32_t token,
