@@ -270,16 +270,20 @@ linear_state_kernel(const __grid_constant__ LinearArgs a, const __grid_constant_
 }
 
 // ------------------------------------------------------ gradients of a chunk
-// A CTA of 512 threads takes one chunk of one (sequence, head).  Products, each
-// 128 x 128 x 128: S, dP and their transposes (so that both dS and dS^T, P^T
+// A CTA of 512 threads takes chunk after chunk of all (sequence, head)s, one CTA
+// an SM (a fresh CTA for each chunk cost 7 k cycles of 32 k between two of them),
+// with the next chunk's loads and first products under the last results of this
+// one.  Products, each 128 x 128 x 128: S, dP and their transposes (so that both dS and dS^T, P^T
 // are rows of a thread and go back to TMEM as operands), dO H^T, V G^T and K G
 // in two parts each, dS K, dS^T Q, P^T dO.
 //   warp 0 loads; warp 1 issues the products, each as soon as its operands are
 //   there; warp 2 makes the decays
-//   warps 4-7   A: thread = query row.  dS and the row sums of W; dQ; then the
-//               second 64 columns of dV, where dQ was
+//   warps 4-7   A: thread = query row.  dS and the row sums of W; dQ
 //   warps 8-11  B: thread = key row.    dS^T and the column sums of W; dK
-//   warps 12-15 C: thread = key row.    <H, G>; P^T; the first 64 columns of dV
+//   warps 12-15 C: thread = key row.    <H, G>; P^T; dV, in two halves of 64
+//               columns for want of TMEM
+// Shared memory holds three of the four state tiles: Hlo comes last, where Hhi
+// was, while B and C work with G.
 // An accumulator takes the state's part first; its thread scales that row in
 // place and the product inside the chunk is added to it.  A token's own product
 // (W_ii's factors, the largest under strong decay) stays out of the bf16 operands
@@ -288,13 +292,15 @@ linear_state_kernel(const __grid_constant__ LinearArgs a, const __grid_constant_
 namespace gr {
 constexpr int kThreads = 512;
 constexpr uint32_t kQ = 0, kK = kTile, kV = 2 * kTile, kDo = 3 * kTile;
-constexpr uint32_t kS0 = 4 * kTile, kS1 = 5 * kTile, kS2 = 6 * kTile;  // Hhi; Hlo, then Glo; Ghi
+constexpr uint32_t kS0 = 4 * kTile, kS1 = 5 * kTile, kS2 = 6 * kTile;  // Hhi, then Hlo; Glo; Ghi
 constexpr uint32_t kGates = 7 * kTile;
 constexpr uint32_t kBars = kGates + sizeof(Gates);
 constexpr uint32_t kSmem = kBars + 512;
 static_assert(kSmem <= 232448, "shared memory of a CTA");
-enum { B_QK, B_VD, B_H, B_GH, B_GL, B_G, B_TAIL, B_A, B_B, B_DSA, B_DSB, B_DSC, B_X1, B_X2, B_X3,
-       B_X1S = B_X3 + 2, B_X2S, B_X3S, B_DQ = B_X3S + 2, B_DK, B_DV, B_DQR = B_DV + 2, B_HG, B_COUNT = B_HG + 2 };
+enum { B_QK, B_VD, B_HH, B_HL, B_GH, B_GL, B_G, B_TAIL, B_A, B_B, B_DSA, B_DSB, B_DSC, B_X1H, B_X1, B_X2, B_X3,
+       B_X1S = B_X3 + 2, B_X2S, B_X3S, B_DQ = B_X3S + 2, B_DK, B_DV, B_HALF = B_DV + 2, B_HG,
+       // free again: the columns of X1, X2, X3; the tiles of H, V, dO; the decays
+       B_XR = B_HG + 2, B_FH = B_XR + 3, B_FV, B_FD, B_PART, B_GFREE, B_END, B_COUNT };
 // TMEM columns: S, dP, S^T, dP^T; then dS over S and P^T behind it, X1 over dP,
 // X2 over S^T, dS^T over dP^T and X3 (64 columns) behind it
 constexpr uint32_t T_S = 0, T_DP = 128, T_ST = 256, T_DPT = 384;
@@ -303,17 +309,15 @@ constexpr uint32_t T_DS = 0, T_PT = 64, T_X1 = 128, T_X2 = 256, T_DST = 384, T_X
 
 // Chunk and head of a block.
 struct Chunk {
-  int h, valid;     // head; tokens (none: no such chunk)
+  int h, valid;     // head; tokens
   int y, qz, vz;    // first token, rows of the key and value heads
 };
 __device__ __forceinline__ Chunk chunk_of(const LinearArgs& a, const BwdWs& w, unsigned block) {
   Chunk u;
   const int ci = block / a.H;
   u.h = block % a.H;
-  u.valid = 0;
   int n, c;
   if (w.first) {
-    if (ci >= w.first[a.N]) return u;
     int lo = 0, hi = a.N;  // first[lo] <= ci < first[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -329,7 +333,7 @@ __device__ __forceinline__ Chunk chunk_of(const LinearArgs& a, const BwdWs& w, u
   int t0, len;
   seq_range(a, n, t0, len);
   const int b = a.cu_seqlens ? 0 : n;
-  u.valid = min(len - c * C, C);
+  u.valid = max(min(len - c * C, C), 0);
   u.y = t0 + c * C;
   u.qz = b * a.Hk + u.h / (a.H / a.Hk);
   u.vz = b * a.H + u.h;
@@ -445,19 +449,15 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
     if (tid == 0) set_status(a.status, CKDA_ERR_CUDA);
     return;
   }
-  const Chunk u = chunk_of(a, w, blockIdx.x);
-  if (u.valid <= 0) return;  // the grid is a bound
-  const int h = u.h, valid = u.valid, y = u.y, qz = u.qz, vz = u.vz;
-  const size_t vrow = (size_t)vz * a.T + y;
-  const size_t krow = (size_t)qz * a.T + y;
-  const char* himg = w.himg + (size_t)blockIdx.x * kImage;
-  const char* gimg = w.gimg + (size_t)blockIdx.x * kImage;
-  const bool tail = a.cu_seqlens && valid < C;
+  // chunks times heads; the grid is no larger
+  const unsigned blocks = (unsigned)(w.first ? min(w.first[a.N], w.chunks) : w.chunks) * a.H;
+  const unsigned step = gridDim.x;
 
   if (tid == 0) {
     for (int i = 0; i < B_COUNT; ++i) {
-      const bool by_warps = (i >= B_DSA && i <= B_DSC) || (i >= B_X1S && i < B_DQ) || i >= B_DQR;
-      mbar_init(bars + i, i == B_TAIL ? 12 : by_warps ? 4 : 1);
+      const bool by_warps = (i >= B_DSA && i <= B_DSC) || (i >= B_X1S && i < B_DQ) ||
+                            (i >= B_HALF && i < B_FH) || i == B_GFREE;
+      mbar_init(bars + i, i == B_TAIL ? 12 : i == B_PART ? 8 : by_warps ? 4 : 1);
     }
     *abort = 0;
     fence_mbar_init();
@@ -473,88 +473,116 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
 
   if (warp == 0) {
     if (lane == 0) {
-      mbar_arrive_expect_tx(bars + B_QK, 2 * kTile);
-      for (int p = 0; p < 2; ++p) {
-        tma_load_3d(sb + kQ + p * kPanel, &mq, bars + B_QK, 64 * p, y, qz);
-        tma_load_3d(sb + kK + p * kPanel, &mk, bars + B_QK, 64 * p, y, qz);
-      }
-      mbar_arrive_expect_tx(bars + B_VD, 2 * kTile);
-      for (int p = 0; p < 2; ++p) {
-        tma_load_3d(sb + kV + p * kPanel, &mv, bars + B_VD, 64 * p, y, vz);
-        tma_load_3d(sb + kDo + p * kPanel, &mo, bars + B_VD, 64 * p, y, vz);
-      }
-      mbar_arrive_expect_tx(bars + B_H, 2 * kTile);
-      load_image(sb + kS0, himg, bars + B_H);
-      load_image(sb + kS1, himg + kTile, bars + B_H);
-      mbar_arrive_expect_tx(bars + B_GH, kTile);
-      load_image(sb + kS2, gimg, bars + B_GH);
-      // What the next block on this SM will read, into L2 while this one works:
-      // the SMs run in step, and without it HBM idles while they compute.
-      const unsigned next = blockIdx.x + kLinSms;
-      if (next < gridDim.x) {
-        const Chunk v = chunk_of(a, w, next);
-        if (v.valid > 0) {
+      uint32_t par = 0;
+      for (unsigned block = blockIdx.x; block < blocks; block += step, par ^= 1) {
+        const Chunk u = chunk_of(a, w, block);
+        const char* himg = w.himg + (size_t)block * kImage;
+        const char* gimg = w.gimg + (size_t)block * kImage;
+        const bool again = block != blockIdx.x;
+        bool ok = true;
+        // a barrier of the chunk before, whose tile is wanted
+        auto last = [&](int bar) { ok = ok && (!again || mbar_wait(bars + bar, par ^ 1)); };
+        last(B_DQ); last(B_DK); last(B_X3 + 1);
+        if (!ok) { *abort = 1; break; }
+        mbar_arrive_expect_tx(bars + B_QK, 2 * kTile);
+        for (int p = 0; p < 2; ++p) {
+          tma_load_3d(sb + kQ + p * kPanel, &mq, bars + B_QK, 64 * p, u.y, u.qz);
+          tma_load_3d(sb + kK + p * kPanel, &mk, bars + B_QK, 64 * p, u.y, u.qz);
+        }
+        last(B_FV); last(B_FD);
+        if (!ok) { *abort = 1; break; }
+        mbar_arrive_expect_tx(bars + B_VD, 2 * kTile);
+        for (int p = 0; p < 2; ++p) {
+          tma_load_3d(sb + kV + p * kPanel, &mv, bars + B_VD, 64 * p, u.y, u.vz);
+          tma_load_3d(sb + kDo + p * kPanel, &mo, bars + B_VD, 64 * p, u.y, u.vz);
+        }
+        last(B_FH);
+        if (!ok) { *abort = 1; break; }
+        mbar_arrive_expect_tx(bars + B_HH, kTile);
+        load_image(sb + kS0, himg, bars + B_HH);
+        mbar_arrive_expect_tx(bars + B_GH, kTile);
+        load_image(sb + kS2, gimg, bars + B_GH);
+        mbar_arrive_expect_tx(bars + B_GL, kTile);
+        load_image(sb + kS1, gimg + kTile, bars + B_GL);
+        if (!mbar_wait(bars + B_X1H, par) || !mbar_wait(bars + B_HG, par)) { *abort = 1; break; }
+        mbar_arrive_expect_tx(bars + B_HL, kTile);  // Hhi has been read
+        load_image(sb + kS0, himg + kTile, bars + B_HL);
+        // What comes next, into L2 while this chunk is worked on: tiles come free
+        // late, and their loads should not wait for HBM then.
+        if (block + step < blocks) {
+          const Chunk v = chunk_of(a, w, block + step);
           prefetch_tile(&mq, v.y, v.qz, a.dk);
           prefetch_tile(&mk, v.y, v.qz, a.dk);
           prefetch_tile(&mv, v.y, v.vz, a.dv);
           prefetch_tile(&mo, v.y, v.vz, a.dv);
-          prefetch_bytes(w.himg + (size_t)next * kImage, kImage);
-          prefetch_bytes(w.gimg + (size_t)next * kImage, kImage);
+          prefetch_bytes(w.himg + (size_t)(block + step) * kImage, kImage);
+          prefetch_bytes(w.gimg + (size_t)(block + step) * kImage, kImage);
         }
-      }
-      if (mbar_wait(bars + B_X1, 0) && mbar_wait(bars + B_HG, 0)) {  // Hlo has been read
-        mbar_arrive_expect_tx(bars + B_GL, kTile);
-        load_image(sb + kS1, gimg + kTile, bars + B_GL);
-      } else {
-        *abort = 1;
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && mbar_wait(bars + B_QK, 0) && (!tail || mbar_wait(bars + B_TAIL, 0)) &&
-        mbar_wait(bars + B_VD, 0)) {
+    if (lane == 0) {
+      uint32_t par = 0, tails = 0;
+      unsigned finished = 0;
+      for (unsigned block = blockIdx.x; block < blocks && !*abort; block += step, par ^= 1) {
+      const Chunk u = chunk_of(a, w, block);
+      const bool again = block != blockIdx.x;
+      bool ok = mbar_wait(bars + B_QK, par);
+      auto last = [&](int bar) { ok = ok && (!again || mbar_wait(bars + bar, par ^ 1)); };
+      if (a.cu_seqlens && u.valid < C) ok = ok && mbar_wait(bars + B_TAIL, tails++ & 1);
+      last(B_DQ); last(B_DV + 1);
+      if (!ok) break;
       tc_fence_after();
       mma_ss<false, false>(tmem + T_S, sb + kQ, sb + kK, 0);
+      last(B_XR);
+      ok = ok && mbar_wait(bars + B_VD, par);
+      if (!ok) break;
+      tc_fence_after();
       mma_ss<false, false>(tmem + T_DP, sb + kDo, sb + kV, 0);
       umma_commit(bars + B_A);
+      last(B_XR + 1); last(B_XR + 2); last(B_DK);
+      if (!ok) break;
+      tc_fence_after();
       mma_ss<false, false>(tmem + T_ST, sb + kK, sb + kQ, 0);
       mma_ss<false, false>(tmem + T_DPT, sb + kV, sb + kDo, 0);
       umma_commit(bars + B_B);
       // what is left, by readiness; `done` keeps the order that TMEM asks for
-      enum { X1 = 1, X2H = 2, X2L = 4, X3A = 8, X3B = 16, DQ = 32, DK = 64, DVA = 128, DVB = 256 };
+      enum { X1H = 1, X1L = 2, X2 = 4, X3A = 8, X3B = 16, DQ = 32, DK = 64, DVA = 128, DVB = 256 };
       uint32_t done = 0;
       const uint64_t start = globaltimer_ns();
       auto ready = [&](uint32_t what, uint32_t after, int bar) {
-        if ((done & (what | after)) != after || !mbar_test(bars + bar, 0)) return false;
+        if ((done & (what | after)) != after || !mbar_test(bars + bar, par)) return false;
         tc_fence_after();
         done |= what;
         return true;
       };
-      bool dsa = false, dsb = false, dsc = false;
+      bool dsb = false, dsc = false, gl = false;
       while (done != 511 && !*abort) {
-        if (!dsa) dsa = mbar_test(bars + B_DSA, 0);
-        if (!dsb) dsb = mbar_test(bars + B_DSB, 0);
-        if (!dsc) dsc = mbar_test(bars + B_DSC, 0);
-        if (dsa && ready(X1, 0, B_H)) {
+        if (!dsb) dsb = mbar_test(bars + B_DSB, par);
+        if (!dsc) dsc = mbar_test(bars + B_DSC, par);
+        if (!gl) gl = mbar_test(bars + B_GH, par) && mbar_test(bars + B_GL, par);
+        if (!(done & X1H) && mbar_test(bars + B_HH, par) && ready(X1H, 0, B_DSA)) {
           mma_ss<false, true>(tmem + T_X1, sb + kDo, sb + kS0, 0);
-          mma_ss<false, true>(tmem + T_X1, sb + kDo, sb + kS1, 1);
+          umma_commit(bars + B_X1H);
+        }
+        if (ready(X1L, X1H, B_HL)) {
+          mma_ss<false, true>(tmem + T_X1, sb + kDo, sb + kS0, 1);
           umma_commit(bars + B_X1);
         }
-        if (dsb && dsc && ready(X2H, 0, B_GH))
-          mma_ss<false, true>(tmem + T_X2, sb + kV, sb + kS2, 0);
-        if (ready(X2L, X2H, B_GL)) {
-          mma_ss<false, true>(tmem + T_X2, sb + kV, sb + kS1, 1);
-          umma_commit(bars + B_X2);
-        }
-        if (ready(DQ, X1, B_X1S)) {
+        if (ready(DQ, X1L, B_X1S)) {
           mma_ts<true>(tmem + T_X1, tmem + T_DS, sb + kK, 1);
           umma_commit(bars + B_DQ);
         }
-        if (dsb && ready(X3A, X2L, B_GL)) {
+        if (gl && dsc && ready(X2, 0, B_DSB)) {
+          mma_ss<false, true>(tmem + T_X2, sb + kV, sb + kS2, 0);
+          mma_ss<false, true>(tmem + T_X2, sb + kV, sb + kS1, 1);
+          umma_commit(bars + B_X2);
           mma_ss<false, false, 64>(tmem + T_X3, sb + kK, sb + kS2, 0);
           mma_ss<false, false, 64>(tmem + T_X3, sb + kK, sb + kS1, 1);
           umma_commit(bars + B_X3);
+          done |= X3A;
         }
-        if (ready(DK, X2L, B_X2S)) {
+        if (ready(DK, X2, B_X2S)) {
           mma_ts<true>(tmem + T_X2, tmem + T_DST, sb + kQ, 1);
           umma_commit(bars + B_DK);
         }
@@ -562,64 +590,80 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
           mma_ts<true, 64>(tmem + T_X3, tmem + T_PT, sb + kDo, 1);
           umma_commit(bars + B_DV);
         }
-        if (ready(X3B, X2L, B_DQR)) {  // dQ has left its columns
-          mma_ss<false, false, 64>(tmem + T_X1, sb + kK, sb + kS2 + kPanel / 2, 0);
-          mma_ss<false, false, 64>(tmem + T_X1, sb + kK, sb + kS1 + kPanel / 2, 1);
+        if (ready(X3B, DVA, B_HALF)) {
+          mma_ss<false, false, 64>(tmem + T_X3, sb + kK, sb + kS2 + kPanel / 2, 0);
+          mma_ss<false, false, 64>(tmem + T_X3, sb + kK, sb + kS1 + kPanel / 2, 1);
           umma_commit(bars + B_X3 + 1);
         }
-        if (dsc && ready(DVB, X3B, B_X3S + 1)) {
-          mma_ts<true, 64>(tmem + T_X1, tmem + T_PT, sb + kDo + kPanel, 1);
+        if (ready(DVB, X3B, B_X3S + 1)) {
+          mma_ts<true, 64>(tmem + T_X3, tmem + T_PT, sb + kDo + kPanel, 1);
           umma_commit(bars + B_DV + 1);
         }
         if (globaltimer_ns() - start > kWaitLimitNs) break;
       }
-      if (done != 511) *abort = 1;
-    } else if (lane == 0) {
-      *abort = 1;
+      if (done != 511) break;
+      ++finished;
+      }
+      if (finished != (blocks > blockIdx.x ? (blocks - 1 - blockIdx.x) / step + 1 : 0)) *abort = 1;
+      umma_commit(bars + B_END);
     }
   } else if (warp == 2) {
-    const float* g = a.g_head ? a.g + h : a.g + vrow;
-    make_gates(gates, load_decays(g, a.g_head ? 0 : 1, valid, lane), lane);
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bars + B_G);
+    uint32_t par = 0;
+    for (unsigned block = blockIdx.x; block < blocks; block += step, par ^= 1) {
+      const Chunk u = chunk_of(a, w, block);
+      const float* g = a.g_head ? a.g + u.h : a.g + (size_t)u.vz * a.T + u.y;
+      const float4 x = load_decays(g, a.g_head ? 0 : 1, u.valid, lane);
+      if (block != blockIdx.x && !warp_wait(bars + B_GFREE, par ^ 1, abort)) break;
+      make_gates(gates, x, lane);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + B_G);
+    }
   } else if (warp >= 4) {
     const int wg = (warp - 4) >> 2, wq = warp & 3, row = tid & 127;
     const uint32_t lanes = tmem + ((uint32_t)(32 * wq) << 16);
-    const bool in = row < valid, lead = row == 0;
-    // a staged result to memory, by its 128 threads
-    auto put = [&](const CUtensorMap* m, void* dst, size_t at, int width, uint32_t tile, int head,
-                   int p0, int p1) {
-      fence_proxy_async_smem();
-      named_sync(1 + wg, 128);
-      if (tail)
-        store_rows(static_cast<__nv_bfloat16*>(dst) + at * width, sm + tile, valid, width, p0, p1,
-                   row);
-      else if (lead && 64 * p0 < width)
-        store_tile(m, sb + tile, y, head, p0, min(p1, (width + 63) / 64));
-    };
-    do {
+    const bool lead = row == 0;
+    uint32_t par = 0;
+    for (unsigned block = blockIdx.x; block < blocks; block += step, par ^= 1) {
+      const Chunk u = chunk_of(a, w, block);
+      const int valid = u.valid;
+      const size_t vrow = (size_t)u.vz * a.T + u.y, krow = (size_t)u.qz * a.T + u.y;
+      const bool tail = a.cu_seqlens && valid < C;
+      const bool in = row < valid;
+      // a staged result to memory, by its 128 threads
+      auto put = [&](const CUtensorMap* m, void* dst, size_t at, int width, uint32_t tile, int head,
+                     int p0, int p1) {
+        fence_proxy_async_smem();
+        named_sync(1 + wg, 128);
+        if (tail) {
+          store_rows(static_cast<__nv_bfloat16*>(dst) + at * width, sm + tile, valid, width, p0, p1,
+                     row);
+          named_sync(1 + wg, 128);
+        } else if (lead && 64 * p0 < width) {
+          store_tile(m, sb + tile, u.y, head, p0, min(p1, (width + 63) / 64));
+        }
+      };
       if (tail) {  // tokens of the next sequence behind this one: out of every sum over tokens
-        if (!warp_wait(bars + (wg == 2 ? B_VD : B_QK), 0, abort)) break;
+        if (!warp_wait(bars + (wg == 2 ? B_VD : B_QK), par, abort)) break;
         if (!in) zero_row(sm + (wg == 0 ? kQ : wg == 1 ? kK : kDo), row);
         warp_publish(bars + B_TAIL);
       }
       float hgsum = 0.f;
       if (wg == 2) {
-        // <H, G>, first (Hhi + Hlo, Ghi); (Hhi, Glo) follows when Glo has come
-        // (plain loads of it from memory arrived thousands of cycles later than
-        // the tiles).  (Hlo, Glo) is 2^-18 of the rest and left out.
-        if (!warp_wait(bars + B_H, 0, abort) || !warp_wait(bars + B_GH, 0, abort)) break;
-        hgsum = tile_dot(sm + kS0, sm + kS2, row) + tile_dot(sm + kS1, sm + kS2, row);
+        // <H, G>, first (Hhi, Ghi + Glo); (Hlo, Ghi) follows when Hlo has come.
+        // (Hlo, Glo) is 2^-18 of the rest and left out.
+        if (!warp_wait(bars + B_HH, par, abort) || !warp_wait(bars + B_GH, par, abort) ||
+            !warp_wait(bars + B_GL, par, abort))
+          break;
+        hgsum = tile_dot(sm + kS0, sm + kS2, row) + tile_dot(sm + kS0, sm + kS1, row);
         warp_arrive(bars + B_HG);
       }
-      if (!warp_wait(bars + B_G, 0, abort)) break;
+      if (!warp_wait(bars + B_G, par, abort)) break;
       const float pre = gates->pre[row], es = gates->es[row];
       const float into = a.scale * gates->eL[row], out = gates->w[row], s = a.scale;
-      // own, own_p: s do_i.v_i (A, B) and s q_i.k_i (A; C has it in own)
-      float wsum = 0.f, dot = 0.f, own = 0.f, own_p = 0.f;
+      float wsum = 0.f, dot = 0.f, own = 0.f;  // own: s do_i.v_i (A, B), s q_i.k_i (C)
       if (wg == 0) {
         // row i: j over blocks up to its own
-        if (!warp_wait(bars + B_A, 0, abort)) break;
+        if (!warp_wait(bars + B_A, par, abort)) break;
         tc_fence_after();
 #pragma unroll 1
         for (int p = 0; p < wq; ++p) {
@@ -662,10 +706,7 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
               const float dp = s * __uint_as_float(d[j]);
               v[z] = j < lane ? dp * ex2(pre - gg[z]) : 0.f;
               if (j < lane) wsum = fmaf(v[z], __uint_as_float(x[j]), wsum);
-              if (j == lane) {
-                own = dp;
-                own_p = s * __uint_as_float(x[j]);
-              }
+              if (j == lane) own = dp;
             }
             o[2 * e] = pack_bf162(v[0], v[1]);
             o[2 * e + 1] = pack_bf162(v[2], v[3]);
@@ -678,24 +719,25 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
         }
         tmem_st_wait();
         warp_arrive(bars + B_DSA);
-        if (!warp_wait(bars + B_X1, 0, abort)) break;
+        if (!warp_wait(bars + B_X1, par, abort)) break;
         tc_fence_after();
         dot = scale_acc(lanes + T_X1, into, own, sm + kK, sm + kQ, row, 0, 4);
         warp_arrive(bars + B_X1S);
-        if (!warp_wait(bars + B_DQ, 0, abort)) break;
+        if (!warp_wait(bars + B_DQ, par, abort)) break;
         tc_fence_after();
-        // over Hhi's tile
-        if (!warp_wait(bars + B_HG + 1, 0, abort)) break;
+        // over H's tile
+        if (!warp_wait(bars + B_HG + 1, par, abort)) break;
         stage_acc(lanes + T_X1, sm + kS0, w.dq ? w.dq + (vrow + row) * a.dk : nullptr, a.dk, in,
                   row, 0, 4);
-        if (!w.dq) put(&mdq, a.dq, krow, a.dk, kS0, qz, 0, 2);
+        warp_arrive(bars + B_XR);
+        if (!w.dq) put(&mdq, a.dq, krow, a.dk, kS0, u.qz, 0, 2);
       } else {
         // row j: i over blocks from its own on.  B forms dS^T (over dP^T) and the
         // sums of W, C forms P^T (behind dS, so after A).
         const bool isb = wg == 1;
         const uint32_t to = lanes + (isb ? T_DST : T_PT);
-        if (!warp_wait(bars + B_B, 0, abort)) break;
-        if (!isb && !warp_wait(bars + B_DSA, 0, abort)) break;
+        if (!warp_wait(bars + B_B, par, abort)) break;
+        if (!isb && !warp_wait(bars + B_DSA, par, abort)) break;
         tc_fence_after();
         uint32_t o[16];
 #pragma unroll
@@ -766,81 +808,95 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
         tmem_st_wait();
         warp_arrive(bars + (isb ? B_DSB : B_DSC));
         if (isb) {
-          if (!warp_wait(bars + B_X2, 0, abort)) break;
+          if (!warp_wait(bars + B_X2, par, abort)) break;
           tc_fence_after();
           dot = scale_acc(lanes + T_X2, out, own, sm + kQ, sm + kK, row, 0, 4);
           warp_arrive(bars + B_X2S);
-          if (!warp_wait(bars + B_DK, 0, abort)) break;
+          if (!warp_wait(bars + B_DK, par, abort)) break;
           tc_fence_after();
           // over V's tile: X2 was its last reader
           stage_acc(lanes + T_X2, sm + kV, w.dk ? w.dk + (vrow + row) * a.dk : nullptr, a.dk, in,
                     row, 0, 4);
-          if (!w.dk) put(&mdk, a.dkey, krow, a.dk, kV, qz, 0, 2);
+          warp_arrive(bars + B_XR + 1);
+          if (!w.dk) put(&mdk, a.dkey, krow, a.dk, kV, u.qz, 0, 2);
         } else {
-          own_p = own;
-          if (!warp_wait(bars + B_GL, 0, abort)) break;
-          hgsum += tile_dot(sm + kS0, sm + kS1, row);
-          warp_arrive(bars + B_HG + 1);
+          bool ok = true;
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            if (!(ok = warp_wait(bars + B_X3 + half, par, abort))) break;
+            tc_fence_after();
+            scale_acc(lanes + T_X3, out, own, sm + kDo, sm + kDo, row, 2 * half, 2 * half + 2);
+            warp_arrive(bars + B_X3S + half);
+            if (half == 0) {  // meanwhile
+              if (!(ok = warp_wait(bars + B_HL, par, abort))) break;
+              hgsum += tile_dot(sm + kS0, sm + kS2, row);
+              warp_arrive(bars + B_HG + 1);
 #pragma unroll
-          for (int m = 16; m >= 1; m >>= 1) hgsum += __shfl_xor_sync(0xffffffffu, hgsum, m);
-          if (lane == 0) hg[wq] = hgsum;
+              for (int m = 16; m >= 1; m >>= 1) hgsum += __shfl_xor_sync(0xffffffffu, hgsum, m);
+              if (lane == 0) hg[wq] = hgsum;
+            }
+            // over this panel of dO: its readers were this product and dO H^T
+            if (!(ok = warp_wait(bars + B_DV + half, par, abort))) break;
+            if (!(ok = warp_wait(bars + B_X1, par, abort))) break;
+            tc_fence_after();
+            stage_acc(lanes + T_X3, sm + kDo, nullptr, a.dv, in, row, 2 * half, 2 * half + 2);
+            warp_arrive(bars + (half == 0 ? B_HALF : B_XR + 2));
+            put(&mdv, a.dval, vrow, a.dv, kDo, u.vz, half, half + 1);
+          }
+          if (!ok) break;
         }
       }
-      if (wg != 1) {
-        // dV: C the first panel, A the second
-        const int half = wg == 0 ? 1 : 0;
-        const uint32_t acc = lanes + (half ? T_X1 : T_X3);
-        if (half) warp_arrive(bars + B_DQR);
-        if (!warp_wait(bars + B_X3 + half, 0, abort)) break;
-        tc_fence_after();
-        scale_acc(acc, out, own_p, sm + kDo, sm + kDo, row, 2 * half, 2 * half + 2);
-        warp_arrive(bars + B_X3S + half);
-        if (!warp_wait(bars + B_DV + half, 0, abort)) break;
-        tc_fence_after();
-        // over this panel of dO: its readers were this product and dO H^T
-        if (!warp_wait(bars + B_X1, 0, abort)) break;
-        stage_acc(acc, sm + kDo, nullptr, a.dv, in, row, 2 * half, 2 * half + 2);
-        put(&mdv, a.dval, vrow, a.dv, kDo, vz, half, half + 1);
+      if (lead) {
+        store_read_wait();
+        mbar_arrive(bars + (wg == 0 ? B_FH : wg == 1 ? B_FV : B_FD));
       }
-      if (lead) store_read_wait();
-      // dg's sums by token, over the decays once all three are done with them
-      if (wg != 2) {
-        if (!warp_wait(bars + B_DSA, 0, abort) || !warp_wait(bars + B_DSB, 0, abort) ||
-            !warp_wait(bars + B_DSC, 0, abort))
-          break;
-        (wg == 0 ? gates->pre : gates->eL)[row] = in ? wsum : 0.f;
-        (wg == 0 ? gates->es : gates->w)[row] = in ? dot : 0.f;
+      // dg_t = e^{L_C} <H, G> + sum_{j<t} kd_j + sum_{i>=t} (qd_i + row_i - col_i):
+      // B hands its sums by token to A, over decays that all three have read
+      if (wg == 1) {
+        if (!warp_wait(bars + B_DSA, par, abort) || !warp_wait(bars + B_DSC, par, abort)) break;
+        gates->eL[row] = in ? wsum : 0.f;
+        gates->w[row] = in ? dot : 0.f;
       }
-    } while (false);
+      if (wg != 0) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + B_PART);
+        continue;
+      }
+      if (!warp_wait(bars + B_PART, par, abort)) break;
+      float fwd = gates->w[row];
+      float back = in ? dot + wsum - gates->eL[row] : 0.f;
+#pragma unroll
+      for (int m = 1; m < 32; m <<= 1) {
+        const float x = __shfl_up_sync(0xffffffffu, fwd, m);
+        const float z = __shfl_down_sync(0xffffffffu, back, m);
+        if (lane >= m) fwd += x;
+        if (lane + m < 32) back += z;
+      }
+      float excl = __shfl_up_sync(0xffffffffu, fwd, 1);
+      if (lane == 0) excl = 0.f;
+      if (lane == 31) run[wq] = fwd;
+      if (lane == 0) run[4 + wq] = back;
+      named_sync(1, 128);
+      float t = gates->all * (hg[0] + hg[1] + hg[2] + hg[3]) + excl + back;
+      for (int i = 0; i < wq; ++i) t += run[i];
+      for (int i = wq + 1; i < 4; ++i) t += run[4 + i];
+      if (in) (w.dg ? w.dg : a.dg)[vrow + row] = t;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + B_GFREE);
+    }
   }
 
+  // ------------------------------------------------------------- teardown
   tc_fence_before();
   __syncthreads();
-  if (warp >= 4 && warp < 8 && !*abort) {
-    // dg_t = e^{L_C} <H, G> + sum_{j<t} kd_j + sum_{i>=t} (qd_i + row_i - col_i)
-    const int t = tid & 127, wq = warp & 3;
-    float fwd = gates->w[t], back = gates->es[t] + gates->pre[t] - gates->eL[t];
-#pragma unroll
-    for (int m = 1; m < 32; m <<= 1) {
-      const float x = __shfl_up_sync(0xffffffffu, fwd, m), z = __shfl_down_sync(0xffffffffu, back, m);
-      if (lane >= m) fwd += x;
-      if (lane + m < 32) back += z;
+  if (tid == 0) {
+    if (!mbar_wait(bars + B_END, 0)) *abort = 1;
+    if (*abort) {
+      // let copies in flight land before the memory is given back
+      set_status(a.status, CKDA_ERR_TIMEOUT);
+      const int land[] = {B_QK, B_VD, B_HH, B_HL, B_GH, B_GL};
+      for (int i : land) mbar_wait(bars + i, 0, 1u << 12, 1000u);
     }
-    float excl = __shfl_up_sync(0xffffffffu, fwd, 1);
-    if (lane == 0) excl = 0.f;
-    if (lane == 31) run[wq] = fwd;
-    if (lane == 0) run[4 + wq] = back;
-    named_sync(1, 128);
-    float r = gates->all * (hg[0] + hg[1] + hg[2] + hg[3]) + excl + back;
-    for (int i = 0; i < wq; ++i) r += run[i];
-    for (int i = wq + 1; i < 4; ++i) r += run[4 + i];
-    if (t < valid) (w.dg ? w.dg : a.dg)[vrow + t] = r;
-  }
-  if (tid == 0 && *abort) {
-    // let copies and products in flight land before the memory is given back
-    set_status(a.status, CKDA_ERR_TIMEOUT);
-    const int land[] = {B_QK, B_VD, B_H, B_GH, B_GL, B_B, B_X1, B_X2, B_DQ, B_DK, B_DV, B_DV + 1};
-    for (int i : land) mbar_wait(bars + i, 0, 1u << 12, 1000u);
   }
   __syncthreads();
   tc_fence_after();
@@ -912,8 +968,9 @@ cudaError_t linear_chunk_bwd(const LinearArgs& a, char* ws, cudaStream_t s) {
   linear_state_kernel<true><<<units, st::kThreads, st::kSmem, s>>>(a, w, mq, mo);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (a.T > 0) {
-    linear_grad_kernel<<<(unsigned)(p.chunks * a.H), gr::kThreads, gr::kSmem, s>>>(
-        a, w, mq, mk, mv, mo, mdq, mdk, mdv);
+    const size_t units_c = p.chunks * a.H;
+    linear_grad_kernel<<<(unsigned)(units_c < kLinSms ? units_c : kLinSms), gr::kThreads, gr::kSmem,
+                         s>>>(a, w, mq, mk, mv, mo, mdq, mdk, mdv);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (w.dq && (e = linear_sum_heads(a, w.dq, w.dk, nullptr, s)) != cudaSuccess) return e;
   }
