@@ -37,8 +37,12 @@ extern "C" {
 
 size_t ckda_linear_fwd_workspace_bytes(int num_seqs, int B, int H, int T, int dk, int dv,
                                        ckda_dtype io_dtype) {
-  (void)B; (void)H; (void)T; (void)dk; (void)dv; (void)io_dtype;
-  return head_bytes(num_seqs);
+  if (num_seqs < 0 || B < 1 || H < 1 || T < 0 || dk < 1 || dv < 1) return 0;
+  const size_t chunk =
+      linear_chunk_path(io_dtype, dk, dv)
+          ? linear_chunk_fwd_bytes(num_seqs > 0 ? num_seqs : B, B, H, T, dk, dv, num_seqs > 0)
+          : 0;
+  return head_bytes(num_seqs) + chunk;
 }
 
 ckda_status ckda_linear_fwd(const void* q, const void* k, const void* v, const float* g,
@@ -72,7 +76,8 @@ ckda_status ckda_linear_fwd(const void* q, const void* k, const void* v, const f
       e = launch_seq_order(cu_seqlens, num_seqs, order, s);
       a.order = order;
     }
-    if (e == cudaSuccess) e = linear_chunk_fwd(a, s);
+    char* scratch = static_cast<char*>(workspace) + head_bytes(cu_seqlens ? num_seqs : 0);
+    if (e == cudaSuccess) e = linear_chunk_fwd(a, scratch, s);
   } else {
     e = linear_serial_fwd(a, s);
   }
@@ -86,7 +91,7 @@ size_t ckda_linear_bwd_workspace_bytes(int num_seqs, int B, int H, int Hk, int T
   // what either path takes: which one runs depends on the pointers' alignment too
   size_t bytes = linear_serial_bwd_bytes(N, B, H, T, dk, dv, num_seqs > 0);
   if (linear_chunk_path(io_dtype, dk, dv)) {
-    const size_t chunk = linear_chunk_bwd_bytes(N, B, H, Hk, T, dk, num_seqs > 0);
+    const size_t chunk = linear_chunk_bwd_bytes(N, B, H, Hk, T, dk, dv, num_seqs > 0);
     if (chunk > bytes) bytes = chunk;
   }
   return head_bytes(num_seqs) + bytes;

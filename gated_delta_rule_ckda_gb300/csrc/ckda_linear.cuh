@@ -67,8 +67,9 @@ inline bool linear_chunk_path(ckda_dtype io, int dk, int dv) {
 }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 // Chunks of 128 tokens on the tensor cores.
-cudaError_t linear_chunk_fwd(const LinearArgs& a, cudaStream_t s);
-size_t linear_chunk_bwd_bytes(int N, int B, int H, int Hk, int T, int dk, bool packed);
+size_t linear_chunk_fwd_bytes(int N, int B, int H, int T, int dk, int dv, bool packed);
+cudaError_t linear_chunk_fwd(const LinearArgs& a, char* ws, cudaStream_t s);
+size_t linear_chunk_bwd_bytes(int N, int B, int H, int Hk, int T, int dk, int dv, bool packed);
 cudaError_t linear_chunk_bwd(const LinearArgs& a, char* ws, cudaStream_t s);
 
 // dq and dk of the key heads: the sum over the H / Hk heads that share one, of

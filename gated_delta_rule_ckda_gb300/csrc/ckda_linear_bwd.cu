@@ -14,10 +14,10 @@
 // token's own product W_ii, which no decay touches, is not in it, and pairs on
 // the same side of t cancel inside one chunk only.
 //
-// Three launches:
-//   1. linear_state_kernel, forward in time: H entering every chunk;
-//   2. the same kernel, backward in time over (q, do): G at every chunk's end;
-//   3. linear_grad_kernel: a chunk to a CTA, all gradients.
+// Three steps:
+//   1. linear_chunk_states, forward in time: H entering every chunk;
+//   2. the same, backward in time over (q, do): G at every chunk's end;
+//   3. linear_grad_kernel: all gradients of a chunk.
 // The states pass through HBM in two bf16 parts (hi + lo, 64 KiB a chunk and
 // direction): dg and dh0 are fp32 and need more than one bf16 rounding.
 #include "ckda_linear_chunk.cuh"
@@ -25,8 +25,6 @@
 namespace ckda {
 namespace {
 using namespace chunk;
-
-constexpr uint32_t kImage = 2 * kTile;  // a state: hi tile, lo tile, [dv][dk], swizzled
 
 struct BwdWs {
   char* himg;           // [slots * H] images of H
@@ -59,214 +57,6 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(LinearArgs a, int32_t*
     before += (len + C - 1) / C;
   }
   if (threadIdx.x == 1023) first[a.N] = before;
-}
-
-// ----------------------------------------------------------- states of chunks
-// One CTA of 512 threads walks the chunks of one (sequence, head), forward over
-// (k, v) from h0 or backward over (q, do) from dhT, writes the state met at
-// each chunk and, backward, dh0.  Bound by HBM: two tiles in and an image out,
-// 128 KiB a chunk.
-//   warp 0 loads, warp 1 issues the products, warp 2 makes the decays,
-//   warps 4-7 scale a chunk's keys (queries) in two bf16 parts,
-//   warps 8-15 hold the state: thread (r, s) has its channels 64 s .. + 63 of
-//   value column r in fp32 registers.  They stage the image in shared memory
-//   and one bulk copy writes it (rows written by their own threads would take
-//   an L1 pass for every 16 bytes).
-namespace st {
-constexpr int kThreads = 512;
-constexpr int kSlots = 4;                       // x and y tiles of two chunks
-constexpr uint32_t kLo = kSlots * kTile;        // lo part of the scaled tile
-constexpr uint32_t kStage = kLo + kTile;        // the image on its way out
-constexpr uint32_t kGates = kStage + kImage;
-constexpr uint32_t kBars = kGates + sizeof(Gates);
-constexpr uint32_t kSmem = kBars + 512;
-static_assert(kSmem <= 232448, "shared memory of a CTA");
-enum { B_FULL = 0, B_EMPTY = 4, B_KT = 8, B_DF, B_DFREE = B_DF + 2, B_G = B_DFREE + 2, B_GFREE,
-       B_END, B_COUNT };
-}  // namespace st
-
-template <bool BACK>
-__global__ void __launch_bounds__(st::kThreads, 1)
-linear_state_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ BwdWs w,
-                    const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap my) {
-  using namespace st;
-  extern __shared__ __align__(1024) char sm[];
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kBars);
-  Gates* gates = reinterpret_cast<Gates*>(sm + kGates);
-  volatile int* abort = reinterpret_cast<volatile int*>(sm + kBars + 400);
-  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(sm + kBars + 404);
-  const uint32_t sb = smem_u32(sm);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (sb & 1023u) {
-    if (tid == 0) set_status(a.status, CKDA_ERR_CUDA);
-    return;
-  }
-  const int order = blockIdx.x / a.H, h = blockIdx.x % a.H;
-  const int n = a.order ? a.order[order] : order;
-  const int b = a.cu_seqlens ? 0 : n, hk = h / (a.H / a.Hk);
-  int t0, len;
-  seq_range(a, n, t0, len);
-  const int chunks = (len + C - 1) / C;
-  const int xz = b * a.Hk + hk, yz = b * a.H + h;
-  const size_t vrow = (size_t)yz * a.T + t0;
-  const size_t state = ((size_t)n * a.H + h) * (size_t)a.dk * a.dv;
-  const size_t first = w.first ? (size_t)w.first[n] : (size_t)n * chunks;
-  auto at = [&](int i) { return BACK ? chunks - 1 - i : i; };  // chunk of step i
-  // forward, no chunk is entered by what the last one leaves
-  const int steps = BACK ? chunks : chunks - 1;
-
-  if (tid == 0) {
-    for (int i = 0; i < B_COUNT; ++i)
-      mbar_init(bars + i, i == B_KT                         ? 4
-                          : i >= B_DFREE && i < B_DFREE + 2 ? 8
-                          : i == B_GFREE                    ? 12
-                                                            : 1);
-    *abort = 0;
-    fence_mbar_init();
-  }
-  if (warp == 3) {
-    tmem_alloc(tmem_at, 256);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_at;
-
-  if (warp == 0) {
-    if (lane == 0) {
-      for (int i = 0; i < 2 * steps; ++i) {
-        const int slot = i % kSlots, use = i / kSlots;
-        if (use > 0 && !mbar_wait(bars + B_EMPTY + slot, (use - 1) & 1)) { *abort = 1; break; }
-        if (*abort) break;
-        load_tile(sb + slot * kTile, i & 1 ? &my : &mx, bars + B_FULL + slot, t0 + at(i / 2) * C,
-                  i & 1 ? yz : xz);
-      }
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      for (int i = 0; i < steps; ++i) {
-        const int ix = (2 * i) % kSlots, iy = ix + 1, p = i & 1;
-        bool ok = mbar_wait(bars + B_FULL + iy, (i / 2) & 1);
-        if (ok && i >= 2) ok = mbar_wait(bars + B_DFREE + p, (i / 2 - 1) & 1);
-        if (!ok || !mbar_wait(bars + B_KT, p)) { *abort = 1; break; }
-        tc_fence_after();
-        mma_ss<true, true>(tmem + 128 * p, sb + iy * kTile, sb + ix * kTile, 0);
-        mma_ss<true, true>(tmem + 128 * p, sb + iy * kTile, sb + kLo, 1);
-        umma_commit(bars + B_DF + p);
-        umma_commit(bars + B_EMPTY + ix);
-        umma_commit(bars + B_EMPTY + iy);
-      }
-      umma_commit(bars + B_END);
-    }
-  } else if (warp == 2) {
-    const float* g = a.g_head ? a.g + h : a.g + vrow;
-    const int gs = a.g_head ? 0 : 1;
-    for (int i = 0; i < steps; ++i) {
-      const int c = at(i);
-      const float4 x = load_decays(g + (size_t)c * C * gs, gs, min(len - c * C, C), lane);
-      if (i >= 1 && !warp_wait(bars + B_GFREE, (i - 1) & 1, abort)) break;
-      make_gates(gates, x, lane);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bars + B_G);
-    }
-  } else if (warp >= 4 && warp < 8) {
-    const int t = tid - 128;
-    for (int i = 0; i < steps; ++i) {
-      const int ix = (2 * i) % kSlots, valid = min(len - at(i) * C, C);
-      const uint32_t par = (i / 2) & 1;
-      if (!warp_wait(bars + B_G, i & 1, abort)) break;
-      const float wt = BACK ? a.scale * gates->eL[t] : gates->w[t];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bars + B_GFREE);
-      if (!warp_wait(bars + B_FULL + ix, par, abort)) break;
-      if (a.cu_seqlens && valid < C) {  // tokens of the next sequence behind this one
-        if (!warp_wait(bars + B_FULL + ix + 1, par, abort)) break;
-        if (t >= valid) zero_row(sm + (ix + 1) * kTile, t);
-      }
-      if (i >= 1 && !warp_wait(bars + B_DF + ((i - 1) & 1), ((i - 1) / 2) & 1, abort)) break;
-#pragma unroll 1
-      for (int p = 0; p < 2; ++p)
-        scale_row(sm + ix * kTile, sm + kLo, t, p, wt, t < valid);
-      warp_publish(bars + B_KT);
-    }
-  } else if (warp >= 8) {
-    const int s = (warp - 8) >> 2, r = (tid - 256) & 127;
-    const uint32_t lanes = tmem + ((uint32_t)(r & 96) << 16);
-    const float* init = BACK ? a.dhT : a.h0;
-    char* img = BACK ? w.gimg : w.himg;
-    float S[64];
-#pragma unroll
-    for (int i = 0; i < 64; ++i) {
-      const int d = 64 * s + i;
-      S[i] = init && r < a.dv && d < a.dk ? init[state + (size_t)d * a.dv + r] : 0.f;
-    }
-    bool ok = true;
-    for (int i = 0; i < chunks; ++i) {
-      const int p = i & 1, c = at(i);
-      // (offsets that are no packing would run past the workspace)
-      const size_t slot = min(first + c, (size_t)w.chunks - 1) * a.H + h;
-      if (i > 0) {  // the last image has left the stage
-        if (tid == 256) store_read_wait();
-        named_sync(1, 256);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float x = S[8 * j + 2 * e], y = S[8 * j + 2 * e + 1];
-          hi[e] = pack_bf162(x, y);
-          lo[e] = pack_bf162(x - __uint_as_float(hi[e] << 16),
-                             y - __uint_as_float(hi[e] & 0xffff0000u));
-        }
-        char* out = sm + kStage + sw128_chunk(128, r, 8 * s + j);
-        *reinterpret_cast<uint4*>(out) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(out + kTile) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-      }
-      fence_proxy_async_smem();
-      named_sync(1, 256);
-      if (tid == 256) store_bytes(img + slot * kImage, sb + kStage, kImage);
-      if (i >= steps) break;
-      if (!(ok = warp_wait(bars + B_G, p, abort))) break;
-      const float all = gates->all;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bars + B_GFREE);
-      if (!(ok = warp_wait(bars + B_DF + p, (i / 2) & 1, abort))) break;
-      tc_fence_after();
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        uint32_t x[32];
-        tmem_ld32<32>(lanes + 128 * p + 64 * s + 32 * q, x);
-        tmem_ld_wait();
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-          S[32 * q + e] = fmaf(all, S[32 * q + e], __uint_as_float(x[e]));
-      }
-      warp_arrive(bars + B_DFREE + p);
-    }
-    if (tid == 256) store_read_wait();
-    if (BACK && ok && a.dh0 && r < a.dv) {
-#pragma unroll
-      for (int i = 0; i < 64; ++i) {
-        const int d = 64 * s + i;
-        if (d < a.dk) a.dh0[state + (size_t)d * a.dv + r] = S[i];
-      }
-    }
-  }
-
-  tc_fence_before();
-  __syncthreads();
-  if (tid == 0) {
-    if (!mbar_wait(bars + B_END, 0)) *abort = 1;
-    if (*abort) {
-      set_status(a.status, CKDA_ERR_TIMEOUT);
-      for (int i = 0; i < kSlots; ++i) mbar_wait(bars + B_FULL + i, 0, 1u << 12, 1000u);
-    }
-  }
-  __syncthreads();
-  tc_fence_after();
-  if (warp == 3) tmem_dealloc(tmem, 256);
 }
 
 // ------------------------------------------------------ gradients of a chunk
@@ -903,13 +693,12 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
   if (warp == 3) tmem_dealloc(tmem, 512);
 }
 
-size_t up256(size_t x) { return (x + 255) / 256 * 256; }
-
 struct ChunkPlan {
-  size_t chunks, himg, gimg, dg, dq, dk, first, total;
+  size_t chunks, himg, gimg, dg, dq, dk, first, split, total;
 };
-ChunkPlan chunk_plan(int N, int B, int H, int Hk, int T, int dk, bool packed) {
+ChunkPlan chunk_plan(int N, int B, int H, int Hk, int T, int dk, int dv, bool packed) {
   ChunkPlan p;
+  auto up256 = [](size_t x) { return (x + 255) / 256 * 256; };
   // packed: ceil(len / 128) over sequences that add up to T
   p.chunks = packed ? (size_t)T / C + N : (size_t)N * ((T + C - 1) / C);
   const size_t rows = (size_t)B * H * T;
@@ -920,18 +709,20 @@ ChunkPlan chunk_plan(int N, int B, int H, int Hk, int T, int dk, bool packed) {
   p.dq = at; at += Hk == H ? 0 : up256(rows * dk * 4);
   p.dk = at; at += Hk == H ? 0 : up256(rows * dk * 4);
   p.first = at; at += up256(((size_t)N + 1) * 4);
+  p.split = at; at += linear_split_bytes(linear_split(N, B, H, T, packed), N, H, dk, dv, packed, 2);
   p.total = at;
   return p;
 }
 
 }  // namespace
 
-size_t linear_chunk_bwd_bytes(int N, int B, int H, int Hk, int T, int dk, bool packed) {
-  return chunk_plan(N, B, H, Hk, T, dk, packed).total;
+size_t linear_chunk_bwd_bytes(int N, int B, int H, int Hk, int T, int dk, int dv, bool packed) {
+  return chunk_plan(N, B, H, Hk, T, dk, dv, packed).total;
 }
 
 cudaError_t linear_chunk_bwd(const LinearArgs& a, char* ws, cudaStream_t s) {
-  const ChunkPlan p = chunk_plan(a.N, a.B, a.H, a.Hk, a.T, a.dk, a.cu_seqlens != nullptr);
+  const ChunkPlan p =
+      chunk_plan(a.N, a.B, a.H, a.Hk, a.T, a.dk, a.dv, a.cu_seqlens != nullptr);
   BwdWs w{};
   w.himg = ws + p.himg;
   w.gimg = ws + p.gimg;
@@ -954,22 +745,19 @@ cudaError_t linear_chunk_bwd(const LinearArgs& a, char* ws, cudaStream_t s) {
     chunk_plan_kernel<<<1, 1024, 0, s>>>(a, w.first);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  const struct { const void* f; uint32_t bytes; } kernels[] = {
-      {(const void*)linear_state_kernel<false>, st::kSmem},
-      {(const void*)linear_state_kernel<true>, st::kSmem},
-      {(const void*)linear_grad_kernel, gr::kSmem}};
-  for (const auto& k : kernels)
-    if ((e = cudaFuncSetAttribute(k.f, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  (int)k.bytes)) != cudaSuccess)
-      return e;
-  const unsigned units = (unsigned)a.N * a.H;
-  linear_state_kernel<false><<<units, st::kThreads, st::kSmem, s>>>(a, w, mk, mv);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  linear_state_kernel<true><<<units, st::kThreads, st::kSmem, s>>>(a, w, mq, mo);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  Split sp = linear_split(a.N, a.B, a.H, a.T, a.cu_seqlens != nullptr);
+  if ((e = linear_split_plan(a, sp, ws + p.split, s)) != cudaSuccess) return e;
+  for (int back = 0; back < 2; ++back) {
+    if ((e = linear_segment_states(a, sp, ws + p.split, back, back, s)) != cudaSuccess) return e;
+    const ChunkImages out{back ? w.gimg : w.himg, w.first, w.chunks};
+    if ((e = linear_chunk_states(a, sp, out, back, s)) != cudaSuccess) return e;
+  }
   if (a.T > 0) {
-    const size_t units_c = p.chunks * a.H;
-    linear_grad_kernel<<<(unsigned)(units_c < kLinSms ? units_c : kLinSms), gr::kThreads, gr::kSmem,
+    e = cudaFuncSetAttribute(linear_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)gr::kSmem);
+    if (e != cudaSuccess) return e;
+    const size_t blocks = p.chunks * a.H;
+    linear_grad_kernel<<<(unsigned)(blocks < kLinSms ? blocks : kLinSms), gr::kThreads, gr::kSmem,
                          s>>>(a, w, mq, mk, mv, mo, mdq, mdk, mdv);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (w.dq && (e = linear_sum_heads(a, w.dq, w.dk, nullptr, s)) != cudaSuccess) return e;

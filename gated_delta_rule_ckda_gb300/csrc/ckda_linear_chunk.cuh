@@ -11,14 +11,57 @@ namespace chunk {
 constexpr int C = 128;                 // tokens of a chunk
 constexpr uint32_t kTile = 32768;      // bytes of a 128 x 128 bf16 tile, two 64-column panels
 constexpr uint32_t kPanel = 16384;
+constexpr uint32_t kImage = 2 * kTile; // a state: hi tile, lo tile, [dv][dk], swizzled
 
-// A unit of work: one (sequence, head), or one segment of it.
-struct Unit {
-  int n, h, hk, b;     // sequence, head, key head, batch row
-  int t0, len;         // tokens on the T axis
-  int seg;             // segment of the sequence (0 when not split)
-  size_t krow, vrow;   // row of token t0 among [B * Hk * T] and [B * H * T]
+// Sequences are cut into segments where there are too few (sequence, head)s for
+// the SMs, or one is much longer than an SM's share.  The state entering each
+// segment comes first: every segment but the last (backward, the first) runs
+// from zero, and a scan joins them.
+struct Split {
+  int per;               // dense: segments of a sequence; packed: most chunks of a segment
+  int items;             // segments of all sequences; packed: a bound on them
+  const int32_t* item0;  // packed: [N + 1] first segment by rank in a.order
+  float* state;          // [items * H][dk][dv]: what each segment hands on
+  float* decay;          // [items * H]: over the segment
 };
+// A segment of one (sequence, head).
+struct Piece {
+  int n, h, qz, vz;      // sequence, head, rows of the key and value heads
+  int t0, len;           // tokens on the T axis
+  int c0, chunks;        // chunks, counted inside the sequence
+  int seg, segs, item;
+};
+__device__ __forceinline__ bool piece_of(const LinearArgs& a, const Split& sp, unsigned block,
+                                         Piece& u) {
+  u.item = block / a.H;
+  u.h = block % a.H;
+  if (a.cu_seqlens) {
+    if (u.item >= sp.item0[a.N]) return false;
+    int lo = 0, hi = a.N;  // item0[lo] <= item < item0[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (sp.item0[mid] <= u.item) lo = mid; else hi = mid;
+    }
+    u.n = a.order[lo];
+    u.seg = u.item - sp.item0[lo];
+    u.segs = sp.item0[lo + 1] - sp.item0[lo];
+  } else {
+    u.n = u.item / sp.per;
+    u.seg = u.item % sp.per;
+    u.segs = sp.per;
+  }
+  int len;
+  seq_range(a, u.n, u.t0, len);
+  const int all = (len + C - 1) / C;
+  u.c0 = (int)((long long)all * u.seg / u.segs);
+  u.chunks = (int)((long long)all * (u.seg + 1) / u.segs) - u.c0;
+  u.t0 += u.c0 * C;
+  u.len = min(len - u.c0 * C, u.chunks * C);
+  const int b = a.cu_seqlens ? 0 : u.n;
+  u.qz = b * a.Hk + u.h / (a.H / a.Hk);
+  u.vz = b * a.H + u.h;
+  return true;
+}
 
 // ------------------------------------------------------------------- TMA
 // Box of 64 channels x 128 tokens of one head; coordinates (channel, token,
@@ -282,6 +325,27 @@ __device__ __forceinline__ void scale_row(char* tile, char* lo, int row, int pan
 }
 
 }  // namespace chunk
+
+// The cut for these sizes, its bytes after `at`, and its tables filled in from a
+// workspace; the plan of packed sequences is made on the device.
+chunk::Split linear_split(int N, int B, int H, int T, bool packed);
+size_t linear_split_bytes(const chunk::Split& sp, int N, int H, int dk, int dv, bool packed,
+                          int directions);
+cudaError_t linear_split_plan(const LinearArgs& a, chunk::Split& sp, char* ws, cudaStream_t s);
+// What each segment hands on, in time (back = false: over k, v from h0) or against
+// it (over q, dout from dhT), joined.  `dir`: which of the workspace's tables.
+cudaError_t linear_segment_states(const LinearArgs& a, chunk::Split& sp, char* ws, bool back,
+                                  int dir, cudaStream_t s);
+
+// The state entering every chunk (back: dL/dH at every chunk's end, and dh0),
+// as images.
+struct ChunkImages {
+  char* img;             // [chunks * H] images
+  const int32_t* first;  // packed: [N + 1] first chunk of each sequence
+  int chunks;            // a bound on the chunks
+};
+cudaError_t linear_chunk_states(const LinearArgs& a, const chunk::Split& sp, const ChunkImages& out,
+                                bool back, cudaStream_t s);
 
 // Tensor map of a [heads, T, width] bf16 tensor for load_tile.
 bool linear_map(CUtensorMap* m, const void* base, uint64_t heads, uint64_t T, uint64_t width);

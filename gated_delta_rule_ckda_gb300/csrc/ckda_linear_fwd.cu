@@ -8,8 +8,8 @@
 //     H <- e^{L_C} H + sum_j e^{L_C - L_j} k_j v_j^T.
 // Every exponent is a sum of log decays, so with g <= 0 no factor exceeds one.
 //
-// One CTA of 512 threads walks the chunks of one (sequence, head); the state
-// never leaves the SM.  It is bound by HBM: 1 KiB a token at 128 x 128 against
+// One CTA of 512 threads walks the chunks of one (sequence, head), or of one
+// segment of it; the state never leaves the SM.  It is bound by HBM: 1 KiB a token at 128 x 128 against
 // five 128 x 128 x 128 products a chunk.
 //   warp 0       loads tiles with TMA into a ring of five 32 KB slots, in the
 //                order q, k, v of chunk after chunk
@@ -55,7 +55,8 @@ enum {
 constexpr uint32_t T_S = 0, T_P = 0, T_DF = 128, T_OI = 256, T_O = 384;
 
 __global__ void __launch_bounds__(kThreads, 1)
-linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ CUtensorMap mq,
+linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ Split sp,
+                  const __grid_constant__ CUtensorMap mq,
                   const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                   const __grid_constant__ CUtensorMap mo) {
   extern __shared__ __align__(1024) char sm[];
@@ -70,15 +71,14 @@ linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ 
     return;
   }
 
-  const int order = blockIdx.x / a.H, h = blockIdx.x % a.H;
-  const int n = a.order ? a.order[order] : order;
-  const int b = a.cu_seqlens ? 0 : n, hk = h / (a.H / a.Hk);
-  int t0, len;
-  seq_range(a, n, t0, len);
-  const int chunks = (len + C - 1) / C;
-  const int qz = b * a.Hk + hk, vz = b * a.H + h;
+  Piece u;
+  if (!piece_of(a, sp, blockIdx.x, u)) return;
+  const int t0 = u.t0, len = u.len, chunks = u.chunks, qz = u.qz, vz = u.vz;
   const size_t vrow = (size_t)vz * a.T + t0;
-  const size_t st = ((size_t)n * a.H + h) * (size_t)a.dk * a.dv;
+  const size_t states = (size_t)a.dk * a.dv, st = ((size_t)u.n * a.H + u.h) * states;
+  const float* from = u.seg > 0 ? sp.state + ((size_t)(u.item - 1) * a.H + u.h) * states
+                      : a.h0    ? a.h0 + st
+                                : nullptr;
 
   if (tid == 0) {
     for (int i = 0; i < B_COUNT; ++i) {
@@ -172,7 +172,7 @@ linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ 
     }
   } else if (warp == 2) {
     // ------------------------------------------------------------- decays
-    const float* g = a.g_head ? a.g + h : a.g + vrow;
+    const float* g = a.g_head ? a.g + u.h : a.g + vrow;
     const int gs = a.g_head ? 0 : 1;
     float4 x = load_decays(g, gs, min(len, C), lane);
     for (int c = 0; c < chunks; ++c) {
@@ -292,7 +292,7 @@ linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ 
 #pragma unroll
     for (int i = 0; i < 64; ++i) {
       const int d = 64 * s + i;
-      H[i] = a.h0 && r < a.dv && d < a.dk ? a.h0[st + (size_t)d * a.dv + r] : 0.f;
+      H[i] = from && r < a.dv && d < a.dk ? from[(size_t)d * a.dv + r] : 0.f;
     }
     bool ok = true;
     for (int c = 0; c < chunks; ++c) {
@@ -331,7 +331,7 @@ linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ 
       }
       tc_fence_before();
     }
-    if (ok && a.hT && r < a.dv) {
+    if (ok && a.hT && u.seg == u.segs - 1 && r < a.dv) {
 #pragma unroll
       for (int i = 0; i < 64; ++i) {
         const int d = 64 * s + i;
@@ -371,17 +371,25 @@ bool linear_map(CUtensorMap* m, const void* base, uint64_t heads, uint64_t T, ui
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-cudaError_t linear_chunk_fwd(const LinearArgs& a, cudaStream_t s) {
+size_t linear_chunk_fwd_bytes(int N, int B, int H, int T, int dk, int dv, bool packed) {
+  return linear_split_bytes(linear_split(N, B, H, T, packed), N, H, dk, dv, packed, 1);
+}
+
+cudaError_t linear_chunk_fwd(const LinearArgs& a, char* ws, cudaStream_t s) {
   CUtensorMap mq{}, mk{}, mv{}, mo{};
   if (a.T > 0 && (!linear_map(&mq, a.q, (uint64_t)a.B * a.Hk, a.T, a.dk) ||
                   !linear_map(&mk, a.k, (uint64_t)a.B * a.Hk, a.T, a.dk) ||
                   !linear_map(&mv, a.v, (uint64_t)a.B * a.H, a.T, a.dv) ||
                   !linear_map(&mo, a.o, (uint64_t)a.B * a.H, a.T, a.dv)))
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(linear_fwd_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  Split sp = linear_split(a.N, a.B, a.H, a.T, a.cu_seqlens != nullptr);
+  cudaError_t e = linear_split_plan(a, sp, ws, s);
+  if (e == cudaSuccess) e = linear_segment_states(a, sp, ws, false, 0, s);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(linear_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)kSmem);
   if (e != cudaSuccess) return e;
-  linear_fwd_kernel<<<(unsigned)a.N * a.H, kThreads, kSmem, s>>>(a, mq, mk, mv, mo);
+  linear_fwd_kernel<<<(unsigned)sp.items * a.H, kThreads, kSmem, s>>>(a, sp, mq, mk, mv, mo);
   return cudaGetLastError();
 }
 

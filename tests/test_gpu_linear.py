@@ -282,3 +282,23 @@ def test_step_misaligned_state(ck):
     o = ck.linear_decode_step(**p, state=st)
     ref.check(o[:, :, None], want_o, ref.token_tol(F32, 1), "o")
     ref.check(st, want_h, ref.state_tol(F32, 1), "state")
+
+
+# --------------------------------------------------------------- cut sequences
+@pytest.mark.parametrize("T", [1152, 2000, 3071])
+@pytest.mark.parametrize("d", [64, 128])
+def test_few_heads_are_cut_into_segments(ck, T, d):
+    """Far fewer heads than SMs: the sequence runs as segments and a scan joins their states."""
+    x, e = make(1, 2, 1, T, d, d, BF, T, decay=0.02)
+    x["g"][0, 0, T // 2] = -float("inf")
+    compare(ck, x, e, scale=d ** -0.5)
+
+
+def test_no_states_at_either_end_of_segments(ck):
+    x, e = make(2, 1, 1, 1500, 128, 72, BF, 3, decay=0.01, h0=False)
+    compare(ck, x, e, scale=0.1, dh=False)
+
+
+def test_long_packed_sequences_are_cut(ck):
+    cu = [0, 40, 1940, 1940, 3300, 3301]
+    compare(ck, *make(1, 2, 1, 3301, 64, 96, BF, 5, decay=0.02, N=5), scale=0.125, cu=cu)
