@@ -19,6 +19,7 @@ packed sequences when cu_seqlens (int32 [N + 1], B == 1) is given.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -153,6 +154,8 @@ def _io_dtype(t):
 
 
 def _check(t, name, dtype, shape, device):
+    if t.dtype == dtype and t.shape == shape and t.is_contiguous() and t.device == device:
+        return
     if t.dtype != dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if tuple(t.shape) != tuple(shape):
@@ -602,6 +605,31 @@ def decode_step_raw(q_raw, k_raw, v, a_raw, b_raw, state, scale=1.0, normalize_q
     return o
 
 
+# What the calls below share.  A single token or a few rows take the GPU a few
+# microseconds, so the host's part is kept short: plain addresses, and the
+# device switched only when it is another.
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _call(fn, where, device, stream, *args):
+    """fn(*args, stream) on the tensors' device; raises CkdaError."""
+    handle = (torch._C._cuda_getCurrentRawStream(device.index) if stream is None
+              else stream.cuda_stream)
+    if device.index == torch.cuda.current_device():
+        rc = fn(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, handle)
+    if rc != 0:
+        raise CkdaError(rc, where)
+
+
+@functools.lru_cache(maxsize=4096)
+def _bytes(name, *args):
+    return int(getattr(lib(), name)(*args))
+
+
 # ------------------------------------ linear attention with a decay per head
 def _check_linear(q, k, v, g, cu_seqlens, states, more=()):
     """Checks the arguments that linear_fwd and linear_bwd share; returns
@@ -635,12 +663,12 @@ def _check_linear(q, k, v, g, cu_seqlens, states, more=()):
 
 def linear_fwd_workspace_bytes(B, H, T, dk, dv, dtype=torch.bfloat16, num_seqs=0) -> int:
     io = _BF16 if dtype == torch.bfloat16 else _F32
-    return int(lib().ckda_linear_fwd_workspace_bytes(num_seqs, B, H, T, dk, dv, io))
+    return _bytes("ckda_linear_fwd_workspace_bytes", num_seqs, B, H, T, dk, dv, io)
 
 
 def linear_bwd_workspace_bytes(B, H, Hk, T, dk, dv, dtype=torch.bfloat16, num_seqs=0) -> int:
     io = _BF16 if dtype == torch.bfloat16 else _F32
-    return int(lib().ckda_linear_bwd_workspace_bytes(num_seqs, B, H, Hk, T, dk, dv, io))
+    return _bytes("ckda_linear_bwd_workspace_bytes", num_seqs, B, H, Hk, T, dk, dv, io)
 
 
 def linear_fwd(q, k, v, g, h0=None, cu_seqlens=None, scale=1.0, store_final_state=True, o=None,
@@ -663,15 +691,12 @@ def linear_fwd(q, k, v, g, h0=None, cu_seqlens=None, scale=1.0, store_final_stat
         hT = torch.empty((N, H, dk, dv), dtype=torch.float32, device=device)
     nseq = N if cu_seqlens is not None else 0
     if workspace is None:
-        workspace = torch.empty(L.ckda_linear_fwd_workspace_bytes(nseq, B, H, T, dk, dv, io),
-                                dtype=torch.uint8, device=device)
-    with torch.cuda.device(device):
-        rc = L.ckda_linear_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), int(per_head), _ptr(h0),
-                               _ptr(o), _ptr(hT), _ptr(cu_seqlens), nseq, B, H, Hk, T, dk, dv, io,
-                               float(scale), _ptr(workspace), workspace.numel(),
-                               _stream_handle(stream, device))
-    if rc != 0:
-        raise CkdaError(rc, "ckda_linear_fwd")
+        workspace = torch.empty(
+            _bytes("ckda_linear_fwd_workspace_bytes", nseq, B, H, T, dk, dv, io),
+            dtype=torch.uint8, device=device)
+    _call(L.ckda_linear_fwd, "ckda_linear_fwd", device, stream, _addr(q), _addr(k), _addr(v),
+          _addr(g), int(per_head), _addr(h0), _addr(o), _addr(hT), _addr(cu_seqlens), nseq, B,
+          H, Hk, T, dk, dv, io, float(scale), _addr(workspace), workspace.numel())
     linear_fwd.last_workspace = workspace
     return o, hT
 
@@ -687,19 +712,16 @@ def linear_bwd(q, k, v, g, do, h0=None, dhT=None, cu_seqlens=None, scale=1.0, st
                                                          (("h0", h0), ("dhT", dhT)), (("do", do),))
     nseq = N if cu_seqlens is not None else 0
     if workspace is None:
-        workspace = torch.empty(L.ckda_linear_bwd_workspace_bytes(nseq, B, H, Hk, T, dk, dv, io),
-                                dtype=torch.uint8, device=device)
+        workspace = torch.empty(
+            _bytes("ckda_linear_bwd_workspace_bytes", nseq, B, H, Hk, T, dk, dv, io),
+            dtype=torch.uint8, device=device)
     dq, dkk, dvv, dg = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v),
                         torch.empty_like(g))
     dh0 = torch.empty((N, H, dk, dv), dtype=torch.float32, device=device) if store_dh0 else None
-    with torch.cuda.device(device):
-        rc = L.ckda_linear_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), int(per_head), _ptr(h0),
-                               _ptr(do), _ptr(dhT), _ptr(dq), _ptr(dkk), _ptr(dvv), _ptr(dg),
-                               _ptr(dh0), _ptr(cu_seqlens), nseq, B, H, Hk, T, dk, dv, io,
-                               float(scale), _ptr(workspace), workspace.numel(),
-                               _stream_handle(stream, device))
-    if rc != 0:
-        raise CkdaError(rc, "ckda_linear_bwd")
+    _call(L.ckda_linear_bwd, "ckda_linear_bwd", device, stream, _addr(q), _addr(k), _addr(v),
+          _addr(g), int(per_head), _addr(h0), _addr(do), _addr(dhT), _addr(dq), _addr(dkk),
+          _addr(dvv), _addr(dg), _addr(dh0), _addr(cu_seqlens), nseq, B, H, Hk, T, dk, dv, io,
+          float(scale), _addr(workspace), workspace.numel())
     linear_bwd.last_workspace = workspace
     return dq, dkk, dvv, dg, dh0
 
@@ -727,12 +749,9 @@ def linear_decode_step(q, k, v, g, state, scale=1.0, o=None, stream=None):
         o = torch.empty((B, H, dv), dtype=dt, device=device)
     else:
         _check(o, "o", dt, (B, H, dv), device)
-    with torch.cuda.device(device):
-        rc = L.ckda_linear_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), int(per_head),
-                                       _ptr(state), _ptr(o), B, H, Hk, dk, dv, io, float(scale),
-                                       _stream_handle(stream, device))
-    if rc != 0:
-        raise CkdaError(rc, "ckda_linear_decode_step")
+    _call(L.ckda_linear_decode_step, "ckda_linear_decode_step", device, stream, _addr(q),
+          _addr(k), _addr(v), _addr(g), int(per_head), _addr(state), _addr(o), B, H, Hk, dk, dv,
+          io, float(scale))
     return o
 
 
@@ -773,12 +792,9 @@ def layernorm_fwd(x, weight=None, bias=None, eps=1e-5, y=None, mean=None, rstd=N
         rstd = torch.empty(lead, dtype=torch.float32, device=device)
     else:
         _check(rstd, "rstd", torch.float32, lead, device)
-    with torch.cuda.device(device):
-        rc = L.ckda_layernorm_fwd(_ptr(x), _ptr(weight), _ptr(bias), _ptr(y), _ptr(mean),
-                                  _ptr(rstd), mean.numel(), width, io, wcode, float(eps),
-                                  _stream_handle(stream, device))
-    if rc != 0:
-        raise CkdaError(rc, "ckda_layernorm_fwd")
+    _call(L.ckda_layernorm_fwd, "ckda_layernorm_fwd", device, stream, _addr(x), _addr(weight),
+          _addr(bias), _addr(y), _addr(mean), _addr(rstd), mean.numel(), width, io, wcode,
+          float(eps))
     return y, mean, rstd
 
 
@@ -809,15 +825,11 @@ def layernorm_bwd(dy, x, mean, rstd, weight=None, weight_grad=True, dx=None, wor
         dw = torch.empty(width, dtype=wdt, device=device)
         db = torch.empty(width, dtype=wdt, device=device)
         if workspace is None:
-            workspace = torch.empty(L.ckda_layernorm_bwd_workspace_bytes(rows, width),
+            workspace = torch.empty(_bytes("ckda_layernorm_bwd_workspace_bytes", rows, width),
                                     dtype=torch.uint8, device=device)
-    with torch.cuda.device(device):
-        rc = L.ckda_layernorm_bwd(_ptr(dy), _ptr(x), _ptr(mean), _ptr(rstd), _ptr(weight),
-                                  _ptr(dx), _ptr(dw), _ptr(db), rows, width, io, wcode,
-                                  _ptr(workspace), 0 if workspace is None else workspace.numel(),
-                                  _stream_handle(stream, device))
-    if rc != 0:
-        raise CkdaError(rc, "ckda_layernorm_bwd")
+    _call(L.ckda_layernorm_bwd, "ckda_layernorm_bwd", device, stream, _addr(dy), _addr(x),
+          _addr(mean), _addr(rstd), _addr(weight), _addr(dx), _addr(dw), _addr(db), rows, width,
+          io, wcode, _addr(workspace), 0 if workspace is None else workspace.numel())
     return dx, dw, db
 
 
