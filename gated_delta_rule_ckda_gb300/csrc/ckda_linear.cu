@@ -38,11 +38,14 @@ extern "C" {
 size_t ckda_linear_fwd_workspace_bytes(int num_seqs, int B, int H, int T, int dk, int dv,
                                        ckda_dtype io_dtype) {
   if (num_seqs < 0 || B < 1 || H < 1 || T < 0 || dk < 1 || dv < 1) return 0;
-  const size_t chunk =
-      linear_chunk_path(io_dtype, dk, dv)
-          ? linear_chunk_fwd_bytes(num_seqs > 0 ? num_seqs : B, B, H, T, dk, dv, num_seqs > 0)
-          : 0;
-  return head_bytes(num_seqs) + chunk;
+  const int N = num_seqs > 0 ? num_seqs : B;
+  // what either path takes: which one runs depends on the pointers' alignment too
+  size_t bytes = linear_serial_fwd_bytes(N, H, T, dk, dv, num_seqs > 0);
+  if (linear_chunk_path(io_dtype, dk, dv)) {
+    const size_t chunk = linear_chunk_fwd_bytes(N, B, H, T, dk, dv, num_seqs > 0);
+    if (chunk > bytes) bytes = chunk;
+  }
+  return head_bytes(num_seqs) + bytes;
 }
 
 ckda_status ckda_linear_fwd(const void* q, const void* k, const void* v, const float* g,
@@ -68,6 +71,7 @@ ckda_status ckda_linear_fwd(const void* q, const void* k, const void* v, const f
   a.g_head = g_per_head ? 1 : 0;
   a.scale = scale; a.io = io_dtype;
   if (cudaMemsetAsync(workspace, 0, sizeof(int), s) != cudaSuccess) return CKDA_ERR_CUDA;
+  char* scratch = static_cast<char*>(workspace) + head_bytes(cu_seqlens ? num_seqs : 0);
   cudaError_t e = cudaSuccess;
   if (linear_chunk_path(io_dtype, dk, dv) && aligned16(q) && aligned16(k) && aligned16(v) &&
       aligned16(o)) {
@@ -76,10 +80,9 @@ ckda_status ckda_linear_fwd(const void* q, const void* k, const void* v, const f
       e = launch_seq_order(cu_seqlens, num_seqs, order, s);
       a.order = order;
     }
-    char* scratch = static_cast<char*>(workspace) + head_bytes(cu_seqlens ? num_seqs : 0);
     if (e == cudaSuccess) e = linear_chunk_fwd(a, scratch, s);
   } else {
-    e = linear_serial_fwd(a, s);
+    e = linear_serial_fwd(a, scratch, s);
   }
   return e == cudaSuccess ? CKDA_OK : CKDA_ERR_CUDA;
 }

@@ -11,7 +11,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // A decay of exp2(-160) is zero in fp32 whatever it multiplies; log decays are
 // clamped there so that g = -inf (a reset) leaves sums and differences finite.
 constexpr float kMinLog2Decay = -160.f;
-constexpr int kCkptTokens = 64;    // token-serial backward: tokens between stored states
+constexpr int kCkptTokens = 64;    // token-serial backward: tokens of a piece
 
 struct LinearArgs {
   const void* q;      // io   [B, Hk, T, dk]
@@ -56,7 +56,8 @@ __device__ __forceinline__ float log2_decay(float g) {
 }
 
 // Token-serial kernels on CUDA cores: every type and width up to 128.
-cudaError_t linear_serial_fwd(const LinearArgs& a, cudaStream_t s);
+size_t linear_serial_fwd_bytes(int N, int H, int T, int dk, int dv, bool packed);
+cudaError_t linear_serial_fwd(const LinearArgs& a, char* ws, cudaStream_t s);
 size_t linear_serial_bwd_bytes(int N, int B, int H, int T, int dk, int dv, bool packed);
 cudaError_t linear_serial_bwd(const LinearArgs& a, char* ws, cudaStream_t s);
 

@@ -10,12 +10,19 @@
 //   dq : forward,         c over dk, y = k,  x = v,  z = do, a_t = e^{g_t}
 //   dk : backward,        c over dk, y = q,  x = do, z = v,  a_t = e^{g_{t+1}}
 //   dv : backward,        c over dv, y = do, x = q,  z = k,  a_t = e^{g_{t+1}}
-// The rows of S do not meet, so a block owns 32 of them and a unit (sequence,
-// head) spreads over ceil(rows / 32) blocks; four threads share a row, each
-// with every fourth group of four columns in registers.  Per token a thread
-// does one fma for the update and one for the readout per column, on x and z
-// from shared memory, so the bound is the latency of a token times the tokens
-// of a unit, and FMA throughput when the units fill the SMs.
+// The rows of S do not meet, so a block owns 32 of them and a (sequence, head)
+// spreads over ceil(rows / 32) blocks; four threads share a row, each with every
+// fourth group of four columns in registers.  Per token a thread does one fma
+// for the update and one for the readout per column, on x and z from shared
+// memory, 64 tokens of which are staged at a time: the bound is the latency of a
+// token, and FMA throughput when the blocks fill the SMs.
+//
+// Tokens are serial, so a sequence is cut into pieces that run side by side: a
+// first kernel sums each piece's own contribution to the state (all tokens with
+// their decay to the piece's end, in no order), a scan joins them, and then every
+// piece's runs start from the state that enters them.  Backward a piece is 64
+// tokens, whatever the size; forward as many as leave enough blocks for the SMs,
+// or the whole sequence where the heads alone do.
 //
 // The decay's gradient is dg_t = <H_{t-1} e^{g_t}, dL/dH_t>.  With L the
 // cumulative log decay, dL/dL_i = q_i.dq_i - k_i.dk_i, and dg is its suffix
@@ -25,257 +32,389 @@
 //     touches and which is the largest term under strong decay, is left out:
 //     the dq and dk runs read the decayed state before the token's write, and
 //     the own part, k_t (v_t.do_t) and q_t (v_t.do_t), joins dq and dk last;
-//   - the sum restarts every kCkptTokens tokens from <H, dL/dH> itself: the dq
-//     run stores the state there and the dk run, which holds dL/dH in the same
-//     layout, takes the product.
+//   - the sum restarts at every piece from <H, dL/dH> itself.
 #include "ckda_linear.cuh"
 
 namespace ckda {
 namespace {
 
-constexpr int kTok = 16;     // tokens staged at a time
+constexpr int kTok = 64;     // tokens staged at a time
 constexpr int kOwn = 32;     // state rows of a block
 constexpr int kSplit = 4;    // threads of a row
+constexpr int kThreads = kOwn * kSplit;
 
 enum { RUN_O, RUN_DQ, RUN_DK, RUN_DV };
 
+// Pieces of a sequence, and the tables over them.  Slot p of a sequence is the
+// state entering its piece p (H) or the gradient of that state (G); the slot
+// after its last piece is the final state's.
+struct Pieces {
+  int tokens;             // of a piece
+  const int32_t* slot0;   // packed: [N + 1] first slot of a sequence
+  size_t slots;           // of a head
+  float* H;               // [slots][H][dk][dv]
+  float* G;
+};
 struct SerialWs {
+  Pieces p;
   float* dq;      // [B, H, T, dk], without the token's own part
   float* dk;      // [B, H, T, dk], the same
   float* dg;      // [B, H, T] (a decay per head only)
   float* own;     // [B, H, T]: scale v_t.do_t
-  float* ckpt;    // [slots][dk][dv]: the state entering each 64-token piece, and the last one
-  float* dots;    // [slots][slices]: <H, dL/dH> at each piece's end
-  int32_t* slot0; // [N + 1]: first slot of a sequence (packed; times H)
-  size_t slots;   // slots of a head in the workspace
 };
 
-// Slots of sequence n of len tokens: its pieces, and one for its final state.
-__host__ __device__ inline int pieces_of(int len) { return (len + kCkptTokens - 1) / kCkptTokens; }
+__host__ __device__ inline int pieces_of(int len, int tokens) { return (len + tokens - 1) / tokens; }
 
-__device__ __forceinline__ size_t slot_of(const LinearArgs& a, const SerialWs& w, int n, int h,
-                                          int piece) {
-  const size_t first = a.cu_seqlens ? (size_t)w.slot0[n] : (size_t)n * (pieces_of(a.T) + 1);
-  // (offsets that are no packing would run past the workspace)
-  const size_t slot = first + piece;
-  return (slot < w.slots ? slot : w.slots - 1) * a.H + h;
+// A piece of one (sequence, head).
+struct Where {
+  int n, h, piece, pieces;
+  int t0, len;            // its tokens on the T axis
+  size_t slot;            // of the state entering it
+  size_t krow, vrow;      // row of its first token in q, k and in v, do, ...
+};
+// Block x runs over slots times heads, final states' slots among them; false
+// where there is no piece.
+__device__ __forceinline__ bool where(const LinearArgs& a, const Pieces& p, size_t block, Where& u) {
+  size_t s = block / a.H;
+  u.h = block % a.H;
+  u.slot = s;
+  if (a.cu_seqlens) {
+    if (s >= (size_t)p.slot0[a.N]) return false;
+    int lo = 0, hi = a.N;  // slot0[lo] <= s < slot0[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if ((size_t)p.slot0[mid] <= s) lo = mid; else hi = mid;
+    }
+    u.n = lo;
+    u.piece = (int)(s - p.slot0[lo]);
+  } else {
+    const int per = pieces_of(a.T, p.tokens) + 1;
+    u.n = (int)(s / per);
+    u.piece = (int)(s % per);
+  }
+  int t0, len;
+  seq_range(a, u.n, t0, len);
+  u.pieces = pieces_of(len, p.tokens);
+  u.t0 = t0 + u.piece * p.tokens;
+  u.len = min(len - u.piece * p.tokens, p.tokens);
+  const int b = a.cu_seqlens ? 0 : u.n, hk = u.h / (a.H / a.Hk);
+  u.krow = ((size_t)b * a.Hk + hk) * a.T + u.t0;
+  u.vrow = ((size_t)b * a.H + u.h) * a.T + u.t0;
+  return true;
 }
 
-__global__ void slot_plan_kernel(LinearArgs a, int32_t* slot0) {
+__global__ void slot_plan_kernel(LinearArgs a, int tokens, int32_t* slot0) {
   // one block; each thread adds up a run of sequences, then the runs are joined
   __shared__ int32_t sum[1024];
-  const int per = (a.N + 1023) / 1024, i0 = threadIdx.x * per;
+  const int per = (a.N + 1023) / 1024, i0 = threadIdx.x * per, i1 = min(i0 + per, a.N);
   int32_t s = 0;
-  for (int i = i0; i < min(i0 + per, a.N); ++i) {
+  for (int i = i0; i < i1; ++i) {
     int t0, len;
     seq_range(a, i, t0, len);
-    s += pieces_of(len) + 1;
+    s += pieces_of(len, tokens) + 1;
   }
   sum[threadIdx.x] = s;
   __syncthreads();
   int32_t before = 0;
   for (int j = 0; j < (int)threadIdx.x; ++j) before += sum[j];
-  for (int i = i0; i < min(i0 + per, a.N); ++i) {
+  for (int i = i0; i < i1; ++i) {
     slot0[i] = before;
     int t0, len;
     seq_range(a, i, t0, len);
-    before += pieces_of(len) + 1;
+    before += pieces_of(len, tokens) + 1;
+  }
+  if (threadIdx.x == 1023) slot0[a.N] = before;
+}
+
+// Register i of a thread's quarter p of a row: column.
+__device__ __forceinline__ int col(int p, int i) { return 4 * (p + kSplit * (i / 4)) + i % 4; }
+
+// Stages `nt` tokens of `n` columns from `c0` on into [kTok][WIDTH], the rest
+// zeros; back: in reverse, ending with the token at `src`.
+template <typename IO, int WIDTH>
+__device__ __forceinline__ void stage(float* dst, const IO* src, int stride, int c0, int n, int nt,
+                                      float scale, bool back) {
+#pragma unroll 8
+  for (int e = threadIdx.x; e < kTok * WIDTH; e += kThreads) {
+    const int tt = e / WIDTH, c = e % WIDTH;
+    const size_t t = back ? nt - 1 - tt : tt;
+    dst[e] = tt < nt && c < n ? scale * ld_io(src + t * stride + c0 + c) : 0.f;
   }
 }
 
-// R4: columns of a thread / 4 (so R <= 16 R4 contracted columns).
+// A piece's own contribution to the state after it (block z = 0: over k and v,
+// into the slot behind it) or to the gradient of the state before it (z = 1:
+// over q and do, into its own slot).  R4: columns of a thread / 4.
+template <typename IO, int R4>
+__global__ void __launch_bounds__(kThreads) piece_sum_kernel(LinearArgs a, Pieces p, int first_z) {
+  constexpr int kR = 16 * R4;
+  extern __shared__ __align__(16) float sm[];
+  float *sx = sm, *sy = sm + kTok * kR, *sw = sy + kTok * kOwn;
+  Where u;
+  if (!where(a, p, blockIdx.x, u) || u.piece >= u.pieces) return;
+  const bool back = blockIdx.z + first_z == 1;
+  const IO* X = back ? static_cast<const IO*>(a.dout) + u.vrow * a.dv
+                     : static_cast<const IO*>(a.v) + u.vrow * a.dv;
+  const IO* Y = (back ? static_cast<const IO*>(a.q) : static_cast<const IO*>(a.k)) + u.krow * a.dk;
+  const float* g = a.g_head ? a.g + u.h : a.g + u.vrow;
+  const int gs = a.g_head ? 0 : 1;
+  const int own = threadIdx.x / kSplit, part = threadIdx.x % kSplit;
+  const int c0 = blockIdx.y * kOwn, c = c0 + own;
+  float S[4 * R4];
+#pragma unroll
+  for (int i = 0; i < 4 * R4; ++i) S[i] = 0.f;
+  float* out = (back ? p.G : p.H);
+  const size_t slot = min(u.slot + (back ? 0 : 1), p.slots - 1);
+  out += (slot * a.H + u.h) * (size_t)a.dk * a.dv;
+  // tiles of 64 tokens in the direction of time, backward against it: the
+  // decays of later tiles multiply what is there
+  for (int s0 = 0; s0 < u.len; s0 += kTok) {
+    const int nt = min(kTok, u.len - s0), t0 = back ? u.len - s0 - nt : s0;
+    __syncthreads();
+    stage<IO, kR>(sx, X + (size_t)t0 * a.dv, a.dv, 0, a.dv, nt, 1.f, false);
+    stage<IO, kOwn>(sy, Y + (size_t)t0 * a.dk, a.dk, c0, min(kOwn, a.dk - c0), nt,
+                    back ? a.scale : 1.f, false);
+    if (threadIdx.x < kTok) sw[kTok + threadIdx.x] =
+        (int)threadIdx.x < nt ? g[(size_t)(t0 + threadIdx.x) * gs] : 0.f;
+    __syncthreads();
+    if (threadIdx.x <= kTok) {
+      // forward: from after token t to the tile's end; backward: from its start
+      // to t; entry kTok: over the tile
+      const int t = threadIdx.x;
+      float x = 0.f;
+      if (t == kTok || back)
+        for (int i = 0; i < (t == kTok ? nt : min(t + 1, nt)); ++i) x += sw[kTok + i];
+      else
+        for (int i = nt - 1; i > t; --i) x += sw[kTok + i];
+      sw[t == kTok ? 2 * kTok : t] = expf(x);
+    }
+    __syncthreads();
+    const float all = sw[2 * kTok];
+#pragma unroll
+    for (int i = 0; i < 4 * R4; ++i) S[i] *= s0 ? all : 1.f;
+#pragma unroll 2
+    for (int t = 0; t < nt; ++t) {
+      const float y = sw[t] * sy[t * kOwn + own];
+#pragma unroll
+      for (int i = 0; i < 4 * R4; ++i) S[i] = fmaf(y, sx[t * kR + col(part, i)], S[i]);
+    }
+  }
+  if (c < a.dk)
+#pragma unroll
+    for (int i = 0; i < 4 * R4; ++i)
+      if (col(part, i) < a.dv) out[(size_t)c * a.dv + col(part, i)] = S[i];
+}
+
+// Joins the pieces, in place: H[p + 1] = e^{g over p} H[p] + its own, from h0, and
+// G[p] = e^{g over p} G[p + 1] + its own, from dhT (back).
+__global__ void __launch_bounds__(256) piece_scan_kernel(LinearArgs a, Pieces p, int first_z) {
+  __shared__ float dec[256];
+  const bool back = blockIdx.z + first_z == 1;
+  const int n = blockIdx.x / a.H, h = blockIdx.x % a.H, b = a.cu_seqlens ? 0 : n;
+  int t0, len;
+  seq_range(a, n, t0, len);
+  const int pieces = pieces_of(len, p.tokens);
+  const size_t first = a.cu_seqlens ? (size_t)p.slot0[n]
+                                    : (size_t)n * (pieces_of(a.T, p.tokens) + 1);
+  const int states = a.dk * a.dv, e = blockIdx.y * 256 + threadIdx.x;
+  const float* g = a.g_head ? a.g + h : a.g + ((size_t)b * a.H + h) * a.T + t0;
+  const int gs = a.g_head ? 0 : 1;
+  auto at = [&](int k) {  // slot k of this sequence
+    return (min(first + k, p.slots - 1) * a.H + h) * (size_t)states + e;
+  };
+  float* S = back ? p.G : p.H;
+  const float* from = back ? a.dhT : a.h0;
+  const size_t st = ((size_t)n * a.H + h) * states + e;
+  float s = from && e < states ? from[st] : 0.f;
+  if (e < states) S[at(back ? pieces : 0)] = s;
+  for (int k0 = 0; k0 < pieces; k0 += 256) {
+    // the decays of up to 256 pieces, a warp a piece in turn
+    __syncthreads();
+    const int nk = min(256, pieces - k0);
+    for (int k = threadIdx.x >> 5; k < nk; k += 8) {
+      const int piece = back ? pieces - 1 - (k0 + k) : k0 + k, i0 = piece * p.tokens;
+      double x = 0.0;
+      for (int i = i0 + (threadIdx.x & 31); i < min(i0 + p.tokens, len); i += 32)
+        x += (double)g[(size_t)i * gs];
+#pragma unroll
+      for (int m = 16; m >= 1; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
+      if ((threadIdx.x & 31) == 0) dec[k] = (float)exp(x);
+    }
+    __syncthreads();
+    if (e < states) {
+#pragma unroll 4
+      for (int k = 0; k < nk; ++k) {
+        float* q = S + at(back ? pieces - 1 - (k0 + k) : k0 + k + 1);
+        s = fmaf(dec[k], s, *q);
+        *q = s;
+      }
+    }
+  }
+  if (e < states) {
+    if (!back && a.hT) a.hT[st] = s;
+    if (back && a.dh0) a.dh0[st] = s;
+  }
+}
+
+// A run over the tokens of a piece (or, without tables, of a sequence).  R4:
+// columns of a thread / 4 (so R <= 16 R4 contracted columns).
 template <typename IO, typename OUT, int RUN, int R4>
-__global__ void __launch_bounds__(kOwn* kSplit) serial_kernel(LinearArgs a, SerialWs w, OUT* out) {
+__device__ __forceinline__ void run_piece(const LinearArgs& a, const Pieces& p, const Where& u,
+                                          int slice, OUT* out, float* sm) {
   constexpr bool kBack = RUN == RUN_DK || RUN == RUN_DV;
   constexpr bool kOwnV = RUN == RUN_O || RUN == RUN_DV;   // rows are value columns
   constexpr bool kDecayed = RUN == RUN_DQ || RUN == RUN_DK;  // read before the write
   constexpr int kR = 16 * R4;
-  __shared__ __align__(16) float sx[kTok][kR], sz[kTok][kR], sy[kTok][kOwn];
-  __shared__ float sa[kTok];
-  __shared__ float red[kOwn * kSplit / 32];
+  float *sx = sm, *sz = sx + kTok * kR, *sy = sz + kTok * kR, *sa = sy + kTok * kOwn;
 
-  const int unit = blockIdx.x, n = unit / a.H, h = unit % a.H;
-  const int b = a.cu_seqlens ? 0 : n, hk = h / (a.H / a.Hk);
-  int t0, len;
-  seq_range(a, n, t0, len);
   const int own_n = kOwnV ? a.dv : a.dk, R = kOwnV ? a.dk : a.dv;
-  const size_t krow = ((size_t)b * a.Hk + hk) * a.T + t0;  // first row of q and k
-  const size_t vrow = ((size_t)b * a.H + h) * a.T + t0;    // first row of v, do, o, dq, ...
-  const IO* q = static_cast<const IO*>(a.q) + krow * a.dk;
-  const IO* k = static_cast<const IO*>(a.k) + krow * a.dk;
-  const IO* v = static_cast<const IO*>(a.v) + vrow * a.dv;
-  const IO* dout = static_cast<const IO*>(a.dout) + vrow * a.dv;
+  const IO* q = static_cast<const IO*>(a.q) + u.krow * a.dk;
+  const IO* k = static_cast<const IO*>(a.k) + u.krow * a.dk;
+  const IO* v = static_cast<const IO*>(a.v) + u.vrow * a.dv;
+  const IO* dout = static_cast<const IO*>(a.dout) + u.vrow * a.dv;
   const IO* X = RUN == RUN_O ? k : RUN == RUN_DQ ? v : RUN == RUN_DK ? dout : q;
   const IO* Y = RUN == RUN_O ? v : RUN == RUN_DQ ? k : RUN == RUN_DK ? q : dout;
   const IO* Z = RUN == RUN_O ? q : RUN == RUN_DQ ? dout : RUN == RUN_DK ? v : k;
   // where the query scale goes: on the readout of o and dq, into the state of dk and dv
   const float out_scale = kBack ? 1.f : a.scale, y_scale = kBack ? a.scale : 1.f;
-  const float* g = a.g_head ? a.g + h : a.g + vrow;
+  const float* g = a.g_head ? a.g + u.h : a.g + u.vrow;
   const int gs = a.g_head ? 0 : 1;
 
-  const int own = threadIdx.x / kSplit, p = threadIdx.x % kSplit;
-  const int c0 = blockIdx.y * kOwn, c = c0 + own;
+  const int own = threadIdx.x / kSplit, part = threadIdx.x % kSplit;
+  const int c0 = slice * kOwn, c = c0 + own;
   const bool row = c < own_n;
-  auto col = [&](int i) { return 4 * (p + kSplit * (i / 4)) + i % 4; };  // of register i
   // element (row c, column r) of a [dk, dv] state
   auto at = [&](int r) { return kOwnV ? (size_t)r * a.dv + c : (size_t)c * a.dv + r; };
 
   float S[4 * R4];
-  const float* init = kBack ? a.dhT : a.h0;
-  const size_t st = ((size_t)n * a.H + h) * (size_t)a.dk * a.dv;
+  const size_t states = (size_t)a.dk * a.dv;
+  const float* init;
+  if (kBack)
+    init = p.G + (min(u.slot + 1, p.slots - 1) * a.H + u.h) * states;
+  else if (p.H)
+    init = p.H + (u.slot * a.H + u.h) * states;
+  else
+    init = a.h0 ? a.h0 + ((size_t)u.n * a.H + u.h) * states : nullptr;
 #pragma unroll
   for (int i = 0; i < 4 * R4; ++i)
-    S[i] = init && row && col(i) < R ? init[st + at(col(i))] : 0.f;
+    S[i] = init && row && col(part, i) < R ? init[at(col(part, i))] : 0.f;
 
-  // <stored state, S> over this block's rows, at the end of a piece (dk run)
-  auto take_dot = [&](int piece) {
-    const float* ck = w.ckpt + slot_of(a, w, n, h, piece + 1) * (size_t)a.dk * a.dv;
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4 * R4; ++i)
-      if (row && col(i) < R) s = fmaf(S[i], ck[at(col(i))], s);
-#pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+  for (int s0 = 0; s0 < u.len; s0 += kTok) {
+    const int nt = min(kTok, u.len - s0), t0 = kBack ? u.len - s0 - nt : s0;
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      float t = 0.f;
-      for (int i = 0; i < kOwn * kSplit / 32; ++i) t += red[i];
-      w.dots[slot_of(a, w, n, h, piece) * gridDim.y + blockIdx.y] = t;
-    }
-  };
-  auto store_ckpt = [&](int piece) {
-    float* ck = w.ckpt + slot_of(a, w, n, h, piece) * (size_t)a.dk * a.dv;
-#pragma unroll
-    for (int i = 0; i < 4 * R4; ++i)
-      if (row && col(i) < R) ck[at(col(i))] = S[i];
-  };
-
-  for (int s0 = 0; s0 < len; s0 += kTok) {
-    const int nt = min(kTok, len - s0);
-    __syncthreads();
-    for (int e = threadIdx.x; e < kTok * kR; e += kOwn * kSplit) {
-      const int tt = e / kR, r = e % kR;
-      const size_t t = kBack ? len - 1 - (s0 + tt) : s0 + tt;
-      const bool in = tt < nt && r < R;
-      sx[tt][r] = in ? ld_io(X + t * R + r) : 0.f;
-      sz[tt][r] = in ? ld_io(Z + t * R + r) : 0.f;
-    }
-    for (int e = threadIdx.x; e < kTok * kOwn; e += kOwn * kSplit) {
-      const int tt = e / kOwn, cc = e % kOwn;
-      const size_t t = kBack ? len - 1 - (s0 + tt) : s0 + tt;
-      sy[tt][cc] = tt < nt && c0 + cc < own_n ? y_scale * ld_io(Y + t * own_n + c0 + cc) : 0.f;
-    }
+    stage<IO, kR>(sx, X + (size_t)t0 * R, R, 0, R, nt, 1.f, kBack);
+    stage<IO, kR>(sz, Z + (size_t)t0 * R, R, 0, R, nt, 1.f, kBack);
+    stage<IO, kOwn>(sy, Y + (size_t)t0 * own_n, own_n, c0, min(kOwn, own_n - c0), nt, y_scale,
+                    kBack);
     if (threadIdx.x < kTok && (int)threadIdx.x < nt) {
-      const int i = s0 + threadIdx.x;
-      // backward, the decay from token t + 1 to t; none into the last token
-      sa[threadIdx.x] = kBack ? (i == 0 ? 1.f : expf(g[(size_t)(len - i) * gs]))
-                              : expf(g[(size_t)i * gs]);
+      const int t = kBack ? t0 + nt - 1 - threadIdx.x : t0 + threadIdx.x;
+      // backward, the decay from token t + 1 to t; none into the piece's last token
+      sa[threadIdx.x] = kBack ? (t == u.len - 1 ? 1.f : expf(g[(size_t)(t + 1) * gs]))
+                              : expf(g[(size_t)t * gs]);
     }
     __syncthreads();
     for (int tt = 0; tt < nt; ++tt) {
-      const int t = kBack ? len - 1 - (s0 + tt) : s0 + tt;
-      if (RUN == RUN_DQ && t % kCkptTokens == 0) store_ckpt(t / kCkptTokens);
-      const float dec = sa[tt], y = sy[tt][own];
-      float acc = 0.f;
-      if (kDecayed) {
+      const int t = kBack ? t0 + nt - 1 - tt : t0 + tt;
+      const float dec = sa[tt], y = sy[tt * kOwn + own];
+      const float *x = sx + tt * kR, *z = sz + tt * kR;
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};  // four chains: the sum is the token's latency
 #pragma unroll
-        for (int i = 0; i < 4 * R4; ++i) {
+      for (int i = 0; i < 4 * R4; ++i) {
+        if (kDecayed) {
           S[i] *= dec;
-          acc = fmaf(S[i], sz[tt][col(i)], acc);
-        }
-        if (RUN == RUN_DK && (t == len - 1 || t % kCkptTokens == kCkptTokens - 1))
-          take_dot(t / kCkptTokens);
-#pragma unroll
-        for (int i = 0; i < 4 * R4; ++i) S[i] = fmaf(y, sx[tt][col(i)], S[i]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4 * R4; ++i) {
-          S[i] = fmaf(dec, S[i], y * sx[tt][col(i)]);
-          acc = fmaf(S[i], sz[tt][col(i)], acc);
+          acc[i % 4] = fmaf(S[i], z[col(part, i)], acc[i % 4]);
+          S[i] = fmaf(y, x[col(part, i)], S[i]);
+        } else {
+          S[i] = fmaf(dec, S[i], y * x[col(part, i)]);
+          acc[i % 4] = fmaf(S[i], z[col(part, i)], acc[i % 4]);
         }
       }
-      acc += __shfl_xor_sync(0xffffffffu, acc, 1);
-      acc += __shfl_xor_sync(0xffffffffu, acc, 2);
-      if (p == 0 && row) st_io(out + (vrow + t) * own_n + c, out_scale * acc);
+      float s = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+      s += __shfl_xor_sync(0xffffffffu, s, 1);
+      s += __shfl_xor_sync(0xffffffffu, s, 2);
+      if (part == 0 && row) st_io(out + (u.vrow + t) * own_n + c, out_scale * s);
     }
   }
-  if (RUN == RUN_DQ) store_ckpt(pieces_of(len));
-  if (RUN == RUN_DK && a.dh0) {
-    const float dec = len > 0 ? expf(g[0]) : 1.f;
+  if (RUN == RUN_O && !p.H && a.hT && row) {
+    float* to = a.hT + ((size_t)u.n * a.H + u.h) * states;
 #pragma unroll
     for (int i = 0; i < 4 * R4; ++i)
-      if (row && col(i) < R) a.dh0[st + at(col(i))] = dec * S[i];
-  }
-  if (RUN == RUN_O && a.hT) {
-#pragma unroll
-    for (int i = 0; i < 4 * R4; ++i)
-      if (row && col(i) < R) a.hT[st + at(col(i))] = S[i];
+      if (col(part, i) < R) to[at(col(part, i))] = S[i];
   }
 }
 
-template <typename IO, typename OUT, int RUN>
-cudaError_t launch_run(const LinearArgs& a, const SerialWs& w, OUT* out, cudaStream_t s) {
-  constexpr bool kOwnV = RUN == RUN_O || RUN == RUN_DV;
-  const int own = kOwnV ? a.dv : a.dk, R = kOwnV ? a.dk : a.dv;
-  const dim3 grid((unsigned)a.N * a.H, (own + kOwn - 1) / kOwn);
-  if (R <= 32)
-    serial_kernel<IO, OUT, RUN, 2><<<grid, kOwn * kSplit, 0, s>>>(a, w, out);
-  else if (R <= 64)
-    serial_kernel<IO, OUT, RUN, 4><<<grid, kOwn * kSplit, 0, s>>>(a, w, out);
+template <typename IO, int R4>
+__global__ void __launch_bounds__(kThreads) run_o_kernel(LinearArgs a, Pieces p) {
+  extern __shared__ __align__(16) float sm[];
+  Where u;
+  if (!where(a, p, blockIdx.x, u)) return;
+  // (uncut, an empty sequence still hands its state on)
+  if (u.piece >= u.pieces && !(u.piece == 0 && !p.H)) return;
+  if (u.len < 0) u.len = 0;
+  run_piece<IO, IO, RUN_O, R4>(a, p, u, blockIdx.y, static_cast<IO*>(a.o), sm);
+}
+
+// dq, dk and dv side by side, as block z.
+template <typename IO, int R4K, int R4V>
+__global__ void __launch_bounds__(kThreads) run_grads_kernel(LinearArgs a, SerialWs w) {
+  extern __shared__ __align__(16) float sm[];
+  const int slice = blockIdx.y;
+  Where u;
+  if (!where(a, w.p, blockIdx.x, u) || u.piece >= u.pieces) return;
+  if (slice * kOwn >= (blockIdx.z == 2 ? a.dv : a.dk)) return;
+  if (blockIdx.z == 0)
+    run_piece<IO, float, RUN_DQ, R4V>(a, w.p, u, slice, w.dq, sm);
+  else if (blockIdx.z == 1)
+    run_piece<IO, float, RUN_DK, R4V>(a, w.p, u, slice, w.dk, sm);
   else
-    serial_kernel<IO, OUT, RUN, 8><<<grid, kOwn * kSplit, 0, s>>>(a, w, out);
-  return cudaGetLastError();
+    run_piece<IO, IO, RUN_DV, R4K>(a, w.p, u, slice, static_cast<IO*>(a.dval), sm);
 }
 
-// dg, a piece of one (sequence, head) at a time: each of the four warps takes
-// the dot products of every fourth token, then a thread a token sums a suffix.
+// dg of one piece of one (sequence, head): <H, G> at its end by all 256 threads,
+// the dot products of every eighth token by a warp, then a thread a token sums a
+// suffix.
 template <typename IO>
-__global__ void __launch_bounds__(128) serial_dg_kernel(LinearArgs a, SerialWs w, float* dg,
-                                                        int slices) {
-  __shared__ float x[kCkptTokens];
-  const int unit = blockIdx.x, n = unit / a.H, h = unit % a.H;
-  const int b = a.cu_seqlens ? 0 : n, hk = h / (a.H / a.Hk);
-  int t0, len;
-  seq_range(a, n, t0, len);
-  const size_t krow = ((size_t)b * a.Hk + hk) * a.T + t0;
-  const size_t vrow = ((size_t)b * a.H + h) * a.T + t0;
-  const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int piece = blockIdx.y; piece * kCkptTokens < len; piece += gridDim.y) {
-    const int p0 = piece * kCkptTokens, nt = min(kCkptTokens, len - p0);
-    for (int i = wid; i < kCkptTokens; i += 4) {
-      float s = 0.f, own = 0.f;
-      if (i < nt) {
-        const IO* q = static_cast<const IO*>(a.q) + (krow + p0 + i) * a.dk;
-        const IO* k = static_cast<const IO*>(a.k) + (krow + p0 + i) * a.dk;
-        const float* dq = w.dq + (vrow + p0 + i) * a.dk;
-        const float* dk = w.dk + (vrow + p0 + i) * a.dk;
-        for (int r = lane; r < a.dk; r += 32)
-          s += fmaf(ld_io(q + r), dq[r], -(ld_io(k + r) * dk[r]));
-        const IO* v = static_cast<const IO*>(a.v) + (vrow + p0 + i) * a.dv;
-        const IO* dout = static_cast<const IO*>(a.dout) + (vrow + p0 + i) * a.dv;
-        for (int c = lane; c < a.dv; c += 32) own = fmaf(ld_io(v + c), ld_io(dout + c), own);
-      }
+__global__ void __launch_bounds__(256) piece_dg_kernel(LinearArgs a, SerialWs w, float* dg) {
+  __shared__ float x[kCkptTokens], red[8];
+  Where u;
+  if (!where(a, w.p, blockIdx.x, u) || u.piece >= u.pieces) return;
+  const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31, states = a.dk * a.dv;
+  const size_t end = (min(u.slot + 1, w.p.slots - 1) * a.H + u.h) * (size_t)states;
+  float s = 0.f;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < states; i += 256) s = fmaf(w.p.H[end + i], w.p.G[end + i], s);
 #pragma unroll
-      for (int m = 16; m >= 1; m >>= 1) {
-        s += __shfl_xor_sync(0xffffffffu, s, m);
-        own += __shfl_xor_sync(0xffffffffu, own, m);
-      }
-      if (lane == 0) {
-        x[i] = s;
-        if (i < nt) w.own[vrow + p0 + i] = a.scale * own;
-      }
+  for (int m = 16; m >= 1; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+  if (lane == 0) red[wid] = s;
+  for (int i = wid; i < kCkptTokens; i += 8) {
+    float d = 0.f, own = 0.f;
+    if (i < u.len) {
+      const IO* q = static_cast<const IO*>(a.q) + (u.krow + i) * a.dk;
+      const IO* k = static_cast<const IO*>(a.k) + (u.krow + i) * a.dk;
+      const float* dq = w.dq + (u.vrow + i) * a.dk;
+      const float* dk = w.dk + (u.vrow + i) * a.dk;
+      for (int r = lane; r < a.dk; r += 32)
+        d += fmaf(ld_io(q + r), dq[r], -(ld_io(k + r) * dk[r]));
+      const IO* v = static_cast<const IO*>(a.v) + (u.vrow + i) * a.dv;
+      const IO* dout = static_cast<const IO*>(a.dout) + (u.vrow + i) * a.dv;
+      for (int c = lane; c < a.dv; c += 32) own = fmaf(ld_io(v + c), ld_io(dout + c), own);
     }
-    __syncthreads();
-    if (threadIdx.x < kCkptTokens && (int)threadIdx.x < nt) {
-      float s = 0.f;
-      const float* d = w.dots + slot_of(a, w, n, h, piece) * slices;
-      for (int i = 0; i < slices; ++i) s += d[i];
-      for (int i = kCkptTokens - 1; i >= (int)threadIdx.x; --i) s += x[i];
-      dg[vrow + p0 + threadIdx.x] = s;
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) {
+      d += __shfl_xor_sync(0xffffffffu, d, m);
+      own += __shfl_xor_sync(0xffffffffu, own, m);
     }
-    __syncthreads();
+    if (lane == 0) {
+      x[i] = d;
+      if (i < u.len) w.own[u.vrow + i] = a.scale * own;
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x < kCkptTokens && (int)threadIdx.x < u.len) {
+    float t = 0.f;
+    for (int i = 0; i < 8; ++i) t += red[i];
+    for (int i = kCkptTokens - 1; i >= (int)threadIdx.x; --i) t += x[i];
+    dg[u.vrow + threadIdx.x] = t;
   }
 }
 
@@ -324,52 +463,170 @@ __global__ void __launch_bounds__(1024) sum_decay_kernel(LinearArgs a, const flo
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
+// Bytes of shared memory of a run with R columns (a multiple of 16).
+size_t run_smem(int kR) { return (size_t)(2 * kTok * kR + kTok * kOwn + kTok) * sizeof(float); }
+size_t sum_smem(int kR) {
+  return (size_t)(kTok * kR + kTok * kOwn + 2 * kTok + 1) * sizeof(float);
+}
+int r4_of(int R) { return R <= 32 ? 2 : R <= 64 ? 4 : 8; }
+
+size_t slots_of(int N, int T, int tokens, bool packed) {
+  // packed: ceil(len / tokens) pieces of each sequence, and a final state
+  return packed ? (size_t)T / tokens + 2 * (size_t)N : (size_t)N * (pieces_of(T, tokens) + 1);
+}
+
+// Tokens of a forward piece: 64 and up, so that 608 blocks (four an SM) have one;
+// the whole sequence, with no pass before it, where the heads alone make half of
+// that (cutting runs the state's update twice).
+int fwd_piece(int N, int H, int T, int dv, bool packed) {
+  const long long blocks = (long long)N * H * ((dv + kOwn - 1) / kOwn);
+  if (blocks >= 2 * kLinSms || T <= 2 * kTok) return 0;
+  const long long each = packed ? (long long)H * ((dv + kOwn - 1) / kOwn) : blocks;
+  const long long want = (4 * kLinSms + each - 1) / each;  // pieces of the T axis
+  const long long tokens = (T + want - 1) / want;
+  return (int)((tokens + kTok - 1) / kTok * kTok);
+}
+
+template <typename F>
+cudaError_t smem_limit(F kernel, size_t bytes) {
+  if (bytes <= 48 * 1024) return cudaSuccess;
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+// What each piece adds to the states, and the scan.  directions: 1 forward only.
+template <typename IO, int R4>
+cudaError_t launch_sum(const LinearArgs& a, const Pieces& p, int directions, cudaStream_t s) {
+  const auto kernel = piece_sum_kernel<IO, R4>;
+  const size_t smem = sum_smem(16 * R4);
+  const cudaError_t e = smem_limit(kernel, smem);
+  if (e != cudaSuccess) return e;
+  const dim3 grid((unsigned)(p.slots * a.H), (a.dk + kOwn - 1) / kOwn, directions);
+  kernel<<<grid, kThreads, smem, s>>>(a, p, 0);
+  return cudaGetLastError();
+}
+template <typename IO>
+cudaError_t join_pieces(const LinearArgs& a, const Pieces& p, int directions, cudaStream_t s) {
+  const int r4 = r4_of(a.dv);
+  cudaError_t e = r4 == 2   ? launch_sum<IO, 2>(a, p, directions, s)
+                  : r4 == 4 ? launch_sum<IO, 4>(a, p, directions, s)
+                            : launch_sum<IO, 8>(a, p, directions, s);
+  if (e != cudaSuccess) return e;
+  const dim3 grid((unsigned)a.N * a.H, (a.dk * a.dv + 255) / 256, directions);
+  piece_scan_kernel<<<grid, 256, 0, s>>>(a, p, 0);
+  return cudaGetLastError();
+}
+
+template <typename IO, int R4>
+cudaError_t launch_o(const LinearArgs& a, const Pieces& p, cudaStream_t s) {
+  const auto kernel = run_o_kernel<IO, R4>;
+  const size_t smem = run_smem(16 * R4);
+  const cudaError_t e = smem_limit(kernel, smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<dim3((unsigned)(p.slots * a.H), (a.dv + kOwn - 1) / kOwn), kThreads, smem, s>>>(a, p);
+  return cudaGetLastError();
+}
+
+struct FwdPlan {
+  int tokens;
+  size_t slots, H, slot0, total;
+};
+FwdPlan fwd_plan(int N, int H, int T, int dk, int dv, bool packed) {
+  FwdPlan p;
+  const int cut = fwd_piece(N, H, T, dv, packed);
+  p.tokens = cut ? cut : (T > 0 ? T : 1);
+  p.slots = slots_of(N, T, p.tokens, packed);
+  size_t at = 0;
+  p.slot0 = at; at += up256(((size_t)N + 1) * 4);
+  p.H = at; at += cut ? up256(p.slots * H * dk * dv * 4) : 0;
+  p.total = at;
+  return p;
+}
+
+template <typename IO>
+cudaError_t serial_fwd_io(const LinearArgs& a, char* ws, cudaStream_t s) {
+  const FwdPlan f = fwd_plan(a.N, a.H, a.T, a.dk, a.dv, a.cu_seqlens != nullptr);
+  const bool cut = fwd_piece(a.N, a.H, a.T, a.dv, a.cu_seqlens != nullptr) != 0;
+  Pieces p{};
+  p.tokens = f.tokens;
+  p.slots = f.slots;
+  p.H = cut ? reinterpret_cast<float*>(ws + f.H) : nullptr;
+  cudaError_t e = cudaSuccess;
+  if (a.cu_seqlens) {
+    int32_t* slot0 = reinterpret_cast<int32_t*>(ws + f.slot0);
+    p.slot0 = slot0;
+    slot_plan_kernel<<<1, 1024, 0, s>>>(a, p.tokens, slot0);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  if (cut && (e = join_pieces<IO>(a, p, 1, s)) != cudaSuccess) return e;
+  const int r4 = r4_of(a.dk);
+  return r4 == 2 ? launch_o<IO, 2>(a, p, s) : r4 == 4 ? launch_o<IO, 4>(a, p, s) : launch_o<IO, 8>(a, p, s);
+}
+
 struct SerialPlan {
-  size_t slots, dq, dk, dg, own, ckpt, dots, slot0, total;
+  size_t slots, dq, dk, dg, own, H, G, slot0, total;
 };
 SerialPlan serial_plan(int N, int B, int H, int T, int dk, int dv, bool packed) {
-  // packed: each sequence has at most T_n / 64 + 1 pieces, and a final state
   SerialPlan p;
-  p.slots = packed ? (size_t)T / kCkptTokens + 2 * (size_t)N : (size_t)N * (pieces_of(T) + 1);
-  const size_t slots = p.slots * H;
+  p.slots = slots_of(N, T, kCkptTokens, packed);
+  const size_t states = p.slots * H * dk * dv * 4;
   const size_t rows = (size_t)B * H * T;
   size_t at = 0;
   p.dq = at; at += up256(rows * dk * 4);
   p.dk = at; at += up256(rows * dk * 4);
   p.dg = at; at += up256(rows * 4);
   p.own = at; at += up256(rows * 4);
-  p.ckpt = at; at += up256(slots * dk * dv * 4);
-  p.dots = at; at += up256(slots * ((dk + kOwn - 1) / kOwn) * 4);
+  p.H = at; at += up256(states);
+  p.G = at; at += up256(states);
   p.slot0 = at; at += up256(((size_t)N + 1) * 4);
   p.total = at;
   return p;
 }
 
+template <typename IO, int R4K, int R4V>
+cudaError_t launch_grads(const LinearArgs& a, const SerialWs& w, cudaStream_t s) {
+  const auto kernel = run_grads_kernel<IO, R4K, R4V>;
+  const size_t smem = run_smem(16 * (R4K > R4V ? R4K : R4V));
+  const cudaError_t e = smem_limit(kernel, smem);
+  if (e != cudaSuccess) return e;
+  const int most = a.dk > a.dv ? a.dk : a.dv;
+  kernel<<<dim3((unsigned)(w.p.slots * a.H), (most + kOwn - 1) / kOwn, 3), kThreads, smem, s>>>(a, w);
+  return cudaGetLastError();
+}
+template <typename IO, int R4K>
+cudaError_t launch_grads_v(const LinearArgs& a, const SerialWs& w, cudaStream_t s) {
+  const int r4 = r4_of(a.dv);
+  return r4 == 2   ? launch_grads<IO, R4K, 2>(a, w, s)
+         : r4 == 4 ? launch_grads<IO, R4K, 4>(a, w, s)
+                   : launch_grads<IO, R4K, 8>(a, w, s);
+}
+
 template <typename IO>
 cudaError_t serial_bwd_io(const LinearArgs& a, char* ws, cudaStream_t s) {
   const SerialPlan p = serial_plan(a.N, a.B, a.H, a.T, a.dk, a.dv, a.cu_seqlens != nullptr);
-  SerialWs w;
+  SerialWs w{};
   w.dq = reinterpret_cast<float*>(ws + p.dq);
   w.dk = reinterpret_cast<float*>(ws + p.dk);
   w.dg = reinterpret_cast<float*>(ws + p.dg);
   w.own = reinterpret_cast<float*>(ws + p.own);
-  w.ckpt = reinterpret_cast<float*>(ws + p.ckpt);
-  w.dots = reinterpret_cast<float*>(ws + p.dots);
-  w.slot0 = reinterpret_cast<int32_t*>(ws + p.slot0);
-  w.slots = p.slots;
+  w.p.tokens = kCkptTokens;
+  w.p.slots = p.slots;
+  w.p.H = reinterpret_cast<float*>(ws + p.H);
+  w.p.G = reinterpret_cast<float*>(ws + p.G);
   cudaError_t e = cudaSuccess;
   if (a.cu_seqlens) {
-    slot_plan_kernel<<<1, 1024, 0, s>>>(a, w.slot0);
+    int32_t* slot0 = reinterpret_cast<int32_t*>(ws + p.slot0);
+    w.p.slot0 = slot0;
+    slot_plan_kernel<<<1, 1024, 0, s>>>(a, kCkptTokens, slot0);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  if ((e = launch_run<IO, float, RUN_DQ>(a, w, w.dq, s)) != cudaSuccess) return e;
-  if ((e = launch_run<IO, float, RUN_DK>(a, w, w.dk, s)) != cudaSuccess) return e;
-  if ((e = launch_run<IO, IO, RUN_DV>(a, w, static_cast<IO*>(a.dval), s)) != cudaSuccess) return e;
+  if ((e = join_pieces<IO>(a, w.p, 2, s)) != cudaSuccess) return e;
   if (a.T > 0) {
-    const int pieces = pieces_of(a.T);
-    const dim3 grid((unsigned)a.N * a.H, pieces < 64 ? pieces : 64);
-    float* dg = a.g_head ? w.dg : a.dg;
-    serial_dg_kernel<IO><<<grid, 128, 0, s>>>(a, w, dg, (a.dk + kOwn - 1) / kOwn);
+    const int r4 = r4_of(a.dk);
+    e = r4 == 2   ? launch_grads_v<IO, 2>(a, w, s)
+        : r4 == 4 ? launch_grads_v<IO, 4>(a, w, s)
+                  : launch_grads_v<IO, 8>(a, w, s);
+    if (e != cudaSuccess) return e;
+    piece_dg_kernel<IO><<<(unsigned)(p.slots * a.H), 256, 0, s>>>(a, w, a.g_head ? w.dg : a.dg);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if ((e = linear_sum_heads(a, w.dq, w.dk, w.own, s)) != cudaSuccess) return e;
   }
@@ -378,12 +635,12 @@ cudaError_t serial_bwd_io(const LinearArgs& a, char* ws, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t linear_serial_fwd(const LinearArgs& a, cudaStream_t s) {
-  SerialWs w{};
-  return a.io == CKDA_F32
-             ? launch_run<float, float, RUN_O>(a, w, static_cast<float*>(a.o), s)
-             : launch_run<__nv_bfloat16, __nv_bfloat16, RUN_O>(
-                   a, w, static_cast<__nv_bfloat16*>(a.o), s);
+size_t linear_serial_fwd_bytes(int N, int H, int T, int dk, int dv, bool packed) {
+  return fwd_plan(N, H, T, dk, dv, packed).total;
+}
+
+cudaError_t linear_serial_fwd(const LinearArgs& a, char* ws, cudaStream_t s) {
+  return a.io == CKDA_F32 ? serial_fwd_io<float>(a, ws, s) : serial_fwd_io<__nv_bfloat16>(a, ws, s);
 }
 
 size_t linear_serial_bwd_bytes(int N, int B, int H, int T, int dk, int dv, bool packed) {
