@@ -33,6 +33,7 @@
 //     the dq and dk runs read the decayed state before the token's write, and
 //     the own part, k_t (v_t.do_t) and q_t (v_t.do_t), joins dq and dk last;
 //   - the sum restarts at every piece from <H, dL/dH> itself.
+#include <type_traits>
 #include "ckda_linear.cuh"
 
 namespace ckda {
@@ -129,17 +130,72 @@ __global__ void slot_plan_kernel(LinearArgs a, int tokens, int32_t* slot0) {
 // Register i of a thread's quarter p of a row: column.
 __device__ __forceinline__ int col(int p, int i) { return 4 * (p + kSplit * (i / 4)) + i % 4; }
 
+// Two columns an instruction: issue is what bounds a run that fills the SMs.
+struct alignas(8) F2 {
+  float x, y;
+};
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 d;
+  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " mov.b64 c, {%6, %7};\n fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 d;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " mul.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+__device__ __forceinline__ void copy16(float* dst, const float* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src), "r"(in ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+  const uint2 v = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u),
+                     __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
+}
+
 // Stages `nt` tokens of `n` columns from `c0` on into [kTok][WIDTH], the rest
-// zeros; back: in reverse, ending with the token at `src`.
+// zeros; back: in reverse, ending with the token at `src`.  Four columns at a
+// time where rows and base allow it (fp32 by cp.async, all at once in flight:
+// staging one element a load took most of a piece's time).
 template <typename IO, int WIDTH>
 __device__ __forceinline__ void stage(float* dst, const IO* src, int stride, int c0, int n, int nt,
-                                      float scale, bool back) {
+                                      bool back) {
+  constexpr uintptr_t kMask = 4 * sizeof(IO) - 1;
+  const bool four = ((stride | n) & 3) == 0 && (reinterpret_cast<uintptr_t>(src) & kMask) == 0;
+  if (four) {
+#pragma unroll 8
+    for (int e = threadIdx.x; e < kTok * WIDTH / 4; e += kThreads) {
+      const int tt = e / (WIDTH / 4), c = 4 * (e % (WIDTH / 4));
+      const int t = back ? nt - 1 - tt : tt;
+      const bool in = tt < nt && c < n;
+      const IO* from = in ? src + (size_t)t * stride + c0 + c : src;
+      if constexpr (sizeof(IO) == 4)
+        copy16(dst + 4 * e, from, in);
+      else
+        *reinterpret_cast<float4*>(dst + 4 * e) = in ? load4(from) : make_float4(0, 0, 0, 0);
+    }
+    return;
+  }
 #pragma unroll 8
   for (int e = threadIdx.x; e < kTok * WIDTH; e += kThreads) {
     const int tt = e / WIDTH, c = e % WIDTH;
     const size_t t = back ? nt - 1 - tt : tt;
-    dst[e] = tt < nt && c < n ? scale * ld_io(src + t * stride + c0 + c) : 0.f;
+    dst[e] = tt < nt && c < n ? ld_io(src + t * stride + c0 + c) : 0.f;
   }
+}
+__device__ __forceinline__ void staged() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
 }
 
 // A piece's own contribution to the state after it (block z = 0: over k and v,
@@ -160,9 +216,9 @@ __global__ void __launch_bounds__(kThreads) piece_sum_kernel(LinearArgs a, Piece
   const int gs = a.g_head ? 0 : 1;
   const int own = threadIdx.x / kSplit, part = threadIdx.x % kSplit;
   const int c0 = blockIdx.y * kOwn, c = c0 + own;
-  float S[4 * R4];
+  F2 S[2 * R4];
 #pragma unroll
-  for (int i = 0; i < 4 * R4; ++i) S[i] = 0.f;
+  for (int i = 0; i < 2 * R4; ++i) S[i] = F2{0.f, 0.f};
   float* out = (back ? p.G : p.H);
   const size_t slot = min(u.slot + (back ? 0 : 1), p.slots - 1);
   out += (slot * a.H + u.h) * (size_t)a.dk * a.dv;
@@ -171,12 +227,11 @@ __global__ void __launch_bounds__(kThreads) piece_sum_kernel(LinearArgs a, Piece
   for (int s0 = 0; s0 < u.len; s0 += kTok) {
     const int nt = min(kTok, u.len - s0), t0 = back ? u.len - s0 - nt : s0;
     __syncthreads();
-    stage<IO, kR>(sx, X + (size_t)t0 * a.dv, a.dv, 0, a.dv, nt, 1.f, false);
-    stage<IO, kOwn>(sy, Y + (size_t)t0 * a.dk, a.dk, c0, min(kOwn, a.dk - c0), nt,
-                    back ? a.scale : 1.f, false);
+    stage<IO, kR>(sx, X + (size_t)t0 * a.dv, a.dv, 0, a.dv, nt, false);
+    stage<IO, kOwn>(sy, Y + (size_t)t0 * a.dk, a.dk, c0, min(kOwn, a.dk - c0), nt, false);
     if (threadIdx.x < kTok) sw[kTok + threadIdx.x] =
         (int)threadIdx.x < nt ? g[(size_t)(t0 + threadIdx.x) * gs] : 0.f;
-    __syncthreads();
+    staged();
     if (threadIdx.x <= kTok) {
       // forward: from after token t to the tile's end; backward: from its start
       // to t; entry kTok: over the tile
@@ -186,23 +241,28 @@ __global__ void __launch_bounds__(kThreads) piece_sum_kernel(LinearArgs a, Piece
         for (int i = 0; i < (t == kTok ? nt : min(t + 1, nt)); ++i) x += sw[kTok + i];
       else
         for (int i = nt - 1; i > t; --i) x += sw[kTok + i];
-      sw[t == kTok ? 2 * kTok : t] = expf(x);
+      sw[t == kTok ? 2 * kTok : t] = (t < kTok && back ? a.scale : 1.f) * expf(x);
     }
     __syncthreads();
     const float all = sw[2 * kTok];
 #pragma unroll
-    for (int i = 0; i < 4 * R4; ++i) S[i] *= s0 ? all : 1.f;
+    for (int i = 0; i < 2 * R4; ++i) S[i] = mul2(S[i], s0 ? F2{all, all} : F2{1.f, 1.f});
 #pragma unroll 2
     for (int t = 0; t < nt; ++t) {
       const float y = sw[t] * sy[t * kOwn + own];
+      const float4* x = reinterpret_cast<const float4*>(sx + t * kR) + part;
 #pragma unroll
-      for (int i = 0; i < 4 * R4; ++i) S[i] = fmaf(y, sx[t * kR + col(part, i)], S[i]);
+      for (int i = 0; i < R4; ++i) {
+        const float4 xv = x[kSplit * i];
+        S[2 * i] = fma2(F2{y, y}, F2{xv.x, xv.y}, S[2 * i]);
+        S[2 * i + 1] = fma2(F2{y, y}, F2{xv.z, xv.w}, S[2 * i + 1]);
+      }
     }
   }
   if (c < a.dk)
 #pragma unroll
     for (int i = 0; i < 4 * R4; ++i)
-      if (col(part, i) < a.dv) out[(size_t)c * a.dv + col(part, i)] = S[i];
+      if (col(part, i) < a.dv) out[(size_t)c * a.dv + col(part, i)] = i % 2 ? S[i / 2].y : S[i / 2].x;
 }
 
 // Joins the pieces, in place: H[p + 1] = e^{g over p} H[p] + its own, from h0, and
@@ -234,6 +294,7 @@ __global__ void __launch_bounds__(256) piece_scan_kernel(LinearArgs a, Pieces p,
     for (int k = threadIdx.x >> 5; k < nk; k += 8) {
       const int piece = back ? pieces - 1 - (k0 + k) : k0 + k, i0 = piece * p.tokens;
       double x = 0.0;
+#pragma unroll 2
       for (int i = i0 + (threadIdx.x & 31); i < min(i0 + p.tokens, len); i += 32)
         x += (double)g[(size_t)i * gs];
 #pragma unroll
@@ -242,11 +303,17 @@ __global__ void __launch_bounds__(256) piece_scan_kernel(LinearArgs a, Pieces p,
     }
     __syncthreads();
     if (e < states) {
-#pragma unroll 4
-      for (int k = 0; k < nk; ++k) {
-        float* q = S + at(back ? pieces - 1 - (k0 + k) : k0 + k + 1);
-        s = fmaf(dec[k], s, *q);
-        *q = s;
+      for (int k = 0; k < nk; k += 8) {  // eight loads in flight
+        float own[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          own[i] = k + i < nk ? S[at(back ? pieces - 1 - (k0 + k + i) : k0 + k + i + 1)] : 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (k + i < nk) {
+            s = fmaf(dec[k + i], s, own[i]);
+            S[at(back ? pieces - 1 - (k0 + k + i) : k0 + k + i + 1)] = s;
+          }
       }
     }
   }
@@ -286,7 +353,7 @@ __device__ __forceinline__ void run_piece(const LinearArgs& a, const Pieces& p, 
   // element (row c, column r) of a [dk, dv] state
   auto at = [&](int r) { return kOwnV ? (size_t)r * a.dv + c : (size_t)c * a.dv + r; };
 
-  float S[4 * R4];
+  F2 S[2 * R4];
   const size_t states = (size_t)a.dk * a.dv;
   const float* init;
   if (kBack)
@@ -297,39 +364,47 @@ __device__ __forceinline__ void run_piece(const LinearArgs& a, const Pieces& p, 
     init = a.h0 ? a.h0 + ((size_t)u.n * a.H + u.h) * states : nullptr;
 #pragma unroll
   for (int i = 0; i < 4 * R4; ++i)
-    S[i] = init && row && col(part, i) < R ? init[at(col(part, i))] : 0.f;
+    (i % 2 ? S[i / 2].y : S[i / 2].x) =
+        init && row && col(part, i) < R ? init[at(col(part, i))] : 0.f;
 
   for (int s0 = 0; s0 < u.len; s0 += kTok) {
     const int nt = min(kTok, u.len - s0), t0 = kBack ? u.len - s0 - nt : s0;
     __syncthreads();
-    stage<IO, kR>(sx, X + (size_t)t0 * R, R, 0, R, nt, 1.f, kBack);
-    stage<IO, kR>(sz, Z + (size_t)t0 * R, R, 0, R, nt, 1.f, kBack);
-    stage<IO, kOwn>(sy, Y + (size_t)t0 * own_n, own_n, c0, min(kOwn, own_n - c0), nt, y_scale,
-                    kBack);
+    stage<IO, kR>(sx, X + (size_t)t0 * R, R, 0, R, nt, kBack);
+    stage<IO, kR>(sz, Z + (size_t)t0 * R, R, 0, R, nt, kBack);
+    stage<IO, kOwn>(sy, Y + (size_t)t0 * own_n, own_n, c0, min(kOwn, own_n - c0), nt, kBack);
     if (threadIdx.x < kTok && (int)threadIdx.x < nt) {
       const int t = kBack ? t0 + nt - 1 - threadIdx.x : t0 + threadIdx.x;
       // backward, the decay from token t + 1 to t; none into the piece's last token
       sa[threadIdx.x] = kBack ? (t == u.len - 1 ? 1.f : expf(g[(size_t)(t + 1) * gs]))
                               : expf(g[(size_t)t * gs]);
     }
-    __syncthreads();
+    staged();
     for (int tt = 0; tt < nt; ++tt) {
       const int t = kBack ? t0 + nt - 1 - tt : t0 + tt;
-      const float dec = sa[tt], y = sy[tt * kOwn + own];
-      const float *x = sx + tt * kR, *z = sz + tt * kR;
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};  // four chains: the sum is the token's latency
+      const float dec = sa[tt], y = y_scale * sy[tt * kOwn + own];
+      const float4* x = reinterpret_cast<const float4*>(sx + tt * kR) + part;
+      const float4* z = reinterpret_cast<const float4*>(sz + tt * kR) + part;
+      const F2 d2{dec, dec}, y2{y, y};
+      F2 acc[2] = {{0.f, 0.f}, {0.f, 0.f}};  // four chains: the sum is the token's latency
 #pragma unroll
-      for (int i = 0; i < 4 * R4; ++i) {
-        if (kDecayed) {
-          S[i] *= dec;
-          acc[i % 4] = fmaf(S[i], z[col(part, i)], acc[i % 4]);
-          S[i] = fmaf(y, x[col(part, i)], S[i]);
-        } else {
-          S[i] = fmaf(dec, S[i], y * x[col(part, i)]);
-          acc[i % 4] = fmaf(S[i], z[col(part, i)], acc[i % 4]);
+      for (int i = 0; i < R4; ++i) {
+        const float4 xv = x[kSplit * i], zv = z[kSplit * i];
+        const F2 x2[2] = {{xv.x, xv.y}, {xv.z, xv.w}}, z2[2] = {{zv.x, zv.y}, {zv.z, zv.w}};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          F2& S2 = S[2 * i + e];
+          if (kDecayed) {
+            S2 = mul2(S2, d2);
+            acc[e] = fma2(S2, z2[e], acc[e]);
+            S2 = fma2(y2, x2[e], S2);
+          } else {
+            S2 = fma2(d2, S2, mul2(y2, x2[e]));
+            acc[e] = fma2(S2, z2[e], acc[e]);
+          }
         }
       }
-      float s = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+      float s = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
       s += __shfl_xor_sync(0xffffffffu, s, 1);
       s += __shfl_xor_sync(0xffffffffu, s, 2);
       if (part == 0 && row) st_io(out + (u.vrow + t) * own_n + c, out_scale * s);
@@ -339,7 +414,7 @@ __device__ __forceinline__ void run_piece(const LinearArgs& a, const Pieces& p, 
     float* to = a.hT + ((size_t)u.n * a.H + u.h) * states;
 #pragma unroll
     for (int i = 0; i < 4 * R4; ++i)
-      if (col(part, i) < R) to[at(col(part, i))] = S[i];
+      if (col(part, i) < R) to[at(col(part, i))] = i % 2 ? S[i / 2].y : S[i / 2].x;
   }
 }
 
@@ -354,25 +429,27 @@ __global__ void __launch_bounds__(kThreads) run_o_kernel(LinearArgs a, Pieces p)
   run_piece<IO, IO, RUN_O, R4>(a, p, u, blockIdx.y, static_cast<IO*>(a.o), sm);
 }
 
-// dq, dk and dv side by side, as block z.
-template <typename IO, int R4K, int R4V>
-__global__ void __launch_bounds__(kThreads) run_grads_kernel(LinearArgs a, SerialWs w) {
+// dq and dk side by side as block z (they contract over dv), and dv.
+template <typename IO, int R4>
+__global__ void __launch_bounds__(kThreads) run_dqk_kernel(LinearArgs a, SerialWs w) {
   extern __shared__ __align__(16) float sm[];
-  const int slice = blockIdx.y;
   Where u;
   if (!where(a, w.p, blockIdx.x, u) || u.piece >= u.pieces) return;
-  if (slice * kOwn >= (blockIdx.z == 2 ? a.dv : a.dk)) return;
   if (blockIdx.z == 0)
-    run_piece<IO, float, RUN_DQ, R4V>(a, w.p, u, slice, w.dq, sm);
-  else if (blockIdx.z == 1)
-    run_piece<IO, float, RUN_DK, R4V>(a, w.p, u, slice, w.dk, sm);
+    run_piece<IO, float, RUN_DQ, R4>(a, w.p, u, blockIdx.y, w.dq, sm);
   else
-    run_piece<IO, IO, RUN_DV, R4K>(a, w.p, u, slice, static_cast<IO*>(a.dval), sm);
+    run_piece<IO, float, RUN_DK, R4>(a, w.p, u, blockIdx.y, w.dk, sm);
+}
+template <typename IO, int R4>
+__global__ void __launch_bounds__(kThreads) run_dv_kernel(LinearArgs a, SerialWs w) {
+  extern __shared__ __align__(16) float sm[];
+  Where u;
+  if (!where(a, w.p, blockIdx.x, u) || u.piece >= u.pieces) return;
+  run_piece<IO, IO, RUN_DV, R4>(a, w.p, u, blockIdx.y, static_cast<IO*>(a.dval), sm);
 }
 
 // dg of one piece of one (sequence, head): <H, G> at its end by all 256 threads,
-// the dot products of every eighth token by a warp, then a thread a token sums a
-// suffix.
+// the dot products of a token by four, then a thread a token sums a suffix.
 template <typename IO>
 __global__ void __launch_bounds__(256) piece_dg_kernel(LinearArgs a, SerialWs w, float* dg) {
   __shared__ float x[kCkptTokens], red[8];
@@ -386,25 +463,28 @@ __global__ void __launch_bounds__(256) piece_dg_kernel(LinearArgs a, SerialWs w,
 #pragma unroll
   for (int m = 16; m >= 1; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
   if (lane == 0) red[wid] = s;
-  for (int i = wid; i < kCkptTokens; i += 8) {
+  {  // four threads a token
+    const int i = threadIdx.x >> 2, part = threadIdx.x & 3;
     float d = 0.f, own = 0.f;
     if (i < u.len) {
       const IO* q = static_cast<const IO*>(a.q) + (u.krow + i) * a.dk;
       const IO* k = static_cast<const IO*>(a.k) + (u.krow + i) * a.dk;
       const float* dq = w.dq + (u.vrow + i) * a.dk;
       const float* dk = w.dk + (u.vrow + i) * a.dk;
-      for (int r = lane; r < a.dk; r += 32)
+#pragma unroll 4
+      for (int r = part; r < a.dk; r += 4)
         d += fmaf(ld_io(q + r), dq[r], -(ld_io(k + r) * dk[r]));
       const IO* v = static_cast<const IO*>(a.v) + (u.vrow + i) * a.dv;
       const IO* dout = static_cast<const IO*>(a.dout) + (u.vrow + i) * a.dv;
-      for (int c = lane; c < a.dv; c += 32) own = fmaf(ld_io(v + c), ld_io(dout + c), own);
+#pragma unroll 4
+      for (int c = part; c < a.dv; c += 4) own = fmaf(ld_io(v + c), ld_io(dout + c), own);
     }
 #pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) {
+    for (int m = 2; m >= 1; m >>= 1) {
       d += __shfl_xor_sync(0xffffffffu, d, m);
       own += __shfl_xor_sync(0xffffffffu, own, m);
     }
-    if (lane == 0) {
+    if (part == 0) {
       x[i] = d;
       if (i < u.len) w.own[u.vrow + i] = a.scale * own;
     }
@@ -468,7 +548,21 @@ size_t run_smem(int kR) { return (size_t)(2 * kTok * kR + kTok * kOwn + kTok) * 
 size_t sum_smem(int kR) {
   return (size_t)(kTok * kR + kTok * kOwn + 2 * kTok + 1) * sizeof(float);
 }
-int r4_of(int R) { return R <= 32 ? 2 : R <= 64 ? 4 : 8; }
+
+// Calls f with the columns of a thread / 4 that hold R columns, as a constant.
+template <typename F>
+cudaError_t with_columns(int R, F f) {
+  switch ((R + 15) / 16) {
+    case 1: return f(std::integral_constant<int, 1>());
+    case 2: return f(std::integral_constant<int, 2>());
+    case 3: return f(std::integral_constant<int, 3>());
+    case 4: return f(std::integral_constant<int, 4>());
+    case 5: return f(std::integral_constant<int, 5>());
+    case 6: return f(std::integral_constant<int, 6>());
+    case 7: return f(std::integral_constant<int, 7>());
+    default: return f(std::integral_constant<int, 8>());
+  }
+}
 
 size_t slots_of(int N, int T, int tokens, bool packed) {
   // packed: ceil(len / tokens) pieces of each sequence, and a final state
@@ -506,10 +600,8 @@ cudaError_t launch_sum(const LinearArgs& a, const Pieces& p, int directions, cud
 }
 template <typename IO>
 cudaError_t join_pieces(const LinearArgs& a, const Pieces& p, int directions, cudaStream_t s) {
-  const int r4 = r4_of(a.dv);
-  cudaError_t e = r4 == 2   ? launch_sum<IO, 2>(a, p, directions, s)
-                  : r4 == 4 ? launch_sum<IO, 4>(a, p, directions, s)
-                            : launch_sum<IO, 8>(a, p, directions, s);
+  const cudaError_t e = with_columns(
+      a.dv, [&](auto r4) { return launch_sum<IO, decltype(r4)::value>(a, p, directions, s); });
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)a.N * a.H, (a.dk * a.dv + 255) / 256, directions);
   piece_scan_kernel<<<grid, 256, 0, s>>>(a, p, 0);
@@ -558,8 +650,7 @@ cudaError_t serial_fwd_io(const LinearArgs& a, char* ws, cudaStream_t s) {
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   if (cut && (e = join_pieces<IO>(a, p, 1, s)) != cudaSuccess) return e;
-  const int r4 = r4_of(a.dk);
-  return r4 == 2 ? launch_o<IO, 2>(a, p, s) : r4 == 4 ? launch_o<IO, 4>(a, p, s) : launch_o<IO, 8>(a, p, s);
+  return with_columns(a.dk, [&](auto r4) { return launch_o<IO, decltype(r4)::value>(a, p, s); });
 }
 
 struct SerialPlan {
@@ -582,22 +673,25 @@ SerialPlan serial_plan(int N, int B, int H, int T, int dk, int dv, bool packed) 
   return p;
 }
 
-template <typename IO, int R4K, int R4V>
-cudaError_t launch_grads(const LinearArgs& a, const SerialWs& w, cudaStream_t s) {
-  const auto kernel = run_grads_kernel<IO, R4K, R4V>;
-  const size_t smem = run_smem(16 * (R4K > R4V ? R4K : R4V));
+template <typename IO, int R4>
+cudaError_t launch_dqk(const LinearArgs& a, const SerialWs& w, cudaStream_t s) {
+  const auto kernel = run_dqk_kernel<IO, R4>;
+  const size_t smem = run_smem(16 * R4);
   const cudaError_t e = smem_limit(kernel, smem);
   if (e != cudaSuccess) return e;
-  const int most = a.dk > a.dv ? a.dk : a.dv;
-  kernel<<<dim3((unsigned)(w.p.slots * a.H), (most + kOwn - 1) / kOwn, 3), kThreads, smem, s>>>(a, w);
+  const dim3 grid((unsigned)(w.p.slots * a.H), (a.dk + kOwn - 1) / kOwn, 2);
+  kernel<<<grid, kThreads, smem, s>>>(a, w);
   return cudaGetLastError();
 }
-template <typename IO, int R4K>
-cudaError_t launch_grads_v(const LinearArgs& a, const SerialWs& w, cudaStream_t s) {
-  const int r4 = r4_of(a.dv);
-  return r4 == 2   ? launch_grads<IO, R4K, 2>(a, w, s)
-         : r4 == 4 ? launch_grads<IO, R4K, 4>(a, w, s)
-                   : launch_grads<IO, R4K, 8>(a, w, s);
+template <typename IO, int R4>
+cudaError_t launch_dv(const LinearArgs& a, const SerialWs& w, cudaStream_t s) {
+  const auto kernel = run_dv_kernel<IO, R4>;
+  const size_t smem = run_smem(16 * R4);
+  const cudaError_t e = smem_limit(kernel, smem);
+  if (e != cudaSuccess) return e;
+  const dim3 grid((unsigned)(w.p.slots * a.H), (a.dv + kOwn - 1) / kOwn);
+  kernel<<<grid, kThreads, smem, s>>>(a, w);
+  return cudaGetLastError();
 }
 
 template <typename IO>
@@ -621,10 +715,9 @@ cudaError_t serial_bwd_io(const LinearArgs& a, char* ws, cudaStream_t s) {
   }
   if ((e = join_pieces<IO>(a, w.p, 2, s)) != cudaSuccess) return e;
   if (a.T > 0) {
-    const int r4 = r4_of(a.dk);
-    e = r4 == 2   ? launch_grads_v<IO, 2>(a, w, s)
-        : r4 == 4 ? launch_grads_v<IO, 4>(a, w, s)
-                  : launch_grads_v<IO, 8>(a, w, s);
+    e = with_columns(a.dv, [&](auto r4) { return launch_dqk<IO, decltype(r4)::value>(a, w, s); });
+    if (e == cudaSuccess)
+      e = with_columns(a.dk, [&](auto r4) { return launch_dv<IO, decltype(r4)::value>(a, w, s); });
     if (e != cudaSuccess) return e;
     piece_dg_kernel<IO><<<(unsigned)(p.slots * a.H), 256, 0, s>>>(a, w, a.g_head ? w.dg : a.dg);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
