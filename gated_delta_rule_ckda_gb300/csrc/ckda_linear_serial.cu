@@ -380,6 +380,7 @@ __device__ __forceinline__ void run_piece(const LinearArgs& a, const Pieces& p, 
                               : expf(g[(size_t)t * gs]);
     }
     staged();
+#pragma unroll 2
     for (int tt = 0; tt < nt; ++tt) {
       const int t = kBack ? t0 + nt - 1 - tt : t0 + tt;
       const float dec = sa[tt], y = y_scale * sy[tt * kOwn + own];
@@ -553,13 +554,12 @@ size_t sum_smem(int kR) {
 template <typename F>
 cudaError_t with_columns(int R, F f) {
   switch ((R + 15) / 16) {
-    case 1: return f(std::integral_constant<int, 1>());
+    case 1:
     case 2: return f(std::integral_constant<int, 2>());
     case 3: return f(std::integral_constant<int, 3>());
     case 4: return f(std::integral_constant<int, 4>());
     case 5: return f(std::integral_constant<int, 5>());
     case 6: return f(std::integral_constant<int, 6>());
-    case 7: return f(std::integral_constant<int, 7>());
     default: return f(std::integral_constant<int, 8>());
   }
 }
