@@ -48,6 +48,7 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(LinearArgs a, int32_t*
   }
   sum[threadIdx.x] = s;
   __syncthreads();
+  if (i0 >= i1) return;
   int32_t before = 0;
   for (int j = 0; j < (int)threadIdx.x; ++j) before += sum[j];
   for (int i = i0; i < i1; ++i) {
@@ -56,7 +57,7 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(LinearArgs a, int32_t*
     seq_range(a, i, t0, len);
     before += (len + C - 1) / C;
   }
-  if (threadIdx.x == 1023) first[a.N] = before;
+  if (i1 == a.N) first[a.N] = before;
 }
 
 // ------------------------------------------------------ gradients of a chunk

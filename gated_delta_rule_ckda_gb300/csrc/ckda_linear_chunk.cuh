@@ -74,12 +74,11 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
-// Both panels of a tile; completion counts kTile bytes on `bar`.
+// The panels of a tile; completion counts their bytes on `bar`.
 __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, uint64_t* bar,
-                                          int32_t token, int32_t head) {
-  mbar_arrive_expect_tx(bar, kTile);
-  tma_load_3d(dst, map, bar, 0, token, head);
-  tma_load_3d(dst + kPanel, map, bar, 64, token, head);
+                                          int32_t token, int32_t head, int panels = 2) {
+  mbar_arrive_expect_tx(bar, panels * kPanel);
+  for (int p = 0; p < panels; ++p) tma_load_3d(dst + p * kPanel, map, bar, 64 * p, token, head);
 }
 
 // The same tile, and `bytes` of memory, into L2 only.
@@ -145,7 +144,7 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// 128 x N products over K = 128, bf16 operands, issued by one thread.  AMN,
+// 128 x N products over K = 16 KS, bf16 operands, issued by one thread.  AMN,
 // BMN: the operand is stored with its K index along the rows.  One copy of the
 // issue code for each pair of layouts, out of line (see the note on short loops
 // below), with the descriptors' steps as constants: one that is looked up costs
@@ -160,12 +159,12 @@ template <bool MN>
 __device__ __forceinline__ uint64_t desc_step(int k) {
   return MN ? 128u * k : 1024u * (k >> 2) + 2u * (k & 3);
 }
-template <bool AMN, bool BMN, int N = 128>
+template <bool AMN, bool BMN, int N = 128, int KS = 8>
 static __device__ __noinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t accumulate) {
   const uint64_t da = tile_desc<AMN>(a), db = tile_desc<BMN>(b);
   umma_ss(d, da, db, idesc_f16(128, N, 1, AMN, BMN), accumulate);
 #pragma unroll
-  for (int k = 1; k < 8; ++k)
+  for (int k = 1; k < KS; ++k)
     umma_ss(d, da + desc_step<AMN>(k), db + desc_step<BMN>(k), idesc_f16(128, N, 1, AMN, BMN), 1);
 }
 template <bool BMN, int N = 128>
@@ -296,18 +295,18 @@ __device__ __forceinline__ void zero_row(char* tile, int row) {
 // chunk come from beyond the instruction cache, and unrolled rows took three
 // times as long.)
 //
-// A token row of 64 channels times w, in two bf16 parts: hi in place, lo at the
+// Channels 8 j0 .. 8 j1 of a token row times w, in two bf16 parts: hi in place, lo at the
 // same place of another tile.  With w = wh + wl in bf16, hi = round(k wh), what
 // that rounding left is exact in bf16 (k wh has 16 bits), and k wl joins it:
 // hi + lo is w k to 2^-16, which fp32 results need, in three packed operations.
-__device__ __forceinline__ void scale_row(char* tile, char* lo, int row, int panel, float w,
-                                          bool keep) {
+__device__ __forceinline__ void scale_row(char* tile, char* lo, int row, int j0, int j1,
+                                          float w, bool keep) {
   const __nv_bfloat16 h = __float2bfloat16_rn(w);
   const __nv_bfloat162 wh = __bfloat162bfloat162(h);
   const __nv_bfloat162 wl = __float2bfloat162_rn(w - __bfloat162float(h));
 #pragma unroll 2
-  for (int j = 0; j < 8; ++j) {
-    const uint32_t off = sw128_chunk(128, row, 8 * panel + j);
+  for (int j = j0; j < j1; ++j) {
+    const uint32_t off = sw128_chunk(128, row, j);
     const uint4 v = *reinterpret_cast<const uint4*>(tile + off);
     const uint32_t in[4] = {v.x, v.y, v.z, v.w};
     uint32_t hi[4], rest[4];

@@ -11,16 +11,16 @@
 // One CTA of 512 threads walks the chunks of one (sequence, head), or of one
 // segment of it; the state never leaves the SM.  It is bound by HBM: 1 KiB a token at 128 x 128 against
 // five 128 x 128 x 128 products a chunk.
-//   warp 0       loads tiles with TMA into a ring of five 32 KB slots, in the
-//                order q, k, v of chunk after chunk
+//   warp 0       loads tiles with TMA into a ring of slots, in the order q, k, v
+//                of chunk after chunk
 //   warp 1       issues the products (tcgen05, one thread)
 //   warp 2       the decay factors of a chunk
 //   warps 4-7    one row of S a thread: P as bf16 into TMEM, where the product
 //                P V reads it; later the row of o, staged in the state's
 //                tile (between its readers and the next state) and stored with TMA (a thread's own 256-byte rows cost
 //                four times the L1 passes)
-//   warps 8-15   the state: thread (r, s) holds H[64 s .. 64 s + 63][r] in
-//                fp32 registers, rounded to nearest at every step (tensor-core
+//   warps 8-15   the state: thread (r, s) holds one half s of H's rows in column r
+//                in fp32 registers, rounded to nearest at every step (tensor-core
 //                accumulators truncate, which over thousands of chunks would
 //                bias a slowly decaying state).  A chunk's own contribution is
 //                a product of its own into fresh TMEM columns, so it does not
@@ -38,27 +38,42 @@ namespace {
 using namespace chunk;
 
 constexpr int kThreads = 512;
-constexpr int kSlots = 5;
-constexpr uint32_t kLo = kSlots * kTile;        // lo part of the scaled keys
-constexpr uint32_t kH = kLo + kTile;            // bf16 state, [dv][dk]
-constexpr uint32_t kGates = kH + kTile;
-constexpr uint32_t kBars = kGates + sizeof(Gates);
-constexpr uint32_t kSmem = kBars + 512;
-static_assert(kSmem <= 232448, "shared memory of a CTA");
+
+// KD: key channels, 64 or 128 (narrower keys are filled with zeros).  128: a
+// ring of five 32 KB slots, one tile each.  64: q and k take 16 KB, and there is
+// room for two whole chunks.
+template <int KD>
+struct Layout {
+  static constexpr int kSlots = KD == 128 ? 5 : 6;
+  static constexpr int kPanels = KD / 64;
+  static constexpr uint32_t kLo = KD == 128 ? 5 * kTile : 4 * kTile;  // lo part of the scaled keys
+  static constexpr uint32_t kH = kLo + kPanels * kPanel;              // bf16 state, [dv][dk]; o
+  static constexpr uint32_t kGates = kH + kTile;
+  static constexpr uint32_t kBars = kGates + sizeof(Gates);
+  static constexpr uint32_t kSmem = kBars + 512;
+  static_assert(kSmem <= 232448, "shared memory of a CTA");
+  __device__ static __forceinline__ uint32_t at(int slot) {
+    return KD == 128 ? slot * kTile : slot / 3 * 2 * kTile + slot % 3 * kPanel;
+  }
+};
 
 enum {
   // B_O and B_DF by chunk parity: the loads wait on them too, and may lag a chunk
-  B_FULL = 0, B_S = kSlots, B_P, B_PV, B_O, B_HREADY = B_O + 2, B_HFREE, B_KT, B_DF, B_G = B_DF + 2,
+  B_FULL = 0, B_S = 6, B_P, B_PV, B_O, B_HREADY = B_O + 2, B_HFREE, B_KT, B_DF, B_G = B_DF + 2,
   B_GFREE, B_END, B_COUNT
 };
 // TMEM columns
 constexpr uint32_t T_S = 0, T_P = 0, T_DF = 128, T_OI = 256, T_O = 384;
 
+template <int KD>
 __global__ void __launch_bounds__(kThreads, 1)
 linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ Split sp,
                   const __grid_constant__ CUtensorMap mq,
                   const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                   const __grid_constant__ CUtensorMap mo) {
+  using L = Layout<KD>;
+  constexpr int kSlots = L::kSlots, kHalf = KD / 2;
+  constexpr uint32_t kLo = L::kLo, kH = L::kH, kGates = L::kGates, kBars = L::kBars;
   extern __shared__ __align__(1024) char sm[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kBars);
   Gates* gates = reinterpret_cast<Gates*>(sm + kGates);
@@ -111,7 +126,9 @@ linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ 
         }
         if (*abort) break;
         const CUtensorMap* m = i % 3 == 0 ? &mq : i % 3 == 1 ? &mk : &mv;
-        load_tile(sb + slot * kTile, m, bars + B_FULL + slot, t0 + c * C, i % 3 == 2 ? vz : qz);
+        // (a second panel of v that no channel reaches is never looked at)
+        load_tile(sb + L::at(slot), m, bars + B_FULL + slot, t0 + c * C, i % 3 == 2 ? vz : qz,
+                  i % 3 == 2 ? (a.dv > 64 ? 2 : 1) : L::kPanels);
       }
     }
   } else if (warp == 1) {
@@ -137,11 +154,11 @@ linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ 
           wait(B_FULL + sv, rv & 1);
           if (!wait(B_P, par)) break;  // and o of the last chunk has been read
           tc_fence_after();
-          mma_ts<true>(tmem + T_O, tmem + T_P, sb + sv * kTile, 0);
+          mma_ts<true>(tmem + T_O, tmem + T_P, sb + L::at(sv), 0);
           umma_commit(bars + B_PV);
           if (!wait(B_HREADY, par)) break;
           tc_fence_after();
-          mma_ss<false, false>(tmem + T_OI, sb + sq * kTile, sb + kH, 0);
+          mma_ss<false, false, 128, KD / 16>(tmem + T_OI, sb + L::at(sq), sb + kH, 0);
           umma_commit(bars + B_O + par);
         }
         if (c + 1 < chunks) {
@@ -154,14 +171,15 @@ linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ 
           if (c >= 0) wait(B_PV, par);  // P shares the columns of S
           if (!ok) break;
           tc_fence_after();
-          mma_ss<false, false>(tmem + T_S, sb + nq * kTile, sb + (nk < kSlots ? nk : 0) * kTile, 0);
+          mma_ss<false, false, 128, KD / 16>(tmem + T_S, sb + L::at(nq),
+                                             sb + L::at(nk < kSlots ? nk : 0), 0);
           umma_commit(bars + B_S);
         }
         if (c < 0) continue;
         if (!wait(B_KT, par)) break;
         tc_fence_after();
-        mma_ss<true, true>(tmem + T_DF, sb + sv * kTile, sb + sk * kTile, 0);
-        mma_ss<true, true>(tmem + T_DF, sb + sv * kTile, sb + kLo, 1);
+        mma_ss<true, true, KD>(tmem + T_DF, sb + L::at(sv), sb + L::at(sk), 0);
+        mma_ss<true, true, KD>(tmem + T_DF, sb + L::at(sv), sb + kLo, 1);
         umma_commit(bars + B_DF + par);
         sq = sv + 1;
         round = rv;
@@ -193,7 +211,7 @@ linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ 
       if (a.cu_seqlens && valid < C) {  // tokens of the next sequence behind this one
         const int iv = 3 * c + 2;
         if (!warp_wait(bars + B_FULL + iv % kSlots, (iv / kSlots) & 1, abort)) break;
-        if (i >= valid) zero_row(sm + (iv % kSlots) * kTile, i);
+        if (i >= valid) zero_row(sm + L::at(iv % kSlots), i);
       }
       if (!warp_wait(bars + B_G, par, abort)) break;
       const float pre = gates->pre[i], into = gates->eL[i];
@@ -254,6 +272,7 @@ linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ 
       const float fo = a.scale, fi = a.scale * into;
 #pragma unroll 1
       for (int p = 0; p < 4; ++p) {
+        if (32 * p >= a.dv) break;
         uint32_t x[32], y[32];
         tmem_ld32<32>(lanes + T_O + 32 * p, x);
         tmem_ld32<32>(lanes + T_OI + 32 * p, y);
@@ -286,12 +305,12 @@ linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ 
     }
   } else if (warp >= 8) {
     // --------------------------------------------------------------- state
-    const int s = (warp - 8) >> 2, r = (tid - 256) & 127;   // panel of dk, value column
+    const int s = (warp - 8) >> 2, r = (tid - 256) & 127;   // half of dk, value column
     const uint32_t lanes = tmem + ((uint32_t)(r & 96) << 16);
-    float H[64];
+    float H[kHalf];
 #pragma unroll
-    for (int i = 0; i < 64; ++i) {
-      const int d = 64 * s + i;
+    for (int i = 0; i < kHalf; ++i) {
+      const int d = kHalf * s + i;
       H[i] = from && r < a.dv && d < a.dk ? from[(size_t)d * a.dv + r] : 0.f;
     }
     bool ok = true;
@@ -302,8 +321,8 @@ linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ 
       // theirs and o has left the tile again
       if (c > 0 && !(ok = warp_wait(bars + B_HFREE, (c - 1) & 1, abort))) break;
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        *reinterpret_cast<uint4*>(sm + kH + sw128_chunk(128, r, 8 * s + j)) =
+      for (int j = 0; j < kHalf / 8; ++j)
+        *reinterpret_cast<uint4*>(sm + kH + sw128_chunk(128, r, kHalf / 8 * s + j)) =
             make_uint4(pack_bf162(H[8 * j], H[8 * j + 1]), pack_bf162(H[8 * j + 2], H[8 * j + 3]),
                        pack_bf162(H[8 * j + 4], H[8 * j + 5]),
                        pack_bf162(H[8 * j + 6], H[8 * j + 7]));
@@ -315,15 +334,16 @@ linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ 
       if (lane == 0) mbar_arrive(bars + B_GFREE);
       if (!(ok = warp_wait(bars + B_FULL + ik % kSlots, (ik / kSlots) & 1, abort))) break;
       if (!(ok = warp_wait(bars + B_S, par, abort))) break;
-      scale_row(sm + (ik % kSlots) * kTile, sm + kLo, r, s, wt, r < valid);
+      scale_row(sm + L::at(ik % kSlots), sm + kLo, r, kHalf / 8 * s, kHalf / 8 * (s + 1), wt,
+                r < valid);
       warp_publish(bars + B_KT);
       // the chunk's contribution
       if (!(ok = warp_wait(bars + B_DF + par, (c >> 1) & 1, abort))) break;
       tc_fence_after();
 #pragma unroll
-      for (int p = 0; p < 2; ++p) {
+      for (int p = 0; p < kHalf / 32; ++p) {
         uint32_t x[32];
-        tmem_ld32<32>(lanes + T_DF + 64 * s + 32 * p, x);
+        tmem_ld32<32>(lanes + T_DF + kHalf * s + 32 * p, x);
         tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 32; ++i)
@@ -333,8 +353,8 @@ linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ 
     }
     if (ok && a.hT && u.seg == u.segs - 1 && r < a.dv) {
 #pragma unroll
-      for (int i = 0; i < 64; ++i) {
-        const int d = 64 * s + i;
+      for (int i = 0; i < kHalf; ++i) {
+        const int d = kHalf * s + i;
         if (d < a.dk) a.hT[st + (size_t)d * a.dv + r] = H[i];
       }
     }
@@ -385,11 +405,12 @@ cudaError_t linear_chunk_fwd(const LinearArgs& a, char* ws, cudaStream_t s) {
   Split sp = linear_split(a.N, a.B, a.H, a.T, a.cu_seqlens != nullptr);
   cudaError_t e = linear_split_plan(a, sp, ws, s);
   if (e == cudaSuccess) e = linear_segment_states(a, sp, ws, false, 0, s);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(linear_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)kSmem);
   if (e != cudaSuccess) return e;
-  linear_fwd_kernel<<<(unsigned)sp.items * a.H, kThreads, kSmem, s>>>(a, sp, mq, mk, mv, mo);
+  const auto kernel = a.dk <= 64 ? linear_fwd_kernel<64> : linear_fwd_kernel<128>;
+  const uint32_t smem = a.dk <= 64 ? Layout<64>::kSmem : Layout<128>::kSmem;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<(unsigned)sp.items * a.H, kThreads, smem, s>>>(a, sp, mq, mk, mv, mo);
   return cudaGetLastError();
 }
 

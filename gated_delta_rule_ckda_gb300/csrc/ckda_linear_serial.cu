@@ -116,6 +116,7 @@ __global__ void slot_plan_kernel(LinearArgs a, int tokens, int32_t* slot0) {
   }
   sum[threadIdx.x] = s;
   __syncthreads();
+  if (i0 >= i1) return;
   int32_t before = 0;
   for (int j = 0; j < (int)threadIdx.x; ++j) before += sum[j];
   for (int i = i0; i < i1; ++i) {
@@ -124,7 +125,7 @@ __global__ void slot_plan_kernel(LinearArgs a, int tokens, int32_t* slot0) {
     seq_range(a, i, t0, len);
     before += pieces_of(len, tokens) + 1;
   }
-  if (threadIdx.x == 1023) slot0[a.N] = before;
+  if (i1 == a.N) slot0[a.N] = before;
 }
 
 // Register i of a thread's quarter p of a row: column.

@@ -139,7 +139,7 @@ linear_state_kernel(const __grid_constant__ LinearArgs a, const __grid_constant_
       if (i >= 1 && !warp_wait(bars + B_DF + ((i - 1) & 1), ((i - 1) / 2) & 1, abort)) break;
 #pragma unroll 1
       for (int p = 0; p < 2; ++p)
-        scale_row(sm + ix * kTile, sm + kLo, t, p, wt, t < valid);
+        scale_row(sm + ix * kTile, sm + kLo, t, 8 * p, 8 * p + 8, wt, t < valid);
       warp_publish(bars + B_KT);
     }
   } else if (warp >= 8) {
@@ -242,30 +242,40 @@ __global__ void __launch_bounds__(1024) split_plan_kernel(LinearArgs a, int per,
   for (int i = i0; i < i1; ++i) s += segments(i);
   sum[threadIdx.x] = s;
   __syncthreads();
+  if (i0 >= i1) return;
   int32_t before = 0;
   for (int j = 0; j < (int)threadIdx.x; ++j) before += sum[j];
   for (int i = i0; i < i1; ++i) {
     item0[i] = before;
     before += segments(i);
   }
-  if (threadIdx.x == 1023) item0[a.N] = before;
+  if (i1 == a.N) item0[a.N] = before;
 }
 
 // Joins what the segments hand on: in order, each adds its own to the decayed
-// state before it.  A block takes 1024 elements of one (sequence, head).
+// state before it.  A thread takes one element of one (sequence, head), and loads
+// eight segments' ahead.
 __global__ void __launch_bounds__(256) segment_scan_kernel(LinearArgs a, Split sp, int back) {
   const int rank = blockIdx.x / a.H, h = blockIdx.x % a.H;
   const int i0 = sp.item0 ? sp.item0[rank] : rank * sp.per;
   const int segs = sp.item0 ? min(sp.item0[rank + 1], sp.items) - i0 : sp.per;
-  const int n = a.dk * a.dv;
-  for (int e = blockIdx.y * 1024 + threadIdx.x; e < min(n, (int)(blockIdx.y + 1) * 1024); e += 256) {
-    float s = 0.f;
-    for (int k = 0; k < segs - 1; ++k) {
-      const size_t at = (size_t)(i0 + (back ? segs - 1 - k : k)) * a.H + h;
-      float* p = sp.state + at * n + e;
-      s = k == 0 ? *p : fmaf(sp.decay[at], s, *p);
-      *p = s;
+  const int n = a.dk * a.dv, e = blockIdx.y * 256 + threadIdx.x;
+  if (e >= n) return;
+  auto slot = [&](int k) { return (size_t)(i0 + (back ? segs - 1 - k : k)) * a.H + h; };
+  float s = 0.f;
+  for (int k0 = 0; k0 < segs - 1; k0 += 8) {
+    float own[8], dec[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      own[k] = k0 + k < segs - 1 ? sp.state[slot(k0 + k) * n + e] : 0.f;
+      dec[k] = k0 + k < segs - 1 ? sp.decay[slot(k0 + k)] : 0.f;
     }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k0 + k < segs - 1) {
+        s = k0 + k == 0 ? own[k] : fmaf(dec[k], s, own[k]);
+        sp.state[slot(k0 + k) * n + e] = s;
+      }
   }
 }
 
@@ -350,7 +360,7 @@ cudaError_t linear_segment_states(const LinearArgs& a, Split& sp, char* ws, bool
   cudaError_t e = back ? launch_states<true, false>(a, sp, ChunkImages{}, s)
                        : launch_states<false, false>(a, sp, ChunkImages{}, s);
   if (e != cudaSuccess) return e;
-  segment_scan_kernel<<<dim3((unsigned)a.N * a.H, (a.dk * a.dv + 1023) / 1024), 256, 0, s>>>(
+  segment_scan_kernel<<<dim3((unsigned)a.N * a.H, (a.dk * a.dv + 255) / 256), 256, 0, s>>>(
       a, sp, back ? 1 : 0);
   return cudaGetLastError();
 }
