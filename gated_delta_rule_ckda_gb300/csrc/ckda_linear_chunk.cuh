@@ -23,6 +23,8 @@ struct Split {
   const int32_t* item0;  // packed: [N + 1] first segment by rank in a.order
   float* state;          // [items * H][dk][dv]: what each segment hands on
   float* decay;          // [items * H]: over the segment
+  float* begin;          // [N * H][dk][dv]: h0 again, for the first segments of sequences
+                         // that are cut (hT may be h0, and another CTA writes it)
 };
 // A segment of one (sequence, head).
 struct Piece {
@@ -31,12 +33,14 @@ struct Piece {
   int c0, chunks;        // chunks, counted inside the sequence
   int seg, segs, item;
 };
-__device__ __forceinline__ bool piece_of(const LinearArgs& a, const Split& sp, unsigned block,
-                                         Piece& u) {
+__device__ __forceinline__ unsigned pieces(const LinearArgs& a, const Split& sp) {
+  return (unsigned)(a.cu_seqlens ? min(sp.item0[a.N], sp.items) : sp.items) * a.H;
+}
+__device__ __forceinline__ Piece piece_of(const LinearArgs& a, const Split& sp, unsigned block) {
+  Piece u;
   u.item = block / a.H;
   u.h = block % a.H;
   if (a.cu_seqlens) {
-    if (u.item >= sp.item0[a.N]) return false;
     int lo = 0, hi = a.N;  // item0[lo] <= item < item0[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -60,7 +64,7 @@ __device__ __forceinline__ bool piece_of(const LinearArgs& a, const Split& sp, u
   const int b = a.cu_seqlens ? 0 : u.n;
   u.qz = b * a.Hk + u.h / (a.H / a.Hk);
   u.vz = b * a.H + u.h;
-  return true;
+  return u;
 }
 
 // ------------------------------------------------------------------- TMA

@@ -86,14 +86,15 @@ linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ 
     return;
   }
 
-  Piece u;
-  if (!piece_of(a, sp, blockIdx.x, u)) return;
+  if (blockIdx.x >= pieces(a, sp)) return;  // the grid is a bound
+  const Piece u = piece_of(a, sp, blockIdx.x);
   const int t0 = u.t0, len = u.len, chunks = u.chunks, qz = u.qz, vz = u.vz;
   const size_t vrow = (size_t)vz * a.T + t0;
   const size_t states = (size_t)a.dk * a.dv, st = ((size_t)u.n * a.H + u.h) * states;
-  const float* from = u.seg > 0 ? sp.state + ((size_t)(u.item - 1) * a.H + u.h) * states
-                      : a.h0    ? a.h0 + st
-                                : nullptr;
+  const float* from = u.seg > 0    ? sp.state + ((size_t)(u.item - 1) * a.H + u.h) * states
+                      : u.segs > 1 ? sp.begin + st
+                      : a.h0       ? a.h0 + st
+                                   : nullptr;
 
   if (tid == 0) {
     for (int i = 0; i < B_COUNT; ++i) {

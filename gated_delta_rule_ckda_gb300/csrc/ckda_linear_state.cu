@@ -50,8 +50,8 @@ linear_state_kernel(const __grid_constant__ LinearArgs a, const __grid_constant_
     if (tid == 0) set_status(a.status, CKDA_ERR_CUDA);
     return;
   }
-  Piece u;
-  if (!piece_of(a, sp, blockIdx.x, u)) return;
+  if (blockIdx.x >= pieces(a, sp)) return;  // the grid is a bound
+  const Piece u = piece_of(a, sp, blockIdx.x);
   // the first segment in this direction, and the one that hands nothing on
   const bool starts = BACK ? u.seg == u.segs - 1 : u.seg == 0;
   const bool ends = BACK ? u.seg == 0 : u.seg == u.segs - 1;
@@ -261,6 +261,11 @@ __global__ void __launch_bounds__(256) segment_scan_kernel(LinearArgs a, Split s
   const int segs = sp.item0 ? min(sp.item0[rank + 1], sp.items) - i0 : sp.per;
   const int n = a.dk * a.dv, e = blockIdx.y * 256 + threadIdx.x;
   if (e >= n) return;
+  if (!back) {
+    const int seq = a.order ? a.order[rank] : rank;
+    const size_t st = ((size_t)seq * a.H + h) * n + e;
+    sp.begin[st] = a.h0 ? a.h0[st] : 0.f;
+  }
   auto slot = [&](int k) { return (size_t)(i0 + (back ? segs - 1 - k : k)) * a.H + h; };
   float s = 0.f;
   for (int k0 = 0; k0 < segs - 1; k0 += 8) {
@@ -314,13 +319,16 @@ Split linear_split(int N, int B, int H, int T, bool packed) {
   return sp;
 }
 
-// [N + 1] plan, then for each direction the states and decays of the segments.
+// [N + 1] plan, h0 again, then for each direction the states and decays of the
+// segments.
 size_t linear_split_bytes(const Split& sp, int N, int H, int dk, int dv, bool packed,
                           int directions) {
   const size_t slots = (size_t)sp.items * H;
   const bool cut = packed || sp.per > 1;
   return up256(((size_t)N + 1) * 4) +
-         (cut ? directions * (up256(slots * dk * dv * 4) + up256(slots * 4)) : 0);
+         (cut ? up256((size_t)N * H * dk * dv * 4) +
+                    directions * (up256(slots * dk * dv * 4) + up256(slots * 4))
+              : 0);
 }
 
 cudaError_t linear_split_plan(const LinearArgs& a, Split& sp, char* ws, cudaStream_t s) {
@@ -352,7 +360,9 @@ cudaError_t linear_segment_states(const LinearArgs& a, Split& sp, char* ws, bool
   if (!a.cu_seqlens && sp.per == 1) return cudaSuccess;
   const size_t slots = (size_t)sp.items * a.H;
   const size_t states = up256(slots * a.dk * a.dv * 4), decays = up256(slots * 4);
-  char* at = ws + up256(((size_t)a.N + 1) * 4) + dir * (states + decays);
+  char* at = ws + up256(((size_t)a.N + 1) * 4);
+  sp.begin = reinterpret_cast<float*>(at);
+  at += up256((size_t)a.N * a.H * a.dk * a.dv * 4) + dir * (states + decays);
   sp.state = reinterpret_cast<float*>(at);
   sp.decay = reinterpret_cast<float*>(at + states);
   // packed, every sequence shorter than a segment: nothing to join

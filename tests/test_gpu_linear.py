@@ -302,3 +302,38 @@ def test_no_states_at_either_end_of_segments(ck):
 def test_long_packed_sequences_are_cut(ck):
     cu = [0, 40, 1940, 1940, 3300, 3301]
     compare(ck, *make(1, 2, 1, 3301, 64, 96, BF, 5, decay=0.02, N=5), scale=0.125, cu=cu)
+
+
+def test_cut_sequence_updates_its_state_in_place(ck):
+    """hT may be h0, although different segments read the one and write the other."""
+    x, _ = make(1, 2, 2, 2500, 64, 64, BF, 7, decay=0.01)
+    want = ref.linear(**x, scale=0.1)
+    s = gpu(x)
+    o, _ = ck.linear_fwd(**s, hT=s["h0"], scale=0.1)
+    ref.check(o, want[0], ref.token_tol(BF, 2500), "o")
+    ref.check(s["h0"], want[1], ref.state_tol(BF, 2500), "state")
+
+
+@pytest.mark.parametrize("T", [1, 100, 300])
+def test_more_heads_than_sms(ck, T):
+    """A CTA goes through several short sequences; widths and tails among them."""
+    x, e = make(41, 8, 4, T, 64, 40, BF, T)
+    d, eo = gpu(x), gpu(e)
+    o, hT = ck.linear_fwd(**d, scale=0.125)
+    grads = ck.linear_bwd(d["q"], d["k"], d["v"], d["g"], eo["do"], h0=d["h0"], dhT=eo["dhT"], scale=0.125)
+    for b in (0, 18, 37, 40):   # sequences of different rounds
+        y = {n: t[b:b + 1] for n, t in x.items()}
+        z = {n: t[b:b + 1] for n, t in e.items()}
+        want = ref.linear(**y, scale=0.125, **z)
+        ref.check(o[b:b + 1], want[0], ref.token_tol(BF, T), "o")
+        ref.check(hT[b:b + 1], want[1], ref.state_tol(BF, T), "hT")
+        for name, t, w in zip(("dq", "dk", "dv"), grads, want[2:]):
+            ref.check(t[b:b + 1], w, ref.token_tol(BF, T), name)
+        ref.check(grads[3][b:b + 1], want[5], ref.decay_tol(BF, T), "dg")
+        ref.check(grads[4][b:b + 1], want[6], ref.state_tol(BF, T), "dh0")
+
+
+def test_many_packed_sequences(ck):
+    gen = torch.Generator().manual_seed(9)
+    cu = [0] + torch.randint(0, 200, (60,), generator=gen).cumsum(0).tolist()
+    compare(ck, *make(1, 6, 3, cu[-1], 64, 64, BF, 11, N=60), scale=0.125, cu=cu)
