@@ -74,7 +74,8 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(LinearArgs a, int32_t*
 //   warps 12-15 C: thread = key row.    <H, G>; P^T; dV, in two halves of 64
 //               columns for want of TMEM
 // Shared memory holds three of the four state tiles: Hlo comes last, where Hhi
-// was, while B and C work with G.
+// was, while B and C work with G.  Results are staged where their tile's readers
+// are done: dQ over H, dK over q, dV over v and Glo.
 // An accumulator takes the state's part first; its thread scales that row in
 // place and the product inside the chunk is added to it.  A token's own product
 // (W_ii's factors, the largest under strong decay) stays out of the bf16 operands
@@ -89,13 +90,14 @@ constexpr uint32_t kBars = kGates + sizeof(Gates);
 constexpr uint32_t kSmem = kBars + 512;
 static_assert(kSmem <= 232448, "shared memory of a CTA");
 enum { B_QK, B_VD, B_HH, B_HL, B_GH, B_GL, B_G, B_TAIL, B_A, B_B, B_DSA, B_DSB, B_DSC, B_X1H, B_X1, B_X2, B_X3,
-       B_X1S = B_X3 + 2, B_X2S, B_X3S, B_DQ = B_X3S + 2, B_DK, B_DV, B_HALF = B_DV + 2, B_HG,
-       // free again: the columns of X1, X2, X3; the tiles of H, V, dO; the decays
-       B_XR = B_HG + 2, B_FH = B_XR + 3, B_FV, B_FD, B_PART, B_GFREE, B_END, B_COUNT };
+       B_X1S = B_X3 + 2, B_X2S, B_X3S, B_DQ = B_X3S + 2, B_DK, B_DV, B_HG = B_DV + 2,
+       // free again: the columns of X1, X2, X3; the tiles of H, q, v, Glo; the decays
+       B_XR, B_FH = B_XR + 3, B_FQ, B_FV, B_FG, B_PART, B_GFREE, B_END, B_COUNT };
 // TMEM columns: S, dP, S^T, dP^T; then dS over S and P^T behind it, X1 over dP,
-// X2 over S^T, dS^T over dP^T and X3 (64 columns) behind it
+// X2 over S^T, dS^T over dP^T and the first half of X3 (64 columns) behind it,
+// the second over dS
 constexpr uint32_t T_S = 0, T_DP = 128, T_ST = 256, T_DPT = 384;
-constexpr uint32_t T_DS = 0, T_PT = 64, T_X1 = 128, T_X2 = 256, T_DST = 384, T_X3 = 448;
+constexpr uint32_t T_DS = 0, T_PT = 64, T_X1 = 128, T_X2 = 256, T_DST = 384, T_X3 = 448, T_X3B = 0;
 }  // namespace gr
 
 // Chunk and head of a block.
@@ -232,8 +234,8 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
   Gates* gates = reinterpret_cast<Gates*>(sm + kGates);
   volatile int* abort = reinterpret_cast<volatile int*>(sm + kBars + 400);
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(sm + kBars + 404);
-  float* hg = reinterpret_cast<float*>(sm + kBars + 408);   // <H, G> by warp of C
-  float* run = reinterpret_cast<float*>(sm + kBars + 424);  // sums by warp of A
+  float* hg = reinterpret_cast<float*>(sm + kBars + 408);   // <H, G> by warp of A, C
+  float* run = reinterpret_cast<float*>(sm + kBars + 440);  // sums by warp of A
   const uint32_t sb = smem_u32(sm);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (sb & 1023u) {
@@ -247,7 +249,7 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
   if (tid == 0) {
     for (int i = 0; i < B_COUNT; ++i) {
       const bool by_warps = (i >= B_DSA && i <= B_DSC) || (i >= B_X1S && i < B_DQ) ||
-                            (i >= B_HALF && i < B_FH) || i == B_GFREE;
+                            (i >= B_HG && i < B_FH) || i == B_GFREE;
       mbar_init(bars + i, i == B_TAIL ? 12 : i == B_PART ? 8 : by_warps ? 4 : 1);
     }
     *abort = 0;
@@ -273,14 +275,14 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
         bool ok = true;
         // a barrier of the chunk before, whose tile is wanted
         auto last = [&](int bar) { ok = ok && (!again || mbar_wait(bars + bar, par ^ 1)); };
-        last(B_DQ); last(B_DK); last(B_X3 + 1);
+        last(B_DQ); last(B_X3 + 1); last(B_FQ);
         if (!ok) { *abort = 1; break; }
         mbar_arrive_expect_tx(bars + B_QK, 2 * kTile);
         for (int p = 0; p < 2; ++p) {
           tma_load_3d(sb + kQ + p * kPanel, &mq, bars + B_QK, 64 * p, u.y, u.qz);
           tma_load_3d(sb + kK + p * kPanel, &mk, bars + B_QK, 64 * p, u.y, u.qz);
         }
-        last(B_FV); last(B_FD);
+        last(B_FV); last(B_DV + 1);
         if (!ok) { *abort = 1; break; }
         mbar_arrive_expect_tx(bars + B_VD, 2 * kTile);
         for (int p = 0; p < 2; ++p) {
@@ -293,6 +295,8 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
         load_image(sb + kS0, himg, bars + B_HH);
         mbar_arrive_expect_tx(bars + B_GH, kTile);
         load_image(sb + kS2, gimg, bars + B_GH);
+        last(B_FG);
+        if (!ok) { *abort = 1; break; }
         mbar_arrive_expect_tx(bars + B_GL, kTile);
         load_image(sb + kS1, gimg + kTile, bars + B_GL);
         if (!mbar_wait(bars + B_X1H, par) || !mbar_wait(bars + B_HG, par)) { *abort = 1; break; }
@@ -321,20 +325,17 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
       bool ok = mbar_wait(bars + B_QK, par);
       auto last = [&](int bar) { ok = ok && (!again || mbar_wait(bars + bar, par ^ 1)); };
       if (a.cu_seqlens && u.valid < C) ok = ok && mbar_wait(bars + B_TAIL, tails++ & 1);
-      last(B_DQ); last(B_DV + 1);
+      last(B_DQ); last(B_DV + 1); last(B_XR + 2); last(B_XR + 1);
       if (!ok) break;
       tc_fence_after();
       mma_ss<false, false>(tmem + T_S, sb + kQ, sb + kK, 0);
-      last(B_XR);
+      mma_ss<false, false>(tmem + T_ST, sb + kK, sb + kQ, 0);
+      last(B_XR); last(B_DK);
       ok = ok && mbar_wait(bars + B_VD, par);
       if (!ok) break;
       tc_fence_after();
       mma_ss<false, false>(tmem + T_DP, sb + kDo, sb + kV, 0);
       umma_commit(bars + B_A);
-      last(B_XR + 1); last(B_XR + 2); last(B_DK);
-      if (!ok) break;
-      tc_fence_after();
-      mma_ss<false, false>(tmem + T_ST, sb + kK, sb + kQ, 0);
       mma_ss<false, false>(tmem + T_DPT, sb + kV, sb + kDo, 0);
       umma_commit(bars + B_B);
       // what is left, by readiness; `done` keeps the order that TMEM asks for
@@ -381,13 +382,13 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
           mma_ts<true, 64>(tmem + T_X3, tmem + T_PT, sb + kDo, 1);
           umma_commit(bars + B_DV);
         }
-        if (ready(X3B, DVA, B_HALF)) {
-          mma_ss<false, false, 64>(tmem + T_X3, sb + kK, sb + kS2 + kPanel / 2, 0);
-          mma_ss<false, false, 64>(tmem + T_X3, sb + kK, sb + kS1 + kPanel / 2, 1);
+        if (ready(X3B, X2 | DQ, B_DQ)) {  // dS has been read
+          mma_ss<false, false, 64>(tmem + T_X3B, sb + kK, sb + kS2 + kPanel / 2, 0);
+          mma_ss<false, false, 64>(tmem + T_X3B, sb + kK, sb + kS1 + kPanel / 2, 1);
           umma_commit(bars + B_X3 + 1);
         }
         if (ready(DVB, X3B, B_X3S + 1)) {
-          mma_ts<true, 64>(tmem + T_X3, tmem + T_PT, sb + kDo + kPanel, 1);
+          mma_ts<true, 64>(tmem + T_X3B, tmem + T_PT, sb + kDo + kPanel, 1);
           umma_commit(bars + B_DV + 1);
         }
         if (globaltimer_ns() - start > kWaitLimitNs) break;
@@ -514,10 +515,12 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
         tc_fence_after();
         dot = scale_acc(lanes + T_X1, into, own, sm + kK, sm + kQ, row, 0, 4);
         warp_arrive(bars + B_X1S);
+        // the rest of <H, G> meanwhile: (Hlo, Ghi)
+        if (!warp_wait(bars + B_HL, par, abort) || !warp_wait(bars + B_GH, par, abort)) break;
+        hgsum = tile_dot(sm + kS0, sm + kS2, row);
+        named_sync(1, 128);  // dQ goes over Hlo
         if (!warp_wait(bars + B_DQ, par, abort)) break;
         tc_fence_after();
-        // over H's tile
-        if (!warp_wait(bars + B_HG + 1, par, abort)) break;
         stage_acc(lanes + T_X1, sm + kS0, w.dq ? w.dq + (vrow + row) * a.dk : nullptr, a.dk, in,
                   row, 0, 4);
         warp_arrive(bars + B_XR);
@@ -605,41 +608,41 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
           warp_arrive(bars + B_X2S);
           if (!warp_wait(bars + B_DK, par, abort)) break;
           tc_fence_after();
-          // over V's tile: X2 was its last reader
-          stage_acc(lanes + T_X2, sm + kV, w.dk ? w.dk + (vrow + row) * a.dk : nullptr, a.dk, in,
+          // over q, which A has to have read too
+          if (!warp_wait(bars + B_X1S, par, abort)) break;
+          stage_acc(lanes + T_X2, sm + kQ, w.dk ? w.dk + (vrow + row) * a.dk : nullptr, a.dk, in,
                     row, 0, 4);
           warp_arrive(bars + B_XR + 1);
-          if (!w.dk) put(&mdk, a.dkey, krow, a.dk, kV, u.qz, 0, 2);
+          if (!w.dk) put(&mdk, a.dkey, krow, a.dk, kQ, u.qz, 0, 2);
         } else {
           bool ok = true;
 #pragma unroll 1
           for (int half = 0; half < 2; ++half) {
+            const uint32_t acc = lanes + (half ? T_X3B : T_X3), to = half ? kS1 : kV;
             if (!(ok = warp_wait(bars + B_X3 + half, par, abort))) break;
             tc_fence_after();
-            scale_acc(lanes + T_X3, out, own, sm + kDo, sm + kDo, row, 2 * half, 2 * half + 2);
+            scale_acc(acc, out, own, sm + kDo, sm + kDo, row, 2 * half, 2 * half + 2);
             warp_arrive(bars + B_X3S + half);
-            if (half == 0) {  // meanwhile
-              if (!(ok = warp_wait(bars + B_HL, par, abort))) break;
-              hgsum += tile_dot(sm + kS0, sm + kS2, row);
-              warp_arrive(bars + B_HG + 1);
-#pragma unroll
-              for (int m = 16; m >= 1; m >>= 1) hgsum += __shfl_xor_sync(0xffffffffu, hgsum, m);
-              if (lane == 0) hg[wq] = hgsum;
-            }
-            // over this panel of dO: its readers were this product and dO H^T
             if (!(ok = warp_wait(bars + B_DV + half, par, abort))) break;
-            if (!(ok = warp_wait(bars + B_X1, par, abort))) break;
             tc_fence_after();
-            stage_acc(lanes + T_X3, sm + kDo, nullptr, a.dv, in, row, 2 * half, 2 * half + 2);
-            warp_arrive(bars + (half == 0 ? B_HALF : B_XR + 2));
-            put(&mdv, a.dval, vrow, a.dv, kDo, u.vz, half, half + 1);
+            // the first panel over v, once X2 has read it; the second over Glo, once
+            // X3 has
+            if (half == 0) {
+              if (!(ok = warp_wait(bars + B_X2, par, abort))) break;
+            } else if (lead) {
+              store_read_wait();
+              mbar_arrive(bars + B_FV);
+            }
+            stage_acc(acc, sm + to, nullptr, a.dv, in, row, 2 * half, 2 * half + 2);
+            if (half) warp_arrive(bars + B_XR + 2);
+            put(&mdv, a.dval, vrow, a.dv, to, u.vz, half, half + 1);
           }
           if (!ok) break;
         }
       }
       if (lead) {
         store_read_wait();
-        mbar_arrive(bars + (wg == 0 ? B_FH : wg == 1 ? B_FV : B_FD));
+        mbar_arrive(bars + (wg == 0 ? B_FH : wg == 1 ? B_FQ : B_FG));
       }
       // dg_t = e^{L_C} <H, G> + sum_{j<t} kd_j + sum_{i>=t} (qd_i + row_i - col_i):
       // B hands its sums by token to A, over decays that all three have read
@@ -647,6 +650,11 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
         if (!warp_wait(bars + B_DSA, par, abort) || !warp_wait(bars + B_DSC, par, abort)) break;
         gates->eL[row] = in ? wsum : 0.f;
         gates->w[row] = in ? dot : 0.f;
+      }
+      if (wg != 1) {
+#pragma unroll
+        for (int m = 16; m >= 1; m >>= 1) hgsum += __shfl_xor_sync(0xffffffffu, hgsum, m);
+        if (lane == 0) hg[wg * 2 + wq] = hgsum;  // A 0 .. 3, C 4 .. 7
       }
       if (wg != 0) {
         __syncwarp();
@@ -668,7 +676,10 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
       if (lane == 31) run[wq] = fwd;
       if (lane == 0) run[4 + wq] = back;
       named_sync(1, 128);
-      float t = gates->all * (hg[0] + hg[1] + hg[2] + hg[3]) + excl + back;
+      float t = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t += hg[i];
+      t = gates->all * t + excl + back;
       for (int i = 0; i < wq; ++i) t += run[i];
       for (int i = wq + 1; i < 4; ++i) t += run[4 + i];
       if (in) (w.dg ? w.dg : a.dg)[vrow + row] = t;
