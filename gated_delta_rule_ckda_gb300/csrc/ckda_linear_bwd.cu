@@ -73,8 +73,8 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(LinearArgs a, int32_t*
 //   warps 8-11  B: thread = key row.    dS^T and the column sums of W; dK
 //   warps 12-15 C: thread = key row.    <H, G>; P^T; dV, in two halves of 64
 //               columns for want of TMEM
-// Shared memory holds three of the four state tiles: Hlo comes last, where Hhi
-// was, while B and C work with G.  Results are staged where their tile's readers
+// Shared memory holds three of the four state tiles: Glo comes last, where Hlo
+// was, once dO H^T is done.  Results are staged where their tile's readers
 // are done: dQ over H, dK over q, dV over v and Glo.
 // An accumulator takes the state's part first; its thread scales that row in
 // place and the product inside the chunk is added to it.  A token's own product
@@ -84,12 +84,12 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(LinearArgs a, int32_t*
 namespace gr {
 constexpr int kThreads = 512;
 constexpr uint32_t kQ = 0, kK = kTile, kV = 2 * kTile, kDo = 3 * kTile;
-constexpr uint32_t kS0 = 4 * kTile, kS1 = 5 * kTile, kS2 = 6 * kTile;  // Hhi, then Hlo; Glo; Ghi
+constexpr uint32_t kS0 = 4 * kTile, kS1 = 5 * kTile, kS2 = 6 * kTile;  // Hhi; Hlo, then Glo; Ghi
 constexpr uint32_t kGates = 7 * kTile;
 constexpr uint32_t kBars = kGates + sizeof(Gates);
 constexpr uint32_t kSmem = kBars + 512;
 static_assert(kSmem <= 232448, "shared memory of a CTA");
-enum { B_QK, B_VD, B_HH, B_HL, B_GH, B_GL, B_G, B_TAIL, B_A, B_B, B_DSA, B_DSB, B_DSC, B_X1H, B_X1, B_X2, B_X3,
+enum { B_QK, B_VD, B_H, B_GH, B_GL, B_G, B_TAIL, B_A, B_B, B_DSA, B_DSB, B_DSC, B_X1, B_X2, B_X3,
        B_X1S = B_X3 + 2, B_X2S, B_X3S, B_DQ = B_X3S + 2, B_DK, B_DV, B_HG = B_DV + 2,
        // free again: the columns of X1, X2, X3; the tiles of H, q, v, Glo; the decays
        B_XR, B_FH = B_XR + 3, B_FQ, B_FV, B_FG, B_PART, B_GFREE, B_END, B_COUNT };
@@ -289,19 +289,16 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
           tma_load_3d(sb + kV + p * kPanel, &mv, bars + B_VD, 64 * p, u.y, u.vz);
           tma_load_3d(sb + kDo + p * kPanel, &mo, bars + B_VD, 64 * p, u.y, u.vz);
         }
-        last(B_FH);
+        last(B_FH); last(B_FG);
         if (!ok) { *abort = 1; break; }
-        mbar_arrive_expect_tx(bars + B_HH, kTile);
-        load_image(sb + kS0, himg, bars + B_HH);
+        mbar_arrive_expect_tx(bars + B_H, 2 * kTile);
+        load_image(sb + kS0, himg, bars + B_H);
+        load_image(sb + kS1, himg + kTile, bars + B_H);
         mbar_arrive_expect_tx(bars + B_GH, kTile);
         load_image(sb + kS2, gimg, bars + B_GH);
-        last(B_FG);
-        if (!ok) { *abort = 1; break; }
-        mbar_arrive_expect_tx(bars + B_GL, kTile);
+        if (!mbar_wait(bars + B_X1, par) || !mbar_wait(bars + B_HG, par)) { *abort = 1; break; }
+        mbar_arrive_expect_tx(bars + B_GL, kTile);  // Hlo has been read
         load_image(sb + kS1, gimg + kTile, bars + B_GL);
-        if (!mbar_wait(bars + B_X1H, par) || !mbar_wait(bars + B_HG, par)) { *abort = 1; break; }
-        mbar_arrive_expect_tx(bars + B_HL, kTile);  // Hhi has been read
-        load_image(sb + kS0, himg + kTile, bars + B_HL);
         // What comes next, into L2 while this chunk is worked on: tiles come free
         // late, and their loads should not wait for HBM then.
         if (block + step < blocks) {
@@ -339,7 +336,7 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
       mma_ss<false, false>(tmem + T_DPT, sb + kV, sb + kDo, 0);
       umma_commit(bars + B_B);
       // what is left, by readiness; `done` keeps the order that TMEM asks for
-      enum { X1H = 1, X1L = 2, X2 = 4, X3A = 8, X3B = 16, DQ = 32, DK = 64, DVA = 128, DVB = 256 };
+      enum { X1 = 1, X2H = 2, X2L = 4, X3B = 8, DQ = 16, DK = 32, DVA = 64, DVB = 128, ALL = 255 };
       uint32_t done = 0;
       const uint64_t start = globaltimer_ns();
       auto ready = [&](uint32_t what, uint32_t after, int bar) {
@@ -348,52 +345,48 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
         done |= what;
         return true;
       };
-      bool dsb = false, dsc = false, gl = false;
-      while (done != 511 && !*abort) {
-        if (!dsb) dsb = mbar_test(bars + B_DSB, par);
-        if (!dsc) dsc = mbar_test(bars + B_DSC, par);
-        if (!gl) gl = mbar_test(bars + B_GH, par) && mbar_test(bars + B_GL, par);
-        if (!(done & X1H) && mbar_test(bars + B_HH, par) && ready(X1H, 0, B_DSA)) {
-          mma_ss<false, true>(tmem + T_X1, sb + kDo, sb + kS0, 0);
-          umma_commit(bars + B_X1H);
-        }
-        if (ready(X1L, X1H, B_HL)) {
-          mma_ss<false, true>(tmem + T_X1, sb + kDo, sb + kS0, 1);
-          umma_commit(bars + B_X1);
-        }
-        if (ready(DQ, X1L, B_X1S)) {
+      for (uint32_t look = 1; done != ALL; ++look) {
+        if (!(done & X1)) {
+          if (mbar_test(bars + B_H, par) && ready(X1, 0, B_DSA)) {
+            mma_ss<false, true>(tmem + T_X1, sb + kDo, sb + kS0, 0);
+            mma_ss<false, true>(tmem + T_X1, sb + kDo, sb + kS1, 1);
+            umma_commit(bars + B_X1);
+          }
+        } else if (ready(DQ, X1, B_X1S)) {
           mma_ts<true>(tmem + T_X1, tmem + T_DS, sb + kK, 1);
           umma_commit(bars + B_DQ);
         }
-        if (gl && dsc && ready(X2, 0, B_DSB)) {
-          mma_ss<false, true>(tmem + T_X2, sb + kV, sb + kS2, 0);
+        if (!(done & X2H)) {
+          if (mbar_test(bars + B_GH, par) && mbar_test(bars + B_DSC, par) && ready(X2H, 0, B_DSB))
+            mma_ss<false, true>(tmem + T_X2, sb + kV, sb + kS2, 0);
+        } else if (ready(X2L, X2H, B_GL)) {
           mma_ss<false, true>(tmem + T_X2, sb + kV, sb + kS1, 1);
           umma_commit(bars + B_X2);
           mma_ss<false, false, 64>(tmem + T_X3, sb + kK, sb + kS2, 0);
           mma_ss<false, false, 64>(tmem + T_X3, sb + kK, sb + kS1, 1);
           umma_commit(bars + B_X3);
-          done |= X3A;
+        } else if (done & X2L) {
+          if (ready(DK, X2L, B_X2S)) {
+            mma_ts<true>(tmem + T_X2, tmem + T_DST, sb + kQ, 1);
+            umma_commit(bars + B_DK);
+          }
+          if (ready(DVA, X2L, B_X3S)) {
+            mma_ts<true, 64>(tmem + T_X3, tmem + T_PT, sb + kDo, 1);
+            umma_commit(bars + B_DV);
+          }
+          if (ready(X3B, X2L | DQ, B_DQ)) {  // dS has been read
+            mma_ss<false, false, 64>(tmem + T_X3B, sb + kK, sb + kS2 + kPanel / 2, 0);
+            mma_ss<false, false, 64>(tmem + T_X3B, sb + kK, sb + kS1 + kPanel / 2, 1);
+            umma_commit(bars + B_X3 + 1);
+          }
+          if (ready(DVB, X3B, B_X3S + 1)) {
+            mma_ts<true, 64>(tmem + T_X3B, tmem + T_PT, sb + kDo + kPanel, 1);
+            umma_commit(bars + B_DV + 1);
+          }
         }
-        if (ready(DK, X2, B_X2S)) {
-          mma_ts<true>(tmem + T_X2, tmem + T_DST, sb + kQ, 1);
-          umma_commit(bars + B_DK);
-        }
-        if (ready(DVA, X3A, B_X3S)) {
-          mma_ts<true, 64>(tmem + T_X3, tmem + T_PT, sb + kDo, 1);
-          umma_commit(bars + B_DV);
-        }
-        if (ready(X3B, X2 | DQ, B_DQ)) {  // dS has been read
-          mma_ss<false, false, 64>(tmem + T_X3B, sb + kK, sb + kS2 + kPanel / 2, 0);
-          mma_ss<false, false, 64>(tmem + T_X3B, sb + kK, sb + kS1 + kPanel / 2, 1);
-          umma_commit(bars + B_X3 + 1);
-        }
-        if (ready(DVB, X3B, B_X3S + 1)) {
-          mma_ts<true, 64>(tmem + T_X3B, tmem + T_PT, sb + kDo + kPanel, 1);
-          umma_commit(bars + B_DV + 1);
-        }
-        if (globaltimer_ns() - start > kWaitLimitNs) break;
+        if ((look & 255) == 0 && (*abort || globaltimer_ns() - start > kWaitLimitNs)) break;
       }
-      if (done != 511) break;
+      if (done != ALL) break;
       ++finished;
       }
       if (finished != (blocks > blockIdx.x ? (blocks - 1 - blockIdx.x) / step + 1 : 0)) *abort = 1;
@@ -441,12 +434,10 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
       }
       float hgsum = 0.f;
       if (wg == 2) {
-        // <H, G>, first (Hhi, Ghi + Glo); (Hlo, Ghi) follows when Hlo has come.
+        // <H, G>, first (Hhi + Hlo, Ghi); A adds (Hhi, Glo) when Glo has come.
         // (Hlo, Glo) is 2^-18 of the rest and left out.
-        if (!warp_wait(bars + B_HH, par, abort) || !warp_wait(bars + B_GH, par, abort) ||
-            !warp_wait(bars + B_GL, par, abort))
-          break;
-        hgsum = tile_dot(sm + kS0, sm + kS2, row) + tile_dot(sm + kS0, sm + kS1, row);
+        if (!warp_wait(bars + B_H, par, abort) || !warp_wait(bars + B_GH, par, abort)) break;
+        hgsum = tile_dot(sm + kS0, sm + kS2, row) + tile_dot(sm + kS1, sm + kS2, row);
         warp_arrive(bars + B_HG);
       }
       if (!warp_wait(bars + B_G, par, abort)) break;
@@ -515,10 +506,10 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
         tc_fence_after();
         dot = scale_acc(lanes + T_X1, into, own, sm + kK, sm + kQ, row, 0, 4);
         warp_arrive(bars + B_X1S);
-        // the rest of <H, G> meanwhile: (Hlo, Ghi)
-        if (!warp_wait(bars + B_HL, par, abort) || !warp_wait(bars + B_GH, par, abort)) break;
-        hgsum = tile_dot(sm + kS0, sm + kS2, row);
-        named_sync(1, 128);  // dQ goes over Hlo
+        // the rest of <H, G> meanwhile: (Hhi, Glo)
+        if (!warp_wait(bars + B_H, par, abort) || !warp_wait(bars + B_GL, par, abort)) break;
+        hgsum = tile_dot(sm + kS0, sm + kS1, row);
+        named_sync(1, 128);  // dQ goes over Hhi
         if (!warp_wait(bars + B_DQ, par, abort)) break;
         tc_fence_after();
         stage_acc(lanes + T_X1, sm + kS0, w.dq ? w.dq + (vrow + row) * a.dk : nullptr, a.dk, in,
@@ -696,7 +687,7 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
     if (*abort) {
       // let copies in flight land before the memory is given back
       set_status(a.status, CKDA_ERR_TIMEOUT);
-      const int land[] = {B_QK, B_VD, B_HH, B_HL, B_GH, B_GL};
+      const int land[] = {B_QK, B_VD, B_H, B_GH, B_GL};
       for (int i : land) mbar_wait(bars + i, 0, 1u << 12, 1000u);
     }
   }
