@@ -74,8 +74,9 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(LinearArgs a, int32_t*
 //   warps 12-15 C: thread = key row.    <H, G>; P^T; dV, in two halves of 64
 //               columns for want of TMEM
 // Shared memory holds three of the four state tiles: Glo comes last, where Hlo
-// was, once dO H^T is done.  Results are staged where their tile's readers
-// are done: dQ over H, dK over q, dV over v and Glo.
+// was, once dO H^T is done.  Results are staged over the state tiles (dQ over
+// Hhi, dK over Ghi, dV over Glo), so that the next chunk's q, k, v and do can be
+// loaded as soon as this chunk's products have read theirs.
 // An accumulator takes the state's part first; its thread scales that row in
 // place and the product inside the chunk is added to it.  A token's own product
 // (W_ii's factors, the largest under strong decay) stays out of the bf16 operands
@@ -86,13 +87,14 @@ constexpr int kThreads = 512;
 constexpr uint32_t kQ = 0, kK = kTile, kV = 2 * kTile, kDo = 3 * kTile;
 constexpr uint32_t kS0 = 4 * kTile, kS1 = 5 * kTile, kS2 = 6 * kTile;  // Hhi; Hlo, then Glo; Ghi
 constexpr uint32_t kGates = 7 * kTile;
-constexpr uint32_t kBars = kGates + sizeof(Gates);
-constexpr uint32_t kSmem = kBars + 512;
+constexpr uint32_t kEp = kGates + sizeof(Gates);  // exp2(pre_t)
+constexpr uint32_t kBars = kEp + C * sizeof(float);
+constexpr uint32_t kSmem = kBars + 480;
 static_assert(kSmem <= 232448, "shared memory of a CTA");
-enum { B_QK, B_VD, B_H, B_GH, B_GL, B_G, B_TAIL, B_A, B_B, B_DSA, B_DSB, B_DSC, B_X1, B_X2, B_X3,
+enum { B_QK, B_VD, B_H, B_GH, B_GL, B_G, B_TAIL, B_A, B_B, B_DSA, B_DSB, B_DSC, B_X1L, B_X1, B_X2, B_X3,
        B_X1S = B_X3 + 2, B_X2S, B_X3S, B_DQ = B_X3S + 2, B_DK, B_DV, B_HG = B_DV + 2,
-       // free again: the columns of X1, X2, X3; the tiles of H, q, v, Glo; the decays
-       B_XR, B_FH = B_XR + 3, B_FQ, B_FV, B_FG, B_PART, B_GFREE, B_END, B_COUNT };
+       // free again: the columns of X1, X2, X3; the state tiles; the decays
+       B_XR = B_HG + 2, B_F0 = B_XR + 3, B_F1, B_F2, B_PART, B_GFREE, B_END, B_COUNT };
 // TMEM columns: S, dP, S^T, dP^T; then dS over S and P^T behind it, X1 over dP,
 // X2 over S^T, dS^T over dP^T and the first half of X3 (64 columns) behind it,
 // the second over dS
@@ -232,6 +234,7 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
   extern __shared__ __align__(1024) char sm[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kBars);
   Gates* gates = reinterpret_cast<Gates*>(sm + kGates);
+  float* ep = reinterpret_cast<float*>(sm + kEp);
   volatile int* abort = reinterpret_cast<volatile int*>(sm + kBars + 400);
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(sm + kBars + 404);
   float* hg = reinterpret_cast<float*>(sm + kBars + 408);   // <H, G> by warp of A, C
@@ -249,7 +252,7 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
   if (tid == 0) {
     for (int i = 0; i < B_COUNT; ++i) {
       const bool by_warps = (i >= B_DSA && i <= B_DSC) || (i >= B_X1S && i < B_DQ) ||
-                            (i >= B_HG && i < B_FH) || i == B_GFREE;
+                            (i >= B_HG && i < B_F0) || i == B_GFREE;
       mbar_init(bars + i, i == B_TAIL ? 12 : i == B_PART ? 8 : by_warps ? 4 : 1);
     }
     *abort = 0;
@@ -275,28 +278,28 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
         bool ok = true;
         // a barrier of the chunk before, whose tile is wanted
         auto last = [&](int bar) { ok = ok && (!again || mbar_wait(bars + bar, par ^ 1)); };
-        last(B_DQ); last(B_X3 + 1); last(B_FQ);
+        last(B_DQ); last(B_X3 + 1); last(B_DK);
         if (!ok) { *abort = 1; break; }
         mbar_arrive_expect_tx(bars + B_QK, 2 * kTile);
         for (int p = 0; p < 2; ++p) {
           tma_load_3d(sb + kQ + p * kPanel, &mq, bars + B_QK, 64 * p, u.y, u.qz);
           tma_load_3d(sb + kK + p * kPanel, &mk, bars + B_QK, 64 * p, u.y, u.qz);
         }
-        last(B_FV); last(B_DV + 1);
+        last(B_X2); last(B_DV + 1);
         if (!ok) { *abort = 1; break; }
         mbar_arrive_expect_tx(bars + B_VD, 2 * kTile);
         for (int p = 0; p < 2; ++p) {
           tma_load_3d(sb + kV + p * kPanel, &mv, bars + B_VD, 64 * p, u.y, u.vz);
           tma_load_3d(sb + kDo + p * kPanel, &mo, bars + B_VD, 64 * p, u.y, u.vz);
         }
-        last(B_FH); last(B_FG);
+        last(B_F0); last(B_F1); last(B_F2);
         if (!ok) { *abort = 1; break; }
         mbar_arrive_expect_tx(bars + B_H, 2 * kTile);
         load_image(sb + kS0, himg, bars + B_H);
         load_image(sb + kS1, himg + kTile, bars + B_H);
         mbar_arrive_expect_tx(bars + B_GH, kTile);
         load_image(sb + kS2, gimg, bars + B_GH);
-        if (!mbar_wait(bars + B_X1, par) || !mbar_wait(bars + B_HG, par)) { *abort = 1; break; }
+        if (!mbar_wait(bars + B_X1L, par) || !mbar_wait(bars + B_HG, par)) { *abort = 1; break; }
         mbar_arrive_expect_tx(bars + B_GL, kTile);  // Hlo has been read
         load_image(sb + kS1, gimg + kTile, bars + B_GL);
         // What comes next, into L2 while this chunk is worked on: tiles come free
@@ -322,7 +325,7 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
       bool ok = mbar_wait(bars + B_QK, par);
       auto last = [&](int bar) { ok = ok && (!again || mbar_wait(bars + bar, par ^ 1)); };
       if (a.cu_seqlens && u.valid < C) ok = ok && mbar_wait(bars + B_TAIL, tails++ & 1);
-      last(B_DQ); last(B_DV + 1); last(B_XR + 2); last(B_XR + 1);
+      last(B_DV + 1); last(B_XR + 1); last(B_XR + 2);
       if (!ok) break;
       tc_fence_after();
       mma_ss<false, false>(tmem + T_S, sb + kQ, sb + kK, 0);
@@ -348,8 +351,9 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
       for (uint32_t look = 1; done != ALL; ++look) {
         if (!(done & X1)) {
           if (mbar_test(bars + B_H, par) && ready(X1, 0, B_DSA)) {
-            mma_ss<false, true>(tmem + T_X1, sb + kDo, sb + kS0, 0);
-            mma_ss<false, true>(tmem + T_X1, sb + kDo, sb + kS1, 1);
+            mma_ss<false, true>(tmem + T_X1, sb + kDo, sb + kS1, 0);
+            umma_commit(bars + B_X1L);  // Glo may come
+            mma_ss<false, true>(tmem + T_X1, sb + kDo, sb + kS0, 1);
             umma_commit(bars + B_X1);
           }
         } else if (ready(DQ, X1, B_X1S)) {
@@ -357,15 +361,21 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
           umma_commit(bars + B_DQ);
         }
         if (!(done & X2H)) {
-          if (mbar_test(bars + B_GH, par) && mbar_test(bars + B_DSC, par) && ready(X2H, 0, B_DSB))
+          if (mbar_test(bars + B_GH, par) && mbar_test(bars + B_DSC, par) && ready(X2H, 0, B_DSB)) {
             mma_ss<false, true>(tmem + T_X2, sb + kV, sb + kS2, 0);
+            mma_ss<false, false, 64>(tmem + T_X3, sb + kK, sb + kS2, 0);
+          }
         } else if (ready(X2L, X2H, B_GL)) {
           mma_ss<false, true>(tmem + T_X2, sb + kV, sb + kS1, 1);
           umma_commit(bars + B_X2);
-          mma_ss<false, false, 64>(tmem + T_X3, sb + kK, sb + kS2, 0);
           mma_ss<false, false, 64>(tmem + T_X3, sb + kK, sb + kS1, 1);
           umma_commit(bars + B_X3);
         } else if (done & X2L) {
+          if (ready(X3B, X2L | DQ, B_DQ)) {  // dS has been read
+            mma_ss<false, false, 64>(tmem + T_X3B, sb + kK, sb + kS2 + kPanel / 2, 0);
+            mma_ss<false, false, 64>(tmem + T_X3B, sb + kK, sb + kS1 + kPanel / 2, 1);
+            umma_commit(bars + B_X3 + 1);
+          }
           if (ready(DK, X2L, B_X2S)) {
             mma_ts<true>(tmem + T_X2, tmem + T_DST, sb + kQ, 1);
             umma_commit(bars + B_DK);
@@ -373,11 +383,6 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
           if (ready(DVA, X2L, B_X3S)) {
             mma_ts<true, 64>(tmem + T_X3, tmem + T_PT, sb + kDo, 1);
             umma_commit(bars + B_DV);
-          }
-          if (ready(X3B, X2L | DQ, B_DQ)) {  // dS has been read
-            mma_ss<false, false, 64>(tmem + T_X3B, sb + kK, sb + kS2 + kPanel / 2, 0);
-            mma_ss<false, false, 64>(tmem + T_X3B, sb + kK, sb + kS1 + kPanel / 2, 1);
-            umma_commit(bars + B_X3 + 1);
           }
           if (ready(DVB, X3B, B_X3S + 1)) {
             mma_ts<true, 64>(tmem + T_X3B, tmem + T_PT, sb + kDo + kPanel, 1);
@@ -400,6 +405,8 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
       const float4 x = load_decays(g, a.g_head ? 0 : 1, u.valid, lane);
       if (block != blockIdx.x && !warp_wait(bars + B_GFREE, par ^ 1, abort)) break;
       make_gates(gates, x, lane);
+      const float4 pre = reinterpret_cast<const float4*>(gates->pre)[lane];
+      reinterpret_cast<float4*>(ep)[lane] = make_float4(ex2(pre.x), ex2(pre.y), ex2(pre.z), ex2(pre.w));
       __syncwarp();
       if (lane == 0) mbar_arrive(bars + B_G);
     }
@@ -509,6 +516,7 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
         // the rest of <H, G> meanwhile: (Hhi, Glo)
         if (!warp_wait(bars + B_H, par, abort) || !warp_wait(bars + B_GL, par, abort)) break;
         hgsum = tile_dot(sm + kS0, sm + kS1, row);
+        warp_arrive(bars + B_HG + 1);
         named_sync(1, 128);  // dQ goes over Hhi
         if (!warp_wait(bars + B_DQ, par, abort)) break;
         tc_fence_after();
@@ -576,13 +584,13 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
           }
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float4 g = reinterpret_cast<const float4*>(gates->pre + 32 * p)[e];
+            const float4 g = reinterpret_cast<const float4*>(ep + 32 * p)[e];
             const float gg[4] = {g.x, g.y, g.z, g.w};
             float v[4];
 #pragma unroll
             for (int z = 0; z < 4; ++z) {
               const int i = 4 * e + z;
-              v[z] = __uint_as_float(d[i]) * (f * ex2(gg[z]));
+              v[z] = __uint_as_float(d[i]) * (f * gg[z]);
               wsum = fmaf(v[z], __uint_as_float(x[i]), wsum);
             }
             o[2 * e] = pack_bf162(v[0], v[1]);
@@ -599,41 +607,36 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
           warp_arrive(bars + B_X2S);
           if (!warp_wait(bars + B_DK, par, abort)) break;
           tc_fence_after();
-          // over q, which A has to have read too
-          if (!warp_wait(bars + B_X1S, par, abort)) break;
-          stage_acc(lanes + T_X2, sm + kQ, w.dk ? w.dk + (vrow + row) * a.dk : nullptr, a.dk, in,
+          // over Ghi: the products' last reader is X3, C's dot product came before
+          if (!warp_wait(bars + B_X3 + 1, par, abort) || !warp_wait(bars + B_HG, par, abort)) break;
+          stage_acc(lanes + T_X2, sm + kS2, w.dk ? w.dk + (vrow + row) * a.dk : nullptr, a.dk, in,
                     row, 0, 4);
           warp_arrive(bars + B_XR + 1);
-          if (!w.dk) put(&mdk, a.dkey, krow, a.dk, kQ, u.qz, 0, 2);
+          if (!w.dk) put(&mdk, a.dkey, krow, a.dk, kS2, u.qz, 0, 2);
         } else {
           bool ok = true;
 #pragma unroll 1
           for (int half = 0; half < 2; ++half) {
-            const uint32_t acc = lanes + (half ? T_X3B : T_X3), to = half ? kS1 : kV;
+            const uint32_t acc = lanes + (half ? T_X3B : T_X3);
             if (!(ok = warp_wait(bars + B_X3 + half, par, abort))) break;
             tc_fence_after();
             scale_acc(acc, out, own, sm + kDo, sm + kDo, row, 2 * half, 2 * half + 2);
             warp_arrive(bars + B_X3S + half);
             if (!(ok = warp_wait(bars + B_DV + half, par, abort))) break;
             tc_fence_after();
-            // the first panel over v, once X2 has read it; the second over Glo, once
-            // X3 has
-            if (half == 0) {
-              if (!(ok = warp_wait(bars + B_X2, par, abort))) break;
-            } else if (lead) {
-              store_read_wait();
-              mbar_arrive(bars + B_FV);
-            }
-            stage_acc(acc, sm + to, nullptr, a.dv, in, row, 2 * half, 2 * half + 2);
+            // over Glo, which X3 and A have read
+            if (!(ok = warp_wait(bars + B_X3 + 1, par, abort))) break;
+            if (!(ok = warp_wait(bars + B_HG + 1, par, abort))) break;
+            stage_acc(acc, sm + kS1, nullptr, a.dv, in, row, 2 * half, 2 * half + 2);
             if (half) warp_arrive(bars + B_XR + 2);
-            put(&mdv, a.dval, vrow, a.dv, to, u.vz, half, half + 1);
+            put(&mdv, a.dval, vrow, a.dv, kS1, u.vz, half, half + 1);
           }
           if (!ok) break;
         }
       }
       if (lead) {
         store_read_wait();
-        mbar_arrive(bars + (wg == 0 ? B_FH : wg == 1 ? B_FQ : B_FG));
+        mbar_arrive(bars + (wg == 0 ? B_F0 : wg == 1 ? B_F2 : B_F1));
       }
       // dg_t = e^{L_C} <H, G> + sum_{j<t} kd_j + sum_{i>=t} (qd_i + row_i - col_i):
       // B hands its sums by token to A, over decays that all three have read
