@@ -69,10 +69,10 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(LinearArgs a, int32_t*
 // in two parts each, dS K, dS^T Q, P^T dO.
 //   warp 0 loads; warp 1 issues the products, each as soon as its operands are
 //   there; warp 2 makes the decays
-//   warps 4-7   A: thread = query row.  dS and the row sums of W; dQ
+//   warps 4-7   A: thread = query row.  dS and the row sums of W; dQ; then the
+//               second half of dV's columns, whose accumulator follows dQ's
 //   warps 8-11  B: thread = key row.    dS^T and the column sums of W; dK
-//   warps 12-15 C: thread = key row.    <H, G>; P^T; dV, in two halves of 64
-//               columns for want of TMEM
+//   warps 12-15 C: thread = key row.    <H, G>; P^T; the first half of dV's columns
 // Shared memory holds three of the four state tiles: Glo comes last, where Hlo
 // was, once dO H^T is done.  Results are staged over the state tiles (dQ over
 // Hhi, dK over Ghi, dV over Glo), so that the next chunk's q, k, v and do can be
@@ -92,14 +92,13 @@ constexpr uint32_t kBars = kEp + C * sizeof(float);
 constexpr uint32_t kSmem = kBars + 480;
 static_assert(kSmem <= 232448, "shared memory of a CTA");
 enum { B_QK, B_VD, B_H, B_GH, B_GL, B_G, B_TAIL, B_A, B_B, B_DSA, B_DSB, B_DSC, B_X1L, B_X1, B_X2, B_X3,
-       B_X1S = B_X3 + 2, B_X2S, B_X3S, B_DQ = B_X3S + 2, B_DK, B_DV, B_HG = B_DV + 2,
+       B_X1S, B_X2S, B_X3S, B_DQ, B_DK, B_DV, B_HG,
        // free again: the columns of X1, X2, X3; the state tiles; the decays
        B_XR = B_HG + 2, B_F0 = B_XR + 3, B_F1, B_F2, B_PART, B_GFREE, B_END, B_COUNT };
-// TMEM columns: S, dP, S^T, dP^T; then dS over S and P^T behind it, X1 over dP,
-// X2 over S^T, dS^T over dP^T and the first half of X3 (64 columns) behind it,
-// the second over dS
+// TMEM columns: S, dP, S^T, dP^T; then dS over S and P^T behind it, X1 and after
+// it X3 over dP, X2 over S^T, dS^T over dP^T
 constexpr uint32_t T_S = 0, T_DP = 128, T_ST = 256, T_DPT = 384;
-constexpr uint32_t T_DS = 0, T_PT = 64, T_X1 = 128, T_X2 = 256, T_DST = 384, T_X3 = 448, T_X3B = 0;
+constexpr uint32_t T_DS = 0, T_PT = 64, T_X1 = 128, T_X3 = 128, T_X2 = 256, T_DST = 384;
 }  // namespace gr
 
 // Chunk and head of a block.
@@ -253,7 +252,11 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
     for (int i = 0; i < B_COUNT; ++i) {
       const bool by_warps = (i >= B_DSA && i <= B_DSC) || (i >= B_X1S && i < B_DQ) ||
                             (i >= B_HG && i < B_F0) || i == B_GFREE;
-      mbar_init(bars + i, i == B_TAIL ? 12 : i == B_PART ? 8 : by_warps ? 4 : 1);
+      mbar_init(bars + i, i == B_TAIL                                           ? 12
+                          : i == B_PART || i == B_X3S || i == B_XR + 2 ? 8
+                          : by_warps                                            ? 4
+                          : i == B_F1                                           ? 2
+                                                                                : 1);
     }
     *abort = 0;
     fence_mbar_init();
@@ -278,14 +281,14 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
         bool ok = true;
         // a barrier of the chunk before, whose tile is wanted
         auto last = [&](int bar) { ok = ok && (!again || mbar_wait(bars + bar, par ^ 1)); };
-        last(B_DQ); last(B_X3 + 1); last(B_DK);
+        last(B_DQ); last(B_X3); last(B_DK);
         if (!ok) { *abort = 1; break; }
         mbar_arrive_expect_tx(bars + B_QK, 2 * kTile);
         for (int p = 0; p < 2; ++p) {
           tma_load_3d(sb + kQ + p * kPanel, &mq, bars + B_QK, 64 * p, u.y, u.qz);
           tma_load_3d(sb + kK + p * kPanel, &mk, bars + B_QK, 64 * p, u.y, u.qz);
         }
-        last(B_X2); last(B_DV + 1);
+        last(B_X2); last(B_DV);
         if (!ok) { *abort = 1; break; }
         mbar_arrive_expect_tx(bars + B_VD, 2 * kTile);
         for (int p = 0; p < 2; ++p) {
@@ -325,7 +328,7 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
       bool ok = mbar_wait(bars + B_QK, par);
       auto last = [&](int bar) { ok = ok && (!again || mbar_wait(bars + bar, par ^ 1)); };
       if (a.cu_seqlens && u.valid < C) ok = ok && mbar_wait(bars + B_TAIL, tails++ & 1);
-      last(B_DV + 1); last(B_XR + 1); last(B_XR + 2);
+      last(B_DV); last(B_XR + 1); last(B_XR + 2);
       if (!ok) break;
       tc_fence_after();
       mma_ss<false, false>(tmem + T_S, sb + kQ, sb + kK, 0);
@@ -339,7 +342,7 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
       mma_ss<false, false>(tmem + T_DPT, sb + kV, sb + kDo, 0);
       umma_commit(bars + B_B);
       // what is left, by readiness; `done` keeps the order that TMEM asks for
-      enum { X1 = 1, X2H = 2, X2L = 4, X3B = 8, DQ = 16, DK = 32, DVA = 64, DVB = 128, ALL = 255 };
+      enum { X1 = 1, X2H = 2, X2L = 4, X3 = 8, DQ = 16, DK = 32, DV = 64, ALL = 127 };
       uint32_t done = 0;
       const uint64_t start = globaltimer_ns();
       auto ready = [&](uint32_t what, uint32_t after, int bar) {
@@ -363,30 +366,23 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
         if (!(done & X2H)) {
           if (mbar_test(bars + B_GH, par) && mbar_test(bars + B_DSC, par) && ready(X2H, 0, B_DSB)) {
             mma_ss<false, true>(tmem + T_X2, sb + kV, sb + kS2, 0);
-            mma_ss<false, false, 64>(tmem + T_X3, sb + kK, sb + kS2, 0);
           }
         } else if (ready(X2L, X2H, B_GL)) {
           mma_ss<false, true>(tmem + T_X2, sb + kV, sb + kS1, 1);
           umma_commit(bars + B_X2);
-          mma_ss<false, false, 64>(tmem + T_X3, sb + kK, sb + kS1, 1);
-          umma_commit(bars + B_X3);
         } else if (done & X2L) {
-          if (ready(X3B, X2L | DQ, B_DQ)) {  // dS has been read
-            mma_ss<false, false, 64>(tmem + T_X3B, sb + kK, sb + kS2 + kPanel / 2, 0);
-            mma_ss<false, false, 64>(tmem + T_X3B, sb + kK, sb + kS1 + kPanel / 2, 1);
-            umma_commit(bars + B_X3 + 1);
-          }
           if (ready(DK, X2L, B_X2S)) {
             mma_ts<true>(tmem + T_X2, tmem + T_DST, sb + kQ, 1);
             umma_commit(bars + B_DK);
           }
-          if (ready(DVA, X2L, B_X3S)) {
-            mma_ts<true, 64>(tmem + T_X3, tmem + T_PT, sb + kDo, 1);
-            umma_commit(bars + B_DV);
+          if (ready(X3, DQ, B_XR)) {  // dQ has left its columns
+            mma_ss<false, false>(tmem + T_X3, sb + kK, sb + kS2, 0);
+            mma_ss<false, false>(tmem + T_X3, sb + kK, sb + kS1, 1);
+            umma_commit(bars + B_X3);
           }
-          if (ready(DVB, X3B, B_X3S + 1)) {
-            mma_ts<true, 64>(tmem + T_X3B, tmem + T_PT, sb + kDo + kPanel, 1);
-            umma_commit(bars + B_DV + 1);
+          if (ready(DV, X3, B_X3S)) {
+            mma_ts<true>(tmem + T_X3, tmem + T_PT, sb + kDo, 1);
+            umma_commit(bars + B_DV);
           }
         }
         if ((look & 255) == 0 && (*abort || globaltimer_ns() - start > kWaitLimitNs)) break;
@@ -450,7 +446,8 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
       if (!warp_wait(bars + B_G, par, abort)) break;
       const float pre = gates->pre[row], es = gates->es[row];
       const float into = a.scale * gates->eL[row], out = gates->w[row], s = a.scale;
-      float wsum = 0.f, dot = 0.f, own = 0.f;  // own: s do_i.v_i (A, B), s q_i.k_i (C)
+      // own, own_p: s do_i.v_i (A, B) and s q_i.k_i (A; C has it in own)
+      float wsum = 0.f, dot = 0.f, own = 0.f, own_p = 0.f;
       if (wg == 0) {
         // row i: j over blocks up to its own
         if (!warp_wait(bars + B_A, par, abort)) break;
@@ -496,7 +493,10 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
               const float dp = s * __uint_as_float(d[j]);
               v[z] = j < lane ? dp * ex2(pre - gg[z]) : 0.f;
               if (j < lane) wsum = fmaf(v[z], __uint_as_float(x[j]), wsum);
-              if (j == lane) own = dp;
+              if (j == lane) {
+                own = dp;
+                own_p = s * __uint_as_float(x[j]);
+              }
             }
             o[2 * e] = pack_bf162(v[0], v[1]);
             o[2 * e + 1] = pack_bf162(v[2], v[3]);
@@ -608,35 +608,36 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
           if (!warp_wait(bars + B_DK, par, abort)) break;
           tc_fence_after();
           // over Ghi: the products' last reader is X3, C's dot product came before
-          if (!warp_wait(bars + B_X3 + 1, par, abort) || !warp_wait(bars + B_HG, par, abort)) break;
+          if (!warp_wait(bars + B_X3, par, abort) || !warp_wait(bars + B_HG, par, abort)) break;
           stage_acc(lanes + T_X2, sm + kS2, w.dk ? w.dk + (vrow + row) * a.dk : nullptr, a.dk, in,
                     row, 0, 4);
           warp_arrive(bars + B_XR + 1);
           if (!w.dk) put(&mdk, a.dkey, krow, a.dk, kS2, u.qz, 0, 2);
         } else {
-          bool ok = true;
-#pragma unroll 1
-          for (int half = 0; half < 2; ++half) {
-            const uint32_t acc = lanes + (half ? T_X3B : T_X3);
-            if (!(ok = warp_wait(bars + B_X3 + half, par, abort))) break;
-            tc_fence_after();
-            scale_acc(acc, out, own, sm + kDo, sm + kDo, row, 2 * half, 2 * half + 2);
-            warp_arrive(bars + B_X3S + half);
-            if (!(ok = warp_wait(bars + B_DV + half, par, abort))) break;
-            tc_fence_after();
-            // over Glo, which X3 and A have read
-            if (!(ok = warp_wait(bars + B_X3 + 1, par, abort))) break;
-            if (!(ok = warp_wait(bars + B_HG + 1, par, abort))) break;
-            stage_acc(acc, sm + kS1, nullptr, a.dv, in, row, 2 * half, 2 * half + 2);
-            if (half) warp_arrive(bars + B_XR + 2);
-            put(&mdv, a.dval, vrow, a.dv, kS1, u.vz, half, half + 1);
-          }
-          if (!ok) break;
+          own_p = own;
         }
+      }
+      if (wg != 1) {
+        // dV: C the first panel, A the second
+        const int half = wg == 0 ? 1 : 0;
+        if (!warp_wait(bars + B_X3, par, abort)) break;
+        tc_fence_after();
+        scale_acc(lanes + T_X3 + 64 * half, out, own_p, sm + kDo, sm + kDo, row, 2 * half,
+                  2 * half + 2);
+        warp_arrive(bars + B_X3S);
+        if (!warp_wait(bars + B_DV, par, abort)) break;
+        tc_fence_after();
+        // over Glo, which X3 and A have read
+        if (!warp_wait(bars + B_HG + 1, par, abort)) break;
+        stage_acc(lanes + T_X3 + 64 * half, sm + kS1, nullptr, a.dv, in, row, 2 * half,
+                  2 * half + 2);
+        warp_arrive(bars + B_XR + 2);
+        put(&mdv, a.dval, vrow, a.dv, kS1, u.vz, half, half + 1);
       }
       if (lead) {
         store_read_wait();
-        mbar_arrive(bars + (wg == 0 ? B_F0 : wg == 1 ? B_F2 : B_F1));
+        if (wg == 0) mbar_arrive(bars + B_F0);
+        mbar_arrive(bars + (wg == 1 ? B_F2 : B_F1));
       }
       // dg_t = e^{L_C} <H, G> + sum_{j<t} kd_j + sum_{i>=t} (qd_i + row_i - col_i):
       // B hands its sums by token to A, over decays that all three have read
