@@ -73,11 +73,6 @@ cudaError_t linear_chunk_fwd(const LinearArgs& a, char* ws, cudaStream_t s);
 size_t linear_chunk_bwd_bytes(int N, int B, int H, int Hk, int T, int dk, int dv, bool packed);
 cudaError_t linear_chunk_bwd(const LinearArgs& a, char* ws, cudaStream_t s);
 
-// dq and dk of the key heads: the sum over the H / Hk heads that share one, of
-// fp32 [B, H, T, dk] partial gradients.  own (or null): fp32 [B, H, T], scale
-// v_t.do_t, where the partial gradients lack own_t k_t and own_t q_t.
-cudaError_t linear_sum_heads(const LinearArgs& a, const float* dq_part, const float* dk_part,
-                             const float* own, cudaStream_t s);
 // dg of a decay per head: the sum of fp32 [B, H, T] over B and T.
 cudaError_t linear_sum_decay(const LinearArgs& a, const float* dg_full, cudaStream_t s);
 

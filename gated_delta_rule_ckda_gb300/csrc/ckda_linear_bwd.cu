@@ -30,8 +30,8 @@ struct BwdWs {
   char* himg;           // [slots * H] images of H
   char* gimg;           // of G
   float* dg;            // [B, H, T] (a decay per head only)
-  float* dq;            // [B, H, T, dk] (shared key heads only)
-  float* dk;
+  __nv_bfloat16* dq;    // [B, H, T, dk]: each head's part of dq and dk (shared key
+  __nv_bfloat16* dk;    // heads only)
   int32_t* first;       // [N + 1] first chunk of each sequence (packed only)
   int chunks;           // slots of a head: chunks, or a bound on them
 };
@@ -100,6 +100,35 @@ enum { B_QK, B_VD, B_H, B_GH, B_GL, B_G, B_TAIL, B_A, B_B, B_DSA, B_DSB, B_DSC, 
 constexpr uint32_t T_S = 0, T_DP = 128, T_ST = 256, T_DPT = 384;
 constexpr uint32_t T_DS = 0, T_PT = 64, T_X1 = 128, T_X3 = 128, T_X2 = 256, T_DST = 384;
 }  // namespace gr
+
+// dq and dk of shared key heads from their heads' parts.  The parts are bf16: each
+// is rounded once, as dq and dk would be of a head of its own, and added in fp32;
+// fp32 parts would double the bytes of a pass that is bound by them.
+__global__ void __launch_bounds__(256) sum_parts_kernel(LinearArgs a, BwdWs w) {
+  const int group = a.H / a.Hk;
+  const size_t per = (size_t)a.T * a.dk / 8, total = (size_t)a.B * a.Hk * per;  // vectors of 8
+  for (size_t e = (size_t)blockIdx.x * 256 + threadIdx.x; e < total; e += (size_t)gridDim.x * 256) {
+    const size_t first = e / per * group * per + e % per;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      const uint4* part = reinterpret_cast<const uint4*>(which ? w.dk : w.dq);
+      float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+      for (int i = 0; i < group; ++i) {
+        const uint4 v = part[first + i * per];
+        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          s[2 * k] += __uint_as_float(x[k] << 16);
+          s[2 * k + 1] += __uint_as_float(x[k] & 0xffff0000u);
+        }
+      }
+      reinterpret_cast<uint4*>(which ? a.dkey : a.dq)[e] =
+          make_uint4(pack_bf162(s[0], s[1]), pack_bf162(s[2], s[3]), pack_bf162(s[4], s[5]),
+                     pack_bf162(s[6], s[7]));
+    }
+  }
+}
 
 // Chunk and head of a block.
 struct Chunk {
@@ -191,33 +220,21 @@ static __device__ __noinline__ float scale_acc(uint32_t acc, float f, float m, c
   return dot;
 }
 
-// The same columns as bf16 into a tile, or (part) as fp32 partial gradients to
-// memory.
-static __device__ __noinline__ void stage_acc(uint32_t acc, char* tile, float* part, int width,
-                                              bool keep, int row, int p0, int p1) {
+// The same columns as bf16 into a tile.
+static __device__ __noinline__ void stage_acc(uint32_t acc, char* tile, int row, int p0, int p1) {
 #pragma unroll 1
   for (int p = p0; p < p1; ++p) {
     uint32_t x[32];
     tmem_ld32<32>(acc + 32 * (p - p0), x);
     tmem_ld_wait();
-    if (part) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (keep && 32 * p + 4 * j < width)
-          *reinterpret_cast<uint4*>(part + 32 * p + 4 * j) =
-              make_uint4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
-      __syncwarp();
-    } else {
+    for (int j = 0; j < 4; ++j) {
+      uint32_t o[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t o[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          o[e] = pack_bf162(__uint_as_float(x[8 * j + 2 * e]),
-                            __uint_as_float(x[8 * j + 2 * e + 1]));
-        *reinterpret_cast<uint4*>(tile + sw128_chunk(128, row, 4 * p + j)) =
-            make_uint4(o[0], o[1], o[2], o[3]);
-      }
+      for (int e = 0; e < 4; ++e)
+        o[e] = pack_bf162(__uint_as_float(x[8 * j + 2 * e]), __uint_as_float(x[8 * j + 2 * e + 1]));
+      *reinterpret_cast<uint4*>(tile + sw128_chunk(128, row, 4 * p + j)) =
+          make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
 }
@@ -332,13 +349,16 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
       if (!ok) break;
       tc_fence_after();
       mma_ss<false, false>(tmem + T_S, sb + kQ, sb + kK, 0);
-      mma_ss<false, false>(tmem + T_ST, sb + kK, sb + kQ, 0);
+      // A waits for dP: S^T meanwhile only where v and do are still on their way
+      const bool soon = mbar_test(bars + B_VD, par);
+      if (!soon) mma_ss<false, false>(tmem + T_ST, sb + kK, sb + kQ, 0);
       last(B_XR); last(B_DK);
       ok = ok && mbar_wait(bars + B_VD, par);
       if (!ok) break;
       tc_fence_after();
       mma_ss<false, false>(tmem + T_DP, sb + kDo, sb + kV, 0);
       umma_commit(bars + B_A);
+      if (soon) mma_ss<false, false>(tmem + T_ST, sb + kK, sb + kQ, 0);
       mma_ss<false, false>(tmem + T_DPT, sb + kV, sb + kDo, 0);
       umma_commit(bars + B_B);
       // what is left, by readiness; `done` keeps the order that TMEM asks for
@@ -520,10 +540,9 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
         named_sync(1, 128);  // dQ goes over Hhi
         if (!warp_wait(bars + B_DQ, par, abort)) break;
         tc_fence_after();
-        stage_acc(lanes + T_X1, sm + kS0, w.dq ? w.dq + (vrow + row) * a.dk : nullptr, a.dk, in,
-                  row, 0, 4);
+        stage_acc(lanes + T_X1, sm + kS0, row, 0, 4);
         warp_arrive(bars + B_XR);
-        if (!w.dq) put(&mdq, a.dq, krow, a.dk, kS0, u.qz, 0, 2);
+        put(&mdq, w.dq ? w.dq : a.dq, w.dq ? vrow : krow, a.dk, kS0, w.dq ? u.vz : u.qz, 0, 2);
       } else {
         // row j: i over blocks from its own on.  B forms dS^T (over dP^T) and the
         // sums of W, C forms P^T (behind dS, so after A).
@@ -609,10 +628,9 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
           tc_fence_after();
           // over Ghi: the products' last reader is X3, C's dot product came before
           if (!warp_wait(bars + B_X3, par, abort) || !warp_wait(bars + B_HG, par, abort)) break;
-          stage_acc(lanes + T_X2, sm + kS2, w.dk ? w.dk + (vrow + row) * a.dk : nullptr, a.dk, in,
-                    row, 0, 4);
+          stage_acc(lanes + T_X2, sm + kS2, row, 0, 4);
           warp_arrive(bars + B_XR + 1);
-          if (!w.dk) put(&mdk, a.dkey, krow, a.dk, kS2, u.qz, 0, 2);
+          put(&mdk, w.dk ? w.dk : a.dkey, w.dk ? vrow : krow, a.dk, kS2, w.dk ? u.vz : u.qz, 0, 2);
         } else {
           own_p = own;
         }
@@ -629,8 +647,7 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
         tc_fence_after();
         // over Glo, which X3 and A have read
         if (!warp_wait(bars + B_HG + 1, par, abort)) break;
-        stage_acc(lanes + T_X3 + 64 * half, sm + kS1, nullptr, a.dv, in, row, 2 * half,
-                  2 * half + 2);
+        stage_acc(lanes + T_X3 + 64 * half, sm + kS1, row, 2 * half, 2 * half + 2);
         warp_arrive(bars + B_XR + 2);
         put(&mdv, a.dval, vrow, a.dv, kS1, u.vz, half, half + 1);
       }
@@ -713,8 +730,8 @@ ChunkPlan chunk_plan(int N, int B, int H, int Hk, int T, int dk, int dv, bool pa
   p.himg = at; at += p.chunks * H * kImage;
   p.gimg = at; at += p.chunks * H * kImage;
   p.dg = at; at += up256(rows * 4);
-  p.dq = at; at += Hk == H ? 0 : up256(rows * dk * 4);
-  p.dk = at; at += Hk == H ? 0 : up256(rows * dk * 4);
+  p.dq = at; at += Hk == H ? 0 : up256(rows * dk * 2);
+  p.dk = at; at += Hk == H ? 0 : up256(rows * dk * 2);
   p.first = at; at += up256(((size_t)N + 1) * 4);
   p.split = at; at += linear_split_bytes(linear_split(N, B, H, T, packed), N, H, dk, dv, packed, 2);
   p.total = at;
@@ -734,17 +751,18 @@ cudaError_t linear_chunk_bwd(const LinearArgs& a, char* ws, cudaStream_t s) {
   w.himg = ws + p.himg;
   w.gimg = ws + p.gimg;
   w.dg = a.g_head ? reinterpret_cast<float*>(ws + p.dg) : nullptr;
-  w.dq = a.Hk == a.H ? nullptr : reinterpret_cast<float*>(ws + p.dq);
-  w.dk = a.Hk == a.H ? nullptr : reinterpret_cast<float*>(ws + p.dk);
+  w.dq = a.Hk == a.H ? nullptr : reinterpret_cast<__nv_bfloat16*>(ws + p.dq);
+  w.dk = a.Hk == a.H ? nullptr : reinterpret_cast<__nv_bfloat16*>(ws + p.dk);
   w.chunks = (int)p.chunks;
   cudaError_t e = cudaSuccess;
   CUtensorMap mq{}, mk{}, mv{}, mo{}, mdq{}, mdk{}, mdv{};
+  const uint64_t heads = (uint64_t)a.B * (w.dq ? a.H : a.Hk);
   if (a.T > 0 && (!linear_map(&mq, a.q, (uint64_t)a.B * a.Hk, a.T, a.dk) ||
                   !linear_map(&mk, a.k, (uint64_t)a.B * a.Hk, a.T, a.dk) ||
                   !linear_map(&mv, a.v, (uint64_t)a.B * a.H, a.T, a.dv) ||
                   !linear_map(&mo, a.dout, (uint64_t)a.B * a.H, a.T, a.dv) ||
-                  !linear_map(&mdq, a.dq, (uint64_t)a.B * a.Hk, a.T, a.dk) ||
-                  !linear_map(&mdk, a.dkey, (uint64_t)a.B * a.Hk, a.T, a.dk) ||
+                  !linear_map(&mdq, w.dq ? w.dq : a.dq, heads, a.T, a.dk) ||
+                  !linear_map(&mdk, w.dk ? w.dk : a.dkey, heads, a.T, a.dk) ||
                   !linear_map(&mdv, a.dval, (uint64_t)a.B * a.H, a.T, a.dv)))
     return cudaErrorInvalidValue;
   if (a.cu_seqlens) {
@@ -767,7 +785,11 @@ cudaError_t linear_chunk_bwd(const LinearArgs& a, char* ws, cudaStream_t s) {
     linear_grad_kernel<<<(unsigned)(blocks < kLinSms ? blocks : kLinSms), gr::kThreads, gr::kSmem,
                          s>>>(a, w, mq, mk, mv, mo, mdq, mdk, mdv);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if (w.dq && (e = linear_sum_heads(a, w.dq, w.dk, nullptr, s)) != cudaSuccess) return e;
+    if (w.dq) {
+      const size_t n = (size_t)a.B * a.Hk * a.T * a.dk / 8, blocks = (n + 255) / 256;
+      sum_parts_kernel<<<(unsigned)(blocks < 16 * kLinSms ? blocks : 16 * kLinSms), 256, 0, s>>>(a, w);
+      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
   }
   return a.g_head ? linear_sum_decay(a, w.dg, s) : e;
 }

@@ -500,7 +500,7 @@ __global__ void __launch_bounds__(256) piece_dg_kernel(LinearArgs a, SerialWs w,
   }
 }
 
-// One thread per element of dq and dk; `own` (may be null) as in SerialWs.
+// One thread per element of dq and dk; `own` as in SerialWs.
 template <typename IO>
 __global__ void sum_heads_kernel(LinearArgs a, const float* dq, const float* dk,
                                  const float* own) {
@@ -515,12 +515,10 @@ __global__ void sum_heads_kernel(LinearArgs a, const float* dq, const float* dk,
     for (int i = 0; i < group; ++i) {
       x += dq[first + i * per];
       y += dk[first + i * per];
-      if (own) o += own[(head * group + i) * a.T + (e % per) / a.dk];
+      o += own[(head * group + i) * a.T + (e % per) / a.dk];
     }
-    if (own) {
-      x = fmaf(o, ld_io(static_cast<const IO*>(a.k) + e), x);
-      y = fmaf(o, ld_io(static_cast<const IO*>(a.q) + e), y);
-    }
+    x = fmaf(o, ld_io(static_cast<const IO*>(a.k) + e), x);
+    y = fmaf(o, ld_io(static_cast<const IO*>(a.q) + e), y);
     st_io(static_cast<IO*>(a.dq) + e, x);
     st_io(static_cast<IO*>(a.dkey) + e, y);
   }
@@ -696,6 +694,14 @@ cudaError_t launch_dv(const LinearArgs& a, const SerialWs& w, cudaStream_t s) {
 }
 
 template <typename IO>
+cudaError_t sum_heads(const LinearArgs& a, const SerialWs& w, cudaStream_t s) {
+  const size_t total = (size_t)a.B * a.Hk * a.T * a.dk, blocks = (total + 255) / 256;
+  const unsigned grid = (unsigned)(blocks < 32 * kLinSms ? blocks : 32 * kLinSms);
+  sum_heads_kernel<IO><<<grid, 256, 0, s>>>(a, w.dq, w.dk, w.own);
+  return cudaGetLastError();
+}
+
+template <typename IO>
 cudaError_t serial_bwd_io(const LinearArgs& a, char* ws, cudaStream_t s) {
   const SerialPlan p = serial_plan(a.N, a.B, a.H, a.T, a.dk, a.dv, a.cu_seqlens != nullptr);
   SerialWs w{};
@@ -722,7 +728,7 @@ cudaError_t serial_bwd_io(const LinearArgs& a, char* ws, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     piece_dg_kernel<IO><<<(unsigned)(p.slots * a.H), 256, 0, s>>>(a, w, a.g_head ? w.dg : a.dg);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if ((e = linear_sum_heads(a, w.dq, w.dk, w.own, s)) != cudaSuccess) return e;
+    if ((e = sum_heads<IO>(a, w, s)) != cudaSuccess) return e;
   }
   return a.g_head ? linear_sum_decay(a, w.dg, s) : e;
 }
@@ -744,19 +750,6 @@ size_t linear_serial_bwd_bytes(int N, int B, int H, int T, int dk, int dv, bool 
 cudaError_t linear_serial_bwd(const LinearArgs& a, char* ws, cudaStream_t s) {
   return a.io == CKDA_F32 ? serial_bwd_io<float>(a, ws, s)
                           : serial_bwd_io<__nv_bfloat16>(a, ws, s);
-}
-
-cudaError_t linear_sum_heads(const LinearArgs& a, const float* dq_part, const float* dk_part,
-                             const float* own, cudaStream_t s) {
-  const size_t total = (size_t)a.B * a.Hk * a.T * a.dk;
-  if (total == 0) return cudaSuccess;
-  const size_t blocks = (total + 255) / 256;
-  const unsigned grid = (unsigned)(blocks < 32 * kLinSms ? blocks : 32 * kLinSms);
-  if (a.io == CKDA_F32)
-    sum_heads_kernel<float><<<grid, 256, 0, s>>>(a, dq_part, dk_part, own);
-  else
-    sum_heads_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a, dq_part, dk_part, own);
-  return cudaGetLastError();
 }
 
 cudaError_t linear_sum_decay(const LinearArgs& a, const float* dg_full, cudaStream_t s) {
