@@ -70,11 +70,11 @@ ckda_status ckda_linear_fwd(const void* q, const void* k, const void* v, const f
   a.N = N; a.B = B; a.H = H; a.Hk = Hk; a.T = T; a.dk = dk; a.dv = dv;
   a.g_head = g_per_head ? 1 : 0;
   a.scale = scale; a.io = io_dtype;
-  if (cudaMemsetAsync(workspace, 0, sizeof(int), s) != cudaSuccess) return CKDA_ERR_CUDA;
   char* scratch = static_cast<char*>(workspace) + head_bytes(cu_seqlens ? num_seqs : 0);
   cudaError_t e = cudaSuccess;
   if (linear_chunk_path(io_dtype, dk, dv) && aligned16(q) && aligned16(k) && aligned16(v) &&
       aligned16(o)) {
+    a.clear = 1;
     if (cu_seqlens) {
       int32_t* order = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + kWsStatusBytes);
       e = launch_seq_order(cu_seqlens, num_seqs, order, s);
@@ -82,7 +82,8 @@ ckda_status ckda_linear_fwd(const void* q, const void* k, const void* v, const f
     }
     if (e == cudaSuccess) e = linear_chunk_fwd(a, scratch, s);
   } else {
-    e = linear_serial_fwd(a, scratch, s);
+    e = cudaMemsetAsync(workspace, 0, sizeof(int), s);
+    if (e == cudaSuccess) e = linear_serial_fwd(a, scratch, s);
   }
   return e == cudaSuccess ? CKDA_OK : CKDA_ERR_CUDA;
 }

@@ -2,6 +2,7 @@
 // attention with a scalar decay per head:
 //     H_t = exp(g_t) H_{t-1} + k_t v_t^T,    o_t = H_t^T (scale q_t)
 #pragma once
+#include <atomic>
 #include "ckda_internal.cuh"
 
 namespace ckda {
@@ -24,6 +25,7 @@ struct LinearArgs {
   const int32_t* cu_seqlens;
   const int32_t* order;
   int* status;
+  int clear;          // the status word is still to be cleared, by the first kernel
   int N;              // sequences: B, or the packed ones
   int B, H, Hk, T, dk, dv;
   int g_head;
@@ -55,6 +57,22 @@ __device__ __forceinline__ float log2_decay(float g) {
   return x < kMinLog2Decay ? kMinLog2Decay : x;
 }
 
+// Lets a kernel have `bytes` of shared memory on the current device; asked once for
+// each kernel and device (a call of its own costs a microsecond of the host's part
+// of a short prompt).  Calls from several threads at worst ask twice.
+template <auto KERNEL>
+cudaError_t allow_smem(size_t bytes) {
+  static std::atomic<uint64_t> done{0};
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = device < 64 ? 1ull << device : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
 // Token-serial kernels on CUDA cores: every type and width up to 128.
 size_t linear_serial_fwd_bytes(int N, int H, int T, int dk, int dv, bool packed);
 cudaError_t linear_serial_fwd(const LinearArgs& a, char* ws, cudaStream_t s);
@@ -69,7 +87,7 @@ inline bool linear_chunk_path(ckda_dtype io, int dk, int dv) {
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 // Chunks of 128 tokens on the tensor cores.
 size_t linear_chunk_fwd_bytes(int N, int B, int H, int T, int dk, int dv, bool packed);
-cudaError_t linear_chunk_fwd(const LinearArgs& a, char* ws, cudaStream_t s);
+cudaError_t linear_chunk_fwd(LinearArgs a, char* ws, cudaStream_t s);
 size_t linear_chunk_bwd_bytes(int N, int B, int H, int Hk, int T, int dk, int dv, bool packed);
 cudaError_t linear_chunk_bwd(const LinearArgs& a, char* ws, cudaStream_t s);
 

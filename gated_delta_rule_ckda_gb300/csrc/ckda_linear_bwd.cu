@@ -778,8 +778,7 @@ cudaError_t linear_chunk_bwd(const LinearArgs& a, char* ws, cudaStream_t s) {
     if ((e = linear_chunk_states(a, sp, out, back, s)) != cudaSuccess) return e;
   }
   if (a.T > 0) {
-    e = cudaFuncSetAttribute(linear_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)gr::kSmem);
+    e = allow_smem<linear_grad_kernel>(gr::kSmem);
     if (e != cudaSuccess) return e;
     const size_t blocks = p.chunks * a.H;
     linear_grad_kernel<<<(unsigned)(blocks < kLinSms ? blocks : kLinSms), gr::kThreads, gr::kSmem,

@@ -81,6 +81,8 @@ linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ 
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(sm + kBars + 404);
   const uint32_t sb = smem_u32(sm);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // (a wait gives up after a second: no other CTA has anything to report yet)
+  if (a.clear && blockIdx.x == 0 && tid == 0) *a.status = 0;
   if (sb & 1023u) {  // swizzled tiles need it; no room to align by hand
     if (tid == 0) set_status(a.status, CKDA_ERR_CUDA);
     return;
@@ -396,7 +398,7 @@ size_t linear_chunk_fwd_bytes(int N, int B, int H, int T, int dk, int dv, bool p
   return linear_split_bytes(linear_split(N, B, H, T, packed), N, H, dk, dv, packed, 1);
 }
 
-cudaError_t linear_chunk_fwd(const LinearArgs& a, char* ws, cudaStream_t s) {
+cudaError_t linear_chunk_fwd(LinearArgs a, char* ws, cudaStream_t s) {
   CUtensorMap mq{}, mk{}, mv{}, mo{};
   if (a.T > 0 && (!linear_map(&mq, a.q, (uint64_t)a.B * a.Hk, a.T, a.dk) ||
                   !linear_map(&mk, a.k, (uint64_t)a.B * a.Hk, a.T, a.dk) ||
@@ -404,14 +406,22 @@ cudaError_t linear_chunk_fwd(const LinearArgs& a, char* ws, cudaStream_t s) {
                   !linear_map(&mo, a.o, (uint64_t)a.B * a.H, a.T, a.dv)))
     return cudaErrorInvalidValue;
   Split sp = linear_split(a.N, a.B, a.H, a.T, a.cu_seqlens != nullptr);
+  if (a.clear && (a.cu_seqlens || sp.per > 1)) {  // more kernels than one
+    if (cudaMemsetAsync(a.status, 0, sizeof(int), s) != cudaSuccess) return cudaErrorUnknown;
+    a.clear = 0;
+  }
   cudaError_t e = linear_split_plan(a, sp, ws, s);
   if (e == cudaSuccess) e = linear_segment_states(a, sp, ws, false, 0, s);
   if (e != cudaSuccess) return e;
-  const auto kernel = a.dk <= 64 ? linear_fwd_kernel<64> : linear_fwd_kernel<128>;
-  const uint32_t smem = a.dk <= 64 ? Layout<64>::kSmem : Layout<128>::kSmem;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const bool half = a.dk <= 64;
+  e = half ? allow_smem<linear_fwd_kernel<64>>(Layout<64>::kSmem)
+           : allow_smem<linear_fwd_kernel<128>>(Layout<128>::kSmem);
   if (e != cudaSuccess) return e;
-  kernel<<<(unsigned)sp.items * a.H, kThreads, smem, s>>>(a, sp, mq, mk, mv, mo);
+  const unsigned blocks = (unsigned)sp.items * a.H;
+  if (half)
+    linear_fwd_kernel<64><<<blocks, kThreads, Layout<64>::kSmem, s>>>(a, sp, mq, mk, mv, mo);
+  else
+    linear_fwd_kernel<128><<<blocks, kThreads, Layout<128>::kSmem, s>>>(a, sp, mq, mk, mv, mo);
   return cudaGetLastError();
 }
 

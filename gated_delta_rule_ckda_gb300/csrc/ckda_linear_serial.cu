@@ -580,21 +580,14 @@ int fwd_piece(int N, int H, int T, int dv, bool packed) {
   return (int)((tokens + kTok - 1) / kTok * kTok);
 }
 
-template <typename F>
-cudaError_t smem_limit(F kernel, size_t bytes) {
-  if (bytes <= 48 * 1024) return cudaSuccess;
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
-
 // What each piece adds to the states, and the scan.  directions: 1 forward only.
 template <typename IO, int R4>
 cudaError_t launch_sum(const LinearArgs& a, const Pieces& p, int directions, cudaStream_t s) {
-  const auto kernel = piece_sum_kernel<IO, R4>;
   const size_t smem = sum_smem(16 * R4);
-  const cudaError_t e = smem_limit(kernel, smem);
+  const cudaError_t e = allow_smem<piece_sum_kernel<IO, R4>>(smem);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)(p.slots * a.H), (a.dk + kOwn - 1) / kOwn, directions);
-  kernel<<<grid, kThreads, smem, s>>>(a, p, 0);
+  piece_sum_kernel<IO, R4><<<grid, kThreads, smem, s>>>(a, p, 0);
   return cudaGetLastError();
 }
 template <typename IO>
@@ -609,11 +602,11 @@ cudaError_t join_pieces(const LinearArgs& a, const Pieces& p, int directions, cu
 
 template <typename IO, int R4>
 cudaError_t launch_o(const LinearArgs& a, const Pieces& p, cudaStream_t s) {
-  const auto kernel = run_o_kernel<IO, R4>;
   const size_t smem = run_smem(16 * R4);
-  const cudaError_t e = smem_limit(kernel, smem);
+  const cudaError_t e = allow_smem<run_o_kernel<IO, R4>>(smem);
   if (e != cudaSuccess) return e;
-  kernel<<<dim3((unsigned)(p.slots * a.H), (a.dv + kOwn - 1) / kOwn), kThreads, smem, s>>>(a, p);
+  const dim3 grid((unsigned)(p.slots * a.H), (a.dv + kOwn - 1) / kOwn);
+  run_o_kernel<IO, R4><<<grid, kThreads, smem, s>>>(a, p);
   return cudaGetLastError();
 }
 
@@ -674,22 +667,20 @@ SerialPlan serial_plan(int N, int B, int H, int T, int dk, int dv, bool packed) 
 
 template <typename IO, int R4>
 cudaError_t launch_dqk(const LinearArgs& a, const SerialWs& w, cudaStream_t s) {
-  const auto kernel = run_dqk_kernel<IO, R4>;
   const size_t smem = run_smem(16 * R4);
-  const cudaError_t e = smem_limit(kernel, smem);
+  const cudaError_t e = allow_smem<run_dqk_kernel<IO, R4>>(smem);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)(w.p.slots * a.H), (a.dk + kOwn - 1) / kOwn, 2);
-  kernel<<<grid, kThreads, smem, s>>>(a, w);
+  run_dqk_kernel<IO, R4><<<grid, kThreads, smem, s>>>(a, w);
   return cudaGetLastError();
 }
 template <typename IO, int R4>
 cudaError_t launch_dv(const LinearArgs& a, const SerialWs& w, cudaStream_t s) {
-  const auto kernel = run_dv_kernel<IO, R4>;
   const size_t smem = run_smem(16 * R4);
-  const cudaError_t e = smem_limit(kernel, smem);
+  const cudaError_t e = allow_smem<run_dv_kernel<IO, R4>>(smem);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)(w.p.slots * a.H), (a.dv + kOwn - 1) / kOwn);
-  kernel<<<grid, kThreads, smem, s>>>(a, w);
+  run_dv_kernel<IO, R4><<<grid, kThreads, smem, s>>>(a, w);
   return cudaGetLastError();
 }
 

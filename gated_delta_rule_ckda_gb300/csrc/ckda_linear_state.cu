@@ -347,11 +347,10 @@ static cudaError_t launch_states(const LinearArgs& a, const Split& sp, const Chu
       (!linear_map(&mx, BACK ? a.q : a.k, (uint64_t)a.B * a.Hk, a.T, a.dk) ||
        !linear_map(&my, BACK ? a.dout : a.v, (uint64_t)a.B * a.H, a.T, a.dv)))
     return cudaErrorInvalidValue;
-  const auto kernel = linear_state_kernel<BACK, IMAGES>;
-  const cudaError_t e = cudaFuncSetAttribute(
-      kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)st::kSmem);
+  const cudaError_t e = allow_smem<linear_state_kernel<BACK, IMAGES>>(st::kSmem);
   if (e != cudaSuccess) return e;
-  kernel<<<(unsigned)sp.items * a.H, st::kThreads, st::kSmem, s>>>(a, sp, out, mx, my);
+  linear_state_kernel<BACK, IMAGES>
+      <<<(unsigned)sp.items * a.H, st::kThreads, st::kSmem, s>>>(a, sp, out, mx, my);
   return cudaGetLastError();
 }
 
