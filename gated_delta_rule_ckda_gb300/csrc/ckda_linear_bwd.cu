@@ -33,11 +33,12 @@ struct BwdWs {
   __nv_bfloat16* dq;    // [B, H, T, dk]: each head's part of dq and dk (shared key
   __nv_bfloat16* dk;    // heads only)
   int32_t* first;       // [N + 1] first chunk of each sequence (packed only)
+  int2* table;          // [chunks] first token, tokens (packed only)
   int chunks;           // slots of a head: chunks, or a bound on them
 };
 
-// Chunks of the packed sequences before each.
-__global__ void __launch_bounds__(1024) chunk_plan_kernel(LinearArgs a, int32_t* first) {
+// Chunks of the packed sequences before each, and the table of all.
+__global__ void __launch_bounds__(1024) chunk_plan_kernel(LinearArgs a, BwdWs w, int32_t* first) {
   __shared__ int32_t sum[1024];
   const int per = (a.N + 1023) / 1024, i0 = threadIdx.x * per, i1 = min(i0 + per, a.N);
   int32_t s = 0;
@@ -55,7 +56,9 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(LinearArgs a, int32_t*
     first[i] = before;
     int t0, len;
     seq_range(a, i, t0, len);
-    before += (len + C - 1) / C;
+    // (offsets that are no packing would run past the table)
+    for (int c = 0; c * C < len && before < w.chunks; ++c, ++before)
+      w.table[before] = make_int2(t0 + c * C, min(len - c * C, C));
   }
   if (i1 == a.N) first[a.N] = before;
 }
@@ -139,25 +142,17 @@ __device__ __forceinline__ Chunk chunk_of(const LinearArgs& a, const BwdWs& w, u
   Chunk u;
   const int ci = block / a.H;
   u.h = block % a.H;
-  int n, c;
+  int b = 0;
   if (w.first) {
-    int lo = 0, hi = a.N;  // first[lo] <= ci < first[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (w.first[mid] <= ci) lo = mid; else hi = mid;
-    }
-    n = lo;
-    c = ci - w.first[n];
+    const int2 t = w.table[ci];
+    u.y = t.x;
+    u.valid = t.y;
   } else {
     const int per = (a.T + C - 1) / C;
-    n = ci / per;
-    c = ci % per;
+    b = ci / per;
+    u.y = ci % per * C;
+    u.valid = min(a.T - u.y, C);
   }
-  int t0, len;
-  seq_range(a, n, t0, len);
-  const int b = a.cu_seqlens ? 0 : n;
-  u.valid = max(min(len - c * C, C), 0);
-  u.y = t0 + c * C;
   u.qz = b * a.Hk + u.h / (a.H / a.Hk);
   u.vz = b * a.H + u.h;
   return u;
@@ -718,7 +713,7 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
 }
 
 struct ChunkPlan {
-  size_t chunks, himg, gimg, dg, dq, dk, first, split, total;
+  size_t chunks, himg, gimg, dg, dq, dk, first, table, split, total;
 };
 ChunkPlan chunk_plan(int N, int B, int H, int Hk, int T, int dk, int dv, bool packed) {
   ChunkPlan p;
@@ -733,6 +728,7 @@ ChunkPlan chunk_plan(int N, int B, int H, int Hk, int T, int dk, int dv, bool pa
   p.dq = at; at += Hk == H ? 0 : up256(rows * dk * 2);
   p.dk = at; at += Hk == H ? 0 : up256(rows * dk * 2);
   p.first = at; at += up256(((size_t)N + 1) * 4);
+  p.table = at; at += packed ? up256(p.chunks * 8) : 0;
   p.split = at; at += linear_split_bytes(linear_split(N, B, H, T, packed), N, H, dk, dv, packed, 2);
   p.total = at;
   return p;
@@ -767,7 +763,8 @@ cudaError_t linear_chunk_bwd(const LinearArgs& a, char* ws, cudaStream_t s) {
     return cudaErrorInvalidValue;
   if (a.cu_seqlens) {
     w.first = reinterpret_cast<int32_t*>(ws + p.first);
-    chunk_plan_kernel<<<1, 1024, 0, s>>>(a, w.first);
+    w.table = reinterpret_cast<int2*>(ws + p.table);
+    chunk_plan_kernel<<<1, 1024, 0, s>>>(a, w, w.first);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   Split sp = linear_split(a.N, a.B, a.H, a.T, a.cu_seqlens != nullptr);

@@ -21,6 +21,11 @@ struct Split {
   int per;               // dense: segments of a sequence; packed: most chunks of a segment
   int items;             // segments of all sequences; packed: a bound on them
   const int32_t* item0;  // packed: [N + 1] first segment by rank in a.order
+                         // and behind it the numbers of cut sequences and of cuts
+  const int4* table;     // packed: [items] sequence, segment, segments, unused (one load
+                         // for a CTA; a search through item0 takes several, one after another)
+  const int2* cuts;      // packed: [cuts] rank of a cut sequence, segment before a cut
+  int most_cuts;
   float* state;          // [items * H][dk][dv]: what each segment hands on
   float* decay;          // [items * H]: over the segment
   float* begin;          // [N * H][dk][dv]: h0 again, for the first segments of sequences
@@ -41,14 +46,10 @@ __device__ __forceinline__ Piece piece_of(const LinearArgs& a, const Split& sp, 
   u.item = block / a.H;
   u.h = block % a.H;
   if (a.cu_seqlens) {
-    int lo = 0, hi = a.N;  // item0[lo] <= item < item0[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (sp.item0[mid] <= u.item) lo = mid; else hi = mid;
-    }
-    u.n = a.order[lo];
-    u.seg = u.item - sp.item0[lo];
-    u.segs = sp.item0[lo + 1] - sp.item0[lo];
+    const int4 t = sp.table[u.item];
+    u.n = t.x;
+    u.seg = t.y;
+    u.segs = t.z;
   } else {
     u.n = u.item / sp.per;
     u.seg = u.item % sp.per;

@@ -50,8 +50,14 @@ linear_state_kernel(const __grid_constant__ LinearArgs a, const __grid_constant_
     if (tid == 0) set_status(a.status, CKDA_ERR_CUDA);
     return;
   }
-  if (blockIdx.x >= pieces(a, sp)) return;  // the grid is a bound
-  const Piece u = piece_of(a, sp, blockIdx.x);
+  // the grid is a bound; without images, only the segments at cuts run
+  unsigned block = blockIdx.x;
+  if (!IMAGES && a.cu_seqlens) {
+    if ((int)(block / a.H) >= sp.item0[a.N + 2]) return;
+    block = (sp.cuts[block / a.H].y + (BACK ? 1 : 0)) * a.H + block % a.H;
+  }
+  if (block >= pieces(a, sp)) return;
+  const Piece u = piece_of(a, sp, block);
   // the first segment in this direction, and the one that hands nothing on
   const bool starts = BACK ? u.seg == u.segs - 1 : u.seg == 0;
   const bool ends = BACK ? u.seg == 0 : u.seg == u.segs - 1;
@@ -229,34 +235,58 @@ linear_state_kernel(const __grid_constant__ LinearArgs a, const __grid_constant_
 }
 
 // ---------------------------------------------------------------- segments
-// Segments of the packed sequences before each, by rank.
-__global__ void __launch_bounds__(1024) split_plan_kernel(LinearArgs a, int per, int32_t* item0) {
-  __shared__ int32_t sum[1024];
+// Segments of the packed sequences before each, by rank, the table of all, and the
+// cuts.  Offsets that are no packing would run past the tables; the bounds are kept.
+__global__ void __launch_bounds__(1024) split_plan_kernel(LinearArgs a, int per, int items,
+                                                          int most_cuts, int32_t* item0,
+                                                          int4* table, int2* cuts) {
+  __shared__ int32_t sum[1024], cut[1024];
   const int share = (a.N + 1023) / 1024, i0 = threadIdx.x * share, i1 = min(i0 + share, a.N);
   auto segments = [&](int i) {
     int t0, len;
     seq_range(a, a.order[i], t0, len);
     return max(1, ((len + C - 1) / C + per - 1) / per);
   };
-  int32_t s = 0;
-  for (int i = i0; i < i1; ++i) s += segments(i);
+  int32_t s = 0, n_cut = 0;
+  for (int i = i0; i < i1; ++i) {
+    const int k = segments(i);
+    s += k;
+    n_cut += k > 1;
+  }
   sum[threadIdx.x] = s;
+  cut[threadIdx.x] = n_cut;
   __syncthreads();
   if (i0 >= i1) return;
-  int32_t before = 0;
-  for (int j = 0; j < (int)threadIdx.x; ++j) before += sum[j];
+  int32_t before = 0, cut_before = 0;
+  for (int j = 0; j < (int)threadIdx.x; ++j) {
+    before += sum[j];
+    cut_before += cut[j];
+  }
   for (int i = i0; i < i1; ++i) {
     item0[i] = before;
-    before += segments(i);
+    const int n = a.order[i], segs = segments(i);
+    for (int k = 0; k < segs && before + k < items; ++k)
+      table[before + k] = make_int4(n, k, segs, 0);
+    // segment k of this rank is the (before - i + k)-th that a cut follows
+    for (int k = 0; k + 1 < segs && before - i + k < most_cuts; ++k)
+      cuts[before - i + k].y = before + k;
+    if (segs > 1 && cut_before < most_cuts) cuts[cut_before++].x = i;
+    before += segs;
   }
-  if (i1 == a.N) item0[a.N] = before;
+  if (i1 == a.N) {
+    item0[a.N] = before;
+    item0[a.N + 1] = min(cut_before, most_cuts);
+    item0[a.N + 2] = min(before - a.N, most_cuts);
+  }
 }
 
 // Joins what the segments hand on: in order, each adds its own to the decayed
 // state before it.  A thread takes one element of one (sequence, head), and loads
 // eight segments' ahead.
 __global__ void __launch_bounds__(256) segment_scan_kernel(LinearArgs a, Split sp, int back) {
-  const int rank = blockIdx.x / a.H, h = blockIdx.x % a.H;
+  const int at = blockIdx.x / a.H, h = blockIdx.x % a.H;
+  if (sp.item0 && at >= sp.item0[a.N + 1]) return;
+  const int rank = sp.item0 ? sp.cuts[at].x : at;
   const int i0 = sp.item0 ? sp.item0[rank] : rank * sp.per;
   const int segs = sp.item0 ? min(sp.item0[rank + 1], sp.items) - i0 : sp.per;
   const int n = a.dk * a.dv, e = blockIdx.y * 256 + threadIdx.x;
@@ -299,7 +329,8 @@ Split linear_split(int N, int B, int H, int T, bool packed) {
   if (packed) {
     const long long share = (chunks * H * 5 / 4 + kLinSms - 1) / kLinSms;
     sp.per = (int)(share > 8 ? share : 8);
-    sp.items = (int)(N + chunks / sp.per);
+    sp.most_cuts = (int)(chunks / sp.per);
+    sp.items = N + sp.most_cuts;
     return sp;
   }
   const long long units = (long long)N * H;
@@ -319,13 +350,18 @@ Split linear_split(int N, int B, int H, int T, bool packed) {
   return sp;
 }
 
-// [N + 1] plan, h0 again, then for each direction the states and decays of the
+static size_t plan_bytes(const Split& sp, int N, bool packed) {
+  return packed ? up256(((size_t)N + 3) * 4) + up256((size_t)sp.items * 16) +
+                      up256((size_t)sp.most_cuts * 8)
+                : 0;
+}
+// The plan and its tables, h0 again, then for each direction the states and decays of the
 // segments.
 size_t linear_split_bytes(const Split& sp, int N, int H, int dk, int dv, bool packed,
                           int directions) {
   const size_t slots = (size_t)sp.items * H;
   const bool cut = packed || sp.per > 1;
-  return up256(((size_t)N + 1) * 4) +
+  return plan_bytes(sp, N, packed) +
          (cut ? up256((size_t)N * H * dk * dv * 4) +
                     directions * (up256(slots * dk * dv * 4) + up256(slots * 4))
               : 0);
@@ -334,8 +370,13 @@ size_t linear_split_bytes(const Split& sp, int N, int H, int dk, int dv, bool pa
 cudaError_t linear_split_plan(const LinearArgs& a, Split& sp, char* ws, cudaStream_t s) {
   if (!a.cu_seqlens) return cudaSuccess;
   int32_t* item0 = reinterpret_cast<int32_t*>(ws);
+  int4* table = reinterpret_cast<int4*>(ws + up256(((size_t)a.N + 3) * 4));
+  int2* cuts = reinterpret_cast<int2*>(ws + up256(((size_t)a.N + 3) * 4) +
+                                       up256((size_t)sp.items * 16));
   sp.item0 = item0;
-  split_plan_kernel<<<1, 1024, 0, s>>>(a, sp.per, item0);
+  sp.table = table;
+  sp.cuts = cuts;
+  split_plan_kernel<<<1, 1024, 0, s>>>(a, sp.per, sp.items, sp.most_cuts, item0, table, cuts);
   return cudaGetLastError();
 }
 
@@ -349,8 +390,10 @@ static cudaError_t launch_states(const LinearArgs& a, const Split& sp, const Chu
     return cudaErrorInvalidValue;
   const cudaError_t e = allow_smem<linear_state_kernel<BACK, IMAGES>>(st::kSmem);
   if (e != cudaSuccess) return e;
+  const unsigned blocks =
+      (unsigned)(!IMAGES && a.cu_seqlens ? sp.most_cuts : sp.items) * a.H;
   linear_state_kernel<BACK, IMAGES>
-      <<<(unsigned)sp.items * a.H, st::kThreads, st::kSmem, s>>>(a, sp, out, mx, my);
+      <<<blocks, st::kThreads, st::kSmem, s>>>(a, sp, out, mx, my);
   return cudaGetLastError();
 }
 
@@ -359,17 +402,18 @@ cudaError_t linear_segment_states(const LinearArgs& a, Split& sp, char* ws, bool
   if (!a.cu_seqlens && sp.per == 1) return cudaSuccess;
   const size_t slots = (size_t)sp.items * a.H;
   const size_t states = up256(slots * a.dk * a.dv * 4), decays = up256(slots * 4);
-  char* at = ws + up256(((size_t)a.N + 1) * 4);
+  char* at = ws + plan_bytes(sp, a.N, a.cu_seqlens != nullptr);
   sp.begin = reinterpret_cast<float*>(at);
   at += up256((size_t)a.N * a.H * a.dk * a.dv * 4) + dir * (states + decays);
   sp.state = reinterpret_cast<float*>(at);
   sp.decay = reinterpret_cast<float*>(at + states);
   // packed, every sequence shorter than a segment: nothing to join
-  if (a.cu_seqlens && a.T <= sp.per * C) return cudaSuccess;
+  if (a.cu_seqlens && sp.most_cuts == 0) return cudaSuccess;
   cudaError_t e = back ? launch_states<true, false>(a, sp, ChunkImages{}, s)
                        : launch_states<false, false>(a, sp, ChunkImages{}, s);
   if (e != cudaSuccess) return e;
-  segment_scan_kernel<<<dim3((unsigned)a.N * a.H, (a.dk * a.dv + 255) / 256), 256, 0, s>>>(
+  const unsigned cut = a.cu_seqlens ? sp.most_cuts : a.N;  // sequences, at most
+  segment_scan_kernel<<<dim3(cut * a.H, (a.dk * a.dv + 255) / 256), 256, 0, s>>>(
       a, sp, back ? 1 : 0);
   return cudaGetLastError();
 }
