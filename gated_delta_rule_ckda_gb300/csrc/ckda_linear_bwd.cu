@@ -20,6 +20,7 @@
 //   3. linear_grad_kernel: all gradients of a chunk.
 // The states pass through HBM in two bf16 parts (hi + lo, 64 KiB a chunk and
 // direction): dg and dh0 are fp32 and need more than one bf16 rounding.
+#include <type_traits>
 #include "ckda_linear_chunk.cuh"
 
 namespace ckda {
@@ -158,20 +159,26 @@ __device__ __forceinline__ Chunk chunk_of(const LinearArgs& a, const BwdWs& w, u
   return u;
 }
 
+// One part of an image into a tile: KP panels of 64 channels, VP x 64 value rows.
+template <int KP, int VP>
 __device__ __forceinline__ void load_image(uint32_t dst, const char* src, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          dst),
-      "l"(src), "r"(kTile), "r"(smem_u32(bar))
-      : "memory");
+#pragma unroll
+  for (int p = 0; p < KP; ++p)
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, "
+        "[%3];" ::"r"(dst + p * kPanel),
+        "l"(src + p * kPanel), "r"(VP * (kPanel / 2)), "r"(smem_u32(bar))
+        : "memory");
 }
 
-// A 128th of the elementwise product of two tiles, summed.
+// A 128th of the elementwise product of two image tiles, summed.
+template <int KP, int VP>
 static __device__ __noinline__ float tile_dot(const char* a, const char* b, int t) {
   float s0 = 0.f, s1 = 0.f;
 #pragma unroll 4
-  for (int i = t; i < (int)kTile / 16; i += 128) {
-    const uint4 u = reinterpret_cast<const uint4*>(a)[i], v = reinterpret_cast<const uint4*>(b)[i];
+  for (int i = t; i < KP * VP * (int)kPanel / 32; i += 128) {
+    const int at = VP == 2 ? i : i / 512 * 1024 + i % 512;  // 64 rows of a panel: its first half
+    const uint4 u = reinterpret_cast<const uint4*>(a)[at], v = reinterpret_cast<const uint4*>(b)[at];
     const uint32_t x[4] = {u.x, u.y, u.z, u.w}, y[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -234,6 +241,8 @@ static __device__ __noinline__ void stage_acc(uint32_t acc, char* tile, int row,
   }
 }
 
+// KP, VP: panels of 64 key and value channels.
+template <int KP, int VP>
 __global__ void __launch_bounds__(gr::kThreads, 1)
 linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ BwdWs w,
                    const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
@@ -242,6 +251,7 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
                    const __grid_constant__ CUtensorMap mdk,
                    const __grid_constant__ CUtensorMap mdv) {
   using namespace gr;
+  constexpr uint32_t kPart = KP * VP * kPanel / 2;  // bytes of an image's hi or lo
   extern __shared__ __align__(1024) char sm[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kBars);
   Gates* gates = reinterpret_cast<Gates*>(sm + kGates);
@@ -264,11 +274,12 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
     for (int i = 0; i < B_COUNT; ++i) {
       const bool by_warps = (i >= B_DSA && i <= B_DSC) || (i >= B_X1S && i < B_DQ) ||
                             (i >= B_HG && i < B_F0) || i == B_GFREE;
-      mbar_init(bars + i, i == B_TAIL                                           ? 12
-                          : i == B_PART || i == B_X3S || i == B_XR + 2 ? 8
-                          : by_warps                                            ? 4
-                          : i == B_F1                                           ? 2
-                                                                                : 1);
+      mbar_init(bars + i, i == B_TAIL                          ? 12
+                          : i == B_PART                        ? 8
+                          : i == B_X3S || i == B_XR + 2        ? 4 * VP
+                          : by_warps                           ? 4
+                          : i == B_F1                          ? VP
+                                                               : 1);
     }
     *abort = 0;
     fence_mbar_init();
@@ -295,28 +306,28 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
         auto last = [&](int bar) { ok = ok && (!again || mbar_wait(bars + bar, par ^ 1)); };
         last(B_DQ); last(B_X3); last(B_DK);
         if (!ok) { *abort = 1; break; }
-        mbar_arrive_expect_tx(bars + B_QK, 2 * kTile);
-        for (int p = 0; p < 2; ++p) {
+        mbar_arrive_expect_tx(bars + B_QK, 2 * KP * kPanel);
+        for (int p = 0; p < KP; ++p) {
           tma_load_3d(sb + kQ + p * kPanel, &mq, bars + B_QK, 64 * p, u.y, u.qz);
           tma_load_3d(sb + kK + p * kPanel, &mk, bars + B_QK, 64 * p, u.y, u.qz);
         }
         last(B_X2); last(B_DV);
         if (!ok) { *abort = 1; break; }
-        mbar_arrive_expect_tx(bars + B_VD, 2 * kTile);
-        for (int p = 0; p < 2; ++p) {
+        mbar_arrive_expect_tx(bars + B_VD, 2 * VP * kPanel);
+        for (int p = 0; p < VP; ++p) {
           tma_load_3d(sb + kV + p * kPanel, &mv, bars + B_VD, 64 * p, u.y, u.vz);
           tma_load_3d(sb + kDo + p * kPanel, &mo, bars + B_VD, 64 * p, u.y, u.vz);
         }
         last(B_F0); last(B_F1); last(B_F2);
         if (!ok) { *abort = 1; break; }
-        mbar_arrive_expect_tx(bars + B_H, 2 * kTile);
-        load_image(sb + kS0, himg, bars + B_H);
-        load_image(sb + kS1, himg + kTile, bars + B_H);
-        mbar_arrive_expect_tx(bars + B_GH, kTile);
-        load_image(sb + kS2, gimg, bars + B_GH);
+        mbar_arrive_expect_tx(bars + B_H, 2 * kPart);
+        load_image<KP, VP>(sb + kS0, himg, bars + B_H);
+        load_image<KP, VP>(sb + kS1, himg + kTile, bars + B_H);
+        mbar_arrive_expect_tx(bars + B_GH, kPart);
+        load_image<KP, VP>(sb + kS2, gimg, bars + B_GH);
         if (!mbar_wait(bars + B_X1L, par) || !mbar_wait(bars + B_HG, par)) { *abort = 1; break; }
-        mbar_arrive_expect_tx(bars + B_GL, kTile);  // Hlo has been read
-        load_image(sb + kS1, gimg + kTile, bars + B_GL);
+        mbar_arrive_expect_tx(bars + B_GL, kPart);  // Hlo has been read
+        load_image<KP, VP>(sb + kS1, gimg + kTile, bars + B_GL);
         // What comes next, into L2 while this chunk is worked on: tiles come free
         // late, and their loads should not wait for HBM then.
         if (block + step < blocks) {
@@ -325,8 +336,12 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
           prefetch_tile(&mk, v.y, v.qz, a.dk);
           prefetch_tile(&mv, v.y, v.vz, a.dv);
           prefetch_tile(&mo, v.y, v.vz, a.dv);
-          prefetch_bytes(w.himg + (size_t)(block + step) * kImage, kImage);
-          prefetch_bytes(w.gimg + (size_t)(block + step) * kImage, kImage);
+          for (int z = 0; z < 2; ++z)
+            for (int x = 0; x < KP; ++x) {
+              const size_t at = (size_t)(block + step) * kImage + z * kTile + x * kPanel;
+              prefetch_bytes(w.himg + at, VP * kPanel / 2);
+              prefetch_bytes(w.gimg + at, VP * kPanel / 2);
+            }
         }
       }
     }
@@ -343,18 +358,18 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
       last(B_DV); last(B_XR + 1); last(B_XR + 2);
       if (!ok) break;
       tc_fence_after();
-      mma_ss<false, false>(tmem + T_S, sb + kQ, sb + kK, 0);
+      mma_ss<false, false, 128, 4 * KP>(tmem + T_S, sb + kQ, sb + kK, 0);
       // A waits for dP: S^T meanwhile only where v and do are still on their way
       const bool soon = mbar_test(bars + B_VD, par);
-      if (!soon) mma_ss<false, false>(tmem + T_ST, sb + kK, sb + kQ, 0);
+      if (!soon) mma_ss<false, false, 128, 4 * KP>(tmem + T_ST, sb + kK, sb + kQ, 0);
       last(B_XR); last(B_DK);
       ok = ok && mbar_wait(bars + B_VD, par);
       if (!ok) break;
       tc_fence_after();
-      mma_ss<false, false>(tmem + T_DP, sb + kDo, sb + kV, 0);
+      mma_ss<false, false, 128, 4 * VP>(tmem + T_DP, sb + kDo, sb + kV, 0);
       umma_commit(bars + B_A);
-      if (soon) mma_ss<false, false>(tmem + T_ST, sb + kK, sb + kQ, 0);
-      mma_ss<false, false>(tmem + T_DPT, sb + kV, sb + kDo, 0);
+      if (soon) mma_ss<false, false, 128, 4 * KP>(tmem + T_ST, sb + kK, sb + kQ, 0);
+      mma_ss<false, false, 128, 4 * VP>(tmem + T_DPT, sb + kV, sb + kDo, 0);
       umma_commit(bars + B_B);
       // what is left, by readiness; `done` keeps the order that TMEM asks for
       enum { X1 = 1, X2H = 2, X2L = 4, X3 = 8, DQ = 16, DK = 32, DV = 64, ALL = 127 };
@@ -369,34 +384,34 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
       for (uint32_t look = 1; done != ALL; ++look) {
         if (!(done & X1)) {
           if (mbar_test(bars + B_H, par) && ready(X1, 0, B_DSA)) {
-            mma_ss<false, true>(tmem + T_X1, sb + kDo, sb + kS1, 0);
+            mma_ss<false, true, 64 * KP, 4 * VP>(tmem + T_X1, sb + kDo, sb + kS1, 0);
             umma_commit(bars + B_X1L);  // Glo may come
-            mma_ss<false, true>(tmem + T_X1, sb + kDo, sb + kS0, 1);
+            mma_ss<false, true, 64 * KP, 4 * VP>(tmem + T_X1, sb + kDo, sb + kS0, 1);
             umma_commit(bars + B_X1);
           }
         } else if (ready(DQ, X1, B_X1S)) {
-          mma_ts<true>(tmem + T_X1, tmem + T_DS, sb + kK, 1);
+          mma_ts<true, 64 * KP>(tmem + T_X1, tmem + T_DS, sb + kK, 1);
           umma_commit(bars + B_DQ);
         }
         if (!(done & X2H)) {
           if (mbar_test(bars + B_GH, par) && mbar_test(bars + B_DSC, par) && ready(X2H, 0, B_DSB)) {
-            mma_ss<false, true>(tmem + T_X2, sb + kV, sb + kS2, 0);
+            mma_ss<false, true, 64 * KP, 4 * VP>(tmem + T_X2, sb + kV, sb + kS2, 0);
           }
         } else if (ready(X2L, X2H, B_GL)) {
-          mma_ss<false, true>(tmem + T_X2, sb + kV, sb + kS1, 1);
+          mma_ss<false, true, 64 * KP, 4 * VP>(tmem + T_X2, sb + kV, sb + kS1, 1);
           umma_commit(bars + B_X2);
         } else if (done & X2L) {
           if (ready(DK, X2L, B_X2S)) {
-            mma_ts<true>(tmem + T_X2, tmem + T_DST, sb + kQ, 1);
+            mma_ts<true, 64 * KP>(tmem + T_X2, tmem + T_DST, sb + kQ, 1);
             umma_commit(bars + B_DK);
           }
           if (ready(X3, DQ, B_XR)) {  // dQ has left its columns
-            mma_ss<false, false>(tmem + T_X3, sb + kK, sb + kS2, 0);
-            mma_ss<false, false>(tmem + T_X3, sb + kK, sb + kS1, 1);
+            mma_ss<false, false, 64 * VP, 4 * KP>(tmem + T_X3, sb + kK, sb + kS2, 0);
+            mma_ss<false, false, 64 * VP, 4 * KP>(tmem + T_X3, sb + kK, sb + kS1, 1);
             umma_commit(bars + B_X3);
           }
           if (ready(DV, X3, B_X3S)) {
-            mma_ts<true>(tmem + T_X3, tmem + T_PT, sb + kDo, 1);
+            mma_ts<true, 64 * VP>(tmem + T_X3, tmem + T_PT, sb + kDo, 1);
             umma_commit(bars + B_DV);
           }
         }
@@ -455,7 +470,7 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
         // <H, G>, first (Hhi + Hlo, Ghi); A adds (Hhi, Glo) when Glo has come.
         // (Hlo, Glo) is 2^-18 of the rest and left out.
         if (!warp_wait(bars + B_H, par, abort) || !warp_wait(bars + B_GH, par, abort)) break;
-        hgsum = tile_dot(sm + kS0, sm + kS2, row) + tile_dot(sm + kS1, sm + kS2, row);
+        hgsum = tile_dot<KP, VP>(sm + kS0, sm + kS2, row) + tile_dot<KP, VP>(sm + kS1, sm + kS2, row);
         warp_arrive(bars + B_HG);
       }
       if (!warp_wait(bars + B_G, par, abort)) break;
@@ -526,18 +541,18 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
         warp_arrive(bars + B_DSA);
         if (!warp_wait(bars + B_X1, par, abort)) break;
         tc_fence_after();
-        dot = scale_acc(lanes + T_X1, into, own, sm + kK, sm + kQ, row, 0, 4);
+        dot = scale_acc(lanes + T_X1, into, own, sm + kK, sm + kQ, row, 0, 2 * KP);
         warp_arrive(bars + B_X1S);
         // the rest of <H, G> meanwhile: (Hhi, Glo)
         if (!warp_wait(bars + B_H, par, abort) || !warp_wait(bars + B_GL, par, abort)) break;
-        hgsum = tile_dot(sm + kS0, sm + kS1, row);
+        hgsum = tile_dot<KP, VP>(sm + kS0, sm + kS1, row);
         warp_arrive(bars + B_HG + 1);
         named_sync(1, 128);  // dQ goes over Hhi
         if (!warp_wait(bars + B_DQ, par, abort)) break;
         tc_fence_after();
-        stage_acc(lanes + T_X1, sm + kS0, row, 0, 4);
+        stage_acc(lanes + T_X1, sm + kS0, row, 0, 2 * KP);
         warp_arrive(bars + B_XR);
-        put(&mdq, w.dq ? w.dq : a.dq, w.dq ? vrow : krow, a.dk, kS0, w.dq ? u.vz : u.qz, 0, 2);
+        put(&mdq, w.dq ? w.dq : a.dq, w.dq ? vrow : krow, a.dk, kS0, w.dq ? u.vz : u.qz, 0, KP);
       } else {
         // row j: i over blocks from its own on.  B forms dS^T (over dP^T) and the
         // sums of W, C forms P^T (behind dS, so after A).
@@ -617,20 +632,20 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
         if (isb) {
           if (!warp_wait(bars + B_X2, par, abort)) break;
           tc_fence_after();
-          dot = scale_acc(lanes + T_X2, out, own, sm + kQ, sm + kK, row, 0, 4);
+          dot = scale_acc(lanes + T_X2, out, own, sm + kQ, sm + kK, row, 0, 2 * KP);
           warp_arrive(bars + B_X2S);
           if (!warp_wait(bars + B_DK, par, abort)) break;
           tc_fence_after();
           // over Ghi: the products' last reader is X3, C's dot product came before
           if (!warp_wait(bars + B_X3, par, abort) || !warp_wait(bars + B_HG, par, abort)) break;
-          stage_acc(lanes + T_X2, sm + kS2, row, 0, 4);
+          stage_acc(lanes + T_X2, sm + kS2, row, 0, 2 * KP);
           warp_arrive(bars + B_XR + 1);
-          put(&mdk, w.dk ? w.dk : a.dkey, w.dk ? vrow : krow, a.dk, kS2, w.dk ? u.vz : u.qz, 0, 2);
+          put(&mdk, w.dk ? w.dk : a.dkey, w.dk ? vrow : krow, a.dk, kS2, w.dk ? u.vz : u.qz, 0, KP);
         } else {
           own_p = own;
         }
       }
-      if (wg != 1) {
+      if (wg == 2 || (wg == 0 && VP == 2)) {
         // dV: C the first panel, A the second
         const int half = wg == 0 ? 1 : 0;
         if (!warp_wait(bars + B_X3, par, abort)) break;
@@ -649,7 +664,8 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
       if (lead) {
         store_read_wait();
         if (wg == 0) mbar_arrive(bars + B_F0);
-        mbar_arrive(bars + (wg == 1 ? B_F2 : B_F1));
+        if (wg == 1) mbar_arrive(bars + B_F2);
+        if (wg == 2 || (wg == 0 && VP == 2)) mbar_arrive(bars + B_F1);
       }
       // dg_t = e^{L_C} <H, G> + sum_{j<t} kd_j + sum_{i>=t} (qd_i + row_i - col_i):
       // B hands its sums by token to A, over decays that all three have read
@@ -775,12 +791,20 @@ cudaError_t linear_chunk_bwd(const LinearArgs& a, char* ws, cudaStream_t s) {
     if ((e = linear_chunk_states(a, sp, out, back, s)) != cudaSuccess) return e;
   }
   if (a.T > 0) {
-    e = allow_smem<linear_grad_kernel>(gr::kSmem);
-    if (e != cudaSuccess) return e;
     const size_t blocks = p.chunks * a.H;
-    linear_grad_kernel<<<(unsigned)(blocks < kLinSms ? blocks : kLinSms), gr::kThreads, gr::kSmem,
-                         s>>>(a, w, mq, mk, mv, mo, mdq, mdk, mdv);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const auto grad = [&](auto kp, auto vp) {
+      constexpr int KP = decltype(kp)::value, VP = decltype(vp)::value;
+      const cudaError_t e = allow_smem<linear_grad_kernel<KP, VP>>(gr::kSmem);
+      if (e != cudaSuccess) return e;
+      linear_grad_kernel<KP, VP><<<(unsigned)(blocks < kLinSms ? blocks : kLinSms), gr::kThreads,
+                                   gr::kSmem, s>>>(a, w, mq, mk, mv, mo, mdq, mdk, mdv);
+      return cudaGetLastError();
+    };
+    const std::integral_constant<int, 1> one;
+    const std::integral_constant<int, 2> two;
+    e = a.dk <= 64 ? (a.dv <= 64 ? grad(one, one) : grad(one, two))
+                   : (a.dv <= 64 ? grad(two, one) : grad(two, two));
+    if (e != cudaSuccess) return e;
     if (w.dq) {
       const size_t n = (size_t)a.B * a.Hk * a.T * a.dk / 8, blocks = (n + 255) / 256;
       sum_parts_kernel<<<(unsigned)(blocks < 16 * kLinSms ? blocks : 16 * kLinSms), 256, 0, s>>>(a, w);

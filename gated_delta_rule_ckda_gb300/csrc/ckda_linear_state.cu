@@ -33,7 +33,9 @@ enum { B_FULL = 0, B_EMPTY = 4, B_KT = 8, B_DF, B_DFREE = B_DF + 2, B_G = B_DFRE
        B_END, B_COUNT };
 }  // namespace st
 
-template <bool BACK, bool IMAGES>
+// KP: panels of 64 key channels.  Of an image only the panels and value rows that
+// exist are written.
+template <bool BACK, bool IMAGES, int KP>
 __global__ void __launch_bounds__(st::kThreads, 1)
 linear_state_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ Split sp,
                     const __grid_constant__ ChunkImages images,
@@ -97,8 +99,9 @@ linear_state_kernel(const __grid_constant__ LinearArgs a, const __grid_constant_
         const int slot = i % kSlots, use = i / kSlots;
         if (use > 0 && !mbar_wait(bars + B_EMPTY + slot, (use - 1) & 1)) { *abort = 1; break; }
         if (*abort) break;
+        // (a second panel of values that no channel reaches is never looked at)
         load_tile(sb + slot * kTile, i & 1 ? &my : &mx, bars + B_FULL + slot, t0 + at(i / 2) * C,
-                  i & 1 ? yz : xz);
+                  i & 1 ? yz : xz, i & 1 ? (a.dv > 64 ? 2 : 1) : KP);
       }
     }
   } else if (warp == 1) {
@@ -109,8 +112,8 @@ linear_state_kernel(const __grid_constant__ LinearArgs a, const __grid_constant_
         if (ok && i >= 2) ok = mbar_wait(bars + B_DFREE + p, (i / 2 - 1) & 1);
         if (!ok || !mbar_wait(bars + B_KT, p)) { *abort = 1; break; }
         tc_fence_after();
-        mma_ss<true, true>(tmem + 128 * p, sb + iy * kTile, sb + ix * kTile, 0);
-        mma_ss<true, true>(tmem + 128 * p, sb + iy * kTile, sb + kLo, 1);
+        mma_ss<true, true, 64 * KP>(tmem + 128 * p, sb + iy * kTile, sb + ix * kTile, 0);
+        mma_ss<true, true, 64 * KP>(tmem + 128 * p, sb + iy * kTile, sb + kLo, 1);
         umma_commit(bars + B_DF + p);
         umma_commit(bars + B_EMPTY + ix);
         umma_commit(bars + B_EMPTY + iy);
@@ -143,9 +146,7 @@ linear_state_kernel(const __grid_constant__ LinearArgs a, const __grid_constant_
         if (t >= valid) zero_row(sm + (ix + 1) * kTile, t);
       }
       if (i >= 1 && !warp_wait(bars + B_DF + ((i - 1) & 1), ((i - 1) / 2) & 1, abort)) break;
-#pragma unroll 1
-      for (int p = 0; p < 2; ++p)
-        scale_row(sm + ix * kTile, sm + kLo, t, 8 * p, 8 * p + 8, wt, t < valid);
+      scale_row(sm + ix * kTile, sm + kLo, t, 0, 8 * KP, wt, t < valid);
       warp_publish(bars + B_KT);
     }
   } else if (warp >= 8) {
@@ -185,7 +186,12 @@ linear_state_kernel(const __grid_constant__ LinearArgs a, const __grid_constant_
         }
         fence_proxy_async_smem();
         named_sync(1, 256);
-        if (tid == 256) store_bytes(images.img + slot * kImage, sb + kStage, kImage);
+        if (tid == 256)
+          for (int z = 0; z < 2 * KP; ++z) {  // (part, panel)
+            const uint32_t off = z / KP * kTile + z % KP * kPanel;
+            store_bytes(images.img + slot * kImage + off, sb + kStage + off,
+                        a.dv > 64 ? kPanel : kPanel / 2);
+          }
       }
       if (i >= steps) break;
       if (!(ok = warp_wait(bars + B_G, p, abort))) break;
@@ -380,21 +386,28 @@ cudaError_t linear_split_plan(const LinearArgs& a, Split& sp, char* ws, cudaStre
   return cudaGetLastError();
 }
 
-template <bool BACK, bool IMAGES>
-static cudaError_t launch_states(const LinearArgs& a, const Split& sp, const ChunkImages& out,
+template <bool BACK, bool IMAGES, int KP>
+static cudaError_t launch_states_of(const LinearArgs& a, const Split& sp, const ChunkImages& out,
                                  cudaStream_t s) {
   CUtensorMap mx{}, my{};
   if (a.T > 0 &&
       (!linear_map(&mx, BACK ? a.q : a.k, (uint64_t)a.B * a.Hk, a.T, a.dk) ||
        !linear_map(&my, BACK ? a.dout : a.v, (uint64_t)a.B * a.H, a.T, a.dv)))
     return cudaErrorInvalidValue;
-  const cudaError_t e = allow_smem<linear_state_kernel<BACK, IMAGES>>(st::kSmem);
+  const cudaError_t e = allow_smem<linear_state_kernel<BACK, IMAGES, KP>>(st::kSmem);
   if (e != cudaSuccess) return e;
   const unsigned blocks =
       (unsigned)(!IMAGES && a.cu_seqlens ? sp.most_cuts : sp.items) * a.H;
-  linear_state_kernel<BACK, IMAGES>
+  linear_state_kernel<BACK, IMAGES, KP>
       <<<blocks, st::kThreads, st::kSmem, s>>>(a, sp, out, mx, my);
   return cudaGetLastError();
+}
+
+template <bool BACK, bool IMAGES>
+static cudaError_t launch_states(const LinearArgs& a, const Split& sp, const ChunkImages& out,
+                                 cudaStream_t s) {
+  return a.dk <= 64 ? launch_states_of<BACK, IMAGES, 1>(a, sp, out, s)
+                    : launch_states_of<BACK, IMAGES, 2>(a, sp, out, s);
 }
 
 cudaError_t linear_segment_states(const LinearArgs& a, Split& sp, char* ws, bool back, int dir,
