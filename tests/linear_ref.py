@@ -136,3 +136,36 @@ def state_tol(io, T):
 def decay_tol(io, T):
     """dg, fp32: differences of sums that are up to 8 times what is left."""
     return 8 * state_tol(io, T)
+
+
+def smoke_error(ck, dev):
+    """Largest rms error over tolerance of a small forward, its gradients, a step
+    and a layer norm with its gradients, times the bf16 tolerance of an output."""
+    gen = torch.Generator().manual_seed(11)
+    B, H, Hk, T, d, bf = 1, 4, 2, 200, 64, torch.bfloat16
+    mk = lambda *s: torch.randn(*s, generator=gen)
+    q, k, v, do = (mk(B, n, T, d).to(bf) for n in (Hk, Hk, H, H))
+    g, h0, dhT = -0.1 * mk(B, H, T).abs(), mk(B, H, d, d), mk(B, H, d, d)
+    c = [x.to(dev) for x in (q, k, v, g, do, h0, dhT)]
+    o, hT = ck.linear_fwd(*c[:4], c[5], scale=0.125)
+    grads = ck.linear_bwd(*c[:5], h0=c[5], dhT=c[6], scale=0.125)
+    for call in (ck.linear_fwd, ck.linear_bwd):
+        st = ck.fwd_status(call.last_workspace)
+        if st != 0:
+            raise RuntimeError(f"linear attention: device status {ck.STATUS.get(st, st)}")
+    ref = linear(q, k, v, g, h0, None, 0.125, do, dhT)
+    tol = [token_tol(bf, T), state_tol(bf, T), *[token_tol(bf, T)] * 3, decay_tol(bf, T),
+           state_tol(bf, T)]
+    worst = [far(a, r)[0] / t for a, r, t in zip((o, hT, *grads), ref, tol)]
+    state, x = hT.clone(), [y[:, :, -1].contiguous() for y in c[:4]]
+    so = ck.linear_decode_step(*x, state, scale=0.125)
+    one = linear(*(y[:, :, -1:] for y in (q, k, v, g)), hT, None, 0.125)
+    worst += [far(so, one[0][:, :, 0])[0] / token_tol(bf, 1), far(state, one[1])[0] / state_tol(bf, 1)]
+    w, b = 1 + 0.1 * mk(d), mk(d)
+    y, mean, rstd = ck.layernorm_fwd(c[2], w.to(dev), b.to(dev))
+    n = layer_norm(v, w, b, 1e-5)
+    dx, dw, db = ck.layernorm_bwd(c[4], c[2], mean, rstd, w.to(dev))
+    m = layer_norm_bwd(do, v, n[1], n[2], w)
+    worst += [far(y, n[0])[0] / token_tol(bf, 1), far(dx, m[0])[0] / token_tol(bf, 1),
+              far(dw, m[1])[0] / state_tol(bf, T * H), far(db, m[2])[0] / state_tol(bf, T * H)]
+    return max(worst) * token_tol(bf, 1)
