@@ -93,7 +93,7 @@ size_t ckda_linear_bwd_workspace_bytes(int num_seqs, int B, int H, int Hk, int T
   if (num_seqs < 0 || B < 1 || H < 1 || Hk < 1 || T < 0 || dk < 1 || dv < 1) return 0;
   const int N = num_seqs > 0 ? num_seqs : B;
   // what either path takes: which one runs depends on the pointers' alignment too
-  size_t bytes = linear_serial_bwd_bytes(N, B, H, T, dk, dv, num_seqs > 0);
+  size_t bytes = linear_serial_bwd_bytes(N, B, H, Hk, T, dk, dv, num_seqs > 0);
   if (linear_chunk_path(io_dtype, dk, dv)) {
     const size_t chunk = linear_chunk_bwd_bytes(N, B, H, Hk, T, dk, dv, num_seqs > 0);
     if (chunk > bytes) bytes = chunk;

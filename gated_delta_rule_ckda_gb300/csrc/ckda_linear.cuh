@@ -12,7 +12,6 @@ constexpr float kLog2e = 1.4426950408889634f;
 // A decay of exp2(-160) is zero in fp32 whatever it multiplies; log decays are
 // clamped there so that g = -inf (a reset) leaves sums and differences finite.
 constexpr float kMinLog2Decay = -160.f;
-constexpr int kCkptTokens = 64;    // token-serial backward: tokens of a piece
 
 struct LinearArgs {
   const void* q;      // io   [B, Hk, T, dk]
@@ -61,7 +60,7 @@ __device__ __forceinline__ float log2_decay(float g) {
 // each kernel and device (a call of its own costs a microsecond of the host's part
 // of a short prompt).  Calls from several threads at worst ask twice.
 template <auto KERNEL>
-cudaError_t allow_smem(size_t bytes) {
+cudaError_t allow_smem(size_t bytes) {  // the most that any launch of it takes
   static std::atomic<uint64_t> done{0};
   int device = 0;
   cudaError_t e = cudaGetDevice(&device);
@@ -76,7 +75,7 @@ cudaError_t allow_smem(size_t bytes) {
 // Token-serial kernels on CUDA cores: every type and width up to 128.
 size_t linear_serial_fwd_bytes(int N, int H, int T, int dk, int dv, bool packed);
 cudaError_t linear_serial_fwd(const LinearArgs& a, char* ws, cudaStream_t s);
-size_t linear_serial_bwd_bytes(int N, int B, int H, int T, int dk, int dv, bool packed);
+size_t linear_serial_bwd_bytes(int N, int B, int H, int Hk, int T, int dk, int dv, bool packed);
 cudaError_t linear_serial_bwd(const LinearArgs& a, char* ws, cudaStream_t s);
 
 // Shapes and pointers the chunked tensor-core kernels take: TMA wants 16-byte
