@@ -24,6 +24,11 @@
 // owns the column, writes one partial row to the workspace, and a second
 // kernel adds the partial rows in a fixed order.  No atomics: two calls on the
 // same input give the same bits.
+//
+// Measured, bf16 with fp32 weights: forward of 1,048,576 rows of 128 94 us, 85% of the
+// copy bandwidth; backward of 16,384 rows of 4096 84 us, 71% (76 us the rows, the rest
+// the second kernel and its start); backward of 2,999 rows of 1031 in fp32 28 us,
+// single elements and mostly launch and host time.
 #include "ckda_internal.cuh"
 
 namespace ckda {
@@ -493,7 +498,7 @@ __global__ void __launch_bounds__(1024) norm_weight_grad_kernel(NormArgs a) {
 
 // ----------------------------------------------------------------- dispatch
 // Vectors of 16 bytes where the width and every row-indexed pointer allow it,
-// single elements otherwise.
+// single elements otherwise (16,384 rows of 4096, backward: 84 us and 355 us).
 inline bool vector_ok(int D, int vec, const void* p0, const void* p1, const void* p2) {
   const uintptr_t m = reinterpret_cast<uintptr_t>(p0) | reinterpret_cast<uintptr_t>(p1) |
                       reinterpret_cast<uintptr_t>(p2);
@@ -539,8 +544,11 @@ cudaError_t run_bwd(NormArgs& a, int per_sm, cudaStream_t s) {
 }
 
 // Threads of a row by its width: the fewest lanes that hold it in one or two
-// vectors each; wide rows a block.  The ring is as deep as keeps 40 KB or more
-// of an SM in flight.
+// vectors each (rows of 128 by 16 lanes 94 us, by 32 half of which idle 194 us);
+// wide rows a block.  The ring is as deep as keeps 40 KB or more of an SM in flight.
+// Backward, blocks an SM: a row of 4096 takes 141 us with its two numbers loaded at
+// their use, then 100 with three blocks, 97 with four and 84 with two, whose rows
+// come to the memory in longer runs; a row by 512 threads takes 109.
 template <typename IO, typename W, int VEC>
 cudaError_t fwd_vec(const NormArgs& a, cudaStream_t s) {
   const int D = a.D;

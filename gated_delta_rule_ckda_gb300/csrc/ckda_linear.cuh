@@ -72,7 +72,7 @@ cudaError_t allow_smem(size_t bytes) {  // the most that any launch of it takes
   return e;
 }
 
-// Token-serial kernels on CUDA cores: every type and width up to 128.
+// Kernels on CUDA cores: every type and width up to 128.
 size_t linear_serial_fwd_bytes(int N, int H, int T, int dk, int dv, bool packed);
 cudaError_t linear_serial_fwd(const LinearArgs& a, char* ws, cudaStream_t s);
 size_t linear_serial_bwd_bytes(int N, int B, int H, int Hk, int T, int dk, int dv, bool packed);

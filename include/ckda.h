@@ -485,12 +485,19 @@ ckda_status ckda_prep_bwd(const void *q_raw, const void *k_raw, const void *a_ra
  *          its h0 on as hT.  hT may alias h0, o no input.
  *
  * dk, dv <= 128.  bf16 I/O with dk and dv multiples of 8 and 16-byte aligned
- * q, k, v runs chunks of 128 tokens on the tensor cores; everything else runs
- * token by token on CUDA cores.  The state is fp32 on both.
+ * q, k, v, o runs chunks of 128 tokens on the tensor cores; everything else runs
+ * on CUDA cores in fp32.  The state is fp32 on both.
+ *
+ * Values that are not finite: on CUDA cores a token reaches only what the formula
+ * says.  On the tensor cores a product with the zeros of the causal mask spreads
+ * an infinity or a NaN of k or v (backward: of q, k, v or dout) to the other
+ * tokens of its own chunk of 128 as well, also to earlier ones (backward, later).
+ * Neither path reaches another sequence or head.
  *
  * workspace: ckda_linear_fwd_workspace_bytes(cu_seqlens ? num_seqs : 0, ...)
  * bytes, 256-byte aligned, scratch with the status word ckda_fwd_status() reads
- * (CKDA_ERR_TIMEOUT only).
+ * (CKDA_ERR_TIMEOUT only: a wait inside a kernel that ran out, results invalid).
+ * Calls that overlap need a workspace each.
  */
 size_t ckda_linear_fwd_workspace_bytes(int num_seqs, int B, int H, int T, int dk, int dv,
                                        ckda_dtype io_dtype);

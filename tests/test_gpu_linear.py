@@ -337,3 +337,24 @@ def test_many_packed_sequences(ck):
     gen = torch.Generator().manual_seed(9)
     cu = [0] + torch.randint(0, 200, (60,), generator=gen).cumsum(0).tolist()
     compare(ck, *make(1, 6, 3, cu[-1], 64, 64, BF, 11, N=60), scale=0.125, cu=cu)
+
+
+def test_values_that_are_not_finite_keep_to_their_tokens(ck):
+    """On CUDA cores: a NaN of v, k or q reaches only what the formula says."""
+    T, at = 200, 70
+    x, e = make(1, 2, 2, T, 20, 36, F32, 43)
+    d, e = gpu(x), gpu(e)
+    c, h0, do, dhT = [d[n] for n in "qkvg"], d["h0"], e["do"], e["dhT"]
+    plain = ck.linear_fwd(*c, h0, scale=0.2)[0]
+    for i in range(3):
+        y = [z.clone() for z in c]
+        y[i][:, :, at] = float("nan")
+        o = ck.linear_fwd(*y, h0, scale=0.2)[0]
+        torch.testing.assert_close(o[:, :, :at], plain[:, :, :at], rtol=0, atol=0)
+        assert torch.isnan(o[:, :, at]).any()
+        dq, dk, dv, dg, _ = ck.linear_bwd(*y, do, h0=h0, dhT=dhT, scale=0.2)
+        if i > 0:  # k, v: queries before
+            assert torch.isfinite(dq[:, :, :at]).all()
+        if i != 1:  # q, v: keys behind
+            assert torch.isfinite(dk[:, :, at + 1:]).all()
+        assert torch.isfinite(dv[:, :, at + 1:]).all()
