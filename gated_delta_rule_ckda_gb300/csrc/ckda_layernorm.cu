@@ -26,10 +26,11 @@
 // same input give the same bits.
 //
 // Measured, bf16 with fp32 weights: forward of 1,048,576 rows of 128 94 us, 85% of the
-// copy bandwidth; backward of 16,384 rows of 4096 84 us, 71% (76 us the rows, the rest
-// the second kernel and its start); backward of 2,999 rows of 1031 in fp32 28 us,
+// copy bandwidth; backward of 16,384 rows of 4096 82 us, 72% (76 us the rows, the rest
+// the second kernel and its start); backward of 2,999 rows of 1031 in fp32 25 us,
 // single elements and mostly launch and host time.
 #include "ckda_internal.cuh"
+#include "ckda_launch.cuh"
 
 namespace ckda {
 namespace {
@@ -298,6 +299,8 @@ __global__ void __launch_bounds__(1024) norm_fwd_long_kernel(NormArgs a) {
 // One partial row of dw and db for each block.
 template <typename IO, typename W, int VEC, int TB, int LPR, int NV, int S>
 __global__ void __launch_bounds__(TB) norm_bwd_kernel(NormArgs a) {
+  after_previous();
+  let_next_start();
   constexpr int kGroups = TB / LPR;
   extern __shared__ __align__(16) char sm[];
   __shared__ float red[4 * TB / 32];
@@ -444,6 +447,8 @@ __global__ void __launch_bounds__(TB) norm_bwd_kernel(NormArgs a) {
 // and db in its row of the workspace.
 template <typename IO, typename W>
 __global__ void __launch_bounds__(1024) norm_bwd_long_kernel(NormArgs a) {
+  after_previous();
+  let_next_start();
   __shared__ float red[32];
   const float inv_d = 1.f / (float)a.D;
   float* pw = a.part ? a.part + (size_t)blockIdx.x * a.D : nullptr;
@@ -479,6 +484,8 @@ __global__ void __launch_bounds__(1024) norm_bwd_long_kernel(NormArgs a) {
 // over the partial rows, joined in a fixed order.
 template <typename W>
 __global__ void __launch_bounds__(1024) norm_weight_grad_kernel(NormArgs a) {
+  after_previous();
+  let_next_start();
   __shared__ float s[32][33];
   const int c = threadIdx.x & 31, g = threadIdx.x >> 5;
   const int i = blockIdx.x * 32 + c;
@@ -593,8 +600,7 @@ cudaError_t launch_norm(NormArgs a, bool back, cudaStream_t s) {
   }
   if (back && a.part) {
     if (a.rows == 0) a.parts = 0;  // the sums over no rows are zero
-    norm_weight_grad_kernel<W><<<dim3((a.D + 31) / 32, 2), 1024, 0, s>>>(a);
-    e = cudaGetLastError();
+    e = launch_next(a.rows > 0, norm_weight_grad_kernel<W>, dim3((a.D + 31) / 32, 2), 1024, 0, s, a);
   }
   return e;
 }

@@ -4,6 +4,7 @@
 #pragma once
 #include <atomic>
 #include "ckda_internal.cuh"
+#include "ckda_launch.cuh"
 
 namespace ckda {
 

@@ -43,6 +43,8 @@ struct BwdWs {
 
 // Chunks of the packed sequences before each, and the table of all.
 __global__ void __launch_bounds__(1024) chunk_plan_kernel(LinearArgs a, BwdWs w, int32_t* first) {
+  after_previous();
+  let_next_start();
   __shared__ int32_t sum[1024];
   const int per = (a.N + 1023) / 1024, i0 = threadIdx.x * per, i1 = min(i0 + per, a.N);
   int32_t s = 0;
@@ -113,6 +115,8 @@ constexpr uint32_t T_DS = 0, T_PT = 64, T_X1 = 128, T_X3 = 128, T_X2 = 256, T_DS
 // is rounded once, as dq and dk would be of a head of its own, and added in fp32;
 // fp32 parts would double the bytes of a pass that is bound by them.
 __global__ void __launch_bounds__(256) sum_parts_kernel(LinearArgs a, BwdWs w) {
+  after_previous();
+  let_next_start();
   const int group = a.H / a.Hk;
   const size_t per = (size_t)a.T * a.dk / 8, total = (size_t)a.B * a.Hk * per;  // vectors of 8
   for (size_t e = (size_t)blockIdx.x * 256 + threadIdx.x; e < total; e += (size_t)gridDim.x * 256) {
@@ -784,8 +788,8 @@ cudaError_t linear_chunk_bwd(const LinearArgs& a, char* ws, cudaStream_t s) {
   if (a.cu_seqlens) {
     w.first = reinterpret_cast<int32_t*>(ws + p.first);
     w.table = reinterpret_cast<int2*>(ws + p.table);
-    chunk_plan_kernel<<<1, 1024, 0, s>>>(a, w, w.first);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = launch_next(true, chunk_plan_kernel, 1, 1024, 0, s, a, w, w.first);
+    if (e != cudaSuccess) return e;
   }
   Split sp = linear_split(a.N, a.B, a.H, a.T, a.cu_seqlens != nullptr);
   if ((e = linear_split_plan(a, sp, ws + p.split, s)) != cudaSuccess) return e;
@@ -800,9 +804,9 @@ cudaError_t linear_chunk_bwd(const LinearArgs& a, char* ws, cudaStream_t s) {
       constexpr int KP = decltype(kp)::value, VP = decltype(vp)::value;
       const cudaError_t e = allow_smem<linear_grad_kernel<KP, VP>>(gr::kSmem);
       if (e != cudaSuccess) return e;
-      linear_grad_kernel<KP, VP><<<(unsigned)(blocks < kLinSms ? blocks : kLinSms), gr::kThreads,
-                                   gr::kSmem, s>>>(a, w, mq, mk, mv, mo, mdq, mdk, mdv);
-      return cudaGetLastError();
+      return launch_next(false, linear_grad_kernel<KP, VP>,
+                         (unsigned)(blocks < kLinSms ? blocks : kLinSms), gr::kThreads, gr::kSmem,
+                         s, a, w, mq, mk, mv, mo, mdq, mdk, mdv);
     };
     const std::integral_constant<int, 1> one;
     const std::integral_constant<int, 2> two;
@@ -811,8 +815,9 @@ cudaError_t linear_chunk_bwd(const LinearArgs& a, char* ws, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (w.dq) {
       const size_t n = (size_t)a.B * a.Hk * a.T * a.dk / 8, blocks = (n + 255) / 256;
-      sum_parts_kernel<<<(unsigned)(blocks < 16 * kLinSms ? blocks : 16 * kLinSms), 256, 0, s>>>(a, w);
-      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+      e = launch_next(true, sum_parts_kernel,
+                      (unsigned)(blocks < 16 * kLinSms ? blocks : 16 * kLinSms), 256, 0, s, a, w);
+      if (e != cudaSuccess) return e;
     }
   }
   return a.g_head ? linear_sum_decay(a, w.dg, s) : e;

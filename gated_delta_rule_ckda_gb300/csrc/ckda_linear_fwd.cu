@@ -87,6 +87,7 @@ linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ 
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(sm + kBars + 404);
   const uint32_t sb = smem_u32(sm);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (!a.clear) after_previous();
   // (a wait gives up after a second: no other CTA has anything to report yet)
   if (a.clear && blockIdx.x == 0 && tid == 0) *a.status = 0;
   if (sb & 1023u) {  // swizzled tiles need it; no room to align by hand
@@ -412,11 +413,12 @@ cudaError_t linear_chunk_fwd(LinearArgs a, char* ws, cudaStream_t s) {
                   !linear_map(&mo, a.o, (uint64_t)a.B * a.H, a.T, a.dv)))
     return cudaErrorInvalidValue;
   Split sp = linear_split(a.N, a.B, a.H, a.T, a.cu_seqlens != nullptr);
-  if (a.clear && (a.cu_seqlens || sp.per > 1)) {  // more kernels than one
+  if (a.clear && !a.cu_seqlens && sp.per > 1) {  // more kernels than one
     if (cudaMemsetAsync(a.status, 0, sizeof(int), s) != cudaSuccess) return cudaErrorUnknown;
     a.clear = 0;
   }
   cudaError_t e = linear_split_plan(a, sp, ws, s);
+  if (a.cu_seqlens) a.clear = 0;  // the plan's kernel has done it
   if (e == cudaSuccess) e = linear_segment_states(a, sp, ws, false, 0, s);
   if (e != cudaSuccess) return e;
   const bool half = a.dk <= 64;
@@ -424,11 +426,10 @@ cudaError_t linear_chunk_fwd(LinearArgs a, char* ws, cudaStream_t s) {
            : allow_smem<linear_fwd_kernel<128>>(Layout<128>::kSmem);
   if (e != cudaSuccess) return e;
   const unsigned blocks = (unsigned)sp.items * a.H;
-  if (half)
-    linear_fwd_kernel<64><<<blocks, kThreads, Layout<64>::kSmem, s>>>(a, sp, mq, mk, mv, mo);
-  else
-    linear_fwd_kernel<128><<<blocks, kThreads, Layout<128>::kSmem, s>>>(a, sp, mq, mk, mv, mo);
-  return cudaGetLastError();
+  return half ? launch_next(!a.clear, linear_fwd_kernel<64>, blocks, kThreads, Layout<64>::kSmem, s,
+                            a, sp, mq, mk, mv, mo)
+              : launch_next(!a.clear, linear_fwd_kernel<128>, blocks, kThreads,
+                            Layout<128>::kSmem, s, a, sp, mq, mk, mv, mo);
 }
 
 }  // namespace ckda

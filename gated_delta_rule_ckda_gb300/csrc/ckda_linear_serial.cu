@@ -23,6 +23,8 @@ constexpr int kSplit = 4;    // threads of a row
 constexpr int kThreads = kOwn * kSplit;
 
 __global__ void slot_plan_kernel(LinearArgs a, int32_t* slot0) {
+  after_previous();
+  let_next_start();
   // one block; each thread adds up a run of sequences, then the runs are joined
   __shared__ int32_t sum[1024];
   const int per = (a.N + 1023) / 1024, i0 = threadIdx.x * per, i1 = min(i0 + per, a.N);
@@ -174,6 +176,8 @@ __global__ void __launch_bounds__(kThreads) run_kernel(LinearArgs a) {
 // other products; CV: value channels / 16.
 template <typename IO, int CV>
 __global__ void __launch_bounds__(kPieceThreads) piece_sum_kernel(LinearArgs a, Pieces p) {
+  after_previous();
+  let_next_start();
   const int sv = row_floats(a.dv);
   extern __shared__ __align__(16) float sm[];
   float *sx = sm, *sy = sx + kTok * sv, *sg = sy + kTok * kPS, *sw = sg + kTok;
@@ -222,6 +226,8 @@ __global__ void __launch_bounds__(kPieceThreads) piece_sum_kernel(LinearArgs a, 
 // Joins the pieces, in place: H[p + 1] = e^{g over p} H[p] + its own, from h0, and
 // G[p] = e^{g over p} G[p + 1] + its own, from dhT (back).
 __global__ void __launch_bounds__(256) piece_scan_kernel(LinearArgs a, Pieces p) {
+  after_previous();
+  let_next_start();
   const bool back = blockIdx.z == 1;
   const int n = blockIdx.x / a.H, h = blockIdx.x % a.H;
   int t0, len;
@@ -266,6 +272,8 @@ size_t out_smem(int CK, int slabs, int dv) {
 }
 template <typename IO, int CK, int CV>
 __global__ void __launch_bounds__(kPieceThreads, 2) piece_out_kernel(LinearArgs a, Pieces p) {
+  after_previous();
+  let_next_start();
   extern __shared__ __align__(16) float sm[];
   Where u;
   if (!where(a, p, blockIdx.x, u) || u.piece >= u.pieces) return;
@@ -346,8 +354,8 @@ cudaError_t sum_pieces(const LinearArgs& a, const Pieces& p, int directions, cud
     const cudaError_t e = allow_smem<piece_sum_kernel<IO, CV>>(sum_smem(16 * CV));
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(p.slots * a.H), (a.dk + 63) / 64, directions);
-    piece_sum_kernel<IO, CV><<<grid, kPieceThreads, sum_smem(a.dv), s>>>(a, p);
-    return cudaGetLastError();
+    return launch_next(a.cu_seqlens, piece_sum_kernel<IO, CV>, grid, kPieceThreads, sum_smem(a.dv),
+                       s, a, p);
   });
 }
 
@@ -396,8 +404,8 @@ cudaError_t serial_fwd_io(const LinearArgs& a, char* ws, cudaStream_t s) {
       const cudaError_t e =
           allow_smem<piece_out_kernel<IO, CK, CV>>(out_smem(CK, kMostSlabs<CK>, 16 * CV));
       if (e != cudaSuccess) return e;
-      piece_out_kernel<IO, CK, CV><<<(unsigned)(p.slots * a.H), kPieceThreads, smem, s>>>(a, p);
-      return cudaGetLastError();
+      return launch_next(true, piece_out_kernel<IO, CK, CV>, (unsigned)(p.slots * a.H),
+                         kPieceThreads, smem, s, a, p);
     });
   });
 }
@@ -415,8 +423,7 @@ cudaError_t linear_join_pieces(const LinearArgs& a, const Pieces& p, int directi
                                          : sum_pieces<__nv_bfloat16>(a, p, directions, s);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)a.N * a.H, (a.dk * a.dv + 255) / 256, directions);
-  piece_scan_kernel<<<grid, 256, 0, s>>>(a, p);
-  return cudaGetLastError();
+  return launch_next(true, piece_scan_kernel, grid, 256, 0, s, a, p);
 }
 
 size_t linear_serial_fwd_bytes(int N, int H, int T, int dk, int dv, bool packed) {

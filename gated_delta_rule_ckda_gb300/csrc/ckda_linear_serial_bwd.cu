@@ -9,7 +9,7 @@
 //     dq_i = scale e_i H do_i + sum_{j <= i} B_ij k_j
 //     dk_j = w_j G v_j + sum_{i >= j} B_ij q_i
 //     dv_j = w_j G^T k_j + sum_{i >= j} A_ij do_i
-// 2 x 6 heads of 48 and 80 channels, three to a key head, 1001 tokens in fp32: 74 us, of
+// 2 x 6 heads of 48 and 80 channels, three to a key head, 1001 tokens in fp32: 69 us, of
 // which 15 are the pieces' own states, 10 their scan and 43 this (token by token, in
 // three runs bound by a token's latency, 131 us).  4 x 16 x 2048, 128 channels: 1308 us.
 //
@@ -43,7 +43,7 @@ struct SerialWs {
 //
 // 64 tokens of 48 and 80 channels are 1.6 M fmas a piece.  Issue bounds it, of fmas and
 // of shared-memory reads about equally, and with few pieces the fetch of its code.
-// Paired fmas with their sums in two halves were slower (82 us for 74: registers).
+// Paired fmas with their sums in two halves were slower (82 us for 74 then: registers).
 size_t grad_smem(int CK, int slabs, int dv) {
   return (size_t)(2 * kTok * (16 * CK * slabs + 4) + (2 * kTok + 16 * CK) * row_floats(dv) +
                   kTok * kPS + 5 * kTok + 8) * sizeof(float);
@@ -52,6 +52,8 @@ size_t grad_smem(int CK, int slabs, int dv) {
 template <typename IO, int CK, int CV>
 __global__ void __launch_bounds__(kPieceThreads, 2) piece_grad_kernel(LinearArgs a, SerialWs w,
                                                                      float* dg) {
+  after_previous();
+  let_next_start();
   extern __shared__ __align__(16) float sm[];
   Where u;
   if (!where(a, w.p, blockIdx.x, u) || u.piece >= u.pieces) return;
@@ -232,6 +234,8 @@ __global__ void __launch_bounds__(kPieceThreads, 2) piece_grad_kernel(LinearArgs
 // One thread per element of dq and dk: the sums over the heads that share them.
 template <typename IO>
 __global__ void sum_heads_kernel(LinearArgs a, const float* dq, const float* dk) {
+  after_previous();
+  let_next_start();
   const size_t per = (size_t)a.T * a.dk;         // elements of one head
   const size_t total = (size_t)a.B * a.Hk * per;
   const int group = a.H / a.Hk;
@@ -252,6 +256,8 @@ __global__ void sum_heads_kernel(LinearArgs a, const float* dq, const float* dk)
 // One block a head: B * T values, each thread a strided run in double (the sum
 // is long), joined in a fixed order.
 __global__ void __launch_bounds__(1024) sum_decay_kernel(LinearArgs a, const float* dg) {
+  after_previous();
+  let_next_start();
   __shared__ double red[1024];
   const int h = blockIdx.x;
   double s = 0.0;
@@ -291,9 +297,8 @@ cudaError_t launch_grad(const LinearArgs& a, const SerialWs& w, cudaStream_t s) 
   const size_t smem = grad_smem(CK, (a.dk + 16 * CK - 1) / (16 * CK), a.dv);
   const cudaError_t e = allow_smem<piece_grad_kernel<IO, CK, CV>>(grad_smem(CK, kMostSlabs<CK>, 16 * CV));
   if (e != cudaSuccess) return e;
-  piece_grad_kernel<IO, CK, CV><<<(unsigned)(w.p.slots * a.H), kPieceThreads, smem, s>>>(
-      a, w, a.g_head ? w.dg : a.dg);
-  return cudaGetLastError();
+  return launch_next(true, piece_grad_kernel<IO, CK, CV>, (unsigned)(w.p.slots * a.H),
+                     kPieceThreads, smem, s, a, w, a.g_head ? w.dg : a.dg);
 }
 template <typename IO>
 cudaError_t grad(const LinearArgs& a, const SerialWs& w, cudaStream_t s) {
@@ -308,8 +313,7 @@ template <typename IO>
 cudaError_t sum_heads(const LinearArgs& a, const SerialWs& w, cudaStream_t s) {
   const size_t total = (size_t)a.B * a.Hk * a.T * a.dk, blocks = (total + 255) / 256;
   const unsigned grid = (unsigned)(blocks < 32 * kLinSms ? blocks : 32 * kLinSms);
-  sum_heads_kernel<IO><<<grid, 256, 0, s>>>(a, w.dq, w.dk);
-  return cudaGetLastError();
+  return launch_next(true, sum_heads_kernel<IO>, grid, 256, 0, s, a, w.dq, w.dk);
 }
 
 template <typename IO>
@@ -351,8 +355,7 @@ cudaError_t linear_serial_bwd(const LinearArgs& a, char* ws, cudaStream_t s) {
 }
 
 cudaError_t linear_sum_decay(const LinearArgs& a, const float* dg_full, cudaStream_t s) {
-  sum_decay_kernel<<<a.H, 1024, 0, s>>>(a, dg_full);
-  return cudaGetLastError();
+  return launch_next(true, sum_decay_kernel, a.H, 1024, 0, s, a, dg_full);
 }
 
 }  // namespace ckda

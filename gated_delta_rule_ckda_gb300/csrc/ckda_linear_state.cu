@@ -48,6 +48,10 @@ linear_state_kernel(const __grid_constant__ LinearArgs a, const __grid_constant_
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(sm + kBars + 404);
   const uint32_t sb = smem_u32(sm);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (!IMAGES) {
+    after_previous();
+    let_next_start();
+  }
   if (sb & 1023u) {
     if (tid == 0) set_status(a.status, CKDA_ERR_CUDA);
     return;
@@ -247,6 +251,9 @@ __global__ void __launch_bounds__(1024) split_plan_kernel(LinearArgs a, int per,
                                                           int most_cuts, int32_t* item0,
                                                           int4* table, int2* cuts) {
   __shared__ int32_t sum[1024], cut[1024];
+  after_previous();
+  let_next_start();
+  if (a.clear && threadIdx.x == 0) *a.status = 0;
   const int share = (a.N + 1023) / 1024, i0 = threadIdx.x * share, i1 = min(i0 + share, a.N);
   auto segments = [&](int i) {
     int t0, len;
@@ -290,6 +297,8 @@ __global__ void __launch_bounds__(1024) split_plan_kernel(LinearArgs a, int per,
 // state before it.  A thread takes one element of one (sequence, head), and loads
 // eight segments' ahead.
 __global__ void __launch_bounds__(256) segment_scan_kernel(LinearArgs a, Split sp, int back) {
+  after_previous();
+  let_next_start();
   const int at = blockIdx.x / a.H, h = blockIdx.x % a.H;
   if (sp.item0 && at >= sp.item0[a.N + 1]) return;
   const int rank = sp.item0 ? sp.cuts[at].x : at;
@@ -327,10 +336,10 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 // Dense: segments of a sequence, the count with the least time by this model, in
 // chunks: rounds of CTAs over the SMs times a segment's chunks, plus the states'
 // pass over all segments but one at 0.6 of that, and 6 for the two more launches.
-// (One sequence of 16 heads and 32,768 tokens: 9 segments, 783 -> 187 us.)
+// (One sequence of 16 heads and 32,768 tokens: 9 segments, 783 -> 182 us.)
 // Packed: sequences longer than 5/4 of an SM's share of all tokens are cut (24 of
 // 50,021 tokens, 16 heads of 64 and 128 channels: 215 us with passes over every
-// sequence and a search for each CTA's, 194 us with the tables).
+// sequence and a search for each CTA's, 164 us with the tables).
 Split linear_split(int N, int B, int H, int T, bool packed) {
   Split sp{};
   const long long chunks = (T + C - 1) / C;
@@ -384,8 +393,8 @@ cudaError_t linear_split_plan(const LinearArgs& a, Split& sp, char* ws, cudaStre
   sp.item0 = item0;
   sp.table = table;
   sp.cuts = cuts;
-  split_plan_kernel<<<1, 1024, 0, s>>>(a, sp.per, sp.items, sp.most_cuts, item0, table, cuts);
-  return cudaGetLastError();
+  return launch_next(true, split_plan_kernel, 1, 1024, 0, s, a, sp.per, sp.items, sp.most_cuts,
+                     item0, table, cuts);
 }
 
 template <bool BACK, bool IMAGES, int KP>
@@ -400,9 +409,10 @@ static cudaError_t launch_states_of(const LinearArgs& a, const Split& sp, const 
   if (e != cudaSuccess) return e;
   const unsigned blocks =
       (unsigned)(!IMAGES && a.cu_seqlens ? sp.most_cuts : sp.items) * a.H;
-  linear_state_kernel<BACK, IMAGES, KP>
-      <<<blocks, st::kThreads, st::kSmem, s>>>(a, sp, out, mx, my);
-  return cudaGetLastError();
+  // (early, the kernels that fill the SMs for long cost the one before them more than
+  // they save: backward of 8 x 16 x 2048 268 us, and 272 with states and gradients early)
+  return launch_next(!IMAGES && (BACK || a.cu_seqlens), linear_state_kernel<BACK, IMAGES, KP>, blocks,
+                     st::kThreads, st::kSmem, s, a, sp, out, mx, my);
 }
 
 template <bool BACK, bool IMAGES>
@@ -428,9 +438,8 @@ cudaError_t linear_segment_states(const LinearArgs& a, Split& sp, char* ws, bool
                        : launch_states<false, false>(a, sp, ChunkImages{}, s);
   if (e != cudaSuccess) return e;
   const unsigned cut = a.cu_seqlens ? sp.most_cuts : a.N;  // sequences, at most
-  segment_scan_kernel<<<dim3(cut * a.H, (a.dk * a.dv + 255) / 256), 256, 0, s>>>(
-      a, sp, back ? 1 : 0);
-  return cudaGetLastError();
+  return launch_next(true, segment_scan_kernel, dim3(cut * a.H, (a.dk * a.dv + 255) / 256), 256, 0,
+                     s, a, sp, back ? 1 : 0);
 }
 
 cudaError_t linear_chunk_states(const LinearArgs& a, const Split& sp, const ChunkImages& out,
