@@ -334,9 +334,14 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 }  // namespace
 
 // Dense: segments of a sequence, the count with the least time by this model, in
-// chunks: rounds of CTAs over the SMs times a segment's chunks, plus the states'
-// pass over all segments but one at 0.6 of that, and 6 for the two more launches.
-// (One sequence of 16 heads and 32,768 tokens: 9 segments, 783 -> 182 us.)
+// chunks (3.1 us): rounds of CTAs over the SMs times a segment's chunks and 1.8 for a
+// CTA's start and end, the same at 0.6 of the chunks for the states' pass over all
+// segments but one, and 7 for the two more launches and the scan.  Measured, us, the
+// forward at 128 x 128 uncut, as the model has it, and as counts around it:
+//   16 heads, 32,768 tokens   797   9 segments 175   (7: 210, 14: 224, 19: 185)
+//   32 heads, 16,384 tokens   403   4 segments 189   (3: 242, 7: 224, 9: 188)
+//   64 heads, 8,192 tokens    207   2 segments 196   (3: 215, 4: 208, 7: 200)
+//   80 heads, 8,192 tokens    207   uncut            (2: 301, 3: 264, 7: 258)
 // Packed: sequences longer than 5/4 of an SM's share of all tokens are cut (24 of
 // 50,021 tokens, 16 heads of 64 and 128 channels: 215 us with passes over every
 // sequence and a search for each CTA's, 164 us with the tables).
@@ -357,7 +362,8 @@ Split linear_split(int N, int B, int H, int T, bool packed) {
     const double each = (double)((chunks + s - 1) / s);
     const double rounds = (double)((units * s + kLinSms - 1) / kLinSms);
     const double before = (double)((units * (s - 1) + kLinSms - 1) / kLinSms);
-    const double cost = rounds * each + (s > 1 ? 0.6 * before * each + 6 : 0);
+    const double cost =
+        rounds * (each + 1.8) + (s > 1 ? before * (0.6 * each + 1.8) + 7 : 0);
     if (s == 1 || cost < best) {
       best = cost;
       sp.per = s;
