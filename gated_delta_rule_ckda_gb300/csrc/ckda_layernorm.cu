@@ -516,11 +516,10 @@ inline int blocks_for(long long units, int per_sm) {
   return (int)(units < most ? (units < 1 ? 1 : units) : most);
 }
 // Partial rows of the weight gradients, at most: a block each.
-constexpr int kMostPerSm = 4;
-inline int weight_parts(long long rows) { return blocks_for(rows, kMostPerSm); }
+inline int weight_parts(long long rows, int D) { return blocks_for(rows, D <= 2048 ? 8 : 2); }
 
 template <typename IO, typename W, int VEC, int TB, int LPR, int NV, int S>
-cudaError_t run_fwd(const NormArgs& a, cudaStream_t s) {
+cudaError_t run_fwd(const NormArgs& a, int per_sm, cudaStream_t s) {
   constexpr size_t smem = RowRing<IO, VEC, TB, LPR, NV, S, 1>::kSmem;
   const auto kernel = norm_fwd_kernel<IO, W, VEC, TB, LPR, NV, S>;
   if (smem > 40 * 1024) {  // (the static part counts towards the default 48 KB)
@@ -529,8 +528,7 @@ cudaError_t run_fwd(const NormArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
   }
   constexpr int kGroups = TB / LPR;
-  kernel<<<blocks_for((a.rows + kGroups - 1) / kGroups, LPR <= 32 ? 8 : 4), TB, smem,
-           s>>>(a);
+  kernel<<<blocks_for((a.rows + kGroups - 1) / kGroups, per_sm), TB, smem, s>>>(a);
   return cudaGetLastError();
 }
 template <typename IO, typename W, int VEC, int TB, int LPR, int NV, int S>
@@ -550,23 +548,30 @@ cudaError_t run_bwd(NormArgs& a, int per_sm, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// Threads of a row by its width: the fewest lanes that hold it in one or two
-// vectors each (rows of 128 by 16 lanes 94 us, by 32 half of which idle 194 us);
-// wide rows a block.  The ring is as deep as keeps 40 KB or more of an SM in flight.
+// Threads of a row by its width: the fewest lanes that hold it in one or two vectors
+// each, a warp at most (rows of 128 by 16 lanes 94 us, by 32 half of which idle 194 us);
+// wider rows a block, of 128 threads first (rows of 768 to 2048 by 256 threads took
+// 246 to 116 us for 2^27 elements, by 128 it is 124 to 89).  The ring is as deep as
+// keeps 40 KB or more of an SM in flight.
+//
 // Backward, blocks an SM: a row of 4096 takes 141 us with its two numbers loaded at
 // their use, then 100 with three blocks, 97 with four and 84 with two, whose rows
-// come to the memory in longer runs; a row by 512 threads takes 109.
+// come to the memory in longer runs; a row by 512 threads takes 109.  Rows of 1024 by
+// blocks of 128 threads: 392 us with two, 227 with four, 179 with six, 160 with eight.
+// The widest rows in registers (8192 in fp32, 16384 in bf16): one block of 1024
+// threads, 325 and 313 us; read again for each sum 634 and 627.
 template <typename IO, typename W, int VEC>
 cudaError_t fwd_vec(const NormArgs& a, cudaStream_t s) {
   const int D = a.D;
-  if (D <= 8 * VEC) return run_fwd<IO, W, VEC, 256, 8, 1, 4>(a, s);
-  if (D <= 16 * VEC) return run_fwd<IO, W, VEC, 256, 16, 1, 4>(a, s);
-  if (D <= 32 * VEC) return run_fwd<IO, W, VEC, 256, 32, 1, 4>(a, s);
-  if (D <= 64 * VEC) return run_fwd<IO, W, VEC, 256, 32, 2, 3>(a, s);
-  if (D <= 256 * VEC) return run_fwd<IO, W, VEC, 256, 256, 1, 4>(a, s);
-  if (D <= 512 * VEC) return run_fwd<IO, W, VEC, 256, 256, 2, 4>(a, s);
-  if (D <= 1024 * VEC) return run_fwd<IO, W, VEC, 512, 512, 2, 4>(a, s);
-  if (D <= 2048 * VEC) return run_fwd<IO, W, VEC, 512, 512, 4, 2>(a, s);
+  if (D <= 8 * VEC) return run_fwd<IO, W, VEC, 256, 8, 1, 4>(a, 8, s);
+  if (D <= 16 * VEC) return run_fwd<IO, W, VEC, 256, 16, 1, 4>(a, 8, s);
+  if (D <= 32 * VEC) return run_fwd<IO, W, VEC, 256, 32, 1, 4>(a, 8, s);
+  if (D <= 64 * VEC) return run_fwd<IO, W, VEC, 256, 32, 2, 3>(a, 8, s);
+  if (D <= 128 * VEC) return run_fwd<IO, W, VEC, 128, 128, 1, 4>(a, 16, s);
+  if (D <= 256 * VEC) return run_fwd<IO, W, VEC, 128, 128, 2, 4>(a, 12, s);
+  if (D <= 512 * VEC) return run_fwd<IO, W, VEC, 256, 256, 2, 4>(a, 4, s);
+  if (D <= 1024 * VEC) return run_fwd<IO, W, VEC, 512, 512, 2, 4>(a, 4, s);
+  if (D <= 2048 * VEC) return run_fwd<IO, W, VEC, 512, 512, 4, 2>(a, 4, s);
   norm_fwd_long_kernel<IO, W><<<blocks_for(a.rows, 2), 1024, 0, s>>>(a);
   return cudaGetLastError();
 }
@@ -578,9 +583,12 @@ cudaError_t bwd_vec(NormArgs& a, cudaStream_t s) {
   if (D <= 16 * VEC) return run_bwd<IO, W, VEC, 256, 16, 1, 4>(a, 4, s);
   if (D <= 32 * VEC) return run_bwd<IO, W, VEC, 256, 32, 1, 4>(a, 4, s);
   if (D <= 64 * VEC) return run_bwd<IO, W, VEC, 256, 32, 2, 3>(a, 4, s);
-  if (D <= 256 * VEC) return run_bwd<IO, W, VEC, 256, 256, 1, 4>(a, 3, s);
+  if (D <= 128 * VEC) return run_bwd<IO, W, VEC, 128, 128, 1, 4>(a, 8, s);
+  if (D <= 256 * VEC) return run_bwd<IO, W, VEC, 128, 128, 2, 3>(a, 4, s);
   if (D <= 512 * VEC) return run_bwd<IO, W, VEC, 256, 256, 2, 4>(a, 2, s);
   if (D <= 1024 * VEC) return run_bwd<IO, W, VEC, 512, 512, 2, 3>(a, 2, s);
+  if constexpr (VEC > 1)
+    if (D <= 2048 * VEC) return run_bwd<IO, W, VEC, 1024, 1024, 2, 2>(a, 1, s);
   // (single elements: odd widths, four a thread)
   if (VEC == 1 && D <= 2048) return run_bwd<IO, W, VEC, 512, 512, VEC == 1 ? 4 : 2, 3>(a, 2, s);
   a.parts = blocks_for(a.rows, 2);
@@ -648,7 +656,7 @@ ckda_status ckda_layernorm_fwd(const void* x, const void* weight, const void* bi
 
 size_t ckda_layernorm_bwd_workspace_bytes(long long rows, int width) {
   if (rows < 0 || width < 1) return 0;
-  return (size_t)2 * weight_parts(rows) * width * sizeof(float);
+  return (size_t)2 * weight_parts(rows, width) * width * sizeof(float);
 }
 
 ckda_status ckda_layernorm_bwd(const void* dy, const void* x, const float* mean,
@@ -672,7 +680,7 @@ ckda_status ckda_layernorm_bwd(const void* dy, const void* x, const float* mean,
   a.part = dweight ? static_cast<float*>(workspace) : nullptr;
   a.dw = dweight; a.db = dbias;
   a.rows = rows; a.D = width;
-  a.parts = weight_parts(rows);
+  a.parts = weight_parts(rows, width);
   return launch_any(a, io_dtype, weight_dtype, true, static_cast<cudaStream_t>(stream)) ==
                  cudaSuccess
              ? CKDA_OK

@@ -13,6 +13,9 @@
 // the SMs (each warp still reads whole 128-byte lines).  256 x 32 pairs of 128 x 128:
 // 160 us, 99% of the copy bandwidth, and 194 us with 32 columns; 16 pairs, from the
 // call to its result: 22.6 us with 32 columns, 23.7 us with 128, most of it the host's.
+// Narrower states take as many lanes as they have columns, and half the rows: 1024 x 32
+// pairs of 64 x 64 in 175 us, 317 us in blocks for 128 x 128, half of them idle.
+#include <type_traits>
 #include "ckda_linear.cuh"
 
 namespace ckda {
@@ -31,10 +34,11 @@ struct StepArgs {
   float scale;
 };
 
-template <typename IO, int VEC, int LANES>
+// DK: 64 or 128, at least dk.
+template <typename IO, int VEC, int LANES, int DK>
 __global__ void __launch_bounds__(kThreads) linear_step_kernel(StepArgs a) {
   constexpr int kGroups = kThreads / LANES;
-  constexpr int kRows = (128 + kGroups - 1) / kGroups;
+  constexpr int kRows = (DK + kGroups - 1) / kGroups;
   __shared__ float sk[128], sq[128];
   __shared__ float red[kGroups][LANES * VEC];
   const size_t unit = blockIdx.x;
@@ -99,13 +103,21 @@ template <typename IO>
 cudaError_t launch_step(const StepArgs& a, int B, cudaStream_t s) {
   const unsigned units = (unsigned)B * a.H;
   const bool vec = a.dv % 4 == 0 && (reinterpret_cast<uintptr_t>(a.state) & 15) == 0;
-  if (!vec)
-    linear_step_kernel<IO, 1, 32><<<dim3(units, (a.dv + 31) / 32), kThreads, 0, s>>>(a);
-  else if (units >= 2 * kLinSms && a.dv > 32)
-    linear_step_kernel<IO, 4, 32><<<units, kThreads, 0, s>>>(a);
-  else
-    linear_step_kernel<IO, 4, 8><<<dim3(units, (a.dv + 31) / 32), kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  const auto step = [&](auto dk) {
+    constexpr int DK = decltype(dk)::value;
+    const bool many = units >= 2 * kLinSms;
+    const dim3 by32(units, (a.dv + 31) / 32);
+    if (!vec)
+      linear_step_kernel<IO, 1, 32, DK><<<by32, kThreads, 0, s>>>(a);
+    else if (many && a.dv > 64)
+      linear_step_kernel<IO, 4, 32, DK><<<units, kThreads, 0, s>>>(a);
+    else if (many && a.dv > 32)
+      linear_step_kernel<IO, 4, 16, DK><<<units, kThreads, 0, s>>>(a);
+    else
+      linear_step_kernel<IO, 4, 8, DK><<<by32, kThreads, 0, s>>>(a);
+    return cudaGetLastError();
+  };
+  return a.dk <= 64 ? step(std::integral_constant<int, 64>()) : step(std::integral_constant<int, 128>());
 }
 
 }  // namespace

@@ -171,3 +171,10 @@ def test_autograd_and_graph(ck):
     torch.cuda.synchronize()
     for a, r in zip(got, ck.layernorm_bwd(dy, x, m[1], m[2], w)):
         assert torch.equal(a, r)
+
+
+@pytest.mark.parametrize("dt,width", [(BF, 768), (BF, 1000), (BF, 1536), (BF, 12288), (BF, 16384), (F32, 400),
+                                      (F32, 900), (F32, 5120), (F32, 8192)])
+def test_more_rows_than_blocks(ck, dt, width):
+    """Rows by a block each, several to a block: the ring comes round."""
+    compare(ck, *make(2500 if width < 5000 else 700, width, dt, F32, width))
