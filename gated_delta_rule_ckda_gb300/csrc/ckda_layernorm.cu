@@ -516,7 +516,7 @@ inline int blocks_for(long long units, int per_sm) {
   return (int)(units < most ? (units < 1 ? 1 : units) : most);
 }
 // Partial rows of the weight gradients, at most: a block each.
-inline int weight_parts(long long rows, int D) { return blocks_for(rows, D <= 2048 ? 8 : 2); }
+inline int weight_parts(long long rows, int D) { return blocks_for(rows, D <= 2048 ? 8 : 3); }
 
 template <typename IO, typename W, int VEC, int TB, int LPR, int NV, int S>
 cudaError_t run_fwd(const NormArgs& a, int per_sm, cudaStream_t s) {
@@ -551,8 +551,10 @@ cudaError_t run_bwd(NormArgs& a, int per_sm, cudaStream_t s) {
 // Threads of a row by its width: the fewest lanes that hold it in one or two vectors
 // each, a warp at most (rows of 128 by 16 lanes 94 us, by 32 half of which idle 194 us);
 // wider rows a block, of 128 threads first (rows of 768 to 2048 by 256 threads took
-// 246 to 116 us for 2^27 elements, by 128 it is 124 to 89).  The ring is as deep as
-// keeps 40 KB or more of an SM in flight.
+// 246 to 116 us for 2^27 elements, by 128 it is 124 to 89), and three vectors a thread
+// before twice the threads (2560: 97 us and 115; 5120: 106 and 128; backward 2560: 150
+// and 168, but 5120: 208 and 184).  The ring is as deep as keeps 40 KB or more of an
+// SM in flight.
 //
 // Backward, blocks an SM: a row of 4096 takes 141 us with its two numbers loaded at
 // their use, then 100 with three blocks, 97 with four and 84 with two, whose rows
@@ -569,7 +571,9 @@ cudaError_t fwd_vec(const NormArgs& a, cudaStream_t s) {
   if (D <= 64 * VEC) return run_fwd<IO, W, VEC, 256, 32, 2, 3>(a, 8, s);
   if (D <= 128 * VEC) return run_fwd<IO, W, VEC, 128, 128, 1, 4>(a, 16, s);
   if (D <= 256 * VEC) return run_fwd<IO, W, VEC, 128, 128, 2, 4>(a, 12, s);
+  if (D <= 384 * VEC) return run_fwd<IO, W, VEC, 128, 128, 3, 3>(a, 8, s);
   if (D <= 512 * VEC) return run_fwd<IO, W, VEC, 256, 256, 2, 4>(a, 4, s);
+  if (D <= 768 * VEC) return run_fwd<IO, W, VEC, 256, 256, 3, 3>(a, 4, s);
   if (D <= 1024 * VEC) return run_fwd<IO, W, VEC, 512, 512, 2, 4>(a, 4, s);
   if (D <= 2048 * VEC) return run_fwd<IO, W, VEC, 512, 512, 4, 2>(a, 4, s);
   norm_fwd_long_kernel<IO, W><<<blocks_for(a.rows, 2), 1024, 0, s>>>(a);
@@ -585,6 +589,7 @@ cudaError_t bwd_vec(NormArgs& a, cudaStream_t s) {
   if (D <= 64 * VEC) return run_bwd<IO, W, VEC, 256, 32, 2, 3>(a, 4, s);
   if (D <= 128 * VEC) return run_bwd<IO, W, VEC, 128, 128, 1, 4>(a, 8, s);
   if (D <= 256 * VEC) return run_bwd<IO, W, VEC, 128, 128, 2, 3>(a, 4, s);
+  if (D <= 384 * VEC) return run_bwd<IO, W, VEC, 128, 128, 3, 3>(a, 3, s);
   if (D <= 512 * VEC) return run_bwd<IO, W, VEC, 256, 256, 2, 4>(a, 2, s);
   if (D <= 1024 * VEC) return run_bwd<IO, W, VEC, 512, 512, 2, 3>(a, 2, s);
   if constexpr (VEC > 1)

@@ -173,7 +173,7 @@ def test_autograd_and_graph(ck):
         assert torch.equal(a, r)
 
 
-@pytest.mark.parametrize("dt,width", [(BF, 768), (BF, 1000), (BF, 1536), (BF, 12288), (BF, 16384), (F32, 400),
+@pytest.mark.parametrize("dt,width", [(BF, 768), (BF, 1000), (BF, 1536), (BF, 2560), (BF, 5120), (BF, 12288), (BF, 16384), (F32, 400),
                                       (F32, 900), (F32, 5120), (F32, 8192)])
 def test_more_rows_than_blocks(ck, dt, width):
     """Rows by a block each, several to a block: the ring comes round."""
