@@ -56,6 +56,8 @@ def library_path() -> str:
 def lib():
     """The loaded libckda (ctypes.CDLL).  Raises if the library is not built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(_LIB_PATH):
@@ -616,7 +618,7 @@ def _call(fn, where, device, stream, *args):
     """fn(*args, stream) on the tensors' device; raises CkdaError."""
     handle = (torch._C._cuda_getCurrentRawStream(device.index) if stream is None
               else stream.cuda_stream)
-    if device.index == torch.cuda.current_device():
+    if device.index == torch._C._cuda_getDevice():
         rc = fn(*args, handle)
     else:
         with torch.cuda.device(device):
@@ -778,7 +780,8 @@ def layernorm_fwd(x, weight=None, bias=None, eps=1e-5, y=None, mean=None, rstd=N
     if x.dim() < 1:
         raise ValueError("x has no last axis")
     lead, width = x.shape[:-1], x.shape[-1]
-    _check(x, "x", x.dtype, x.shape, device)
+    if not x.is_contiguous():
+        raise ValueError("x: must be contiguous")
     wcode = _check_weight(weight, bias, width, device)
     if y is None:
         y = torch.empty_like(x)
@@ -809,7 +812,8 @@ def layernorm_bwd(dy, x, mean, rstd, weight=None, weight_grad=True, dx=None, wor
     if x.dim() < 1:
         raise ValueError("x has no last axis")
     lead, width = x.shape[:-1], x.shape[-1]
-    _check(x, "x", x.dtype, x.shape, device)
+    if not x.is_contiguous():
+        raise ValueError("x: must be contiguous")
     _check(dy, "dy", x.dtype, x.shape, device)
     _check(mean, "mean", torch.float32, lead, device)
     _check(rstd, "rstd", torch.float32, lead, device)

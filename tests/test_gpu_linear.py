@@ -358,3 +358,50 @@ def test_values_that_are_not_finite_keep_to_their_tokens(ck):
         if i != 1:  # q, v: keys behind
             assert torch.isfinite(dk[:, :, at + 1:]).all()
         assert torch.isfinite(dv[:, :, at + 1:]).all()
+
+
+CHAINS = [("cut", BF, 2, 2, 1500, 64, None), ("packed", BF, 4, 2, 1700, 128, [0, 3, 3, 1500, 1700]),
+          ("shared", BF, 4, 1, 260, 64, None), ("pieces", F32, 4, 2, 500, 40, None),
+          ("packed pieces", F32, 2, 2, 500, 24, [0, 0, 130, 131, 500])]
+
+
+@pytest.mark.parametrize("name,dt,H,Hk,T,d,cu", CHAINS, ids=[c[0] for c in CHAINS])
+def test_calls_of_several_kernels(ck, name, dt, H, Hk, T, d, cu):
+    """Kernels of a call may start under the one before: calls back to back on one
+    workspace, and replayed from a graph, give the bits of calls apart."""
+    N = 1 if cu is None else len(cu) - 1
+    cud = None if cu is None else torch.tensor(cu, dtype=torch.int32, device="cuda")
+    inputs, apart = [], []
+    nseq = 0 if cu is None else N
+    per_head = -torch.rand(H, device="cuda") * 0.1
+
+    def run(x, e, wf=None, wb=None):
+        return [*ck.linear_fwd(**x, cu_seqlens=cud, workspace=wf),
+                *ck.linear_bwd(x["q"], x["k"], x["v"], x["g"], e["do"], h0=x["h0"], dhT=e["dhT"],
+                               cu_seqlens=cud, workspace=wb)]
+
+    for seed in range(4):
+        x, e = make(1, H, Hk, T, d, d, dt, seed, N=N)
+        x, e = gpu(x), gpu(e)
+        if seed % 2:
+            x["g"] = per_head
+        inputs.append((x, e))
+        apart.append(run(x, e))
+        torch.cuda.synchronize()
+    wf = torch.empty(ck.linear_fwd_workspace_bytes(1, H, T, d, d, dt, nseq), dtype=torch.uint8, device="cuda")
+    wb = torch.empty(ck.linear_bwd_workspace_bytes(1, H, Hk, T, d, d, dt, nseq), dtype=torch.uint8, device="cuda")
+    for _ in range(3):
+        together = [run(x, e, wf, wb) for x, e in inputs]
+        for a, b in zip(apart, together):
+            assert all(torch.equal(s, t) for s, t in zip(a, b))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        replayed = [run(x, e, wf, wb) for x, e in inputs]
+    for _ in range(3):
+        for outs in replayed:
+            for t in outs:
+                t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(apart, replayed):
+            assert all(torch.equal(s, t) for s, t in zip(a, b))
