@@ -6,9 +6,9 @@
 // e_i the one from the piece's start through i and w_j the one from j to its end,
 //     A_ij = scale D_ij q_i.k_j,   o_i = scale e_i H^T q_i + sum_{j <= i} A_ij v_j,
 //     (state after the piece) = e H + sum_j w_j k_j v_j^T.
-// D is a running product down its columns, so a decay that is strong or -infinity
-// somewhere leaves the others their full precision, which a difference of
-// cumulative sums would not.  Masks are taken exactly: a token's values, whatever
+// D is the exponential of a sum that runs down its column, so a decay that is strong
+// or -infinity somewhere leaves the others their full precision, which a difference
+// of cumulative sums would not (and 64 factors multiplied lose three bits).  Masks are taken exactly: a token's values, whatever
 // they are, enter no result that they do not belong to.
 #pragma once
 #include <type_traits>
@@ -191,22 +191,23 @@ __device__ __forceinline__ void add_diag(float (&acc)[4][C], const float* a, int
   }
 }
 
-// The decays of a piece of nt tokens from their a_t = e^{g_t} (ones behind them) by
-// 65 threads: D, e and w.
-__device__ __forceinline__ void piece_decays(float* D, float* e, float* w, const float* a, int nt) {
+// The decays of a piece of nt tokens from their log decays g (zeros behind them) by 65
+// threads: e, w, and the logarithms of D.
+__device__ __forceinline__ void piece_decays(float* logD, float* e, float* w, const float* g,
+                                             int nt) {
   const int tid = threadIdx.x;
   if (tid < kTok) {
-    float d = 1.f;
+    float d = 0.f;
 #pragma unroll 8
     for (int i = 0; i < kTok; ++i) {
-      d = i > tid ? d * a[i] : 1.f;
-      D[i * kPS + tid] = d;
-      if (i == nt - 1) w[tid] = tid < nt ? d : 0.f;
+      d = i > tid ? d + g[i] : 0.f;
+      logD[i * kPS + tid] = d;
+      if (i == nt - 1) w[tid] = tid < nt ? expf(d) : 0.f;
     }
   } else if (tid == kTok) {
-    float x = 1.f;
+    float x = 0.f;
 #pragma unroll 8
-    for (int i = 0; i < kTok; ++i) e[i] = x *= a[i];
+    for (int i = 0; i < kTok; ++i) e[i] = expf(x += g[i]);
   }
 }
 __device__ __forceinline__ void copies_arrived() {

@@ -189,23 +189,24 @@ __global__ void __launch_bounds__(kPieceThreads) piece_sum_kernel(LinearArgs a, 
   const int tid = threadIdx.x, nt = u.len, r0 = blockIdx.y * 64, row = 4 * (tid >> 4), c = tid & 15;
   stage_rows(sx, sv, X, a.dv, a.dv, nt, kTok, sv - 4);
   stage_rows(sy, kPS, Y + r0, a.dk, min(64, a.dk - r0), nt, kTok, 64);
-  if (tid < kTok) sg[tid] = tid < nt ? expf(a.g_head ? a.g[u.h] : a.g[u.vrow + tid]) : 1.f;
+  if (tid < kTok) sg[tid] = tid < nt ? (a.g_head ? a.g[u.h] : a.g[u.vrow + tid]) : 0.f;
   __syncthreads();
   if (tid < 32) {
-    // lane l has tokens 2 l and 2 l + 1; forward the product of what follows a
-    // token, backward of what leads to it and itself
-    const float a0 = sg[2 * tid], a1 = sg[2 * tid + 1];
-    float run = a0 * a1;  // over the lanes before (after) this one
+    // lane l has tokens 2 l and 2 l + 1; forward the decay by what follows a
+    // token, backward by what leads to it and itself
+    const float g0 = sg[2 * tid], g1 = sg[2 * tid + 1];
+    float run = g0 + g1;  // over the lanes up to (from) this one
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
       const float y = back ? __shfl_up_sync(0xffffffffu, run, m) : __shfl_down_sync(0xffffffffu, run, m);
-      if (back ? tid >= m : tid + m < 32) run *= y;
+      if (back ? tid >= m : tid + m < 32) run += y;
     }
-    if (tid == 0 && !back && blockIdx.y == 0) p.dec[u.slot * a.H + u.h] = run;
+    if (tid == 0 && !back && blockIdx.y == 0) p.dec[u.slot * a.H + u.h] = expf(run);
+    // over the others: shifted, not subtracted
     float other = back ? __shfl_up_sync(0xffffffffu, run, 1) : __shfl_down_sync(0xffffffffu, run, 1);
-    if (tid == (back ? 0 : 31)) other = 1.f;
-    sw[2 * tid] = back ? a.scale * other * a0 : other * a1;
-    sw[2 * tid + 1] = back ? a.scale * other * a0 * a1 : other;
+    if (tid == (back ? 0 : 31)) other = 0.f;
+    sw[2 * tid] = back ? a.scale * expf(other + g0) : expf(other + g1);
+    sw[2 * tid + 1] = back ? a.scale * expf(other + g0 + g1) : expf(other);
   }
   copies_arrived();
   for (int e = tid; e < kTok * 64; e += kPieceThreads) sy[e / 64 * kPS + e % 64] *= sw[e / 64];
@@ -292,7 +293,7 @@ __global__ void __launch_bounds__(kPieceThreads, 2) piece_out_kernel(LinearArgs 
   stage_rows(skey, sk, static_cast<const IO*>(a.k) + u.krow * a.dk, a.dk, a.dk, nt, kTok, cols);
   stage_rows(sval, sv, static_cast<const IO*>(a.v) + u.vrow * a.dv, a.dv, a.dv, nt, kTok, sv - 4);
   stage_slab(0);
-  if (tid < kTok) sg[tid] = tid < nt ? expf(a.g_head ? a.g[u.h] : a.g[u.vrow + tid]) : 1.f;
+  if (tid < kTok) sg[tid] = tid < nt ? (a.g_head ? a.g[u.h] : a.g[u.vrow + tid]) : 0.f;
   __syncthreads();
   piece_decays(sp, se, sw, sg, nt);
   copies_arrived();
@@ -305,7 +306,7 @@ __global__ void __launch_bounds__(kPieceThreads, 2) piece_out_kernel(LinearArgs 
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int at = (row + i) * kPS + c + 16 * j;
-        sp[at] = row + i >= c + 16 * j ? sp[at] * b[i][j] : 0.f;
+        sp[at] = row + i >= c + 16 * j ? expf(sp[at]) * b[i][j] : 0.f;
       }
   }
   float acc[4][CV] = {};

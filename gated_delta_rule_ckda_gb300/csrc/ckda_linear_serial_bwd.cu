@@ -9,7 +9,7 @@
 //     dq_i = scale e_i H do_i + sum_{j <= i} B_ij k_j
 //     dk_j = w_j G v_j + sum_{i >= j} B_ij q_i
 //     dv_j = w_j G^T k_j + sum_{i >= j} A_ij do_i
-// 2 x 6 heads of 48 and 80 channels, three to a key head, 1001 tokens in fp32: 69 us, of
+// 2 x 6 heads of 48 and 80 channels, three to a key head, 1001 tokens in fp32: 71 us, of
 // which 15 are the pieces' own states, 10 their scan and 43 this (token by token, in
 // three runs bound by a token's latency, 131 us).  4 x 16 x 2048, 128 channels: 1308 us.
 //
@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kPieceThreads, 2) piece_grad_kernel(LinearArgs
   stage_rows(skey, sk, static_cast<const IO*>(a.k) + u.krow * a.dk, a.dk, a.dk, nt, kTok, cols);
   stage_slab(H, 0);
   if (tid < kTok)
-    sg[tid] = tid < nt ? expf(a.g_head ? a.g[u.h] : a.g[u.vrow + tid]) : 1.f;
+    sg[tid] = tid < nt ? (a.g_head ? a.g[u.h] : a.g[u.vrow + tid]) : 0.f;
   __syncthreads();
   piece_decays(sp, se, sw, sg, nt);
   copies_arrived();
@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kPieceThreads, 2) piece_grad_kernel(LinearArgs
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int from = c + 16 * j, at = (row + i) * kPS + from;
-        D[i][j] = sp[at];
+        D[i][j] = expf(sp[at]);
         sp[at] = row + i > from ? a.scale * D[i][j] * b[i][j] : 0.f;
         if (row + i == from) own[from] = a.scale * b[i][j];
       }
