@@ -63,6 +63,8 @@ struct Layout {
   }
 };
 
+// A barrier is looked at by the parity of a phase: whoever waits for one has to have seen
+// it before anything that the phase after the next one waits for.
 enum {
   // B_O and B_DF by chunk parity: the loads wait on them too, and may lag a chunk
   B_FULL = 0, B_S = 6, B_P, B_PV, B_O, B_HREADY = B_O + 2, B_HFREE, B_KT, B_DF, B_G = B_DF + 2,
@@ -336,14 +338,17 @@ linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ 
             make_uint4(pack_bf162(H[8 * j], H[8 * j + 1]), pack_bf162(H[8 * j + 2], H[8 * j + 3]),
                        pack_bf162(H[8 * j + 4], H[8 * j + 5]),
                        pack_bf162(H[8 * j + 6], H[8 * j + 7]));
+      // S has read the keys.  Looked at before these warps publish: the next S waits for
+      // that, and a warp that looked after it could find S two phases on and wait for a
+      // third, which waits for its keys.
+      if (!(ok = warp_wait(bars + B_S, par, abort))) break;
       warp_publish(bars + B_HREADY);
-      // the keys, scaled, once S has read them
+      // the keys, scaled
       if (!(ok = warp_wait(bars + B_G, par, abort))) break;
       const float wt = gates->w[r], all = gates->all;
       __syncwarp();
       if (lane == 0) mbar_arrive(bars + B_GFREE);
       if (!(ok = warp_wait(bars + B_FULL + ik % kSlots, (ik / kSlots) & 1, abort))) break;
-      if (!(ok = warp_wait(bars + B_S, par, abort))) break;
       scale_row(sm + L::at(ik % kSlots), sm + kLo, r, kHalf / 8 * s, kHalf / 8 * (s + 1), wt,
                 r < valid);
       warp_publish(bars + B_KT);
