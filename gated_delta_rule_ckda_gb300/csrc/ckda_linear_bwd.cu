@@ -449,6 +449,11 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
     const uint32_t lanes = tmem + ((uint32_t)(32 * wq) << 16);
     const bool lead = row == 0;
     uint32_t par = 0;
+    int met = 0;  // barriers of this group so far
+    auto together = [&] {
+      ++met;
+      named_sync(1 + wg, 128);
+    };
     for (unsigned block = blockIdx.x; block < blocks; block += step, par ^= 1) {
       const Chunk u = chunk_of(a, w, block);
       const int valid = u.valid;
@@ -459,11 +464,11 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
       auto put = [&](const CUtensorMap* m, void* dst, size_t at, int width, uint32_t tile, int head,
                      int p0, int p1) {
         fence_proxy_async_smem();
-        named_sync(1 + wg, 128);
+        together();
         if (tail) {
           store_rows(static_cast<__nv_bfloat16*>(dst) + at * width, sm + tile, valid, width, p0, p1,
                      row);
-          named_sync(1 + wg, 128);
+          together();
         } else if (lead && 64 * p0 < width) {
           store_tile(m, sb + tile, u.y, head, p0, min(p1, (width + 63) / 64));
         }
@@ -555,7 +560,7 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
         if (!warp_wait(bars + B_H, par, abort) || !warp_wait(bars + B_GL, par, abort)) break;
         hgsum = tile_dot<KP, VP>(sm + kS0, sm + kS1, row);
         warp_arrive(bars + B_HG + 1);
-        named_sync(1, 128);  // dQ goes over Hhi
+        together();  // dQ goes over Hhi
         if (!warp_wait(bars + B_DQ, par, abort)) break;
         tc_fence_after();
         stage_acc(lanes + T_X1, sm + kS0, row, 0, 2 * KP);
@@ -706,7 +711,7 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
       if (lane == 0) excl = 0.f;
       if (lane == 31) run[wq] = fwd;
       if (lane == 0) run[4 + wq] = back;
-      named_sync(1, 128);
+      together();
       float t = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) t += hg[i];
@@ -716,6 +721,15 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
       if (in) (w.dg ? w.dg : a.dg)[vrow + row] = t;
       __syncwarp();
       if (lane == 0) mbar_arrive(bars + B_GFREE);
+    }
+    if (*abort) {
+      int all = 0;  // a put, or two and what A meets in besides; each once more in a tail
+      for (unsigned block = blockIdx.x; block < blocks; block += step) {
+        const bool tail = a.cu_seqlens && chunk_of(a, w, block).valid < C;
+        all += (wg == 0 ? VP : 1) * (tail ? 2 : 1) + (wg == 0 ? 2 : 0);
+      }
+      leave_group(1 + wg, 128, all - met);
+      if (lead) store_read_wait();
     }
   }
 

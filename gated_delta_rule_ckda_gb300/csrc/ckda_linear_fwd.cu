@@ -217,7 +217,8 @@ linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ 
     // ------------------------------------------------------------- P and o
     const int w = warp - 4, i = tid - 128;
     const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16);
-    for (int c = 0; c < chunks; ++c) {
+    int c = 0;
+    for (; c < chunks; ++c) {
       const uint32_t par = c & 1;
       const int valid = min(len - c * C, C);
       if (a.cu_seqlens && valid < C) {  // tokens of the next sequence behind this one
@@ -315,6 +316,7 @@ linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ 
         mbar_arrive(bars + B_HFREE);
       }
     }
+    leave_group(1, 128, chunks - c);
   } else if (warp >= 8) {
     // --------------------------------------------------------------- state
     const int s = (warp - 8) >> 2, r = (tid - 256) & 127;   // half of dk, value column

@@ -165,7 +165,8 @@ linear_state_kernel(const __grid_constant__ LinearArgs a, const __grid_constant_
       S[i] = from && r < a.dv && d < a.dk ? from[(size_t)d * a.dv + r] : 0.f;
     }
     bool ok = true;
-    for (int i = 0; i < chunks; ++i) {
+    int i = 0;
+    for (; i < chunks; ++i) {
       const int p = i & 1, c = at(i);
       if (IMAGES) {
         // (offsets that are no packing would run past the workspace)
@@ -216,6 +217,7 @@ linear_state_kernel(const __grid_constant__ LinearArgs a, const __grid_constant_
       }
       warp_arrive(bars + B_DFREE + p);
     }
+    if (IMAGES) leave_group(1, 256, 2 * (chunks - 1 - i));
     if (IMAGES && tid == 256) store_read_wait();
     float* to = !IMAGES ? sp.state + ((size_t)u.item * a.H + u.h) * states
                 : BACK && ends && a.dh0 ? a.dh0 + state

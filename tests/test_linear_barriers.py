@@ -35,7 +35,7 @@ def role(text, start, end):
     """(operation, barrier) in the order of the source between two marks."""
     body = text[text.index(start):text.index(end, text.index(start))]
     body = re.sub(r"//[^\n]*", "", body)
-    body = body[body.index("for (int c = 0; c < chunks; ++c)"):]
+    body = body[re.search(r"for \((int c = 0)?; c < chunks; \+\+c\)", body).start():]
     ops = re.findall(r"(warp_wait|warp_publish|warp_arrive|mbar_arrive|group_sync)\(bars \+ (B_\w+)",
                      body)
     assert len(ops) > 4
@@ -135,3 +135,60 @@ def test_forward_waits_see_their_phase(slots, victim):
     while left:
         if not any([move(i) for i in sorted(left) if i != victim]):
             assert victim in left and move(victim), f"warps {sorted(left)} wait for ever"
+
+
+def code_of(name):
+    return re.sub(r"//[^\n]*", "", source(name))
+
+
+def loop_at(code, start):
+    """The braces' content of the loop that begins at or behind `start`, and what follows it."""
+    at = code.index("{", start)
+    depth, end = 0, at
+    for end in range(at, len(code)):
+        depth += {"{": 1, "}": -1}.get(code[end], 0)
+        if depth == 0:
+            break
+    return code[at + 1:end], code[end + 1:]
+
+
+@pytest.mark.parametrize("name,mark,counter,per", [
+    ("ckda_linear_fwd.cu", "int w = warp - 4", "c", lambda i: 1),
+    ("ckda_linear_state.cu", "const int s = (warp - 8) >> 2", "i", lambda i: 1 + (i > 0))])
+def test_a_warp_that_gives_up_meets_the_others(name, mark, counter, per):
+    """Named hardware barriers wait without a limit: wherever a warp leaves its loop, it meets
+    the others in as many more as they may come to."""
+    code = code_of(name)
+    body, behind = loop_at(code, code.index(f"for (; {counter} < chunks;", code.index(mark)))
+    assert body.count("named_sync(") == per(1)
+    left = re.search(r"leave_group\(\d, \d+, ([^;]*)\);", behind[:200]).group(1)
+    syncs = [m.start() for m in re.finditer(r"named_sync\(", body)]
+    gives_up = [m.start() for m in re.finditer(r"warp_wait\(", body)]
+    assert syncs and gives_up
+    for chunks in (1, 2, 5):
+        for i in range(chunks + 1):
+            done = sum(per(j) for j in range(i))
+            more = [sum(s < g for s in syncs) - (per(1) - per(i)) for g in gives_up]
+            for m in [0] if i == chunks else more:
+                rest = eval(left, {"chunks": chunks, counter: i})
+                assert done + m + max(rest, 0) == sum(per(j) for j in range(chunks)), (i, m)
+
+
+def test_gradient_groups_count_their_barriers():
+    """The same for the gradient kernel, whose groups of warps count the barriers they met."""
+    code = code_of("ckda_linear_bwd.cu")
+    body, behind = loop_at(code, code.index("for (unsigned block", code.index("auto together")))
+    assert "named_sync" not in body
+    put = body[body.index("auto put"):body.index("};", body.index("auto put"))]
+    tail, rest = loop_at(put, put.index("if (tail)"))
+    assert tail.count("together()") == 1 and put.count("together()") == 2
+    # A: dQ, half of dV where values are wider than 64, and two more; B: dK; C: half of dV
+    assert body.count("together()") - 2 == 2
+    assert [m for m in re.findall(r"put\(&(\w+)", body)] == ["mdq", "mdk", "mdv"]
+    assert "if (wg == 2 || (wg == 0 && VP == 2))" in body
+    each = re.search(r"all \+= ([^;]*);", behind).group(1)
+    py = re.sub(r"\(([^()]*) \? (\w+) : (\w+)\)", r"(\2 if \1 else \3)", each)
+    for wg, VP, t in ((wg, VP, t) for wg in range(3) for VP in (1, 2) for t in (False, True)):
+        puts = 1 + (wg == 0 and VP == 2)
+        assert eval(py, dict(wg=wg, VP=VP, tail=t)) == puts * (1 + t) + 2 * (wg == 0)
+    assert "leave_group(1 + wg, 128, all - met)" in behind
