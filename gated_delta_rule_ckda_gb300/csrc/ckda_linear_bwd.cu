@@ -304,7 +304,9 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
   if (warp == 0) {
     if (lane == 0) {
       uint32_t par = 0;
-      for (unsigned block = blockIdx.x; block < blocks; block += step, par ^= 1) {
+      int begun = 0;  // loads of this chunk: q and k; v and do; H and Ghi; Glo
+      unsigned block = blockIdx.x;
+      for (; block < blocks; block += step, par ^= 1, begun = 0) {
         const Chunk u = chunk_of(a, w, block);
         const char* himg = w.himg + (size_t)block * kImage;
         const char* gimg = w.gimg + (size_t)block * kImage;
@@ -319,6 +321,7 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
           tma_load_3d(sb + kQ + p * kPanel, &mq, bars + B_QK, 64 * p, u.y, u.qz);
           tma_load_3d(sb + kK + p * kPanel, &mk, bars + B_QK, 64 * p, u.y, u.qz);
         }
+        begun = 1;
         last(B_X2); last(B_DV);
         if (!ok) { *abort = 1; break; }
         mbar_arrive_expect_tx(bars + B_VD, 2 * VP * kPanel);
@@ -326,6 +329,7 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
           tma_load_3d(sb + kV + p * kPanel, &mv, bars + B_VD, 64 * p, u.y, u.vz);
           tma_load_3d(sb + kDo + p * kPanel, &mo, bars + B_VD, 64 * p, u.y, u.vz);
         }
+        begun = 2;
         last(B_F0); last(B_F1); last(B_F2);
         if (!ok) { *abort = 1; break; }
         mbar_arrive_expect_tx(bars + B_H, 2 * kPart);
@@ -333,9 +337,11 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
         load_image<KP, VP>(sb + kS1, himg + kTile, bars + B_H);
         mbar_arrive_expect_tx(bars + B_GH, kPart);
         load_image<KP, VP>(sb + kS2, gimg, bars + B_GH);
+        begun = 3;
         if (!mbar_wait(bars + B_X1L, par) || !mbar_wait(bars + B_HG, par)) { *abort = 1; break; }
         mbar_arrive_expect_tx(bars + B_GL, kPart);  // Hlo has been read
         load_image<KP, VP>(sb + kS1, gimg + kTile, bars + B_GL);
+        begun = 4;
         // What comes next, into L2 while this chunk is worked on: tiles come free
         // late, and their loads should not wait for HBM then.
         if (block + step < blocks) {
@@ -352,6 +358,11 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
             }
         }
       }
+      // (none is left in flight, whatever the others do)
+      const int loads[][2] = {{B_QK, 1}, {B_VD, 2}, {B_H, 3}, {B_GH, 3}, {B_GL, 4}};
+      for (auto& l : loads)
+        if (begun >= l[1] || block != blockIdx.x)
+          mbar_wait(bars + l[0], begun >= l[1] ? par : par ^ 1);
     }
   } else if (warp == 1) {
     if (lane == 0) {
@@ -738,12 +749,7 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
   __syncthreads();
   if (tid == 0) {
     if (!mbar_wait(bars + B_END, 0)) *abort = 1;
-    if (*abort) {
-      // let copies in flight land before the memory is given back
-      set_status(a.status, CKDA_ERR_TIMEOUT);
-      const int land[] = {B_QK, B_VD, B_H, B_GH, B_GL};
-      for (int i : land) mbar_wait(bars + i, 0, 1u << 12, 1000u);
-    }
+    if (*abort) set_status(a.status, CKDA_ERR_TIMEOUT);
   }
   __syncthreads();
   tc_fence_after();

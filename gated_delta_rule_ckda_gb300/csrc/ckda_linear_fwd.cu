@@ -130,7 +130,8 @@ linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ 
   if (warp == 0) {
     // ------------------------------------------------------------- loads
     if (lane == 0) {
-      for (int i = 0; i < 3 * chunks; ++i) {
+      int i = 0;
+      for (; i < 3 * chunks; ++i) {
         const int slot = i % kSlots, use = i / kSlots, c = i / 3;
         if (use > 0) {  // the slot's last tile has been read: q by Q H, k and v by the state's product
           const int j = i - kSlots, cj = j / 3;
@@ -142,6 +143,9 @@ linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ 
         load_tile(sb + L::at(slot), m, bars + B_FULL + slot, t0 + c * C, i % 3 == 2 ? vz : qz,
                   i % 3 == 2 ? (a.dv > 64 ? 2 : 1) : L::kPanels);
       }
+      // (none is left in flight, whatever the others do)
+      for (int j = max(0, i - kSlots); j < i; ++j)
+        mbar_wait(bars + B_FULL + j % kSlots, (j / kSlots) & 1);
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------- products
@@ -383,10 +387,7 @@ linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ 
   if (tid == 0) {
     // every commit has arrived before the memory is given back
     if (!mbar_wait(bars + B_END, 0)) *abort = 1;
-    if (*abort) {
-      set_status(a.status, CKDA_ERR_TIMEOUT);
-      for (int i = 0; i < kSlots; ++i) mbar_wait(bars + B_FULL + i, 0, 1u << 12, 1000u);
-    }
+    if (*abort) set_status(a.status, CKDA_ERR_TIMEOUT);
   }
   __syncthreads();
   tc_fence_after();

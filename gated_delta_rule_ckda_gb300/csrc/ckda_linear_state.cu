@@ -99,7 +99,8 @@ linear_state_kernel(const __grid_constant__ LinearArgs a, const __grid_constant_
 
   if (warp == 0) {
     if (lane == 0) {
-      for (int i = 0; i < 2 * steps; ++i) {
+      int i = 0;
+      for (; i < 2 * steps; ++i) {
         const int slot = i % kSlots, use = i / kSlots;
         if (use > 0 && !mbar_wait(bars + B_EMPTY + slot, (use - 1) & 1)) { *abort = 1; break; }
         if (*abort) break;
@@ -107,6 +108,9 @@ linear_state_kernel(const __grid_constant__ LinearArgs a, const __grid_constant_
         load_tile(sb + slot * kTile, i & 1 ? &my : &mx, bars + B_FULL + slot, t0 + at(i / 2) * C,
                   i & 1 ? yz : xz, i & 1 ? (a.dv > 64 ? 2 : 1) : KP);
       }
+      // (none is left in flight, whatever the others do)
+      for (int j = max(0, i - kSlots); j < i; ++j)
+        mbar_wait(bars + B_FULL + j % kSlots, (j / kSlots) & 1);
     }
   } else if (warp == 1) {
     if (lane == 0) {
@@ -236,10 +240,7 @@ linear_state_kernel(const __grid_constant__ LinearArgs a, const __grid_constant_
   __syncthreads();
   if (tid == 0) {
     if (!mbar_wait(bars + B_END, 0)) *abort = 1;
-    if (*abort) {
-      set_status(a.status, CKDA_ERR_TIMEOUT);
-      for (int i = 0; i < kSlots; ++i) mbar_wait(bars + B_FULL + i, 0, 1u << 12, 1000u);
-    }
+    if (*abort) set_status(a.status, CKDA_ERR_TIMEOUT);
   }
   __syncthreads();
   tc_fence_after();

@@ -192,3 +192,42 @@ def test_gradient_groups_count_their_barriers():
         puts = 1 + (wg == 0 and VP == 2)
         assert eval(py, dict(wg=wg, VP=VP, tail=t)) == puts * (1 + t) + 2 * (wg == 0)
     assert "leave_group(1 + wg, 128, all - met)" in behind
+
+
+@pytest.mark.parametrize("name", ["ckda_linear_fwd.cu", "ckda_linear_state.cu"])
+def test_loads_in_flight_are_waited_for(name):
+    """However many loads a CTA has begun when it gives up, it waits for the last phase of each
+    slot before its shared memory is given back."""
+    code = code_of(name)
+    m = re.search(r"for \(int j = (max\(0, i - kSlots\)); j < i; \+\+j\)\s*"
+                  r"mbar_wait\(bars \+ B_FULL \+ ([^,]*), ([^;]*)\);", code)
+    assert m
+    slot, parity = m.group(2), m.group(3).replace("/", "//")
+    for slots in (4, 5, 6):
+        for begun in range(20):
+            last = {}
+            for i in range(begun):
+                last[i % slots] = (i // slots) & 1  # parity of the phase that this load completes
+            env = lambda **kw: dict(kSlots=slots, i=begun, max=max, **kw)
+            waited = {eval(slot, env(j=j)): eval(parity, env(j=j))
+                      for j in range(eval(m.group(1), env()), begun)}
+            assert waited == last, (slots, begun)
+
+
+def test_gradient_loads_in_flight_are_waited_for():
+    """The same for the gradient kernel: five barriers, a phase a chunk each."""
+    code = code_of("ckda_linear_bwd.cu")
+    at = code.index("int begun = 0;")
+    body, behind = loop_at(code, code.index("for (; block < blocks;", at))
+    stages = {b: int(s) for b, s in re.findall(r"\{(B_\w+), (\d)\}", behind[:300])}
+    assert len(stages) == 5
+    for b, s in stages.items():  # begun reaches s right behind the loads on b
+        loads = [m.start() for m in re.finditer(rf"bars \+ {b}[,)]", body)]
+        mark = body.index(f"begun = {s};")
+        assert loads and all(x < mark for x in loads)
+        assert s == 1 or min(loads) > body.index(f"begun = {s - 1};")
+    head = code[code.index("for (; block < blocks;", at):][:90]
+    assert "par ^= 1, begun = 0" in head
+    rule = re.sub(r"\s+", " ", behind[:500])
+    assert ("if (begun >= l[1] || block != blockIdx.x) "
+            "mbar_wait(bars + l[0], begun >= l[1] ? par : par ^ 1);") in rule
