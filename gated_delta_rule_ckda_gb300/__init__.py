@@ -15,6 +15,11 @@ layernorm_bwd).
 Shapes follow the C ABI: q, k, alpha [B, H, T, dk]; v [B, H, T, dv];
 beta [B, H, T]; h0 / hT fp32 [N, H, dk, dv] with N = B, or the number of
 packed sequences when cu_seqlens (int32 [N + 1], B == 1) is given.
+
+Calls run on the current stream of the tensors' device, or on `stream`.  With a
+stream of its own, a call takes its memory there too; that the stream sees its
+inputs, and the caller's its results, is the caller's part (wait_stream), as it
+is for torch's own calls under torch.cuda.stream.
 """
 from __future__ import annotations
 
@@ -147,6 +152,27 @@ def _stream_handle(stream, device):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _on_stream(call, args):
+    """call(**args) where args["stream"] is given: with that stream current, so that what the
+    call allocates is the stream's memory, which goes to another use behind the call's kernels
+    and not beside them.  The results may be used, and freed, on the caller's stream too."""
+    stream = args.pop("stream")
+    tensors = [t for t in args.values() if isinstance(t, torch.Tensor)]
+    for t in tensors:
+        if t.is_cuda and t.device != stream.device:
+            raise ValueError(f"stream: on {stream.device}, expected {t.device}")
+    here = torch.cuda.current_stream(stream.device)
+    if stream == here:
+        return call(**args)
+    with torch.cuda.stream(stream):
+        out = call(**args)
+    given = {id(t) for a in args.values() for t in (a if isinstance(a, (tuple, list)) else (a,))}
+    for t in out if isinstance(out, tuple) else (out,):
+        if isinstance(t, torch.Tensor) and t.is_cuda and id(t) not in given:
+            t.record_stream(here)
+    return out
+
+
 def _io_dtype(t):
     if t.dtype == torch.bfloat16:
         return _BF16
@@ -190,6 +216,8 @@ def fwd_raw(q_raw, k_raw, v, a_raw, b_raw, h0=None, cu_seqlens=None, scale=1.0,
 def fwd(q, k, v, alpha, beta, h0=None, cu_seqlens=None, scale=1.0, chunk_size=0,
         store_final_state=True, o=None, hT=None, workspace=None, stream=None, _raw=None):
     """Forward over [B, H, T, d] (or packed) inputs.  Returns (o, hT or None)."""
+    if stream is not None:
+        return _on_stream(fwd, locals())
     L = lib()
     device = q.device
     B, H, T, dk = q.shape
@@ -222,12 +250,12 @@ def fwd(q, k, v, alpha, beta, h0=None, cu_seqlens=None, scale=1.0, chunk_size=0,
         rc = L.ckda_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _ptr(h0), _ptr(o),
                         _ptr(hT), _ptr(cu_seqlens), nseq, B, H, T, dk, dv, _io_dtype(q),
                         float(scale), int(chunk_size), _ptr(workspace), int(workspace.numel()),
-                        _stream_handle(stream, device))
+                        _stream_handle(None, device))
     else:
         rc = L.ckda_fwd_raw(_ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _ptr(h0), _ptr(o),
                             _ptr(hT), _ptr(cu_seqlens), nseq, B, H, T, dk, dv, _io_dtype(q),
                             float(scale), int(_raw[0]), float(_raw[1]), _ptr(workspace),
-                            int(workspace.numel()), _stream_handle(stream, device))
+                            int(workspace.numel()), _stream_handle(None, device))
     if rc != 0:
         raise CkdaError(rc, "ckda_fwd" if _raw is None else "ckda_fwd_raw")
     fwd.last_workspace = workspace
@@ -252,6 +280,8 @@ def fwd_split(q, k, v, alpha, beta, h0=None, scale=1.0, segments=0, store_final_
     """ckda_fwd_split: the dense forward with each sequence cut into segments
     run in parallel (two passes and a scan of the segment operators).
     Returns (o, hT or None)."""
+    if stream is not None:
+        return _on_stream(fwd_split, locals())
     L = lib()
     device = q.device
     B, H, T, dk = q.shape
@@ -280,7 +310,7 @@ def fwd_split(q, k, v, alpha, beta, h0=None, scale=1.0, segments=0, store_final_
         rc = L.ckda_fwd_split(_ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _ptr(h0),
                               _ptr(o), _ptr(hT), B, H, T, dk, dv, io, float(scale),
                               int(segments), _ptr(workspace), int(workspace.numel()),
-                              _stream_handle(stream, device))
+                              _stream_handle(None, device))
     if rc != 0:
         raise CkdaError(rc, "ckda_fwd_split")
     fwd_split.last_workspace = workspace
@@ -303,6 +333,8 @@ def fwd_split_varlen(q, k, v, alpha, beta, cu_seqlens, h0=None, scale=1.0, seg_l
     than seg_len cut into segments run in parallel.  q, k, alpha, v are
     [1, H, T, d], beta [1, H, T], cu_seqlens int32 [N + 1] on the device.
     Returns (o, hT [N, H, dk, dv] or None)."""
+    if stream is not None:
+        return _on_stream(fwd_split_varlen, locals())
     L = lib()
     device = q.device
     B, H, T, dk = q.shape
@@ -337,7 +369,7 @@ def fwd_split_varlen(q, k, v, alpha, beta, cu_seqlens, h0=None, scale=1.0, seg_l
         rc = L.ckda_fwd_split_varlen(_ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _ptr(h0),
                                      _ptr(o), _ptr(hT), _ptr(cu_seqlens), N, H, T, dk, dv, io,
                                      float(scale), int(seg_len), _ptr(workspace),
-                                     int(workspace.numel()), _stream_handle(stream, device))
+                                     int(workspace.numel()), _stream_handle(None, device))
     if rc != 0:
         raise CkdaError(rc, "ckda_fwd_split_varlen")
     fwd_split_varlen.last_workspace = workspace
@@ -360,6 +392,8 @@ def fwd_host(q, k, v, alpha, beta, h0=None, scale=1.0, slice_tokens=0, o=None, h
     tensors; pinned memory copies at full speed).  The copies of one slice of
     tokens overlap the computation of another.  Returns (o, hT or None) as CPU
     tensors; they are complete once `stream` is (this call does not wait)."""
+    if stream is not None:
+        return _on_stream(fwd_host, locals())
     L = lib()
     device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
     B, H, T, dk = q.shape
@@ -386,7 +420,7 @@ def fwd_host(q, k, v, alpha, beta, h0=None, scale=1.0, slice_tokens=0, o=None, h
         scratch = torch.empty(need, dtype=torch.uint8, device=device)
     rc = L.ckda_fwd_host(_ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _ptr(h0), _ptr(o),
                          _ptr(hT), B, H, T, dk, dv, io, float(scale), int(slice_tokens),
-                         _ptr(scratch), int(scratch.numel()), _stream_handle(stream, device))
+                         _ptr(scratch), int(scratch.numel()), _stream_handle(None, device))
     if rc != 0:
         raise CkdaError(rc, "ckda_fwd_host")
     fwd_host.last_scratch = scratch
@@ -395,6 +429,8 @@ def fwd_host(q, k, v, alpha, beta, h0=None, scale=1.0, slice_tokens=0, o=None, h
 
 def decode_step(q, k, v, alpha, beta, state, scale=1.0, o=None, stream=None):
     """One token per (batch, head); `state` [B, H, dk, dv] fp32 is updated in place."""
+    if stream is not None:
+        return _on_stream(decode_step, locals())
     L = lib()
     device = q.device
     B, H, dk = q.shape
@@ -411,7 +447,7 @@ def decode_step(q, k, v, alpha, beta, state, scale=1.0, o=None, stream=None):
         _check(o, "o", dt, (B, H, dv), device)
     rc = L.ckda_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _ptr(state),
                             _ptr(o), B, H, dk, dv, _io_dtype(q), float(scale),
-                            _stream_handle(stream, device))
+                            _stream_handle(None, device))
     if rc != 0:
         raise CkdaError(rc, "ckda_decode_step")
     return o
@@ -432,6 +468,8 @@ def fwd_noalloc(q, k, v, alpha, beta, h0=None, cu_seqlens=None, scale=1.0, chunk
     """ckda_fwd_noalloc: the forward without a workspace, for callers that may
     not allocate device memory (its scratch is a fixed array inside libckda).
     o and hT may be passed in so that the call itself allocates nothing."""
+    if stream is not None:
+        return _on_stream(fwd_noalloc, locals())
     L = lib()
     fn = L.ckda_fwd_noalloc
     if fn.argtypes is None:
@@ -449,7 +487,7 @@ def fwd_noalloc(q, k, v, alpha, beta, h0=None, cu_seqlens=None, scale=1.0, chunk
         hT = torch.empty((N, H, dk, dv), dtype=torch.float32, device=device)
     rc = fn(_ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _ptr(h0), _ptr(o), _ptr(hT),
             _ptr(cu_seqlens), int(N if cu_seqlens is not None else 0), B, H, T, dk, dv,
-            _io_dtype(q), float(scale), int(chunk_size), _stream_handle(stream, device))
+            _io_dtype(q), float(scale), int(chunk_size), _stream_handle(None, device))
     if rc != 0:
         raise CkdaError(rc, "ckda_fwd_noalloc")
     return o, hT
@@ -464,6 +502,8 @@ def prep(k_raw, a_raw, b_raw, q_raw=None, normalize_q=True, norm_eps=1e-6, out=N
     (q or None, k, alpha, beta) in the input dtype.  `out` may give the four
     output tensors (q may be None); passing the inputs themselves works in place.
     """
+    if stream is not None:
+        return _on_stream(prep, locals())
     L = lib()
     device = k_raw.device
     dt = k_raw.dtype
@@ -488,7 +528,7 @@ def prep(k_raw, a_raw, b_raw, q_raw=None, normalize_q=True, norm_eps=1e-6, out=N
     rows = k_raw.numel() // dk if dk else 0
     rc = L.ckda_prep(_ptr(q_raw), _ptr(k_raw), _ptr(a_raw), _ptr(b_raw), _ptr(q), _ptr(k),
                      _ptr(alpha), _ptr(beta), int(rows), int(dk), _io_dtype(k_raw),
-                     int(bool(normalize_q)), float(norm_eps), _stream_handle(stream, device))
+                     int(bool(normalize_q)), float(norm_eps), _stream_handle(None, device))
     if rc != 0:
         raise CkdaError(rc, "ckda_prep")
     return q, k, alpha, beta
@@ -502,6 +542,8 @@ def prep_bwd(k_raw, a_raw, b_raw, d_k, d_alpha, d_beta, q_raw=None, d_q=None, no
 
     Returns (d_q_raw or None, d_k_raw, d_a_raw, d_b_raw) in the input dtype;
     `out` may give the four output tensors (d_q_raw may be None)."""
+    if stream is not None:
+        return _on_stream(prep_bwd, locals())
     L = lib()
     device = k_raw.device
     dt = k_raw.dtype
@@ -533,7 +575,7 @@ def prep_bwd(k_raw, a_raw, b_raw, d_k, d_alpha, d_beta, q_raw=None, d_q=None, no
     rc = L.ckda_prep_bwd(_ptr(q_raw), _ptr(k_raw), _ptr(a_raw), _ptr(b_raw), _ptr(d_q),
                          _ptr(d_k), _ptr(d_alpha), _ptr(d_beta), _ptr(dq_raw), _ptr(dk_raw),
                          _ptr(da_raw), _ptr(db_raw), int(rows), int(dk), _io_dtype(k_raw),
-                         int(bool(normalize_q)), float(norm_eps), _stream_handle(stream, device))
+                         int(bool(normalize_q)), float(norm_eps), _stream_handle(None, device))
     if rc != 0:
         raise CkdaError(rc, "ckda_prep_bwd")
     return dq_raw, dk_raw, da_raw, db_raw
@@ -548,6 +590,8 @@ def bwd(q, k, v, alpha, beta, do, h0=None, dhT=None, cu_seqlens=None, scale=1.0,
     """Backward of fwd (ckda_bwd): gradients of sum <o, do> + <hT, dhT>.
 
     Returns (dq, dk, dv, dalpha, dbeta, dh0 or None); dh0 is fp32."""
+    if stream is not None:
+        return _on_stream(bwd, locals())
     L = lib()
     device = q.device
     B, H, T, dk = q.shape
@@ -575,7 +619,7 @@ def bwd(q, k, v, alpha, beta, do, h0=None, dhT=None, cu_seqlens=None, scale=1.0,
                     _ptr(dhT), _ptr(dq), _ptr(dkk), _ptr(dvv), _ptr(dal), _ptr(dbe), _ptr(dh0),
                     _ptr(cu_seqlens), int(N if cu_seqlens is not None else 0), B, H, T, dk, dv,
                     _io_dtype(q), float(scale), _ptr(workspace), int(workspace.numel()),
-                    _stream_handle(stream, device))
+                    _stream_handle(None, device))
     if rc != 0:
         raise CkdaError(rc, "ckda_bwd")
     return dq, dkk, dvv, dal, dbe, dh0
@@ -586,6 +630,8 @@ def decode_step_raw(q_raw, k_raw, v, a_raw, b_raw, state, scale=1.0, normalize_q
     """One decode step on raw inputs with the input preparation fused in
     (ckda_decode_step_raw): unit-norm k (and q), alpha and beta from the gate
     logits a and b.  state [B, H, 128, 128] fp32 is updated in place; returns o."""
+    if stream is not None:
+        return _on_stream(decode_step_raw, locals())
     L = lib()
     device = q_raw.device
     B, H, dk = q_raw.shape
@@ -601,7 +647,7 @@ def decode_step_raw(q_raw, k_raw, v, a_raw, b_raw, state, scale=1.0, normalize_q
     rc = L.ckda_decode_step_raw(_ptr(q_raw), _ptr(k_raw), _ptr(v), _ptr(a_raw), _ptr(b_raw),
                                 _ptr(state), _ptr(o), B, H, dk, dv, _io_dtype(q_raw),
                                 float(scale), int(bool(normalize_q)), float(norm_eps),
-                                _stream_handle(stream, device))
+                                _stream_handle(None, device))
     if rc != 0:
         raise CkdaError(rc, "ckda_decode_step_raw")
     return o
@@ -614,10 +660,9 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _call(fn, where, device, stream, *args):
-    """fn(*args, stream) on the tensors' device; raises CkdaError."""
-    handle = (torch._C._cuda_getCurrentRawStream(device.index) if stream is None
-              else stream.cuda_stream)
+def _call(fn, where, device, *args):
+    """fn(*args, current stream) on the tensors' device; raises CkdaError."""
+    handle = torch._C._cuda_getCurrentRawStream(device.index)
     if device.index == torch._C._cuda_getDevice():
         rc = fn(*args, handle)
     else:
@@ -681,6 +726,8 @@ def linear_fwd(q, k, v, g, h0=None, cu_seqlens=None, scale=1.0, store_final_stat
     q, k [B, Hk, T, dk] with Hk dividing H (heads share keys in order),
     v [B, H, T, dv], g fp32 [B, H, T] or [H] (one decay for all of a head's
     tokens); h0, hT fp32 [N, H, dk, dv].  Returns (o, hT or None)."""
+    if stream is not None:
+        return _on_stream(linear_fwd, locals())
     L = lib()
     device = q.device
     B, H, Hk, T, dk, dv, N, per_head, io = _check_linear(q, k, v, g, cu_seqlens,
@@ -696,7 +743,7 @@ def linear_fwd(q, k, v, g, h0=None, cu_seqlens=None, scale=1.0, store_final_stat
         workspace = torch.empty(
             _bytes("ckda_linear_fwd_workspace_bytes", nseq, B, H, T, dk, dv, io),
             dtype=torch.uint8, device=device)
-    _call(L.ckda_linear_fwd, "ckda_linear_fwd", device, stream, _addr(q), _addr(k), _addr(v),
+    _call(L.ckda_linear_fwd, "ckda_linear_fwd", device, _addr(q), _addr(k), _addr(v),
           _addr(g), int(per_head), _addr(h0), _addr(o), _addr(hT), _addr(cu_seqlens), nseq, B,
           H, Hk, T, dk, dv, io, float(scale), _addr(workspace), workspace.numel())
     linear_fwd.last_workspace = workspace
@@ -708,6 +755,8 @@ def linear_bwd(q, k, v, g, do, h0=None, dhT=None, cu_seqlens=None, scale=1.0, st
     """Backward of linear_fwd (ckda_linear_bwd): gradients of
     sum <o, do> + <hT, dhT>.  Returns (dq, dk, dv, dg, dh0 or None); dg (of g's
     shape) and dh0 are fp32."""
+    if stream is not None:
+        return _on_stream(linear_bwd, locals())
     L = lib()
     device = q.device
     B, H, Hk, T, dk, dv, N, per_head, io = _check_linear(q, k, v, g, cu_seqlens,
@@ -720,7 +769,7 @@ def linear_bwd(q, k, v, g, do, h0=None, dhT=None, cu_seqlens=None, scale=1.0, st
     dq, dkk, dvv, dg = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v),
                         torch.empty_like(g))
     dh0 = torch.empty((N, H, dk, dv), dtype=torch.float32, device=device) if store_dh0 else None
-    _call(L.ckda_linear_bwd, "ckda_linear_bwd", device, stream, _addr(q), _addr(k), _addr(v),
+    _call(L.ckda_linear_bwd, "ckda_linear_bwd", device, _addr(q), _addr(k), _addr(v),
           _addr(g), int(per_head), _addr(h0), _addr(do), _addr(dhT), _addr(dq), _addr(dkk),
           _addr(dvv), _addr(dg), _addr(dh0), _addr(cu_seqlens), nseq, B, H, Hk, T, dk, dv, io,
           float(scale), _addr(workspace), workspace.numel())
@@ -732,6 +781,8 @@ def linear_decode_step(q, k, v, g, state, scale=1.0, o=None, stream=None):
     """One token of linear attention (ckda_linear_decode_step) on a resident
     state [B, H, dk, dv] fp32, updated in place.  q, k [B, Hk, dk],
     v [B, H, dv], g fp32 [B, H] or [H].  Returns o [B, H, dv]."""
+    if stream is not None:
+        return _on_stream(linear_decode_step, locals())
     L = lib()
     device, dt = q.device, q.dtype
     io = _io_dtype(q)
@@ -751,7 +802,7 @@ def linear_decode_step(q, k, v, g, state, scale=1.0, o=None, stream=None):
         o = torch.empty((B, H, dv), dtype=dt, device=device)
     else:
         _check(o, "o", dt, (B, H, dv), device)
-    _call(L.ckda_linear_decode_step, "ckda_linear_decode_step", device, stream, _addr(q),
+    _call(L.ckda_linear_decode_step, "ckda_linear_decode_step", device, _addr(q),
           _addr(k), _addr(v), _addr(g), int(per_head), _addr(state), _addr(o), B, H, Hk, dk, dv,
           io, float(scale))
     return o
@@ -774,6 +825,8 @@ def layernorm_fwd(x, weight=None, bias=None, eps=1e-5, y=None, mean=None, rstd=N
     """Layer norm over the last axis (ckda_layernorm_fwd).  Returns (y, mean,
     rstd); mean and rstd are fp32 of x's leading shape.  weight and bias are
     bf16 or fp32 [width], whatever x's type.  y may be x (in place)."""
+    if stream is not None:
+        return _on_stream(layernorm_fwd, locals())
     L = lib()
     device = x.device
     io = _io_dtype(x)
@@ -795,7 +848,7 @@ def layernorm_fwd(x, weight=None, bias=None, eps=1e-5, y=None, mean=None, rstd=N
         rstd = torch.empty(lead, dtype=torch.float32, device=device)
     else:
         _check(rstd, "rstd", torch.float32, lead, device)
-    _call(L.ckda_layernorm_fwd, "ckda_layernorm_fwd", device, stream, _addr(x), _addr(weight),
+    _call(L.ckda_layernorm_fwd, "ckda_layernorm_fwd", device, _addr(x), _addr(weight),
           _addr(bias), _addr(y), _addr(mean), _addr(rstd), mean.numel(), width, io, wcode,
           float(eps))
     return y, mean, rstd
@@ -806,6 +859,8 @@ def layernorm_bwd(dy, x, mean, rstd, weight=None, weight_grad=True, dx=None, wor
     """Backward of layernorm_fwd (ckda_layernorm_bwd).  Returns (dx, dweight,
     dbias); the last two have weight's type (fp32 without one) and are None
     when weight_grad is false.  dx may be dy or x (in place)."""
+    if stream is not None:
+        return _on_stream(layernorm_bwd, locals())
     L = lib()
     device = x.device
     io = _io_dtype(x)
@@ -831,7 +886,7 @@ def layernorm_bwd(dy, x, mean, rstd, weight=None, weight_grad=True, dx=None, wor
         if workspace is None:
             workspace = torch.empty(_bytes("ckda_layernorm_bwd_workspace_bytes", rows, width),
                                     dtype=torch.uint8, device=device)
-    _call(L.ckda_layernorm_bwd, "ckda_layernorm_bwd", device, stream, _addr(dy), _addr(x),
+    _call(L.ckda_layernorm_bwd, "ckda_layernorm_bwd", device, _addr(dy), _addr(x),
           _addr(mean), _addr(rstd), _addr(weight), _addr(dx), _addr(dw), _addr(db), rows, width,
           io, wcode, _addr(workspace), 0 if workspace is None else workspace.numel())
     return dx, dw, db
