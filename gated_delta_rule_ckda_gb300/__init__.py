@@ -147,6 +147,8 @@ def _ptr(t):
 
 
 def _stream_handle(stream, device):
+    if device.type != "cuda":
+        raise ValueError(f"tensors on {device}, expected CUDA")
     if stream is None:
         stream = torch.cuda.current_stream(device)
     return ctypes.c_void_p(stream.cuda_stream)
@@ -192,6 +194,15 @@ def _check(t, name, dtype, shape, device):
         raise ValueError(f"{name}: must be contiguous")
     if t.device != device:
         raise ValueError(f"{name}: on {t.device}, expected {device}")
+
+
+def _given(t, device, name="workspace"):
+    """Bytes of scratch memory that the caller gave: on the tensors' device, in one run."""
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t.numel() * t.element_size()
 
 
 def workspace_bytes(num_seqs: int, H: int) -> int:
@@ -249,13 +260,13 @@ def fwd(q, k, v, alpha, beta, h0=None, cu_seqlens=None, scale=1.0, chunk_size=0,
     if _raw is None:
         rc = L.ckda_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _ptr(h0), _ptr(o),
                         _ptr(hT), _ptr(cu_seqlens), nseq, B, H, T, dk, dv, _io_dtype(q),
-                        float(scale), int(chunk_size), _ptr(workspace), int(workspace.numel()),
+                        float(scale), int(chunk_size), _ptr(workspace), _given(workspace, device),
                         _stream_handle(None, device))
     else:
         rc = L.ckda_fwd_raw(_ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _ptr(h0), _ptr(o),
                             _ptr(hT), _ptr(cu_seqlens), nseq, B, H, T, dk, dv, _io_dtype(q),
                             float(scale), int(_raw[0]), float(_raw[1]), _ptr(workspace),
-                            int(workspace.numel()), _stream_handle(None, device))
+                            _given(workspace, device), _stream_handle(None, device))
     if rc != 0:
         raise CkdaError(rc, "ckda_fwd" if _raw is None else "ckda_fwd_raw")
     fwd.last_workspace = workspace
@@ -309,7 +320,7 @@ def fwd_split(q, k, v, alpha, beta, h0=None, scale=1.0, segments=0, store_final_
     with torch.cuda.device(device):
         rc = L.ckda_fwd_split(_ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _ptr(h0),
                               _ptr(o), _ptr(hT), B, H, T, dk, dv, io, float(scale),
-                              int(segments), _ptr(workspace), int(workspace.numel()),
+                              int(segments), _ptr(workspace), _given(workspace, device),
                               _stream_handle(None, device))
     if rc != 0:
         raise CkdaError(rc, "ckda_fwd_split")
@@ -369,7 +380,7 @@ def fwd_split_varlen(q, k, v, alpha, beta, cu_seqlens, h0=None, scale=1.0, seg_l
         rc = L.ckda_fwd_split_varlen(_ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _ptr(h0),
                                      _ptr(o), _ptr(hT), _ptr(cu_seqlens), N, H, T, dk, dv, io,
                                      float(scale), int(seg_len), _ptr(workspace),
-                                     int(workspace.numel()), _stream_handle(None, device))
+                                     _given(workspace, device), _stream_handle(None, device))
     if rc != 0:
         raise CkdaError(rc, "ckda_fwd_split_varlen")
     fwd_split_varlen.last_workspace = workspace
@@ -395,7 +406,9 @@ def fwd_host(q, k, v, alpha, beta, h0=None, scale=1.0, slice_tokens=0, o=None, h
     if stream is not None:
         return _on_stream(fwd_host, locals())
     L = lib()
-    device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+    device = torch.device("cuda" if device is None else device)
+    if device.type == "cuda" and device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
     B, H, T, dk = q.shape
     dv = v.shape[-1]
     dt = q.dtype
@@ -420,7 +433,8 @@ def fwd_host(q, k, v, alpha, beta, h0=None, scale=1.0, slice_tokens=0, o=None, h
         scratch = torch.empty(need, dtype=torch.uint8, device=device)
     rc = L.ckda_fwd_host(_ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _ptr(h0), _ptr(o),
                          _ptr(hT), B, H, T, dk, dv, io, float(scale), int(slice_tokens),
-                         _ptr(scratch), int(scratch.numel()), _stream_handle(None, device))
+                         _ptr(scratch), _given(scratch, device, "scratch"),
+                         _stream_handle(None, device))
     if rc != 0:
         raise CkdaError(rc, "ckda_fwd_host")
     fwd_host.last_scratch = scratch
@@ -481,10 +495,22 @@ def fwd_noalloc(q, k, v, alpha, beta, h0=None, cu_seqlens=None, scale=1.0, chunk
     B, H, T, dk = q.shape
     dv = v.shape[-1]
     N = B if cu_seqlens is None else cu_seqlens.numel() - 1
+    for name, t, shp in (("q", q, (B, H, T, dk)), ("k", k, (B, H, T, dk)),
+                         ("alpha", alpha, (B, H, T, dk)), ("v", v, (B, H, T, dv)),
+                         ("beta", beta, (B, H, T))):
+        _check(t, name, q.dtype, shp, device)
+    if cu_seqlens is not None:
+        _check(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,), device)
+    if h0 is not None:
+        _check(h0, "h0", torch.float32, (N, H, dk, dv), device)
     if o is None:
         o = torch.empty((B, H, T, dv), dtype=q.dtype, device=device)
+    else:
+        _check(o, "o", q.dtype, (B, H, T, dv), device)
     if hT is None:
         hT = torch.empty((N, H, dk, dv), dtype=torch.float32, device=device)
+    else:
+        _check(hT, "hT", torch.float32, (N, H, dk, dv), device)
     rc = fn(_ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _ptr(h0), _ptr(o), _ptr(hT),
             _ptr(cu_seqlens), int(N if cu_seqlens is not None else 0), B, H, T, dk, dv,
             _io_dtype(q), float(scale), int(chunk_size), _stream_handle(None, device))
@@ -618,7 +644,7 @@ def bwd(q, k, v, alpha, beta, do, h0=None, dhT=None, cu_seqlens=None, scale=1.0,
     rc = L.ckda_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _ptr(h0), _ptr(do),
                     _ptr(dhT), _ptr(dq), _ptr(dkk), _ptr(dvv), _ptr(dal), _ptr(dbe), _ptr(dh0),
                     _ptr(cu_seqlens), int(N if cu_seqlens is not None else 0), B, H, T, dk, dv,
-                    _io_dtype(q), float(scale), _ptr(workspace), int(workspace.numel()),
+                    _io_dtype(q), float(scale), _ptr(workspace), _given(workspace, device),
                     _stream_handle(None, device))
     if rc != 0:
         raise CkdaError(rc, "ckda_bwd")
@@ -644,6 +670,8 @@ def decode_step_raw(q_raw, k_raw, v, a_raw, b_raw, state, scale=1.0, normalize_q
     _check(state, "state", torch.float32, (B, H, dk, dv), device)
     if o is None:
         o = torch.empty((B, H, dv), dtype=dt, device=device)
+    else:
+        _check(o, "o", dt, (B, H, dv), device)
     rc = L.ckda_decode_step_raw(_ptr(q_raw), _ptr(k_raw), _ptr(v), _ptr(a_raw), _ptr(b_raw),
                                 _ptr(state), _ptr(o), B, H, dk, dv, _io_dtype(q_raw),
                                 float(scale), int(bool(normalize_q)), float(norm_eps),
@@ -662,6 +690,8 @@ def _addr(t):
 
 def _call(fn, where, device, *args):
     """fn(*args, current stream) on the tensors' device; raises CkdaError."""
+    if device.type != "cuda":
+        raise ValueError(f"tensors on {device}, expected CUDA")
     handle = torch._C._cuda_getCurrentRawStream(device.index)
     if device.index == torch._C._cuda_getDevice():
         rc = fn(*args, handle)
@@ -745,7 +775,7 @@ def linear_fwd(q, k, v, g, h0=None, cu_seqlens=None, scale=1.0, store_final_stat
             dtype=torch.uint8, device=device)
     _call(L.ckda_linear_fwd, "ckda_linear_fwd", device, _addr(q), _addr(k), _addr(v),
           _addr(g), int(per_head), _addr(h0), _addr(o), _addr(hT), _addr(cu_seqlens), nseq, B,
-          H, Hk, T, dk, dv, io, float(scale), _addr(workspace), workspace.numel())
+          H, Hk, T, dk, dv, io, float(scale), _addr(workspace), _given(workspace, device))
     linear_fwd.last_workspace = workspace
     return o, hT
 
@@ -772,7 +802,7 @@ def linear_bwd(q, k, v, g, do, h0=None, dhT=None, cu_seqlens=None, scale=1.0, st
     _call(L.ckda_linear_bwd, "ckda_linear_bwd", device, _addr(q), _addr(k), _addr(v),
           _addr(g), int(per_head), _addr(h0), _addr(do), _addr(dhT), _addr(dq), _addr(dkk),
           _addr(dvv), _addr(dg), _addr(dh0), _addr(cu_seqlens), nseq, B, H, Hk, T, dk, dv, io,
-          float(scale), _addr(workspace), workspace.numel())
+          float(scale), _addr(workspace), _given(workspace, device))
     linear_bwd.last_workspace = workspace
     return dq, dkk, dvv, dg, dh0
 
@@ -888,7 +918,8 @@ def layernorm_bwd(dy, x, mean, rstd, weight=None, weight_grad=True, dx=None, wor
                                     dtype=torch.uint8, device=device)
     _call(L.ckda_layernorm_bwd, "ckda_layernorm_bwd", device, _addr(dy), _addr(x),
           _addr(mean), _addr(rstd), _addr(weight), _addr(dx), _addr(dw), _addr(db), rows, width,
-          io, wcode, _addr(workspace), 0 if workspace is None else workspace.numel())
+          io, wcode, _addr(workspace),
+          0 if workspace is None else _given(workspace, device))
     return dx, dw, db
 
 
