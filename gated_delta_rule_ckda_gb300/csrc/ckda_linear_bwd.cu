@@ -449,7 +449,7 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
       const float* g = a.g_head ? a.g + u.h : a.g + (size_t)u.vz * a.T + u.y;
       const float4 x = load_decays(g, a.g_head ? 0 : 1, u.valid, lane);
       if (block != blockIdx.x && !warp_wait(bars + B_GFREE, par ^ 1, abort)) break;
-      make_gates(gates, x, lane);
+      make_gates<true>(gates, x, lane);
       const float4 pre = reinterpret_cast<const float4*>(gates->pre)[lane];
       reinterpret_cast<float4*>(ep)[lane] = make_float4(ex2(pre.x), ex2(pre.y), ex2(pre.z), ex2(pre.w));
       __syncwarp();
@@ -498,8 +498,8 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
         warp_arrive(bars + B_HG);
       }
       if (!warp_wait(bars + B_G, par, abort)) break;
-      const float pre = gates->pre[row], es = gates->es[row];
-      const float into = a.scale * gates->eL[row], out = gates->w[row], s = a.scale;
+      const float pre = gates->pre[row], pre_lo = gates->lo[row], es = gates->es[row];
+      const float into = a.scale * from_start(gates, row), out = gates->w[row], s = a.scale;
       // own, own_p: s do_i.v_i (A, B) and s q_i.k_i (A; C has it in own)
       float wsum = 0.f, dot = 0.f, own = 0.f, own_p = 0.f;
       if (wg == 0) {
@@ -539,13 +539,16 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float4 g = reinterpret_cast<const float4*>(gates->pre + 32 * wq)[e];
-            const float gg[4] = {g.x, g.y, g.z, g.w};
+            const float4 r = reinterpret_cast<const float4*>(gates->lo + 32 * wq)[e];
+            const float2 g0 = gaps(g.x, g.y, r.x, r.y, -pre, -pre_lo);
+            const float2 g1 = gaps(g.z, g.w, r.z, r.w, -pre, -pre_lo);
+            const float gg[4] = {g0.x, g0.y, g1.x, g1.y};  // from this row to those
             float v[4];
 #pragma unroll
             for (int z = 0; z < 4; ++z) {
               const int j = 4 * e + z;
               const float dp = s * __uint_as_float(d[j]);
-              v[z] = j < lane ? dp * ex2(pre - gg[z]) : 0.f;
+              v[z] = j < lane ? dp * ex2(-gg[z]) : 0.f;
               if (j < lane) wsum = fmaf(v[z], __uint_as_float(x[j]), wsum);
               if (j == lane) {
                 own = dp;
@@ -604,13 +607,16 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float4 g = reinterpret_cast<const float4*>(gates->pre + 32 * wq)[e];
-            const float gg[4] = {g.x, g.y, g.z, g.w};
+            const float4 r = reinterpret_cast<const float4*>(gates->lo + 32 * wq)[e];
+            const float2 g0 = gaps(g.x, g.y, r.x, r.y, -pre, -pre_lo);
+            const float2 g1 = gaps(g.z, g.w, r.z, r.w, -pre, -pre_lo);
+            const float gg[4] = {g0.x, g0.y, g1.x, g1.y};  // from this row to those
             float v[4];
 #pragma unroll
             for (int z = 0; z < 4; ++z) {
               const int i = 4 * e + z;
               const float dp = s * __uint_as_float(d[i]);
-              v[z] = i > lane ? dp * ex2(gg[z] - pre) : 0.f;
+              v[z] = i > lane ? dp * ex2(gg[z]) : 0.f;
               if (i > lane) wsum = fmaf(v[z], __uint_as_float(x[i]), wsum);
               if (i == lane) own = dp;
             }
@@ -695,7 +701,7 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
       // B hands its sums by token to A, over decays that all three have read
       if (wg == 1) {
         if (!warp_wait(bars + B_DSA, par, abort) || !warp_wait(bars + B_DSC, par, abort)) break;
-        gates->eL[row] = in ? wsum : 0.f;
+        gates->lo[row] = in ? wsum : 0.f;
         gates->w[row] = in ? dot : 0.f;
       }
       if (wg != 1) {
@@ -710,7 +716,7 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
       }
       if (!warp_wait(bars + B_PART, par, abort)) break;
       float fwd = gates->w[row];
-      float back = in ? dot + wsum - gates->eL[row] : 0.f;
+      float back = in ? dot + wsum - gates->lo[row] : 0.f;
 #pragma unroll
       for (int m = 1; m < 32; m <<= 1) {
         const float x = __shfl_up_sync(0xffffffffu, fwd, m);

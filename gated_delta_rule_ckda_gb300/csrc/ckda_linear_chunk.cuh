@@ -234,49 +234,91 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
 // Factors of a chunk of 128 tokens in four blocks of 32, from log2 decays x_t
 // (zero past the end).  Sums run inside a block and over whole blocks, each
 // from the side it is read from, so that no factor is the exponential of a
-// difference of large sums:
+// difference of large sums, but for the pairs inside a block:
 //   pre_t  sum of x over the block's tokens up to t
+//   eL_t   exp2 of the sum from the chunk's start to t; or, with LO, in its place
+//   lo_t   what the roundings of pre_t left: a block of 32 may hold resets of -160 each,
+//          and pre_i - pre_j alone gives the mild decays behind four of them an error of
+//          1e-4, behind sixteen 4e-4.  The decay's gradient is fp32 and takes the second
+//          sum; o is bf16, its P rounded by up to 2e-3, and does without (forward of
+//          4 x 32 x 8192 208 us, with it 216)
 //   es_t   exp2 of the sum over the block's tokens after t
-//   eL_t   exp2 of the sum from the chunk's start to t
 //   w_t    exp2 of the sum after t to the chunk's end
 //   tot_b  sum over block b;   all = exp2 of the sum over the chunk
 struct Gates {
-  float pre[C], es[C], eL[C], w[C];
+  float pre[C];
+  union {
+    float eL[C], lo[C];
+  };
+  float es[C], w[C];
   float tot[4];
   float all;
   float pad[3];
 };
+// eL_t where lo has its place.
+__device__ __forceinline__ float from_start(const Gates* g, int t) {
+  float x = 0.f;
+  for (int b = 0; b < t >> 5; ++b) x += g->tot[b];
+  return ex2(x + g->pre[t]);
+}
+// A sum and the error of its rounding, joined to those of its terms.
+template <bool LO>
+__device__ __forceinline__ float2 add_pair(float2 a, float2 b) {
+  if (!LO) return make_float2(a.x + b.x, 0.f);
+  const float s = a.x + b.x, t = s - a.x;
+  return make_float2(s, (a.x - (s - t)) + (b.x - t) + (a.y + b.y));
+}
+// (q + p) + (r + l) for two columns, an instruction for both.
+__device__ __forceinline__ float2 gaps(float qx, float qy, float rx, float ry, float p, float l) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%6, %6};\n"
+      " add.rn.f32x2 a, a, b;\n mov.b64 b, {%4, %5};\n mov.b64 c, {%7, %7};\n"
+      " add.rn.f32x2 b, b, c;\n add.rn.f32x2 a, a, b;\n mov.b64 {%0, %1}, a;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(qx), "f"(qy), "f"(rx), "f"(ry), "f"(p), "f"(l));
+  return d;
+}
 // One warp: lane l brings tokens 4l .. 4l+3.
+template <bool LO>
 __device__ __forceinline__ void make_gates(Gates* g, float4 x, int lane) {
-  const float p0 = x.x, p1 = p0 + x.y, p2 = p1 + x.z, sum = p2 + x.w;
+  const float2 p0 = make_float2(x.x, 0.f), p1 = add_pair<LO>(p0, make_float2(x.y, 0.f));
+  const float2 p2 = add_pair<LO>(p1, make_float2(x.z, 0.f)), sum = add_pair<LO>(p2, make_float2(x.w, 0.f));
   const float s2 = x.w, s1 = x.z + s2, s0 = x.y + s1;
-  float up = sum, down = sum;  // inclusive scans over the block's eight lanes
+  float2 up = sum;  // inclusive scans over the block's eight lanes
+  float down = sum.x;
 #pragma unroll
   for (int m = 1; m < 8; m <<= 1) {
-    const float a = __shfl_up_sync(0xffffffffu, up, m, 8);
+    const float2 a = make_float2(__shfl_up_sync(0xffffffffu, up.x, m, 8),
+                                 LO ? __shfl_up_sync(0xffffffffu, up.y, m, 8) : 0.f);
     const float b = __shfl_down_sync(0xffffffffu, down, m, 8);
-    if ((lane & 7) >= m) up += a;
+    if ((lane & 7) >= m) up = add_pair<LO>(up, a);
     if ((lane & 7) + m < 8) down += b;
   }
   // exclusive: shifted, not subtracted
-  float before = __shfl_up_sync(0xffffffffu, up, 1, 8);
+  float2 before = make_float2(__shfl_up_sync(0xffffffffu, up.x, 1, 8),
+                              LO ? __shfl_up_sync(0xffffffffu, up.y, 1, 8) : 0.f);
   float after = __shfl_down_sync(0xffffffffu, down, 1, 8);
-  if ((lane & 7) == 0) before = 0.f;
+  if ((lane & 7) == 0) before = make_float2(0.f, 0.f);
   if ((lane & 7) == 7) after = 0.f;
-  const float tot = __shfl_sync(0xffffffffu, up, 7, 8);
+  const float tot = __shfl_sync(0xffffffffu, up.x, 7, 8);
   const float t0 = __shfl_sync(0xffffffffu, tot, 0), t1 = __shfl_sync(0xffffffffu, tot, 8);
   const float t2 = __shfl_sync(0xffffffffu, tot, 16), t3 = __shfl_sync(0xffffffffu, tot, 24);
   const int b = lane >> 3;
-  const float earlier = b == 0 ? 0.f : b == 1 ? t0 : b == 2 ? t0 + t1 : t0 + t1 + t2;
   const float later = b == 3 ? 0.f : b == 2 ? t3 : b == 1 ? t3 + t2 : t3 + t2 + t1;
-  const float4 pre = make_float4(before + p0, before + p1, before + p2, before + sum);
+  const float2 q0 = add_pair<LO>(before, p0), q1 = add_pair<LO>(before, p1), q2 = add_pair<LO>(before, p2);
+  const float2 q3 = add_pair<LO>(before, sum);
   const float4 suf = make_float4(after + s0, after + s1, after + s2, after);
-  reinterpret_cast<float4*>(g->pre)[lane] = pre;
+  reinterpret_cast<float4*>(g->pre)[lane] = make_float4(q0.x, q1.x, q2.x, q3.x);
+  if (LO) {
+    reinterpret_cast<float4*>(g->lo)[lane] = make_float4(q0.y, q1.y, q2.y, q3.y);
+  } else {
+    const float earlier = b == 0 ? 0.f : b == 1 ? t0 : b == 2 ? t0 + t1 : t0 + t1 + t2;
+    reinterpret_cast<float4*>(g->eL)[lane] =
+        make_float4(ex2(earlier + q0.x), ex2(earlier + q1.x), ex2(earlier + q2.x),
+                    ex2(earlier + q3.x));
+  }
   reinterpret_cast<float4*>(g->es)[lane] =
       make_float4(ex2(suf.x), ex2(suf.y), ex2(suf.z), ex2(suf.w));
-  reinterpret_cast<float4*>(g->eL)[lane] =
-      make_float4(ex2(earlier + pre.x), ex2(earlier + pre.y), ex2(earlier + pre.z),
-                  ex2(earlier + pre.w));
   reinterpret_cast<float4*>(g->w)[lane] =
       make_float4(ex2(later + suf.x), ex2(later + suf.y), ex2(later + suf.z),
                   ex2(later + suf.w));

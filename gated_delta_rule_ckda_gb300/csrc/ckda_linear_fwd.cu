@@ -211,7 +211,7 @@ linear_fwd_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ 
     float4 x = load_decays(g, gs, min(len, C), lane);
     for (int c = 0; c < chunks; ++c) {
       if (c > 0 && !warp_wait(bars + B_GFREE, (c - 1) & 1, abort)) break;
-      make_gates(gates, x, lane);
+      make_gates<false>(gates, x, lane);
       __syncwarp();
       if (lane == 0) mbar_arrive(bars + B_G);
       if (c + 1 < chunks)

@@ -135,7 +135,7 @@ linear_state_kernel(const __grid_constant__ LinearArgs a, const __grid_constant_
       const int c = at(i);
       const float4 x = load_decays(g + (size_t)c * C * gs, gs, min(len - c * C, C), lane);
       if (i >= 1 && !warp_wait(bars + B_GFREE, (i - 1) & 1, abort)) break;
-      make_gates(gates, x, lane);
+      make_gates<false>(gates, x, lane);
       __syncwarp();
       if (lane == 0) mbar_arrive(bars + B_G);
     }
