@@ -927,6 +927,34 @@ def layernorm_bwd(dy, x, mean, rstd, weight=None, weight_grad=True, dx=None, wor
 # Training use: the forward (fwd) with its backward (bwd), and the input
 # preparation (prep) with its backward (prep_bwd), as torch.autograd
 # functions.  They only route tensors between the calls above.
+#
+# None has a second derivative.  Where one would be needed (create_graph=True), the gradients
+# are tied to whatever they depend on, with an error in place of a derivative; without the tie
+# they would count as constants.
+class _NoDerivative(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, n, *tensors):
+        return tuple(t.view_as(t) for t in tensors[:n])
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("the gradients of this library's calls have no second derivative")
+
+
+def _once(backward):
+    @functools.wraps(backward)
+    def wrapped(ctx, *grads):
+        with torch.no_grad():
+            outs = list(backward(ctx, *grads))
+        if torch.is_grad_enabled():
+            have = [i for i, t in enumerate(outs) if t is not None]
+            behind = [t for t in (*grads, *ctx.saved_tensors) if t is not None]
+            tied = _NoDerivative.apply(len(have), *(outs[i] for i in have), *behind)
+            for i, t in zip(have, tied):
+                outs[i] = t
+        return tuple(outs)
+    return wrapped
+
 
 class _Recurrence(torch.autograd.Function):
     @staticmethod
@@ -937,6 +965,7 @@ class _Recurrence(torch.autograd.Function):
         return o, hT
 
     @staticmethod
+    @_once
     def backward(ctx, do, dhT):
         q, k, v, alpha, beta, h0, cu = ctx.saved_tensors
         do = torch.zeros_like(v) if do is None else do.contiguous()
@@ -962,6 +991,7 @@ class _Prepare(torch.autograd.Function):
         return q, k, alpha, beta
 
     @staticmethod
+    @_once
     def backward(ctx, dq, dk, dalpha, dbeta):
         q_raw, k_raw, a_raw, b_raw = ctx.saved_tensors
         z = lambda g, like: torch.zeros_like(like) if g is None else g.contiguous()
@@ -987,6 +1017,7 @@ class _LinearAttention(torch.autograd.Function):
         return o, hT
 
     @staticmethod
+    @_once
     def backward(ctx, do, dhT):
         q, k, v, g, h0, cu = ctx.saved_tensors
         do = torch.zeros_like(v) if do is None else do.contiguous()
@@ -1011,6 +1042,7 @@ class _LayerNorm(torch.autograd.Function):
         return y
 
     @staticmethod
+    @_once
     def backward(ctx, dy):
         x, mean, rstd, weight = ctx.saved_tensors
         need = (weight is not None and ctx.needs_input_grad[1]) or \
