@@ -630,7 +630,8 @@ ckda_status check_norm(long long rows, int width, ckda_dtype io, ckda_dtype wt) 
   if (io != CKDA_F32 && io != CKDA_BF16) return CKDA_ERR_INVALID_ARG;
   if (wt != CKDA_F32 && wt != CKDA_BF16) return CKDA_ERR_INVALID_ARG;
   if (rows < 0 || width < 1) return CKDA_ERR_INVALID_ARG;
-  if (rows > 0x7fffffffLL) return CKDA_ERR_UNSUPPORTED;
+  // (columns are counted in 32 bits, up to a block's step past the row)
+  if (rows > 0x7fffffffLL || width > 1 << 30) return CKDA_ERR_UNSUPPORTED;
   return CKDA_OK;
 }
 

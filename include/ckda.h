@@ -547,9 +547,9 @@ ckda_status ckda_linear_decode_step(const void *q, const void *k, const void *v,
  *   x, y         : io [rows, width]; y may alias x
  *   weight, bias : weight_dtype [width], each may be NULL (one, zero)
  *   mean, rstd   : fp32 [rows], for the backward pass
- * Arithmetic in fp32 with one rounding to io_dtype.  Rows of any width; 16-byte
- * aligned rows (width a multiple of 8 in bf16, 4 in fp32, and aligned bases) are
- * moved in 16-byte vectors.  rows = 0 launches nothing.
+ * Arithmetic in fp32 with one rounding to io_dtype.  Up to 2^31 - 1 rows of any
+ * width up to 2^30; 16-byte aligned rows (width a multiple of 8 in bf16, 4 in fp32,
+ * and aligned bases) are moved in 16-byte vectors.  rows = 0 launches nothing.
  */
 ckda_status ckda_layernorm_fwd(const void *x, const void *weight, const void *bias, void *y,
                                float *mean, float *rstd, long long rows, int width,
