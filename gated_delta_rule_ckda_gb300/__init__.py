@@ -121,12 +121,13 @@ def lib():
             L.ckda_fwd_split.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32,
                                          i32, f32, i32, vp, sz, vp]
             lin = [vp, vp, vp, vp, i32, vp]
-            L.ckda_linear_fwd_workspace_bytes.restype = sz
-            L.ckda_linear_fwd_workspace_bytes.argtypes = [i32] * 7
+            for n, fn in ((7, L.ckda_linear_fwd_workspace_bytes),
+                          (7, L.ckda_linear_fwd_aligned_workspace_bytes),
+                          (8, L.ckda_linear_bwd_workspace_bytes),
+                          (8, L.ckda_linear_bwd_aligned_workspace_bytes)):
+                fn.restype, fn.argtypes = sz, [i32] * n
             L.ckda_linear_fwd.restype = i32
             L.ckda_linear_fwd.argtypes = lin + [vp] * 3 + [i32] * 8 + [f32, vp, sz, vp]
-            L.ckda_linear_bwd_workspace_bytes.restype = sz
-            L.ckda_linear_bwd_workspace_bytes.argtypes = [i32] * 8
             L.ckda_linear_bwd.restype = i32
             L.ckda_linear_bwd.argtypes = lin + [vp] * 8 + [i32] * 8 + [f32, vp, sz, vp]
             L.ckda_linear_decode_step.restype = i32
@@ -738,6 +739,15 @@ def _check_linear(q, k, v, g, cu_seqlens, states, more=()):
     return B, H, Hk, T, dk, dv, N, per_head, io
 
 
+def _bytes_by_base(name, tensors, *args):
+    """Workspace of a call on these tensors: the bytes for 16-byte aligned ones, which are far
+    fewer where the tensor-core kernels take them, or for any."""
+    at = 0
+    for t in tensors:
+        at |= t.data_ptr()
+    return _bytes(name % ("" if at & 15 else "_aligned"), *args)
+
+
 def linear_fwd_workspace_bytes(B, H, T, dk, dv, dtype=torch.bfloat16, num_seqs=0) -> int:
     io = _BF16 if dtype == torch.bfloat16 else _F32
     return _bytes("ckda_linear_fwd_workspace_bytes", num_seqs, B, H, T, dk, dv, io)
@@ -771,7 +781,8 @@ def linear_fwd(q, k, v, g, h0=None, cu_seqlens=None, scale=1.0, store_final_stat
     nseq = N if cu_seqlens is not None else 0
     if workspace is None:
         workspace = torch.empty(
-            _bytes("ckda_linear_fwd_workspace_bytes", nseq, B, H, T, dk, dv, io),
+            _bytes_by_base("ckda_linear_fwd%s_workspace_bytes", (q, k, v, o), nseq, B, H, T, dk, dv,
+                           io),
             dtype=torch.uint8, device=device)
     _call(L.ckda_linear_fwd, "ckda_linear_fwd", device, _addr(q), _addr(k), _addr(v),
           _addr(g), int(per_head), _addr(h0), _addr(o), _addr(hT), _addr(cu_seqlens), nseq, B,
@@ -794,7 +805,8 @@ def linear_bwd(q, k, v, g, do, h0=None, dhT=None, cu_seqlens=None, scale=1.0, st
     nseq = N if cu_seqlens is not None else 0
     if workspace is None:
         workspace = torch.empty(
-            _bytes("ckda_linear_bwd_workspace_bytes", nseq, B, H, Hk, T, dk, dv, io),
+            _bytes_by_base("ckda_linear_bwd%s_workspace_bytes", (q, k, v, do), nseq, B, H, Hk, T,
+                           dk, dv, io),
             dtype=torch.uint8, device=device)
     dq, dkk, dvv, dg = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v),
                         torch.empty_like(g))

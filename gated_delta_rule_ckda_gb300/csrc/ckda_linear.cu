@@ -5,9 +5,8 @@
 namespace ckda {
 namespace {
 
-ckda_status check(int N, int B, int H, int Hk, int T, int dk, int dv, ckda_dtype io, float scale,
+ckda_status check(int B, int H, int Hk, int T, int dk, int dv, ckda_dtype io, float scale,
                   const int32_t* cu, int num_seqs) {
-  (void)N;
   if (io != CKDA_F32 && io != CKDA_BF16) return CKDA_ERR_INVALID_ARG;
   if (B < 1 || H < 1 || Hk < 1 || H % Hk != 0 || T < 0 || dk < 1 || dv < 1)
     return CKDA_ERR_INVALID_ARG;
@@ -28,6 +27,23 @@ size_t head_bytes(int num_seqs) {  // status word, order of packed sequences
   return kWsStatusBytes + (n * sizeof(int32_t) + 255) / 256 * 256;
 }
 
+// Of a call on the tensor cores (chunked) or on CUDA cores.
+size_t fwd_bytes(bool chunked, int num_seqs, int B, int H, int T, int dk, int dv) {
+  if (num_seqs < 0 || B < 1 || H < 1 || T < 0 || dk < 1 || dv < 1) return 0;
+  const int N = num_seqs > 0 ? num_seqs : B;
+  return head_bytes(num_seqs) +
+         (chunked ? linear_chunk_fwd_bytes(N, B, H, T, dk, dv, num_seqs > 0)
+                  : linear_serial_fwd_bytes(N, H, T, dk, dv, num_seqs > 0));
+}
+size_t bwd_bytes(bool chunked, int num_seqs, int B, int H, int Hk, int T, int dk, int dv) {
+  if (num_seqs < 0 || B < 1 || H < 1 || Hk < 1 || T < 0 || dk < 1 || dv < 1) return 0;
+  const int N = num_seqs > 0 ? num_seqs : B;
+  return head_bytes(num_seqs) +
+         (chunked ? linear_chunk_bwd_bytes(N, B, H, Hk, T, dk, dv, num_seqs > 0)
+                  : linear_serial_bwd_bytes(N, B, H, Hk, T, dk, dv, num_seqs > 0));
+}
+size_t most(size_t a, size_t b) { return a > b ? a : b; }
+
 }  // namespace
 }  // namespace ckda
 
@@ -37,15 +53,13 @@ extern "C" {
 
 size_t ckda_linear_fwd_workspace_bytes(int num_seqs, int B, int H, int T, int dk, int dv,
                                        ckda_dtype io_dtype) {
-  if (num_seqs < 0 || B < 1 || H < 1 || T < 0 || dk < 1 || dv < 1) return 0;
-  const int N = num_seqs > 0 ? num_seqs : B;
-  // what either path takes: which one runs depends on the pointers' alignment too
-  size_t bytes = linear_serial_fwd_bytes(N, H, T, dk, dv, num_seqs > 0);
-  if (linear_chunk_path(io_dtype, dk, dv)) {
-    const size_t chunk = linear_chunk_fwd_bytes(N, B, H, T, dk, dv, num_seqs > 0);
-    if (chunk > bytes) bytes = chunk;
-  }
-  return head_bytes(num_seqs) + bytes;
+  return most(fwd_bytes(false, num_seqs, B, H, T, dk, dv),
+              ckda_linear_fwd_aligned_workspace_bytes(num_seqs, B, H, T, dk, dv, io_dtype));
+}
+
+size_t ckda_linear_fwd_aligned_workspace_bytes(int num_seqs, int B, int H, int T, int dk, int dv,
+                                               ckda_dtype io_dtype) {
+  return fwd_bytes(linear_chunk_path(io_dtype, dk, dv), num_seqs, B, H, T, dk, dv);
 }
 
 ckda_status ckda_linear_fwd(const void* q, const void* k, const void* v, const float* g,
@@ -54,12 +68,13 @@ ckda_status ckda_linear_fwd(const void* q, const void* k, const void* v, const f
                             int dk, int dv, ckda_dtype io_dtype, float scale, void* workspace,
                             size_t workspace_bytes, void* stream) {
   const int N = cu_seqlens ? num_seqs : B;
-  const ckda_status st = check(N, B, H, Hk, T, dk, dv, io_dtype, scale, cu_seqlens, num_seqs);
+  const ckda_status st = check(B, H, Hk, T, dk, dv, io_dtype, scale, cu_seqlens, num_seqs);
   if (st != CKDA_OK) return st;
   if (T > 0 && (!q || !k || !v || !g || !o)) return CKDA_ERR_INVALID_ARG;
+  const bool chunked = linear_chunk_path(io_dtype, dk, dv) && aligned16(q) && aligned16(k) &&
+                       aligned16(v) && aligned16(o);
   if (!workspace ||
-      workspace_bytes < ckda_linear_fwd_workspace_bytes(cu_seqlens ? num_seqs : 0, B, H, T, dk, dv,
-                                                        io_dtype) ||
+      workspace_bytes < fwd_bytes(chunked, cu_seqlens ? num_seqs : 0, B, H, T, dk, dv) ||
       (reinterpret_cast<uintptr_t>(workspace) & 255) != 0)
     return CKDA_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -72,8 +87,7 @@ ckda_status ckda_linear_fwd(const void* q, const void* k, const void* v, const f
   a.scale = scale; a.io = io_dtype;
   char* scratch = static_cast<char*>(workspace) + head_bytes(cu_seqlens ? num_seqs : 0);
   cudaError_t e = cudaSuccess;
-  if (linear_chunk_path(io_dtype, dk, dv) && aligned16(q) && aligned16(k) && aligned16(v) &&
-      aligned16(o)) {
+  if (chunked) {
     a.clear = 1;
     if (cu_seqlens) {
       int32_t* order = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + kWsStatusBytes);
@@ -90,15 +104,13 @@ ckda_status ckda_linear_fwd(const void* q, const void* k, const void* v, const f
 
 size_t ckda_linear_bwd_workspace_bytes(int num_seqs, int B, int H, int Hk, int T, int dk, int dv,
                                        ckda_dtype io_dtype) {
-  if (num_seqs < 0 || B < 1 || H < 1 || Hk < 1 || T < 0 || dk < 1 || dv < 1) return 0;
-  const int N = num_seqs > 0 ? num_seqs : B;
-  // what either path takes: which one runs depends on the pointers' alignment too
-  size_t bytes = linear_serial_bwd_bytes(N, B, H, Hk, T, dk, dv, num_seqs > 0);
-  if (linear_chunk_path(io_dtype, dk, dv)) {
-    const size_t chunk = linear_chunk_bwd_bytes(N, B, H, Hk, T, dk, dv, num_seqs > 0);
-    if (chunk > bytes) bytes = chunk;
-  }
-  return head_bytes(num_seqs) + bytes;
+  return most(bwd_bytes(false, num_seqs, B, H, Hk, T, dk, dv),
+              ckda_linear_bwd_aligned_workspace_bytes(num_seqs, B, H, Hk, T, dk, dv, io_dtype));
+}
+
+size_t ckda_linear_bwd_aligned_workspace_bytes(int num_seqs, int B, int H, int Hk, int T, int dk,
+                                               int dv, ckda_dtype io_dtype) {
+  return bwd_bytes(linear_chunk_path(io_dtype, dk, dv), num_seqs, B, H, Hk, T, dk, dv);
 }
 
 ckda_status ckda_linear_bwd(const void* q, const void* k, const void* v, const float* g,
@@ -108,13 +120,15 @@ ckda_status ckda_linear_bwd(const void* q, const void* k, const void* v, const f
                             int dk, int dv, ckda_dtype io_dtype, float scale, void* workspace,
                             size_t workspace_bytes, void* stream) {
   const int N = cu_seqlens ? num_seqs : B;
-  const ckda_status st = check(N, B, H, Hk, T, dk, dv, io_dtype, scale, cu_seqlens, num_seqs);
+  const ckda_status st = check(B, H, Hk, T, dk, dv, io_dtype, scale, cu_seqlens, num_seqs);
   if (st != CKDA_OK) return st;
   if (T > 0 && (!q || !k || !v || !g || !dout || !dq || !dkey || !dval)) return CKDA_ERR_INVALID_ARG;
   if ((T > 0 || g_per_head) && !dg) return CKDA_ERR_INVALID_ARG;
+  const bool chunked = linear_chunk_path(io_dtype, dk, dv) && aligned16(q) && aligned16(k) &&
+                       aligned16(v) && aligned16(dout) && aligned16(dq) && aligned16(dkey) &&
+                       aligned16(dval);
   if (!workspace ||
-      workspace_bytes < ckda_linear_bwd_workspace_bytes(cu_seqlens ? num_seqs : 0, B, H, Hk, T, dk, dv,
-                                                        io_dtype) ||
+      workspace_bytes < bwd_bytes(chunked, cu_seqlens ? num_seqs : 0, B, H, Hk, T, dk, dv) ||
       (reinterpret_cast<uintptr_t>(workspace) & 255) != 0)
     return CKDA_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -130,8 +144,7 @@ ckda_status ckda_linear_bwd(const void* q, const void* k, const void* v, const f
   if (cudaMemsetAsync(workspace, 0, sizeof(int), s) != cudaSuccess) return CKDA_ERR_CUDA;
   char* scratch = static_cast<char*>(workspace) + head_bytes(cu_seqlens ? num_seqs : 0);
   cudaError_t e = cudaSuccess;
-  if (linear_chunk_path(io_dtype, dk, dv) && aligned16(q) && aligned16(k) && aligned16(v) &&
-      aligned16(dout) && aligned16(dq) && aligned16(dkey) && aligned16(dval)) {
+  if (chunked) {
     if (cu_seqlens) {
       int32_t* order = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + kWsStatusBytes);
       e = launch_seq_order(cu_seqlens, num_seqs, order, s);

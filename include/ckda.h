@@ -497,10 +497,15 @@ ckda_status ckda_prep_bwd(const void *q_raw, const void *k_raw, const void *a_ra
  * workspace: ckda_linear_fwd_workspace_bytes(cu_seqlens ? num_seqs : 0, ...)
  * bytes, 256-byte aligned, scratch with the status word ckda_fwd_status() reads
  * (CKDA_ERR_TIMEOUT only: a wait inside a kernel that ran out, results invalid).
- * Calls that overlap need a workspace each.
+ * Calls that overlap need a workspace each.  That is enough for pointers of any
+ * alignment; where q, k, v and o are 16-byte aligned, the bytes of
+ * ckda_linear_fwd_aligned_workspace_bytes are (4 x 32 x 8192 tokens of 128
+ * channels: 256 bytes, and 1.1 GB else).
  */
 size_t ckda_linear_fwd_workspace_bytes(int num_seqs, int B, int H, int T, int dk, int dv,
                                        ckda_dtype io_dtype);
+size_t ckda_linear_fwd_aligned_workspace_bytes(int num_seqs, int B, int H, int T, int dk, int dv,
+                                               ckda_dtype io_dtype);
 ckda_status ckda_linear_fwd(const void *q, const void *k, const void *v, const float *g,
                             int g_per_head, const float *h0, void *o, float *hT,
                             const int32_t *cu_seqlens, int num_seqs, int B, int H, int Hk,
@@ -518,10 +523,14 @@ ckda_status ckda_linear_fwd(const void *q, const void *k, const void *v, const f
  *   dh0         : fp32 [N, H, dk, dv] or NULL (not stored)
  *
  * The forward's states are recomputed.  No atomics: the same inputs give the
- * same bits.  workspace as above, of ckda_linear_bwd_workspace_bytes bytes.
+ * same bits.  workspace as above, of ckda_linear_bwd_workspace_bytes bytes, or
+ * where q, k, v, dout, dq, dkey and dval are 16-byte aligned of
+ * ckda_linear_bwd_aligned_workspace_bytes.
  */
 size_t ckda_linear_bwd_workspace_bytes(int num_seqs, int B, int H, int Hk, int T, int dk,
                                        int dv, ckda_dtype io_dtype);
+size_t ckda_linear_bwd_aligned_workspace_bytes(int num_seqs, int B, int H, int Hk, int T, int dk,
+                                               int dv, ckda_dtype io_dtype);
 ckda_status ckda_linear_bwd(const void *q, const void *k, const void *v, const float *g,
                             int g_per_head, const float *h0, const void *dout,
                             const float *dhT, void *dq, void *dkey, void *dval, float *dg,
