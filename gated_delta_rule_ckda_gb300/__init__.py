@@ -739,15 +739,6 @@ def _check_linear(q, k, v, g, cu_seqlens, states, more=()):
     return B, H, Hk, T, dk, dv, N, per_head, io
 
 
-def _bytes_by_base(name, tensors, *args):
-    """Workspace of a call on these tensors: the bytes for 16-byte aligned ones, which are far
-    fewer where the tensor-core kernels take them, or for any."""
-    at = 0
-    for t in tensors:
-        at |= t.data_ptr()
-    return _bytes(name % ("" if at & 15 else "_aligned"), *args)
-
-
 def linear_fwd_workspace_bytes(B, H, T, dk, dv, dtype=torch.bfloat16, num_seqs=0) -> int:
     io = _BF16 if dtype == torch.bfloat16 else _F32
     return _bytes("ckda_linear_fwd_workspace_bytes", num_seqs, B, H, T, dk, dv, io)
@@ -779,14 +770,16 @@ def linear_fwd(q, k, v, g, h0=None, cu_seqlens=None, scale=1.0, store_final_stat
     if store_final_state and hT is None:
         hT = torch.empty((N, H, dk, dv), dtype=torch.float32, device=device)
     nseq = N if cu_seqlens is not None else 0
+    pq, pk, pv, po = q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr()
     if workspace is None:
-        workspace = torch.empty(
-            _bytes_by_base("ckda_linear_fwd%s_workspace_bytes", (q, k, v, o), nseq, B, H, T, dk, dv,
-                           io),
-            dtype=torch.uint8, device=device)
-    _call(L.ckda_linear_fwd, "ckda_linear_fwd", device, _addr(q), _addr(k), _addr(v),
-          _addr(g), int(per_head), _addr(h0), _addr(o), _addr(hT), _addr(cu_seqlens), nseq, B,
-          H, Hk, T, dk, dv, io, float(scale), _addr(workspace), _given(workspace, device))
+        size = _bytes("ckda_linear_fwd_workspace_bytes" if (pq | pk | pv | po) & 15 else
+                      "ckda_linear_fwd_aligned_workspace_bytes", nseq, B, H, T, dk, dv, io)
+        workspace = torch.empty(size, dtype=torch.uint8, device=device)
+    else:
+        size = _given(workspace, device)
+    _call(L.ckda_linear_fwd, "ckda_linear_fwd", device, pq, pk, pv, g.data_ptr(), int(per_head),
+          _addr(h0), po, _addr(hT), _addr(cu_seqlens), nseq, B, H, Hk, T, dk, dv, io, float(scale),
+          workspace.data_ptr(), size)
     linear_fwd.last_workspace = workspace
     return o, hT
 
@@ -803,18 +796,20 @@ def linear_bwd(q, k, v, g, do, h0=None, dhT=None, cu_seqlens=None, scale=1.0, st
     B, H, Hk, T, dk, dv, N, per_head, io = _check_linear(q, k, v, g, cu_seqlens,
                                                          (("h0", h0), ("dhT", dhT)), (("do", do),))
     nseq = N if cu_seqlens is not None else 0
+    pq, pk, pv, pdo = q.data_ptr(), k.data_ptr(), v.data_ptr(), do.data_ptr()
     if workspace is None:
-        workspace = torch.empty(
-            _bytes_by_base("ckda_linear_bwd%s_workspace_bytes", (q, k, v, do), nseq, B, H, Hk, T,
-                           dk, dv, io),
-            dtype=torch.uint8, device=device)
+        size = _bytes("ckda_linear_bwd_workspace_bytes" if (pq | pk | pv | pdo) & 15 else
+                      "ckda_linear_bwd_aligned_workspace_bytes", nseq, B, H, Hk, T, dk, dv, io)
+        workspace = torch.empty(size, dtype=torch.uint8, device=device)
+    else:
+        size = _given(workspace, device)
     dq, dkk, dvv, dg = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v),
                         torch.empty_like(g))
     dh0 = torch.empty((N, H, dk, dv), dtype=torch.float32, device=device) if store_dh0 else None
-    _call(L.ckda_linear_bwd, "ckda_linear_bwd", device, _addr(q), _addr(k), _addr(v),
-          _addr(g), int(per_head), _addr(h0), _addr(do), _addr(dhT), _addr(dq), _addr(dkk),
-          _addr(dvv), _addr(dg), _addr(dh0), _addr(cu_seqlens), nseq, B, H, Hk, T, dk, dv, io,
-          float(scale), _addr(workspace), _given(workspace, device))
+    _call(L.ckda_linear_bwd, "ckda_linear_bwd", device, pq, pk, pv, g.data_ptr(), int(per_head),
+          _addr(h0), pdo, _addr(dhT), dq.data_ptr(), dkk.data_ptr(), dvv.data_ptr(), dg.data_ptr(),
+          _addr(dh0), _addr(cu_seqlens), nseq, B, H, Hk, T, dk, dv, io, float(scale),
+          workspace.data_ptr(), size)
     linear_bwd.last_workspace = workspace
     return dq, dkk, dvv, dg, dh0
 
