@@ -175,7 +175,7 @@ __device__ __forceinline__ void load_image(uint32_t dst, const char* src, uint64
     asm volatile(
         "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, "
         "[%3];" ::"r"(dst + p * kPanel),
-        "l"(src + p * kPanel), "r"(VP * (kPanel / 2)), "r"(smem_u32(bar))
+        "l"(src + p * (VP * kPanel / 2)), "r"(VP * (kPanel / 2)), "r"(smem_u32(bar))
         : "memory");
 }
 
@@ -308,8 +308,8 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
       unsigned block = blockIdx.x;
       for (; block < blocks; block += step, par ^= 1, begun = 0) {
         const Chunk u = chunk_of(a, w, block);
-        const char* himg = w.himg + (size_t)block * kImage;
-        const char* gimg = w.gimg + (size_t)block * kImage;
+        const char* himg = w.himg + (size_t)block * 2 * kPart;
+        const char* gimg = w.gimg + (size_t)block * 2 * kPart;
         const bool again = block != blockIdx.x;
         bool ok = true;
         // a barrier of the chunk before, whose tile is wanted
@@ -334,13 +334,13 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
         if (!ok) { *abort = 1; break; }
         mbar_arrive_expect_tx(bars + B_H, 2 * kPart);
         load_image<KP, VP>(sb + kS0, himg, bars + B_H);
-        load_image<KP, VP>(sb + kS1, himg + kTile, bars + B_H);
+        load_image<KP, VP>(sb + kS1, himg + kPart, bars + B_H);
         mbar_arrive_expect_tx(bars + B_GH, kPart);
         load_image<KP, VP>(sb + kS2, gimg, bars + B_GH);
         begun = 3;
         if (!mbar_wait(bars + B_X1L, par) || !mbar_wait(bars + B_HG, par)) { *abort = 1; break; }
         mbar_arrive_expect_tx(bars + B_GL, kPart);  // Hlo has been read
-        load_image<KP, VP>(sb + kS1, gimg + kTile, bars + B_GL);
+        load_image<KP, VP>(sb + kS1, gimg + kPart, bars + B_GL);
         begun = 4;
         // What comes next, into L2 while this chunk is worked on: tiles come free
         // late, and their loads should not wait for HBM then.
@@ -350,12 +350,11 @@ linear_grad_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__
           prefetch_tile(&mk, v.y, v.qz, a.dk);
           prefetch_tile(&mv, v.y, v.vz, a.dv);
           prefetch_tile(&mo, v.y, v.vz, a.dv);
-          for (int z = 0; z < 2; ++z)
-            for (int x = 0; x < KP; ++x) {
-              const size_t at = (size_t)(block + step) * kImage + z * kTile + x * kPanel;
-              prefetch_bytes(w.himg + at, VP * kPanel / 2);
-              prefetch_bytes(w.gimg + at, VP * kPanel / 2);
-            }
+          for (int z = 0; z < 2 * KP; ++z) {
+            const size_t at = (size_t)(block + step) * 2 * kPart + z * (VP * kPanel / 2);
+            prefetch_bytes(w.himg + at, VP * kPanel / 2);
+            prefetch_bytes(w.gimg + at, VP * kPanel / 2);
+          }
         }
       }
       // (none is left in flight, whatever the others do)
@@ -772,8 +771,8 @@ ChunkPlan chunk_plan(int N, int B, int H, int Hk, int T, int dk, int dv, bool pa
   p.chunks = packed ? (size_t)T / C + N : (size_t)N * ((T + C - 1) / C);
   const size_t rows = (size_t)B * H * T;
   size_t at = 0;
-  p.himg = at; at += p.chunks * H * kImage;
-  p.gimg = at; at += p.chunks * H * kImage;
+  p.himg = at; at += p.chunks * H * image_bytes(dk, dv);
+  p.gimg = at; at += p.chunks * H * image_bytes(dk, dv);
   p.dg = at; at += up256(rows * 4);
   p.dq = at; at += Hk == H ? 0 : up256(rows * dk * 2);
   p.dk = at; at += Hk == H ? 0 : up256(rows * dk * 2);

@@ -12,6 +12,12 @@ constexpr int C = 128;                 // tokens of a chunk
 constexpr uint32_t kTile = 32768;      // bytes of a 128 x 128 bf16 tile, two 64-column panels
 constexpr uint32_t kPanel = 16384;
 constexpr uint32_t kImage = 2 * kTile; // a state: hi tile, lo tile, [dv][dk], swizzled
+// In memory an image has the panels of its hi part, then of its lo part, one behind the
+// other, and of a panel only the 64 value rows where there are no more.
+__host__ __device__ inline uint32_t panel_bytes(int dv) { return dv > 64 ? kPanel : kPanel / 2; }
+__host__ __device__ inline uint32_t image_bytes(int dk, int dv) {
+  return 2 * (dk > 64 ? 2 : 1) * panel_bytes(dv);
+}
 
 // Sequences are cut into segments where there are too few (sequence, head)s for
 // the SMs, or one is much longer than an SM's share.  The state entering each

@@ -196,11 +196,9 @@ linear_state_kernel(const __grid_constant__ LinearArgs a, const __grid_constant_
         fence_proxy_async_smem();
         named_sync(1, 256);
         if (tid == 256)
-          for (int z = 0; z < 2 * KP; ++z) {  // (part, panel)
-            const uint32_t off = z / KP * kTile + z % KP * kPanel;
-            store_bytes(images.img + slot * kImage + off, sb + kStage + off,
-                        a.dv > 64 ? kPanel : kPanel / 2);
-          }
+          for (int z = 0; z < 2 * KP; ++z)  // (part, panel)
+            store_bytes(images.img + (slot * 2 * KP + z) * panel_bytes(a.dv),
+                        sb + kStage + z / KP * kTile + z % KP * kPanel, panel_bytes(a.dv));
       }
       if (i >= steps) break;
       if (!(ok = warp_wait(bars + B_G, p, abort))) break;

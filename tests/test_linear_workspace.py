@@ -107,3 +107,15 @@ def test_calls_on_workspaces_of_just_their_bytes(ck, T):
         ref.check(hT, want[1], ref.state_tol(torch.bfloat16, T), "hT")
         ref.check(grads[3], want[5], ref.decay_tol(torch.bfloat16, T), "dg")
         ref.check(grads[4], want[6], ref.state_tol(torch.bfloat16, T), "dh0")
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (8, 40), (128, 64), (72, 48), (64, 128), (128, 128)])
+def test_states_of_narrow_heads_take_no_more_than_their_panels(ck, dk, dv):
+    """A state crosses memory in two bf16 parts and both directions, rounded up to panels of 64
+    channels by 64 values; for single tokens the rest of the workspace is small beside it."""
+    L = ck.lib()
+    B, H = 512, 32
+    panels = -(-dk // 64) * -(-dv // 64)
+    states = B * H * 2 * 2 * panels * 64 * 64 * 2
+    need = L.ckda_linear_bwd_aligned_workspace_bytes(0, B, H, H, 1, dk, dv, BF16)
+    assert states <= need <= 1.01 * states + 4096
