@@ -739,6 +739,13 @@ def _check_linear(q, k, v, g, cu_seqlens, states, more=()):
     return B, H, Hk, T, dk, dv, N, per_head, io
 
 
+# A call's last_workspace is for fwd_status.  What the call made for itself is given back before
+# the next is made where it is more than _SMALL, and at the call's end, all but the status word,
+# where it is more than _LARGE: that copy takes 4 us, a call on so much memory over a
+# millisecond (on 268 MB, the backward of 8 x 16 x 2048, it would be 272 us and 276).
+_SMALL, _LARGE = 1 << 20, 1 << 30
+
+
 def linear_fwd_workspace_bytes(B, H, T, dk, dv, dtype=torch.bfloat16, num_seqs=0) -> int:
     io = _BF16 if dtype == torch.bfloat16 else _F32
     return _bytes("ckda_linear_fwd_workspace_bytes", num_seqs, B, H, T, dk, dv, io)
@@ -771,16 +778,19 @@ def linear_fwd(q, k, v, g, h0=None, cu_seqlens=None, scale=1.0, store_final_stat
         hT = torch.empty((N, H, dk, dv), dtype=torch.float32, device=device)
     nseq = N if cu_seqlens is not None else 0
     pq, pk, pv, po = q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr()
-    if workspace is None:
+    own = workspace is None
+    if own:
         size = _bytes("ckda_linear_fwd_workspace_bytes" if (pq | pk | pv | po) & 15 else
                       "ckda_linear_fwd_aligned_workspace_bytes", nseq, B, H, T, dk, dv, io)
+        if size > _SMALL:
+            linear_fwd.last_workspace = None
         workspace = torch.empty(size, dtype=torch.uint8, device=device)
     else:
         size = _given(workspace, device)
     _call(L.ckda_linear_fwd, "ckda_linear_fwd", device, pq, pk, pv, g.data_ptr(), int(per_head),
           _addr(h0), po, _addr(hT), _addr(cu_seqlens), nseq, B, H, Hk, T, dk, dv, io, float(scale),
           workspace.data_ptr(), size)
-    linear_fwd.last_workspace = workspace
+    linear_fwd.last_workspace = workspace[:256].clone() if own and size > _LARGE else workspace
     return o, hT
 
 
@@ -797,9 +807,12 @@ def linear_bwd(q, k, v, g, do, h0=None, dhT=None, cu_seqlens=None, scale=1.0, st
                                                          (("h0", h0), ("dhT", dhT)), (("do", do),))
     nseq = N if cu_seqlens is not None else 0
     pq, pk, pv, pdo = q.data_ptr(), k.data_ptr(), v.data_ptr(), do.data_ptr()
-    if workspace is None:
+    own = workspace is None
+    if own:
         size = _bytes("ckda_linear_bwd_workspace_bytes" if (pq | pk | pv | pdo) & 15 else
                       "ckda_linear_bwd_aligned_workspace_bytes", nseq, B, H, Hk, T, dk, dv, io)
+        if size > _SMALL:
+            linear_bwd.last_workspace = None
         workspace = torch.empty(size, dtype=torch.uint8, device=device)
     else:
         size = _given(workspace, device)
@@ -810,7 +823,7 @@ def linear_bwd(q, k, v, g, do, h0=None, dhT=None, cu_seqlens=None, scale=1.0, st
           _addr(h0), pdo, _addr(dhT), dq.data_ptr(), dkk.data_ptr(), dvv.data_ptr(), dg.data_ptr(),
           _addr(dh0), _addr(cu_seqlens), nseq, B, H, Hk, T, dk, dv, io, float(scale),
           workspace.data_ptr(), size)
-    linear_bwd.last_workspace = workspace
+    linear_bwd.last_workspace = workspace[:256].clone() if own and size > _LARGE else workspace
     return dq, dkk, dvv, dg, dh0
 
 

@@ -119,3 +119,44 @@ def test_states_of_narrow_heads_take_no_more_than_their_panels(ck, dk, dv):
     states = B * H * 2 * 2 * panels * 64 * 64 * 2
     need = L.ckda_linear_bwd_aligned_workspace_bytes(0, B, H, H, 1, dk, dv, BF16)
     assert states <= need <= 1.01 * states + 4096
+
+
+def test_a_call_holds_no_large_workspace(ck, monkeypatch):
+    """What a call made for itself: given back before the next is made, and at its end but for
+    the status word where it is large.  What the caller gave stays the caller's."""
+    import weakref
+    made, real = [], torch.empty
+
+    def empty(*a, **kw):
+        t = real(*a, **kw)
+        if kw.get("dtype") == torch.uint8:
+            assert t.numel() <= 1 << 20 or all(w() is None for w in made), "still held"
+            made.append(weakref.ref(t))
+        return t
+    monkeypatch.setattr(ck, "_call", lambda fn, where, *a: None)
+    monkeypatch.setattr(ck, "_LARGE", 64 << 20, raising=False)
+    monkeypatch.setattr(torch, "empty", empty)
+    q, g = torch.zeros(1, 16, 4000, 128, dtype=torch.bfloat16), torch.zeros(1, 16, 4000)
+    for _ in range(3):
+        ck.linear_bwd(q, q, q, g, q)
+        held = ck.linear_bwd.last_workspace
+        assert held.numel() == 256 and held.untyped_storage().nbytes() == 256
+        assert made[-1]() is None
+    made.clear()
+    for _ in range(2):  # a small one is held, without a copy
+        ck.linear_bwd(q[:, :2, :300].contiguous(), *[q[:, :2, :300].contiguous()] * 2,
+                      g[:, :2, :300].contiguous(), q[:, :2, :300].contiguous())
+        assert made[-1]() is ck.linear_bwd.last_workspace
+    mine = real(1 << 30, dtype=torch.uint8, device="cpu")
+    ck.linear_bwd(q, q, q, g, q, workspace=mine)
+    assert ck.linear_bwd.last_workspace is mine
+    ck.linear_bwd.last_workspace = None
+
+
+@pytest.mark.gpu
+def test_status_of_a_call_that_gave_its_workspace_back(ck, monkeypatch):
+    monkeypatch.setattr(ck, "_LARGE", 1 << 16)
+    x = torch.randn(1, 2, 1000, 64, device="cuda").bfloat16()
+    ck.linear_bwd(x, x, x, torch.zeros(1, 2, 1000, device="cuda"), x, scale=0.01)
+    assert ck.linear_bwd.last_workspace.numel() == 256
+    assert ck.fwd_status(ck.linear_bwd.last_workspace) == 0
