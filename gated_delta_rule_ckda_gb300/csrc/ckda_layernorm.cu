@@ -27,8 +27,8 @@
 //
 // Measured, bf16 with fp32 weights: forward of 1,048,576 rows of 128 94 us, 85% of the
 // copy bandwidth; backward of 16,384 rows of 4096 82 us, 72% (76 us the rows, the rest
-// the second kernel and its start); backward of 2,999 rows of 1031 in fp32 24 us,
-// single elements and mostly launch and host time.
+// the second kernel and its start); backward of 2,999 rows of 1031 in fp32 25 to 28 us,
+// 17 and 5 of them the kernels, the rest launches and the host.
 #include "ckda_internal.cuh"
 #include "ckda_launch.cuh"
 

@@ -11,8 +11,10 @@
 // Longer ones are cut into pieces of 64 tokens that run side by side, as matrix
 // products: a first kernel sums each piece's own contribution to the state, a scan
 // joins them, and then every piece starts from the state that enters it.  4 x 16
-// heads x 2048 tokens of 128 channels in fp32: 568 us (932 us token by token with
-// the longest pieces that fill the SMs); bound by FMA issue and shared-memory reads.
+// heads x 2048 tokens of 128 channels in fp32: 568 us in a loop on one input (932 us token
+// by token with the longest pieces that fill the SMs), 600 us on inputs that are not in
+// L2; bound by FMA issue and shared-memory reads.  8 x 16 x 2048 of 100 channels in bf16,
+// which the tensor-core kernels do not take: 1330 us.
 #include "ckda_linear_piece.cuh"
 
 namespace ckda {

@@ -11,9 +11,11 @@ using namespace chunk;
 // One CTA of 512 threads walks the chunks of one (sequence, head), or of one
 // segment of it, forward over (k, v) or backward over (q, do).  IMAGES: it
 // starts from the state entering it and writes the state met at each chunk
-// and, backward, dh0; bound by HBM, two tiles in and an image out, 128 KiB a
-// chunk (8 x 16 x 2048 tokens: 42 us, 6.4 TB/s).  Otherwise it starts from zero (at the sequence's end from h0 or dhT)
-// and writes the one state that it hands on.
+// and, backward, dh0: two tiles in and an image out, 128 KiB a chunk.  8 x 16 x 2048
+// tokens: 42 us a direction for 268 MB, of which 210 MB pass DRAM (58 to 62% of its peak;
+// tensor pipe 21%): 128 of 152 SMs, with the tiles of two chunks in flight each.
+// Otherwise it starts from zero (at the sequence's end from h0 or dhT) and writes the one
+// state that it hands on.
 //   warp 0 loads, warp 1 issues the products, warp 2 makes the decays,
 //   warps 4-7 scale a chunk's keys (queries) in two bf16 parts,
 //   warps 8-15 hold the state: thread (r, s) has its channels 64 s .. + 63 of
@@ -344,8 +346,9 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 //   64 heads, 8,192 tokens    207   2 segments 196   (3: 215, 4: 208, 7: 200)
 //   80 heads, 8,192 tokens    207   uncut            (2: 301, 3: 264, 7: 258)
 // Packed: sequences longer than 5/4 of an SM's share of all tokens are cut (24 of
-// 50,021 tokens, 16 heads of 64 and 128 channels: 215 us with passes over every
-// sequence and a search for each CTA's, 164 us with the tables).
+// 50,021 tokens, 16 heads of 64 and 128 channels, in a loop on one set of lengths: 215 us
+// with passes over every sequence and a search for each CTA's, 164 us with the tables;
+// 178 to 190 us on lengths that change from call to call).
 Split linear_split(int N, int B, int H, int T, bool packed) {
   Split sp{};
   const long long chunks = (T + C - 1) / C;

@@ -13,6 +13,8 @@
 // the SMs (each warp still reads whole 128-byte lines).  256 x 32 pairs of 128 x 128:
 // 160 us, 99% of the copy bandwidth, and 194 us with 32 columns; 16 pairs, from the
 // call to its result: 22.6 us with 32 columns, 23.7 us with 128, most of it the host's.
+// Widths that are not multiples of 4, and unaligned states, go by single columns: 256 x 32
+// pairs of 128 x 127 in 304 us, 52% of the copy bandwidth.
 // Narrower states take as many lanes as they have columns, and half the rows: 1024 x 32
 // pairs of 64 x 64 in 175 us, 317 us in blocks for 128 x 128, half of them idle.
 #include <type_traits>
