@@ -9,19 +9,20 @@
 //     dq_i = scale e_i H do_i + sum_{j <= i} B_ij k_j
 //     dk_j = w_j G v_j + sum_{i >= j} B_ij q_i
 //     dv_j = w_j G^T k_j + sum_{i >= j} A_ij do_i
-// 2 x 6 heads of 48 and 80 channels, three to a key head, 1001 tokens in fp32: 71 us, of
-// which 15 are the pieces' own states, 10 their scan and 43 this (token by token, in
-// three runs bound by a token's latency, 131 us).  4 x 16 x 2048, 128 channels: 1308 us, on inputs that are not in L2 1350; 8 x
-// 16 x 2048 of 100 channels in bf16 2710 us.
+// 2 x 6 heads of 48 and 80 channels, three to a key head, 1001 tokens in fp32: 73 us, of
+// which 15 are the pieces' own states, 10 their scan and 45 this (token by token, in
+// three runs bound by a token's latency, 131 us).  4 x 16 x 2048, 128 channels: 1372 us;
+// 8 x 16 x 2048 of 100 channels in bf16 2726 us.
 //
-// The decay's gradient is dg_t = <H_{t-1} e^{g_t}, dL/dH_t>.  With L the
-// cumulative log decay, dL/dL_i = q_i.dq_i - k_i.dk_i, and dg is its suffix
-// sum plus <hT, dhT>.  Terms that cancel in it are larger than what is left,
-// and two measures keep them small:
-//   - a token's own product (its key read by its own query), which no decay
-//     touches and which is the largest term under strong decay, is left out of
-//     the sums of dq and dk and joins them last;
-//   - the sum restarts at every piece from <H, dL/dH> itself.
+// The decay's gradient is dg_t = <H_{t-1} e^{g_t}, dL/dH_t>, in a piece
+//     dg_t = e <H, G> + sum_{j<t} w_j k_j.(G v_j)
+//            + sum_{i>=t} [ scale e_i q_i.(H do_i) + sum_{j<i} W_ij - sum_{l>i} W_li ],
+//     W_ij = B_ij (q_i.k_j)
+// with no term that is larger than what it counts: a token's own product W_ii, which no
+// decay touches and which is the largest under strong decay, is left out of the sums of dq
+// and dk and joins them last.  (The suffix sums of q.dq - k.dk from <H, G> at the piece's
+// end are the same in exact arithmetic, but take the products of G that t does not count
+// off again: at g = -8 that left dg 1e-3 to 5e-3 of its rms.  It cost 2% less time.)
 #include "ckda_linear_piece.cuh"
 
 namespace ckda {
@@ -67,8 +68,7 @@ __global__ void __launch_bounds__(kPieceThreads, 2) piece_grad_kernel(LinearArgs
   const int r = tid >> 4, c = tid & 15, row = 4 * r;
   const size_t states = (size_t)a.dk * a.dv;
   const float* H = w.p.H + (u.slot * a.H + u.h) * states;
-  const size_t behind = (min(u.slot + 1, w.p.slots - 1) * a.H + u.h) * states;
-  const float *Hend = w.p.H + behind, *G = w.p.G + behind;
+  const float* G = w.p.G + (min(u.slot + 1, w.p.slots - 1) * a.H + u.h) * states;
   auto stage_slab = [&](const float* S, int s) {
     stage_rows(slab, sv, S + (size_t)16 * CK * s * a.dv, a.dv, a.dv,
                min(16 * CK, a.dk - 16 * CK * s), 16 * CK, sv - 4);
@@ -101,8 +101,11 @@ __global__ void __launch_bounds__(kPieceThreads, 2) piece_grad_kernel(LinearArgs
       }
   }
   __syncthreads();
+  // from here on the values go into products with the decay to the piece's end
+  for (int i = tid >> 5; i < kTok; i += kPieceThreads / 32)
+    for (int j = tid & 31; j < sv - 4; j += 32) sval[i * sv + j] *= sw[i];
 
-  float x[4] = {};  // q.dq - k.dk, this thread's columns
+  float x[4] = {};  // q.dq - k.dk without G's part of dk, this thread's columns
   // a column of a result, with the token's own part
   auto put = [&](float (&acc)[4][CK], int s, const float* with, IO* out, float* parts) {
     const auto put_to = [&](auto* to) {
@@ -155,11 +158,6 @@ __global__ void __launch_bounds__(kPieceThreads, 2) piece_grad_kernel(LinearArgs
 #pragma unroll 1
   for (int s = 0; s < slabs; ++s) {  // dk, and the state's part of dv
     float acc[4][CK] = {};
-    add_nt(acc, sval + row * sv, sv, slab + c * sv, sv, dv4);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < CK; ++j) acc[i][j] *= sw[row + i];
     const float* q = sq + 16 * CK * s + c;
     add_diag<true, false>(acc, sp + row, kPS, q, sk, row);
     add_nn<true>(acc, sp + row, kPS, q, sk, row + 4, nt4);
@@ -168,11 +166,12 @@ __global__ void __launch_bounds__(kPieceThreads, 2) piece_grad_kernel(LinearArgs
 #pragma unroll
       for (int j = 0; j < CK; ++j)
         x[i] = fmaf(-skey[(row + i) * sk + 16 * CK * s + c + 16 * j], acc[i][j], x[i]);
+    add_nt(acc, sval + row * sv, sv, slab + c * sv, sv, dv4);
     put(acc, s, sq, static_cast<IO*>(a.dkey), w.dk);
     const int rows = min(16 * CK, a.dk - 16 * CK * s);
     // (keys past dk are zeros, as are the slab's rows)
     add_nn<false>(dv, skey + row * sk + 16 * CK * s, sk, slab + c, sv, 0, (rows + 3) & ~3);
-    const float* h = Hend + (size_t)16 * CK * s * a.dv;
+    const float* h = H + (size_t)16 * CK * s * a.dv;
 #pragma unroll
     for (int i = 0; i < 2 * CK; ++i)  // a warp a row, all its loads in flight
 #pragma unroll
@@ -188,11 +187,21 @@ __global__ void __launch_bounds__(kPieceThreads, 2) piece_grad_kernel(LinearArgs
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
+    float y = 0.f;  // w k.(G v)
 #pragma unroll
-    for (int j = 0; j < CV; ++j) dv[i][j] *= sw[row + i];
+    for (int j = 0; j < CV; ++j) {
+      if (c + 16 * j < a.dv) y = fmaf(sval[(row + i) * sv + c + 16 * j], dv[i][j], y);
+      dv[i][j] *= sw[row + i];
+    }
 #pragma unroll
-    for (int m = 8; m >= 1; m >>= 1) x[i] += __shfl_xor_sync(0xffffffffu, x[i], m);
-    if (c == 0) sx[row + i] = x[i];
+    for (int m = 8; m >= 1; m >>= 1) {
+      x[i] += __shfl_xor_sync(0xffffffffu, x[i], m);
+      y += __shfl_xor_sync(0xffffffffu, y, m);
+    }
+    if (c == 0) {
+      sx[row + i] = x[i];
+      sg[row + i] = y;  // (the decays have been read)
+    }
   }
 #pragma unroll
   for (int m = 16; m >= 1; m >>= 1) hg += __shfl_xor_sync(0xffffffffu, hg, m);
@@ -217,18 +226,26 @@ __global__ void __launch_bounds__(kPieceThreads, 2) piece_grad_kernel(LinearArgs
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (row + i < nt) st_io(dval + (u.vrow + row + i) * a.dv + c + 16 * j, dv[i][j]);
-  if (tid < 32) {  // sums from a token to the piece's end, lane l has tokens l and 32 + l
-    float lo = sx[tid], hi = sx[32 + tid], end = 0.f;
-    for (int i = 0; i < 8; ++i) end += red[i];
+  if (tid < 32) {  // lane l has tokens l and 32 + l
+    // sums of x from a token to the piece's end, and of y over the tokens before it
+    float lo = sx[tid], hi = sx[32 + tid], ylo = sg[tid], yhi = sg[32 + tid], all = 0.f;
+    for (int i = 0; i < 8; ++i) all += red[i];
+    all *= se[kTok - 1];
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
       const float y = __shfl_down_sync(0xffffffffu, lo, m), z = __shfl_down_sync(0xffffffffu, hi, m);
+      const float p = __shfl_up_sync(0xffffffffu, ylo, m), o = __shfl_up_sync(0xffffffffu, yhi, m);
       if (tid + m < 32) lo += y, hi += z;
+      if (tid >= m) ylo += p, yhi += o;
     }
-    hi += end;
     lo += __shfl_sync(0xffffffffu, hi, 0);
-    if (tid < nt) dg[u.vrow + tid] = lo;
-    if (32 + tid < nt) dg[u.vrow + 32 + tid] = hi;
+    yhi += __shfl_sync(0xffffffffu, ylo, 31);
+    const float last = __shfl_sync(0xffffffffu, ylo, 31);
+    ylo = __shfl_up_sync(0xffffffffu, ylo, 1);  // before the token: shifted, not subtracted
+    yhi = __shfl_up_sync(0xffffffffu, yhi, 1);
+    if (tid == 0) ylo = 0.f, yhi = last;
+    if (tid < nt) dg[u.vrow + tid] = all + ylo + lo;
+    if (32 + tid < nt) dg[u.vrow + 32 + tid] = all + yhi + hi;
   }
 }
 
