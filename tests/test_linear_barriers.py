@@ -31,13 +31,32 @@ class Barrier:
         return (self.phase & 1) != parity
 
 
+def play(warps, victim):
+    """Runs generators that yield (barrier, parity) to wait for, or None: the victim moves only
+    when no other can, and all get to their end."""
+    waits, left = {}, set(range(len(warps)))
+
+    def move(i):
+        """Whether warp i got further."""
+        if waits.get(i) is not None and not waits[i][0].done(waits[i][1]):
+            return False
+        try:
+            waits[i] = next(warps[i])
+        except StopIteration:
+            left.discard(i)
+        return True
+
+    while left:
+        if not any([move(i) for i in sorted(left) if i != victim]):
+            assert victim in left and move(victim), f"warps {sorted(left)} wait for ever"
+
+
 def role(text, start, end):
     """(operation, barrier) in the order of the source between two marks."""
     body = text[text.index(start):text.index(end, text.index(start))]
     body = re.sub(r"//[^\n]*", "", body)
     body = body[re.search(r"for \((int c = 0)?; c < chunks; \+\+c\)", body).start():]
-    ops = re.findall(r"(warp_wait|warp_publish|warp_arrive|mbar_arrive|group_sync)\(bars \+ (B_\w+)",
-                     body)
+    ops = re.findall(r"(warp_wait|warp_publish|warp_arrive|mbar_arrive)\(bars \+ (B_\w+)", body)
     assert len(ops) > 4
     return ops
 
@@ -117,24 +136,73 @@ def test_forward_waits_see_their_phase(slots, victim):
                     yield bar(name), par
                 yield None  # another may go first
 
-    warps = [loads(), issues(), decays()] + [warp(p_ops, i == 0) for i in range(4)] + \
-            [warp(s_ops, False) for _ in range(8)]
-    waits = {}
+    play([loads(), issues(), decays()] + [warp(p_ops, i == 0) for i in range(4)] +
+         [warp(s_ops, False) for _ in range(8)], victim)
 
-    def move(i):
-        """Whether warp i, held back or not, got further."""
-        if i in waits and waits[i] is not None and not waits[i][0].done(waits[i][1]):
-            return False
-        try:
-            waits[i] = next(warps[i])
-        except StopIteration:
-            left.discard(i)
-        return True
 
-    left = set(range(len(warps)))
-    while left:
-        if not any([move(i) for i in sorted(left) if i != victim]):
-            assert victim in left and move(victim), f"warps {sorted(left)} wait for ever"
+@pytest.mark.parametrize("back", [False, True])
+@pytest.mark.parametrize("victim", range(15))
+def test_state_waits_see_their_phase(back, victim):
+    """The same for the kernel of the states: loads, products, decays, four scaling warps and
+    eight with the state."""
+    code = code_of("ckda_linear_state.cu")
+    at = code.index("else if (warp >= 4 && warp < 8)")
+    split = code.index("else if (warp >= 8)", at)
+    pattern = r"(warp_wait|warp_publish|warp_arrive|mbar_arrive)\(bars \+ (B_\w+)(?: \+ (ix \+ 1))?"
+    scale = [o[:2] for o in re.findall(pattern, code[at:split]) if not o[2]]  # (but tails)
+    body, _ = loop_at(code, code.index("for (; i < chunks;", split))
+    state = [o[:2] for o in re.findall(pattern, body)]
+    assert scale == [("warp_wait", "B_G"), ("mbar_arrive", "B_GFREE"), ("warp_wait", "B_FULL"),
+                     ("warp_wait", "B_DF"), ("warp_publish", "B_KT")]
+    assert state == [("warp_wait", "B_G"), ("mbar_arrive", "B_GFREE"), ("warp_wait", "B_DF"),
+                     ("warp_arrive", "B_DFREE")]
+    chunks, slots = 7, 4
+    steps = chunks if back else chunks - 1
+    count = dict(B_KT=4, B_DFREE=8, B_GFREE=12)
+    bars = {}
+
+    def bar(name, i=0):
+        return bars.setdefault((name, i), Barrier(count.get(name, 1)))
+
+    def loads():
+        for i in range(2 * steps):
+            if i >= slots:
+                yield bar("B_EMPTY", i % slots), (i // slots - 1) & 1
+            bar("B_FULL", i % slots).arrive()
+        for j in range(max(0, 2 * steps - slots), 2 * steps):
+            yield bar("B_FULL", j % slots), (j // slots) & 1
+
+    def issues():
+        for i in range(steps):
+            ix, p = 2 * i % slots, i & 1
+            yield bar("B_FULL", ix + 1), (i // 2) & 1
+            if i >= 2:
+                yield bar("B_DFREE", p), (i // 2 - 1) & 1
+            yield bar("B_KT"), p
+            for b in (bar("B_DF", p), bar("B_EMPTY", ix), bar("B_EMPTY", ix + 1)):
+                b.arrive()
+
+    def decays():
+        for i in range(steps):
+            if i >= 1:
+                yield bar("B_GFREE"), (i - 1) & 1
+            bar("B_G").arrive()
+
+    def warp(ops, lag):
+        for i in range(steps):
+            for op, name in ops:
+                if op != "warp_wait":
+                    bar(name, i & 1 if name == "B_DFREE" else 0).arrive()
+                elif name == "B_G":
+                    yield bar(name), i & 1
+                elif name == "B_FULL":
+                    yield bar(name, 2 * i % slots), (i // 2) & 1
+                elif i >= lag:  # the product of this step, or of the one before
+                    yield bar(name, (i - lag) & 1), ((i - lag) // 2) & 1
+                yield None
+
+    play([loads(), issues(), decays()] + [warp(scale, 1) for _ in range(4)] +
+         [warp(state, 0) for _ in range(8)], victim)
 
 
 def code_of(name):
