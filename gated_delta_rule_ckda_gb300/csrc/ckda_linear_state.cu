@@ -348,7 +348,7 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 // Packed: sequences longer than 5/4 of an SM's share of all tokens are cut (24 of
 // 50,021 tokens, 16 heads of 64 and 128 channels, in a loop on one set of lengths: 215 us
 // with passes over every sequence and a search for each CTA's, 164 us with the tables;
-// 178 to 190 us on lengths that change from call to call).
+// 164 to 190 us over sets of lengths).
 Split linear_split(int N, int B, int H, int T, bool packed) {
   Split sp{};
   const long long chunks = (T + C - 1) / C;
