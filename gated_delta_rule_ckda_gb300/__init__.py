@@ -10,7 +10,10 @@ fallback: if the library is missing or fails to load, every call raises.
 
 Next to the recurrence are linear attention with a scalar decay per head
 (linear_fwd, linear_bwd, linear_decode_step) and layer norm (layernorm_fwd,
-layernorm_bwd).
+layernorm_bwd), and the parts of a state space block: the short causal
+convolution (conv_fwd, conv_bwd, conv_decode_step), the selective scan
+(scan_fwd, scan_bwd, scan_decode_step) and RMS norm with a residual's addition
+and outputs in 8 bits (rmsnorm_fwd, rmsnorm_fwd8, rmsnorm_bwd).
 
 Shapes follow the C ABI: q, k, alpha [B, H, T, dk]; v [B, H, T, dv];
 beta [B, H, T]; h0 / hT fp32 [N, H, dk, dv] with N = B, or the number of
@@ -35,7 +38,9 @@ __all__ = ["fwd", "fwd_host", "fwd_split", "decode_step", "decode_step_raw", "pr
            "split_workspace_bytes", "host_scratch_bytes", "selftest_timeout", "lib",
            "library_path", "CkdaError", "STATUS", "recurrence", "prepare", "linear_fwd",
            "linear_bwd", "linear_decode_step", "linear_attention", "layernorm_fwd",
-           "layernorm_bwd", "layer_norm"]
+           "layernorm_bwd", "layer_norm", "conv_fwd", "conv_bwd", "conv_decode_step",
+           "short_conv", "scan_fwd", "scan_bwd", "scan_decode_step", "selective_scan",
+           "rmsnorm_fwd", "rmsnorm_fwd8", "rmsnorm_bwd", "rms_norm"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libckda.so")
@@ -139,6 +144,31 @@ def lib():
             L.ckda_layernorm_bwd.restype = i32
             L.ckda_layernorm_bwd.argtypes = [vp] * 8 + [ctypes.c_longlong, i32, i32, i32, vp, sz,
                                                         vp]
+            i64 = ctypes.c_longlong
+            L.ckda_conv_fwd.restype = i32
+            L.ckda_conv_fwd.argtypes = [vp] * 7 + [i32] * 5 + [i64] + [i32] * 3 + [vp]
+            L.ckda_conv_bwd_workspace_bytes.restype = sz
+            L.ckda_conv_bwd_workspace_bytes.argtypes = [i32] * 4
+            L.ckda_conv_bwd.restype = i32
+            L.ckda_conv_bwd.argtypes = [vp] * 11 + [i32] * 5 + [i64] + [i32] * 3 + [vp, sz, vp]
+            L.ckda_conv_decode_step.restype = i32
+            L.ckda_conv_decode_step.argtypes = [vp] * 5 + [i32] * 3 + [i64] + [i32] * 3 + [vp]
+            for fn in (L.ckda_scan_fwd_workspace_bytes, L.ckda_scan_bwd_workspace_bytes):
+                fn.restype, fn.argtypes = sz, [i32] * 5
+            L.ckda_scan_fwd.restype = i32
+            L.ckda_scan_fwd.argtypes = [vp] * 12 + [i32] * 6 + [i64] * 5 + [i32] * 2 + [vp, sz, vp]
+            L.ckda_scan_bwd.restype = i32
+            L.ckda_scan_bwd.argtypes = [vp] * 21 + [i32] * 6 + [i64] * 5 + [i32] * 2 + [vp, sz, vp]
+            L.ckda_scan_decode_step.restype = i32
+            L.ckda_scan_decode_step.argtypes = [vp] * 10 + [i32] * 4 + [i64] * 5 + [i32] * 2 + [vp]
+            L.ckda_rmsnorm_fwd.restype = i32
+            L.ckda_rmsnorm_fwd.argtypes = [vp] * 6 + [i64] + [i32] * 3 + [f32, vp]
+            L.ckda_rmsnorm_fwd8.restype = i32
+            L.ckda_rmsnorm_fwd8.argtypes = [vp] * 7 + [i64] + [i32] * 4 + [f32, vp]
+            L.ckda_rmsnorm_bwd_workspace_bytes.restype = sz
+            L.ckda_rmsnorm_bwd_workspace_bytes.argtypes = [i64, i32]
+            L.ckda_rmsnorm_bwd.restype = i32
+            L.ckda_rmsnorm_bwd.argtypes = [vp] * 7 + [i64] + [i32] * 3 + [vp, sz, vp]
             _lib = L
     return _lib
 
@@ -943,6 +973,351 @@ def layernorm_bwd(dy, x, mean, rstd, weight=None, weight_grad=True, dx=None, wor
     return dx, dw, db
 
 
+# ----------------------------------------- short convolution and selective scan
+def _apart(t, name, dtype, shape, device, tail=1):
+    """Checks rows of the last `tail` axes: each row in one run, rows evenly apart (a part
+    of a wider projection).  Returns the elements from one row to the next."""
+    if t.dtype != dtype or t.shape != shape or t.device != device:
+        _check(t, name, dtype, shape, device)
+    width = 1
+    strides = t.stride()
+    whole = t.is_contiguous()
+    for i in range(len(shape) - 1, len(shape) - 1 - tail, -1):
+        if not whole and shape[i] > 1 and strides[i] != width:
+            raise ValueError(f"{name}: each row must be contiguous")
+        width *= shape[i]
+    if whole:
+        return width
+    apart, rows = None, 1
+    for i in range(len(shape) - 1 - tail, -1, -1):
+        if shape[i] > 1:
+            if apart is None:
+                apart = strides[i]
+            if strides[i] != apart * rows or apart < width:
+                raise ValueError(f"{name}: rows must be evenly apart and not overlap")
+            rows *= shape[i]
+    return width if apart is None else apart
+
+
+def _sequences(B, cu_seqlens, device):
+    """Sequences of the states, and the count that the library takes."""
+    if cu_seqlens is None:
+        return B, 0
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2 or B != 1:
+        raise ValueError("packed input has B = 1 and cu_seqlens [num_seqs + 1]")
+    n = cu_seqlens.numel() - 1
+    _check(cu_seqlens, "cu_seqlens", torch.int32, (n + 1,), device)
+    return n, n
+
+
+def _check_conv(x, weight, bias, axes):
+    """(io code, weight code, rows' distance, taps) of what the convolution's calls share."""
+    if x.dim() != axes:
+        raise ValueError(f"x [{'B, T, D' if axes == 3 else 'B, D'}] has {axes} axes")
+    io = _io_dtype(x)
+    if weight.dim() != 2:
+        raise ValueError("weight [D, W] has two axes")
+    code = _io_dtype(weight)
+    D, W = x.shape[-1], weight.shape[1]
+    _check(weight, "weight", weight.dtype, (D, W), x.device)
+    if bias is not None:
+        _check(bias, "bias", weight.dtype, (D,), x.device)
+    return io, code, _apart(x, "x", x.dtype, x.shape, x.device), W
+
+
+def conv_fwd(x, weight, bias=None, h0=None, cu_seqlens=None, silu=True, store_final_state=True,
+             y=None, hT=None, stream=None):
+    """Short causal convolution of each channel (ckda_conv_fwd): p_t = bias +
+    sum_j weight_j x_{t-W+1+j}, y = silu(p) or, with silu=False, p.
+
+    x [B, T, D] (it may be a part of a wider projection's last axis), weight [D, W] with
+    W = 2, 3 or 4 and bias [D] in bf16 or fp32, h0, hT [N, W - 1, D] in x's type: the inputs
+    before the first token and the last ones.  Returns (y, hT or None)."""
+    if stream is not None:
+        return _on_stream(conv_fwd, locals())
+    L = lib()
+    device, dt = x.device, x.dtype
+    io, code, ldx, W = _check_conv(x, weight, bias, 3)
+    B, T, D = x.shape
+    N, nseq = _sequences(B, cu_seqlens, device)
+    if h0 is not None:
+        _check(h0, "h0", dt, (N, W - 1, D), device)
+    if y is None:
+        y = torch.empty((B, T, D), dtype=dt, device=device)
+    else:
+        _check(y, "y", dt, (B, T, D), device)
+    if hT is not None:
+        _check(hT, "hT", dt, (N, W - 1, D), device)
+    elif store_final_state:
+        hT = torch.empty((N, W - 1, D), dtype=dt, device=device)
+    _call(L.ckda_conv_fwd, "ckda_conv_fwd", device, x.data_ptr(), weight.data_ptr(), _addr(bias),
+          _addr(h0), y.data_ptr(), _addr(hT), _addr(cu_seqlens), nseq, B, T, D, W, ldx, io, code,
+          int(silu))
+    return y, hT
+
+
+def conv_bwd(dy, x, weight, bias=None, h0=None, dhT=None, cu_seqlens=None, silu=True,
+             store_dh0=True, workspace=None, stream=None):
+    """Backward of conv_fwd (ckda_conv_bwd): gradients of sum <y, dy> + <hT, dhT>.  Returns
+    (dx, dweight, dbias or None, dh0 or None); the weights' have the weights' type."""
+    if stream is not None:
+        return _on_stream(conv_bwd, locals())
+    L = lib()
+    device, dt = x.device, x.dtype
+    io, code, ldx, W = _check_conv(x, weight, bias, 3)
+    B, T, D = x.shape
+    N, nseq = _sequences(B, cu_seqlens, device)
+    _check(dy, "dy", dt, (B, T, D), device)
+    for name, t in (("h0", h0), ("dhT", dhT)):
+        if t is not None:
+            _check(t, name, dt, (N, W - 1, D), device)
+    if workspace is None:
+        size = _bytes("ckda_conv_bwd_workspace_bytes", B, T, D, W)
+        workspace = torch.empty(size, dtype=torch.uint8, device=device)
+    else:
+        size = _given(workspace, device)
+    dx = torch.empty((B, T, D), dtype=dt, device=device)
+    dw = torch.empty_like(weight)
+    db = None if bias is None else torch.empty_like(bias)
+    dh0 = torch.empty((N, W - 1, D), dtype=dt, device=device) if store_dh0 else None
+    _call(L.ckda_conv_bwd, "ckda_conv_bwd", device, dy.data_ptr(), x.data_ptr(), weight.data_ptr(),
+          _addr(bias), _addr(h0), _addr(dhT), dx.data_ptr(), dw.data_ptr(), _addr(db), _addr(dh0),
+          _addr(cu_seqlens), nseq, B, T, D, W, ldx, io, code, int(silu), workspace.data_ptr(), size)
+    return dx, dw, db, dh0
+
+
+def conv_decode_step(x, weight, state, bias=None, silu=True, y=None, stream=None):
+    """One token of the convolution (ckda_conv_decode_step): x [B, D]; state [B, W - 1, D] in
+    x's type is moved on by the token in place.  Returns y [B, D]."""
+    if stream is not None:
+        return _on_stream(conv_decode_step, locals())
+    L = lib()
+    device, dt = x.device, x.dtype
+    io, code, ldx, W = _check_conv(x, weight, bias, 2)
+    B, D = x.shape
+    _check(state, "state", dt, (B, W - 1, D), device)
+    if y is None:
+        y = torch.empty((B, D), dtype=dt, device=device)
+    else:
+        _check(y, "y", dt, (B, D), device)
+    _call(L.ckda_conv_decode_step, "ckda_conv_decode_step", device, x.data_ptr(), weight.data_ptr(),
+          _addr(bias), state.data_ptr(), y.data_ptr(), B, D, W, ldx, io, code, int(silu))
+    return y
+
+
+def _check_scan(x, dt, A, B, C, D, z, dt_bias, axes):
+    """Checks what the scan's calls share; returns (io, N, G, distances of x, dt, B, C, z)."""
+    if x.dim() != axes:
+        raise ValueError(f"x [{'B, T, D' if axes == 3 else 'B, D'}] has {axes} axes")
+    io, device, t, lead = _io_dtype(x), x.device, x.dtype, x.shape[:-1]
+    width = x.shape[-1]
+    if A.dim() != 2:
+        raise ValueError("A [D, N] has two axes")
+    N = A.shape[1]
+    _check(A, "A", torch.float32, (width, N), device)
+    if B.dim() not in (axes, axes + 1) or B.dim() != C.dim():
+        raise ValueError("B and C are both [..., N] or both [..., G, N]")
+    grouped = B.dim() == axes + 1
+    G = B.shape[-2] if grouped else 1
+    if G < 1 or width % G:
+        raise ValueError(f"{width} channels cannot share {G} groups evenly")
+    shape, tail = ((*lead, G, N), 2) if grouped else ((*lead, N), 1)
+    for name, p in (("D", D), ("dt_bias", dt_bias)):
+        if p is not None:
+            _check(p, name, torch.float32, (width,), device)
+    return io, N, G, (_apart(x, "x", t, x.shape, device), _apart(dt, "dt", t, x.shape, device),
+                      _apart(B, "B", t, shape, device, tail), _apart(C, "C", t, shape, device, tail),
+                      0 if z is None else _apart(z, "z", t, x.shape, device))
+
+
+def scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, cu_seqlens=None,
+             softplus=True, store_final_state=True, y=None, hT=None, workspace=None, stream=None):
+    """Selective state space scan (ckda_scan_fwd): delta = softplus(dt + dt_bias),
+    h_t = exp(delta A) h_{t-1} + delta x B_t, y_t = (<C_t, h_t> + D x_t) silu(z_t).
+
+    x, dt, z [B, T, D]; B, C [B, T, N], or [B, T, G, N] with G dividing D; each may be a part
+    of a wider projection's last axis.  A fp32 [D, N], N <= 64; D, dt_bias fp32 [D]; h0, hT
+    fp32 [sequences, D, N].  Returns (y, hT or None)."""
+    if stream is not None:
+        return _on_stream(scan_fwd, locals())
+    L = lib()
+    device = x.device
+    io, N, G, apart = _check_scan(x, dt, A, B, C, D, z, dt_bias, 3)
+    rows, T, width = x.shape
+    count, nseq = _sequences(rows, cu_seqlens, device)
+    if h0 is not None:
+        _check(h0, "h0", torch.float32, (count, width, N), device)
+    if y is None:
+        y = torch.empty((rows, T, width), dtype=x.dtype, device=device)
+    else:
+        _check(y, "y", x.dtype, (rows, T, width), device)
+    if hT is not None:
+        _check(hT, "hT", torch.float32, (count, width, N), device)
+    elif store_final_state:
+        hT = torch.empty((count, width, N), dtype=torch.float32, device=device)
+    if workspace is None:
+        size = _bytes("ckda_scan_fwd_workspace_bytes", rows, T, width, N, G)
+        if size:
+            workspace = torch.empty(size, dtype=torch.uint8, device=device)
+    else:
+        size = _given(workspace, device)
+    _call(L.ckda_scan_fwd, "ckda_scan_fwd", device, x.data_ptr(), dt.data_ptr(), A.data_ptr(),
+          B.data_ptr(), C.data_ptr(), _addr(D), _addr(z), _addr(dt_bias), _addr(h0), y.data_ptr(),
+          _addr(hT), _addr(cu_seqlens), nseq, rows, T, width, N, G, *apart, io, int(softplus),
+          _addr(workspace), size)
+    return y, hT
+
+
+def scan_bwd(dy, x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, dhT=None, cu_seqlens=None,
+             softplus=True, store_dh0=True, workspace=None, stream=None):
+    """Backward of scan_fwd (ckda_scan_bwd): gradients of sum <y, dy> + <hT, dhT>.  Returns
+    (dx, ddt, dA, dB, dC, dD, dz, ddt_bias, dh0); those of what was not given are None."""
+    if stream is not None:
+        return _on_stream(scan_bwd, locals())
+    L = lib()
+    device, f32 = x.device, torch.float32
+    io, N, G, apart = _check_scan(x, dt, A, B, C, D, z, dt_bias, 3)
+    rows, T, width = x.shape
+    count, nseq = _sequences(rows, cu_seqlens, device)
+    _check(dy, "dy", x.dtype, x.shape, device)
+    for name, t in (("h0", h0), ("dhT", dhT)):
+        if t is not None:
+            _check(t, name, f32, (count, width, N), device)
+    if workspace is None:
+        size = _bytes("ckda_scan_bwd_workspace_bytes", rows, T, width, N, G)
+        workspace = torch.empty(size, dtype=torch.uint8, device=device)
+    else:
+        size = _given(workspace, device)
+
+    def like(t):
+        return None if t is None else torch.empty(t.shape, dtype=t.dtype, device=device)
+    dx, ddt, dA, dB, dC, dD, dz, ddt_bias = (like(t) for t in (x, dt, A, B, C, D, z, dt_bias))
+    dh0 = torch.empty((count, width, N), dtype=f32, device=device) if store_dh0 else None
+    _call(L.ckda_scan_bwd, "ckda_scan_bwd", device, dy.data_ptr(), x.data_ptr(), dt.data_ptr(),
+          A.data_ptr(), B.data_ptr(), C.data_ptr(), _addr(D), _addr(z), _addr(dt_bias), _addr(h0),
+          _addr(dhT), dx.data_ptr(), ddt.data_ptr(), dA.data_ptr(), dB.data_ptr(), dC.data_ptr(),
+          _addr(dD), _addr(dz), _addr(ddt_bias), _addr(dh0), _addr(cu_seqlens), nseq, rows, T,
+          width, N, G, *apart, io, int(softplus), workspace.data_ptr(), size)
+    return dx, ddt, dA, dB, dC, dD, dz, ddt_bias, dh0
+
+
+def scan_decode_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, softplus=True, y=None,
+                     stream=None):
+    """One token of the scan (ckda_scan_decode_step) on a resident state [B, D, N] fp32,
+    updated in place.  x, dt, z [B, D]; B, C [B, N] or [B, G, N].  Returns y [B, D]."""
+    if stream is not None:
+        return _on_stream(scan_decode_step, locals())
+    L = lib()
+    device = x.device
+    io, N, G, apart = _check_scan(x, dt, A, B, C, D, z, dt_bias, 2)
+    rows, width = x.shape
+    _check(state, "state", torch.float32, (rows, width, N), device)
+    if y is None:
+        y = torch.empty((rows, width), dtype=x.dtype, device=device)
+    else:
+        _check(y, "y", x.dtype, (rows, width), device)
+    _call(L.ckda_scan_decode_step, "ckda_scan_decode_step", device, x.data_ptr(), dt.data_ptr(),
+          A.data_ptr(), B.data_ptr(), C.data_ptr(), _addr(D), _addr(z), _addr(dt_bias),
+          state.data_ptr(), y.data_ptr(), rows, width, N, G, *apart, io, int(softplus))
+    return y
+
+
+# ------------------------------------------------------------------- RMS norm
+def _check_rms(x, weight, residual):
+    """(io code, weight code, leading shape, width, sum's tensor or None)."""
+    io = _io_dtype(x)
+    if x.dim() < 1:
+        raise ValueError("x has no last axis")
+    if not x.is_contiguous():
+        raise ValueError("x: must be contiguous")
+    code = _check_weight(weight, None, x.shape[-1], x.device)
+    if residual is not None:
+        _check(residual, "residual", x.dtype, x.shape, x.device)
+    return io, code, x.shape[:-1], x.shape[-1]
+
+
+def rmsnorm_fwd(x, weight=None, residual=None, eps=1e-5, y=None, h=None, rstd=None, stream=None):
+    """Root-mean-square norm over the last axis of h = x + residual (ckda_rmsnorm_fwd).
+    Returns (y, h, rstd): h is x itself without a residual; rstd is fp32 of x's leading
+    shape.  weight is bf16 or fp32 [width].  h may be x or residual, y may be x."""
+    if stream is not None:
+        return _on_stream(rmsnorm_fwd, locals())
+    L = lib()
+    device = x.device
+    io, code, lead, width = _check_rms(x, weight, residual)
+    if y is None:
+        y = torch.empty_like(x)
+    else:
+        _check(y, "y", x.dtype, x.shape, device)
+    if residual is None:
+        if h is not None:
+            raise ValueError("h: there is no sum to store without a residual")
+    elif h is None:
+        h = torch.empty_like(x)
+    else:
+        _check(h, "h", x.dtype, x.shape, device)
+    if rstd is None:
+        rstd = torch.empty(lead, dtype=torch.float32, device=device)
+    else:
+        _check(rstd, "rstd", torch.float32, lead, device)
+    _call(L.ckda_rmsnorm_fwd, "ckda_rmsnorm_fwd", device, x.data_ptr(), _addr(residual),
+          _addr(weight), _addr(h), y.data_ptr(), rstd.data_ptr(), rstd.numel(), width, io, code,
+          float(eps))
+    return y, x if h is None else h, rstd
+
+
+def rmsnorm_fwd8(x, weight=None, residual=None, eps=1e-5, group=0, stream=None):
+    """rmsnorm_fwd with y in 8 bits (ckda_rmsnorm_fwd8).  Returns (y8, scale, h, rstd): y8 is
+    float8_e4m3fn and y = y8 scale; scale is fp32 of x's leading shape (group = 0: one for a
+    row), or with a last axis of width / group (group = 32, 64 or 128 columns each)."""
+    if stream is not None:
+        return _on_stream(rmsnorm_fwd8, locals())
+    L = lib()
+    device = x.device
+    io, code, lead, width = _check_rms(x, weight, residual)
+    if group and (group not in (32, 64, 128) or width % group):
+        raise ValueError(f"group: {group}, expected 0, 32, 64 or 128 that divides {width}")
+    y8 = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=device)
+    h = None if residual is None else torch.empty_like(x)
+    rstd = torch.empty(lead, dtype=torch.float32, device=device)
+    scale = torch.empty((*lead, width // group) if group else lead, dtype=torch.float32, device=device)
+    _call(L.ckda_rmsnorm_fwd8, "ckda_rmsnorm_fwd8", device, x.data_ptr(), _addr(residual),
+          _addr(weight), _addr(h), y8.data_ptr(), scale.data_ptr(), rstd.data_ptr(), rstd.numel(),
+          width, int(group), io, code, float(eps))
+    return y8, scale, x if h is None else h, rstd
+
+
+def rmsnorm_bwd(dy, h, rstd, weight=None, dh=None, weight_grad=True, dx=None, workspace=None,
+                stream=None):
+    """Backward of rmsnorm_fwd and rmsnorm_fwd8 (ckda_rmsnorm_bwd), from the h and rstd that
+    they returned; dh is the gradient that arrives at h itself.  Returns (dx, dweight): dx is
+    the gradient of x and of residual alike; dweight has weight's type (fp32 without one) and
+    is None when weight_grad is false.  dx may be dy, h or dh."""
+    if stream is not None:
+        return _on_stream(rmsnorm_bwd, locals())
+    L = lib()
+    device = h.device
+    io, code, lead, width = _check_rms(h, weight, None)
+    _check(dy, "dy", h.dtype, h.shape, device)
+    _check(rstd, "rstd", torch.float32, lead, device)
+    if dh is not None:
+        _check(dh, "dh", h.dtype, h.shape, device)
+    if dx is None:
+        dx = torch.empty_like(h)
+    else:
+        _check(dx, "dx", h.dtype, h.shape, device)
+    rows, dw = rstd.numel(), None
+    if weight_grad:
+        dw = torch.empty(width, dtype=torch.float32 if weight is None else weight.dtype, device=device)
+        if workspace is None:
+            workspace = torch.empty(_bytes("ckda_rmsnorm_bwd_workspace_bytes", rows, width),
+                                    dtype=torch.uint8, device=device)
+    _call(L.ckda_rmsnorm_bwd, "ckda_rmsnorm_bwd", device, dy.data_ptr(), h.data_ptr(),
+          rstd.data_ptr(), _addr(weight), _addr(dh), dx.data_ptr(), _addr(dw), rows, width, io, code,
+          _addr(workspace), 0 if workspace is None else _given(workspace, device))
+    return dx, dw
+
+
 # ------------------------------------------------------------------- autograd
 # Training use: the forward (fwd) with its backward (bwd), and the input
 # preparation (prep) with its backward (prep_bwd), as torch.autograd
@@ -1077,3 +1452,87 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5):
     if weight is None and bias is not None and bias.dtype != torch.float32:
         raise TypeError(f"bias: dtype {bias.dtype}, expected {torch.float32} without a weight")
     return _LayerNorm.apply(x, weight, bias, float(eps))
+
+
+def _or_zeros(grad, shape, like):
+    if grad is None:
+        return torch.zeros(shape, dtype=like.dtype, device=like.device)
+    return grad.contiguous()
+
+
+class _ShortConv(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, h0, cu_seqlens, silu):
+        y, hT = conv_fwd(x, weight, bias, h0, cu_seqlens, silu)
+        ctx.save_for_backward(x, weight, bias, h0, cu_seqlens)
+        ctx.silu = silu
+        ctx.set_materialize_grads(False)
+        return y, hT
+
+    @staticmethod
+    @_once
+    def backward(ctx, dy, dhT):
+        x, weight, bias, h0, cu = ctx.saved_tensors
+        dy = _or_zeros(dy, x.shape, x)
+        dhT = None if dhT is None else dhT.contiguous()
+        dx, dw, db, dh0 = conv_bwd(dy, x, weight, bias, h0=h0, dhT=dhT, cu_seqlens=cu, silu=ctx.silu,
+                                   store_dh0=h0 is not None)
+        return dx, dw, db, dh0, None, None
+
+
+def short_conv(x, weight, bias=None, h0=None, cu_seqlens=None, silu=True):
+    """(y, hT) = conv_fwd(...), differentiable in x, weight, bias and h0 (the gradients come
+    from conv_bwd)."""
+    return _ShortConv.apply(x, weight, bias, h0, cu_seqlens, bool(silu))
+
+
+class _SelectiveScan(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens, softplus):
+        y, hT = scan_fwd(x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens, softplus)
+        ctx.save_for_backward(x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens)
+        ctx.softplus = softplus
+        ctx.set_materialize_grads(False)
+        return y, hT
+
+    @staticmethod
+    @_once
+    def backward(ctx, dy, dhT):
+        x, dt, A, B, C, D, z, dt_bias, h0, cu = ctx.saved_tensors
+        dy = _or_zeros(dy, x.shape, x)
+        dhT = None if dhT is None else dhT.contiguous()
+        return (*scan_bwd(dy, x, dt, A, B, C, D, z, dt_bias, h0, dhT, cu, ctx.softplus,
+                          store_dh0=h0 is not None), None, None)
+
+
+def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, cu_seqlens=None,
+                   softplus=True):
+    """(y, hT) = scan_fwd(...), differentiable in x, dt, A, B, C, D, z, dt_bias and h0 (the
+    gradients come from scan_bwd)."""
+    return _SelectiveScan.apply(x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens, bool(softplus))
+
+
+class _RmsNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps):
+        y, h, rstd = rmsnorm_fwd(x, weight, residual, eps=eps)
+        ctx.save_for_backward(h, rstd, weight)
+        ctx.added = residual is not None
+        ctx.set_materialize_grads(False)
+        return (y, h) if ctx.added else y
+
+    @staticmethod
+    @_once
+    def backward(ctx, dy, dh=None):
+        h, rstd, weight = ctx.saved_tensors
+        dy = _or_zeros(dy, h.shape, h)
+        dh = None if dh is None else dh.contiguous()
+        dx, dw = rmsnorm_bwd(dy, h, rstd, weight, dh=dh,
+                             weight_grad=weight is not None and ctx.needs_input_grad[1])
+        return dx, dw, dx if ctx.added else None, None
+
+
+def rms_norm(x, weight=None, residual=None, eps=1e-5):
+    """y, or with a residual (y, h), of rmsnorm_fwd(...), differentiable in x, weight and
+    residual (the gradients come from rmsnorm_bwd)."""
+    return _RmsNorm.apply(x, weight, residual, float(eps))

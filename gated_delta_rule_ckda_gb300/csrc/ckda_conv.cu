@@ -1,0 +1,605 @@
+// ckda_conv.cu -- short causal convolution of each channel, forward, backward and one
+// token on a resident state.
+//
+// Per channel, over the tokens of a sequence, with W = 2, 3 or 4 taps:
+//     p_t = b + sum_j w_j x_{t-W+1+j},    y_t = p_t / (1 + exp(-p_t))  or  p_t
+// where the inputs before the first token are the W - 1 rows of the initial state (or
+// zero) and the last W - 1 inputs are the final state.  With dp = dy silu'(p):
+//     dx_i = sum_k w_{W-1-k} dp_{i+k},   dw_j = sum_t dp_t x_{t-W+1+j},   db = sum_t dp_t
+// and a final state's gradient adds to the inputs that it holds.
+//
+// Each input is read once and each output written once; 2 W + 4 flop an element leave HBM
+// as the bound.  Channels are the fast axis: a thread has VEC neighbouring channels and
+// walks a run of tokens with the last W - 1 inputs in registers, loads of kAhead tokens in
+// flight.  A run starts W - 1 tokens early (backward: and ends W - 1 late), 5% at 64
+// tokens and mostly from L2.  Runs go over one flat axis of tokens, dense rows or packed
+// sequences alike, and take up the next sequence's state where one begins.
+//
+// The gradients of the weights: sums over a run in registers, over a block's runs in
+// shared memory, then one partial row a block in the workspace, added in a fixed order by
+// a second kernel.  No atomics: the same bits every time.
+#include "ckda_launch.cuh"
+#include "ckda_rows.cuh"
+
+namespace ckda {
+namespace {
+
+constexpr int kBlock = 256;
+constexpr int kAhead = 8;
+
+struct ConvArgs {
+  const void* x;
+  const void* dy;
+  const void* w;  // [D][W]
+  const void* b;
+  const void* h0;  // [seqs][W - 1][D]
+  const void* dhT;
+  void* y;   // dx in the backward pass
+  void* hT;  // dh0 in the backward pass
+  void* dw;
+  void* db;
+  float* part;  // [parts][W + 1][D]: sums of dw by tap, then db
+  const int32_t* cu;
+  long long ldx;  // elements from one token to the next
+  long long tokens;
+  int seqs, T, D;  // T: of a dense row
+  int w_bf16, silu;
+  int run;         // tokens of a run
+  int lanes;       // threads of a token, a power of two
+  int chan_blocks, parts;
+  long long main_blocks;  // blocks behind these have the states
+};
+
+__device__ __forceinline__ float weight_of(const void* w, int bf16, size_t i) {
+  return bf16 ? ld_io(static_cast<const __nv_bfloat16*>(w) + i) : static_cast<const float*>(w)[i];
+}
+__device__ __forceinline__ float sigmoid(float p) { return __fdividef(1.f, 1.f + __expf(-p)); }
+// (p / (1 + e^-p) by a division that gives 0 for e^-p past 2^126, as it should be but for
+// p = -inf, which has no value either way)
+__device__ __forceinline__ float silu(float p) { return __fdividef(p, 1.f + __expf(-p)); }
+__device__ __forceinline__ float silu_grad(float p) {
+  const float g = sigmoid(p);
+  return g * fmaf(p, 1.f - g, 1.f);
+}
+
+// A sequence's tokens [begin, end) on the flat axis.  Offsets that are out of order or out
+// of range leave every access inside the tensors.
+struct Seq {
+  long long begin, end;
+  int n;
+};
+__device__ __forceinline__ long long offset_of(const ConvArgs& a, int n) {
+  const long long o = a.cu[n];
+  return o < 0 ? 0 : o > a.tokens ? a.tokens : o;
+}
+__device__ __forceinline__ Seq seq_at(const ConvArgs& a, long long m) {
+  Seq s;
+  if (!a.cu) {
+    s.n = (int)(m / a.T);
+    s.begin = (long long)s.n * a.T;
+    s.end = s.begin + a.T;
+    return s;
+  }
+  int lo = 0, hi = a.seqs;  // the last n with cu[n] <= m
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a.cu[mid] <= m) lo = mid; else hi = mid;
+  }
+  s.n = lo;
+  s.begin = offset_of(a, lo);
+  s.end = offset_of(a, lo + 1);
+  return s;
+}
+
+template <typename IO, int VEC>
+__device__ __forceinline__ Pack<IO, VEC> load_row(const void* base, long long row, long long ld, int c) {
+  return *reinterpret_cast<const Pack<IO, VEC>*>(static_cast<const IO*>(base) + row * ld + c);
+}
+// Row i of the inputs before a sequence's token m: i = 0 is W - 1 tokens back.
+template <typename IO, int W, int VEC>
+__device__ __forceinline__ void input_before(const ConvArgs& a, const Seq& s, long long m, int i, int c,
+                                             float (&f)[VEC]) {
+  const long long t = m - (W - 1) + i;
+  if (t >= s.begin) {
+    unpack<IO, VEC>(load_row<IO, VEC>(a.x, t, a.ldx, c), f);
+  } else if (a.h0) {
+    const long long r = t - s.begin + W - 1;
+    unpack<IO, VEC>(load_row<IO, VEC>(a.h0, (long long)s.n * (W - 1) + (r < 0 ? 0 : r), a.D, c), f);
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) f[e] = 0.f;
+  }
+}
+
+template <int W, int VEC>
+struct Taps {
+  float w[W][VEC], b[VEC];
+  __device__ __forceinline__ void load(const ConvArgs& a, int c) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+#pragma unroll
+      for (int j = 0; j < W; ++j) w[j][e] = weight_of(a.w, a.w_bf16, (size_t)(c + e) * W + j);
+      b[e] = a.b ? weight_of(a.b, a.w_bf16, c + e) : 0.f;
+    }
+  }
+};
+
+// ------------------------------------------------------------------ forward
+// The final state of every sequence: its last W - 1 inputs, older ones from h0.
+template <typename IO, int W, int VEC>
+__device__ void final_states(const ConvArgs& a) {
+  const int vecs = a.D / VEC;
+  const long long n_all = (long long)a.seqs * (W - 1) * vecs;
+  const long long step = (long long)(gridDim.x - a.main_blocks) * kBlock;
+  for (long long i = ((long long)blockIdx.x - a.main_blocks) * kBlock + threadIdx.x; i < n_all; i += step) {
+    const int c = (int)(i % vecs) * VEC;
+    const int r = (int)(i / vecs % (W - 1));
+    Seq s;
+    s.n = (int)(i / vecs / (W - 1));
+    s.begin = a.cu ? offset_of(a, s.n) : (long long)s.n * a.T;
+    s.end = a.cu ? offset_of(a, s.n + 1) : s.begin + a.T;
+    if (s.end < s.begin) s.end = s.begin;
+    float f[VEC];
+    input_before<IO, W, VEC>(a, s, s.end, r, c, f);
+    store_vec<IO, VEC>(a.hT, ((long long)s.n * (W - 1) + r) * a.D + c, f);
+  }
+}
+
+template <typename IO, int W, int VEC>
+__global__ void __launch_bounds__(kBlock) conv_fwd_kernel(ConvArgs a) {
+  if (blockIdx.x >= a.main_blocks) {
+    final_states<IO, W, VEC>(a);
+    return;
+  }
+  const int chan = (int)(blockIdx.x % a.chan_blocks);
+  const long long tok = blockIdx.x / a.chan_blocks;
+  const int lane = threadIdx.x % a.lanes, grp = threadIdx.x / a.lanes;
+  const int c = (chan * a.lanes + lane) * VEC;
+  long long m = (tok * (kBlock / a.lanes) + grp) * a.run;
+  long long stop = m + a.run;
+  const long long last = a.cu ? offset_of(a, a.seqs) : a.tokens;
+  if (stop > last) stop = last;
+  if (c >= a.D || m >= stop) return;
+  Taps<W, VEC> taps;
+  taps.load(a, c);
+  Seq s = seq_at(a, m);
+  if (m < s.begin) m = s.begin;
+  float in[W - 1][VEC];  // the inputs before token m, oldest first
+#pragma unroll
+  for (int i = 0; i < W - 1; ++i) input_before<IO, W, VEC>(a, s, m, i, c, in[i]);
+  while (m < stop) {
+    Pack<IO, VEC> next[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (m + i < stop) next[i] = load_row<IO, VEC>(a.x, m + i, a.ldx, c);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (m + i >= stop) break;
+      if (m + i >= s.end) {  // the next sequence that has tokens
+        s = seq_at(a, m + i);
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) input_before<IO, W, VEC>(a, s, m + i, k, c, in[k]);
+      }
+      float x[VEC], p[VEC];
+      unpack<IO, VEC>(next[i], x);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        p[e] = fmaf(taps.w[W - 1][e], x[e], taps.b[e]);
+#pragma unroll
+        for (int k = W - 2; k >= 0; --k) p[e] = fmaf(taps.w[k][e], in[k][e], p[e]);
+        if (a.silu) p[e] = silu(p[e]);
+#pragma unroll
+        for (int k = 0; k < W - 2; ++k) in[k][e] = in[k + 1][e];
+        in[W - 2][e] = x[e];
+      }
+      store_vec<IO, VEC>(a.y, (m + i) * a.D + c, p);
+    }
+    m += kAhead;
+  }
+}
+
+// ----------------------------------------------------------------- backward
+// The initial state's gradient: row r feeds tap r - k of token k, and a sequence shorter
+// than the state hands its row r on as row r - length.
+template <typename IO, int W>
+__device__ void initial_grads(const ConvArgs& a) {
+  const long long n_all = (long long)a.seqs * a.D;
+  const long long step = (long long)(gridDim.x - a.main_blocks) * kBlock;
+  for (long long i = ((long long)blockIdx.x - a.main_blocks) * kBlock + threadIdx.x; i < n_all; i += step) {
+    const int c = (int)(i % a.D);
+    Seq s;
+    s.n = (int)(i / a.D);
+    s.begin = a.cu ? offset_of(a, s.n) : (long long)s.n * a.T;
+    s.end = a.cu ? offset_of(a, s.n + 1) : s.begin + a.T;
+    const int length = (int)(s.end - s.begin < W - 1 ? (s.end > s.begin ? s.end - s.begin : 0) : W - 1);
+    Taps<W, 1> taps;
+    taps.load(a, c);
+    float dp[W - 1];
+#pragma unroll
+    for (int t = 0; t < W - 1; ++t) {
+      dp[t] = 0.f;
+      if (t >= length) continue;
+      dp[t] = ld_io(static_cast<const IO*>(a.dy) + (s.begin + t) * a.D + c);
+      if (!a.silu) continue;
+      float p = fmaf(taps.w[W - 1][0], ld_io(static_cast<const IO*>(a.x) + (s.begin + t) * a.ldx + c),
+                     taps.b[0]);
+#pragma unroll
+      for (int k = 0; k < W - 1; ++k) {
+        float f[1];
+        input_before<IO, W, 1>(a, s, s.begin + t, k, c, f);
+        p = fmaf(taps.w[k][0], f[0], p);
+      }
+      dp[t] *= silu_grad(p);
+    }
+#pragma unroll
+    for (int r = 0; r < W - 1; ++r) {
+      float g = 0.f;
+#pragma unroll
+      for (int t = 0; t <= r; ++t) g = fmaf(taps.w[r - t][0], dp[t], g);
+      if (a.dhT && r >= length)
+        g += ld_io(static_cast<const IO*>(a.dhT) + ((long long)s.n * (W - 1) + r - length) * a.D + c);
+      st_io(static_cast<IO*>(a.hT) + ((long long)s.n * (W - 1) + r) * a.D + c, g);
+    }
+  }
+}
+
+template <typename IO, int W, int VEC>
+__global__ void __launch_bounds__(kBlock) conv_bwd_kernel(ConvArgs a) {
+  if (blockIdx.x >= a.main_blocks) {
+    initial_grads<IO, W>(a);
+    return;
+  }
+  const int chan = (int)(blockIdx.x % a.chan_blocks);
+  const long long tok = blockIdx.x / a.chan_blocks;
+  const int lane = threadIdx.x % a.lanes, grp = threadIdx.x / a.lanes, groups = kBlock / a.lanes;
+  const int c = (chan * a.lanes + lane) * VEC;
+  const long long last = a.cu ? offset_of(a, a.seqs) : a.tokens;
+  long long m = (tok * groups + grp) * a.run;
+  long long stop = m + a.run < last ? m + a.run : last;
+  float dw[W][VEC], db[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    db[e] = 0.f;
+#pragma unroll
+    for (int j = 0; j < W; ++j) dw[j][e] = 0.f;
+  }
+  if (c < a.D && m < stop) {
+    Taps<W, VEC> taps;
+    taps.load(a, c);
+    while (m < stop) {  // the run's part of one sequence after another
+      const Seq s = seq_at(a, m);
+      if (m < s.begin) m = s.begin;
+      const long long own = s.end < stop ? s.end : stop;          // tokens of this run
+      const long long seen = s.end < own + W - 1 ? s.end : own + W - 1;  // that its inputs reach
+      float in[W - 1][VEC], dp[W][VEC];  // dp[k]: of token t - (W - 1) + k
+#pragma unroll
+      for (int k = 0; k < W - 1; ++k) input_before<IO, W, VEC>(a, s, m, k, c, in[k]);
+#pragma unroll
+      for (int k = 0; k < W; ++k)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) dp[k][e] = 0.f;
+      constexpr int kN = kAhead / 2;
+      for (long long t0 = m; t0 < own + W - 1; t0 += kN) {
+        Pack<IO, VEC> xs[kN], gs[kN];
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+          if (t0 + i < seen) {
+            xs[i] = load_row<IO, VEC>(a.x, t0 + i, a.ldx, c);
+            gs[i] = load_row<IO, VEC>(a.dy, t0 + i, a.D, c);
+          }
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          const long long t = t0 + i;
+#pragma unroll
+          for (int k = 0; k < W - 1; ++k)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) dp[k][e] = dp[k + 1][e];
+          if (t < seen) {
+            float x[VEC], g[VEC];
+            unpack<IO, VEC>(xs[i], x);
+            unpack<IO, VEC>(gs[i], g);
+            const bool mine = t < own;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+              if (a.silu) {
+                float p = fmaf(taps.w[W - 1][e], x[e], taps.b[e]);
+#pragma unroll
+                for (int k = W - 2; k >= 0; --k) p = fmaf(taps.w[k][e], in[k][e], p);
+                g[e] *= silu_grad(p);
+              }
+              dp[W - 1][e] = g[e];
+              if (mine) {
+                db[e] += g[e];
+                dw[W - 1][e] = fmaf(g[e], x[e], dw[W - 1][e]);
+#pragma unroll
+                for (int k = 0; k < W - 1; ++k) dw[k][e] = fmaf(g[e], in[k][e], dw[k][e]);
+              }
+#pragma unroll
+              for (int k = 0; k < W - 2; ++k) in[k][e] = in[k + 1][e];
+              in[W - 2][e] = x[e];
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) dp[W - 1][e] = 0.f;
+          }
+          const long long out = t - (W - 1);  // the input that has met all its tokens
+          if (out < m || out >= own) continue;
+          float dx[VEC];
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            dx[e] = taps.w[W - 1][e] * dp[0][e];
+#pragma unroll
+            for (int k = 1; k < W; ++k) dx[e] = fmaf(taps.w[W - 1 - k][e], dp[k][e], dx[e]);
+          }
+          const long long row = out - (s.end - (W - 1));
+          if (a.dhT && row >= 0) {
+            float f[VEC];
+            unpack<IO, VEC>(load_row<IO, VEC>(a.dhT, (long long)s.n * (W - 1) + row, a.D, c), f);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) dx[e] += f[e];
+          }
+          store_vec<IO, VEC>(a.y, out * a.D + c, dx);
+        }
+      }
+      m = own > m ? own : stop;
+    }
+  }
+  // the runs of a block that share channels, in order
+  __shared__ float sum[kBlock][VEC + 1];
+#pragma unroll
+  for (int j = 0; j <= W; ++j) {
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) sum[threadIdx.x][e] = j < W ? dw[j < W ? j : 0][e] : db[e];
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.lanes * VEC; i += kBlock) {
+      const int at = chan * a.lanes * VEC + i;
+      if (at >= a.D) continue;
+      float t = 0.f;
+      for (int g = 0; g < groups; ++g) t += sum[g * a.lanes + i / VEC][i % VEC];
+      a.part[((size_t)tok * (W + 1) + j) * a.D + at] = t;
+    }
+  }
+}
+
+// dw and db from the partial rows: 32 channels to a block, 32 threads a channel over the
+// partial rows, joined in a fixed order.
+template <int W>
+__global__ void __launch_bounds__(1024) conv_weight_grad_kernel(ConvArgs a) {
+  after_previous();
+  __shared__ float s[32][33];
+  const int c = threadIdx.x & 31, g = threadIdx.x >> 5, j = blockIdx.y;
+  const int i = blockIdx.x * 32 + c;
+  float t = 0.f;
+  if (i < a.D)
+#pragma unroll 8
+    for (int r = g; r < a.parts; r += 32) t += a.part[((size_t)r * (W + 1) + j) * a.D + i];
+  s[g][c] = t;
+  __syncthreads();
+  if (g == 0 && i < a.D) {
+#pragma unroll
+    for (int k = 1; k < 32; ++k) t += s[k][c];
+    void* out = j < W ? a.dw : a.db;
+    const size_t at = j < W ? (size_t)i * W + j : i;
+    if (!out) return;
+    if (a.w_bf16)
+      st_io(static_cast<__nv_bfloat16*>(out) + at, t);
+    else
+      static_cast<float*>(out)[at] = t;
+  }
+}
+
+// --------------------------------------------------------------- single token
+template <typename IO, int W, int VEC>
+__global__ void __launch_bounds__(kBlock) conv_step_kernel(ConvArgs a) {
+  const int vecs = a.D / VEC;
+  const long long i = (long long)blockIdx.x * kBlock + threadIdx.x;
+  if (i >= a.tokens * vecs) return;
+  const long long row = i / vecs;
+  const int c = (int)(i % vecs) * VEC;
+  IO* st = static_cast<IO*>(a.hT) + row * (W - 1) * a.D + c;
+  Pack<IO, VEC> in[W];
+#pragma unroll
+  for (int k = 0; k < W - 1; ++k) in[k] = *reinterpret_cast<const Pack<IO, VEC>*>(st + (size_t)k * a.D);
+  in[W - 1] = load_row<IO, VEC>(a.x, row, a.ldx, c);
+  Taps<W, VEC> taps;
+  taps.load(a, c);
+  float p[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    p[e] = taps.b[e];
+#pragma unroll
+    for (int k = W - 1; k >= 0; --k) p[e] = fmaf(taps.w[k][e], ld_io(&in[k].v[e]), p[e]);
+    if (a.silu) p[e] = silu(p[e]);
+  }
+  store_vec<IO, VEC>(a.y, row * a.D + c, p);
+#pragma unroll
+  for (int k = 0; k < W - 1; ++k) *reinterpret_cast<Pack<IO, VEC>*>(st + (size_t)k * a.D) = in[k + 1];
+}
+
+// ----------------------------------------------------------------- dispatch
+inline bool aligned(const void* p, size_t bytes) {
+  return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
+}
+// Threads of a token: a warp, fewer where the channels are fewer.
+inline int lanes_of(int vecs) {
+  int lanes = 1;
+  while (lanes < 32 && lanes < vecs) lanes *= 2;
+  return lanes;
+}
+inline int chan_blocks_of(int D, int vec) {
+  const int lanes = lanes_of((D + vec - 1) / vec);
+  return (D + lanes * vec - 1) / (lanes * vec);
+}
+// Tokens of a run: 64 where there are enough for every SM, shorter ones else.
+inline int run_of(long long tokens, int D, int vec) {
+  const int lanes = lanes_of((D + vec - 1) / vec);
+  int run = 64;
+  while (run > 8 && (tokens + (long long)run * (kBlock / lanes) - 1) / (run * (kBlock / lanes)) *
+                            chan_blocks_of(D, vec) < 2 * kSms)
+    run /= 2;
+  return run;
+}
+constexpr int kBwdVec = 4;
+inline long long token_blocks(long long tokens, int D, int vec) {
+  const long long per = (long long)run_of(tokens, D, vec) * (kBlock / lanes_of((D + vec - 1) / vec));
+  return (tokens + per - 1) / per;
+}
+
+template <int VEC>
+void plan(ConvArgs& a) {
+  a.lanes = lanes_of((a.D + VEC - 1) / VEC);
+  a.chan_blocks = chan_blocks_of(a.D, VEC);
+  a.run = run_of(a.tokens, a.D, VEC);
+  a.parts = (int)token_blocks(a.tokens, a.D, VEC);
+  a.main_blocks = (long long)a.parts * a.chan_blocks;
+}
+
+template <typename IO, int W, int VEC>
+cudaError_t run_fwd(ConvArgs a, cudaStream_t s) {
+  plan<VEC>(a);
+  const long long more =
+      a.hT ? blocks_for(((long long)a.seqs * (W - 1) * (a.D / VEC) + kBlock - 1) / kBlock, 2) : 0;
+  if (a.main_blocks + more == 0) return cudaSuccess;
+  conv_fwd_kernel<IO, W, VEC><<<(unsigned)(a.main_blocks + more), kBlock, 0, s>>>(a);
+  return cudaGetLastError();
+}
+template <typename IO, int W, int VEC>
+cudaError_t run_bwd(ConvArgs a, cudaStream_t s) {
+  plan<VEC>(a);
+  const long long more = a.hT ? blocks_for(((long long)a.seqs * a.D + kBlock - 1) / kBlock, 2) : 0;
+  if (a.main_blocks + more > 0)
+    conv_bwd_kernel<IO, W, VEC><<<(unsigned)(a.main_blocks + more), kBlock, 0, s>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_next(a.main_blocks + more > 0, conv_weight_grad_kernel<W>, dim3((a.D + 31) / 32, W + 1),
+                     1024, 0, s, a);
+}
+template <typename IO, int W, int VEC>
+cudaError_t run_step(const ConvArgs& a, cudaStream_t s) {
+  const long long n = a.tokens * (a.D / VEC);
+  conv_step_kernel<IO, W, VEC><<<(unsigned)((n + kBlock - 1) / kBlock), kBlock, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+enum class Call { kFwd, kBwd, kStep };
+
+template <typename IO, int W>
+cudaError_t launch_taps(const ConvArgs& a, Call call, cudaStream_t s) {
+  constexpr int kVec = 16 / sizeof(IO);
+  const auto fits = [&](int vec) {
+    const size_t bytes = vec * sizeof(IO);
+    return a.D % vec == 0 && a.ldx % vec == 0 && aligned(a.x, bytes) && aligned(a.dy, bytes) &&
+           aligned(a.h0, bytes) && aligned(a.dhT, bytes) && aligned(a.y, bytes) && aligned(a.hT, bytes);
+  };
+  if (call == Call::kFwd) return fits(kVec) ? run_fwd<IO, W, kVec>(a, s) : run_fwd<IO, W, 1>(a, s);
+  if (call == Call::kBwd) return fits(kBwdVec) ? run_bwd<IO, W, kBwdVec>(a, s) : run_bwd<IO, W, 1>(a, s);
+  return fits(kVec) ? run_step<IO, W, kVec>(a, s) : run_step<IO, W, 1>(a, s);
+}
+template <typename IO>
+cudaError_t launch_io(const ConvArgs& a, int W, Call call, cudaStream_t s) {
+  if (W == 2) return launch_taps<IO, 2>(a, call, s);
+  if (W == 3) return launch_taps<IO, 3>(a, call, s);
+  return launch_taps<IO, 4>(a, call, s);
+}
+ckda_status launch(const ConvArgs& a, int W, ckda_dtype io, Call call, void* stream) {
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = io == CKDA_F32 ? launch_io<float>(a, W, call, s)
+                                       : launch_io<__nv_bfloat16>(a, W, call, s);
+  return e == cudaSuccess ? CKDA_OK : CKDA_ERR_CUDA;
+}
+
+ckda_status check_conv(int B, int T, int D, int W, long long ldx, ckda_dtype io, ckda_dtype wt) {
+  if (io != CKDA_F32 && io != CKDA_BF16) return CKDA_ERR_INVALID_ARG;
+  if (wt != CKDA_F32 && wt != CKDA_BF16) return CKDA_ERR_INVALID_ARG;
+  if (B < 1 || T < 0 || D < 1 || ldx < D) return CKDA_ERR_INVALID_ARG;
+  if (W < 2 || W > 4 || D > 1 << 24) return CKDA_ERR_UNSUPPORTED;
+  // (tokens and blocks are counted in 32 bits on the grid)
+  if ((long long)B * T > 0x7fffffffLL || ldx > 1LL << 31) return CKDA_ERR_UNSUPPORTED;
+  if ((long long)B * T * ((D + 31) / 32) > 8LL * 0x7fffffffLL) return CKDA_ERR_UNSUPPORTED;
+  return CKDA_OK;
+}
+inline size_t span_bytes(int B, int T, int D, long long ld, size_t io) {
+  const long long rows = (long long)B * T;
+  return rows > 0 ? (size_t)((rows - 1) * ld + D) * io : 0;
+}
+// Whether [p, p + n) and [q, q + m) share memory.
+inline bool overlap(const void* p, size_t n, const void* q, size_t m) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return p && q && a < b + m && b < a + n;
+}
+
+}  // namespace
+}  // namespace ckda
+
+using namespace ckda;
+
+extern "C" {
+
+ckda_status ckda_conv_fwd(const void* x, const void* weight, const void* bias, const void* h0,
+                          void* y, void* hT, const int32_t* cu_seqlens, int num_seqs, int B, int T,
+                          int D, int W, long long ldx, ckda_dtype io_dtype, ckda_dtype weight_dtype,
+                          int silu, void* stream) {
+  const ckda_status st = check_conv(B, T, D, W, ldx, io_dtype, weight_dtype);
+  if (st != CKDA_OK) return st;
+  if (cu_seqlens && (num_seqs < 1 || B != 1)) return CKDA_ERR_INVALID_ARG;
+  if (!weight || (T > 0 && (!x || !y))) return CKDA_ERR_INVALID_ARG;
+  const int seqs = cu_seqlens ? num_seqs : B;
+  const size_t io = io_dtype == CKDA_F32 ? 4 : 2;
+  // blocks that write one of these run beside blocks that still read the other
+  if (overlap(h0, (size_t)seqs * (W - 1) * D * io, hT, (size_t)seqs * (W - 1) * D * io) ||
+      overlap(x, span_bytes(B, T, D, ldx, io), y, span_bytes(B, T, D, D, io)))
+    return CKDA_ERR_INVALID_ARG;
+  ConvArgs a{};
+  a.x = x; a.w = weight; a.b = bias; a.h0 = h0; a.y = y; a.hT = hT; a.cu = cu_seqlens;
+  a.ldx = ldx; a.tokens = (long long)B * T; a.seqs = seqs; a.T = T; a.D = D;
+  a.w_bf16 = weight_dtype == CKDA_BF16; a.silu = silu != 0;
+  return launch(a, W, io_dtype, Call::kFwd, stream);
+}
+
+size_t ckda_conv_bwd_workspace_bytes(int B, int T, int D, int W) {
+  if (B < 1 || T < 0 || D < 1 || W < 2 || W > 4) return 0;
+  const long long tokens = (long long)B * T;
+  const long long parts = D % kBwdVec == 0 && token_blocks(tokens, D, kBwdVec) > token_blocks(tokens, D, 1)
+                              ? token_blocks(tokens, D, kBwdVec)
+                              : token_blocks(tokens, D, 1);
+  return ((size_t)parts * (W + 1) * D + 4) * sizeof(float);
+}
+
+ckda_status ckda_conv_bwd(const void* dy, const void* x, const void* weight, const void* bias,
+                          const void* h0, const void* dhT, void* dx, void* dweight, void* dbias,
+                          void* dh0, const int32_t* cu_seqlens, int num_seqs, int B, int T, int D,
+                          int W, long long ldx, ckda_dtype io_dtype, ckda_dtype weight_dtype,
+                          int silu, void* workspace, size_t workspace_bytes, void* stream) {
+  const ckda_status st = check_conv(B, T, D, W, ldx, io_dtype, weight_dtype);
+  if (st != CKDA_OK) return st;
+  if (cu_seqlens && (num_seqs < 1 || B != 1)) return CKDA_ERR_INVALID_ARG;
+  if (!weight || !dweight || (T > 0 && (!x || !dy || !dx))) return CKDA_ERR_INVALID_ARG;
+  const size_t io = io_dtype == CKDA_F32 ? 4 : 2;
+  if (overlap(x, span_bytes(B, T, D, ldx, io), dx, span_bytes(B, T, D, D, io)) ||
+      overlap(dy, span_bytes(B, T, D, D, io), dx, span_bytes(B, T, D, D, io)))
+    return CKDA_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < ckda_conv_bwd_workspace_bytes(B, T, D, W) || !aligned(workspace, 16))
+    return CKDA_ERR_WORKSPACE;
+  ConvArgs a{};
+  a.x = x; a.dy = dy; a.w = weight; a.b = bias; a.h0 = h0; a.dhT = dhT; a.y = dx; a.hT = dh0;
+  a.dw = dweight; a.db = dbias; a.part = static_cast<float*>(workspace); a.cu = cu_seqlens;
+  a.ldx = ldx; a.tokens = (long long)B * T; a.seqs = cu_seqlens ? num_seqs : B; a.T = T; a.D = D;
+  a.w_bf16 = weight_dtype == CKDA_BF16; a.silu = silu != 0;
+  return launch(a, W, io_dtype, Call::kBwd, stream);
+}
+
+ckda_status ckda_conv_decode_step(const void* x, const void* weight, const void* bias, void* state,
+                                  void* y, int B, int D, int W, long long ldx, ckda_dtype io_dtype,
+                                  ckda_dtype weight_dtype, int silu, void* stream) {
+  const ckda_status st = check_conv(B, 1, D, W, ldx, io_dtype, weight_dtype);
+  if (st != CKDA_OK) return st;
+  if (!x || !weight || !state || !y) return CKDA_ERR_INVALID_ARG;
+  ConvArgs a{};
+  a.x = x; a.w = weight; a.b = bias; a.hT = state; a.y = y;
+  a.ldx = ldx; a.tokens = B; a.seqs = B; a.T = 1; a.D = D;
+  a.w_bf16 = weight_dtype == CKDA_BF16; a.silu = silu != 0;
+  return launch(a, W, io_dtype, Call::kStep, stream);
+}
+
+}  // extern "C"

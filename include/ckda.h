@@ -29,9 +29,9 @@
  *   - k is NOT normalised by the library: ||k_t|| = 1 is the caller's
  *     precondition, as on the pages.  The library accepts any finite k.
  *   - The compute calls (ckda_fwd, ckda_fwd_raw, the split forwards,
- *     ckda_decode_step(_raw), ckda_prep(_bwd), ckda_bwd, the ckda_linear_ and
- *     ckda_layernorm_ calls) enqueue only kernels
- *     and asynchronous memsets on `stream`, so they may be captured into a
+ *     ckda_decode_step(_raw), ckda_prep(_bwd), ckda_bwd, the ckda_linear_,
+ *     ckda_layernorm_, ckda_conv_, ckda_scan_ and ckda_rmsnorm_ calls) enqueue
+ *     only kernels and asynchronous memsets on `stream`, so they may be captured into a
  *     CUDA graph and replayed; the tensor maps and launch arguments are fixed
  *     at capture.  ckda_fwd_status and ckda_fwd_host synchronise and may not
  *     be captured; ckda_fwd_noalloc only after its first call in the context.
@@ -581,6 +581,167 @@ ckda_status ckda_layernorm_bwd(const void *dy, const void *x, const float *mean,
                                void *dbias, long long rows, int width, ckda_dtype io_dtype,
                                ckda_dtype weight_dtype, void *workspace,
                                size_t workspace_bytes, void *stream);
+
+/*
+ * Short causal convolution of each channel over the tokens of a sequence, W = 2, 3
+ * or 4 taps (before a token mixer: q, k and v of a linear attention layer, x of a
+ * state space one):
+ *     p_t = bias + sum_j weight_j x_{t-W+1+j},   y_t = p_t / (1 + exp(-p_t)), or
+ *     p_t with silu = 0
+ *
+ *   x          : io [B, T, D], channels last; token t of row b at x + (b T + t) ldx
+ *                elements, ldx >= D (a part of a wider projection)
+ *   y          : io [B, T, D]
+ *   weight     : weight_dtype [D, W], bias [D] or NULL (zero)
+ *   h0, hT     : io [N, W - 1, D], the inputs before a sequence's first token and its
+ *                last W - 1 inputs (older ones from h0 where it is shorter), oldest
+ *                first; NULL: zero, not stored.  An empty sequence hands h0 on.
+ *   cu_seqlens, num_seqs: as ckda_fwd (packed sequences, B = 1, N = num_seqs); tokens
+ *                behind the last sequence are left as they were.
+ *
+ * hT must not overlap h0, nor y x (checked).  Arithmetic in fp32, one rounding.
+ * T = 0 hands the states on.  A token that is not finite reaches only the W tokens of its
+ * channel that the formula gives it to.
+ */
+ckda_status ckda_conv_fwd(const void *x, const void *weight, const void *bias, const void *h0,
+                          void *y, void *hT, const int32_t *cu_seqlens, int num_seqs, int B,
+                          int T, int D, int W, long long ldx, ckda_dtype io_dtype,
+                          ckda_dtype weight_dtype, int silu, void *stream);
+
+/*
+ * Its backward: the gradients of sum <y, dy> + <hT, dhT>.
+ *   dy, dx   : io [B, T, D]; dx overlaps neither x nor dy (checked)
+ *   dhT, dh0 : io [N, W - 1, D] or NULL (zero, not stored)
+ *   dweight  : weight_dtype [D, W]; dbias [D] or NULL (not wanted); from fp32 sums in a
+ *              fixed order: the same inputs give the same bits
+ * workspace: ckda_conv_bwd_workspace_bytes(B, T, D, W) bytes, 16-byte aligned, scratch.
+ */
+size_t ckda_conv_bwd_workspace_bytes(int B, int T, int D, int W);
+ckda_status ckda_conv_bwd(const void *dy, const void *x, const void *weight, const void *bias,
+                          const void *h0, const void *dhT, void *dx, void *dweight, void *dbias,
+                          void *dh0, const int32_t *cu_seqlens, int num_seqs, int B, int T,
+                          int D, int W, long long ldx, ckda_dtype io_dtype,
+                          ckda_dtype weight_dtype, int silu, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
+/*
+ * One token of the same convolution: x, y io [B, D] (rows of x ldx elements apart);
+ * state io [B, W - 1, D], moved on by the token in place.
+ */
+ckda_status ckda_conv_decode_step(const void *x, const void *weight, const void *bias,
+                                  void *state, void *y, int B, int D, int W, long long ldx,
+                                  ckda_dtype io_dtype, ckda_dtype weight_dtype, int silu,
+                                  void *stream);
+
+/*
+ * Selective state space scan: N states to each of D channels, with step sizes,
+ * inputs and readouts by token:
+ *     delta_t = softplus(dt_t + dt_bias)          (softplus = 0: dt_t + dt_bias)
+ *     h_t[n]  = exp(delta_t A[n]) h_{t-1}[n] + delta_t x_t Bm_t[n]
+ *     y_t     = (sum_n C_t[n] h_t[n] + D_skip x_t) z_t / (1 + exp(-z_t))
+ *
+ *   x, dt, z, y : io   [B, T, D], channels last; z NULL: no gate
+ *   Bm, C       : io   [B, T, G, N]; channel d reads group d / (D / G); G divides D
+ *   A           : fp32 [D, N], finite; D_skip, dt_bias fp32 [D] or NULL (zero)
+ *   h0, hT      : fp32 [sequences, D, N] or NULL (zero, not stored); hT must not overlap
+ *                 h0 (checked), y no input
+ *   ldx, lddt, ldb, ldc, ldz: elements from one token to the next (at least D, or G N)
+ *   cu_seqlens, num_seqs: as ckda_fwd (packed sequences, B = 1); an empty sequence hands
+ *                 its h0 on; tokens behind the last sequence are left as they were
+ *
+ * N <= 64.  States, steps and sums are fp32, one rounding to io.  A channel count per
+ * group that is a multiple of 8, N = 4, 8, 16, 32 or 64 and 16-byte aligned rows move in
+ * vectors.  Rows with too few channels for the GPU are cut into pieces that run side by
+ * side.  A value that is not finite stays in its own sequence, from its token on, and in
+ * its own channel where it is x's, dt's or z's.
+ *
+ * workspace: ckda_scan_fwd_workspace_bytes(...) bytes (0: may be NULL), 16-byte aligned,
+ * scratch; calls that overlap need one each.
+ */
+size_t ckda_scan_fwd_workspace_bytes(int B, int T, int D, int N, int G);
+ckda_status ckda_scan_fwd(const void *x, const void *dt, const float *A, const void *Bm,
+                          const void *C, const float *D_skip, const void *z,
+                          const float *dt_bias, const float *h0, void *y, float *hT,
+                          const int32_t *cu_seqlens, int num_seqs, int B, int T, int D, int N,
+                          int G, long long ldx, long long lddt, long long ldb, long long ldc,
+                          long long ldz, ckda_dtype io_dtype, int softplus, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
+/*
+ * Its backward: the gradients of sum <y, dy> + <hT, dhT>.
+ *   dy, dx, ddt, dz : io   [B, T, D] (dz NULL exactly where z is)
+ *   dBm, dC         : io   [B, T, G, N], summed over the group's channels
+ *   dA              : fp32 [D, N]; dD_skip, ddt_bias fp32 [D] or NULL (not wanted)
+ *   dhT, dh0        : fp32 [sequences, D, N] or NULL (zero, not stored)
+ * The forward's states are recomputed.  No atomics: the same inputs give the same bits.
+ * workspace: ckda_scan_bwd_workspace_bytes(...) bytes, 16-byte aligned, scratch: mostly
+ * the states before every 8th token.
+ */
+size_t ckda_scan_bwd_workspace_bytes(int B, int T, int D, int N, int G);
+ckda_status ckda_scan_bwd(const void *dy, const void *x, const void *dt, const float *A,
+                          const void *Bm, const void *C, const float *D_skip, const void *z,
+                          const float *dt_bias, const float *h0, const float *dhT, void *dx,
+                          void *ddt, float *dA, void *dBm, void *dC, float *dD_skip, void *dz,
+                          float *ddt_bias, float *dh0, const int32_t *cu_seqlens, int num_seqs,
+                          int B, int T, int D, int N, int G, long long ldx, long long lddt,
+                          long long ldb, long long ldc, long long ldz, ckda_dtype io_dtype,
+                          int softplus, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * One token of the same scan on a resident state, updated in place.
+ *   x, dt, z, y : io [B, D];  Bm, C : io [B, G, N];  state : fp32 [B, D, N]
+ */
+ckda_status ckda_scan_decode_step(const void *x, const void *dt, const float *A, const void *Bm,
+                                  const void *C, const float *D_skip, const void *z,
+                                  const float *dt_bias, float *state, void *y, int B, int D,
+                                  int N, int G, long long ldx, long long lddt, long long ldb,
+                                  long long ldc, long long ldz, ckda_dtype io_dtype,
+                                  int softplus, void *stream);
+
+/*
+ * Root-mean-square norm over the last axis, with a residual added before it:
+ *     h = x + residual (rounded to io),  y = h rstd weight,
+ *     rstd = 1 / sqrt(mean(h^2) + eps)
+ *   x, residual, h, y : io [rows, width]; residual and h are both NULL (h is x) or both
+ *                       set; h may be x or residual, y may be x, and not h
+ *   weight            : weight_dtype [width] or NULL (one)
+ *   rstd              : fp32 [rows]
+ * Arithmetic in fp32 with one rounding (squares of values past 1e19 leave its range).  Up
+ * to 2^31 - 1 rows of any width up to 2^30; 16-byte aligned rows are moved in vectors.
+ */
+ckda_status ckda_rmsnorm_fwd(const void *x, const void *residual, const void *weight, void *h,
+                             void *y, float *rstd, long long rows, int width,
+                             ckda_dtype io_dtype, ckda_dtype weight_dtype, float eps,
+                             void *stream);
+
+/*
+ * The same with y in 8 bits (e4m3) and scales, y = y8 scale:
+ *     scale = max(m, 2^-100) / 448, m the largest |y| of a group of columns
+ *   y8    : [rows, width] bytes, rounded once from y in fp32; overlaps no other tensor
+ *   scale : fp32 [rows] (group = 0: the whole row) or [rows, width / group]
+ *   group : 0, 32, 64 or 128, dividing width
+ */
+ckda_status ckda_rmsnorm_fwd8(const void *x, const void *residual, const void *weight, void *h,
+                              void *y8, float *scale, float *rstd, long long rows, int width,
+                              int group, ckda_dtype io_dtype, ckda_dtype weight_dtype,
+                              float eps, void *stream);
+
+/*
+ * Backward of both (the gradient passes the rounding to 8 bits as it is): with
+ * t = dy weight and xh = h rstd, per row
+ *     dx = rstd (t - xh mean(t xh)) + dh,
+ * the gradient of x and of residual alike, and dweight = sum over rows of dy xh.
+ *   dh : io [rows, width], the gradient that arrives at h itself, or NULL (zero)
+ *   dx may alias dy, h or dh; dweight NULL: not wanted (the workspace may then be NULL).
+ *   rows = 0 writes a zero dweight.  workspace: ckda_rmsnorm_bwd_workspace_bytes(rows,
+ *   width) bytes, 16-byte aligned.
+ */
+size_t ckda_rmsnorm_bwd_workspace_bytes(long long rows, int width);
+ckda_status ckda_rmsnorm_bwd(const void *dy, const void *h, const float *rstd,
+                             const void *weight, const void *dh, void *dx, void *dweight,
+                             long long rows, int width, ckda_dtype io_dtype,
+                             ckda_dtype weight_dtype, void *workspace, size_t workspace_bytes,
+                             void *stream);
 
 /*
  * Self-test of the bounded-wait path: launches one block that waits on a
