@@ -25,7 +25,9 @@ namespace ckda {
 namespace {
 
 constexpr int kBlock = 256;
-constexpr int kAhead = 8;
+constexpr int kAhead = 4;
+constexpr int kVec = 4;
+constexpr float kLog2e = 1.4426950408889634f;
 
 struct ConvArgs {
   const void* x;
@@ -53,13 +55,21 @@ struct ConvArgs {
 __device__ __forceinline__ float weight_of(const void* w, int bf16, size_t i) {
   return bf16 ? ld_io(static_cast<const __nv_bfloat16*>(w) + i) : static_cast<const float*>(w)[i];
 }
-__device__ __forceinline__ float sigmoid(float p) { return __fdividef(1.f, 1.f + __expf(-p)); }
-// (p / (1 + e^-p) by a division that gives 0 for e^-p past 2^126, as it should be but for
-// p = -inf, which has no value either way)
-__device__ __forceinline__ float silu(float p) { return __fdividef(p, 1.f + __expf(-p)); }
-__device__ __forceinline__ float silu_grad(float p) {
-  const float g = sigmoid(p);
-  return g * fmaf(p, 1.f - g, 1.f);
+// 1 / (1 + 2^a), 0 where 2^a leaves fp32 (p / (1 + e^-p) at p = -inf has no value either way)
+__device__ __forceinline__ float one_plus_inverse(float a) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(a));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return r;
+}
+__device__ __forceinline__ float2 one_plus_inverse(float2 a) {
+  float2 e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(a.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(a.y));
+  e = add_(e, both<float2>(1.f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(e.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(e.y));
+  return r;
 }
 
 // A sequence's tokens [begin, end) on the flat axis.  Offsets that are out of order or out
@@ -95,34 +105,82 @@ template <typename IO, int VEC>
 __device__ __forceinline__ Pack<IO, VEC> load_row(const void* base, long long row, long long ld, int c) {
   return *reinterpret_cast<const Pack<IO, VEC>*>(static_cast<const IO*>(base) + row * ld + c);
 }
-// Row i of the inputs before a sequence's token m: i = 0 is W - 1 tokens back.
-template <typename IO, int W, int VEC>
-__device__ __forceinline__ void input_before(const ConvArgs& a, const Seq& s, long long m, int i, int c,
-                                             float (&f)[VEC]) {
-  const long long t = m - (W - 1) + i;
-  if (t >= s.begin) {
-    unpack<IO, VEC>(load_row<IO, VEC>(a.x, t, a.ldx, c), f);
-  } else if (a.h0) {
-    const long long r = t - s.begin + W - 1;
-    unpack<IO, VEC>(load_row<IO, VEC>(a.h0, (long long)s.n * (W - 1) + (r < 0 ? 0 : r), a.D, c), f);
-  } else {
+// A thread's VEC channels as pairs.
+template <int VEC>
+struct Chans {
+  using V = typename Pairs<VEC>::V;
+  static constexpr int kN = Pairs<VEC>::kN;
+  V v[kN];
+  __device__ __forceinline__ float* flat() { return reinterpret_cast<float*>(v); }
+  __device__ __forceinline__ void fill(float f) {
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) f[e] = 0.f;
+    for (int e = 0; e < kN; ++e) v[e] = both<V>(f);
   }
-}
-
+  template <typename IO>
+  __device__ __forceinline__ void from(const Pack<IO, VEC>& p) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) flat()[e] = ld_io(&p.v[e]);
+  }
+  __device__ __forceinline__ void silu() {  // v / (1 + e^-v)
+#pragma unroll
+    for (int e = 0; e < kN; ++e) v[e] = mul_(v[e], one_plus_inverse(mul_(v[e], both<V>(-kLog2e))));
+  }
+  // times the slope g (1 + p (1 - g)), g = 1 / (1 + e^-p)
+  __device__ __forceinline__ void times_silu_grad(const Chans& p) {
+#pragma unroll
+    for (int e = 0; e < kN; ++e) {
+      const V g = one_plus_inverse(mul_(p.v[e], both<V>(-kLog2e)));
+      const V rest = fma_(g, both<V>(-1.f), both<V>(1.f));
+      v[e] = mul_(v[e], mul_(g, fma_(p.v[e], rest, both<V>(1.f))));
+    }
+  }
+  template <typename IO>
+  __device__ __forceinline__ void store(void* base, long long at) {
+    float f[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) f[e] = flat()[e];
+    store_vec<IO, VEC>(base, at, f);
+  }
+};
 template <int W, int VEC>
 struct Taps {
-  float w[W][VEC], b[VEC];
+  Chans<VEC> w[W], b;
   __device__ __forceinline__ void load(const ConvArgs& a, int c) {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
 #pragma unroll
-      for (int j = 0; j < W; ++j) w[j][e] = weight_of(a.w, a.w_bf16, (size_t)(c + e) * W + j);
-      b[e] = a.b ? weight_of(a.b, a.w_bf16, c + e) : 0.f;
+      for (int j = 0; j < W; ++j) w[j].flat()[e] = weight_of(a.w, a.w_bf16, (size_t)(c + e) * W + j);
+      b.flat()[e] = a.b ? weight_of(a.b, a.w_bf16, c + e) : 0.f;
     }
   }
+  // bias + sum over the taps of the inputs before (oldest first) and x
+  __device__ __forceinline__ Chans<VEC> sum(const Chans<VEC> (&in)[W - 1], const Chans<VEC>& x) const {
+    Chans<VEC> p;
+#pragma unroll
+    for (int e = 0; e < Chans<VEC>::kN; ++e) {
+      p.v[e] = fma_(w[W - 1].v[e], x.v[e], b.v[e]);
+#pragma unroll
+      for (int k = W - 2; k >= 0; --k) p.v[e] = fma_(w[k].v[e], in[k].v[e], p.v[e]);
+    }
+    return p;
+  }
 };
+
+// Row i of the inputs before a sequence's token m: i = 0 is W - 1 tokens back.
+template <typename IO, int W, int VEC>
+__device__ __forceinline__ Chans<VEC> input_before(const ConvArgs& a, const Seq& s, long long m, int i, int c) {
+  const long long t = m - (W - 1) + i;
+  Chans<VEC> f;
+  if (t >= s.begin) {
+    f.from(load_row<IO, VEC>(a.x, t, a.ldx, c));
+  } else if (a.h0) {
+    const long long r = t - s.begin + W - 1;
+    f.from(load_row<IO, VEC>(a.h0, (long long)s.n * (W - 1) + (r < 0 ? 0 : r), a.D, c));
+  } else {
+    f.fill(0.f);
+  }
+  return f;
+}
 
 // ------------------------------------------------------------------ forward
 // The final state of every sequence: its last W - 1 inputs, older ones from h0.
@@ -139,14 +197,93 @@ __device__ void final_states(const ConvArgs& a) {
     s.begin = a.cu ? offset_of(a, s.n) : (long long)s.n * a.T;
     s.end = a.cu ? offset_of(a, s.n + 1) : s.begin + a.T;
     if (s.end < s.begin) s.end = s.begin;
-    float f[VEC];
-    input_before<IO, W, VEC>(a, s, s.end, r, c, f);
-    store_vec<IO, VEC>(a.hT, ((long long)s.n * (W - 1) + r) * a.D + c, f);
+    input_before<IO, W, VEC>(a, s, s.end, r, c).template store<IO>(a.hT, ((long long)s.n * (W - 1) + r) * a.D + c);
   }
 }
 
+// The tokens of a run, kAhead to a group, two groups ahead in shared memory: a thread
+// copies with cp.async what it reads itself, so the ring needs no barrier and the loads in
+// flight no registers.  Single bf16 channels (two bytes) come through registers, a group
+// of twice as many at a time.
+template <typename IO, int VEC, int TENSORS>
+struct TokenRing {
+  using P = Pack<IO, VEC>;
+  static constexpr bool kAsync = sizeof(P) >= 4;
+  static constexpr int kStages = 3, kGroup = kAsync ? kAhead : 2 * kAhead;
+  static constexpr size_t kSmem = kAsync ? (size_t)kStages * kGroup * TENSORS * kBlock * sizeof(P) : 0;
+  P* base;
+  int total;
+  const IO* next[TENSORS];
+  long long ld[TENSORS];
+  P own[kAsync ? 1 : kGroup][TENSORS];
+  __device__ __forceinline__ TokenRing(char* sm, int tokens)
+      : base(reinterpret_cast<P*>(sm) + threadIdx.x), total(tokens) {}
+  __device__ __forceinline__ void from(int t, const IO* p, long long apart) {
+    next[t] = p;
+    ld[t] = apart;
+  }
+  __device__ __forceinline__ P& at(P* stage, int u, int t) {
+    if constexpr (kAsync)
+      return stage[(u * TENSORS + t) * kBlock];
+    else
+      return own[u][t];
+  }
+  __device__ __forceinline__ P* stage(int i) const { return base + i * (kGroup * TENSORS * kBlock); }
+  __device__ __forceinline__ void one(P* stage, int u) {
+#pragma unroll
+    for (int t = 0; t < TENSORS; ++t) {
+      if constexpr (kAsync)
+        copy_async<sizeof(P)>(&at(stage, u, t), next[t]);
+      else
+        own[u][t] = *reinterpret_cast<const P*>(next[t]);
+      next[t] += ld[t];
+    }
+  }
+  __device__ __forceinline__ void fetch(P* stage, int first) {
+    if (first + kGroup <= total) {
+#pragma unroll
+      for (int u = 0; u < kGroup; ++u) one(stage, u);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kGroup; ++u)
+        if (first + u < total) one(stage, u);
+    }
+    if (kAsync) copy_commit();
+  }
+  // work(stage, u, t, plain) for every token t, in order; `plain` where the whole group is
+  // below `to` and not below `from`
+  template <typename F>
+  __device__ __forceinline__ void each(int from, int to, F work) {
+    if (kAsync) {
+      fetch(stage(0), 0);
+      fetch(stage(1), kGroup);
+    }
+    int i = 0;
+    for (int g = 0; g < total; g += kGroup) {
+      P* const at = stage(i);
+      if (kAsync) {
+        fetch(stage(i == 0 ? 2 : i - 1), g + 2 * kGroup);
+        copy_wait<2>();
+      } else {
+        fetch(at, g);
+      }
+      if (g >= from && g + kGroup <= to) {
+#pragma unroll
+        for (int u = 0; u < kGroup; ++u) work(at, u, g + u, true);
+      } else {
+#pragma unroll
+        for (int u = 0; u < kGroup; ++u)
+          if (g + u < total) work(at, u, g + u, false);
+      }
+      i = i == 2 ? 0 : i + 1;
+    }
+  }
+};
+
 template <typename IO, int W, int VEC>
 __global__ void __launch_bounds__(kBlock) conv_fwd_kernel(ConvArgs a) {
+  extern __shared__ __align__(16) char sm[];
+  using Ring = TokenRing<IO, VEC, 1>;
   if (blockIdx.x >= a.main_blocks) {
     final_states<IO, W, VEC>(a);
     return;
@@ -162,39 +299,30 @@ __global__ void __launch_bounds__(kBlock) conv_fwd_kernel(ConvArgs a) {
   if (c >= a.D || m >= stop) return;
   Taps<W, VEC> taps;
   taps.load(a, c);
-  Seq s = seq_at(a, m);
-  if (m < s.begin) m = s.begin;
-  float in[W - 1][VEC];  // the inputs before token m, oldest first
+  while (m < stop) {  // the run's part of one sequence after another
+    const Seq s = seq_at(a, m);
+    if (m < s.begin) m = s.begin;
+    const long long own = s.end < stop ? s.end : stop;
+    const int n = (int)(own - m);
+    Chans<VEC> in[W - 1];  // the inputs before the next token, oldest first
 #pragma unroll
-  for (int i = 0; i < W - 1; ++i) input_before<IO, W, VEC>(a, s, m, i, c, in[i]);
-  while (m < stop) {
-    Pack<IO, VEC> next[kAhead];
+    for (int i = 0; i < W - 1; ++i) in[i] = input_before<IO, W, VEC>(a, s, m, i, c);
+    Ring ring(sm, n);
+    ring.from(0, static_cast<const IO*>(a.x) + m * a.ldx + c, a.ldx);
+    IO* py = static_cast<IO*>(a.y) + m * a.D + c;
+    const auto token = [&](typename Ring::P* stage, int u, int, bool) {
+      Chans<VEC> x;
+      x.from(ring.at(stage, u, 0));
+      Chans<VEC> p = taps.sum(in, x);
+      if (a.silu) p.silu();
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      if (m + i < stop) next[i] = load_row<IO, VEC>(a.x, m + i, a.ldx, c);
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      if (m + i >= stop) break;
-      if (m + i >= s.end) {  // the next sequence that has tokens
-        s = seq_at(a, m + i);
-#pragma unroll
-        for (int k = 0; k < W - 1; ++k) input_before<IO, W, VEC>(a, s, m + i, k, c, in[k]);
-      }
-      float x[VEC], p[VEC];
-      unpack<IO, VEC>(next[i], x);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        p[e] = fmaf(taps.w[W - 1][e], x[e], taps.b[e]);
-#pragma unroll
-        for (int k = W - 2; k >= 0; --k) p[e] = fmaf(taps.w[k][e], in[k][e], p[e]);
-        if (a.silu) p[e] = silu(p[e]);
-#pragma unroll
-        for (int k = 0; k < W - 2; ++k) in[k][e] = in[k + 1][e];
-        in[W - 2][e] = x[e];
-      }
-      store_vec<IO, VEC>(a.y, (m + i) * a.D + c, p);
-    }
-    m += kAhead;
+      for (int k = 0; k < W - 2; ++k) in[k] = in[k + 1];
+      in[W - 2] = x;
+      p.template store<IO>(py, 0);
+      py += a.D;
+    };
+    ring.each(0, n, token);
+    m = own > m ? own : stop;
   }
 }
 
@@ -221,21 +349,20 @@ __device__ void initial_grads(const ConvArgs& a) {
       if (t >= length) continue;
       dp[t] = ld_io(static_cast<const IO*>(a.dy) + (s.begin + t) * a.D + c);
       if (!a.silu) continue;
-      float p = fmaf(taps.w[W - 1][0], ld_io(static_cast<const IO*>(a.x) + (s.begin + t) * a.ldx + c),
-                     taps.b[0]);
+      Chans<1> in[W - 1], x;
+      x.v[0] = ld_io(static_cast<const IO*>(a.x) + (s.begin + t) * a.ldx + c);
 #pragma unroll
-      for (int k = 0; k < W - 1; ++k) {
-        float f[1];
-        input_before<IO, W, 1>(a, s, s.begin + t, k, c, f);
-        p = fmaf(taps.w[k][0], f[0], p);
-      }
-      dp[t] *= silu_grad(p);
+      for (int k = 0; k < W - 1; ++k) in[k] = input_before<IO, W, 1>(a, s, s.begin + t, k, c);
+      Chans<1> g;
+      g.v[0] = dp[t];
+      g.times_silu_grad(taps.sum(in, x));
+      dp[t] = g.v[0];
     }
 #pragma unroll
     for (int r = 0; r < W - 1; ++r) {
       float g = 0.f;
 #pragma unroll
-      for (int t = 0; t <= r; ++t) g = fmaf(taps.w[r - t][0], dp[t], g);
+      for (int t = 0; t <= r; ++t) g = fmaf(taps.w[r - t].v[0], dp[t], g);
       if (a.dhT && r >= length)
         g += ld_io(static_cast<const IO*>(a.dhT) + ((long long)s.n * (W - 1) + r - length) * a.D + c);
       st_io(static_cast<IO*>(a.hT) + ((long long)s.n * (W - 1) + r) * a.D + c, g);
@@ -244,7 +371,9 @@ __device__ void initial_grads(const ConvArgs& a) {
 }
 
 template <typename IO, int W, int VEC>
-__global__ void __launch_bounds__(kBlock) conv_bwd_kernel(ConvArgs a) {
+__global__ void __launch_bounds__(kBlock, 2) conv_bwd_kernel(ConvArgs a) {
+  extern __shared__ __align__(16) char sm[];
+  using Ring = TokenRing<IO, VEC, 2>;
   if (blockIdx.x >= a.main_blocks) {
     initial_grads<IO, W>(a);
     return;
@@ -256,90 +385,79 @@ __global__ void __launch_bounds__(kBlock) conv_bwd_kernel(ConvArgs a) {
   const long long last = a.cu ? offset_of(a, a.seqs) : a.tokens;
   long long m = (tok * groups + grp) * a.run;
   long long stop = m + a.run < last ? m + a.run : last;
-  float dw[W][VEC], db[VEC];
+  using V = typename Chans<VEC>::V;
+  constexpr int kN = Chans<VEC>::kN;
+  Chans<VEC> dw[W], db;
+  db.fill(0.f);
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) {
-    db[e] = 0.f;
-#pragma unroll
-    for (int j = 0; j < W; ++j) dw[j][e] = 0.f;
-  }
+  for (int j = 0; j < W; ++j) dw[j].fill(0.f);
   if (c < a.D && m < stop) {
     Taps<W, VEC> taps;
     taps.load(a, c);
     while (m < stop) {  // the run's part of one sequence after another
       const Seq s = seq_at(a, m);
       if (m < s.begin) m = s.begin;
-      const long long own = s.end < stop ? s.end : stop;          // tokens of this run
-      const long long seen = s.end < own + W - 1 ? s.end : own + W - 1;  // that its inputs reach
-      float in[W - 1][VEC], dp[W][VEC];  // dp[k]: of token t - (W - 1) + k
+      const long long own = s.end < stop ? s.end : stop;  // tokens of this run, then W - 1 that its inputs reach
+      const int n = (int)(own - m), seen = (int)((s.end < own + W - 1 ? s.end : own + W - 1) - m);
+      const int kept = (int)(s.end - (W - 1) - m);  // the first input that the final state holds
+      Chans<VEC> in[W - 1], dp[W];                  // dp[k]: of token t - (W - 1) + k
 #pragma unroll
-      for (int k = 0; k < W - 1; ++k) input_before<IO, W, VEC>(a, s, m, k, c, in[k]);
+      for (int k = 0; k < W - 1; ++k) in[k] = input_before<IO, W, VEC>(a, s, m, k, c);
 #pragma unroll
-      for (int k = 0; k < W; ++k)
+      for (int k = 0; k < W; ++k) dp[k].fill(0.f);
+      Ring ring(sm, seen);
+      ring.from(0, static_cast<const IO*>(a.x) + m * a.ldx + c, a.ldx);
+      ring.from(1, static_cast<const IO*>(a.dy) + m * a.D + c, a.D);
+      IO* out = static_cast<IO*>(a.y) + m * a.D + c;
+      const auto meet = [&](typename Ring::P* stage, int u, int t, bool plain) {  // token t
+        Chans<VEC> x, g;
+        x.from(ring.at(stage, u, 0));
+        g.from(ring.at(stage, u, 1));
+        if (a.silu) g.times_silu_grad(taps.sum(in, x));
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) dp[k][e] = 0.f;
-      constexpr int kN = kAhead / 2;
-      for (long long t0 = m; t0 < own + W - 1; t0 += kN) {
-        Pack<IO, VEC> xs[kN], gs[kN];
+        for (int k = 0; k < W - 1; ++k) dp[k] = dp[k + 1];
+        dp[W - 1] = g;
+        if (plain || t < n) {
 #pragma unroll
-        for (int i = 0; i < kN; ++i)
-          if (t0 + i < seen) {
-            xs[i] = load_row<IO, VEC>(a.x, t0 + i, a.ldx, c);
-            gs[i] = load_row<IO, VEC>(a.dy, t0 + i, a.D, c);
+          for (int e = 0; e < kN; ++e) {
+            db.v[e] = add_(db.v[e], g.v[e]);
+            dw[W - 1].v[e] = fma_(g.v[e], x.v[e], dw[W - 1].v[e]);
+#pragma unroll
+            for (int k = 0; k < W - 1; ++k) dw[k].v[e] = fma_(g.v[e], in[k].v[e], dw[k].v[e]);
           }
-#pragma unroll
-        for (int i = 0; i < kN; ++i) {
-          const long long t = t0 + i;
-#pragma unroll
-          for (int k = 0; k < W - 1; ++k)
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) dp[k][e] = dp[k + 1][e];
-          if (t < seen) {
-            float x[VEC], g[VEC];
-            unpack<IO, VEC>(xs[i], x);
-            unpack<IO, VEC>(gs[i], g);
-            const bool mine = t < own;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-              if (a.silu) {
-                float p = fmaf(taps.w[W - 1][e], x[e], taps.b[e]);
-#pragma unroll
-                for (int k = W - 2; k >= 0; --k) p = fmaf(taps.w[k][e], in[k][e], p);
-                g[e] *= silu_grad(p);
-              }
-              dp[W - 1][e] = g[e];
-              if (mine) {
-                db[e] += g[e];
-                dw[W - 1][e] = fmaf(g[e], x[e], dw[W - 1][e]);
-#pragma unroll
-                for (int k = 0; k < W - 1; ++k) dw[k][e] = fmaf(g[e], in[k][e], dw[k][e]);
-              }
-#pragma unroll
-              for (int k = 0; k < W - 2; ++k) in[k][e] = in[k + 1][e];
-              in[W - 2][e] = x[e];
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) dp[W - 1][e] = 0.f;
-          }
-          const long long out = t - (W - 1);  // the input that has met all its tokens
-          if (out < m || out >= own) continue;
-          float dx[VEC];
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            dx[e] = taps.w[W - 1][e] * dp[0][e];
-#pragma unroll
-            for (int k = 1; k < W; ++k) dx[e] = fmaf(taps.w[W - 1 - k][e], dp[k][e], dx[e]);
-          }
-          const long long row = out - (s.end - (W - 1));
-          if (a.dhT && row >= 0) {
-            float f[VEC];
-            unpack<IO, VEC>(load_row<IO, VEC>(a.dhT, (long long)s.n * (W - 1) + row, a.D, c), f);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) dx[e] += f[e];
-          }
-          store_vec<IO, VEC>(a.y, out * a.D + c, dx);
         }
+#pragma unroll
+        for (int k = 0; k < W - 2; ++k) in[k] = in[k + 1];
+        in[W - 2] = x;
+      };
+      const auto emit = [&](int o, bool plain) {  // input o, which has met all its tokens
+        if (!plain && (o < 0 || o >= n)) return;
+        Chans<VEC> dx;
+#pragma unroll
+        for (int e = 0; e < kN; ++e) {
+          V sum = mul_(taps.w[W - 1].v[e], dp[0].v[e]);
+#pragma unroll
+          for (int k = 1; k < W; ++k) sum = fma_(taps.w[W - 1 - k].v[e], dp[k].v[e], sum);
+          dx.v[e] = sum;
+        }
+        if (!plain && o >= kept && a.dhT) {
+          Chans<VEC> f;
+          f.from(load_row<IO, VEC>(a.dhT, (long long)s.n * (W - 1) + o - kept, a.D, c));
+#pragma unroll
+          for (int e = 0; e < kN; ++e) dx.v[e] = add_(dx.v[e], f.v[e]);
+        }
+        dx.template store<IO>(out, 0);
+        out += a.D;
+      };
+      ring.each(W - 1, n < kept ? n : kept, [&](typename Ring::P* stage, int u, int t, bool plain) {
+        meet(stage, u, t, plain);
+        emit(t - (W - 1), plain);
+      });
+      for (int t = seen; t < n + W - 1; ++t) {  // the sequence ended
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) dp[k] = dp[k + 1];
+        dp[W - 1].fill(0.f);
+        emit(t - (W - 1), false);
       }
       m = own > m ? own : stop;
     }
@@ -350,7 +468,7 @@ __global__ void __launch_bounds__(kBlock) conv_bwd_kernel(ConvArgs a) {
   for (int j = 0; j <= W; ++j) {
     __syncthreads();
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) sum[threadIdx.x][e] = j < W ? dw[j < W ? j : 0][e] : db[e];
+    for (int e = 0; e < VEC; ++e) sum[threadIdx.x][e] = j < W ? dw[j < W ? j : 0].flat()[e] : db.flat()[e];
     __syncthreads();
     for (int i = threadIdx.x; i < a.lanes * VEC; i += kBlock) {
       const int at = chan * a.lanes * VEC + i;
@@ -407,10 +525,10 @@ __global__ void __launch_bounds__(kBlock) conv_step_kernel(ConvArgs a) {
   float p[VEC];
 #pragma unroll
   for (int e = 0; e < VEC; ++e) {
-    p[e] = taps.b[e];
+    p[e] = taps.b.flat()[e];
 #pragma unroll
-    for (int k = W - 1; k >= 0; --k) p[e] = fmaf(taps.w[k][e], ld_io(&in[k].v[e]), p[e]);
-    if (a.silu) p[e] = silu(p[e]);
+    for (int k = W - 1; k >= 0; --k) p[e] = fmaf(taps.w[k].flat()[e], ld_io(&in[k].v[e]), p[e]);
+    if (a.silu) p[e] *= one_plus_inverse(-kLog2e * p[e]);
   }
   store_vec<IO, VEC>(a.y, row * a.D + c, p);
 #pragma unroll
@@ -440,10 +558,15 @@ inline int run_of(long long tokens, int D, int vec) {
     run /= 2;
   return run;
 }
-constexpr int kBwdVec = 4;
 inline long long token_blocks(long long tokens, int D, int vec) {
   const long long per = (long long)run_of(tokens, D, vec) * (kBlock / lanes_of((D + vec - 1) / vec));
   return (tokens + per - 1) / per;
+}
+
+template <typename F>
+cudaError_t allow_smem(F kernel, size_t smem) {
+  if (smem <= 32 * 1024) return cudaSuccess;  // (the static part counts towards the default 48 KB)
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
 }
 
 template <int VEC>
@@ -461,16 +584,22 @@ cudaError_t run_fwd(ConvArgs a, cudaStream_t s) {
   const long long more =
       a.hT ? blocks_for(((long long)a.seqs * (W - 1) * (a.D / VEC) + kBlock - 1) / kBlock, 2) : 0;
   if (a.main_blocks + more == 0) return cudaSuccess;
-  conv_fwd_kernel<IO, W, VEC><<<(unsigned)(a.main_blocks + more), kBlock, 0, s>>>(a);
+  constexpr size_t smem = TokenRing<IO, VEC, 1>::kSmem;
+  const cudaError_t e = allow_smem(conv_fwd_kernel<IO, W, VEC>, smem);
+  if (e != cudaSuccess) return e;
+  conv_fwd_kernel<IO, W, VEC><<<(unsigned)(a.main_blocks + more), kBlock, smem, s>>>(a);
   return cudaGetLastError();
 }
 template <typename IO, int W, int VEC>
 cudaError_t run_bwd(ConvArgs a, cudaStream_t s) {
   plan<VEC>(a);
   const long long more = a.hT ? blocks_for(((long long)a.seqs * a.D + kBlock - 1) / kBlock, 2) : 0;
+  constexpr size_t smem = TokenRing<IO, VEC, 2>::kSmem;
+  cudaError_t e = allow_smem(conv_bwd_kernel<IO, W, VEC>, smem);
+  if (e != cudaSuccess) return e;
   if (a.main_blocks + more > 0)
-    conv_bwd_kernel<IO, W, VEC><<<(unsigned)(a.main_blocks + more), kBlock, 0, s>>>(a);
-  const cudaError_t e = cudaGetLastError();
+    conv_bwd_kernel<IO, W, VEC><<<(unsigned)(a.main_blocks + more), kBlock, smem, s>>>(a);
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_next(a.main_blocks + more > 0, conv_weight_grad_kernel<W>, dim3((a.D + 31) / 32, W + 1),
                      1024, 0, s, a);
@@ -486,15 +615,15 @@ enum class Call { kFwd, kBwd, kStep };
 
 template <typename IO, int W>
 cudaError_t launch_taps(const ConvArgs& a, Call call, cudaStream_t s) {
-  constexpr int kVec = 16 / sizeof(IO);
+  constexpr int kWide = 16 / sizeof(IO);
   const auto fits = [&](int vec) {
     const size_t bytes = vec * sizeof(IO);
     return a.D % vec == 0 && a.ldx % vec == 0 && aligned(a.x, bytes) && aligned(a.dy, bytes) &&
            aligned(a.h0, bytes) && aligned(a.dhT, bytes) && aligned(a.y, bytes) && aligned(a.hT, bytes);
   };
   if (call == Call::kFwd) return fits(kVec) ? run_fwd<IO, W, kVec>(a, s) : run_fwd<IO, W, 1>(a, s);
-  if (call == Call::kBwd) return fits(kBwdVec) ? run_bwd<IO, W, kBwdVec>(a, s) : run_bwd<IO, W, 1>(a, s);
-  return fits(kVec) ? run_step<IO, W, kVec>(a, s) : run_step<IO, W, 1>(a, s);
+  if (call == Call::kBwd) return fits(kVec) ? run_bwd<IO, W, kVec>(a, s) : run_bwd<IO, W, 1>(a, s);
+  return fits(kWide) ? run_step<IO, W, kWide>(a, s) : run_step<IO, W, 1>(a, s);
 }
 template <typename IO>
 cudaError_t launch_io(const ConvArgs& a, int W, Call call, cudaStream_t s) {
@@ -560,8 +689,8 @@ ckda_status ckda_conv_fwd(const void* x, const void* weight, const void* bias, c
 size_t ckda_conv_bwd_workspace_bytes(int B, int T, int D, int W) {
   if (B < 1 || T < 0 || D < 1 || W < 2 || W > 4) return 0;
   const long long tokens = (long long)B * T;
-  const long long parts = D % kBwdVec == 0 && token_blocks(tokens, D, kBwdVec) > token_blocks(tokens, D, 1)
-                              ? token_blocks(tokens, D, kBwdVec)
+  const long long parts = D % kVec == 0 && token_blocks(tokens, D, kVec) > token_blocks(tokens, D, 1)
+                              ? token_blocks(tokens, D, kVec)
                               : token_blocks(tokens, D, 1);
   return ((size_t)parts * (W + 1) * D + 4) * sizeof(float);
 }

@@ -49,26 +49,6 @@ struct BwdArgs {
   int chunks;        // of a row
 };
 
-// Sums over LANES lanes, STRIDE apart, of NV values: lane i of them gets the sums of
-// values i r to i r + r - 1 in v[0] to v[r - 1], r = NV / LANES; with more lanes than
-// values, lane i that of value i % NV.
-template <int NV, int LANES, int STRIDE>
-__device__ __forceinline__ void fold_values(float (&v)[NV], int i) {
-  constexpr int kBoth = NV < LANES ? NV : LANES;
-#pragma unroll
-  for (int b = kBoth / 2; b >= 1; b /= 2) {
-    const int s = b * (NV / kBoth);
-    const bool up = (i & b) != 0;
-#pragma unroll
-    for (int j = 0; j < s; ++j) {
-      const float send = up ? v[j] : v[j + s], keep = up ? v[j + s] : v[j];
-      v[j] = keep + __shfl_xor_sync(0xffffffffu, send, b * STRIDE);
-    }
-  }
-#pragma unroll
-  for (int b = kBoth; b < LANES; b *= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], b * STRIDE);
-}
-
 __device__ __forceinline__ float silu_slope(float z, float g) { return g * fmaf(z, 1.f - g, 1.f); }
 
 // -------------------------------------------------- first pass: states and sums
