@@ -9,28 +9,26 @@
 //     dx = delta <g, B> + D dy',   ddelta = <q, A> + <g, B> x,   dz = dy (<C, h> + D x) silu'(z)
 //     ddt = ddelta sigmoid(dt + dt_bias) with the softplus, else ddelta
 //
-// h cannot be run backward (it would be divided by decays), so a first pass walks the
-// tokens forward and leaves the state before every 8th one in the workspace; the second
-// takes the 8-token chunks in reverse: runs a chunk forward from its state, h and a kept
-// in registers, then backward.  That is two exponentials a state for the whole call.
-// Rows with few channels are cut into pieces: the first pass then also leaves what each
+// h cannot be run backward (it would be divided by decays), so a first walk forward leaves
+// the state before every 4th token in the workspace; the second pass takes these chunks in
+// reverse: it runs forward from a chunk's state, the states before its tokens kept in
+// registers, then backward over them.  (Chunks of 8 tokens halve the workspace and run
+// half of each forward twice, which cost more than the memory's traffic.)
+// Rows with few channels are cut into pieces: the first walk then also leaves what each
 // piece adds to the gradient that passes it, and a scan joins both directions.
 //
-// <.,.> are sums over the LP lanes of a channel, dB and dC over the other lanes of the
-// warp, then over the block's warps in shared memory; the blocks' parts go through the
-// workspace and are added in a fixed order, as are dA's, dD's and ddt_bias's.
+// A lane has a channel, as in the forward pass; up to 16 states at a time are spread over
+// LP lanes, more in turns (slices).  <.,.> go to their own lane by shuffles; dB and dC are
+// sums over a lane's channels, then over the other lanes of the warp; a warp's parts go
+// through the workspace and are added in a fixed order, as are dA's, dD's and ddt_bias's.
 #include "ckda_scan.cuh"
 
 namespace ckda {
 namespace {
 
-constexpr int kChunk = 8;
-constexpr int kWarps = kScanBlock / 32;
 
 struct BwdArgs {
   ScanArgs a;
-  const void* dy;
-  const float* dhT;
   void* dx;
   void* ddt;
   void* dz;
@@ -40,148 +38,10 @@ struct BwdArgs {
   float* dskip;
   float* dbias;
   float* dh0;
-  float* chunk;      // [rows][chunks][D][N]: states before chunks, from the piece's own start
-  float* chunk_sum;  // [rows][chunks][D]: steps from the piece's start to the chunk (pieces > 1)
-  float* grad;       // [rows][pieces][D][N]: what a piece adds to G, then the G that reaches its end
-  float* part_bc;    // [blocks of a group][rows][T][G][2][N]: dC, dB
-  float* part_a;     // [rows][pieces][D][N]
-  float* part_d;     // [rows][pieces][2][D]: dD, ddt_bias
-  int chunks;        // of a row
+  float* part_bc;  // [channel blocks of a group][rows][T][G][2][N]: dC, dB
+  float* part_a;   // [rows][pieces][D][N]
+  float* part_d;   // [rows][pieces][2][D]: dD, ddt_bias
 };
-
-__device__ __forceinline__ float silu_slope(float z, float g) { return g * fmaf(z, 1.f - g, 1.f); }
-
-// -------------------------------------------------- first pass: states and sums
-// GRADS: the pieces' sums of gradients too (more than one piece).
-template <typename IO, typename S, bool VEC, bool GRADS>
-__global__ void __launch_bounds__(kScanBlock) scan_states_kernel(BwdArgs b) {
-  constexpr int LP = S::kLanes, NS = S::kStates, K = S::K, NP = S::NP;
-  constexpr int kPairs = NS / 2;
-  const ScanArgs& a = b.a;
-  __shared__ __align__(16) float4 in[K][S::kRow];  // delta, u, dy'
-  __shared__ __align__(16) float sB[K * NP], sC[GRADS ? K * NP : 4];
-  __shared__ Marks<K> marks;
-  let_next_start();
-  const ScanPlace p = scan_place<S::CH>(a);
-  if (p.t0 >= p.t1) return;
-  const int tid = threadIdx.x, l = tid % LP, pos = tid / LP;
-  const int k1 = tid / S::V8, v1 = tid % S::V8;
-  float bias[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-    bias[e] = 8 * v1 + e < p.chans && a.dt_bias ? a.dt_bias[p.c0 + 8 * v1 + e] : 0.f;
-  const int c = S::chan_at(pos);
-  const bool have = c < p.chans;
-  const long long chan = p.c0 + (have ? c : 0);
-  float2 A2[kPairs], h[kPairs], G[kPairs], W[kPairs];  // W: product of decays from the piece's start
-  load_states<NS>(A2, a.A, chan, a.N, l * NS, have);
-#pragma unroll
-  for (int q = 0; q < kPairs; ++q) {
-    A2[q] = mul_(A2[q], both<float2>(kLog2e));
-    h[q] = G[q] = both<float2>(0.f);
-    W[q] = both<float2>(1.f);
-  }
-  float span = 0.f;
-  ScanSeq seq = scan_seq_at(a, p.row, p.t0);
-  bool first = seq.begin < p.t0;  // in the sequence that entered the piece
-  const long long unit = (long long)p.row * a.pieces + p.piece;
-
-  struct Raw {
-    Eight<IO> x, dt, dy, z;
-    GroupTile<IO, S> B, C;
-  } next;
-  const auto load = [&](int t) {
-    const int count = p.t1 - t;
-    const long long at = (long long)p.row * a.T + t;
-    if (k1 < K && k1 < count) {
-      const int cc = p.c0 + 8 * v1, n = p.chans - 8 * v1;
-      next.x.template load<VEC>(a.x, (at + k1) * a.ldx + cc, n);
-      next.dt.template load<VEC>(a.dt, (at + k1) * a.lddt + cc, n);
-      if (GRADS) {
-        next.dy.template load<VEC>(b.dy, (at + k1) * a.D + cc, n);
-        if (a.z) next.z.template load<VEC>(a.z, (at + k1) * a.ldz + cc, n);
-      }
-    }
-    next.B.template load<VEC>(a.B, a.ldb, at, count < K ? count : K, p.g, a.N);
-    if (GRADS) next.C.template load<VEC>(a.C, a.ldc, at, count < K ? count : K, p.g, a.N);
-  };
-  load(p.t0);
-  for (int t = p.t0; t < p.t1; t += K) {
-    const int count = p.t1 - t < K ? p.t1 - t : K;
-    if (k1 < K) {
-      float delta[8];
-      step_sizes(next.dt, bias, a.softplus, k1 < count, delta);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const bool ok = k1 < count && 8 * v1 + e < p.chans;
-        float dy = GRADS && ok ? next.dy.at(e) : 0.f;
-        if (GRADS && ok && a.z) dy *= scan_silu(next.z.at(e));
-        in[k1][e * S::V8 + v1] = make_float4(delta[e], ok ? delta[e] * next.x.at(e) : 0.f, dy, 0.f);
-      }
-    }
-    next.B.template leave<VEC>(sB, count, a.N);
-    if (GRADS) next.C.template leave<VEC>(sC, count, a.N);
-    const bool edges = t <= seq.begin || t + count >= seq.end;
-    if (edges) marks.fill(a, p.row, t, count);
-    __syncthreads();
-    if (t + K < p.t1) load(t + K);
-    const auto walk = [&](auto checked) {
-      constexpr bool kChecked = decltype(checked)::value;
-#pragma unroll 1
-      for (int k0 = 0; k0 < count; k0 += kChunk) {
-        const long long ck = (long long)p.row * b.chunks + (t + k0) / kChunk;
-        store_states<NS>(b.chunk, ck * a.D + chan, a.N, l * NS, have, h);
-        if (GRADS && l == 0 && have) b.chunk_sum[ck * a.D + chan] = span;
-        float part = 0.f;
-#pragma unroll
-        for (int i = 0; i < kChunk; ++i) {
-          const int k = k0 + i;
-          const int mark = kChecked ? marks.mark[k] : 0;
-          if (kChecked && (mark & 1)) {
-            first = false;
-            if (a.h0)
-              load_states<NS>(h, a.h0, (long long)marks.n[k] * a.D + chan, a.N, l * NS, have);
-            else
-#pragma unroll
-              for (int q = 0; q < kPairs; ++q) h[q] = both<float2>(0.f);
-          }
-          const float4 s = in[k][pos];
-          float2 Bk[kPairs], Ck[kPairs];
-          from_shared<NS>(Bk, sB + k * NP + l * NS);
-          if (GRADS) from_shared<NS>(Ck, sC + k * NP + l * NS);
-          part += s.x;
-#pragma unroll
-          for (int q = 0; q < kPairs; ++q) {
-            const float2 decay = ex2(mul_(both<float2>(s.x), A2[q]));
-            h[q] = fma_(decay, h[q], mul_(both<float2>(s.y), Bk[q]));
-            if (GRADS && first) {
-              W[q] = mul_(W[q], decay);
-              G[q] = fma_(W[q], mul_(both<float2>(s.z), Ck[q]), G[q]);
-            }
-          }
-          if (GRADS && kChecked && (mark & 2) && first && b.dhT) {
-            float2 last[kPairs];
-            load_states<NS>(last, b.dhT, (long long)marks.n[k] * a.D + chan, a.N, l * NS, have);
-#pragma unroll
-            for (int q = 0; q < kPairs; ++q) G[q] = fma_(W[q], last[q], G[q]);
-          }
-        }
-        span += part;
-      }
-    };
-    if (edges)
-      walk(std::true_type());
-    else
-      walk(std::false_type());
-    if (t + count >= seq.end && t + count < p.t1) seq = scan_seq_at(a, p.row, t + count);
-    __syncthreads();
-  }
-  if (GRADS) {
-    store_states<NS>(a.state, unit * a.D + chan, a.N, l * NS, have, h);
-    store_states<NS>(b.grad, unit * a.D + chan, a.N, l * NS, have, G);
-    if (l == 0 && have) a.span[unit * a.D + chan] = span;
-  }
-}
 
 // The gradient that reaches each piece's end, from what the pieces behind it add: a
 // thread a state, from the last piece to the first.
@@ -196,305 +56,383 @@ __global__ void __launch_bounds__(256) scan_join_grads_kernel(BwdArgs b) {
   const int d = (int)(i % per / a.N);
   const float rate = a.A[i % per];
   float g = 0.f;
-  for (int s = a.pieces - 1; s >= 0; --s) {
-    const int t0 = s * a.piece_len;
-    if (t0 >= last) continue;
-    const int t1 = t0 + a.piece_len < last ? t0 + a.piece_len : last;
-    const long long unit = (long long)row * a.pieces + s;
-    const float own = b.grad[unit * per + i % per];
-    b.grad[unit * per + i % per] = g;
-    if (scan_seq_at(a, row, t0).begin >= t0)
-      g = 0.f;
-    else
-      g = passes(a, row, t0, t1) ? fmaf(expf(rate * a.span[unit * a.D + d]), g, own) : own;
+  for (int s0 = a.pieces - 1; s0 >= 0; s0 -= 4) {
+    float own[4], sum[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (s0 - k >= 0 && (s0 - k) * a.piece_len < last) {
+        const long long unit = (long long)row * a.pieces + s0 - k;
+        own[k] = a.grad[unit * per + i % per];
+        sum[k] = a.span[unit * a.D + d];
+      }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (s0 - k < 0) return;
+      const int t0 = (s0 - k) * a.piece_len;
+      if (t0 >= last) continue;
+      const int t1 = t0 + a.piece_len < last ? t0 + a.piece_len : last;
+      a.grad[((long long)row * a.pieces + s0 - k) * per + i % per] = g;
+      if (scan_seq_at(a, row, t0).begin >= t0)
+        g = 0.f;
+      else
+        g = passes(a, row, t0, t1) ? fmaf(expf(rate * sum[k]), g, own[k]) : own[k];
+    }
   }
 }
 
 // ------------------------------------------------------ second pass: gradients
-template <typename IO, typename S>
+constexpr int kTile = 2 * kScanChunk;
+
+// Of a warp; behind it, per slice of 4 LP states, [LP][32] float4 each of A log2(e), of G
+// and of dA, each lane's own.
+template <typename IO, typename S, bool SLICES>
 struct GradSmem {
-  Eight<IO> raw[2][4][kScanBlock];       // x, dt, dy, z of a tile, each thread's own
-  float4 slot[S::K][S::kRow];            // delta, u, dy'; then delta, <g, B>, <C, h>, <q, A>
-  float B[S::K * S::NP], C[S::K * S::NP];
-  float red[kWarps][S::K][2 * S::NP];    // dC, dB of the warps' channels
-  float bias[S::CH], skip[S::CH];
-  Marks<S::K> marks;
+  alignas(16) ChanTile<IO, kTile> raw[2][4];  // x, dt, dy, z
+  float4 slot[kTile][kScanChans];             // delta, u, dy'; then delta, <g, B>, <C, h>, <q, A>
+  float sums[SLICES ? kTile : 1][3][kScanChans];  // the last three, over the slices so far
+  float4 state[2][S::kLanes][kScanChans];     // states before the two chunks, each lane's own
+  float before[2][kScanChans];                // steps before them
+};
+template <typename IO, int MOST>
+struct GradGroups {  // B and C of a tile, MOST states
+  GroupTile<IO, kTile, MOST> raw[2][2];
+  alignas(16) float f[2][kTile * MOST];
 };
 
-template <typename IO, typename S, bool VEC>
-__global__ void __launch_bounds__(kScanBlock) scan_grad_kernel(BwdArgs b) {
-  constexpr int LP = S::kLanes, NS = S::kStates, K = S::K, NP = S::NP;
-  constexpr int kPairs = NS / 2, kChanLanes = 32 / LP, kV = 16 / sizeof(IO);
-  static_assert(S::kChans == 1 && K % kChunk == 0, "a channel to a thread, whole chunks");
+// MOST: states, padded; in slices of S::NP.
+template <typename IO, typename S, int MOST, bool VEC>
+__global__ void __launch_bounds__(kScanBlock, 2) scan_grad_kernel(BwdArgs b) {
+  constexpr int LP = S::kLanes, NS = S::kStates, NP = S::NP, kPairs = NS / 2, kGroups = 32 / LP;
+  constexpr int kSlices = MOST / NP;
+  static_assert(NS == 4, "a lane's states of a channel are one vector");
+  using Smem = GradSmem<IO, S, (kSlices > 1)>;
+  struct Own {
+    Smem s;
+    GradGroups<IO, MOST> bc;
+    float4 A2[kSlices][LP][32], g[kSlices][LP][32], dA[kSlices][LP][32];
+  };
   extern __shared__ __align__(16) char sm[];
-  GradSmem<IO, S>& s = *reinterpret_cast<GradSmem<IO, S>*>(sm);
+  Own& w = reinterpret_cast<Own*>(sm)[threadIdx.x >> 5];
+  Smem& s = w.s;
   const ScanArgs& a = b.a;
   after_previous();
   let_next_start();
-  const ScanPlace p = scan_place<S::CH>(a);
-  const int tid = threadIdx.x, l = tid % LP, pos = tid / LP, warp = tid / 32, ci = tid % 32 / LP;
-  const int k1 = tid / S::V8, v1 = tid % S::V8;
+  ScanPlace p;
+  if (!scan_place(a, p)) return;
+  const int lane = threadIdx.x & 31, l = lane % LP, grp = lane / LP;
   const long long unit = (long long)p.row * a.pieces + p.piece;
-  const int c = S::chan_at(pos);
-  const bool have = c < p.chans;
-  const long long chan = p.c0 + (have ? c : 0);
-  if (p.piece == 0 && b.dh0 && (a.cu || a.T == 0)) empty_states<S::CH>(a, p, b.dhT, b.dh0);
-
-  float2 A2[kPairs], g[kPairs], dA[kPairs];
-  load_states<NS>(A2, a.A, chan, a.N, l * NS, have);
+  const bool own = lane < p.chans;
+  const int c = p.c0 + (own ? lane : 0);
+  const auto have = [&](int j) { return (lane ^ j) < p.chans; };
+  const auto chan = [&](int j) { return p.c0 + (have(j) ? lane ^ j : 0); };
+  const auto vec = [](const float2 (&f)[kPairs]) { return make_float4(f[0].x, f[0].y, f[1].x, f[1].y); };
+  const auto from_vec = [](float2 (&f)[kPairs], const float4& v) {
+    f[0] = make_float2(v.x, v.y);
+    f[1] = make_float2(v.z, v.w);
+  };
+  if (p.piece == 0 && b.dh0 && (a.cu || a.T == 0)) empty_states(a, p, a.dhT, b.dh0);
+  float dskip = 0.f, dbias = 0.f;
 #pragma unroll
-  for (int q = 0; q < kPairs; ++q) {
-    A2[q] = mul_(A2[q], both<float2>(kLog2e));
-    g[q] = dA[q] = both<float2>(0.f);
-  }
-  float dskip[8], dbias[8];
+  for (int sl = 0; sl < kSlices; ++sl)
 #pragma unroll
-  for (int e = 0; e < 8; ++e) dskip[e] = dbias[e] = 0.f;
+    for (int j = 0; j < LP; ++j) {
+      float2 f[kPairs], zero[kPairs] = {both<float2>(0.f), both<float2>(0.f)};
+      load_states<NS>(f, a.A, chan(j), a.N, sl * NP + l * NS, have(j));
+#pragma unroll
+      for (int q = 0; q < kPairs; ++q) f[q] = mul_(f[q], both<float2>(kLog2e));
+      w.A2[sl][j][lane] = vec(f);
+      w.g[sl][j][lane] = w.dA[sl][j][lane] = vec(zero);
+      if (a.pieces > 1 && p.t0 < p.t1) {
+        load_states<NS>(f, a.grad, unit * a.D + chan(j), a.N, sl * NP + l * NS, have(j));
+        w.g[sl][j][lane] = vec(f);
+      }
+      s.state[0][j][lane] = s.state[1][j][lane] = vec(zero);  // (lanes without a channel read what nothing writes)
+    }
 
   if (p.t0 < p.t1) {
-    for (int i = tid; i < S::CH; i += kScanBlock) {
-      s.bias[i] = i < p.chans && a.dt_bias ? a.dt_bias[p.c0 + i] : 0.f;
-      s.skip[i] = i < p.chans && a.skip ? a.skip[p.c0 + i] : 0.f;
-    }
-    __syncthreads();
-    if (a.pieces > 1) load_states<NS>(g, b.grad, unit * a.D + chan, a.N, l * NS, have);
-    const int tiles = (p.t1 - p.t0 + K - 1) / K;
-    const auto fetch = [&](int tile, int stage) {  // a thread's own vectors of a tile
-      const int t = p.t0 + tile * K;
-      if (k1 < K && t + k1 < p.t1) {
-        const long long at = (long long)p.row * a.T + t + k1;
-        const int cc = p.c0 + 8 * v1, n = p.chans - 8 * v1;
-        const auto one = [&](int which, const void* base, long long from) {
-          Eight<IO>& to = s.raw[stage][which][tid];
-          if (VEC) {
-            if (n > 0)
+    const float bias = a.dt_bias ? a.dt_bias[c] : 0.f, skip = a.skip ? a.skip[c] : 0.f;
+    const int tiles = (p.t1 - p.t0 + kTile - 1) / kTile;
+    const auto fetch = [&](int tile, int stage) {  // a tile's inputs
+      const int t = p.t0 + tile * kTile, count = p.t1 - t < kTile ? p.t1 - t : kTile;
+      const long long at = (long long)p.row * a.T + t;
+      s.raw[stage][0].template fetch<VEC>(a.x, a.ldx, at, p.c0, count, p.chans);
+      s.raw[stage][1].template fetch<VEC>(a.dt, a.lddt, at, p.c0, count, p.chans);
+      s.raw[stage][2].template fetch<VEC>(a.dy, a.D, at, p.c0, count, p.chans);
+      if (a.z) s.raw[stage][3].template fetch<VEC>(a.z, a.ldz, at, p.c0, count, p.chans);
+      w.bc.raw[stage][0].template fetch<VEC>(a.B, a.ldb, at, count, p.g, a.N);
+      w.bc.raw[stage][1].template fetch<VEC>(a.C, a.ldc, at, count, p.g, a.N);
+      copy_commit();
+    };
+    const auto fetch_states = [&](int tile, int sl) {  // the states before its chunks
 #pragma unroll
-              for (int j = 0; j < 8 / kV; ++j)
-                copy_async<16>(&to.v[j], static_cast<const IO*>(base) + from + j * kV);
+      for (int i = 0; i < 2; ++i) {
+        const int t = p.t0 + tile * kTile + i * kScanChunk;
+        if (t >= p.t1) break;
+        const long long ck = (long long)p.row * a.chunks + t / kScanChunk;
+#pragma unroll
+        for (int j = 0; j < LP; ++j) {
+          if (VEC) {
+            if (have(j) && sl * NP + l * NS < a.N)
+              copy_async<16>(&s.state[i][j][lane], a.chunk + (ck * a.D + chan(j)) * a.N + sl * NP + l * NS);
           } else {
-            to.template load<false>(base, from, n);
+            float2 f[kPairs];
+            load_states<NS>(f, a.chunk, ck * a.D + chan(j), a.N, sl * NP + l * NS, have(j));
+            s.state[i][j][lane] = vec(f);
           }
-        };
-        one(0, a.x, at * a.ldx + cc);
-        one(1, a.dt, at * a.lddt + cc);
-        one(2, b.dy, at * a.D + cc);
-        if (a.z) one(3, a.z, at * a.ldz + cc);
+        }
+        if (a.pieces > 1 && sl == 0) copy_async<4>(&s.before[i][lane], a.chunk_sum + ck * a.D + c);
       }
       copy_commit();
     };
-    GroupTile<IO, S> nextB, nextC;
-    const auto fetch_bc = [&](int tile) {
-      const int t = p.t0 + tile * K, count = p.t1 - t < K ? p.t1 - t : K;
-      const long long at = (long long)p.row * a.T + t;
-      nextB.template load<VEC>(a.B, a.ldb, at, count, p.g, a.N);
-      nextC.template load<VEC>(a.C, a.ldc, at, count, p.g, a.N);
-    };
     fetch(tiles - 1, 0);
-    fetch_bc(tiles - 1);
+    fetch_states(tiles - 1, 0);
     int stage = 0;
     for (int tile = tiles - 1; tile >= 0; --tile, stage ^= 1) {
-      const int t = p.t0 + tile * K, count = p.t1 - t < K ? p.t1 - t : K;
-      if (tile > 0)
-        fetch(tile - 1, stage ^ 1);
-      else
-        copy_commit();
-      copy_wait<1>();
-      // ---- 1
-      Eight<IO>* raw = &s.raw[stage][0][tid];  // raw[which * kScanBlock]
-      if (k1 < K) {
+      const int t = p.t0 + tile * kTile, count = p.t1 - t < kTile ? p.t1 - t : kTile;
+      copy_wait<0>();
+      __syncwarp();
+      const bool whole = count == kTile && p.chans == kScanChans;
+      // ---- the lane's own channel: steps, and dy through the gate
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const bool ok = k1 < count && 8 * v1 + e < p.chans;
-          float delta = 0.f, u = 0.f, dy = 0.f;
-          if (ok) {
-            const float r = raw[kScanBlock].at(e) + s.bias[8 * v1 + e];
-            delta = a.softplus ? softplus(r) : r;
-            u = delta * raw[0].at(e);
-            dy = raw[2 * kScanBlock].at(e);
-            if (a.z) dy *= scan_silu(raw[3 * kScanBlock].at(e));
-          }
-          s.slot[k1][e * S::V8 + v1] = make_float4(delta, u, dy, 0.f);
+      for (int k = 0; k < kTile; k += 2) {
+        float2 x = s.raw[stage][0].pair(k), up = s.raw[stage][2].pair(k);
+        float2 d = step_sizes(s.raw[stage][1].pair(k), both<float2>(bias), a.softplus);
+        if (a.z) up = mul_(up, scan_silu(s.raw[stage][3].pair(k)));
+        if (!whole) {  // (what there is not was not loaded)
+          const bool in0 = own && k < count, in1 = own && k + 1 < count;
+          d = make_float2(in0 ? d.x : 0.f, in1 ? d.y : 0.f);
+          x = make_float2(in0 ? x.x : 0.f, in1 ? x.y : 0.f);
+          up = make_float2(in0 ? up.x : 0.f, in1 ? up.y : 0.f);
         }
+        const float2 u = mul_(d, x);
+        s.slot[k][lane] = make_float4(d.x, u.x, up.x, 0.f);
+        s.slot[k + 1][lane] = make_float4(d.y, u.y, up.y, 0.f);
       }
-      nextB.template leave<VEC>(s.B, count, a.N);
-      nextC.template leave<VEC>(s.C, count, a.N);
+      w.bc.raw[stage][0].template unpack_to<VEC>(w.bc.f[0], count, a.N);
+      w.bc.raw[stage][1].template unpack_to<VEC>(w.bc.f[1], count, a.N);
       const ScanSeq seq = scan_seq_at(a, p.row, t);
       const bool edges = t <= seq.begin || t + count >= seq.end;
-      if (edges) s.marks.fill(a, p.row, t, count);
-      __syncthreads();
-      if (tile > 0) fetch_bc(tile - 1);
-      // ---- 2
-      float2 dA_tile[kPairs];
-#pragma unroll
-      for (int q = 0; q < kPairs; ++q) dA_tile[q] = both<float2>(0.f);
-      const auto walk = [&](auto checked) {
+      Marks marks;
+      if (edges) marks.find(a, p.row, t, count);
+      __syncwarp();
+      if (tile > 0) fetch(tile - 1, stage ^ 1);
+      float* const out_bc = b.part_bc + ((((long long)p.block * a.rows + p.row) * a.T + t) * a.G + p.g) * 2 * a.N;
+      const long long apart_bc = (long long)a.G * 2 * a.N;
+      // ---- a slice of the states
+      const auto walk = [&](auto checked, int sl) {
         constexpr bool kChecked = decltype(checked)::value;
+        const int n0 = sl * NP + l * NS;
+        float2 A2[LP][kPairs], g[LP][kPairs], dA[LP][kPairs], h[LP][kPairs];
+#pragma unroll
+        for (int j = 0; j < LP; ++j) {
+          from_vec(A2[j], w.A2[sl][j][lane]);
+          from_vec(g[j], w.g[sl][j][lane]);
+#pragma unroll
+          for (int q = 0; q < kPairs; ++q) dA[j][q] = both<float2>(0.f);
+        }
+        const auto reset = [&](int k) {  // a sequence starts at token k
+          const int num = marks.number(k);
+#pragma unroll
+          for (int j = 0; j < LP; ++j) {
+            if (a.h0)
+              load_states<NS>(h[j], a.h0, (long long)num * a.D + chan(j), a.N, n0, have(j));
+            else
+#pragma unroll
+              for (int q = 0; q < kPairs; ++q) h[j][q] = both<float2>(0.f);
+          }
+        };
 #pragma unroll 1
-        for (int k0 = (count - 1) / kChunk * kChunk; k0 >= 0; k0 -= kChunk) {
-          const long long ck = (long long)p.row * b.chunks + (t + k0) / kChunk;
-          float2 h[kPairs], old[kChunk][kPairs], decay[kChunk][kPairs];
-          load_states<NS>(h, b.chunk, ck * a.D + chan, a.N, l * NS, have);
+        for (int k0 = (count - 1) / kScanChunk * kScanChunk; k0 >= 0; k0 -= kScanChunk) {
+          const int ch = k0 / kScanChunk;
+#pragma unroll
+          for (int j = 0; j < LP; ++j) from_vec(h[j], s.state[ch][j][lane]);
           const int begin = kChecked ? scan_seq_at(a, p.row, t + k0).begin : seq.begin;
-          if (a.pieces > 1 && begin < p.t0) {  // what entered the piece reaches here
-            float2 enter[kPairs];
-            load_states<NS>(enter, a.state, unit * a.D + chan, a.N, l * NS, have);
-            const float span = have ? b.chunk_sum[ck * a.D + chan] : 0.f;
+          if (a.pieces > 1 && begin < p.t0) {  // what entered the piece reaches the chunk
 #pragma unroll
-            for (int q = 0; q < kPairs; ++q)
-              h[q] = fma_(ex2(mul_(both<float2>(span), A2[q])), enter[q], h[q]);
-          }
+            for (int j = 0; j < LP; ++j) {
+              float2 enter[kPairs];
+              load_states<NS>(enter, a.state, unit * a.D + chan(j), a.N, n0, have(j));
+              const float2 span = both<float2>(s.before[ch][lane ^ j]);
 #pragma unroll
-          for (int i = 0; i < kChunk; ++i) {
-            const int k = k0 + i;
-            if (kChecked && (s.marks.mark[k] & 1)) {
-              if (a.h0)
-                load_states<NS>(h, a.h0, (long long)s.marks.n[k] * a.D + chan, a.N, l * NS, have);
-              else
-#pragma unroll
-                for (int q = 0; q < kPairs; ++q) h[q] = both<float2>(0.f);
+              for (int q = 0; q < kPairs; ++q) h[j][q] = fma_(decay_of(span, A2[j][q]), enter[q], h[j][q]);
             }
-            const float2 step = *reinterpret_cast<const float2*>(&s.slot[k][pos]);
+          }
+          if (k0 == 0) {  // (the states are read: the next ones)
+            __syncwarp();
+            if (sl + 1 < kSlices)
+              fetch_states(tile, sl + 1);
+            else if (tile > 0)
+              fetch_states(tile - 1, 0);
+          }
+          float2 old[kScanChunk][LP][kPairs];
+#pragma unroll
+          for (int i = 0; i < kScanChunk; ++i) {
+            const int k = k0 + i;
+            if (kChecked && (marks.first >> k & 1)) reset(k);
             float2 Bk[kPairs];
-            from_shared<NS>(Bk, s.B + k * NP + l * NS);
+            from_shared<NS>(Bk, w.bc.f[0] + k * MOST + n0);
 #pragma unroll
-            for (int q = 0; q < kPairs; ++q) {
-              old[i][q] = h[q];
-              decay[i][q] = ex2(mul_(both<float2>(step.x), A2[q]));
-              h[q] = fma_(decay[i][q], h[q], mul_(both<float2>(step.y), Bk[q]));
+            for (int j = 0; j < LP; ++j) {
+              const float2 in = *reinterpret_cast<const float2*>(&s.slot[k][lane ^ j]);
+#pragma unroll
+              for (int q = 0; q < kPairs; ++q) {
+                old[i][j][q] = h[j][q];
+                h[j][q] = fma_(decay_of(both<float2>(in.x), A2[j][q]), h[j][q], mul_(both<float2>(in.y), Bk[q]));
+              }
             }
           }
-          float yC[kChunk], gB[kChunk], qA[kChunk];
+          float found[kScanChunk][3];  // <g, B>, <C, h>, <q, A> of the lane's own channel
 #pragma unroll
-          for (int i = kChunk - 1; i >= 0; --i) {
+          for (int i = kScanChunk - 1; i >= 0; --i) {
             const int k = k0 + i;
-            const int mark = kChecked ? s.marks.mark[k] : 0;
-            if (kChecked && (mark & 2)) {
-              if (b.dhT)
-                load_states<NS>(g, b.dhT, (long long)s.marks.n[k] * a.D + chan, a.N, l * NS, have);
-              else
+            const bool first = kChecked && (marks.first >> k & 1), last = kChecked && (marks.last >> k & 1);
+            const int num = kChecked && (first || last) ? marks.number(k) : 0;
+            if (last) {
 #pragma unroll
-                for (int q = 0; q < kPairs; ++q) g[q] = both<float2>(0.f);
+              for (int j = 0; j < LP; ++j) {
+                if (a.dhT)
+                  load_states<NS>(g[j], a.dhT, (long long)num * a.D + chan(j), a.N, n0, have(j));
+                else
+#pragma unroll
+                  for (int q = 0; q < kPairs; ++q) g[j][q] = both<float2>(0.f);
+              }
             }
-            const float4 in = s.slot[k][pos];
-            float2 Bk[kPairs], Ck[kPairs];
-            from_shared<NS>(Bk, s.B + k * NP + l * NS);
-            from_shared<NS>(Ck, s.C + k * NP + l * NS);
-            float sums[2 * NS];
-            float2 y = both<float2>(0.f), gb = y, qa = y;
+            float2 Bk[kPairs], Ck[kPairs], sumC[kPairs], sumB[kPairs];
+            from_shared<NS>(Bk, w.bc.f[0] + k * MOST + n0);
+            from_shared<NS>(Ck, w.bc.f[1] + k * MOST + n0);
 #pragma unroll
-            for (int q = 0; q < kPairs; ++q) {
-              // (a sequence's start between leaves its own initial state in old[i + 1])
-              const float2 now = kChecked ? fma_(decay[i][q], old[i][q], mul_(both<float2>(in.y), Bk[q]))
-                                 : i + 1 < kChunk ? old[i + 1 < kChunk ? i + 1 : i][q] : h[q];
-              const float2 dyv = both<float2>(in.z);
-              g[q] = fma_(dyv, Ck[q], g[q]);
-              y = fma_(Ck[q], now, y);
-              gb = fma_(g[q], Bk[q], gb);
-              const float2 dC = mul_(dyv, now), dB = mul_(g[q], both<float2>(in.y));
-              sums[2 * q] = dC.x;
-              sums[2 * q + 1] = dC.y;
-              sums[NS + 2 * q] = dB.x;
-              sums[NS + 2 * q + 1] = dB.y;
-              g[q] = mul_(g[q], decay[i][q]);
-              const float2 through = mul_(g[q], old[i][q]);
-              qa = fma_(through, A2[q], qa);
-              dA_tile[q] = fma_(through, both<float2>(in.x), dA_tile[q]);
+            for (int j = 0; j < LP; ++j) {
+              const float4 in = s.slot[k][lane ^ j];
+              const float2 delta = both<float2>(in.x), u = both<float2>(in.y), up = both<float2>(in.z);
+              float2 y, gb, qa;
+#pragma unroll
+              for (int q = 0; q < kPairs; ++q) {
+                const float2 decay = decay_of(delta, A2[j][q]);
+                // (a sequence's start between leaves its own initial state in old[i + 1])
+                const float2 now = kChecked ? fma_(decay, old[i][j][q], mul_(u, Bk[q]))
+                                   : i + 1 < kScanChunk ? old[i + 1 < kScanChunk ? i + 1 : i][j][q] : h[j][q];
+                g[j][q] = fma_(up, Ck[q], g[j][q]);
+                y = q == 0 ? mul_(Ck[q], now) : fma_(Ck[q], now, y);
+                gb = q == 0 ? mul_(g[j][q], Bk[q]) : fma_(g[j][q], Bk[q], gb);
+                sumC[q] = j == 0 ? mul_(up, now) : fma_(up, now, sumC[q]);
+                sumB[q] = j == 0 ? mul_(g[j][q], u) : fma_(g[j][q], u, sumB[q]);
+                g[j][q] = mul_(g[j][q], decay);
+                const float2 through = mul_(g[j][q], old[i][j][q]);
+                qa = q == 0 ? mul_(through, A2[j][q]) : fma_(through, A2[j][q], qa);
+                dA[j][q] = fma_(through, delta, dA[j][q]);
+              }
+              const float s0 = gb.x + gb.y, s1 = y.x + y.y, s2 = qa.x + qa.y;
+              found[i][0] = j ? found[i][0] + __shfl_xor_sync(0xffffffffu, s0, j) : s0;
+              found[i][1] = j ? found[i][1] + __shfl_xor_sync(0xffffffffu, s1, j) : s1;
+              found[i][2] = j ? found[i][2] + __shfl_xor_sync(0xffffffffu, s2, j) : s2;
+              if (first) {
+                if (b.dh0) store_states<NS>(b.dh0, (long long)num * a.D + chan(j), a.N, n0, have(j), g[j]);
+#pragma unroll
+                for (int q = 0; q < kPairs; ++q) g[j][q] = both<float2>(0.f);
+              }
             }
-            yC[i] = y.x + y.y;
-            gB[i] = gb.x + gb.y;
-            qA[i] = qa.x + qa.y;
-            if (kChecked && (mark & 1)) {
-              if (b.dh0)
-                store_states<NS>(b.dh0, (long long)s.marks.n[k] * a.D + chan, a.N, l * NS, have, g);
+            float sums[2 * NS] = {sumC[0].x, sumC[0].y, sumC[1].x, sumC[1].y,
+                                  sumB[0].x, sumB[0].y, sumB[1].x, sumB[1].y};
+            fold_values<2 * NS, kGroups, LP>(sums, grp);
+            constexpr int kSums = 2 * NS > kGroups ? 2 * NS / kGroups : 1;
+            if (grp * kSums < 2 * NS && k < count)
 #pragma unroll
-              for (int q = 0; q < kPairs; ++q) g[q] = both<float2>(0.f);
-            }
-            fold_values<2 * NS, kChanLanes, LP>(sums, ci);
-            constexpr int kEach = 2 * NS > kChanLanes ? 2 * NS / kChanLanes : 1;
-            if (ci * kEach < 2 * NS)
-#pragma unroll
-              for (int e = 0; e < kEach; ++e) {
-                const int at = ci * kEach + e;
-                s.red[warp][k][at / NS * NP + l * NS + at % NS] = sums[e];
+              for (int e = 0; e < kSums; ++e) {
+                const int at = grp * kSums + e, n = n0 + at % NS;
+                if (n < a.N) out_bc[k * apart_bc + at / NS * a.N + n] = sums[e];
               }
           }
-          fold_values<kChunk, LP, 1>(yC, l);
-          fold_values<kChunk, LP, 1>(gB, l);
-          fold_values<kChunk, LP, 1>(qA, l);
-          __syncwarp();  // the channel's lanes have read their slots
-          constexpr int kEach = kChunk > LP ? kChunk / LP : 1;
-          if (l * kEach < kChunk)
+          if (kSlices == 1) {
+            __syncwarp();  // the lanes have read these slots
 #pragma unroll
-            for (int e = 0; e < kEach; ++e) {
-              float4& to = s.slot[k0 + l * kEach + e][pos];
-              to.y = gB[e];
-              to.z = yC[e];
-              to.w = qA[e];
+            for (int i = 0; i < kScanChunk; ++i) {
+              float* to = &s.slot[k0 + i][lane].y;
+              to[0] = found[i][0];
+              to[1] = found[i][1];
+              to[2] = found[i][2];
             }
+          } else {
+#pragma unroll
+            for (int i = 0; i < kScanChunk; ++i)
+#pragma unroll
+              for (int f = 0; f < 3; ++f) {
+                float& to = s.sums[kSlices > 1 ? k0 + i : 0][f][lane];
+                to = sl == 0 ? found[i][f] : to + found[i][f];
+              }
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < LP; ++j) {
+          w.g[sl][j][lane] = vec(g[j]);
+          float4& to = w.dA[sl][j][lane];
+          to = make_float4(to.x + dA[j][0].x, to.y + dA[j][0].y, to.z + dA[j][1].x, to.w + dA[j][1].y);
         }
       };
-      if (edges)
-        walk(std::true_type());
-      else
-        walk(std::false_type());
+#pragma unroll 1
+      for (int sl = 0; sl < kSlices; ++sl) {
+        if (sl > 0) copy_wait<0>();
+        if (edges)
+          walk(std::true_type(), sl);
+        else
+          walk(std::false_type(), sl);
+      }
+      // ---- the lane's own channel: its gradients
+      const long long at = ((long long)p.row * a.T + t) * a.D + c;
 #pragma unroll
-      for (int q = 0; q < kPairs; ++q) dA[q] = add_(dA[q], dA_tile[q]);
-      __syncthreads();
-      // ---- 3
-      if (k1 < K && k1 < count) {
-        const long long at = ((long long)p.row * a.T + t + k1) * a.D + p.c0 + 8 * v1;
-        const int n = p.chans - 8 * v1;
-        float dx[8], ddt[8], dz[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          dx[e] = ddt[e] = dz[e] = 0.f;
-          if (e >= n) continue;
-          const float4 r = s.slot[k1][e * S::V8 + v1];
-          const float x = raw[0].at(e), dy = raw[2 * kScanBlock].at(e), skip = s.skip[8 * v1 + e];
-          float up = dy;
-          if (a.z) {
-            const float z = raw[3 * kScanBlock].at(e), gate = scan_sigmoid(z);
-            up = dy * (z * gate);
-            dz[e] = dy * fmaf(skip, x, r.z) * silu_slope(z, gate);
-          }
-          dx[e] = fmaf(r.x, r.y, skip * up);
-          ddt[e] = fmaf(r.w, 1.f / kLog2e, r.y * x);
-          if (a.softplus) ddt[e] *= scan_sigmoid(raw[kScanBlock].at(e) + s.bias[8 * v1 + e]);
-          dskip[e] = fmaf(up, x, dskip[e]);
-          dbias[e] += ddt[e];
+      for (int k = 0; k < kTile; k += 2) {
+        const float4 r0 = s.slot[k][lane], r1 = s.slot[k + 1][lane];
+        const float2 delta = make_float2(r0.x, r1.x);
+        float2 gB, yC, qA;
+        if (kSlices == 1) {
+          gB = make_float2(r0.y, r1.y);
+          yC = make_float2(r0.z, r1.z);
+          qA = make_float2(r0.w, r1.w);
+        } else {
+          const int k2 = kSlices > 1 ? k : 0, k3 = kSlices > 1 ? k + 1 : 0;
+          gB = make_float2(s.sums[k2][0][lane], s.sums[k3][0][lane]);
+          yC = make_float2(s.sums[k2][1][lane], s.sums[k3][1][lane]);
+          qA = make_float2(s.sums[k2][2][lane], s.sums[k3][2][lane]);
         }
-        store_eight<IO, VEC>(b.dx, at, n, dx);
-        store_eight<IO, VEC>(b.ddt, at, n, ddt);
-        if (a.z) store_eight<IO, VEC>(b.dz, at, n, dz);
+        const float2 x = s.raw[stage][0].pair(k);
+        float2 up = s.raw[stage][2].pair(k), dz = both<float2>(0.f);
+        if (a.z) {
+          const float2 z = s.raw[stage][3].pair(k), gate = scan_sigmoid(z), dy = up;
+          // silu'(z) = gate (1 + z (1 - gate))
+          const float2 slope = mul_(gate, fma_(z, fma_(gate, both<float2>(-1.f), both<float2>(1.f)), both<float2>(1.f)));
+          up = mul_(dy, mul_(z, gate));
+          dz = mul_(mul_(dy, fma_(both<float2>(skip), x, yC)), slope);
+        }
+        const float2 dx = fma_(delta, gB, mul_(both<float2>(skip), up));
+        float2 ddt = fma_(gB, x, mul_(qA, both<float2>(1.f / kLog2e)));
+        if (a.softplus) ddt = mul_(ddt, scan_sigmoid(add_(s.raw[stage][1].pair(k), both<float2>(bias))));
+        if (own && k < count) {
+          dskip = fmaf(up.x, x.x, dskip);
+          dbias += ddt.x;
+          st_io(static_cast<IO*>(b.dx) + at + (long long)k * a.D, dx.x);
+          st_io(static_cast<IO*>(b.ddt) + at + (long long)k * a.D, ddt.x);
+          if (a.z) st_io(static_cast<IO*>(b.dz) + at + (long long)k * a.D, dz.x);
+        }
+        if (own && k + 1 < count) {
+          dskip = fmaf(up.y, x.y, dskip);
+          dbias += ddt.y;
+          st_io(static_cast<IO*>(b.dx) + at + (long long)(k + 1) * a.D, dx.y);
+          st_io(static_cast<IO*>(b.ddt) + at + (long long)(k + 1) * a.D, ddt.y);
+          if (a.z) st_io(static_cast<IO*>(b.dz) + at + (long long)(k + 1) * a.D, dz.y);
+        }
       }
-      // the warps' parts of dC and dB
-      const int cb = (int)(blockIdx.x % a.chan_blocks) % (a.chan_blocks / a.G);
-      float* out = b.part_bc + (((long long)cb * a.rows + p.row) * a.T + t) * a.G * 2 * a.N;
-      for (int i = tid; i < count * 2 * NP; i += kScanBlock) {
-        const int k = i / (2 * NP), w = i % (2 * NP) / NP, n = i % NP;
-        if (n >= a.N) continue;
-        float sum = 0.f;
-#pragma unroll
-        for (int w4 = 0; w4 < kWarps; ++w4) sum += s.red[w4][k][w * NP + n];
-        out[((long long)k * a.G + p.g) * 2 * a.N + w * a.N + n] = sum;
-      }
-      __syncthreads();
     }
   }
-  store_states<NS>(b.part_a, unit * a.D + chan, a.N, l * NS, have, dA);
-  // dD and ddt_bias: the threads of a vector, in order, through shared memory
-  float* join = reinterpret_cast<float*>(sm);
 #pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    __syncthreads();
+  for (int sl = 0; sl < kSlices; ++sl)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) join[e * kScanBlock + tid] = which ? dbias[e] : dskip[e];
-    __syncthreads();
-    for (int i = tid; i < p.chans; i += kScanBlock) {
-      float sum = 0.f;
-      for (int k = 0; k < K; ++k) sum += join[i % 8 * kScanBlock + k * S::V8 + i / 8];
-      b.part_d[(unit * 2 + which) * a.D + p.c0 + i] = sum;
+    for (int j = 0; j < LP; ++j) {
+      float2 f[kPairs];
+      from_vec(f, w.dA[sl][j][lane]);
+      store_states<NS>(b.part_a, unit * a.D + chan(j), a.N, sl * NP + l * NS, have(j), f);
     }
+  if (own) {
+    b.part_d[unit * 2 * a.D + c] = dskip;
+    b.part_d[(unit * 2 + 1) * a.D + c] = dbias;
   }
 }
 
@@ -537,31 +475,31 @@ __global__ void __launch_bounds__(256) scan_sums_kernel(BwdArgs b, long long bc_
 }
 
 // ----------------------------------------------------------------- dispatch
-template <typename IO, typename S, bool VEC>
+// S1: of the walk forward; S2 and MOST: of the gradients.
+template <typename IO, typename S1, typename S2, int MOST, bool VEC>
 cudaError_t run(BwdArgs b, cudaStream_t s) {
   ScanArgs& a = b.a;
-  const int dg = a.D / a.G;
-  a.chan_blocks = a.G * ((dg + S::CH - 1) / S::CH);
-  const unsigned grid = (unsigned)((long long)a.rows * a.pieces * a.chan_blocks);
+  a.chan_blocks = scan_chan_blocks(a.D, a.G);
   cudaError_t e = cudaSuccess;
   if (a.pieces > 1) {
-    e = launch_next(false, scan_states_kernel<IO, S, VEC, true>, grid, kScanBlock, 0, s, b);
+    e = launch_walk<IO, S1, VEC, kGrads>(false, a, s);
     if (e == cudaSuccess) e = launch_scan_join(true, a, s);
     const long long n = (long long)a.rows * a.D * a.N;
     if (e == cudaSuccess)
       e = launch_next(true, scan_join_grads_kernel, (unsigned)((n + 255) / 256), 256, 0, s, b);
   } else {
-    e = launch_next(false, scan_states_kernel<IO, S, VEC, false>, grid, kScanBlock, 0, s, b);
+    e = launch_walk<IO, S1, VEC, kChunks>(false, a, s);
   }
   if (e != cudaSuccess) return e;
-  const auto kernel = scan_grad_kernel<IO, S, VEC>;
-  constexpr size_t smem = sizeof(GradSmem<IO, S>);
-  static_assert(smem >= 8 * kScanBlock * sizeof(float), "the last sums go through it");
+  const auto kernel = scan_grad_kernel<IO, S2, MOST, VEC>;
+  constexpr int kSlices = MOST / S2::NP;
+  constexpr size_t smem = kScanWarps * (sizeof(GradSmem<IO, S2, (kSlices > 1)>) + sizeof(GradGroups<IO, MOST>) +
+                                        3 * kSlices * S2::kLanes * 32 * sizeof(float4));
   if (smem > 48 * 1024) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
-  e = launch_next(true, kernel, grid, kScanBlock, smem, s, b);
+  e = launch_next(true, kernel, scan_grid(a), kScanBlock, smem, s, b);
   if (e != cudaSuccess) return e;
   const long long bc = ((long long)a.rows * a.T * a.G * 2 * a.N + 255) / 256;
   const long long ad = ((long long)a.D * (a.N + 2) + 255) / 256;
@@ -571,26 +509,16 @@ cudaError_t run(BwdArgs b, cudaStream_t s) {
 template <typename IO, bool VEC>
 cudaError_t by_states(const BwdArgs& b, cudaStream_t s) {
   const int N = b.a.N;
-  if (N <= 4) return run<IO, ScanShape<1, 4, 1>, VEC>(b, s);
-  if (N <= 8) return run<IO, ScanShape<2, 4, 1>, VEC>(b, s);
-  if (N <= 16) return run<IO, ScanShape<4, 4, 1>, VEC>(b, s);
-  if (N <= 32) return run<IO, ScanShape<8, 4, 1, 32>, VEC>(b, s);
-  return run<IO, ScanShape<16, 4, 1, 16>, VEC>(b, s);
+  if (N <= 4) return run<IO, ScanShape<1, 4>, ScanShape<1, 4>, 4, VEC>(b, s);
+  if (N <= 8) return run<IO, ScanShape<2, 4>, ScanShape<2, 4>, 8, VEC>(b, s);
+  if (N <= 16) return run<IO, ScanShape<2, 8>, ScanShape<4, 4>, 16, VEC>(b, s);
+  if (N <= 32) return run<IO, ScanShape<4, 8>, ScanShape<4, 4>, 32, VEC>(b, s);
+  return run<IO, ScanShape<8, 8>, ScanShape<4, 4>, 64, VEC>(b, s);
 }
-inline int block_chans(int N) { return N <= 4 ? 128 : N <= 8 ? 64 : N <= 16 ? 32 : N <= 32 ? 16 : 8; }
-
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 template <typename IO>
 cudaError_t launch_io(const BwdArgs& b, cudaStream_t s) {
-  constexpr int kV = 16 / sizeof(IO);
-  const ScanArgs& a = b.a;
-  const bool whole = a.N == 4 || a.N == 8 || a.N == 16 || a.N == 32 || a.N == 64;
-  const bool vec = a.D / a.G % 8 == 0 && whole && a.ldx % kV == 0 && a.lddt % kV == 0 &&
-                   (!a.z || a.ldz % kV == 0) && a.ldb % 4 == 0 && a.ldc % 4 == 0 && aligned16(a.x) &&
-                   aligned16(a.dt) && aligned16(a.z) && aligned16(a.B) && aligned16(a.C) &&
-                   aligned16(b.dy) && aligned16(b.dx) && aligned16(b.ddt) && aligned16(b.dz);
-  return vec ? by_states<IO, true>(b, s) : by_states<IO, false>(b, s);
+  return scan_vectors(b.a, sizeof(IO)) ? by_states<IO, true>(b, s) : by_states<IO, false>(b, s);
 }
 
 // The workspace's parts, in order, each a multiple of 256 bytes.
@@ -600,9 +528,8 @@ struct Layout {
 };
 Layout layout_of(int rows, int T, int D, int N, int G) {
   Layout w{};
-  const int ch = block_chans(N), dg = D / G;
-  scan_pieces(rows, T, D, G, ch, 3 * kSms, &w.pieces, &w.len);
-  w.chunks = (T + kChunk - 1) / kChunk;
+  scan_pieces(rows, T, D, G, 24 * kSms, &w.pieces, &w.len);
+  w.chunks = (T + kScanChunk - 1) / kScanChunk;
   const size_t dn = (size_t)D * N * 4, d = (size_t)D * 4, units = (size_t)rows * w.pieces;
   const bool many = w.pieces > 1;
   const auto take = [&](size_t n) {
@@ -615,7 +542,7 @@ Layout layout_of(int rows, int T, int D, int N, int G) {
   w.state = take(many ? units * dn : 0);
   w.span = take(many ? units * d : 0);
   w.grad = take(many ? units * dn : 0);
-  w.part_bc = take((size_t)((dg + ch - 1) / ch) * rows * T * G * 2 * N * 4);
+  w.part_bc = take((size_t)(scan_chan_blocks(D, G) / G) * rows * T * G * 2 * N * 4);
   w.part_a = take(units * dn);
   w.part_d = take(units * 2 * d);
   return w;
@@ -651,7 +578,7 @@ ckda_status ckda_scan_bwd(const void* dy, const void* x, const void* dt, const f
   const size_t states = (size_t)(cu_seqlens ? num_seqs : B) * D * N;
   if (dh0 && dhT && dh0 < dhT + states && dhT < dh0 + states) return CKDA_ERR_INVALID_ARG;
   const Layout w = layout_of(B, T, D, N, G);
-  if (!workspace || workspace_bytes < w.bytes || !aligned16(workspace)) return CKDA_ERR_WORKSPACE;
+  if (!workspace || workspace_bytes < w.bytes || !scan_aligned(workspace, 16)) return CKDA_ERR_WORKSPACE;
   if ((long long)B * T * G * 2 * N / 256 + (long long)D * (N + 2) / 256 + 2 > 0x7fffffffLL)
     return CKDA_ERR_UNSUPPORTED;
   char* ws = static_cast<char*>(workspace);
@@ -665,11 +592,12 @@ ckda_status ckda_scan_bwd(const void* dy, const void* x, const void* dt, const f
   a.softplus = softplus != 0;
   a.pieces = w.pieces; a.piece_len = w.len;
   a.state = part(w.state); a.span = part(w.span);
-  b.dy = dy; b.dhT = dhT; b.dx = dx; b.ddt = ddt; b.dz = dz; b.dB = dBm; b.dC = dC; b.dA = dA;
+  a.dy = dy; a.dhT = dhT;
+  b.dx = dx; b.ddt = ddt; b.dz = dz; b.dB = dBm; b.dC = dC; b.dA = dA;
   b.dskip = dD_skip; b.dbias = ddt_bias; b.dh0 = dh0;
-  b.chunk = part(w.chunk); b.chunk_sum = part(w.chunk_sum); b.grad = part(w.grad);
+  a.chunk = part(w.chunk); a.chunk_sum = part(w.chunk_sum); a.grad = part(w.grad);
   b.part_bc = part(w.part_bc); b.part_a = part(w.part_a); b.part_d = part(w.part_d);
-  b.chunks = w.chunks;
+  a.chunks = w.chunks;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = io_dtype == CKDA_F32 ? launch_io<float>(b, s) : launch_io<__nv_bfloat16>(b, s);
   return e == cudaSuccess ? CKDA_OK : CKDA_ERR_CUDA;

@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(ScanArgs a) {
     float2 s = both<float2>(0.f);
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      const float2 decay = ex2(mul_(both<float2>(d), A2[q]));
+      const float2 decay = decay_of(both<float2>(d), A2[q]);
       h[r][q] = fma_(decay, h[r][q], mul_(both<float2>(v), make_float2(f[2 * q], f[2 * q + 1])));
       s = fma_(make_float2(g[2 * q], g[2 * q + 1]), h[r][q], s);
     }

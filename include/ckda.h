@@ -675,7 +675,7 @@ ckda_status ckda_scan_fwd(const void *x, const void *dt, const float *A, const v
  *   dhT, dh0        : fp32 [sequences, D, N] or NULL (zero, not stored)
  * The forward's states are recomputed.  No atomics: the same inputs give the same bits.
  * workspace: ckda_scan_bwd_workspace_bytes(...) bytes, 16-byte aligned, scratch: mostly
- * the states before every 8th token.
+ * the states before every 4th token.
  */
 size_t ckda_scan_bwd_workspace_bytes(int B, int T, int D, int N, int G);
 ckda_status ckda_scan_bwd(const void *dy, const void *x, const void *dt, const float *A,
