@@ -3,113 +3,131 @@
 //     y = (sum_n C[n] h[n] + D x) silu(z)
 //
 // Each state is read and written once for one exponential and three more instructions: HBM
-// bandwidth is the bound.  LP lanes share a channel, four states (16 bytes) each.  A thread
-// takes its channel of four rows of the batch: their states are loaded before any is waited
-// for, A and B's unpacking serve all four, and a channel's lanes share the rows' step sizes
-// and outputs (one row a lane, handed round by shuffles) instead of each forming all.
+// bandwidth is the bound.  LP lanes share a channel, four states (16 bytes) each.  A block
+// walks the batch four rows at a time, the states of the next four rows on their way
+// through a ring in shared memory (a thread copies what it reads itself); A and its
+// products serve all rows, and a channel's lanes share the rows' step sizes and outputs
+// (one row a lane, handed round by shuffles) instead of each forming all.
 #include "ckda_scan.cuh"
 
 namespace ckda {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kRows = 4;
+constexpr int kThreads = 128;
+constexpr int kRows = 4, kStages = 2;
+constexpr int kPerSm = 8;
 
 // VEC: N a multiple of 4, states and rates 16-byte aligned, B and C in whole vectors.
 template <typename IO, int LP, bool VEC>
-__global__ void __launch_bounds__(kThreads) scan_step_kernel(ScanArgs a) {
+__global__ void __launch_bounds__(kThreads, kPerSm) scan_step_kernel(ScanArgs a, int groups) {
   constexpr int kApart = kThreads / LP, kOwn = LP < kRows ? kRows / LP : 1;
+  __shared__ float4 ring[VEC ? kStages : 1][kRows][kThreads];
   const int l = threadIdx.x % LP, n0 = 4 * l;
-  const int b0 = (int)(blockIdx.x / a.chan_blocks) * kRows;
+  const int first = (int)(blockIdx.x / a.chan_blocks) * groups * kRows;  // of the block's rows
   const int chan = (int)(blockIdx.x % a.chan_blocks) * kApart + threadIdx.x / LP;
   const bool in = chan < a.D;
   const int c = in ? chan : 0;
   const bool have = in && n0 < a.N;
-  const int rows = a.rows - b0 < kRows ? a.rows - b0 : kRows;
-  float* const state = a.hT + (long long)b0 * a.D * a.N;
-  const long long row = (long long)a.D * a.N, at = (long long)c * a.N + n0;
-  float2 h[kRows][2];
-#pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-    if (r >= rows) break;
+  const int end = first + groups * kRows < a.rows ? first + groups * kRows : a.rows;
+  const long long row = (long long)a.D * a.N;
+  float* const state = a.hT + (long long)c * a.N + n0;
+  const auto fetch = [&](int b0, int stage) {
     if (VEC) {
-      if (have) {
-        const float4 v = *reinterpret_cast<const float4*>(state + r * row + at);
-        h[r][0] = make_float2(v.x, v.y);
-        h[r][1] = make_float2(v.z, v.w);
-      }
-    } else {
-      load_states<4>(h[r], state + r * row, c, a.N, n0, in);
-    }
-  }
-  // the rows of this lane: steps, and what finishes the output
-  const float bias = a.dt_bias ? a.dt_bias[c] : 0.f;
-  float delta[kOwn], u[kOwn], x[kOwn], z[kOwn];
 #pragma unroll
-  for (int j = 0; j < kOwn; ++j) {
-    const int r = LP < kRows ? l * kOwn + j : l % kRows;
-    const long long b = b0 + (r < rows ? r : 0);
-    x[j] = ld_io(static_cast<const IO*>(a.x) + b * a.ldx + c);
-    const float raw = ld_io(static_cast<const IO*>(a.dt) + b * a.lddt + c) + bias;
-    z[j] = a.z ? ld_io(static_cast<const IO*>(a.z) + b * a.ldz + c) : 0.f;
-    delta[j] = a.softplus ? softplus(raw) : raw;
-    u[j] = delta[j] * x[j];
-  }
+      for (int r = 0; r < kRows; ++r)
+        if (b0 + r < end && have) copy_async<16>(&ring[VEC ? stage : 0][r][threadIdx.x], state + (b0 + r) * row);
+      copy_commit();
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) fetch(first + s * kRows, s);
   float2 A2[2];
-  if (VEC) {
-    const float4 v = have ? *reinterpret_cast<const float4*>(a.A + at) : make_float4(0.f, 0.f, 0.f, 0.f);
-    A2[0] = make_float2(v.x, v.y);
-    A2[1] = make_float2(v.z, v.w);
-  } else {
-    load_states<4>(A2, a.A, c, a.N, n0, in);
-  }
+  load_states<4>(A2, a.A, c, a.N, n0, in);
   A2[0] = mul_(A2[0], both<float2>(kLog2e));
   A2[1] = mul_(A2[1], both<float2>(kLog2e));
+  const float bias = a.dt_bias ? a.dt_bias[c] : 0.f, skip = a.skip ? a.skip[c] : 0.f;
   const long long group = (long long)(c / (a.D / a.G)) * a.N + n0;
-  float y[kRows];
+  int stage = 0;
+  for (int b0 = first; b0 < end; b0 += kRows, stage = stage + 1 == kStages ? 0 : stage + 1) {
+    const int rows = end - b0 < kRows ? end - b0 : kRows;
+    // B and C of every row, as they are
+    Pack<IO, 4> rowB[kRows], rowC[kRows];
 #pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-    const int from = LP < kRows ? r / kOwn : r;
-    const float d = __shfl_sync(0xffffffffu, delta[LP < kRows ? r % kOwn : 0], from, LP);
-    const float v = __shfl_sync(0xffffffffu, u[LP < kRows ? r % kOwn : 0], from, LP);
-    y[r] = 0.f;
-    if (r >= rows || !have) continue;
-    float f[4], g[4];
-    const IO* pB = static_cast<const IO*>(a.B) + (b0 + r) * a.ldb + group;
-    const IO* pC = static_cast<const IO*>(a.C) + (b0 + r) * a.ldc + group;
-    if (VEC) {
-      unpack<IO, 4>(*reinterpret_cast<const Pack<IO, 4>*>(pB), f);
-      unpack<IO, 4>(*reinterpret_cast<const Pack<IO, 4>*>(pC), g);
-    } else {
+    for (int r = 0; r < kRows; ++r) {
+      if (r >= rows || !have) break;
+      const IO* pB = static_cast<const IO*>(a.B) + (b0 + r) * a.ldb + group;
+      const IO* pC = static_cast<const IO*>(a.C) + (b0 + r) * a.ldc + group;
+      if (VEC) {
+        rowB[r] = *reinterpret_cast<const Pack<IO, 4>*>(pB);
+        rowC[r] = *reinterpret_cast<const Pack<IO, 4>*>(pC);
+      } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        f[e] = n0 + e < a.N ? ld_io(pB + e) : 0.f;
-        g[e] = n0 + e < a.N ? ld_io(pC + e) : 0.f;
+        for (int e = 0; e < 4; ++e)
+          if (n0 + e < a.N) {
+            rowB[r].v[e] = pB[e];
+            rowC[r].v[e] = pC[e];
+          }
       }
     }
-    float2 s = both<float2>(0.f);
+    // the rows of this lane: steps, and what finishes the output
+    float delta[kOwn], u[kOwn], x[kOwn], z[kOwn];
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const float2 decay = decay_of(both<float2>(d), A2[q]);
-      h[r][q] = fma_(decay, h[r][q], mul_(both<float2>(v), make_float2(f[2 * q], f[2 * q + 1])));
-      s = fma_(make_float2(g[2 * q], g[2 * q + 1]), h[r][q], s);
+    for (int j = 0; j < kOwn; ++j) {
+      const int r = LP < kRows ? l * kOwn + j : l % kRows;
+      const long long b = b0 + (r < rows ? r : 0);
+      x[j] = ld_io(static_cast<const IO*>(a.x) + b * a.ldx + c);
+      const float raw = ld_io(static_cast<const IO*>(a.dt) + b * a.lddt + c) + bias;
+      z[j] = a.z ? ld_io(static_cast<const IO*>(a.z) + b * a.ldz + c) : 0.f;
+      delta[j] = a.softplus ? softplus(raw) : raw;
+      u[j] = delta[j] * x[j];
     }
-    y[r] = s.x + s.y;
-    if (VEC)
-      *reinterpret_cast<float4*>(state + r * row + at) =
-          make_float4(h[r][0].x, h[r][0].y, h[r][1].x, h[r][1].y);
-    else
-      store_states<4>(state + r * row, c, a.N, n0, true, h[r]);
-  }
-  fold_values<kRows, LP, 1>(y, l);
-  const float skip = a.skip ? a.skip[c] : 0.f;
+    fetch(b0 + (kStages - 1) * kRows, stage == 0 ? kStages - 1 : stage - 1);
+    if (VEC) copy_wait<kStages - 1>();
+    float y[kRows];
 #pragma unroll
-  for (int j = 0; j < kOwn; ++j) {
-    const int r = LP < kRows ? l * kOwn + j : l;
-    if (r >= rows || !in) continue;
-    float o = fmaf(skip, x[j], y[j]);
-    if (a.z) o *= scan_silu(z[j]);
-    st_io(static_cast<IO*>(a.y) + (long long)(b0 + r) * a.D + c, o);
+    for (int r = 0; r < kRows; ++r) {
+      const int from = LP < kRows ? r / kOwn : r;
+      const float d = __shfl_sync(0xffffffffu, delta[LP < kRows ? r % kOwn : 0], from, LP);
+      const float v = __shfl_sync(0xffffffffu, u[LP < kRows ? r % kOwn : 0], from, LP);
+      y[r] = 0.f;
+      if (r >= rows || !have) continue;
+      float2 h[2];
+      if (VEC) {
+        const float4 w = ring[VEC ? stage : 0][r][threadIdx.x];
+        h[0] = make_float2(w.x, w.y);
+        h[1] = make_float2(w.z, w.w);
+      } else {
+        load_states<4>(h, state + (b0 + r) * row - n0, 0, a.N, n0, true);
+      }
+      float f[4], g[4];
+      unpack<IO, 4>(rowB[r], f);
+      unpack<IO, 4>(rowC[r], g);
+      if (!VEC)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (n0 + e >= a.N) f[e] = g[e] = 0.f;
+      float2 s = both<float2>(0.f);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const float2 decay = decay_of(both<float2>(d), A2[q]);
+        h[q] = fma_(decay, h[q], mul_(both<float2>(v), make_float2(f[2 * q], f[2 * q + 1])));
+        s = fma_(make_float2(g[2 * q], g[2 * q + 1]), h[q], s);
+      }
+      y[r] = s.x + s.y;
+      if (VEC)
+        *reinterpret_cast<float4*>(state + (b0 + r) * row) = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
+      else
+        store_states<4>(state + (b0 + r) * row - n0, 0, a.N, n0, true, h);
+    }
+    fold_values<kRows, LP, 1>(y, l);
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) {
+      const int r = LP < kRows ? l * kOwn + j : l;
+      if (r >= rows || !in) continue;
+      float o = fmaf(skip, x[j], y[j]);
+      if (a.z) o *= scan_silu(z[j]);
+      st_io(static_cast<IO*>(a.y) + (long long)(b0 + r) * a.D + c, o);
+    }
   }
 }
 
@@ -117,8 +135,14 @@ template <typename IO, int LP, bool VEC>
 cudaError_t run(ScanArgs a, cudaStream_t s) {
   constexpr int kPer = kThreads / LP;
   a.chan_blocks = (a.D + kPer - 1) / kPer;
-  const long long blocks = (long long)((a.rows + kRows - 1) / kRows) * a.chan_blocks;
-  scan_step_kernel<IO, LP, VEC><<<(unsigned)blocks, kThreads, 0, s>>>(a);
+  // as few rows to a block as leave all blocks running at once
+  const long long room = (long long)kPerSm * kSms;
+  const int all = (a.rows + kRows - 1) / kRows;
+  long long wide = room / a.chan_blocks;
+  if (wide < 1) wide = 1;
+  const int groups = (int)((all + wide - 1) / wide);
+  const long long blocks = (long long)((all + groups - 1) / groups) * a.chan_blocks;
+  scan_step_kernel<IO, LP, VEC><<<(unsigned)blocks, kThreads, 0, s>>>(a, groups);
   return cudaGetLastError();
 }
 template <typename IO, bool VEC>

@@ -146,9 +146,9 @@ def test_workspace_sizes(L):
             assert f(*a) == 0
         assert f(1, 64, 16, 4, 3) == 0
     assert L.ckda_conv_bwd_workspace_bytes(1, 64, 16, 1) == 0 and L.ckda_conv_bwd_workspace_bytes(1, 64, 16, 5) == 0
-    # the states before every 8th token are most of the backward's
+    # the states before every 4th token are most of the backward's
     n = L.ckda_scan_bwd_workspace_bytes(4, 2048, 4096, 16, 1)
-    assert 4 * 256 * 4096 * 16 * 4 < n < 2 * 4 * 256 * 4096 * 16 * 4
+    assert 4 * 512 * 4096 * 16 * 4 < n < 2 * 4 * 512 * 4096 * 16 * 4
 
 
 # ------------------------------------------------------------------------ binding
