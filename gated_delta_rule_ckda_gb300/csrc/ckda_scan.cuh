@@ -155,7 +155,11 @@ struct ScanShape {
 };
 
 // A tile's inputs of a warp's channels, raw: [K][32] of each tensor, and [K][N] of B and
-// C, padded to NP.  VEC: copied in whole vectors with cp.async.
+// C, padded to NP.  VEC: in whole vectors.  They come with cp.async, but for single bf16
+// elements, which it does not copy: those are held in registers on their way.
+template <typename IO, bool VEC>
+constexpr bool kScanAsync = VEC || sizeof(IO) == 4;
+
 template <typename IO, int K>
 struct ChanTile {
   IO v[K][kScanChans];
@@ -163,16 +167,18 @@ struct ChanTile {
   __device__ __forceinline__ void fetch(const void* base, long long ld, long long at, int c0, int count, int chans) {
     const int lane = threadIdx.x & 31;
     const IO* from = static_cast<const IO*>(base) + at * ld + c0;
-    if (VEC) {
+    if constexpr (VEC) {
       constexpr int kV = 16 / sizeof(IO), kPer = kScanChans / kV;  // vectors of a token
       const int c = lane % kPer * kV, k0 = lane / kPer;
       const IO* p = from + k0 * ld + c;
 #pragma unroll
       for (int k = 0; k < K; k += 32 / kPer, p += 32 / kPer * ld)
         if (k + k0 < count && c < chans) copy_async<16>(&v[k + k0][c], p);
-    } else if (lane < chans) {
-#pragma unroll 8
-      for (int k = 0; k < count; ++k) v[k][lane] = from[k * ld + lane];
+    } else if constexpr (sizeof(IO) == 4) {
+      from += lane;
+#pragma unroll
+      for (int k = 0; k < K; ++k, from += ld)
+        if (k < count && lane < chans) copy_async<4>(&v[k][lane], from);
     }
   }
   __device__ __forceinline__ float2 pair(int k) const {
@@ -187,15 +193,18 @@ struct GroupTile {
   __device__ __forceinline__ void fetch(const void* base, long long ld, long long at, int count, int g, int N) {
     const int lane = threadIdx.x & 31;
     const IO* from = static_cast<const IO*>(base) + at * ld + (long long)g * N;
-    if (VEC) {  // (N a multiple of 4)
+    if constexpr (VEC) {  // (N a multiple of 4)
 #pragma unroll
       for (int j = 0; j < (K * NP / 4 + 31) / 32; ++j) {
         const int i = (j * 32 + lane) * 4, k = i / NP, n = i % NP;
         if (k < count && n < N) copy_async<4 * sizeof(IO)>(&v[i], from + k * ld + n);
       }
-    } else {
-      for (int i = lane; i < count * NP; i += 32)
-        if (i % NP < N) v[i] = from[i / NP * ld + i % NP];
+    } else if constexpr (sizeof(IO) == 4) {
+#pragma unroll
+      for (int j = 0; j < K * NP / 32; ++j) {
+        const int i = j * 32 + lane, k = i / NP, n = i % NP;
+        if (k < count && n < N) copy_async<4>(&v[i], from + k * ld + n);
+      }
     }
   }
   // To fp32, zero where there is no token or no state.
@@ -213,6 +222,38 @@ struct GroupTile {
         if (k >= count || n + (VEC ? 0 : e) >= N) f[e] = 0.f;
       *reinterpret_cast<float4*>(to + i) = make_float4(f[0], f[1], f[2], f[3]);
     }
+  }
+};
+// A tile's elements in registers: load() starts the loads, leave() puts them down.
+template <typename IO, int K>
+struct HeldChans {
+  IO v[K];
+  __device__ __forceinline__ void load(const void* base, long long ld, long long at, int c0, int count, int chans) {
+    const int lane = threadIdx.x & 31;
+    const IO* from = static_cast<const IO*>(base) + at * ld + c0 + lane;
+#pragma unroll
+    for (int k = 0; k < K; ++k, from += ld)
+      if (k < count && lane < chans) v[k] = *from;
+  }
+  __device__ __forceinline__ void leave(ChanTile<IO, K>& to) const {
+#pragma unroll
+    for (int k = 0; k < K; ++k) to.v[k][threadIdx.x & 31] = v[k];
+  }
+};
+template <typename IO, int K, int NP>
+struct HeldGroups {
+  IO v[K * NP / 32];
+  __device__ __forceinline__ void load(const void* base, long long ld, long long at, int count, int g, int N) {
+    const IO* from = static_cast<const IO*>(base) + at * ld + (long long)g * N;
+#pragma unroll
+    for (int j = 0; j < K * NP / 32; ++j) {
+      const int i = j * 32 + (threadIdx.x & 31), k = i / NP, n = i % NP;
+      if (k < count && n < N) v[j] = from[k * ld + n];
+    }
+  }
+  __device__ __forceinline__ void leave(GroupTile<IO, K, NP>& to) const {
+#pragma unroll
+    for (int j = 0; j < K * NP / 32; ++j) to.v[j * 32 + (threadIdx.x & 31)] = v[j];
   }
 };
 
@@ -366,19 +407,42 @@ __global__ void __launch_bounds__(kScanBlock) scan_walk_kernel(ScanArgs a) {
   if (MODE == kOut && p.piece == 0 && a.hT && (a.cu || a.T == 0)) empty_states(a, p, a.h0, a.hT);
   if (p.t0 >= p.t1) return;
 
+  constexpr bool kAsync = kScanAsync<IO, VEC>;
+  HeldChans<IO, kAsync ? 1 : K> held[Smem::kTensors];
+  HeldGroups<IO, K, kAsync ? 32 / K : NP> held_bc[2];
   const auto fetch = [&](int t, int stage) {
     const int count = p.t1 - t < K ? p.t1 - t : K;
     const long long at = (long long)p.row * a.T + t;
-    s.raw[stage][0].template fetch<VEC>(a.x, a.ldx, at, p.c0, count, p.chans);
-    s.raw[stage][1].template fetch<VEC>(a.dt, a.lddt, at, p.c0, count, p.chans);
-    if (MODE == kGrads) s.raw[stage][MODE == kGrads ? 2 : 0].template fetch<VEC>(a.dy, a.D, at, p.c0, count, p.chans);
-    if (Smem::kC && a.z)
-      s.raw[stage][Smem::kTensors - 1].template fetch<VEC>(a.z, a.ldz, at, p.c0, count, p.chans);
-    s.bc[stage][0].template fetch<VEC>(a.B, a.ldb, at, count, p.g, a.N);
-    if (Smem::kC) s.bc[stage][Smem::kC ? 1 : 0].template fetch<VEC>(a.C, a.ldc, at, count, p.g, a.N);
+    const auto chans = [&](int i, const void* base, long long ld) {
+      if constexpr (kAsync)
+        s.raw[stage][i].template fetch<VEC>(base, ld, at, p.c0, count, p.chans);
+      else
+        held[i].load(base, ld, at, p.c0, count, p.chans);
+    };
+    const auto groups = [&](int i, const void* base, long long ld) {
+      if constexpr (kAsync)
+        s.bc[stage][i].template fetch<VEC>(base, ld, at, count, p.g, a.N);
+      else
+        held_bc[i].load(base, ld, at, count, p.g, a.N);
+    };
+    chans(0, a.x, a.ldx);
+    chans(1, a.dt, a.lddt);
+    if (MODE == kGrads) chans(MODE == kGrads ? 2 : 0, a.dy, a.D);
+    if (Smem::kC && a.z) chans(Smem::kTensors - 1, a.z, a.ldz);
+    groups(0, a.B, a.ldb);
+    if (Smem::kC) groups(Smem::kC ? 1 : 0, a.C, a.ldc);
     copy_commit();
   };
+  const auto land = [&](int stage) {
+    if constexpr (!kAsync) {
+#pragma unroll
+      for (int i = 0; i < Smem::kTensors; ++i) held[i].leave(s.raw[stage][i]);
+      held_bc[0].leave(s.bc[stage][0]);
+      if constexpr (Smem::kC) held_bc[1].leave(s.bc[stage][1]);
+    }
+  };
   fetch(p.t0, 0);
+  land(0);
 
   const bool own = lane < p.chans;
   const int c = p.c0 + (own ? lane : 0);  // the lane's own channel
@@ -522,6 +586,7 @@ __global__ void __launch_bounds__(kScanBlock) scan_walk_kernel(ScanArgs a) {
     else
       recur(std::false_type());
     if (t + count >= seq.end && t + count < p.t1) seq = scan_seq_at(a, p.row, t + count);
+    if (t + K < p.t1) land(stage ^ 1);
   }
   if (MODE == kEnds || MODE == kGrads) {
 #pragma unroll

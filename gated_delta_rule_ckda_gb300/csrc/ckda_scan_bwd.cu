@@ -152,15 +152,31 @@ __global__ void __launch_bounds__(kScanBlock, 2) scan_grad_kernel(BwdArgs b) {
   if (p.t0 < p.t1) {
     const float bias = a.dt_bias ? a.dt_bias[c] : 0.f, skip = a.skip ? a.skip[c] : 0.f;
     const int tiles = (p.t1 - p.t0 + kTile - 1) / kTile;
+    constexpr bool kAsync = kScanAsync<IO, VEC>;
     const auto fetch = [&](int tile, int stage) {  // a tile's inputs
       const int t = p.t0 + tile * kTile, count = p.t1 - t < kTile ? p.t1 - t : kTile;
       const long long at = (long long)p.row * a.T + t;
-      s.raw[stage][0].template fetch<VEC>(a.x, a.ldx, at, p.c0, count, p.chans);
-      s.raw[stage][1].template fetch<VEC>(a.dt, a.lddt, at, p.c0, count, p.chans);
-      s.raw[stage][2].template fetch<VEC>(a.dy, a.D, at, p.c0, count, p.chans);
-      if (a.z) s.raw[stage][3].template fetch<VEC>(a.z, a.ldz, at, p.c0, count, p.chans);
-      w.bc.raw[stage][0].template fetch<VEC>(a.B, a.ldb, at, count, p.g, a.N);
-      w.bc.raw[stage][1].template fetch<VEC>(a.C, a.ldc, at, count, p.g, a.N);
+      if constexpr (kAsync) {
+        s.raw[stage][0].template fetch<VEC>(a.x, a.ldx, at, p.c0, count, p.chans);
+        s.raw[stage][1].template fetch<VEC>(a.dt, a.lddt, at, p.c0, count, p.chans);
+        s.raw[stage][2].template fetch<VEC>(a.dy, a.D, at, p.c0, count, p.chans);
+        if (a.z) s.raw[stage][3].template fetch<VEC>(a.z, a.ldz, at, p.c0, count, p.chans);
+        w.bc.raw[stage][0].template fetch<VEC>(a.B, a.ldb, at, count, p.g, a.N);
+        w.bc.raw[stage][1].template fetch<VEC>(a.C, a.ldc, at, count, p.g, a.N);
+      } else {  // (no registers to hold them beside the recurrence)
+        HeldChans<IO, kTile> held[4];
+        HeldGroups<IO, kTile, MOST> held_bc[2];
+        held[0].load(a.x, a.ldx, at, p.c0, count, p.chans);
+        held[1].load(a.dt, a.lddt, at, p.c0, count, p.chans);
+        held[2].load(a.dy, a.D, at, p.c0, count, p.chans);
+        if (a.z) held[3].load(a.z, a.ldz, at, p.c0, count, p.chans);
+        held_bc[0].load(a.B, a.ldb, at, count, p.g, a.N);
+        held_bc[1].load(a.C, a.ldc, at, count, p.g, a.N);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) held[i].leave(s.raw[stage][i]);
+        held_bc[0].leave(w.bc.raw[stage][0]);
+        held_bc[1].leave(w.bc.raw[stage][1]);
+      }
       copy_commit();
     };
     const auto fetch_states = [&](int tile, int sl) {  // the states before its chunks
@@ -175,9 +191,11 @@ __global__ void __launch_bounds__(kScanBlock, 2) scan_grad_kernel(BwdArgs b) {
             if (have(j) && sl * NP + l * NS < a.N)
               copy_async<16>(&s.state[i][j][lane], a.chunk + (ck * a.D + chan(j)) * a.N + sl * NP + l * NS);
           } else {
-            float2 f[kPairs];
-            load_states<NS>(f, a.chunk, ck * a.D + chan(j), a.N, sl * NP + l * NS, have(j));
-            s.state[i][j][lane] = vec(f);
+#pragma unroll
+            for (int e = 0; e < NS; ++e)
+              if (have(j) && sl * NP + l * NS + e < a.N)
+                copy_async<4>(reinterpret_cast<float*>(&s.state[i][j][lane]) + e,
+                              a.chunk + (ck * a.D + chan(j)) * a.N + sl * NP + l * NS + e);
           }
         }
         if (a.pieces > 1 && sl == 0) copy_async<4>(&s.before[i][lane], a.chunk_sum + ck * a.D + c);
@@ -189,6 +207,7 @@ __global__ void __launch_bounds__(kScanBlock, 2) scan_grad_kernel(BwdArgs b) {
     int stage = 0;
     for (int tile = tiles - 1; tile >= 0; --tile, stage ^= 1) {
       const int t = p.t0 + tile * kTile, count = p.t1 - t < kTile ? p.t1 - t : kTile;
+      if (!kAsync && tile + 1 < tiles) fetch(tile, stage);
       copy_wait<0>();
       __syncwarp();
       const bool whole = count == kTile && p.chans == kScanChans;
@@ -215,7 +234,7 @@ __global__ void __launch_bounds__(kScanBlock, 2) scan_grad_kernel(BwdArgs b) {
       Marks marks;
       if (edges) marks.find(a, p.row, t, count);
       __syncwarp();
-      if (tile > 0) fetch(tile - 1, stage ^ 1);
+      if (kAsync && tile > 0) fetch(tile - 1, stage ^ 1);
       float* const out_bc = b.part_bc + ((((long long)p.block * a.rows + p.row) * a.T + t) * a.G + p.g) * 2 * a.N;
       const long long apart_bc = (long long)a.G * 2 * a.N;
       // ---- a slice of the states
