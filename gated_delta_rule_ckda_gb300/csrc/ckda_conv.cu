@@ -9,15 +9,22 @@
 // and a final state's gradient adds to the inputs that it holds.
 //
 // Each input is read once and each output written once; 2 W + 4 flop an element leave HBM
-// as the bound.  Channels are the fast axis: a thread has VEC neighbouring channels and
-// walks a run of tokens with the last W - 1 inputs in registers, loads of kAhead tokens in
-// flight.  A run starts W - 1 tokens early (backward: and ends W - 1 late), 5% at 64
-// tokens and mostly from L2.  Runs go over one flat axis of tokens, dense rows or packed
-// sequences alike, and take up the next sequence's state where one begins.
+// as the bound.  Channels are the fast axis: a thread has VEC neighbouring channels, in
+// pairs, and walks a run of tokens with the last W - 1 inputs in registers, the next 8
+// tokens on their way through a ring in shared memory.  A run starts W - 1 tokens early
+// (backward: and ends W - 1 late), 5% at 64 tokens and mostly from L2.  Runs go over one
+// flat axis of tokens, dense rows or packed sequences alike, and take up the next
+// sequence's state where one begins.
 //
 // The gradients of the weights: sums over a run in registers, over a block's runs in
 // shared memory, then one partial row a block in the workspace, added in a fixed order by
 // a second kernel.  No atomics: the same bits every time.
+//
+// Measured, bf16 with four taps, bias and silu: 24 packed prompts, 50,021 tokens of 4096
+// channels, 141 us, 87% of the copy bandwidth (8 channels a thread with the loads held in
+// registers 488, 4 channels 176, 2 channels 163); backward of 8 x 2048 tokens 101 us, 60%
+// (458 in registers, 202 by groups of tokens in registers, 117 with checks in every token).
+// Odd channel counts go by single elements: 4 x 2048 tokens of 4095 in 41 us, 50%.
 #include "ckda_launch.cuh"
 #include "ckda_rows.cuh"
 
@@ -374,6 +381,7 @@ template <typename IO, int W, int VEC>
 __global__ void __launch_bounds__(kBlock, 2) conv_bwd_kernel(ConvArgs a) {
   extern __shared__ __align__(16) char sm[];
   using Ring = TokenRing<IO, VEC, 2>;
+  let_next_start();
   if (blockIdx.x >= a.main_blocks) {
     initial_grads<IO, W>(a);
     return;
@@ -549,7 +557,8 @@ inline int chan_blocks_of(int D, int vec) {
   const int lanes = lanes_of((D + vec - 1) / vec);
   return (D + lanes * vec - 1) / (lanes * vec);
 }
-// Tokens of a run: 64 where there are enough for every SM, shorter ones else.
+// Tokens of a run: 64 where there are enough for every SM (packed prompts 141 us, by 128
+// 140, by 256 147; a training batch's gradients 101 each way), shorter ones else.
 inline int run_of(long long tokens, int D, int vec) {
   const int lanes = lanes_of((D + vec - 1) / vec);
   int run = 64;
@@ -708,6 +717,8 @@ ckda_status ckda_conv_bwd(const void* dy, const void* x, const void* weight, con
   if (overlap(x, span_bytes(B, T, D, ldx, io), dx, span_bytes(B, T, D, D, io)) ||
       overlap(dy, span_bytes(B, T, D, D, io), dx, span_bytes(B, T, D, D, io)))
     return CKDA_ERR_INVALID_ARG;
+  const size_t states = (size_t)(cu_seqlens ? num_seqs : B) * (W - 1) * D * io;
+  if (overlap(h0, states, dh0, states) || overlap(dhT, states, dh0, states)) return CKDA_ERR_INVALID_ARG;
   if (!workspace || workspace_bytes < ckda_conv_bwd_workspace_bytes(B, T, D, W) || !aligned(workspace, 16))
     return CKDA_ERR_WORKSPACE;
   ConvArgs a{};

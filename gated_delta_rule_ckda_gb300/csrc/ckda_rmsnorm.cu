@@ -294,6 +294,7 @@ __global__ void __launch_bounds__(1024) rms_fwd_long_kernel(RmsArgs a) {
 // ----------------------------------------------------------------- backward
 template <typename IO, int VEC, int TB, int LPR, int NV, int S>
 __global__ void __launch_bounds__(TB) rms_bwd_kernel(RmsArgs a) {
+  let_next_start();
   constexpr int kGroups = TB / LPR;
   extern __shared__ __align__(16) char sm[];
   __shared__ float red[2 * TB / 32];
@@ -411,6 +412,7 @@ __global__ void __launch_bounds__(TB) rms_bwd_kernel(RmsArgs a) {
 // the workspace.
 template <typename IO>
 __global__ void __launch_bounds__(1024) rms_bwd_long_kernel(RmsArgs a) {
+  let_next_start();
   __shared__ float red[64];
   const float inv_d = 1.f / (float)a.D;
   float* pw = a.part ? a.part + (size_t)blockIdx.x * a.D : nullptr;

@@ -8,6 +8,10 @@
 // through a ring in shared memory (a thread copies what it reads itself); A and its
 // products serve all rows, and a channel's lanes share the rows' step sizes and outputs
 // (one row a lane, handed round by shuffles) instead of each forming all.
+//
+// 256 rows of 4096 channels of 16 states: 33 us, 65% of the copy bandwidth (each lane its
+// own steps and one row after another, 140 instructions a state: 57; four rows held in
+// registers 37; eight blocks an SM, with five 37).
 #include "ckda_scan.cuh"
 
 namespace ckda {

@@ -611,7 +611,8 @@ ckda_status ckda_conv_fwd(const void *x, const void *weight, const void *bias, c
 /*
  * Its backward: the gradients of sum <y, dy> + <hT, dhT>.
  *   dy, dx   : io [B, T, D]; dx overlaps neither x nor dy (checked)
- *   dhT, dh0 : io [N, W - 1, D] or NULL (zero, not stored)
+ *   dhT, dh0 : io [N, W - 1, D] or NULL (zero, not stored); dh0 overlaps neither h0 nor
+ *              dhT (checked)
  *   dweight  : weight_dtype [D, W]; dbias [D] or NULL (not wanted); from fp32 sums in a
  *              fixed order: the same inputs give the same bits
  * workspace: ckda_conv_bwd_workspace_bytes(B, T, D, W) bytes, 16-byte aligned, scratch.
@@ -649,9 +650,9 @@ ckda_status ckda_conv_decode_step(const void *x, const void *weight, const void 
  *   cu_seqlens, num_seqs: as ckda_fwd (packed sequences, B = 1); an empty sequence hands
  *                 its h0 on; tokens behind the last sequence are left as they were
  *
- * N <= 64.  States, steps and sums are fp32, one rounding to io.  A channel count per
- * group that is a multiple of 8, N = 4, 8, 16, 32 or 64 and 16-byte aligned rows move in
- * vectors.  Rows with too few channels for the GPU are cut into pieces that run side by
+ * N <= 64.  States, steps and sums are fp32, one rounding to io.  N a multiple of 4, a
+ * channel count per group that is a multiple of 8 (fp32: 4) and 16-byte aligned rows move
+ * in vectors.  Rows with too few channels for the GPU are cut into pieces that run side by
  * side.  A value that is not finite stays in its own sequence, from its token on, and in
  * its own channel where it is x's, dt's or z's.
  *
@@ -672,7 +673,8 @@ ckda_status ckda_scan_fwd(const void *x, const void *dt, const float *A, const v
  *   dy, dx, ddt, dz : io   [B, T, D] (dz NULL exactly where z is)
  *   dBm, dC         : io   [B, T, G, N], summed over the group's channels
  *   dA              : fp32 [D, N]; dD_skip, ddt_bias fp32 [D] or NULL (not wanted)
- *   dhT, dh0        : fp32 [sequences, D, N] or NULL (zero, not stored)
+ *   dhT, dh0        : fp32 [sequences, D, N] or NULL (zero, not stored), not overlapping
+ *                     (checked)
  * The forward's states are recomputed.  No atomics: the same inputs give the same bits.
  * workspace: ckda_scan_bwd_workspace_bytes(...) bytes, 16-byte aligned, scratch: mostly
  * the states before every 4th token.

@@ -99,3 +99,38 @@ def test_one_graph_of_the_whole_pass(example):
         torch.cuda.synchronize()
         for a, e in zip(got, run()):
             assert torch.equal(a, e)
+
+
+def test_calls_side_by_side_on_two_streams(example):
+    """Every call on two streams at once, each with other inputs: the results of each alone."""
+    ck = example.ck
+    gen = torch.Generator().manual_seed(6)
+    mk = lambda *s: torch.randn(*s, generator=gen).cuda()  # noqa: E731
+    D, N, T = 256, 16, 900
+
+    def inputs():
+        return dict(u=mk(2, T, D).bfloat16(), r=mk(2, T, D).bfloat16(), w=mk(D), cw=mk(D, 4), A=-mk(D, N).abs(),
+                    b=mk(2, T, N).bfloat16(), c=mk(2, T, N).bfloat16(), dy=mk(2, T, D).bfloat16())
+
+    def run(s):
+        y, h, rstd = ck.rmsnorm_fwd(s["u"], s["w"], residual=s["r"])
+        y8, scale, _, _ = ck.rmsnorm_fwd8(s["u"], s["w"], residual=s["r"], group=64)
+        x, state = ck.conv_fwd(y, s["cw"])
+        o, hT = ck.scan_fwd(x, y, s["A"], s["b"], s["c"], z=y)
+        g = ck.scan_bwd(s["dy"], x, y, s["A"], s["b"], s["c"], z=y)
+        back = ck.conv_bwd(g[0], y, s["cw"])
+        return [o, hT, y8.float(), scale, state, *(t for t in (*g, *back) if t is not None),
+                *ck.rmsnorm_bwd(back[0], h, rstd, s["w"], dh=h)]
+    sets = [inputs(), inputs()]
+    want = [run(s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for _ in range(3):
+        for s, stream in zip(sets, streams):
+            with torch.cuda.stream(stream):
+                got.append(run(s))
+    torch.cuda.synchronize()
+    for i, outs in enumerate(got):
+        for a, b in zip(want[i % 2], outs):
+            assert torch.equal(a, b)

@@ -43,14 +43,15 @@ def test_conv_fwd(L, bad, code):
 
 
 def conv_bwd(L, dy=far(0), x=far(1), w=far(2), dx=far(3), dw=far(4), db=None, B=2, T=8, D=16, W=4, ldx=16, io=1, wt=0,
-             ws=far(9), size=1 << 20, cu=None, seqs=0):
-    return L.ckda_conv_bwd(dy, x, w, None, None, None, dx, dw, db, None, cu, seqs, B, T, D, W, ldx, io, wt, 1, ws, size, None)
+             ws=far(9), size=1 << 20, cu=None, seqs=0, h0=None, dhT=None, dh0=None):
+    return L.ckda_conv_bwd(dy, x, w, None, h0, dhT, dx, dw, db, dh0, cu, seqs, B, T, D, W, ldx, io, wt, 1, ws, size, None)
 
 
 @pytest.mark.parametrize("bad,code", [
     (dict(dy=None), BAD), (dict(x=None), BAD), (dict(w=None), BAD), (dict(dx=None), BAD), (dict(dw=None), BAD),
     (dict(dx=far(0)), BAD), (dict(dx=far(1)), BAD), (dict(W=6), UNS), (dict(ws=None), WS), (dict(size=64), WS),
-    (dict(ws=vp(0x1000008)), WS), (dict(io=3), BAD), (dict(cu=P, seqs=2, B=2), BAD)])
+    (dict(ws=vp(0x1000008)), WS), (dict(io=3), BAD), (dict(cu=P, seqs=2, B=2), BAD),
+    (dict(h0=far(20), dh0=far(20)), BAD), (dict(dhT=far(20), dh0=vp(0x1000000 * 21 + 64)), BAD)])
 def test_conv_bwd(L, bad, code):
     assert conv_bwd(L, **bad) == code
 
