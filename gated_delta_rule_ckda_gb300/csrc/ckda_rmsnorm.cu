@@ -462,6 +462,236 @@ __global__ void __launch_bounds__(1024) rms_weight_grad_kernel(RmsArgs a) {
   }
 }
 
+// ------------------------------------------------------- widths of odd bytes
+// Rows whose bytes are no multiple of 16, on bases that are: a row starts somewhere in a
+// 16-byte vector, so whole vectors come to shared memory as they lie, threads take single
+// columns of it (LPR apart, NV each: weights stay with their columns), leave the results in
+// its place, and whole vectors go out again; what a row shares a vector with stays untouched.
+// One warp a row, or a block.  8,489 rows of 4853 in bf16 with a residual: 103 us forward
+// (48% of the copy bandwidth), 154 backward, which took 363 by single elements from memory.
+template <typename IO>
+struct OddRow {
+  const long long start;  // the row's first byte
+  const int shift, bytes, vecs;
+  __device__ __forceinline__ OddRow(long long row, int D, int size)
+      : start(row * D * size), shift((int)(start & 15)), bytes(D * size), vecs((shift + bytes + 15) / 16) {}
+  // (a vector past the tensor's end is copied as far as the tensor goes)
+  __device__ __forceinline__ void fetch(char* to, const void* base, long long total, int lane, int lanes) const {
+    const char* from = static_cast<const char*>(base) + (start - shift);
+    for (int v = lane; v < vecs; v += lanes) {
+      const long long left = total - (start - shift) - 16LL * v;
+      const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(to + 16 * v));
+      const int n = left < 16 ? (int)left : 16;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(from + 16 * v), "r"(n) : "memory");
+    }
+  }
+  template <typename T>
+  __device__ __forceinline__ void store(void* base, const char* from, int lane, int lanes) const {
+    char* to = static_cast<char*>(base) + (start - shift);
+    for (int v = lane; v < vecs; v += lanes) {
+      const int lo = v == 0 ? shift : 0, hi = 16 * v + 16 <= shift + bytes ? 16 : shift + bytes - 16 * v;
+      if (lo == 0 && hi == 16) {
+        *reinterpret_cast<uint4*>(to + 16 * v) = *reinterpret_cast<const uint4*>(from + 16 * v);
+      } else {
+        for (int i = lo; i < hi; i += (int)sizeof(T))
+          *reinterpret_cast<T*>(to + 16 * v + i) = *reinterpret_cast<const T*>(from + 16 * v + i);
+      }
+    }
+  }
+};
+template <int LPR>
+__device__ __forceinline__ void row_sync() {
+  if (LPR <= 32)
+    __syncwarp();
+  else
+    __syncthreads();
+}
+// Bytes of a row in shared memory.
+inline __host__ __device__ int odd_span(int D, int size) { return (D * size + 15) / 16 * 16 + 16; }
+
+template <typename IO, bool OUT8, int TB, int LPR, int NV>
+__global__ void __launch_bounds__(TB) rms_fwd_odd_kernel(RmsArgs a, int stages) {
+  extern __shared__ __align__(16) char sm[];
+  __shared__ float red[2 * TB / 32];
+  constexpr int kGroups = TB / LPR;
+  const int lane = threadIdx.x % LPR, grp = threadIdx.x / LPR, n_in = a.add ? 2 : 1;
+  const int span = odd_span(a.D, sizeof(IO));
+  char* const buf = sm + (size_t)grp * stages * n_in * span;
+  const long long total = a.rows * a.D * (long long)sizeof(IO);
+  const long long stride = (long long)gridDim.x * kGroups;
+  const float inv_d = 1.f / (float)a.D;
+  int turn = 0;
+  const auto fetch = [&](long long r, int stage) {
+    if (r < a.rows) {
+      const OddRow<IO> row(r, a.D, sizeof(IO));
+      row.fetch(buf + (size_t)stage * n_in * span, a.x, total, lane, LPR);
+      if (a.add) row.fetch(buf + ((size_t)stage * n_in + 1) * span, a.add, total, lane, LPR);
+    }
+    copy_commit();
+  };
+  long long r0 = (long long)blockIdx.x * kGroups;  // (the same in a block: barriers)
+  for (int s = 0; s < stages; ++s) fetch(r0 + grp + s * stride, s);
+  float w[NV];
+#pragma unroll
+  for (int n = 0; n < NV; ++n) w[n] = n * LPR + lane < a.D ? weight_of(a, n * LPR + lane) : 0.f;
+  for (int stage = 0; r0 < a.rows; r0 += stride, stage = stage + 1 == stages ? 0 : stage + 1) {
+    const long long r = r0 + grp;
+    const bool in = r < a.rows;
+    if (stages == 1)
+      copy_wait<0>();
+    else
+      copy_wait<1>();
+    row_sync<LPR>();
+    const OddRow<IO> row(in ? r : 0, a.D, sizeof(IO));
+    char* const raw = buf + (size_t)stage * n_in * span;
+    IO* const x = reinterpret_cast<IO*>(raw + row.shift);
+    IO* const res = reinterpret_cast<IO*>(raw + span + row.shift);
+    float h[NV];
+    float s = 0.f;
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+      const int i = n * LPR + lane;
+      h[n] = 0.f;
+      if (in && i < a.D) {
+        h[n] = ld_io(x + i);
+        if (a.add) {
+          h[n] = rounded<IO>(h[n] + ld_io(res + i));
+          st_io(x + i, h[n]);
+        }
+      }
+      s = fmaf(h[n], h[n], s);
+    }
+    const float rstd = 1.f / sqrtf(row_sum<TB, LPR>(s, red, turn) * inv_d + a.eps);
+    if (in && lane == 0) a.rstd[r] = rstd;
+    float top = 0.f;
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+      h[n] = h[n] * rstd * w[n];
+      if (OUT8) top = max_nan(top, fabsf(h[n]));
+    }
+    // y in the place of the residual, or of x where nothing else goes out from there
+    char* const out = a.add ? raw + span : raw;
+    if (OUT8) {
+      top = max_nan(row_max<TB, LPR>(top, red, turn), kLeastMax);
+      if (in && lane == 0) a.scale[r] = top / kE4m3Max;
+      const float scale = kE4m3Max / top;
+      uint8_t* const y = reinterpret_cast<uint8_t*>(out) + (r * a.D & 15);
+      row_sync<LPR>();  // (bytes lie over other columns)
+#pragma unroll
+      for (int n = 0; n < NV; ++n)
+        if (in && n * LPR + lane < a.D)
+          y[n * LPR + lane] = __nv_cvt_float_to_fp8(h[n] * scale, __NV_SATFINITE, __NV_E4M3);
+    } else {
+      IO* const y = reinterpret_cast<IO*>(out + row.shift);
+#pragma unroll
+      for (int n = 0; n < NV; ++n)
+        if (in && n * LPR + lane < a.D) st_io(y + n * LPR + lane, h[n]);
+    }
+    row_sync<LPR>();
+    if (in) {
+      if (a.add) row.template store<IO>(a.h, raw, lane, LPR);
+      if (OUT8)
+        OddRow<IO>(r, a.D, 1).template store<uint8_t>(a.y, out, lane, LPR);
+      else
+        row.template store<IO>(a.y, out, lane, LPR);
+    }
+    row_sync<LPR>();
+    fetch(r + stages * stride, stage);
+  }
+}
+
+template <typename IO, int TB, int LPR, int NV>
+__global__ void __launch_bounds__(TB) rms_bwd_odd_kernel(RmsArgs a, int stages) {
+  let_next_start();
+  extern __shared__ __align__(16) char sm[];
+  __shared__ float red[2 * TB / 32];
+  constexpr int kGroups = TB / LPR;
+  const int lane = threadIdx.x % LPR, grp = threadIdx.x / LPR, n_in = a.add ? 3 : 2;
+  const int span = odd_span(a.D, sizeof(IO));
+  char* const buf = sm + (size_t)grp * stages * n_in * span;
+  const long long total = a.rows * a.D * (long long)sizeof(IO);
+  const long long stride = (long long)gridDim.x * kGroups;
+  const float inv_d = 1.f / (float)a.D;
+  int turn = 0;
+  const auto fetch = [&](long long r, int stage) {
+    if (r < a.rows) {
+      const OddRow<IO> row(r, a.D, sizeof(IO));
+      char* const to = buf + (size_t)stage * n_in * span;
+      row.fetch(to, a.x, total, lane, LPR);
+      row.fetch(to + span, a.dy, total, lane, LPR);
+      if (a.add) row.fetch(to + 2 * span, a.add, total, lane, LPR);
+    }
+    copy_commit();
+  };
+  long long r0 = (long long)blockIdx.x * kGroups;
+  for (int s = 0; s < stages; ++s) fetch(r0 + grp + s * stride, s);
+  float w[NV], dw[NV];
+#pragma unroll
+  for (int n = 0; n < NV; ++n) {
+    w[n] = n * LPR + lane < a.D ? weight_of(a, n * LPR + lane) : 0.f;
+    dw[n] = 0.f;
+  }
+  for (int stage = 0; r0 < a.rows; r0 += stride, stage = stage + 1 == stages ? 0 : stage + 1) {
+    const long long r = r0 + grp;
+    const bool in = r < a.rows;
+    const float rstd = in ? a.rstd[r] : 0.f;
+    if (stages == 1)
+      copy_wait<0>();
+    else
+      copy_wait<1>();
+    row_sync<LPR>();
+    const OddRow<IO> row(in ? r : 0, a.D, sizeof(IO));
+    char* const raw = buf + (size_t)stage * n_in * span;
+    const IO* const h = reinterpret_cast<const IO*>(raw + row.shift);
+    IO* const dy = reinterpret_cast<IO*>(raw + span + row.shift);
+    const IO* const dh = reinterpret_cast<const IO*>(raw + 2 * span + row.shift);
+    float xh[NV], t[NV];
+    float s = 0.f;
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+      const int i = n * LPR + lane;
+      xh[n] = t[n] = 0.f;
+      if (in && i < a.D) {
+        const float g = ld_io(dy + i);
+        xh[n] = ld_io(h + i) * rstd;
+        dw[n] = fmaf(g, xh[n], dw[n]);
+        t[n] = g * w[n];
+      }
+      s = fmaf(t[n], xh[n], s);
+    }
+    const float m = row_sum<TB, LPR>(s, red, turn) * inv_d;
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+      const int i = n * LPR + lane;
+      if (in && i < a.D) st_io(dy + i, fmaf(t[n] - xh[n] * m, rstd, a.add ? ld_io(dh + i) : 0.f));
+    }
+    row_sync<LPR>();
+    if (in) row.template store<IO>(a.y, raw + span, lane, LPR);
+    row_sync<LPR>();
+    fetch(r + stages * stride, stage);
+  }
+  if (!a.part) return;
+  if (LPR > 32) {
+#pragma unroll
+    for (int n = 0; n < NV; ++n)
+      if (n * LPR + lane < a.D) a.part[(size_t)blockIdx.x * a.D + n * LPR + lane] = dw[n];
+    return;
+  }
+  // the block's warps, through shared memory ([kGroups][D]), in order
+  float* part_s = reinterpret_cast<float*>(sm);
+  copy_wait<0>();
+  __syncthreads();
+#pragma unroll
+  for (int n = 0; n < NV; ++n)
+    if (n * LPR + lane < a.D) part_s[grp * a.D + n * LPR + lane] = dw[n];
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.D; i += TB) {
+    float s = 0.f;
+    for (int g = 0; g < kGroups; ++g) s += part_s[g * a.D + i];
+    a.part[(size_t)blockIdx.x * a.D + i] = s;
+  }
+}
+
 // ----------------------------------------------------------------- dispatch
 template <typename F>
 cudaError_t allow_smem(F kernel, size_t smem) {
@@ -533,14 +763,79 @@ cudaError_t bwd_by_width(RmsArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
+// Two rows on their way to a warp or block where they fit, and as many blocks an SM as
+// shared memory and 64 registers a thread leave room for.
+struct OddPlan {
+  int stages, blocks;
+  size_t smem;
+};
+inline OddPlan odd_plan(long long rows, int D, int size, int n_in, int TB, int LPR, bool join) {
+  OddPlan p;
+  const size_t one = (size_t)(TB / LPR) * n_in * odd_span(D, size);
+  p.stages = 2 * one <= 200 * 1024 ? 2 : 1;
+  p.smem = p.stages * one;
+  const size_t sums = join ? (size_t)(TB / LPR) * D * sizeof(float) : 0;
+  if (p.smem < sums) p.smem = sums;
+  int per_sm = (int)(220 * 1024 / (p.smem + 1024));
+  if (per_sm > 1024 / TB) per_sm = 1024 / TB;
+  if (per_sm < 1) per_sm = 1;
+  p.blocks = blocks_for((rows + TB / LPR - 1) / (TB / LPR), per_sm);
+  return p;
+}
+template <typename IO, bool OUT8, int TB, int LPR, int NV>
+cudaError_t run_fwd_odd(const RmsArgs& a, cudaStream_t s) {
+  const OddPlan p = odd_plan(a.rows, a.D, sizeof(IO), a.add ? 2 : 1, TB, LPR, false);
+  const auto kernel = rms_fwd_odd_kernel<IO, OUT8, TB, LPR, NV>;
+  const cudaError_t e = allow_smem(kernel, p.smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<p.blocks, TB, p.smem, s>>>(a, p.stages);
+  return cudaGetLastError();
+}
+template <typename IO, int TB, int LPR, int NV>
+cudaError_t run_bwd_odd(RmsArgs& a, cudaStream_t s) {
+  OddPlan p = odd_plan(a.rows, a.D, sizeof(IO), a.add ? 3 : 2, TB, LPR, LPR <= 32);
+  if (p.blocks > a.parts) p.blocks = a.parts;
+  const auto kernel = rms_bwd_odd_kernel<IO, TB, LPR, NV>;
+  const cudaError_t e = allow_smem(kernel, p.smem);
+  if (e != cudaSuccess) return e;
+  a.parts = p.blocks;
+  kernel<<<p.blocks, TB, p.smem, s>>>(a, p.stages);
+  return cudaGetLastError();
+}
+// The widest rows that these kernels hold.
+constexpr int kOddMost = 16384;
+template <typename IO, bool OUT8>
+cudaError_t fwd_odd(const RmsArgs& a, cudaStream_t s) {
+  const int D = a.D;
+  if (D <= 128) return run_fwd_odd<IO, OUT8, 256, 32, 4>(a, s);
+  if (D <= 512) return run_fwd_odd<IO, OUT8, 256, 32, 16>(a, s);
+  if (D <= 1024) return run_fwd_odd<IO, OUT8, 64, 64, 16>(a, s);
+  if (D <= 2048) return run_fwd_odd<IO, OUT8, 128, 128, 16>(a, s);
+  if (D <= 4096) return run_fwd_odd<IO, OUT8, 256, 256, 16>(a, s);
+  if (D <= 8192) return run_fwd_odd<IO, OUT8, 512, 512, 16>(a, s);
+  return run_fwd_odd<IO, OUT8, 1024, 1024, 16>(a, s);
+}
+template <typename IO>
+cudaError_t bwd_odd(RmsArgs& a, cudaStream_t s) {
+  const int D = a.D;
+  if (D <= 128) return run_bwd_odd<IO, 256, 32, 4>(a, s);
+  if (D <= 512) return run_bwd_odd<IO, 256, 32, 16>(a, s);
+  if (D <= 1024) return run_bwd_odd<IO, 64, 64, 16>(a, s);
+  if (D <= 2048) return run_bwd_odd<IO, 128, 128, 16>(a, s);
+  if (D <= 4096) return run_bwd_odd<IO, 256, 256, 16>(a, s);
+  if (D <= 8192) return run_bwd_odd<IO, 512, 512, 16>(a, s);
+  return run_bwd_odd<IO, 1024, 1024, 16>(a, s);
+}
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 template <typename IO, bool OUT8>
 cudaError_t launch_fwd_rows(const RmsArgs& a, cudaStream_t s) {
   constexpr int kVec = 16 / sizeof(IO);
   // (8-bit outputs are stored in vectors of kVec bytes)
-  const bool vec = a.D % kVec == 0 && aligned16(a.x) && aligned16(a.add) && aligned16(a.h) && aligned16(a.y);
-  if (vec) return fwd_by_width<IO, OUT8, kVec>(a, s);
+  const bool aligned = aligned16(a.x) && aligned16(a.add) && aligned16(a.h) && aligned16(a.y);
+  if (aligned && a.D % kVec == 0) return fwd_by_width<IO, OUT8, kVec>(a, s);
+  if (aligned && a.D <= kOddMost) return fwd_odd<IO, OUT8>(a, s);  // (groups of columns divide the width)
   if (OUT8 && a.group != 0) {  // groups across warps: the kernel that reads again
     rms_fwd_long_kernel<IO, OUT8><<<blocks_for(a.rows, 2), 1024, 0, s>>>(a);
     return cudaGetLastError();
@@ -552,8 +847,10 @@ cudaError_t launch_bwd_rows(RmsArgs a, cudaStream_t s) {
   constexpr int kVec = 16 / sizeof(IO);
   cudaError_t e = cudaSuccess;
   if (a.rows > 0) {
-    const bool vec = a.D % kVec == 0 && aligned16(a.x) && aligned16(a.dy) && aligned16(a.add) && aligned16(a.y);
-    e = vec ? bwd_by_width<IO, kVec>(a, s) : bwd_by_width<IO, 1>(a, s);
+    const bool aligned = aligned16(a.x) && aligned16(a.dy) && aligned16(a.add) && aligned16(a.y);
+    e = aligned && a.D % kVec == 0    ? bwd_by_width<IO, kVec>(a, s)
+        : aligned && a.D <= kOddMost ? bwd_odd<IO>(a, s)
+                                     : bwd_by_width<IO, 1>(a, s);
     if (e != cudaSuccess) return e;
   }
   if (a.part) {
