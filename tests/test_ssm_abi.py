@@ -106,7 +106,7 @@ def test_scan_bwd(L, bad, code):
     assert scan(L, "bwd", **bad) == code
 
 
-@pytest.mark.parametrize("bad,code", COMMON + [(dict(y=None), BAD)])
+@pytest.mark.parametrize("bad,code", COMMON + [(dict(y=None), BAD), (dict(B=(1 << 30) + 1, D=1, ldx=1, lddt=1), UNS)])
 def test_scan_step(L, bad, code):
     bad = {k: v for k, v in bad.items() if k != "dz"}
     assert scan(L, "step", **bad) == code
