@@ -21,8 +21,8 @@
 // a second kernel.  No atomics: the same bits every time.
 //
 // Measured, bf16 with four taps, bias and silu: 24 packed prompts, 50,021 tokens of 4096
-// channels, 141 us, 87% of the copy bandwidth (8 channels a thread with the loads held in
-// registers 488, 4 channels 176, 2 channels 163); backward of 8 x 2048 tokens 101 us, 60%
+// channels, 138 us, 89% of the copy bandwidth (8 channels a thread with the loads held in
+// registers 488, 4 channels 176, 2 channels 163); backward of 8 x 2048 tokens 99 us, 61%
 // (458 in registers, 202 by groups of tokens in registers, 117 with checks in every token).
 // Odd channel counts go by single elements: 4 x 2048 tokens of 4095 in 41 us, 50%.
 #include "ckda_launch.cuh"

@@ -22,6 +22,8 @@
 
 namespace ckda {
 
+// Warps of a block, which do not meet: one or two instead leave 8 x 2048 tokens of 4096
+// channels of 16 states at 425 and 418 us for 417.
 constexpr int kScanWarps = 4;
 constexpr int kScanBlock = 32 * kScanWarps;
 constexpr int kScanChunk = 4;  // tokens between the states that the backward pass keeps

@@ -4,15 +4,15 @@
 // What bounds it: N exponentials for every channel of every token, four fma-pipe
 // instructions of two states each beside every two of them, and the latency between them:
 // a warp holds 32 channels with all their states, so the card has few warps (1024 for
-// 8 x 2048 tokens of 4096 channels of 16 states, which take 418 us: fma pipe 53%,
-// exponentials 44%, issue 61% of the cycles at 3.4 warps a scheduler).  Memory is read and
+// 8 x 2048 tokens of 4096 channels of 16 states, which take 414 us: fma pipe 41%,
+// exponentials 36%, issue 48% of the cycles at 1.7 warps a scheduler).  Memory is read and
 // written once, 81 us of that.
 //
 // Rows with fewer channels than the card has room for are cut into pieces that run side by
 // side: a first pass leaves each piece's own end state and the sum of its steps (a state
 // decays over a piece by exp(A sum delta)), a scan over the pieces gives the states that
 // enter them, and the second pass runs every piece from its own.  (Three packed documents
-// of 32,768 tokens of 2048 channels: 556 us, 230 of them the first pass.)
+// of 32,768 tokens of 2048 channels: 556 us, 217 of them the first pass.)
 #include "ckda_scan.cuh"
 
 namespace ckda {

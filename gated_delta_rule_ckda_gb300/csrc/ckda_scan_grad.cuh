@@ -22,16 +22,15 @@
 // sums over a lane's channels, then over the other lanes of the warp; a warp's parts go
 // through the workspace and are added in a fixed order, as are dA's, dD's and ddt_bias's.
 //
-// Bound, like the forward pass, by fma and exponentials on few warps (254 registers leave
-// two to a scheduler): 4 x 2048 tokens of 4096 channels of 16 states take 1185 us, 273 of
-// them the walk, 850 the gradients (issue 45% of the cycles, fma pipe 35%), 36 the sums of
+// Bound, like the forward pass, by fma and exponentials on few warps (255 registers leave
+// two to a scheduler): 4 x 2048 tokens of 4096 channels of 16 states take 1235 us, 273 of
+// them the walk, 900 the gradients (issue 43% of the cycles, fma pipe 34%), 36 the sums of
 // dB's and dC's parts; memory 71.  Chunks of 8 tokens, half of them run forward twice,
 // took 1350; three blocks an SM with 0.9 KB of a thread's registers in local memory 1620.
 #pragma once
 #include "ckda_scan.cuh"
 
 namespace ckda {
-
 
 struct ScanBwdArgs {
   ScanArgs a;
@@ -107,7 +106,7 @@ struct GradGroups {  // B and C of a tile, MOST states
 
 // MOST: states, padded; in slices of S::NP.
 template <typename IO, typename S, int MOST, bool VEC>
-__global__ void __launch_bounds__(kScanBlock, 2) scan_grad_kernel(ScanBwdArgs b) {
+__global__ void __launch_bounds__(kScanBlock, 8 / kScanWarps) scan_grad_kernel(ScanBwdArgs b) {
   constexpr int LP = S::kLanes, NS = S::kStates, NP = S::NP, kPairs = NS / 2, kGroups = 32 / LP;
   constexpr int kSlices = MOST / NP;
   static_assert(NS == 4, "a lane's states of a channel are one vector");

@@ -195,3 +195,53 @@ def rms_tol(dt, width):
 
 
 far = linear_ref.far
+
+
+def smoke_error(ck, dev):
+    """Largest rms error over tolerance of a small convolution, scan and norm, their gradients
+    and a step each, times the bf16 tolerance of an output of the norm."""
+    gen = torch.Generator().manual_seed(17)
+    B, T, D, W, N = 2, 70, 64, 4, 16
+    mk = lambda *s: torch.randn(*s, generator=gen)  # noqa: E731
+    x, u, dt, z, dy, b, c = (mk(B, T, n).to(BF) for n in (D, D, D, D, D, N, N))
+    w, A, skip, h0 = 1 + 0.1 * mk(D), -mk(D, N).abs(), mk(D), mk(B, D, N)
+    cw, cb, c0 = 0.5 * mk(D, W), 0.1 * mk(D), mk(B, W - 1, D).to(BF)
+    g = lambda *v: [t.to(dev) for t in v]  # noqa: E731
+    worst = []
+
+    def compare(got, want, tol):
+        worst.append(far(got, want)[0] / tol)
+
+    y, h, rstd = ck.rmsnorm_fwd(*g(x, w, u))
+    compare(y, rms(h, w, 1e-5)[0], rms_tol(BF, D))
+    dx, dw = ck.rmsnorm_bwd(dy.to(dev), h, rstd, w.to(dev), u.to(dev))
+    want = rms_bwd(dy, h, rms(h, w, 1e-5)[1], w, u)
+    compare(dx, want[0], 2 * rms_tol(BF, D))
+    compare(dw, want[1], sum_tol(F32, T, B * T))
+
+    y, hT = ck.conv_fwd(*g(x, cw, cb, c0))
+    grads = ck.conv_bwd(*g(dy, x, cw, cb, c0))
+    want = conv(x, cw, cb, c0, dy=dy)
+    compare(y, want[0], conv_tol(BF, W))
+    compare(hT, want[1], U[BF])
+    for got, n in zip(grads, ("dx", "dw", "db", "dh0")):
+        compare(got, want[2][n], 2 * conv_tol(got.dtype, W) + 2 * T ** 0.5 * U[F32])
+    state = hT.clone()
+    one = conv(x[:, -1:], cw, cb, hT)
+    compare(ck.conv_decode_step(*g(x[:, -1], cw), state, cb.to(dev)), one[0][:, 0], conv_tol(BF, W))
+    compare(state, one[1], U[BF])
+
+    y, hT = ck.scan_fwd(*g(x, dt, A, b, c, skip, z), h0=h0.to(dev))
+    grads = ck.scan_bwd(*g(dy, x, dt, A, b, c, skip, z), h0=h0.to(dev))
+    want = scan(x, dt, A, b, c, skip, z, h0=h0, dy=dy)
+    compare(y, want[0], scan_tol(BF, T))
+    compare(hT, want[1], scan_tol(F32, T))
+    for got, n in zip(grads, ("dx", "ddt", "dA", "dB", "dC", "dD", "dz", "", "dh0")):
+        if n:
+            compare(got, want[2][n], sum_tol(got.dtype, T, B * T))
+    state = hT.clone()
+    one = scan(*(t[:, -1:] for t in (x, dt)), A, *(t[:, -1:] for t in (b, c)), skip, z[:, -1:], h0=hT)
+    got = ck.scan_decode_step(*g(x[:, -1], dt[:, -1], A, b[:, -1], c[:, -1]), state, *g(skip, z[:, -1]))
+    compare(got, one[0][:, 0], scan_tol(BF, 1))
+    compare(state, one[1], scan_tol(F32, 1))
+    return max(worst) * rms_tol(BF, D)

@@ -200,6 +200,33 @@ def test_wide_rows_in_place(ck, width):
     assert torch.equal(y, want[0]) and torch.equal(h, want[1])
 
 
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("rows,width", [(3001, 127), (1501, 301), (701, 1031), (333, 4853)])
+def test_odd_rows_in_place(ck, dt, rows, width):
+    """Rows that share 16-byte vectors with their neighbours, in place, and what lies behind
+    the last one."""
+    s = make(rows, width, dt, F32, 5)
+    c = {k: v.cuda() for k, v in s.items()}
+    n = rows * width
+
+    def framed(t):
+        buf = torch.full((n + 64,), 7.0, dtype=dt, device="cuda")
+        buf[:n] = t.flatten()
+        return buf, buf[:n].view(rows, width)
+
+    want = ck.rmsnorm_fwd(c["x"], c["w"], residual=c["res"])
+    (bx, x), (br, res) = framed(c["x"]), framed(c["res"])
+    y, h, rstd = ck.rmsnorm_fwd(x, c["w"], residual=res, y=x, h=res)
+    assert torch.equal(y, want[0]) and torch.equal(h, want[1]) and torch.equal(rstd, want[2])
+    assert (bx[n:] == 7).all() and (br[n:] == 7).all()
+    grad = ck.rmsnorm_bwd(c["dy"], want[1], want[2], c["w"], dh=c["dh"])
+    for name in ("dy", "dh", "h"):
+        t = {"dy": c["dy"], "dh": c["dh"], "h": want[1]}
+        buf, t[name] = framed(t[name])
+        dx, dw = ck.rmsnorm_bwd(t["dy"], t["h"], want[2], c["w"], dh=t["dh"], dx=t[name])
+        assert torch.equal(dx, grad[0]) and torch.equal(dw, grad[1]) and (buf[n:] == 7).all()
+
+
 def test_no_rows(ck):
     x = torch.empty(0, 64, device="cuda")
     y, h, rstd = ck.rmsnorm_fwd(x)
