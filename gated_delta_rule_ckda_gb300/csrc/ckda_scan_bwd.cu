@@ -13,8 +13,13 @@ struct Layout {
 Layout layout_of(int rows, int T, int D, int N, int G) {
   Layout w{};
   // Room for 24 warps an SM, three times what runs at once: the batch of 512 warps takes
-  // 1206 us so, 1274 with 8, 1267 with 16, 1233 with 32.
-  scan_pieces(rows, T, D, G, 24 * kSms, &w.pieces, &w.len);
+  // 1206 us so, 1274 with 8, 1267 with 16, 1233 with 32.  Pieces of at least 32 tokens: 2 x
+  // 1001 tokens of 480 channels of 12 states take 83 us, with 64 101, with 16 116; 100 of
+  // 2048 of 16 states 64, with 64 91.  More than 16 states leave fewer warps at once and
+  // have more to take up and leave at a piece's ends: 4096 tokens of 512 channels of 64
+  // states take 607 us by 64, by 32 724.
+  const int least = N <= 16 ? 32 : 64;
+  scan_pieces(rows, T, D, G, 24 * kSms, least, least, &w.pieces, &w.len);
   w.chunks = (T + kScanChunk - 1) / kScanChunk;
   const size_t dn = (size_t)D * N * 4, d = (size_t)D * 4, units = (size_t)rows * w.pieces;
   const bool many = w.pieces > 1;

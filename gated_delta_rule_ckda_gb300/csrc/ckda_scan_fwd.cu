@@ -12,7 +12,7 @@
 // side: a first pass leaves each piece's own end state and the sum of its steps (a state
 // decays over a piece by exp(A sum delta)), a scan over the pieces gives the states that
 // enter them, and the second pass runs every piece from its own.  (Three packed documents
-// of 32,768 tokens of 2048 channels: 556 us, 217 of them the first pass.)
+// of 32,768 tokens of 2048 channels: 543 us, 217 of them the first pass.)
 #include "ckda_scan.cuh"
 
 namespace ckda {
@@ -78,10 +78,12 @@ cudaError_t launch_io(const ScanArgs& a, cudaStream_t s) {
   return scan_vectors(a, sizeof(IO)) ? by_states<IO, true>(a, s) : by_states<IO, false>(a, s);
 }
 
-// Room for 12 warps an SM: the documents take 884 us with 8, 557 with 12, 562 with 16; the
-// batch, 1024 warps in one piece, 418, and 631 in two, which 16 would allow.
+// Room for 12 warps an SM: the documents take 884 us with 8, 543 with 12, 562 with 16; the
+// batch, 1024 warps in one piece, 418, and 631 in two, which 16 would allow.  Rows of up to
+// 128 tokens stay whole: 100 tokens of 2048 channels take 28 us, cut 35 like every number up
+// to 300, which take 46 in pieces of 128.
 void pieces_of(int rows, int T, int D, int G, int* pieces, int* len) {
-  scan_pieces(rows, T, D, G, 12 * kSms, pieces, len);
+  scan_pieces(rows, T, D, G, 12 * kSms, 64, 128, pieces, len);
 }
 
 inline size_t state_bytes(int rows, int pieces, int D, int N) {
@@ -95,16 +97,16 @@ cudaError_t launch_scan_join(bool next, const ScanArgs& a, cudaStream_t s) {
   return launch_next(next, scan_join_kernel, (unsigned)((n + 255) / 256), 256, 0, s, a);
 }
 
-void scan_pieces(int rows, int T, int D, int G, int room, int* pieces, int* len) {
+void scan_pieces(int rows, int T, int D, int G, int room, int least, int whole, int* pieces, int* len) {
   const long long units = (long long)rows * scan_chan_blocks(D, G);
   int n = 1;
-  if (2 * units <= room) {
+  if (2 * units <= room && T > whole) {
     n = (int)(room / units);
-    const int most = (T + 63) / 64;
-    if (n > most) n = most < 1 ? 1 : most;
+    const int most = (T + least - 1) / least;
+    if (n > most) n = most;
   }
-  const int each = ((T + n - 1) / n + 63) / 64 * 64;  // whole tiles
-  *len = each > 0 ? each : 64;
+  const int each = ((T + n - 1) / n + kWalkTile - 1) / kWalkTile * kWalkTile;
+  *len = each > 0 ? each : kWalkTile;
   *pieces = T > 0 ? (T + *len - 1) / *len : 1;
 }
 

@@ -152,6 +152,19 @@ def test_one_wide_batch(ck):
     compare(ck, make(40, 33, 520, 16, BF, h0=False))
 
 
+@pytest.mark.parametrize("D,N,dt,h0", [(520, 16, BF, True), (512, 8, F32, False)])
+def test_wide_batch_of_longer_rows(ck, D, N, dt, h0):
+    """Channels that fill the card: one piece a row in the backward pass too."""
+    compare(ck, make(116, 45, D, N, dt, h0=h0))
+
+
+@pytest.mark.parametrize("N,dt,D", [(16, BF, 32), (12, F32, 24), (5, BF, 9)])
+def test_short_pieces(ck, N, dt, D):
+    """Borders at and beside 32 tokens, the least of a piece in the backward pass."""
+    compare(ck, make(1, 160, D, N, dt, cu=[0, 31, 32, 33, 96, 96, 127, 160]))
+    compare(ck, make(2, 65, D, N, dt, h0=True))
+
+
 def test_part_of_a_projection(ck):
     s = make(2, 45, 64, 16, BF, G=2)
     c = cuda(s)
