@@ -148,7 +148,7 @@ def test_many_sequences(ck, lengths):
 
 
 def test_one_wide_batch(ck):
-    """More blocks than the card runs at once: one piece a row."""
+    """More blocks than the card runs at once: one piece a row forward, two backward."""
     compare(ck, make(40, 33, 520, 16, BF, h0=False))
 
 
