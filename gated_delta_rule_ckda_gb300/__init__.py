@@ -145,8 +145,9 @@ def lib():
             L.ckda_layernorm_bwd.argtypes = [vp] * 8 + [ctypes.c_longlong, i32, i32, i32, vp, sz,
                                                         vp]
             i64 = ctypes.c_longlong
-            L.ckda_conv_fwd.restype = i32
-            L.ckda_conv_fwd.argtypes = [vp] * 7 + [i32] * 5 + [i64] + [i32] * 3 + [vp]
+            for fn in (L.ckda_conv_fwd, L.ckda_conv_fwd_filled):
+                fn.restype = i32
+                fn.argtypes = [vp] * 7 + [i32] * 5 + [i64] + [i32] * 3 + [vp]
             L.ckda_conv_bwd_workspace_bytes.restype = sz
             L.ckda_conv_bwd_workspace_bytes.argtypes = [i32] * 4
             L.ckda_conv_bwd.restype = i32
@@ -1042,7 +1043,9 @@ def conv_fwd(x, weight, bias=None, h0=None, cu_seqlens=None, silu=True, store_fi
 
     x [B, T, D] (it may be a part of a wider projection's last axis), weight [D, W] with
     W = 2, 3 or 4 and bias [D] in bf16 or fp32, h0, hT [N, W - 1, D] in x's type: the inputs
-    before the first token and the last ones.  Returns (y, hT or None)."""
+    before the first token and the last ones.  Packed sequences may end before T: rows behind
+    the last one are not read, and zero in y (a y that is given keeps its own there).
+    Returns (y, hT or None)."""
     if stream is not None:
         return _on_stream(conv_fwd, locals())
     L = lib()
@@ -1052,24 +1055,27 @@ def conv_fwd(x, weight, bias=None, h0=None, cu_seqlens=None, silu=True, store_fi
     N, nseq = _sequences(B, cu_seqlens, device)
     if h0 is not None:
         _check(h0, "h0", dt, (N, W - 1, D), device)
+    call = L.ckda_conv_fwd
     if y is None:
         y = _like(x)
+        if nseq:
+            call = L.ckda_conv_fwd_filled
     else:
         _check(y, "y", dt, (B, T, D), device)
     if hT is not None:
         _check(hT, "hT", dt, (N, W - 1, D), device)
     elif store_final_state:
         hT = _like(x, (N, W - 1, D))
-    _call(L.ckda_conv_fwd, "ckda_conv_fwd", device, x.data_ptr(), weight.data_ptr(), _addr(bias),
-          _addr(h0), y.data_ptr(), _addr(hT), _addr(cu_seqlens), nseq, B, T, D, W, ldx, io, code,
-          int(silu))
+    _call(call, "ckda_conv_fwd", device, x.data_ptr(), weight.data_ptr(), _addr(bias), _addr(h0),
+          y.data_ptr(), _addr(hT), _addr(cu_seqlens), nseq, B, T, D, W, ldx, io, code, int(silu))
     return y, hT
 
 
 def conv_bwd(dy, x, weight, bias=None, h0=None, dhT=None, cu_seqlens=None, silu=True,
              store_dh0=True, workspace=None, stream=None):
     """Backward of conv_fwd (ckda_conv_bwd): gradients of sum <y, dy> + <hT, dhT>.  Returns
-    (dx, dweight, dbias or None, dh0 or None); the weights' have the weights' type."""
+    (dx, dweight, dbias or None, dh0 or None); the weights' have the weights' type; dx is zero
+    in rows behind the last packed sequence."""
     if stream is not None:
         return _on_stream(conv_bwd, locals())
     L = lib()

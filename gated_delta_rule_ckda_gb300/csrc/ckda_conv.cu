@@ -53,6 +53,7 @@ struct ConvArgs {
   long long tokens;
   int seqs, T, D;  // T: of a dense row
   int w_bf16, silu;
+  int fill;        // rows of y behind the last sequence become zero
   int run;         // tokens of a run
   int lanes;       // threads of a token, a power of two
   int chan_blocks, parts;
@@ -172,6 +173,14 @@ struct Taps {
     return p;
   }
 };
+
+// Rows of y behind the last sequence, [from, to): zero.  (What nothing writes could be
+// anything, and a NaN there reaches every weight of a layer that takes all rows.)
+template <typename IO, int VEC>
+__device__ __forceinline__ void zero_rows(const ConvArgs& a, long long from, long long to, int c) {
+  const float none[VEC] = {};
+  for (; from < to; ++from) store_vec<IO, VEC>(a.y, from * a.D + c, none);
+}
 
 // Row i of the inputs before a sequence's token m: i = 0 is W - 1 tokens back.
 template <typename IO, int W, int VEC>
@@ -300,10 +309,12 @@ __global__ void __launch_bounds__(kBlock) conv_fwd_kernel(ConvArgs a) {
   const int lane = threadIdx.x % a.lanes, grp = threadIdx.x / a.lanes;
   const int c = (chan * a.lanes + lane) * VEC;
   long long m = (tok * (kBlock / a.lanes) + grp) * a.run;
-  long long stop = m + a.run;
+  long long stop = m + a.run < a.tokens ? m + a.run : a.tokens;
   const long long last = a.cu ? offset_of(a, a.seqs) : a.tokens;
+  if (c >= a.D) return;
+  if (a.fill) zero_rows<IO, VEC>(a, m > last ? m : last, stop, c);
   if (stop > last) stop = last;
-  if (c >= a.D || m >= stop) return;
+  if (m >= stop) return;
   Taps<W, VEC> taps;
   taps.load(a, c);
   while (m < stop) {  // the run's part of one sequence after another
@@ -392,7 +403,9 @@ __global__ void __launch_bounds__(kBlock, 2) conv_bwd_kernel(ConvArgs a) {
   const int c = (chan * a.lanes + lane) * VEC;
   const long long last = a.cu ? offset_of(a, a.seqs) : a.tokens;
   long long m = (tok * groups + grp) * a.run;
-  long long stop = m + a.run < last ? m + a.run : last;
+  long long stop = m + a.run < a.tokens ? m + a.run : a.tokens;
+  if (c < a.D) zero_rows<IO, VEC>(a, m > last ? m : last, stop, c);
+  if (stop > last) stop = last;
   using V = typename Chans<VEC>::V;
   constexpr int kN = Chans<VEC>::kN;
   Chans<VEC> dw[W], db;
@@ -667,17 +680,9 @@ inline bool overlap(const void* p, size_t n, const void* q, size_t m) {
   return p && q && a < b + m && b < a + n;
 }
 
-}  // namespace
-}  // namespace ckda
-
-using namespace ckda;
-
-extern "C" {
-
-ckda_status ckda_conv_fwd(const void* x, const void* weight, const void* bias, const void* h0,
-                          void* y, void* hT, const int32_t* cu_seqlens, int num_seqs, int B, int T,
-                          int D, int W, long long ldx, ckda_dtype io_dtype, ckda_dtype weight_dtype,
-                          int silu, void* stream) {
+ckda_status forward(const void* x, const void* weight, const void* bias, const void* h0, void* y, void* hT,
+                    const int32_t* cu_seqlens, int num_seqs, int B, int T, int D, int W, long long ldx,
+                    ckda_dtype io_dtype, ckda_dtype weight_dtype, int silu, bool fill, void* stream) {
   const ckda_status st = check_conv(B, T, D, W, ldx, io_dtype, weight_dtype);
   if (st != CKDA_OK) return st;
   if (cu_seqlens && (num_seqs < 1 || B != 1)) return CKDA_ERR_INVALID_ARG;
@@ -691,8 +696,30 @@ ckda_status ckda_conv_fwd(const void* x, const void* weight, const void* bias, c
   ConvArgs a{};
   a.x = x; a.w = weight; a.b = bias; a.h0 = h0; a.y = y; a.hT = hT; a.cu = cu_seqlens;
   a.ldx = ldx; a.tokens = (long long)B * T; a.seqs = seqs; a.T = T; a.D = D;
-  a.w_bf16 = weight_dtype == CKDA_BF16; a.silu = silu != 0;
+  a.w_bf16 = weight_dtype == CKDA_BF16; a.silu = silu != 0; a.fill = fill;
   return launch(a, W, io_dtype, Call::kFwd, stream);
+}
+
+}  // namespace
+}  // namespace ckda
+
+using namespace ckda;
+
+extern "C" {
+
+ckda_status ckda_conv_fwd(const void* x, const void* weight, const void* bias, const void* h0,
+                          void* y, void* hT, const int32_t* cu_seqlens, int num_seqs, int B, int T,
+                          int D, int W, long long ldx, ckda_dtype io_dtype, ckda_dtype weight_dtype,
+                          int silu, void* stream) {
+  return forward(x, weight, bias, h0, y, hT, cu_seqlens, num_seqs, B, T, D, W, ldx, io_dtype, weight_dtype,
+                 silu, false, stream);
+}
+ckda_status ckda_conv_fwd_filled(const void* x, const void* weight, const void* bias, const void* h0,
+                                 void* y, void* hT, const int32_t* cu_seqlens, int num_seqs, int B, int T,
+                                 int D, int W, long long ldx, ckda_dtype io_dtype, ckda_dtype weight_dtype,
+                                 int silu, void* stream) {
+  return forward(x, weight, bias, h0, y, hT, cu_seqlens, num_seqs, B, T, D, W, ldx, io_dtype, weight_dtype,
+                 silu, true, stream);
 }
 
 size_t ckda_conv_bwd_workspace_bytes(int B, int T, int D, int W) {

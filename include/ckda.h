@@ -596,8 +596,9 @@ ckda_status ckda_layernorm_bwd(const void *dy, const void *x, const float *mean,
  *   h0, hT     : io [N, W - 1, D], the inputs before a sequence's first token and its
  *                last W - 1 inputs (older ones from h0 where it is shorter), oldest
  *                first; NULL: zero, not stored.  An empty sequence hands h0 on.
- *   cu_seqlens, num_seqs: as ckda_fwd (packed sequences, B = 1, N = num_seqs); tokens
- *                behind the last sequence are left as they were.
+ *   cu_seqlens, num_seqs: as ckda_fwd (packed sequences, B = 1, N = num_seqs), but
+ *                cu_seqlens[num_seqs] may be less than T: tokens behind the last sequence
+ *                are not read, and left as they were in y.
  *
  * hT must not overlap h0, nor y x (checked).  Arithmetic in fp32, one rounding.
  * T = 0 hands the states on.  A token that is not finite reaches only the W tokens of its
@@ -607,10 +608,17 @@ ckda_status ckda_conv_fwd(const void *x, const void *weight, const void *bias, c
                           void *y, void *hT, const int32_t *cu_seqlens, int num_seqs, int B,
                           int T, int D, int W, long long ldx, ckda_dtype io_dtype,
                           ckda_dtype weight_dtype, int silu, void *stream);
+/* The same; rows of y behind the last sequence become zero. */
+ckda_status ckda_conv_fwd_filled(const void *x, const void *weight, const void *bias,
+                                 const void *h0, void *y, void *hT, const int32_t *cu_seqlens,
+                                 int num_seqs, int B, int T, int D, int W, long long ldx,
+                                 ckda_dtype io_dtype, ckda_dtype weight_dtype, int silu,
+                                 void *stream);
 
 /*
  * Its backward: the gradients of sum <y, dy> + <hT, dhT>.
- *   dy, dx   : io [B, T, D]; dx overlaps neither x nor dy (checked)
+ *   dy, dx   : io [B, T, D]; dx overlaps neither x nor dy (checked); its rows behind the
+ *              last sequence become zero
  *   dhT, dh0 : io [N, W - 1, D] or NULL (zero, not stored); dh0 overlaps neither h0 nor
  *              dhT (checked)
  *   dweight  : weight_dtype [D, W]; dbias [D] or NULL (not wanted); from fp32 sums in a
