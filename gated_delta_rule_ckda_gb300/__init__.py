@@ -156,8 +156,9 @@ def lib():
             L.ckda_conv_decode_step.argtypes = [vp] * 5 + [i32] * 3 + [i64] + [i32] * 3 + [vp]
             for fn in (L.ckda_scan_fwd_workspace_bytes, L.ckda_scan_bwd_workspace_bytes):
                 fn.restype, fn.argtypes = sz, [i32] * 5
-            L.ckda_scan_fwd.restype = i32
-            L.ckda_scan_fwd.argtypes = [vp] * 12 + [i32] * 6 + [i64] * 5 + [i32] * 2 + [vp, sz, vp]
+            for fn in (L.ckda_scan_fwd, L.ckda_scan_fwd_filled):
+                fn.restype = i32
+                fn.argtypes = [vp] * 12 + [i32] * 6 + [i64] * 5 + [i32] * 2 + [vp, sz, vp]
             L.ckda_scan_bwd.restype = i32
             L.ckda_scan_bwd.argtypes = [vp] * 21 + [i32] * 6 + [i64] * 5 + [i32] * 2 + [vp, sz, vp]
             L.ckda_scan_decode_step.restype = i32
@@ -1156,7 +1157,8 @@ def scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, cu_seqlens=N
 
     x, dt, z [B, T, D]; B, C [B, T, N], or [B, T, G, N] with G dividing D; each may be a part
     of a wider projection's last axis.  A fp32 [D, N], N <= 64; D, dt_bias fp32 [D]; h0, hT
-    fp32 [sequences, D, N].  Returns (y, hT or None)."""
+    fp32 [sequences, D, N].  Packed sequences may end before T: rows behind the last one are
+    not read, and zero in y (a y that is given keeps its own there).  Returns (y, hT or None)."""
     if stream is not None:
         return _on_stream(scan_fwd, locals())
     L = lib()
@@ -1166,8 +1168,11 @@ def scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, cu_seqlens=N
     count, nseq = _sequences(rows, cu_seqlens, device)
     if h0 is not None:
         _check(h0, "h0", torch.float32, (count, width, N), device)
+    call = L.ckda_scan_fwd
     if y is None:
         y = _like(x)
+        if nseq:
+            call = L.ckda_scan_fwd_filled
     else:
         _check(y, "y", x.dtype, (rows, T, width), device)
     if hT is not None:
@@ -1180,7 +1185,7 @@ def scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, cu_seqlens=N
             workspace = torch.empty(size, dtype=torch.uint8, device=device)
     else:
         size = _given(workspace, device)
-    _call(L.ckda_scan_fwd, "ckda_scan_fwd", device, x.data_ptr(), dt.data_ptr(), A.data_ptr(),
+    _call(call, "ckda_scan_fwd", device, x.data_ptr(), dt.data_ptr(), A.data_ptr(),
           B.data_ptr(), C.data_ptr(), _addr(D), _addr(z), _addr(dt_bias), _addr(h0), y.data_ptr(),
           _addr(hT), _addr(cu_seqlens), nseq, rows, T, width, N, G, *apart, io, int(softplus),
           _addr(workspace), size)
@@ -1190,7 +1195,8 @@ def scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, cu_seqlens=N
 def scan_bwd(dy, x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, dhT=None, cu_seqlens=None,
              softplus=True, store_dh0=True, workspace=None, stream=None):
     """Backward of scan_fwd (ckda_scan_bwd): gradients of sum <y, dy> + <hT, dhT>.  Returns
-    (dx, ddt, dA, dB, dC, dD, dz, ddt_bias, dh0); those of what was not given are None."""
+    (dx, ddt, dA, dB, dC, dD, dz, ddt_bias, dh0); those of what was not given are None, those
+    by token zero in rows behind the last packed sequence."""
     if stream is not None:
         return _on_stream(scan_bwd, locals())
     L = lib()

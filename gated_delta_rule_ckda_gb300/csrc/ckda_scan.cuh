@@ -46,6 +46,7 @@ struct ScanArgs {
   long long ldx, lddt, ldb, ldc, ldz;  // elements from one token to the next
   int rows, T, D, N, G, seqs;
   int softplus;
+  int fill;               // rows of y behind the last sequence become zero
   int pieces, piece_len;  // of a row
   int chan_blocks;        // of all channels; per group chan_blocks / G
   float* state;           // [rows][pieces][D][N]: what a piece adds, then what enters it
@@ -339,6 +340,17 @@ __device__ __forceinline__ bool scan_place(const ScanArgs& a, ScanPlace& p) {
   p.t1 = p.t0 + a.piece_len < last ? p.t0 + a.piece_len : last;
   return true;
 }
+// A warp's part of a [rows][T][D] tensor behind the last sequence: zero.  (What nothing
+// writes could be anything, and a NaN there reaches every weight of a layer that takes all
+// rows.)
+template <typename IO>
+__device__ __forceinline__ void zero_behind(const ScanArgs& a, const ScanPlace& p, void* out) {
+  const int lane = threadIdx.x & 31;
+  const int end = p.t0 + a.piece_len < a.T ? p.t0 + a.piece_len : a.T;
+  if (lane < p.chans)
+    for (int t = p.t0 > p.t1 ? p.t0 : p.t1; t < end; ++t)
+      st_io(static_cast<IO*>(out) + ((long long)p.row * a.T + t) * a.D + p.c0 + lane, 0.f);
+}
 inline int scan_chan_blocks(int D, int G) { return G * ((D / G + kScanChans - 1) / kScanChans); }
 inline unsigned scan_grid(const ScanArgs& a) {
   return (unsigned)(((long long)a.rows * a.pieces * a.chan_blocks + kScanWarps - 1) / kScanWarps);
@@ -409,6 +421,7 @@ __global__ void __launch_bounds__(kScanBlock) scan_walk_kernel(ScanArgs a) {
   if (!scan_place(a, p)) return;
   const int lane = threadIdx.x & 31, n0 = lane % LP * NS;
   if (MODE == kOut && p.piece == 0 && a.hT && (a.cu || a.T == 0)) empty_states(a, p, a.h0, a.hT);
+  if (MODE == kOut && a.fill) zero_behind<IO>(a, p, a.y);
   if (p.t0 >= p.t1) return;
 
   constexpr bool kAsync = kScanAsync<IO, VEC>;

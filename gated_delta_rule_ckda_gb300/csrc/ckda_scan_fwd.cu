@@ -125,21 +125,21 @@ ckda_status check_scan(int rows, int T, int D, int N, int G, const int32_t* cu, 
 
 using namespace ckda;
 
-extern "C" {
-
-size_t ckda_scan_fwd_workspace_bytes(int B, int T, int D, int N, int G) {
+extern "C" size_t ckda_scan_fwd_workspace_bytes(int B, int T, int D, int N, int G) {
   if (B < 1 || T < 0 || D < 1 || N < 1 || G < 1 || D % G != 0) return 0;
   int pieces, len;
   pieces_of(B, T, D, G, &pieces, &len);
   return pieces > 1 ? state_bytes(B, pieces, D, N) + (size_t)B * pieces * D * 4 : 0;
 }
 
-ckda_status ckda_scan_fwd(const void* x, const void* dt, const float* A, const void* Bm, const void* C,
-                          const float* D_skip, const void* z, const float* dt_bias, const float* h0,
-                          void* y, float* hT, const int32_t* cu_seqlens, int num_seqs, int B, int T,
-                          int D, int N, int G, long long ldx, long long lddt, long long ldb,
-                          long long ldc, long long ldz, ckda_dtype io_dtype, int softplus,
-                          void* workspace, size_t workspace_bytes, void* stream) {
+namespace {
+
+ckda_status forward(const void* x, const void* dt, const float* A, const void* Bm, const void* C,
+                    const float* D_skip, const void* z, const float* dt_bias, const float* h0, void* y,
+                    float* hT, const int32_t* cu_seqlens, int num_seqs, int B, int T, int D, int N, int G,
+                    long long ldx, long long lddt, long long ldb, long long ldc, long long ldz,
+                    ckda_dtype io_dtype, int softplus, bool fill, void* workspace, size_t workspace_bytes,
+                    void* stream) {
   const ckda_status st = check_scan(B, T, D, N, G, cu_seqlens, num_seqs, io_dtype);
   if (st != CKDA_OK) return st;
   if (!A || (T > 0 && (!x || !dt || !Bm || !C || !y))) return CKDA_ERR_INVALID_ARG;
@@ -153,7 +153,7 @@ ckda_status ckda_scan_fwd(const void* x, const void* dt, const float* A, const v
   a.h0 = h0; a.y = y; a.hT = hT; a.cu = cu_seqlens;
   a.ldx = ldx; a.lddt = lddt; a.ldb = ldb; a.ldc = ldc; a.ldz = ldz;
   a.rows = B; a.T = T; a.D = D; a.N = N; a.G = G; a.seqs = cu_seqlens ? num_seqs : B;
-  a.softplus = softplus != 0;
+  a.softplus = softplus != 0; a.fill = fill;
   pieces_of(B, T, D, G, &a.pieces, &a.piece_len);
   if (a.pieces > 1) {
     if (!workspace || workspace_bytes < ckda_scan_fwd_workspace_bytes(B, T, D, N, G) || !scan_aligned(workspace, 16))
@@ -164,6 +164,29 @@ ckda_status ckda_scan_fwd(const void* x, const void* dt, const float* A, const v
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = io_dtype == CKDA_F32 ? launch_io<float>(a, s) : launch_io<__nv_bfloat16>(a, s);
   return e == cudaSuccess ? CKDA_OK : CKDA_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+ckda_status ckda_scan_fwd(const void* x, const void* dt, const float* A, const void* Bm, const void* C,
+                          const float* D_skip, const void* z, const float* dt_bias, const float* h0,
+                          void* y, float* hT, const int32_t* cu_seqlens, int num_seqs, int B, int T,
+                          int D, int N, int G, long long ldx, long long lddt, long long ldb,
+                          long long ldc, long long ldz, ckda_dtype io_dtype, int softplus,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  return forward(x, dt, A, Bm, C, D_skip, z, dt_bias, h0, y, hT, cu_seqlens, num_seqs, B, T, D, N, G, ldx, lddt,
+                 ldb, ldc, ldz, io_dtype, softplus, false, workspace, workspace_bytes, stream);
+}
+ckda_status ckda_scan_fwd_filled(const void* x, const void* dt, const float* A, const void* Bm, const void* C,
+                                 const float* D_skip, const void* z, const float* dt_bias, const float* h0,
+                                 void* y, float* hT, const int32_t* cu_seqlens, int num_seqs, int B, int T,
+                                 int D, int N, int G, long long ldx, long long lddt, long long ldb,
+                                 long long ldc, long long ldz, ckda_dtype io_dtype, int softplus,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+  return forward(x, dt, A, Bm, C, D_skip, z, dt_bias, h0, y, hT, cu_seqlens, num_seqs, B, T, D, N, G, ldx, lddt,
+                 ldb, ldc, ldz, io_dtype, softplus, true, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -136,6 +136,11 @@ __global__ void __launch_bounds__(kScanBlock, 8 / kScanWarps) scan_grad_kernel(S
     f[1] = make_float2(v.z, v.w);
   };
   if (p.piece == 0 && b.dh0 && (a.cu || a.T == 0)) empty_states(a, p, a.dhT, b.dh0);
+  if (a.cu) {
+    zero_behind<IO>(a, p, b.dx);
+    zero_behind<IO>(a, p, b.ddt);
+    if (a.z) zero_behind<IO>(a, p, b.dz);
+  }
   // Sums over a piece's tokens, in fp32: dD's and ddt_bias's over a tile, then with what the
   // addition to the rest rounded off carried along; dA's over kSumTiles tiles, then in memory.
   float dskip = 0.f, dbias = 0.f, lost_skip = 0.f, lost_bias = 0.f;
@@ -494,8 +499,8 @@ __global__ void __launch_bounds__(256) scan_sums_kernel(ScanBwdArgs b, long long
     if (i >= per) return;
     const long long tg = i / (2 * a.N);
     const int w = (int)(i % (2 * a.N)) / a.N, n = (int)(i % a.N);
-    if ((int)(tg / a.G % a.T) >= scan_last(a)) return;
-    const int blocks = a.chan_blocks / a.G;
+    // (behind the last sequence there are no parts, and the sum is zero)
+    const int blocks = (int)(tg / a.G % a.T) < scan_last(a) ? a.chan_blocks / a.G : 0;
     float s = 0.f;
 #pragma unroll 8
     for (int k = 0; k < blocks; ++k) s += b.part_bc[k * per + i];

@@ -656,7 +656,8 @@ ckda_status ckda_conv_decode_step(const void *x, const void *weight, const void 
  *                 h0 (checked), y no input
  *   ldx, lddt, ldb, ldc, ldz: elements from one token to the next (at least D, or G N)
  *   cu_seqlens, num_seqs: as ckda_fwd (packed sequences, B = 1); an empty sequence hands
- *                 its h0 on; tokens behind the last sequence are left as they were
+ *                 its h0 on.  cu_seqlens[num_seqs] may be less than T: tokens behind the
+ *                 last sequence are not read, and left as they were in y
  *
  * N <= 64.  States, steps and sums are fp32, one rounding to io.  N a multiple of 4, a
  * channel count per group that is a multiple of 8 (fp32: 4) and 16-byte aligned rows move
@@ -675,11 +676,20 @@ ckda_status ckda_scan_fwd(const void *x, const void *dt, const float *A, const v
                           int G, long long ldx, long long lddt, long long ldb, long long ldc,
                           long long ldz, ckda_dtype io_dtype, int softplus, void *workspace,
                           size_t workspace_bytes, void *stream);
+/* The same; rows of y behind the last sequence become zero. */
+ckda_status ckda_scan_fwd_filled(const void *x, const void *dt, const float *A, const void *Bm,
+                                 const void *C, const float *D_skip, const void *z,
+                                 const float *dt_bias, const float *h0, void *y, float *hT,
+                                 const int32_t *cu_seqlens, int num_seqs, int B, int T, int D,
+                                 int N, int G, long long ldx, long long lddt, long long ldb,
+                                 long long ldc, long long ldz, ckda_dtype io_dtype, int softplus,
+                                 void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * Its backward: the gradients of sum <y, dy> + <hT, dhT>.
  *   dy, dx, ddt, dz : io   [B, T, D] (dz NULL exactly where z is)
  *   dBm, dC         : io   [B, T, G, N], summed over the group's channels
+ *                     (rows of all of these behind the last sequence become zero)
  *   dA              : fp32 [D, N]; dD_skip, ddt_bias fp32 [D] or NULL (not wanted)
  *   dhT, dh0        : fp32 [sequences, D, N] or NULL (zero, not stored), not overlapping
  *                     (checked)
