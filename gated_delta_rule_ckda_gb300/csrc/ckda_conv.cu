@@ -494,9 +494,14 @@ __global__ void __launch_bounds__(kBlock, 2) conv_bwd_kernel(ConvArgs a) {
     for (int i = threadIdx.x; i < a.lanes * VEC; i += kBlock) {
       const int at = chan * a.lanes * VEC + i;
       if (at >= a.D) continue;
-      float t = 0.f;
-      for (int g = 0; g < groups; ++g) t += sum[g * a.lanes + i / VEC][i % VEC];
-      a.part[((size_t)tok * (W + 1) + j) * a.D + at] = t;
+      CarriedSum t;  // (eight at a time: one by one the call took 104 us for 102)
+      for (int g0 = 0; g0 < groups; g0 += 8) {
+        float few = 0.f;
+#pragma unroll
+        for (int g = 0; g < 8; ++g) few += sum[(g0 + g) * a.lanes + i / VEC][i % VEC];
+        t.add(few);
+      }
+      a.part[((size_t)tok * (W + 1) + j) * a.D + at] = t.sum;
     }
   }
 }
@@ -509,22 +514,22 @@ __global__ void __launch_bounds__(1024) conv_weight_grad_kernel(ConvArgs a) {
   __shared__ float s[32][33];
   const int c = threadIdx.x & 31, g = threadIdx.x >> 5, j = blockIdx.y;
   const int i = blockIdx.x * 32 + c;
-  float t = 0.f;
+  CarriedSum t;
   if (i < a.D)
 #pragma unroll 8
-    for (int r = g; r < a.parts; r += 32) t += a.part[((size_t)r * (W + 1) + j) * a.D + i];
-  s[g][c] = t;
+    for (int r = g; r < a.parts; r += 32) t.add(a.part[((size_t)r * (W + 1) + j) * a.D + i]);
+  s[g][c] = t.sum;
   __syncthreads();
   if (g == 0 && i < a.D) {
 #pragma unroll
-    for (int k = 1; k < 32; ++k) t += s[k][c];
+    for (int k = 1; k < 32; ++k) t.add(s[k][c]);
     void* out = j < W ? a.dw : a.db;
     const size_t at = j < W ? (size_t)i * W + j : i;
     if (!out) return;
     if (a.w_bf16)
-      st_io(static_cast<__nv_bfloat16*>(out) + at, t);
+      st_io(static_cast<__nv_bfloat16*>(out) + at, t.sum);
     else
-      static_cast<float*>(out)[at] = t;
+      static_cast<float*>(out)[at] = t.sum;
   }
 }
 

@@ -401,10 +401,10 @@ __global__ void __launch_bounds__(TB) rms_bwd_kernel(RmsArgs a) {
     }
   __syncthreads();
   for (int i = threadIdx.x; i < a.D; i += TB) {
-    float s = 0.f;
+    CarriedSum s;
 #pragma unroll 8
-    for (int g = 0; g < kGroups; ++g) s += part_s[g * a.D + i];
-    a.part[(size_t)blockIdx.x * a.D + i] = s;
+    for (int g = 0; g < kGroups; ++g) s.add(part_s[g * a.D + i]);
+    a.part[(size_t)blockIdx.x * a.D + i] = s.sum;
   }
 }
 
@@ -446,19 +446,19 @@ __global__ void __launch_bounds__(1024) rms_weight_grad_kernel(RmsArgs a) {
   __shared__ float s[32][33];
   const int c = threadIdx.x & 31, g = threadIdx.x >> 5;
   const int i = blockIdx.x * 32 + c;
-  float t = 0.f;
+  CarriedSum t;
   if (i < a.D)
 #pragma unroll 8
-    for (int r = g; r < a.parts; r += 32) t += a.part[(size_t)r * a.D + i];
-  s[g][c] = t;
+    for (int r = g; r < a.parts; r += 32) t.add(a.part[(size_t)r * a.D + i]);
+  s[g][c] = t.sum;
   __syncthreads();
   if (g == 0 && i < a.D) {
 #pragma unroll
-    for (int k = 1; k < 32; ++k) t += s[k][c];
+    for (int k = 1; k < 32; ++k) t.add(s[k][c]);
     if (a.w_bf16)
-      st_io(static_cast<__nv_bfloat16*>(a.dw) + i, t);
+      st_io(static_cast<__nv_bfloat16*>(a.dw) + i, t.sum);
     else
-      static_cast<float*>(a.dw)[i] = t;
+      static_cast<float*>(a.dw)[i] = t.sum;
   }
 }
 
@@ -686,9 +686,9 @@ __global__ void __launch_bounds__(TB) rms_bwd_odd_kernel(RmsArgs a, int stages) 
     if (n * LPR + lane < a.D) part_s[grp * a.D + n * LPR + lane] = dw[n];
   __syncthreads();
   for (int i = threadIdx.x; i < a.D; i += TB) {
-    float s = 0.f;
-    for (int g = 0; g < kGroups; ++g) s += part_s[g * a.D + i];
-    a.part[(size_t)blockIdx.x * a.D + i] = s;
+    CarriedSum s;
+    for (int g = 0; g < kGroups; ++g) s.add(part_s[g * a.D + i]);
+    a.part[(size_t)blockIdx.x * a.D + i] = s.sum;
   }
 }
 

@@ -75,6 +75,17 @@ __device__ __forceinline__ float both<float>(float a) { return a; }
 template <>
 __device__ __forceinline__ float2 both<float2>(float a) { return make_float2(a, a); }
 __device__ __forceinline__ float sum_of(float a) { return a; }
+// A sum that carries along what its additions round off (Kahan's), so that its error does
+// not grow with the number of terms.  A term that is not finite makes it what a plain sum is.
+struct CarriedSum {
+  float sum = 0.f, lost = 0.f;
+  __device__ __forceinline__ void add(float v) {
+    v -= lost;
+    const float next = sum + v, off = (next - sum) - v;
+    lost = off - off == 0.f ? off : 0.f;
+    sum = next;
+  }
+};
 __device__ __forceinline__ float sum_of(float2 a) { return a.x + a.y; }
 template <int VEC>
 struct Pairs {

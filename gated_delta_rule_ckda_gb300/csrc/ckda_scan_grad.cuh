@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kScanBlock, 8 / kScanWarps) scan_grad_kernel(S
   }
   // Sums over a piece's tokens, in fp32: dD's and ddt_bias's over a tile, then with what the
   // addition to the rest rounded off carried along; dA's over kSumTiles tiles, then in memory.
-  float dskip = 0.f, dbias = 0.f, lost_skip = 0.f, lost_bias = 0.f;
+  CarriedSum dskip, dbias;
   bool summed = false;
   const auto put_dA = [&]() {
 #pragma unroll
@@ -471,20 +471,14 @@ __global__ void __launch_bounds__(kScanBlock, 8 / kScanWarps) scan_grad_kernel(S
           if (a.z) st_io(static_cast<IO*>(b.dz) + at + (long long)(k + 1) * a.D, dz.y);
         }
       }
-      const auto carry = [](float& sum, float& lost, float more) {
-        more -= lost;
-        const float next = sum + more;
-        lost = (next - sum) - more;
-        sum = next;
-      };
-      carry(dskip, lost_skip, tile_skip);
-      carry(dbias, lost_bias, tile_bias);
+      dskip.add(tile_skip);
+      dbias.add(tile_bias);
     }
   }
   put_dA();
   if (own) {
-    b.part_d[unit * 2 * a.D + c] = dskip;
-    b.part_d[(unit * 2 + 1) * a.D + c] = dbias;
+    b.part_d[unit * 2 * a.D + c] = dskip.sum;
+    b.part_d[(unit * 2 + 1) * a.D + c] = dbias.sum;
   }
 }
 
@@ -501,28 +495,34 @@ __global__ void __launch_bounds__(256) scan_sums_kernel(ScanBwdArgs b, long long
     const int w = (int)(i % (2 * a.N)) / a.N, n = (int)(i % a.N);
     // (behind the last sequence there are no parts, and the sum is zero)
     const int blocks = (int)(tg / a.G % a.T) < scan_last(a) ? a.chan_blocks / a.G : 0;
-    float s = 0.f;
-#pragma unroll 8
-    for (int k = 0; k < blocks; ++k) s += b.part_bc[k * per + i];
-    st_io(static_cast<IO*>(w ? b.dB : b.dC) + tg * a.N + n, s);
+    CarriedSum s;  // (eight at a time: the batch's gradients take 1185 us, one by one 1199)
+    int k = 0;
+    for (; k + 8 <= blocks; k += 8) {
+      float few = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) few += b.part_bc[(k + e) * per + i];
+      s.add(few);
+    }
+    for (; k < blocks; ++k) s.add(b.part_bc[k * per + i]);
+    st_io(static_cast<IO*>(w ? b.dB : b.dC) + tg * a.N + n, s.sum);
     return;
   }
   const long long i = ((long long)blockIdx.x - bc_blocks) * 256 + threadIdx.x;
   const long long dn = (long long)a.D * a.N;
   const int units = a.rows * a.pieces;
   if (i < dn) {
-    float s = 0.f;
+    CarriedSum s;
 #pragma unroll 8
-    for (int u = 0; u < units; ++u) s += b.part_a[u * dn + i];
-    b.dA[i] = s;
+    for (int u = 0; u < units; ++u) s.add(b.part_a[u * dn + i]);
+    b.dA[i] = s.sum;
   } else if (i < dn + 2 * a.D) {
     const int w = (int)((i - dn) / a.D), d = (int)((i - dn) % a.D);
     float* out = w ? b.dbias : b.dskip;
     if (!out) return;
-    float s = 0.f;
+    CarriedSum s;
 #pragma unroll 8
-    for (int u = 0; u < units; ++u) s += b.part_d[(u * 2LL + w) * a.D + d];
-    out[d] = s;
+    for (int u = 0; u < units; ++u) s.add(b.part_d[(u * 2LL + w) * a.D + d]);
+    out[d] = s.sum;
   }
 }
 
