@@ -73,11 +73,14 @@ __device__ __forceinline__ float rcp(float a) {
   return d;
 }
 __device__ __forceinline__ float2 rcp(float2 a) { return make_float2(rcp(a.x), rcp(a.y)); }
-// exp(delta A) from A log2(e).  ex2.approx comes out low by 2e-8 of the value on average
-// for arguments of 2^-8 to 2^0 (8e-9 for smaller ones; it is exact at 0, with the addend
-// too): nothing for one decay, but a state of a long memory is behind the product of
-// thousands.  The addend takes most of that out, at no cost.
-constexpr float kEx2Bias = 2.5e-8f;
+// exp(delta A) from A log2(e).  ex2.approx comes out low on average, by 1.4e-8 to 2.7e-8 of
+// the value for arguments of 2^-8 to 2^0 and by 5e-9 to 9e-9 for smaller ones (it is exact
+// at 0, with the addend too): nothing for one decay, but a state of a memory of 2^-o tokens
+// is behind the product of as many.  The addend, which costs nothing, leaves 2e-8 low
+// around 2^-7, where memories are short, and 3e-9 high to 2e-9 low below 2^-9: within 6e-6
+// over memories of up to 2048 tokens, 9e-6 over 4096.  (No addend: 5.4e-5 over 8192 and
+// 1e-4 over 16,384; 2.5e-8, which suits short memories best, 8.8e-5 and 1.8e-4.)
+constexpr float kEx2Bias = 1.15e-8f;
 __device__ __forceinline__ float2 decay_of(float2 delta, float2 A2) {
   return ex2(fma_(delta, A2, both<float2>(kEx2Bias)));
 }
