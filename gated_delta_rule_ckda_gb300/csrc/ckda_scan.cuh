@@ -367,11 +367,11 @@ __device__ __forceinline__ float2 step_sizes(float2 dt, float2 bias, int softplu
 
 // States that enter the pieces, from what each adds (ckda_scan_fwd.cu).
 cudaError_t launch_scan_join(bool next, const ScanArgs& a, cudaStream_t s);
-// Pieces of a row: one where its channels fill the room of `room` warps or it has no more
-// than `whole` tokens; else as many as it has room for, of about `least` tokens or more, in
-// whole tiles (in multiples of 64 the batch's gradients took 1235 us for 1194, the documents
-// 555 for 543).
-void scan_pieces(int rows, int T, int D, int G, int room, int least, int whole, int* pieces, int* len);
+// Pieces of a row: one where `room` warps have no room for `fewest` or it has no more than
+// `whole` tokens; else as many as it has room for, of about `least` tokens or more, in whole
+// tiles (in multiples of 64 the batch's gradients took 1235 us for 1194, the documents 555
+// for 543).
+void scan_pieces(int rows, int T, int D, int G, int room, int fewest, int least, int whole, int* pieces, int* len);
 
 // Empty sequences hand their states on: a warp copies its channels' part of `from` (zero
 // if null) to `to`.

@@ -78,12 +78,16 @@ cudaError_t launch_io(const ScanArgs& a, cudaStream_t s) {
   return scan_vectors(a, sizeof(IO)) ? by_states<IO, true>(a, s) : by_states<IO, false>(a, s);
 }
 
-// Room for 12 warps an SM: the documents take 884 us with 8, 543 with 12, 562 with 16; the
-// batch, 1024 warps in one piece, 418, and 631 in two, which 16 would allow.  Rows of up to
-// 128 tokens stay whole: 100 tokens of 2048 channels take 28 us, cut 35 like every number up
-// to 300, which take 46 in pieces of 128.
+// Room for 12 warps an SM: the documents take 884 us with 8, 543 with 12, 562 with 16.  Cut
+// where that holds four pieces, as every decay is then computed twice.  Rows of 2048 tokens
+// of 4096 channels of 16 states, 128 warps each, whole and cut: 1 315 and 92 us, 3 (four
+// pieces) 315 and 248, 4 (three) 316 and 322, 5 and 7 (two) 417 and 471, 419 and 475, 8 420
+// and 648; of 8 states 3 254 and 178, 4 254 and 262, 7 320 and 386; 1024 tokens of 64 states
+// 2 533 and 363, 3 537 and 551, 4 541 and 721.  Rows of up to 128 tokens stay whole: 100
+// tokens of 2048 channels take 28 us, cut 35 like every number up to 300, which take 46 in
+// pieces of 128.
 void pieces_of(int rows, int T, int D, int G, int* pieces, int* len) {
-  scan_pieces(rows, T, D, G, 12 * kSms, 64, 128, pieces, len);
+  scan_pieces(rows, T, D, G, 12 * kSms, 4, 64, 128, pieces, len);
 }
 
 inline size_t state_bytes(int rows, int pieces, int D, int N) {
@@ -97,10 +101,10 @@ cudaError_t launch_scan_join(bool next, const ScanArgs& a, cudaStream_t s) {
   return launch_next(next, scan_join_kernel, (unsigned)((n + 255) / 256), 256, 0, s, a);
 }
 
-void scan_pieces(int rows, int T, int D, int G, int room, int least, int whole, int* pieces, int* len) {
+void scan_pieces(int rows, int T, int D, int G, int room, int fewest, int least, int whole, int* pieces, int* len) {
   const long long units = (long long)rows * scan_chan_blocks(D, G);
   int n = 1;
-  if (2 * units <= room && T > whole) {
+  if (fewest * units <= room && T > whole) {
     n = (int)(room / units);
     const int most = (T + least - 1) / least;
     if (n > most) n = most;
