@@ -675,16 +675,6 @@ ckda_status check_conv(int B, int T, int D, int W, long long ldx, ckda_dtype io,
   if ((long long)B * T * ((D + 31) / 32) > 8LL * 0x7fffffffLL) return CKDA_ERR_UNSUPPORTED;
   return CKDA_OK;
 }
-inline size_t span_bytes(int B, int T, int D, long long ld, size_t io) {
-  const long long rows = (long long)B * T;
-  return rows > 0 ? (size_t)((rows - 1) * ld + D) * io : 0;
-}
-// Whether [p, p + n) and [q, q + m) share memory.
-inline bool overlap(const void* p, size_t n, const void* q, size_t m) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return p && q && a < b + m && b < a + n;
-}
-
 ckda_status forward(const void* x, const void* weight, const void* bias, const void* h0, void* y, void* hT,
                     const int32_t* cu_seqlens, int num_seqs, int B, int T, int D, int W, long long ldx,
                     ckda_dtype io_dtype, ckda_dtype weight_dtype, int silu, bool fill, void* stream) {
@@ -695,8 +685,10 @@ ckda_status forward(const void* x, const void* weight, const void* bias, const v
   const int seqs = cu_seqlens ? num_seqs : B;
   const size_t io = io_dtype == CKDA_F32 ? 4 : 2;
   // blocks that write one of these run beside blocks that still read the other
-  if (overlap(h0, (size_t)seqs * (W - 1) * D * io, hT, (size_t)seqs * (W - 1) * D * io) ||
-      overlap(x, span_bytes(B, T, D, ldx, io), y, span_bytes(B, T, D, D, io)))
+  const size_t states = (size_t)seqs * (W - 1) * D * io, in = rows_bytes((long long)B * T, D, ldx, io),
+               out = rows_bytes((long long)B * T, D, D, io);
+  if (overlap(h0, states, hT, states) || overlap(x, in, y, out) || overlap(x, in, hT, states) ||
+      overlap(y, out, h0, states) || overlap(y, out, hT, states))
     return CKDA_ERR_INVALID_ARG;
   ConvArgs a{};
   a.x = x; a.w = weight; a.b = bias; a.h0 = h0; a.y = y; a.hT = hT; a.cu = cu_seqlens;
@@ -746,11 +738,12 @@ ckda_status ckda_conv_bwd(const void* dy, const void* x, const void* weight, con
   if (cu_seqlens && (num_seqs < 1 || B != 1)) return CKDA_ERR_INVALID_ARG;
   if (!weight || !dweight || (T > 0 && (!x || !dy || !dx))) return CKDA_ERR_INVALID_ARG;
   const size_t io = io_dtype == CKDA_F32 ? 4 : 2;
-  if (overlap(x, span_bytes(B, T, D, ldx, io), dx, span_bytes(B, T, D, D, io)) ||
-      overlap(dy, span_bytes(B, T, D, D, io), dx, span_bytes(B, T, D, D, io)))
+  const size_t states = (size_t)(cu_seqlens ? num_seqs : B) * (W - 1) * D * io,
+               in = rows_bytes((long long)B * T, D, ldx, io), out = rows_bytes((long long)B * T, D, D, io);
+  if (overlap(x, in, dx, out) || overlap(dy, out, dx, out) || overlap(h0, states, dx, out) ||
+      overlap(dhT, states, dx, out) || overlap(h0, states, dh0, states) || overlap(dhT, states, dh0, states) ||
+      overlap(x, in, dh0, states) || overlap(dy, out, dh0, states) || overlap(dx, out, dh0, states))
     return CKDA_ERR_INVALID_ARG;
-  const size_t states = (size_t)(cu_seqlens ? num_seqs : B) * (W - 1) * D * io;
-  if (overlap(h0, states, dh0, states) || overlap(dhT, states, dh0, states)) return CKDA_ERR_INVALID_ARG;
   if (!workspace || workspace_bytes < ckda_conv_bwd_workspace_bytes(B, T, D, W) || !aligned(workspace, 16))
     return CKDA_ERR_WORKSPACE;
   ConvArgs a{};
@@ -767,6 +760,10 @@ ckda_status ckda_conv_decode_step(const void* x, const void* weight, const void*
   const ckda_status st = check_conv(B, 1, D, W, ldx, io_dtype, weight_dtype);
   if (st != CKDA_OK) return st;
   if (!x || !weight || !state || !y) return CKDA_ERR_INVALID_ARG;
+  const size_t io = io_dtype == CKDA_F32 ? 4 : 2, states = (size_t)B * (W - 1) * D * io;
+  if (clash(y, x, B, D, ldx, io) || overlap(y, rows_bytes(B, D, D, io), state, states) ||
+      overlap(x, rows_bytes(B, D, ldx, io), state, states))
+    return CKDA_ERR_INVALID_ARG;
   ConvArgs a{};
   a.x = x; a.w = weight; a.b = bias; a.hT = state; a.y = y;
   a.ldx = ldx; a.tokens = B; a.seqs = B; a.T = 1; a.D = D;

@@ -879,6 +879,15 @@ ckda_status forward(const void* x, const void* residual, const void* weight, voi
     return CKDA_ERR_INVALID_ARG;
   if (rows == 0) return CKDA_OK;
   if (!x || !y || !rstd || (out8 && !scale) || h == y) return CKDA_ERR_INVALID_ARG;
+  // (a block that writes a row runs beside blocks that still read others)
+  const size_t io_bytes = io == CKDA_F32 ? 4 : 2, in = rows_bytes(rows, width, width, io_bytes),
+               out = out8 ? rows_bytes(rows, width, width, 1) : in;
+  if (clash(h, x, rows, width, width, io_bytes) || clash(h, residual, rows, width, width, io_bytes) ||
+      overlap(h, in, y, out))
+    return CKDA_ERR_INVALID_ARG;
+  if (out8 ? overlap(y, out, x, in) || overlap(y, out, residual, in)
+           : clash(y, x, rows, width, width, io_bytes) || clash(y, residual, rows, width, width, io_bytes))
+    return CKDA_ERR_INVALID_ARG;
   RmsArgs a{};
   a.x = x; a.add = residual; a.w = weight; a.h = h; a.y = y; a.scale = scale; a.rstd = rstd;
   a.rows = rows; a.D = width; a.group = group; a.w_bf16 = wt == CKDA_BF16; a.eps = eps;
@@ -929,6 +938,9 @@ ckda_status ckda_rmsnorm_bwd(const void* dy, const void* h, const float* rstd, c
         !aligned16(workspace))
       return CKDA_ERR_WORKSPACE;
   }
+  const size_t io = io_dtype == CKDA_F32 ? 4 : 2;
+  for (const void* in : {dy, h, dh})
+    if (clash(dx, in, rows, width, width, io)) return CKDA_ERR_INVALID_ARG;
   RmsArgs a{};
   a.x = h; a.dy = dy; a.add = dh; a.w = weight; a.y = dx;
   a.rstd = const_cast<float*>(rstd);

@@ -13,6 +13,22 @@ inline int blocks_for(long long units, int per_sm) {
   return (int)(units < most ? (units < 1 ? 1 : units) : most);
 }
 
+// Whether [p, p + n) and [q, q + m) share memory.
+inline bool overlap(const void* p, size_t n, const void* q, size_t m) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return p && q && n > 0 && m > 0 && a < b + m && b < a + n;
+}
+// From the first of so many rows of D, ld apart, to behind the last.
+inline size_t rows_bytes(long long rows, long long D, long long ld, size_t io) {
+  return rows > 0 ? (size_t)((rows - 1) * ld + D) * io : 0;
+}
+// Whether an output of dense rows shares memory with an input of rows ld apart, other than
+// element for element: what writes one part may run beside what still reads another.
+inline bool clash(const void* out, const void* in, long long rows, long long D, long long ld, size_t io) {
+  return !(out == in && (ld == D || rows == 1)) &&
+         overlap(out, rows_bytes(rows, D, D, io), in, rows_bytes(rows, D, ld, io));
+}
+
 template <typename IO, int VEC>
 struct alignas(sizeof(IO) * VEC) Pack {
   IO v[VEC];

@@ -388,6 +388,26 @@ __device__ __forceinline__ void empty_states(const ScanArgs& a, const ScanPlace&
   }
 }
 
+// Tensors by what their rows are: channels, groups of states, or one state of a sequence.
+enum ScanRows { kChannels, kGroups, kStates };
+inline size_t scan_bytes(const ScanArgs& a, ScanRows kind, long long ld, size_t io) {
+  if (kind == kStates) return (size_t)a.seqs * a.D * a.N * 4;
+  return rows_bytes((long long)a.rows * a.T, kind == kChannels ? a.D : (long long)a.G * a.N, ld, io);
+}
+// Whether a dense output shares memory with an input, other than element for element with one
+// of its kind: what writes one part may run beside what still reads another.
+inline bool scan_clash(const ScanArgs& a, const void* out, ScanRows kind, size_t io) {
+  const long long gn = (long long)a.G * a.N, dense = kind == kChannels ? a.D : gn;
+  const struct { const void* p; ScanRows kind; long long ld; } in[8] = {
+      {a.x, kChannels, a.ldx}, {a.dt, kChannels, a.lddt}, {a.z, kChannels, a.ldz}, {a.dy, kChannels, a.D},
+      {a.B, kGroups, a.ldb},   {a.C, kGroups, a.ldc},     {a.h0, kStates, 0},      {a.dhT, kStates, 0}};
+  for (const auto& t : in)
+    if (!(out == t.p && kind == t.kind && (kind == kStates || t.ld == dense || (long long)a.rows * a.T == 1)) &&
+        overlap(out, scan_bytes(a, kind, dense, io), t.p, scan_bytes(a, t.kind, t.ld, io)))
+      return true;
+  return false;
+}
+
 ckda_status check_scan(int rows, int T, int D, int N, int G, const int32_t* cu, int num_seqs, ckda_dtype io);
 
 // ------------------------------------------------------------- a walk forward

@@ -94,6 +94,15 @@ ckda_status ckda_scan_bwd(const void* dy, const void* x, const void* dt, const f
   a.chunk = part(w.chunk); a.chunk_sum = part(w.chunk_sum); a.grad = part(w.grad);
   b.part_bc = part(w.part_bc); b.part_a = part(w.part_a); b.part_d = part(w.part_d);
   a.chunks = w.chunks;
+  const size_t io = io_dtype == CKDA_F32 ? 4 : 2;
+  const struct { const void* p; ScanRows kind; } out[6] = {{dx, kChannels}, {ddt, kChannels}, {dz, kChannels},
+                                                           {dBm, kGroups}, {dC, kGroups}, {dh0, kStates}};
+  const auto size = [&](int i) { return scan_bytes(a, out[i].kind, out[i].kind == kChannels ? D : (long long)G * N, io); };
+  for (int i = 0; i < 6; ++i) {
+    if (scan_clash(a, out[i].p, out[i].kind, io)) return CKDA_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i].p, size(i), out[j].p, size(j))) return CKDA_ERR_INVALID_ARG;
+  }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = io_dtype == CKDA_F32 ? launch_scan_grads<float>(b, s) : launch_scan_grads<__nv_bfloat16>(b, s);
   return e == cudaSuccess ? CKDA_OK : CKDA_ERR_CUDA;

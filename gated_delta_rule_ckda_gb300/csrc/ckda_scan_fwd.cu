@@ -158,6 +158,10 @@ ckda_status forward(const void* x, const void* dt, const float* A, const void* B
   a.ldx = ldx; a.lddt = lddt; a.ldb = ldb; a.ldc = ldc; a.ldz = ldz;
   a.rows = B; a.T = T; a.D = D; a.N = N; a.G = G; a.seqs = cu_seqlens ? num_seqs : B;
   a.softplus = softplus != 0; a.fill = fill;
+  const size_t io = io_dtype == CKDA_F32 ? 4 : 2;
+  if (scan_clash(a, y, kChannels, io) || scan_clash(a, hT, kStates, io) ||
+      overlap(y, scan_bytes(a, kChannels, D, io), hT, scan_bytes(a, kStates, 0, io)))
+    return CKDA_ERR_INVALID_ARG;
   pieces_of(B, T, D, G, &a.pieces, &a.piece_len);
   if (a.pieces > 1) {
     if (!workspace || workspace_bytes < ckda_scan_fwd_workspace_bytes(B, T, D, N, G) || !scan_aligned(workspace, 16))

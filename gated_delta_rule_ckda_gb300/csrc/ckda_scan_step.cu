@@ -181,7 +181,11 @@ extern "C" ckda_status ckda_scan_decode_step(const void* x, const void* dt, cons
   a.hT = state; a.y = y;
   a.ldx = ldx; a.lddt = lddt; a.ldb = ldb; a.ldc = ldc; a.ldz = ldz;
   a.rows = B; a.T = 1; a.D = D; a.N = N; a.G = G; a.seqs = B; a.softplus = softplus != 0;
-  const size_t pack = 4 * (io_dtype == CKDA_F32 ? 4 : 2);  // bytes of four states of B and C
+  const size_t io = io_dtype == CKDA_F32 ? 4 : 2;
+  if (scan_clash(a, y, kChannels, io) || scan_clash(a, state, kStates, io) ||
+      overlap(y, scan_bytes(a, kChannels, D, io), state, scan_bytes(a, kStates, 0, io)))
+    return CKDA_ERR_INVALID_ARG;
+  const size_t pack = 4 * io;  // bytes of four states of B and C
   const bool vec = N % 4 == 0 && ldb % 4 == 0 && ldc % 4 == 0 &&
                    ((reinterpret_cast<uintptr_t>(state) | reinterpret_cast<uintptr_t>(A)) & 15) == 0 &&
                    ((reinterpret_cast<uintptr_t>(Bm) | reinterpret_cast<uintptr_t>(C)) & (pack - 1)) == 0;

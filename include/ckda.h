@@ -600,7 +600,8 @@ ckda_status ckda_layernorm_bwd(const void *dy, const void *x, const float *mean,
  *                cu_seqlens[num_seqs] may be less than T: tokens behind the last sequence
  *                are not read, and left as they were in y.
  *
- * hT must not overlap h0, nor y x (checked).  Arithmetic in fp32, one rounding.
+ * y and hT overlap no input and not each other (checked).  Arithmetic in fp32, one
+ * rounding.
  * T = 0 hands the states on.  A token that is not finite reaches only the W tokens of its
  * channel that the formula gives it to.
  */
@@ -617,10 +618,9 @@ ckda_status ckda_conv_fwd_filled(const void *x, const void *weight, const void *
 
 /*
  * Its backward: the gradients of sum <y, dy> + <hT, dhT>.
- *   dy, dx   : io [B, T, D]; dx overlaps neither x nor dy (checked); its rows behind the
- *              last sequence become zero
- *   dhT, dh0 : io [N, W - 1, D] or NULL (zero, not stored); dh0 overlaps neither h0 nor
- *              dhT (checked)
+ *   dy, dx   : io [B, T, D]; rows of dx behind the last sequence become zero
+ *   dhT, dh0 : io [N, W - 1, D] or NULL (zero, not stored)
+ *              (dx and dh0 overlap no input and not each other: checked)
  *   dweight  : weight_dtype [D, W]; dbias [D] or NULL (not wanted); from fp32 sums in a
  *              fixed order: the same inputs give the same bits
  * workspace: ckda_conv_bwd_workspace_bytes(B, T, D, W) bytes, 16-byte aligned, scratch.
@@ -635,7 +635,8 @@ ckda_status ckda_conv_bwd(const void *dy, const void *x, const void *weight, con
 
 /*
  * One token of the same convolution: x, y io [B, D] (rows of x ldx elements apart);
- * state io [B, W - 1, D], moved on by the token in place.
+ * state io [B, W - 1, D], moved on by the token in place.  y may be x where that is dense;
+ * else y, x and state do not overlap (checked).
  */
 ckda_status ckda_conv_decode_step(const void *x, const void *weight, const void *bias,
                                   void *state, void *y, int B, int D, int W, long long ldx,
@@ -652,8 +653,9 @@ ckda_status ckda_conv_decode_step(const void *x, const void *weight, const void 
  *   x, dt, z, y : io   [B, T, D], channels last; z NULL: no gate
  *   Bm, C       : io   [B, T, G, N]; channel d reads group d / (D / G); G divides D
  *   A           : fp32 [D, N], finite; D_skip, dt_bias fp32 [D] or NULL (zero)
- *   h0, hT      : fp32 [sequences, D, N] or NULL (zero, not stored); hT must not overlap
- *                 h0 (checked), y no input
+ *   h0, hT      : fp32 [sequences, D, N] or NULL (zero, not stored)
+ *                 (y may be x, dt or z where that is dense; else y and hT overlap none of
+ *                 x, dt, z, Bm, C, h0 and not each other: checked)
  *   ldx, lddt, ldb, ldc, ldz: elements from one token to the next (at least D, or G N)
  *   cu_seqlens, num_seqs: as ckda_fwd (packed sequences, B = 1); an empty sequence hands
  *                 its h0 on.  cu_seqlens[num_seqs] may be less than T: tokens behind the
@@ -692,7 +694,9 @@ ckda_status ckda_scan_fwd_filled(const void *x, const void *dt, const float *A, 
  *                     (rows of all of these behind the last sequence become zero)
  *   dA              : fp32 [D, N]; dD_skip, ddt_bias fp32 [D] or NULL (not wanted)
  *   dhT, dh0        : fp32 [sequences, D, N] or NULL (zero, not stored), not overlapping
- *                     (checked)
+ *   A gradient may be a dense input of its kind (dx, ddt, dz: dy, x, dt, z; dBm, dC: Bm, C;
+ *   dh0: h0); else they overlap no input but A, D_skip and dt_bias, and not each other
+ *   (checked).
  * The forward's states are recomputed.  No atomics: the same inputs give the same bits.
  * workspace: ckda_scan_bwd_workspace_bytes(...) bytes, 16-byte aligned, scratch: mostly
  * the states before every 4th token.
@@ -710,6 +714,7 @@ ckda_status ckda_scan_bwd(const void *dy, const void *x, const void *dt, const f
 /*
  * One token of the same scan on a resident state, updated in place.
  *   x, dt, z, y : io [B, D];  Bm, C : io [B, G, N];  state : fp32 [B, D, N]
+ *   y may be x, dt or z where that is dense; else y and state overlap nothing (checked)
  */
 ckda_status ckda_scan_decode_step(const void *x, const void *dt, const float *A, const void *Bm,
                                   const void *C, const float *D_skip, const void *z,
@@ -723,7 +728,8 @@ ckda_status ckda_scan_decode_step(const void *x, const void *dt, const float *A,
  *     h = x + residual (rounded to io),  y = h rstd weight,
  *     rstd = 1 / sqrt(mean(h^2) + eps)
  *   x, residual, h, y : io [rows, width]; residual and h are both NULL (h is x) or both
- *                       set; h may be x or residual, y may be x, and not h
+ *                       set; h and y may each be x or residual, and not the same; other
+ *                       overlaps are refused
  *   weight            : weight_dtype [width] or NULL (one)
  *   rstd              : fp32 [rows]
  * Arithmetic in fp32 with one rounding (squares of values past 1e19 leave its range).  Up
@@ -737,7 +743,8 @@ ckda_status ckda_rmsnorm_fwd(const void *x, const void *residual, const void *we
 /*
  * The same with y in 8 bits (e4m3) and scales, y = y8 scale:
  *     scale = max(m, 2^-100) / 448, m the largest |y| of a group of columns
- *   y8    : [rows, width] bytes, rounded once from y in fp32; overlaps no other tensor
+ *   y8    : [rows, width] bytes, rounded once from y in fp32; overlaps none of x, residual
+ *           and h (checked)
  *   scale : fp32 [rows] (group = 0: the whole row) or [rows, width / group]
  *   group : 0, 32, 64 or 128, dividing width
  */
@@ -752,7 +759,7 @@ ckda_status ckda_rmsnorm_fwd8(const void *x, const void *residual, const void *w
  *     dx = rstd (t - xh mean(t xh)) + dh,
  * the gradient of x and of residual alike, and dweight = sum over rows of dy xh.
  *   dh : io [rows, width], the gradient that arrives at h itself, or NULL (zero)
- *   dx may alias dy, h or dh; dweight NULL: not wanted (the workspace may then be NULL).
+ *   dx may be dy, h or dh (other overlaps are refused); dweight NULL: not wanted (the workspace may then be NULL).
  *   rows = 0 writes a zero dweight.  workspace: ckda_rmsnorm_bwd_workspace_bytes(rows,
  *   width) bytes, 16-byte aligned.
  */
