@@ -467,7 +467,8 @@ __global__ void __launch_bounds__(1024) rms_weight_grad_kernel(RmsArgs a) {
 // 16-byte vector, so whole vectors come to shared memory as they lie, threads take single
 // columns of it (LPR apart, NV each: weights stay with their columns), leave the results in
 // its place, and whole vectors go out again; what a row shares a vector with stays untouched.
-// One warp a row, or a block.  8,489 rows of 4853 in bf16 with a residual: 103 us forward
+// Rows of whole vectors that are wider than a block's registers hold in vectors (fp32 past
+// 8192 columns) go this way too.  One warp a row, or a block.  8,489 rows of 4853 in bf16 with a residual: 103 us forward
 // (48% of the copy bandwidth), 154 backward, which took 363 by single elements from memory.
 template <typename IO>
 struct OddRow {
@@ -802,8 +803,13 @@ cudaError_t run_bwd_odd(RmsArgs& a, cudaStream_t s) {
   kernel<<<p.blocks, TB, p.smem, s>>>(a, p.stages);
   return cudaGetLastError();
 }
-// The widest rows that these kernels hold.
+// The widest rows that these kernels hold, and the widest in vectors of VEC elements.  Rows
+// between the two (fp32, 4096 of 16,384 columns) with a residual take 214 us forward, 210 to 8
+// bits and 294 backward; by the kernels that read a row again, which wider ones need, 242,
+// 441 and 574.  (A few rows are as long under way in both: 7 of them 20 to 29 us and 18 to 26.)
 constexpr int kOddMost = 16384;
+template <int VEC>
+constexpr int kVectorsMost = 2048 * VEC;
 template <typename IO, bool OUT8>
 cudaError_t fwd_odd(const RmsArgs& a, cudaStream_t s) {
   const int D = a.D;
@@ -834,8 +840,9 @@ cudaError_t launch_fwd_rows(const RmsArgs& a, cudaStream_t s) {
   constexpr int kVec = 16 / sizeof(IO);
   // (8-bit outputs are stored in vectors of kVec bytes)
   const bool aligned = aligned16(a.x) && aligned16(a.add) && aligned16(a.h) && aligned16(a.y);
-  if (aligned && a.D % kVec == 0) return fwd_by_width<IO, OUT8, kVec>(a, s);
-  if (aligned && a.D <= kOddMost) return fwd_odd<IO, OUT8>(a, s);  // (groups of columns divide the width)
+  const bool held = aligned && a.D <= kOddMost && a.group == 0;
+  if (aligned && a.D % kVec == 0 && (a.D <= kVectorsMost<kVec> || !held)) return fwd_by_width<IO, OUT8, kVec>(a, s);
+  if (held) return fwd_odd<IO, OUT8>(a, s);
   if (OUT8 && a.group != 0) {  // groups across warps: the kernel that reads again
     rms_fwd_long_kernel<IO, OUT8><<<blocks_for(a.rows, 2), 1024, 0, s>>>(a);
     return cudaGetLastError();
@@ -848,9 +855,11 @@ cudaError_t launch_bwd_rows(RmsArgs a, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   if (a.rows > 0) {
     const bool aligned = aligned16(a.x) && aligned16(a.dy) && aligned16(a.add) && aligned16(a.y);
-    e = aligned && a.D % kVec == 0    ? bwd_by_width<IO, kVec>(a, s)
-        : aligned && a.D <= kOddMost ? bwd_odd<IO>(a, s)
-                                     : bwd_by_width<IO, 1>(a, s);
+    const bool held = aligned && a.D <= kOddMost;
+    if (aligned && a.D % kVec == 0 && (a.D <= kVectorsMost<kVec> || !held))
+      e = bwd_by_width<IO, kVec>(a, s);
+    else
+      e = held ? bwd_odd<IO>(a, s) : bwd_by_width<IO, 1>(a, s);
     if (e != cudaSuccess) return e;
   }
   if (a.part) {

@@ -733,7 +733,8 @@ ckda_status ckda_scan_decode_step(const void *x, const void *dt, const float *A,
  *   weight            : weight_dtype [width] or NULL (one)
  *   rstd              : fp32 [rows]
  * Arithmetic in fp32 with one rounding (squares of values past 1e19 leave its range).  Up
- * to 2^31 - 1 rows of any width up to 2^30; 16-byte aligned rows are moved in vectors.
+ * to 2^31 - 1 rows of any width up to 2^30; rows of up to 16,384 columns on 16-byte aligned
+ * bases are moved in vectors and read once.
  */
 ckda_status ckda_rmsnorm_fwd(const void *x, const void *residual, const void *weight, void *h,
                              void *y, float *rstd, long long rows, int width,
