@@ -174,12 +174,13 @@ struct Taps {
   }
 };
 
-// Rows of y behind the last sequence, [from, to): zero.  (What nothing writes could be
-// anything, and a NaN there reaches every weight of a layer that takes all rows.)
+// Rows of y behind the last sequence, every apart-th from `from` to `to`: zero.  (What
+// nothing writes could be anything, and a NaN there reaches every weight of a layer that
+// takes all rows.)
 template <typename IO, int VEC>
-__device__ __forceinline__ void zero_rows(const ConvArgs& a, long long from, long long to, int c) {
+__device__ __forceinline__ void zero_rows(const ConvArgs& a, long long from, long long to, int apart, int c) {
   const float none[VEC] = {};
-  for (; from < to; ++from) store_vec<IO, VEC>(a.y, from * a.D + c, none);
+  for (; from < to; from += apart) store_vec<IO, VEC>(a.y, from * a.D + c, none);
 }
 
 // Row i of the inputs before a sequence's token m: i = 0 is W - 1 tokens back.
@@ -312,7 +313,7 @@ __global__ void __launch_bounds__(kBlock) conv_fwd_kernel(ConvArgs a) {
   long long stop = m + a.run < a.tokens ? m + a.run : a.tokens;
   const long long last = a.cu ? offset_of(a, a.seqs) : a.tokens;
   if (c >= a.D) return;
-  if (a.fill) zero_rows<IO, VEC>(a, m > last ? m : last, stop, c);
+  if (a.fill) zero_rows<IO, VEC>(a, m > last ? m : last, stop, 1, c);
   if (stop > last) stop = last;
   if (m >= stop) return;
   Taps<W, VEC> taps;
@@ -403,9 +404,7 @@ __global__ void __launch_bounds__(kBlock, 2) conv_bwd_kernel(ConvArgs a) {
   const int c = (chan * a.lanes + lane) * VEC;
   const long long last = a.cu ? offset_of(a, a.seqs) : a.tokens;
   long long m = (tok * groups + grp) * a.run;
-  long long stop = m + a.run < a.tokens ? m + a.run : a.tokens;
-  if (c < a.D) zero_rows<IO, VEC>(a, m > last ? m : last, stop, c);
-  if (stop > last) stop = last;
+  long long stop = m + a.run < last ? m + a.run : last;
   using V = typename Chans<VEC>::V;
   constexpr int kN = Chans<VEC>::kN;
   Chans<VEC> dw[W], db;
@@ -494,42 +493,39 @@ __global__ void __launch_bounds__(kBlock, 2) conv_bwd_kernel(ConvArgs a) {
     for (int i = threadIdx.x; i < a.lanes * VEC; i += kBlock) {
       const int at = chan * a.lanes * VEC + i;
       if (at >= a.D) continue;
-      CarriedSum t;  // (eight at a time: one by one the call took 104 us for 102)
-      for (int g0 = 0; g0 < groups; g0 += 8) {
-        float few = 0.f;
-#pragma unroll
-        for (int g = 0; g < 8; ++g) few += sum[(g0 + g) * a.lanes + i / VEC][i % VEC];
-        t.add(few);
-      }
-      a.part[((size_t)tok * (W + 1) + j) * a.D + at] = t.sum;
+      float t = 0.f;  // (of eight, more only where channels are few: carrying what is rounded off took 2 us more)
+      for (int g = 0; g < groups; ++g) t += sum[g * a.lanes + i / VEC][i % VEC];
+      a.part[((size_t)tok * (W + 1) + j) * a.D + at] = t;
     }
   }
 }
 
 // dw and db from the partial rows: 32 channels to a block, 32 threads a channel over the
-// partial rows, joined in a fixed order.
-template <int W>
+// partial rows, joined in a fixed order (by a warp a channel; by a thread a channel, one
+// after another and carrying what is rounded off, it took 1 us more).  Beside that, dx behind the last sequence (in the
+// kernel before, it cost registers, and odd channel counts 3 us).
+template <typename IO, int W>
 __global__ void __launch_bounds__(1024) conv_weight_grad_kernel(ConvArgs a) {
   after_previous();
   __shared__ float s[32][33];
   const int c = threadIdx.x & 31, g = threadIdx.x >> 5, j = blockIdx.y;
   const int i = blockIdx.x * 32 + c;
+  if (a.cu && i < a.D) zero_rows<IO, 1>(a, offset_of(a, a.seqs) + j * 32 + g, a.tokens, 32 * (W + 1), i);
   CarriedSum t;
   if (i < a.D)
 #pragma unroll 8
     for (int r = g; r < a.parts; r += 32) t.add(a.part[((size_t)r * (W + 1) + j) * a.D + i]);
   s[g][c] = t.sum;
   __syncthreads();
-  if (g == 0 && i < a.D) {
-#pragma unroll
-    for (int k = 1; k < 32; ++k) t.add(s[k][c]);
-    void* out = j < W ? a.dw : a.db;
-    const size_t at = j < W ? (size_t)i * W + j : i;
-    if (!out) return;
+  const float all = lane_sum<32>(s[c][g]);  // of the block's channel g
+  const int own = blockIdx.x * 32 + g;
+  void* out = j < W ? a.dw : a.db;
+  if (c == 0 && own < a.D && out) {
+    const size_t at = j < W ? (size_t)own * W + j : own;
     if (a.w_bf16)
-      st_io(static_cast<__nv_bfloat16*>(out) + at, t.sum);
+      st_io(static_cast<__nv_bfloat16*>(out) + at, all);
     else
-      static_cast<float*>(out)[at] = t.sum;
+      static_cast<float*>(out)[at] = all;
   }
 }
 
@@ -628,7 +624,7 @@ cudaError_t run_bwd(ConvArgs a, cudaStream_t s) {
     conv_bwd_kernel<IO, W, VEC><<<(unsigned)(a.main_blocks + more), kBlock, smem, s>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_next(a.main_blocks + more > 0, conv_weight_grad_kernel<W>, dim3((a.D + 31) / 32, W + 1),
+  return launch_next(a.main_blocks + more > 0, conv_weight_grad_kernel<IO, W>, dim3((a.D + 31) / 32, W + 1),
                      1024, 0, s, a);
 }
 template <typename IO, int W, int VEC>

@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(1024) rms_bwd_long_kernel(RmsArgs a) {
 }
 
 // dw from the partial rows: 32 columns to a block, 32 threads a column over the partial
-// rows, joined in a fixed order.
+// rows, joined in a fixed order by a warp a column.
 __global__ void __launch_bounds__(1024) rms_weight_grad_kernel(RmsArgs a) {
   after_previous();
   __shared__ float s[32][33];
@@ -452,13 +452,13 @@ __global__ void __launch_bounds__(1024) rms_weight_grad_kernel(RmsArgs a) {
     for (int r = g; r < a.parts; r += 32) t.add(a.part[(size_t)r * a.D + i]);
   s[g][c] = t.sum;
   __syncthreads();
-  if (g == 0 && i < a.D) {
-#pragma unroll
-    for (int k = 1; k < 32; ++k) t.add(s[k][c]);
+  const float all = lane_sum<32>(s[c][g]);  // of the block's column g
+  const int own = blockIdx.x * 32 + g;
+  if (c == 0 && own < a.D) {
     if (a.w_bf16)
-      st_io(static_cast<__nv_bfloat16*>(a.dw) + i, t.sum);
+      st_io(static_cast<__nv_bfloat16*>(a.dw) + own, all);
     else
-      static_cast<float*>(a.dw)[i] = t.sum;
+      static_cast<float*>(a.dw)[own] = all;
   }
 }
 
