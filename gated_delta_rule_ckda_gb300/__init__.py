@@ -1196,7 +1196,8 @@ def scan_bwd(dy, x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, dhT=None
              softplus=True, store_dh0=True, workspace=None, stream=None):
     """Backward of scan_fwd (ckda_scan_bwd): gradients of sum <y, dy> + <hT, dhT>.  Returns
     (dx, ddt, dA, dB, dC, dD, dz, ddt_bias, dh0); those of what was not given are None, those
-    by token zero in rows behind the last packed sequence."""
+    by token zero in rows behind the last packed sequence.  Its workspace has about a byte for
+    every token, channel and state."""
     if stream is not None:
         return _on_stream(scan_bwd, locals())
     L = lib()
@@ -1263,7 +1264,8 @@ def _check_rms(x, weight, residual):
 def rmsnorm_fwd(x, weight=None, residual=None, eps=1e-5, y=None, h=None, rstd=None, stream=None):
     """Root-mean-square norm over the last axis of h = x + residual (ckda_rmsnorm_fwd).
     Returns (y, h, rstd): h is x itself without a residual; rstd is fp32 of x's leading
-    shape.  weight is bf16 or fp32 [width].  h may be x or residual, y may be x."""
+    shape.  residual has x's type; weight is bf16 or fp32 [width].  h and y may each be x or
+    residual, not the same (y=x without a residual leaves no h for rmsnorm_bwd)."""
     if stream is not None:
         return _on_stream(rmsnorm_fwd, locals())
     L = lib()
@@ -1293,7 +1295,8 @@ def rmsnorm_fwd(x, weight=None, residual=None, eps=1e-5, y=None, h=None, rstd=No
 def rmsnorm_fwd8(x, weight=None, residual=None, eps=1e-5, group=0, stream=None):
     """rmsnorm_fwd with y in 8 bits (ckda_rmsnorm_fwd8).  Returns (y8, scale, h, rstd): y8 is
     float8_e4m3fn and y = y8 scale; scale is fp32 of x's leading shape (group = 0: one for a
-    row), or with a last axis of width / group (group = 32, 64 or 128 columns each)."""
+    row), or with a last axis of width / group (group = 32, 64 or 128 columns each).  It is
+    for a product in 8 bits of the user's; the library has none."""
     if stream is not None:
         return _on_stream(rmsnorm_fwd8, locals())
     L = lib()

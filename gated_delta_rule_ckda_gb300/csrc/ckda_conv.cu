@@ -18,7 +18,9 @@
 //
 // The gradients of the weights: sums over a run in registers, over a block's runs in
 // shared memory, then one partial row a block in the workspace, added in a fixed order by
-// a second kernel.  No atomics: the same bits every time.
+// a second kernel that carries along what its additions round off.  No atomics: the same
+// bits every time.  (All in fp32; the sum over 64 tokens of a run is most of what is left,
+// 1.7e-7 of dw over 16,384 tokens.)
 //
 // Measured, bf16 with four taps, bias and silu: 24 packed prompts, 50,021 tokens of 4096
 // channels, 138 us, 89% of the copy bandwidth (8 channels a thread with the loads held in

@@ -16,7 +16,9 @@
 // registers by 8, 16 or 32 lanes or by a block, in vectors of VEC elements, and come
 // through a ring of S rows in shared memory that each thread fills for itself with
 // cp.async.  The weight gradients go by a partial row a block and a second kernel that
-// adds them in a fixed order: no atomics, the same bits every time.
+// adds them in a fixed order and carries along what its additions round off: no atomics,
+// the same bits every time.  (A thread's own sum, over its rows, is fp32: 1.6e-7 of dw over
+// 16,384 rows is mostly that.)
 #include <cuda_fp8.h>
 #include "ckda_launch.cuh"
 #include "ckda_rows.cuh"

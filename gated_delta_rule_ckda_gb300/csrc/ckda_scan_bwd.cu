@@ -13,16 +13,16 @@ struct Layout {
 Layout layout_of(int rows, int T, int D, int N, int G) {
   Layout w{};
   // Room for 24 warps an SM, three times what runs at once: the batch of 512 warps takes
-  // 1206 us so, 1274 with 8, 1267 with 16, 1233 with 32.  Cut where that holds four pieces:
+  // 1185 us so, 1329 with 16, 1206 with 32.  Cut where that holds four pieces:
   // rows of 1024 tokens of 4096 channels of 16 states, 128 warps each, whole and cut, 4 1038
   // and 653 us, 7 (four pieces) 1086 and 1041, 8 (three) 1092 and 1270, 14 (two) 1883 and
   // 1984; 512 tokens of 32 states 7 1397 and 1334, 9 1444 and 1694.  More than 32 states give
   // a warp enough to do by itself: 512 tokens of 64 states 2 (fourteen pieces) 1306 and 1098,
   // 3 (nine) 1318 and 1587, 4 1328 and 1936.  Pieces of at least 32 tokens: 2 x
-  // 1001 tokens of 480 channels of 12 states take 83 us, with 64 101, with 16 116; 100 of
-  // 2048 of 16 states 64, with 64 91.  More than 16 states leave fewer warps at once and
+  // 1001 tokens of 480 channels of 12 states take 78 us, with 64 99, with 16 108; 100 of
+  // 2048 of 16 states 62, with 64 90.  More than 16 states leave fewer warps at once and
   // have more to take up and leave at a piece's ends: 4096 tokens of 512 channels of 64
-  // states take 607 us by 64, by 32 724.
+  // states take 604 us by 64, by 32 710.
   const int least = N <= 16 ? 32 : 64;
   scan_pieces(rows, T, D, G, 24 * kSms, N <= 32 ? 4 : 12, least, least, &w.pieces, &w.len);
   w.chunks = (T + kScanChunk - 1) / kScanChunk;

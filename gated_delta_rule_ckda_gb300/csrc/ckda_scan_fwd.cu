@@ -12,7 +12,7 @@
 // side: a first pass leaves each piece's own end state and the sum of its steps (a state
 // decays over a piece by exp(A sum delta)), a scan over the pieces gives the states that
 // enter them, and the second pass runs every piece from its own.  (Three packed documents
-// of 32,768 tokens of 2048 channels: 543 us, 217 of them the first pass.)
+// of 32,768 tokens of 2048 channels: 539 us, 210 of them the first pass.)
 #include "ckda_scan.cuh"
 
 namespace ckda {
@@ -62,8 +62,8 @@ cudaError_t run(ScanArgs a, cudaStream_t s) {
 }
 
 // States of a channel to a lane, by their number.  16 states over two lanes of eight take
-// 438 us for the batch above and 557 for the documents, over four lanes of four 468 and
-// 691 (more shuffles), by one lane 439 and 605 (twice the reads of B and C).
+// 414 us for the batch above and 539 for the documents, over four lanes of four 542 and 690
+// (more shuffles), by one lane 408 and 634 (twice the reads of B and C).
 template <typename IO, bool VEC>
 cudaError_t by_states(const ScanArgs& a, cudaStream_t s) {
   if (a.N <= 4) return run<IO, ScanShape<1, 4>, VEC>(a, s);
@@ -78,14 +78,13 @@ cudaError_t launch_io(const ScanArgs& a, cudaStream_t s) {
   return scan_vectors(a, sizeof(IO)) ? by_states<IO, true>(a, s) : by_states<IO, false>(a, s);
 }
 
-// Room for 12 warps an SM: the documents take 884 us with 8, 543 with 12, 562 with 16.  Cut
+// Room for 12 warps an SM: the documents take 578 us with 8, 543 with 12, 554 with 16.  Cut
 // where that holds four pieces, as every decay is then computed twice.  Rows of 2048 tokens
 // of 4096 channels of 16 states, 128 warps each, whole and cut: 1 315 and 92 us, 3 (four
 // pieces) 315 and 248, 4 (three) 316 and 322, 5 and 7 (two) 417 and 471, 419 and 475, 8 420
 // and 648; of 8 states 3 254 and 178, 4 254 and 262, 7 320 and 386; 1024 tokens of 64 states
 // 2 533 and 363, 3 537 and 551, 4 541 and 721.  Rows of up to 128 tokens stay whole: 100
-// tokens of 2048 channels take 28 us, cut 35 like every number up to 300, which take 46 in
-// pieces of 128.
+// tokens of 2048 channels take 29 us, cut 39, like 300 of 1024, which whole take 57.
 void pieces_of(int rows, int T, int D, int G, int* pieces, int* len) {
   scan_pieces(rows, T, D, G, 12 * kSms, 4, 64, 128, pieces, len);
 }

@@ -20,11 +20,12 @@
 // A lane has a channel, as in the forward pass; up to 16 states at a time are spread over
 // LP lanes, more in turns (slices).  <.,.> go to their own lane by shuffles; dB and dC are
 // sums over a lane's channels, then over the other lanes of the warp; a warp's parts go
-// through the workspace and are added in a fixed order, as are dA's, dD's and ddt_bias's.
+// through the workspace and are added in a fixed order, as are dA's, dD's and ddt_bias's,
+// each carrying along what its additions round off.
 //
 // Bound, like the forward pass, by fma and exponentials on few warps (255 registers leave
-// two to a scheduler): 4 x 2048 tokens of 4096 channels of 16 states take 1190 us, 270 of
-// them the walk, 860 the gradients (issue 43% of the cycles, fma pipe 34%), 36 the sums of
+// two to a scheduler): 4 x 2048 tokens of 4096 channels of 16 states take 1181 us, 257 of
+// them the walk, 867 the gradients (issue 44% of the cycles, fma pipe 35%), 28 the sums of
 // dB's and dC's parts; memory 71.  Chunks of 8 tokens, half of them run forward twice,
 // took 1350; three blocks an SM with 0.9 KB of a thread's registers in local memory 1620.
 #pragma once

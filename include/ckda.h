@@ -699,7 +699,9 @@ ckda_status ckda_scan_fwd_filled(const void *x, const void *dt, const float *A, 
  *   (checked).
  * The forward's states are recomputed.  No atomics: the same inputs give the same bits.
  * workspace: ckda_scan_bwd_workspace_bytes(...) bytes, 16-byte aligned, scratch: mostly
- * the states before every 4th token.
+ * the states before every 4th token, a byte for every state of every channel and token
+ * (4.3 GB for 16,384 tokens of 4096 channels of 64 states).  Less memory: fewer rows to a
+ * call, or shorter parts of a row that hand states and their gradients on.
  */
 size_t ckda_scan_bwd_workspace_bytes(int B, int T, int D, int N, int G);
 ckda_status ckda_scan_bwd(const void *dy, const void *x, const void *dt, const float *A,
