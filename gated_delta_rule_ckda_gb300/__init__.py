@@ -1503,7 +1503,7 @@ class _ShortConv(torch.autograd.Function):
         dy = _or_zeros(dy, x.shape, x)
         dhT = None if dhT is None else dhT.contiguous()
         dx, dw, db, dh0 = conv_bwd(dy, x, weight, bias, h0=h0, dhT=dhT, cu_seqlens=cu, silu=ctx.silu,
-                                   store_dh0=h0 is not None)
+                                   store_dh0=ctx.needs_input_grad[3])
         return dx, dw, db, dh0, None, None
 
 
@@ -1529,7 +1529,7 @@ class _SelectiveScan(torch.autograd.Function):
         dy = _or_zeros(dy, x.shape, x)
         dhT = None if dhT is None else dhT.contiguous()
         return (*scan_bwd(dy, x, dt, A, B, C, D, z, dt_bias, h0, dhT, cu, ctx.softplus,
-                          store_dh0=h0 is not None), None, None)
+                          store_dh0=ctx.needs_input_grad[8]), None, None)
 
 
 def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, cu_seqlens=None,
