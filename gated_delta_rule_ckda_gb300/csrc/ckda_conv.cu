@@ -495,7 +495,8 @@ __global__ void __launch_bounds__(kBlock, 2) conv_bwd_kernel(ConvArgs a) {
     for (int i = threadIdx.x; i < a.lanes * VEC; i += kBlock) {
       const int at = chan * a.lanes * VEC + i;
       if (at >= a.D) continue;
-      float t = 0.f;  // (of eight, more only where channels are few: carrying what is rounded off took 2 us more)
+      // (of eight, more only where channels are few: carrying what is rounded off took 2 us more)
+      float t = 0.f;
       for (int g = 0; g < groups; ++g) t += sum[g * a.lanes + i / VEC][i % VEC];
       a.part[((size_t)tok * (W + 1) + j) * a.D + at] = t;
     }
@@ -503,8 +504,8 @@ __global__ void __launch_bounds__(kBlock, 2) conv_bwd_kernel(ConvArgs a) {
 }
 
 // dw and db from the partial rows: 32 channels to a block, 32 threads a channel over the
-// partial rows, joined in a fixed order (by a warp a channel; by a thread a channel, one
-// after another and carrying what is rounded off, it took 1 us more).  Beside that, dx behind the last sequence (in the
+// partial rows, joined in a fixed order by a warp a channel (one after another, carrying
+// what is rounded off, took 1 us more).  Beside that, dx behind the last sequence (in the
 // kernel before, it cost registers, and odd channel counts 3 us).
 template <typename IO, int W>
 __global__ void __launch_bounds__(1024) conv_weight_grad_kernel(ConvArgs a) {

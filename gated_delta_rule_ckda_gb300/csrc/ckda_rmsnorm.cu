@@ -470,8 +470,9 @@ __global__ void __launch_bounds__(1024) rms_weight_grad_kernel(RmsArgs a) {
 // columns of it (LPR apart, NV each: weights stay with their columns), leave the results in
 // its place, and whole vectors go out again; what a row shares a vector with stays untouched.
 // Rows of whole vectors that are wider than a block's registers hold in vectors (fp32 past
-// 8192 columns) go this way too.  One warp a row, or a block.  8,489 rows of 4853 in bf16 with a residual: 103 us forward
-// (48% of the copy bandwidth), 154 backward, which took 363 by single elements from memory.
+// 8192 columns) go this way too.  One warp a row, or a block.  8,489 rows of 4853 in bf16 with
+// a residual: 103 us forward (48% of the copy bandwidth), 153 backward, which took 363 by
+// single elements from memory.
 template <typename IO>
 struct OddRow {
   const long long start;  // the row's first byte
@@ -806,8 +807,8 @@ cudaError_t run_bwd_odd(RmsArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 // The widest rows that these kernels hold, and the widest in vectors of VEC elements.  Rows
-// between the two (fp32, 4096 of 16,384 columns) with a residual take 214 us forward, 210 to 8
-// bits and 294 backward; by the kernels that read a row again, which wider ones need, 242,
+// between the two (fp32, 4096 of 16,384 columns) with a residual take 213 us forward, 207 to 8
+// bits and 292 backward; by the kernels that read a row again, which wider ones need, 242,
 // 441 and 574.  (A few rows are as long under way in both: 7 of them 20 to 29 us and 18 to 26.)
 constexpr int kOddMost = 16384;
 template <int VEC>

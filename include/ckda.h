@@ -652,7 +652,9 @@ ckda_status ckda_conv_decode_step(const void *x, const void *weight, const void 
  *
  *   x, dt, z, y : io   [B, T, D], channels last; z NULL: no gate
  *   Bm, C       : io   [B, T, G, N]; channel d reads group d / (D / G); G divides D
- *   A           : fp32 [D, N], finite; D_skip, dt_bias fp32 [D] or NULL (zero)
+ *   A           : fp32 [D, N], finite; D_skip, dt_bias fp32 [D] or NULL (zero).  A state that
+ *                 would grow past fp32 over its row (delta A > 0) has no value, not even
+ *                 where it starts at zero
  *   h0, hT      : fp32 [sequences, D, N] or NULL (zero, not stored)
  *                 (y may be x, dt or z where that is dense; else y and hT overlap none of
  *                 x, dt, z, Bm, C, h0 and not each other: checked)
