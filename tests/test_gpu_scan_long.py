@@ -82,3 +82,40 @@ def test_whole_rows(ck, T, N, dt, chans):
         ref.check(rows_of(grads[k]).double() / times, want[k], ref.sum_tol(dt, T, D), k, size=size[k])
     for k in ("dA", "dD", "ddt_bias"):
         check(grads[k].double() / ROWS, 0, ref.sum_tol(F32, T, rows * T), k, want[k], size[k])
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("cuts", [[0, 300, 600, 900], [0, 1, 17, 640, 900]])
+def test_parts_of_a_row(ck, dt, cuts):
+    """Less workspace: a row's parts forward, each from the state of the one before, then their
+    gradients from the last part to the first, dh0 handed on as dhT."""
+    gen = torch.Generator().manual_seed(9)
+    r = lambda *s: torch.randn(*s, generator=gen)  # noqa: E731
+    n, T, D, N = 2, 900, 40, 16
+    s = dict(x=r(n, T, D).to(dt), dt=r(n, T, D).to(dt), B=r(n, T, N).to(dt), C=r(n, T, N).to(dt), z=r(n, T, D).to(dt),
+             dy=r(n, T, D).to(dt))
+    A, skip, bias, h0, dhT = -torch.exp(0.8 * r(D, N)), r(D), r(D) - 3, r(n, D, N), r(n, D, N)
+    y, hT, want, size = ref.scan(s["x"], s["dt"], A, s["B"], s["C"], skip, s["z"], bias, h0, None, True, s["dy"], dhT)
+    c = {k: v.cuda() for k, v in s.items()}
+    A, skip, bias = A.cuda(), skip.cuda(), bias.cuda()
+    # (a batch's rows of a part are not evenly apart: copied)
+    parts = [{k: v[:, a:b].contiguous() for k, v in c.items()} for a, b in zip(cuts, cuts[1:])]
+    state, states, ys = h0.cuda(), [], []
+    for p in parts:
+        states.append(state)
+        out, state = ck.scan_fwd(p["x"], p["dt"], A, p["B"], p["C"], skip, p["z"], bias, state)
+        ys.append(out)
+    ref.check(torch.cat(ys, 1), y, ref.scan_tol(dt, T), "y")
+    ref.check(state, hT, ref.scan_tol(F32, T), "hT")
+    passed, by_token, sums = dhT.cuda(), [], 0
+    for p, h in zip(reversed(parts), reversed(states)):
+        dx, ddt, dA, dB, dC, dD, dz, dbias, passed = ck.scan_bwd(p["dy"], p["x"], p["dt"], A, p["B"], p["C"], skip, p["z"], bias, h,
+                                                                 passed)
+        by_token.insert(0, (dx, ddt, dz, dB, dC))
+        sums = [a + b for a, b in zip(sums, (dA, dD, dbias))] if sums else [dA, dD, dbias]
+    for i, k in enumerate(("dx", "ddt", "dz", "dB", "dC")):
+        tol = ref.scan_tol(dt, T, True) if i < 3 else ref.sum_tol(dt, T, D)
+        ref.check(torch.cat([p[i] for p in by_token], 1), want[k], tol, k, size=size[k])
+    for g, k in zip(sums, ("dA", "dD", "ddt_bias")):
+        ref.check(g, want[k], ref.sum_tol(F32, T, n * T), k, size=size[k])
+    ref.check(passed, want["dh0"], ref.scan_tol(F32, T, True), "dh0", size=size["dh0"])
